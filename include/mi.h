@@ -64,7 +64,8 @@ typedef enum mi_status {
 #define MI_DEVERR_INTERNAL     0x80 /* a kernel could not lay out its shared memory (the call did nothing) */
 #define MI_DEVERR_BAD_QUERY    0x20 /* prefill: query_start not within [0, total_q] and ascending,
                                        a request longer than max_query_len, or more
-                                       new tokens than context */
+                                       new tokens than context; shared prefixes:
+                                       group_start not within [0, B] and ascending */
 
 /* Short human-readable name of a status. */
 const char* mi_status_string(mi_status s);
@@ -116,6 +117,15 @@ mi_status mi_kv_pool_alloc_batch(mi_kv_pool* pool, const int32_t* seq_ids, const
 /* Return all blocks of seq_id to the free list. MI_ERR_UNKNOWN_SEQ if seq_id
  * holds no allocation. */
 mi_status mi_kv_pool_free(mi_kv_pool* pool, int32_t seq_id);
+
+/* Shrink resident sequence seq_id to num_tokens tokens (after an eviction,
+ * mi_paged_kv_evict): the blocks past ceil(num_tokens / block_size) leave its
+ * table and return to the free list in table order (so the next pop returns
+ * the last of them); the kept blocks stay where they are. Shrinking to 0
+ * keeps the sequence, with an empty table. The use clock does not move.
+ * MI_ERR_UNKNOWN_SEQ if seq_id is not resident; MI_ERR_INVALID_ARG if
+ * num_tokens is negative or above what the sequence holds. */
+mi_status mi_kv_pool_shrink(mi_kv_pool* pool, int32_t seq_id, int32_t num_tokens);
 
 /* Number of free blocks, or -1 for a NULL pool. */
 int32_t mi_kv_pool_num_free(const mi_kv_pool* pool);
@@ -319,8 +329,8 @@ mi_status mi_paged_decode_step(const mi_dims* dims, const void* q, const void* k
  * early-start calls take different workspaces (two, used in turn, suffice:
  * the step lets the next launch start only after its own wait, so a
  * launch never runs beside the one two before it), and a call directly
- * after mi_kv_copy_blocks, mi_kv_copy_rows or an append into the same
- * caches, or after a kernel of the caller's that fills the tables or
+ * after mi_kv_copy_blocks, mi_kv_copy_rows, mi_paged_kv_evict or an append
+ * into the same caches, or after a kernel of the caller's that fills the tables or
  * lengths, does not set the flag. */
 #define MI_STEP_EARLY_START 1u
 
@@ -559,6 +569,163 @@ mi_status mi_kv_copy_blocks(const mi_dims* dims, const void* src_k, const void* 
 mi_status mi_kv_copy_rows(const void* src, int64_t src_count, const int32_t* src_ids, void* dst,
                           int64_t dst_count, const int32_t* dst_ids, int32_t n, int64_t row_bytes,
                           int32_t* dev_err, mi_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Shared prefixes. Requests that begin with the same tokens (a system prompt,
+ * a document many questions are asked about) keep those tokens once: the
+ * prefix is a sequence of its own in the pool, and each request's table holds
+ * only the tokens after it. */
+
+/* One decode step of attention for such a batch: every prefix's K and V are
+ * read once for all its requests. num_prefixes groups; group g is the requests
+ * group_start[g] .. group_start[g+1]-1 of the batch, all behind prefix g, whose
+ * first prefix_lens[g] tokens prefix_tables[g] holds. Requests before
+ * group_start[0] or from group_start[num_prefixes] on have no prefix. For
+ * request b of group g with p = prefix_lens[g] and n = context_lens[b] own
+ * tokens (counting the new one; append it with positions[b] = p + n - 1):
+ *   out[b][j] = sum_t softmax_t(scale * <q[b][j], K_t>) V_t
+ * over the p tokens of the prefix and the n of the request. The result is that
+ * of mi_paged_decode_attention on one table holding both, up to the fp32
+ * rounding of the split; with p + n = 0 it is a zero row. The two parts are
+ * fp32 online softmaxes on bf16 tensor-core products, put together by their
+ * log-sum-exps, and a prefix may end anywhere in a block.
+ * Device buffers: as mi_paged_decode_attention, and prefix_tables
+ * [num_prefixes][max_prefix_blocks] int32, prefix_lens [num_prefixes] int32,
+ * group_start [num_prefixes + 1] int32 (prefix tables and lengths may be NULL
+ * when num_prefixes is 0). Any table may name any block; nothing but out and
+ * the workspace is written. The workspace has mi_paged_prefix_workspace_bytes()
+ * bytes, 16-byte aligned, contents and graph replay as for
+ * mi_paged_decode_attention; calls that may run at the same time take
+ * different ones.
+ * Device errors: group_start not ascending within [0, B] (MI_DEVERR_BAD_QUERY):
+ * every request attends to its own tokens only; a prefix length above a table
+ * row clamps to it (MI_DEVERR_BAD_CONTEXT); a bad block id of a prefix drops
+ * that block's keys (MI_DEVERR_BAD_BLOCK); the others as
+ * mi_paged_decode_attention. num_prefixes 0 .. 65535, max_prefix_blocks >= 1. */
+mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks,
+                                           const void* q, const void* k_cache, const void* v_cache,
+                                           const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                           const int32_t* group_start, const int32_t* block_tables,
+                                           const int32_t* context_lens, float scale, void* out, void* workspace,
+                                           size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream);
+
+/* Workspace of mi_paged_decode_attention_prefix in bytes on the current
+ * device; 0 when the sizes are not supported. */
+size_t mi_paged_prefix_workspace_bytes(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks);
+
+/* ------------------------------------------------------------------------ */
+/* Attention weights and eviction. A cache that must shrink keeps the tokens
+ * that attention has used: a score per cached token and KV head, the sum of
+ * the softmax weights the token has received from the query heads of that KV
+ * head. Scores live beside the cache, block by block:
+ *   scores fp32 [num_blocks][Hkv][16], 16-byte aligned,
+ * so they follow their blocks (a swap moves a block's scores with
+ * mi_kv_copy_rows, row = Hkv * 16 floats). A block belongs to one request of a
+ * call (the scores of a block that two requests hold are unspecified). */
+
+/* mi_paged_decode_attention, and the scores of every token read:
+ *   w[b][h][t] = sum over the G query heads j of KV head h of
+ *                softmax_t(scale * <q[b][j], K_t>)
+ *   score = w + score   for the tokens t < context_lens[b] - 1,
+ *   score = w           for the new token t = context_lens[b] - 1.
+ * With fresh != 0 every token's score is set to w (the last step's weights
+ * alone). Weights come from fp32 logits and log-sum-exps. Tokens past
+ * context_lens[b], and tokens in bad blocks, keep what their score holds.
+ * out as mi_paged_decode_attention within its tolerance (the sums take the
+ * weights before their rounding to bf16). Two launches: the attention writes
+ * its logits to the workspace (mi_paged_scored_workspace_bytes() bytes, 16-byte
+ * aligned), and a pass over them updates the scores. Other arguments, errors
+ * and guarantees as mi_paged_decode_attention; after MI_DEVERR_TIMEOUT the
+ * scores are not valid either. */
+mi_status mi_paged_decode_attention_scored(const mi_dims* dims, const void* q, const void* k_cache,
+                                           const void* v_cache, const int32_t* block_tables,
+                                           const int32_t* context_lens, float scale, int32_t fresh, void* out,
+                                           float* scores, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                           mi_stream_t stream);
+
+/* The same over FP8 caches (mi_paged_decode_attention_fp8). */
+mi_status mi_paged_decode_attention_scored_fp8(const mi_dims* dims, const void* q, const void* k_cache,
+                                               const void* v_cache, const float* k_scale, const float* v_scale,
+                                               const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                               int32_t fresh, void* out, float* scores, void* workspace,
+                                               size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream);
+
+/* Workspace of the two scored calls in bytes on the current device (the
+ * decode workspace and one fp32 logit per query head for min(B *
+ * max_blocks_per_seq, num_blocks) blocks); 0 when the dims are not supported. */
+size_t mi_paged_scored_workspace_bytes(const mi_dims* dims);
+
+/* The scores that many query tokens per request give: a prompt's last tokens
+ * (a window that looks back over it) or all of them. dims.B = R requests;
+ * request r's m_r = query_start[r+1] - query_start[r] query tokens are rows of
+ * q [total_q][Hq][d] (RoPE applied) at positions n_r - m_r .. n_r - 1 of its
+ * n_r = context_lens[r] tokens, causal as in mi_paged_prefill_attention:
+ *   w[r][h][t] = sum over query tokens i with t <= n_r - m_r + i and the G
+ *                query heads j of h of softmax_t(scale * <q[row][j], K_t>)
+ *   score = w + score   for the tokens t < n_r - m_r,
+ *   score = w           for the query tokens' own, t >= n_r - m_r,
+ * and score = w for all of them with fresh != 0 (the start of a prompt's
+ * scores). One query token gives the weights of the scored decode step. V is
+ * not read; bf16 caches. Rows at negative positions (m_r > n_r,
+ * MI_DEVERR_BAD_QUERY) see nothing. Each token's rows are summed in a fixed
+ * order.
+ * Host arguments total_q = query_start[R] and max_query_len >= every m_r as in
+ * mi_paged_prefill_attention; the workspace has
+ * mi_paged_prefill_scores_workspace_bytes() bytes, 16-byte aligned.
+ * Device errors: query_start not ascending within [0, total_q]
+ * (MI_DEVERR_BAD_QUERY): the call does nothing; m_r > max_query_len
+ * (MI_DEVERR_BAD_QUERY) skips request r; n_r above a table row clamps to it
+ * (MI_DEVERR_BAD_CONTEXT); a bad block id drops that block's keys
+ * (MI_DEVERR_BAD_BLOCK). B up to 65535. */
+mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_q, int32_t max_query_len, const void* q,
+                                  const void* k_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                  const int32_t* query_start, float scale, int32_t fresh, float* scores,
+                                  void* workspace, size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream);
+
+/* Workspace of mi_paged_prefill_scores in bytes; 0 when the sizes are not
+ * supported. */
+size_t mi_paged_prefill_scores_workspace_bytes(const mi_dims* dims, int32_t total_q, int32_t max_query_len);
+
+/* Evict by score. Request b with n = context_lens[b] tokens keeps k =
+ * min(n, max(budgets[b], 0)) of them, per KV head h: its newest r =
+ * min(recent, k) tokens, and of the n - r older ones the k - r with the
+ * largest scores (equal scores: the lower index; NaN below every number). The
+ * kept tokens, in their order, become tokens 0 .. k-1 of dst_tables[b]: rows of
+ * K and V and scores are copied, nothing else is written but new_lens[b] = k.
+ * Each KV head keeps tokens of its own, so afterwards a token index no longer
+ * means a position: append the next token with its true position
+ * (mi_paged_kv_append, mi_paged_kv_append_fp8) at the slot of index k; the
+ * fused decode steps, which take the position from the length, are not for
+ * evicted sequences. Attention needs no positions (RoPE is in the keys).
+ * dst_tables [B][max_blocks_per_seq] is either block_tables itself (the same
+ * pointer: in place; then give the blocks past the new length back with
+ * mi_kv_pool_shrink) or a table of blocks that no request of the call reads
+ * (out of place, which also leaves the source as it was, e.g. a prefix that
+ * others share); it must hold ceil(k / 16) blocks per request, none twice.
+ * Rows of a moved request's blocks past its new length keep what they hold.
+ * In place, a request that keeps everything is left untouched.
+ * Device buffers: caches and scores as above, all 16-byte aligned; budgets,
+ * new_lens [B] int32 (new_lens overlaps no input); workspace of
+ * mi_paged_kv_evict_workspace_bytes() bytes, 16-byte aligned. recent >= 0.
+ * Device errors: n above a table row clamps to it (MI_DEVERR_BAD_CONTEXT); a
+ * bad block id of the source makes its scores lowest and its rows are not
+ * copied, one of the destination drops its rows (MI_DEVERR_BAD_BLOCK). */
+mi_status mi_paged_kv_evict(const mi_dims* dims, void* k_cache, void* v_cache, float* scores,
+                            const int32_t* block_tables, const int32_t* context_lens, const int32_t* budgets,
+                            int32_t recent, const int32_t* dst_tables, int32_t* new_lens, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream);
+
+/* The same over FP8 caches (one byte per element; the per-head scales do not
+ * change). INT8 caches are not evicted: their codes are relative to their
+ * 64-token group's maximum, which a token takes along to no other group. */
+mi_status mi_paged_kv_evict_fp8(const mi_dims* dims, void* k_cache, void* v_cache, float* scores,
+                                const int32_t* block_tables, const int32_t* context_lens, const int32_t* budgets,
+                                int32_t recent, const int32_t* dst_tables, int32_t* new_lens, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream);
+
+/* Workspace of the two eviction calls in bytes; 0 when the dims are not
+ * supported. */
+size_t mi_paged_kv_evict_workspace_bytes(const mi_dims* dims);
 
 /* ------------------------------------------------------------------------ */
 /* Allocation-free attention. The pages have no counterpart to this entry

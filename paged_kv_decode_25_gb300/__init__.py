@@ -43,6 +43,10 @@ EXPORTS = (
     "mi_paged_kv_append_fp8", "mi_paged_decode_attention_fp8",
     "mi_paged_kv_append_int8", "mi_paged_decode_attention_int8", "mi_paged_kv_append_int8_tokens",
     "mi_paged_prefill_attention", "mi_paged_prefill_attention_variant", "mi_paged_decode_attention_noalloc",
+    "mi_kv_pool_shrink", "mi_paged_decode_attention_prefix", "mi_paged_prefix_workspace_bytes",
+    "mi_paged_decode_attention_scored", "mi_paged_decode_attention_scored_fp8", "mi_paged_scored_workspace_bytes",
+    "mi_paged_prefill_scores", "mi_paged_prefill_scores_workspace_bytes",
+    "mi_paged_kv_evict", "mi_paged_kv_evict_fp8", "mi_paged_kv_evict_workspace_bytes",
     "mi_paged_decode_step", "mi_paged_decode_step_fp8", "mi_test_set_wait_limit", "mi_test_withhold_copy",
 )
 MI_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -112,6 +116,21 @@ def load():
             "mi_paged_decode_step_fp8": (
                 [dims_p, P, P, P, P, i32, P, P, P, P, f32, P, P, P, P, P, ctypes.c_size_t, P, P, ctypes.c_uint32],
                 i32),
+            "mi_kv_pool_shrink": ([P, i32, i32], i32),
+            "mi_paged_prefix_workspace_bytes": ([dims_p, i32, i32], ctypes.c_size_t),
+            "mi_paged_decode_attention_prefix": (
+                [dims_p, i32, i32, P, P, P, P, P, P, P, P, f32, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_scored_workspace_bytes": ([dims_p], ctypes.c_size_t),
+            "mi_paged_decode_attention_scored": (
+                [dims_p, P, P, P, P, P, f32, i32, P, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_decode_attention_scored_fp8": (
+                [dims_p, P, P, P, P, P, P, P, f32, i32, P, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_prefill_scores_workspace_bytes": ([dims_p, i32, i32], ctypes.c_size_t),
+            "mi_paged_prefill_scores": (
+                [dims_p, i32, i32, P, P, P, P, P, f32, i32, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_kv_evict_workspace_bytes": ([dims_p], ctypes.c_size_t),
+            "mi_paged_kv_evict": ([dims_p, P, P, P, P, P, P, i32, P, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_kv_evict_fp8": ([dims_p, P, P, P, P, P, P, i32, P, P, P, ctypes.c_size_t, P, P], i32),
             "mi_test_set_wait_limit": ([ctypes.c_int64], i32),
             "mi_test_withhold_copy": ([i32], i32),
         }
@@ -192,6 +211,10 @@ def mi_kv_pool_alloc_batch(handle, seq_ids, num_tokens):
 
 def mi_kv_pool_free(handle, seq_id):
     return load().mi_kv_pool_free(handle, int(seq_id))
+
+
+def mi_kv_pool_shrink(handle, seq_id, num_tokens):
+    return load().mi_kv_pool_shrink(handle, int(seq_id), int(num_tokens))
 
 
 def mi_kv_pool_num_free(handle):
@@ -280,6 +303,9 @@ class Pool:
 
     def free(self, seq):
         return mi_kv_pool_free(self.handle, seq)
+
+    def shrink(self, seq, num_tokens):
+        return mi_kv_pool_shrink(self.handle, seq, num_tokens)
 
     def num_free(self):
         return mi_kv_pool_num_free(self.handle)
@@ -482,6 +508,91 @@ def mi_paged_decode_step_fp8(d: MiDims, q, k, v, rope_cos_sin, max_pos, block_ta
                                            _ptr(v_scale), float(scale), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
                                            _ptr(out), _ptr(workspace), int(wb), _ptr(dev_err), _stream(stream),
                                            int(flags))
+
+
+def _nbytes(workspace, workspace_bytes):
+    return workspace.numel() * workspace.element_size() if workspace_bytes is None else int(workspace_bytes)
+
+
+def mi_paged_prefix_workspace_bytes(d: MiDims, num_prefixes, max_prefix_blocks) -> int:
+    return int(load().mi_paged_prefix_workspace_bytes(ctypes.byref(d), int(num_prefixes), int(max_prefix_blocks)))
+
+
+def mi_paged_decode_attention_prefix(d: MiDims, num_prefixes, max_prefix_blocks, q, k_cache, v_cache, prefix_tables,
+                                     prefix_lens, group_start, block_tables, context_lens, scale, out, workspace,
+                                     workspace_bytes=None, dev_err=None, stream=None):
+    """Decode attention of requests group_start[g] .. group_start[g+1]-1 over
+    prefix g's tokens and their own (block_tables, context_lens)."""
+    return load().mi_paged_decode_attention_prefix(
+        ctypes.byref(d), int(num_prefixes), int(max_prefix_blocks), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+        _ptr(prefix_tables), _ptr(prefix_lens), _ptr(group_start), _ptr(block_tables), _ptr(context_lens),
+        float(scale), _ptr(out), _ptr(workspace), _nbytes(workspace, workspace_bytes), _ptr(dev_err),
+        _stream(stream))
+
+
+def mi_paged_scored_workspace_bytes(d: MiDims) -> int:
+    return int(load().mi_paged_scored_workspace_bytes(ctypes.byref(d)))
+
+
+def mi_paged_decode_attention_scored(d: MiDims, q, k_cache, v_cache, block_tables, context_lens, scale, fresh, out,
+                                     scores, workspace, workspace_bytes=None, dev_err=None, stream=None):
+    """Decode attention that adds each token's weight to scores
+    [num_blocks][Hkv][16] fp32 (fresh: sets it)."""
+    return load().mi_paged_decode_attention_scored(
+        ctypes.byref(d), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), float(scale),
+        int(bool(fresh)), _ptr(out), _ptr(scores), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+        _ptr(dev_err), _stream(stream))
+
+
+def mi_paged_decode_attention_scored_fp8(d: MiDims, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                         context_lens, scale, fresh, out, scores, workspace, workspace_bytes=None,
+                                         dev_err=None, stream=None):
+    """mi_paged_decode_attention_scored over e4m3 caches."""
+    return load().mi_paged_decode_attention_scored_fp8(
+        ctypes.byref(d), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        _ptr(context_lens), float(scale), int(bool(fresh)), _ptr(out), _ptr(scores), _ptr(workspace),
+        _nbytes(workspace, workspace_bytes), _ptr(dev_err), _stream(stream))
+
+
+def mi_paged_prefill_scores_workspace_bytes(d: MiDims, total_q, max_query_len) -> int:
+    return int(load().mi_paged_prefill_scores_workspace_bytes(ctypes.byref(d), int(total_q), int(max_query_len)))
+
+
+def mi_paged_prefill_scores(d: MiDims, total_q, max_query_len, q, k_cache, block_tables, context_lens, query_start,
+                            scale, fresh, scores, workspace, workspace_bytes=None, dev_err=None, stream=None):
+    """The weights that rows query_start[r] .. query_start[r+1]-1 of q, the
+    last tokens of request r, give its cached tokens (causal)."""
+    return load().mi_paged_prefill_scores(
+        ctypes.byref(d), int(total_q), int(max_query_len), _ptr(q), _ptr(k_cache), _ptr(block_tables),
+        _ptr(context_lens), _ptr(query_start), float(scale), int(bool(fresh)), _ptr(scores), _ptr(workspace),
+        _nbytes(workspace, workspace_bytes), _ptr(dev_err), _stream(stream))
+
+
+def mi_paged_kv_evict_workspace_bytes(d: MiDims) -> int:
+    return int(load().mi_paged_kv_evict_workspace_bytes(ctypes.byref(d)))
+
+
+def _evict(fn, d, k_cache, v_cache, scores, block_tables, context_lens, budgets, recent, dst_tables, new_lens,
+           workspace, workspace_bytes, dev_err, stream):
+    return fn(ctypes.byref(d), _ptr(k_cache), _ptr(v_cache), _ptr(scores), _ptr(block_tables), _ptr(context_lens),
+              _ptr(budgets), int(recent), _ptr(dst_tables), _ptr(new_lens), _ptr(workspace),
+              _nbytes(workspace, workspace_bytes), _ptr(dev_err), _stream(stream))
+
+
+def mi_paged_kv_evict(d: MiDims, k_cache, v_cache, scores, block_tables, context_lens, budgets, recent, dst_tables,
+                      new_lens, workspace, workspace_bytes=None, dev_err=None, stream=None):
+    """Keep each request's newest `recent` tokens and, per KV head, the
+    heaviest of the older ones; dst_tables is block_tables itself (in place)
+    or a table of other blocks."""
+    return _evict(load().mi_paged_kv_evict, d, k_cache, v_cache, scores, block_tables, context_lens, budgets, recent,
+                  dst_tables, new_lens, workspace, workspace_bytes, dev_err, stream)
+
+
+def mi_paged_kv_evict_fp8(d: MiDims, k_cache, v_cache, scores, block_tables, context_lens, budgets, recent,
+                          dst_tables, new_lens, workspace, workspace_bytes=None, dev_err=None, stream=None):
+    """mi_paged_kv_evict over e4m3 caches."""
+    return _evict(load().mi_paged_kv_evict_fp8, d, k_cache, v_cache, scores, block_tables, context_lens, budgets,
+                  recent, dst_tables, new_lens, workspace, workspace_bytes, dev_err, stream)
 
 
 def mi_test_set_wait_limit(ns):

@@ -45,6 +45,7 @@
 #include <random>
 
 #include "common.cuh"
+#include "decode.cuh"
 #include "rope.cuh"
 #include "tma.cuh"
 
@@ -99,6 +100,7 @@ struct AttnParams {
     long long wait_ns;             // bound on every mbarrier wait of the launch
     int early;                     // fused step: plan and first copies before the wait on the kernel before
     int withhold;                  // failure-detection test: each producer withholds its first copy
+    DecodeExt ext;                 // scored and shared-prefix steps only
 };
 
 // ------------------------------------------------------------- the plan ---
@@ -436,11 +438,58 @@ __host__ __device__ inline SmemPlan smem_plan(int W, int S, int HD, int G, bool 
 
 // ---------------------------------------------------- per-warp compute ----
 
+// Scored step: this lane's four logits (heads 2(lane & 3) and the next one of
+// tokens lane / 4 and lane / 4 + 8) into the block's [16][gp] rows.
+__device__ __forceinline__ void store_logits(float* lg, int gp, int lane, float s0, float s1, float s2, float s3) {
+    const int h0 = (lane & 3) * 2;
+    if (h0 < gp) {
+        float* at = lg + (lane >> 2) * gp + h0;
+        *reinterpret_cast<float2*>(at) = make_float2(s0, s1);
+        *reinterpret_cast<float2*>(at + 8 * gp) = make_float2(s2, s3);
+    }
+}
+
+// Shared-prefix step: folds the prefix's partial results of head h's row g of
+// a request (`at`: its entry of DecodeExt::rows) into four of its own outputs
+// v, whose log2-sum-exp is lse (-inf: no own tokens). Partials are taken in order.
+template <int HD>
+__device__ __forceinline__ float4 merge_prefix(const DecodeExt& x, int4 at, int Hkv, int h, int g, int dcol, float lse,
+                                               float4 v) {
+    auto row = [&](int s) { return (long long)(at.x + s * Hkv + h) * x.slot_rows + at.z + g; };
+    float M = lse;
+    for (int s = 0; s < at.y; ++s) M = fmaxf(M, __ldcg(x.part_lse + row(s)));
+    if (M == kNegInf) return make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = exp2f(lse - M);
+    float4 num = den > 0.f ? make_float4(den * v.x, den * v.y, den * v.z, den * v.w) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < at.y; ++s) {
+        const float w = exp2f(__ldcg(x.part_lse + row(s)) - M);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part + row(s) * HD + dcol));
+        den += w;
+        num.x += w * o.x;
+        num.y += w * o.y;
+        num.z += w * o.z;
+        num.w += w * o.w;
+    }
+    const float r = 1.f / den;
+    return make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
+}
+
+__device__ __forceinline__ uint2 pack_bf16x4(float4 v) {
+    return make_uint2((uint32_t)f32_to_bf16(v.x) | ((uint32_t)f32_to_bf16(v.y) << 16),
+                      (uint32_t)f32_to_bf16(v.z) | ((uint32_t)f32_to_bf16(v.w) << 16));
+}
+
 // Tensor-core tile: S^T[16 tokens x 8 heads] = K[16 x HD] . Q^T[HD x 8] with
 // mma.sync m16n8k16 (heads beyond G are zero columns), online softmax on the
 // fragments, then O^T[HD x 8] += V^T[HD x 16] . P^T[16 x 8] (V^T by
 // ldmatrix.trans, P^T by movmatrix.trans of the score fragments).
-template <int HD>
+// With SCORED, a block's base-2 logits also go to `lg` ([16 tokens][gp] in
+// global memory) and the sums take the weights before their rounding to bf16:
+// the row's log-sum-exp then carries fp32 precision, which the weights
+// recomputed from it need and the output (whose values are rounded to 8 bits
+// anyway) does not mind.
+template <int HD, bool SCORED = false>
 struct MmaState {
     static constexpr int kK = HD / 16;
     uint32_t qb[kK][2];
@@ -482,7 +531,8 @@ struct MmaState {
         l[0] = l[1] = 0.f;
     }
 
-    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int valid, float sl2, int lane) {
+    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int valid, float sl2, int lane,
+                                          float* lg = nullptr, int gp = 0) {
         float c[4] = {0.f, 0.f, 0.f, 0.f};
         {
             // two accumulation chains (even / odd k-slices) halve the
@@ -504,6 +554,7 @@ struct MmaState {
         float s1 = t0 < valid ? c[1] * sl2 : kNegInf;  // head 2*(lane&3)+1, token t0
         float s2 = t1 < valid ? c[2] * sl2 : kNegInf;  // head 2*(lane&3),   token t1
         float s3 = t1 < valid ? c[3] * sl2 : kNegInf;  // head 2*(lane&3)+1, token t1
+        if constexpr (SCORED) store_logits(lg, gp, lane, s0, s1, s2, s3);
         float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
@@ -515,11 +566,17 @@ struct MmaState {
         const float al0 = ex2(m[0] - r0), al1 = ex2(m[1] - r1);
         m[0] = mn0;
         m[1] = mn1;
-        const uint32_t x0 = pack_bf16x2(ex2(s0 - r0), ex2(s1 - r1));
-        const uint32_t x1 = pack_bf16x2(ex2(s2 - r0), ex2(s3 - r1));
-        // the sums use the same bf16-rounded weights the PV product uses
-        l[0] = l[0] * al0 + (bf16_lo(x0) + bf16_lo(x1));
-        l[1] = l[1] * al1 + (bf16_hi(x0) + bf16_hi(x1));
+        const float e0 = ex2(s0 - r0), e1 = ex2(s1 - r1), e2 = ex2(s2 - r0), e3 = ex2(s3 - r1);
+        const uint32_t x0 = pack_bf16x2(e0, e1);
+        const uint32_t x1 = pack_bf16x2(e2, e3);
+        if constexpr (SCORED) {
+            l[0] = l[0] * al0 + (e0 + e2);
+            l[1] = l[1] * al1 + (e1 + e3);
+        } else {
+            // the sums use the same bf16-rounded weights the PV product uses
+            l[0] = l[0] * al0 + (bf16_lo(x0) + bf16_lo(x1));
+            l[1] = l[1] * al1 + (bf16_hi(x0) + bf16_hi(x1));
+        }
         // the running max rarely moves once a few blocks are in: skip the
         // rescale when no lane's factor differs from 1
         if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
@@ -583,7 +640,7 @@ struct MmaState {
 // them into (token pair, dim) pairs and converts; the 16 O^T rows of a tile
 // pair are dims 4(8t + r) + {0, 1} (even tile) and + {2, 3} (odd tile).
 // K's per-head scale folds into the exponent scale, V's into the output.
-template <int HD>
+template <int HD, bool SCORED = false>
 struct Fp8State {
     static constexpr int kK = HD / 16;
     uint32_t qb[kK][2];
@@ -629,7 +686,8 @@ struct Fp8State {
         vsc = __ldg(p.v_scale + h);
     }
 
-    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int valid, float /*sl2 of bf16*/, int lane) {
+    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int valid, float /*sl2 of bf16*/, int lane,
+                                          float* lg = nullptr, int gp = 0) {
         float c[4] = {0.f, 0.f, 0.f, 0.f};
         {
             float c1[4] = {0.f, 0.f, 0.f, 0.f};  // second accumulation chain (odd k-slices)
@@ -652,6 +710,7 @@ struct Fp8State {
         float s1 = t0 < valid ? c[1] * sl2 : kNegInf;
         float s2 = t1 < valid ? c[2] * sl2 : kNegInf;
         float s3 = t1 < valid ? c[3] * sl2 : kNegInf;
+        if constexpr (SCORED) store_logits(lg, gp, lane, s0, s1, s2, s3);
         float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
@@ -663,10 +722,16 @@ struct Fp8State {
         const float al0 = ex2(m[0] - r0), al1 = ex2(m[1] - r1);
         m[0] = mn0;
         m[1] = mn1;
-        const uint32_t x0 = pack_f16x2(ex2(s0 - r0), ex2(s1 - r1));
-        const uint32_t x1 = pack_f16x2(ex2(s2 - r0), ex2(s3 - r1));
-        l[0] = l[0] * al0 + (f16_lo(x0) + f16_lo(x1));
-        l[1] = l[1] * al1 + (f16_hi(x0) + f16_hi(x1));
+        const float e0 = ex2(s0 - r0), e1 = ex2(s1 - r1), e2 = ex2(s2 - r0), e3 = ex2(s3 - r1);
+        const uint32_t x0 = pack_f16x2(e0, e1);
+        const uint32_t x1 = pack_f16x2(e2, e3);
+        if constexpr (SCORED) {
+            l[0] = l[0] * al0 + (e0 + e2);
+            l[1] = l[1] * al1 + (e1 + e3);
+        } else {
+            l[0] = l[0] * al0 + (f16_lo(x0) + f16_lo(x1));
+            l[1] = l[1] * al1 + (f16_hi(x0) + f16_hi(x1));
+        }
         if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
             for (int mt = 0; mt < kK; ++mt) {
@@ -1072,14 +1137,14 @@ struct FmaState {
 
 // ------------------------------------------------------ the main kernel ---
 
-template <int HD, int VAR, int GP>
+template <int HD, int VAR, int GP, bool SCORED = false>
 struct StateOf;
-template <int HD, int GP>
-struct StateOf<HD, kVarMma, GP> { using T = MmaState<HD>; };
+template <int HD, int GP, bool SCORED>
+struct StateOf<HD, kVarMma, GP, SCORED> { using T = MmaState<HD, SCORED>; };
 template <int HD, int GP>
 struct StateOf<HD, kVarFma, GP> { using T = FmaState<HD, GP>; };
-template <int HD, int GP>
-struct StateOf<HD, kVarFp8, GP> { using T = Fp8State<HD>; };
+template <int HD, int GP, bool SCORED>
+struct StateOf<HD, kVarFp8, GP, SCORED> { using T = Fp8State<HD, SCORED>; };
 template <int HD, int GP>
 struct StateOf<HD, kVarInt8, GP> { using T = Int8State<HD>; };
 
@@ -1106,7 +1171,10 @@ __device__ __forceinline__ void consumer_sync(int nthreads) {
 // CTA's range it also writes that row of the cache and the unit's q_out. The
 // consumer warp that streams that block copies the two rows into its staged
 // tiles.
-template <int HD, int VAR, int GP, int W, bool FUSED = false>
+// EXT (MMA and e4m3 tiles; not FUSED): kExtScored also keeps every logit and
+// each row's log-sum-exp for the score pass; kExtPrefix merges partial results
+// over a shared prefix into each row where the row is finished.
+template <int HD, int VAR, int GP, int W, bool FUSED = false, int EXT = kExtNone>
 __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 || VAR == kVarInt8) && !FUSED ? 3 : 2)
     attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                 const AttnParams p) {
@@ -1116,6 +1184,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
     constexpr bool kOneByte = VAR == kVarFp8 || VAR == kVarInt8;
     constexpr uint32_t kSleep = kOneByte ? kWaitSleepNs : 0u;
     static_assert(!FUSED || VAR == kVarMma || VAR == kVarFp8, "the fused step runs the MMA or e4m3 tile");
+    static_assert(EXT == kExtNone || (!FUSED && (VAR == kVarMma || VAR == kVarFp8)), "extensions: MMA or e4m3 tile");
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = p.stages;
@@ -1417,6 +1486,17 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                 const int n = __ldg(p.context_lens + b);
                 if (n > p.mbps * kBlock && lane == W) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
                 if (n <= 0) {
+                    if constexpr (EXT == kExtPrefix) {
+                        const int4 at = __ldcg(p.ext.rows + b);
+                        uint2* row = reinterpret_cast<uint2*>(p.out + (long long)b * p.Hq * HD);
+                        for (int i = lane - W; i < p.Hq * HD / 4; i += nl) {
+                            const int j = i / (HD / 4);
+                            row[i] = pack_bf16x4(merge_prefix<HD>(p.ext, at, p.Hkv, j / p.G, j % p.G,
+                                                                  (i % (HD / 4)) * 4, kNegInf,
+                                                                  make_float4(0.f, 0.f, 0.f, 0.f)));
+                        }
+                        continue;
+                    }
                     uint4* row = reinterpret_cast<uint4*>(p.out + (long long)b * p.Hq * HD);
                     for (int i = lane - W; i < p.Hq * HD / 8; i += nl) row[i] = make_uint4(0, 0, 0, 0);
                 }
@@ -1517,7 +1597,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                     sts32(okf, 1u);
                     mbar_arrive(bar);
                 } else {
-                    sts32(okf, 1u);
+                    sts32(okf, EXT == kExtScored ? (uint32_t)blk + 1u : 1u);
                     mbar_arrive_expect_tx(bar, 2 * kTile);
                     tma_load_2d(dst, &tmk, bar, 0, y, policy);
                     tma_load_2d(dst + kTile, &tmv, bar, 0, y, policy);
@@ -1543,7 +1623,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
     float* obuf = reinterpret_cast<float*>(base + sp.obuf);
     float* xbuf = reinterpret_cast<float*>(base + sp.xbuf) + warp * (kBlock * kMaxG + kMaxG);
     const int nc = W * 32;
-    using State = typename StateOf<HD, VAR, GP>::T;
+    using State = typename StateOf<HD, VAR, GP, EXT == kExtScored>::T;
     State st;
     int unit_no = 0;  // fused step: units begun so far (q ring slot and phase)
     const uint16_t* qslot = nullptr;  // fused step: this unit's ring slot
@@ -1640,6 +1720,9 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                     // the block's K and V group maxima, staged with the tiles
                     const uint32_t am = sbase + sp.amx + si * 8;
                     st.block(kt, vt, valid, lane, __uint_as_float(lds32(am)), __uint_as_float(lds32(am + 4)));
+                } else if constexpr (EXT == kExtScored) {
+                    const long long e = p.ext.by_block ? (long long)(okv - 1u) * p.Hkv + cu.h : x;
+                    st.block(kt, vt, valid, p.sl2, lane, p.ext.logits + e * (kBlock * p.ext.gp), p.ext.gp);
                 } else if constexpr (VAR != kVarFma) {
                     st.block(kt, vt, valid, p.sl2, lane);
                 } else {
@@ -1670,6 +1753,8 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
         const bool whole = (sa == cu.start) && (se == cu.start + cu.len);
         const int slot = (sa == ra) ? 0 : 1;
         float* part = p.part + ((long long)cta * 2 + slot) * p.slot_floats;
+        int4 pfx = make_int4(0, 0, 0, 0);
+        if constexpr (EXT == kExtPrefix) pfx = __ldcg(p.ext.rows + cu.b);
         // four consecutive outputs per thread (16-byte shared and global
         // accesses); each thread weighs the warps' states of its head itself
         for (int idx = 4 * tid; idx < p.G * HD; idx += 4 * nc) {
@@ -1694,11 +1779,14 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                 }
             }
             const float r = L > 0.f ? 1.f / L : 0.f;
-            const float4 v = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+            float4 v = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
             if (whole) {
-                *reinterpret_cast<uint2*>(p.out + ((long long)cu.b * p.Hq + (long long)cu.h * p.G + g) * HD + dcol) =
-                    make_uint2((uint32_t)f32_to_bf16(v.x) | ((uint32_t)f32_to_bf16(v.y) << 16),
-                               (uint32_t)f32_to_bf16(v.z) | ((uint32_t)f32_to_bf16(v.w) << 16));
+                const long long row = (long long)cu.b * p.Hq + (long long)cu.h * p.G + g;
+                if constexpr (EXT == kExtPrefix)
+                    v = merge_prefix<HD>(p.ext, pfx, p.Hkv, cu.h, g, dcol, L > 0.f ? M + log2f(L) : kNegInf, v);
+                if constexpr (EXT == kExtScored)
+                    if (dcol == 0) p.ext.lse[row] = L > 0.f ? M + log2f(L) : kNegInf;
+                *reinterpret_cast<uint2*>(p.out + row * HD + dcol) = pack_bf16x4(v);
             } else {
                 *reinterpret_cast<float4*>(part + idx) = v;
                 if (dcol == 0) part[p.G * HD + g] = L > 0.f ? M + log2f(L) : kNegInf;
@@ -1764,10 +1852,14 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                         }
                     }
                     const float r = den > 0.f ? 1.f / den : 0.f;
-                    *reinterpret_cast<uint2*>(p.out + ((long long)cu.b * p.Hq + (long long)cu.h * p.G + g) * HD +
-                                              (idx - g * HD)) =
-                        make_uint2((uint32_t)f32_to_bf16(num.x * r) | ((uint32_t)f32_to_bf16(num.y * r) << 16),
-                                   (uint32_t)f32_to_bf16(num.z * r) | ((uint32_t)f32_to_bf16(num.w * r) << 16));
+                    const long long row = (long long)cu.b * p.Hq + (long long)cu.h * p.G + g;
+                    const int dcol = idx - g * HD;
+                    float4 v = make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
+                    if constexpr (EXT == kExtPrefix)
+                        v = merge_prefix<HD>(p.ext, pfx, p.Hkv, cu.h, g, dcol, den > 0.f ? M + log2f(den) : kNegInf, v);
+                    if constexpr (EXT == kExtScored)
+                        if (dcol == 0) p.ext.lse[row] = den > 0.f ? M + log2f(den) : kNegInf;
+                    *reinterpret_cast<uint2*>(p.out + row * HD + dcol) = pack_bf16x4(v);
                 }
             }
         }
@@ -1836,6 +1928,20 @@ KernelFn pick_kernel(int HD, int var, int G) {
     if (var == kVarInt8)
         return HD == 64 ? attn_kernel<64, kVarInt8, 8, kWarps> : attn_kernel<128, kVarInt8, 8, kWarps>;
     return HD == 64 ? fma_kernel_for<64>(gp_of(G)) : fma_kernel_for<128>(gp_of(G));
+}
+
+// The kernels of the scored and the shared-prefix step (null: not built).
+KernelFn pick_ext_kernel(int HD, int var, int kind) {
+    if (kind == kExtScored && var == kVarMma)
+        return HD == 64 ? attn_kernel<64, kVarMma, 8, kWarps, false, kExtScored>
+                        : attn_kernel<128, kVarMma, 8, kWarps, false, kExtScored>;
+    if (kind == kExtScored && var == kVarFp8)
+        return HD == 64 ? attn_kernel<64, kVarFp8, 8, kWarps, false, kExtScored>
+                        : attn_kernel<128, kVarFp8, 8, kWarps, false, kExtScored>;
+    if (kind == kExtPrefix && var == kVarMma)
+        return HD == 64 ? attn_kernel<64, kVarMma, 8, kWarps, false, kExtPrefix>
+                        : attn_kernel<128, kVarMma, 8, kWarps, false, kExtPrefix>;
+    return nullptr;
 }
 
 struct GridKey {
@@ -1994,7 +2100,7 @@ mi_status attention(const mi_dims* dims, const void* q, const void* k_cache, con
                     const float* k_scale, const float* v_scale, const int32_t* block_tables,
                     const int32_t* context_lens, float scale, void* out, void* workspace,
                     size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream, int var, int32_t ctas,
-                    const StepArgs* step = nullptr) {
+                    const StepArgs* step = nullptr, const DecodeExt* ext = nullptr) {
     const mi_status ds = check_dims(dims);
     if (ds != MI_OK) return ds;
     const mi_dims D = *dims;
@@ -2031,11 +2137,13 @@ mi_status attention(const mi_dims* dims, const void* q, const void* k_cache, con
     const int gmax = max_grid(D);
     if (gmax <= 0) return MI_ERR_CUDA;
     if (workspace_bytes < workspace_for(D, gmax)) return MI_ERR_INVALID_ARG;
-    KernelFn fn = !step ? pick_kernel(HD, var, G)
+    KernelFn fn = ext   ? pick_ext_kernel(HD, var, ext->kind)
+                : !step ? pick_kernel(HD, var, G)
                 : var == kVarFp8 ? (HD == 64 ? attn_kernel<64, kVarFp8, 8, kWarps, true>
                                              : attn_kernel<128, kVarFp8, 8, kWarps, true>)
                                  : (HD == 64 ? attn_kernel<64, kVarMma, 8, kWarps, true>
                                              : attn_kernel<128, kVarMma, 8, kWarps, true>);
+    if (!fn) return MI_ERR_UNSUPPORTED;
     const int gown = grid_for(fn, smem, threads);
     if (gown <= 0 || gown > gmax) return MI_ERR_CUDA;
     const int grid = ctas > 0 && ctas < gown ? ctas : gown;
@@ -2057,7 +2165,8 @@ mi_status attention(const mi_dims* dims, const void* q, const void* k_cache, con
     p.plan_cache = p.plan_stride > 0 ? static_cast<uint8_t*>(workspace) + word_bytes(gmax) +
                                            (partial_bytes(D, gmax) + 127) / 128 * 128
                                      : nullptr;
-    p.plan_kind = var * 2 + (step ? 1 : 0);
+    p.plan_kind = var * 2 + (step ? 1 : 0) + (ext ? 16 * ext->kind : 0);
+    p.ext = ext ? *ext : DecodeExt();
     p.epoch = next_epoch();
     p.dev_err = dev_err;
     p.B = D.B;
@@ -2091,6 +2200,16 @@ mi_status attention(const mi_dims* dims, const void* q, const void* k_cache, con
 }
 
 }  // namespace
+
+mi_status decode_attention_ext(const mi_dims* dims, const void* q, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                               const int32_t* context_lens, float scale, void* out, void* workspace,
+                               size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream, bool fp8,
+                               const DecodeExt& ext) {
+    return attention(dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, workspace,
+                     workspace_bytes, dev_err, stream, fp8 ? kVarFp8 : kVarMma, 0, nullptr, &ext);
+}
+
 }  // namespace mi
 
 extern "C" mi_status mi_paged_decode_attention_variant(const mi_dims* dims, const void* q,

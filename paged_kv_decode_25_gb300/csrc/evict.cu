@@ -1,0 +1,358 @@
+// mi_paged_kv_evict: a smaller paged cache from accumulated attention weights.
+//
+// For request b and KV head h with n tokens, a budget k = min(n, budgets[b])
+// and r = min(recent, k), the kept tokens are the newest r and, of the n - r
+// older ones, the k - r with the largest scores (equal scores: the lower
+// index first). They keep their order and become tokens 0 .. k-1 of the
+// destination table. Each KV head keeps its own tokens: a block holds every
+// head's rows of 16 token indices, and nothing else ties the heads together.
+//
+// Two launches:
+//   * evict_select_kernel finds the (k - r)-th largest score of every (b, h)
+//     by a radix select over an order-preserving 32-bit key, and writes the
+//     kept older tokens' indices in ascending order;
+//   * evict_move_kernel copies the kept rows of K and V and their scores.
+// Both only move bytes: the floor is the scores once, the kept rows in and
+// out.
+#include <algorithm>
+#include <mutex>
+
+#include "batch.cuh"
+
+namespace mi {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kBins = 2048;                // digits of 11, 11 and 10 bits
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 64;              // destination rows per work item
+
+struct EvictParams {
+    uint8_t* k;                    // [num_blocks][Hkv][16] rows of row bytes
+    uint8_t* v;
+    float* scores;                 // [num_blocks][Hkv][16]
+    const int32_t* tables;         // [B][mbps]
+    const int32_t* lens;           // [B]
+    const int32_t* budgets;        // [B]
+    const int32_t* dst;            // [B][mbps]
+    int32_t* new_lens;             // [B]
+    int32_t* list;                 // [B][Hkv][mbps * 16]: kept older tokens, ascending
+    int32_t* dev_err;
+    int B, Hkv, num_blocks, mbps, recent, in_place;
+};
+
+// What request b keeps: n tokens now, `kept` of them afterwards, the last
+// `tail` of which are its newest and the first `heavy` chosen by score among
+// tokens 0 .. old-1. A request that keeps everything has no chosen tokens.
+struct Share {
+    int n, kept, tail, heavy, old;
+};
+
+__device__ __forceinline__ Share share_of(const EvictParams& p, int b) {
+    Share s;
+    s.n = min(max(__ldg(p.lens + b), 0), p.mbps * kBlock);
+    s.kept = min(s.n, max(__ldg(p.budgets + b), 0));
+    s.tail = s.kept == s.n ? s.n : min(p.recent, s.kept);
+    s.heavy = s.kept - s.tail;
+    s.old = s.n - s.tail;
+    return s;
+}
+
+// Monotone in the score, as an unsigned number: NaN lowest, then -inf up to
+// +inf, the two zeros equal.
+__device__ __forceinline__ uint32_t score_key(float x) {
+    uint32_t u = __float_as_uint(x);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
+    if (u == 0x80000000u) u = 0u;
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+// Keys of tokens 4 * t4 .. 4 * t4 + 3 (0 for a block id outside the cache).
+__device__ __forceinline__ void load_keys(const EvictParams& p, int b, int h, int t4, uint32_t (&key)[4], bool report) {
+    const int blk = __ldg(p.tables + (long long)b * p.mbps + (t4 >> 2));
+    if (blk < 0 || blk >= p.num_blocks) {
+        if (report) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+        key[0] = key[1] = key[2] = key[3] = 0u;
+        return;
+    }
+    const float4 s = *reinterpret_cast<const float4*>(p.scores + ((long long)blk * p.Hkv + h) * kBlock + (t4 & 3) * 4);
+    key[0] = score_key(s.x);
+    key[1] = score_key(s.y);
+    key[2] = score_key(s.z);
+    key[3] = score_key(s.w);
+}
+
+// Exclusive sum over the block; `total` is the sum. wsum: 32 words.
+__device__ __forceinline__ uint32_t block_sum_before(uint32_t v, uint32_t* wsum, uint32_t& total) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // the previous use of wsum is over
+    if (lane == 31) wsum[wid] = x;
+    __syncthreads();
+    if (wid == 0) {
+        uint32_t t = lane < nw ? wsum[lane] : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += y;
+        }
+        wsum[lane] = t;
+    }
+    __syncthreads();
+    total = wsum[31];
+    return (wid ? wsum[wid - 1] : 0u) + x - v;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t wsum[32];
+    __shared__ uint32_t found[2];
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, tid = threadIdx.x;
+    const Share s = share_of(p, b);
+    if (h == 0 && tid == 0) {
+        p.new_lens[b] = s.kept;
+        if (__ldg(p.lens + b) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
+    }
+    if (s.heavy == 0) return;
+    const int quads = (s.old + 3) / 4;
+    uint32_t prefix = 0, need = (uint32_t)s.heavy;  // of the tokens whose key starts with `prefix`, take the top `need`
+    int low = 32;                                   // key bits below the prefix
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int bits = pass < 2 ? 11 : 10, up = low;
+        low -= bits;
+        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
+        __syncthreads();
+        for (int t4 = tid; t4 < quads; t4 += kSelThreads) {
+            uint32_t key[4];
+            load_keys(p, b, h, t4, key, pass == 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * t4 + e < s.old && (pass == 0 || (key[e] >> up) == prefix))
+                    atomicAdd(&hist[(key[e] >> low) & ((1u << bits) - 1u)], 1u);
+        }
+        __syncthreads();
+        // thread i counts bins top - 2i and top - 2i - 1, from the largest down
+        const int hi = (1 << bits) - 1 - 2 * tid;
+        const uint32_t c0 = hi >= 0 ? hist[hi] : 0u, c1 = hi >= 1 ? hist[hi - 1] : 0u;
+        uint32_t total;
+        const uint32_t before = block_sum_before(c0 + c1, wsum, total);
+        if (before < need && need <= before + c0 + c1) {
+            const bool first = need <= before + c0;
+            found[0] = (uint32_t)(first ? hi : hi - 1);
+            found[1] = first ? before : before + c0;
+        }
+        __syncthreads();
+        prefix = (prefix << bits) | found[0];
+        need -= found[1];
+        __syncthreads();
+    }
+    // every token with a larger key, and the first `need` of those with the
+    // key itself, in ascending order
+    int32_t* list = p.list + ((long long)b * p.Hkv + h) * p.mbps * kBlock;
+    uint32_t above = 0, equal = 0;  // seen so far
+    for (int base = 0; base < quads; base += kSelThreads) {
+        const int t4 = base + tid;
+        uint32_t key[4] = {0u, 0u, 0u, 0u};
+        uint32_t gt = 0, eq = 0;
+        if (t4 < quads) {
+            load_keys(p, b, h, t4, key, false);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (4 * t4 + e >= s.old) continue;
+                gt += key[e] > prefix;
+                eq += key[e] == prefix;
+            }
+        }
+        uint32_t total;
+        const uint32_t before = block_sum_before((gt << 16) | eq, wsum, total);
+        uint32_t g = above + (before >> 16), q = equal + (before & 0xFFFFu);
+        if (t4 < quads) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * t4 + e;
+                if (t >= s.old) continue;
+                if (key[e] > prefix) {
+                    list[g + min(q, need)] = t;
+                    ++g;
+                } else if (key[e] == prefix) {
+                    if (q < need) list[g + q] = t;
+                    ++q;
+                }
+            }
+        }
+        above += total >> 16;
+        equal += total & 0xFFFFu;
+    }
+}
+
+// Rows of the cache (in units of one token of one head) that destination
+// token i of (b, h) comes from and goes to; -1 for a block id outside the cache.
+__device__ __forceinline__ int2 row_move(const EvictParams& p, const Share& s, int b, int h, int i) {
+    const int t = i < s.heavy ? p.list[((long long)b * p.Hkv + h) * p.mbps * kBlock + i] : s.old + (i - s.heavy);
+    const int from = __ldg(p.tables + (long long)b * p.mbps + t / kBlock);
+    const int to = __ldg(p.dst + (long long)b * p.mbps + i / kBlock);
+    const bool ok_f = from >= 0 && from < p.num_blocks, ok_t = to >= 0 && to < p.num_blocks;
+    if (!ok_f || !ok_t) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+    return make_int2(ok_f && ok_t ? (from * p.Hkv + h) * kBlock + t % kBlock : -1,
+                     ok_f && ok_t ? (to * p.Hkv + h) * kBlock + i % kBlock : -1);
+}
+
+// One work item: destination rows i0 .. i0 + 63 of (b, h). V16: 16-byte
+// vectors of a row.
+template <int V16>
+__device__ __forceinline__ void move_rows(const EvictParams& p, const Share& s, int b, int h, int i0, int2* rows) {
+    constexpr int kVecs = kMoveRows * V16 / kMoveThreads;  // per thread and cache
+    const int tid = threadIdx.x;
+    float sc = 0.f;
+    __syncthreads();  // the previous item is done with `rows` (and, in place, has written what it moves)
+    if (tid < kMoveRows) {
+        const int2 m = i0 + tid < s.kept ? row_move(p, s, b, h, i0 + tid) : make_int2(-1, -1);
+        rows[tid] = m;
+        if (m.x >= 0) sc = p.scores[m.x];
+    }
+    __syncthreads();
+    uint4 a[kVecs], c[kVecs];
+    int2 m[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+        const int i = u * kMoveThreads + tid;
+        m[u] = rows[i / V16];
+        if (m[u].x >= 0) {
+            a[u] = reinterpret_cast<const uint4*>(p.k)[(long long)m[u].x * V16 + i % V16];
+            c[u] = reinterpret_cast<const uint4*>(p.v)[(long long)m[u].x * V16 + i % V16];
+        }
+    }
+    // in place, a row may land on one that another thread of this item still
+    // has to read; rows of later items lie above everything written here
+    if (p.in_place) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+        const int i = u * kMoveThreads + tid;
+        if (m[u].x >= 0) {
+            reinterpret_cast<uint4*>(p.k)[(long long)m[u].y * V16 + i % V16] = a[u];
+            reinterpret_cast<uint4*>(p.v)[(long long)m[u].y * V16 + i % V16] = c[u];
+        }
+    }
+    if (tid < kMoveRows && rows[tid].x >= 0) p.scores[rows[tid].y] = sc;
+}
+
+template <int V16>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+    __shared__ long long sums[flat_words(kMoveThreads)];
+    __shared__ int2 rows[kMoveRows];
+    pdl_wait();
+    pdl_trigger();
+    if (p.in_place) {
+        // a kept row never moves up, so items in ascending order never
+        // overwrite a row that is still to be read: one block per (b, h)
+        const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+        const Share s = share_of(p, b);
+        if (s.kept == s.n) return;
+        for (int i0 = 0; i0 < s.kept; i0 += kMoveRows) move_rows<V16>(p, s, b, h, i0, rows);
+        return;
+    }
+    auto items = [&](int b) { return (long long)p.Hkv * ((share_of(p, b).kept + kMoveRows - 1) / kMoveRows); };
+    const long long total = flat_scan(p.B, items, sums);
+    for (long long x = blockIdx.x; x < total; x += gridDim.x) {
+        long long first;
+        const int b = flat_find(p.B, items, sums, x, first);
+        const Share s = share_of(p, b);
+        const int per = (s.kept + kMoveRows - 1) / kMoveRows;
+        const int o = (int)(x - first);
+        move_rows<V16>(p, s, b, o / per, (o % per) * kMoveRows, rows);
+    }
+}
+
+size_t list_bytes(const mi_dims& D) {
+    return ((size_t)D.B * D.Hkv * D.max_blocks_per_seq * kBlock * 4 + 255) / 256 * 256;
+}
+
+mi_status evict(const mi_dims* dims, void* k_cache, void* v_cache, float* scores, const int32_t* block_tables,
+                const int32_t* context_lens, const int32_t* budgets, int32_t recent, const int32_t* dst_tables,
+                int32_t* new_lens, void* workspace, size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream,
+                int elem) {
+    const mi_status ds = check_paged_dims(dims);
+    if (ds != MI_OK) return ds;
+    const mi_dims D = *dims;
+    if (recent < 0) return MI_ERR_INVALID_ARG;
+    if (D.B == 0) return MI_OK;
+    if (!k_cache || !v_cache || !scores || !block_tables || !context_lens || !budgets || !dst_tables || !new_lens ||
+        !workspace)
+        return MI_ERR_INVALID_ARG;
+    if (!aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(scores, 16) || !aligned_to(workspace, 16) ||
+        !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4) || !aligned_to(budgets, 4) ||
+        !aligned_to(dst_tables, 4) || !aligned_to(new_lens, 4))
+        return MI_ERR_INVALID_ARG;
+    if (workspace_bytes < list_bytes(D)) return MI_ERR_INVALID_ARG;
+    // every block reads the lengths, budgets and tables while one of them writes new_lens
+    const size_t lens_bytes = (size_t)D.B * 4, table_bytes = lens_bytes * D.max_blocks_per_seq;
+    if (overlaps(new_lens, lens_bytes, context_lens, lens_bytes) || overlaps(new_lens, lens_bytes, budgets, lens_bytes) ||
+        overlaps(new_lens, lens_bytes, block_tables, table_bytes) || overlaps(new_lens, lens_bytes, dst_tables, table_bytes))
+        return MI_ERR_INVALID_ARG;
+    if (dst_tables != block_tables && overlaps(dst_tables, table_bytes, block_tables, table_bytes))
+        return MI_ERR_INVALID_ARG;
+    if ((long long)D.B * D.Hkv > 0x7FFFFFFFLL) return MI_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms <= 0) return MI_ERR_CUDA;
+    EvictParams p;
+    p.k = static_cast<uint8_t*>(k_cache);
+    p.v = static_cast<uint8_t*>(v_cache);
+    p.scores = scores;
+    p.tables = block_tables;
+    p.lens = context_lens;
+    p.budgets = budgets;
+    p.dst = dst_tables;
+    p.new_lens = new_lens;
+    p.list = static_cast<int32_t*>(workspace);
+    p.dev_err = dev_err;
+    p.B = D.B;
+    p.Hkv = D.Hkv;
+    p.num_blocks = D.num_blocks;
+    p.mbps = D.max_blocks_per_seq;
+    p.recent = recent;
+    p.in_place = dst_tables == block_tables ? 1 : 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    const int units = D.B * D.Hkv;
+    if (launch_pdl(evict_select_kernel, units, kSelThreads, 0, st, p) != cudaSuccess) return MI_ERR_CUDA;
+    const int grid = p.in_place ? units : 8 * sms;
+    cudaError_t e;
+    switch (D.head_dim * elem / 16) {
+        case 4: e = launch_pdl(evict_move_kernel<4>, grid, kMoveThreads, 0, st, p); break;
+        case 8: e = launch_pdl(evict_move_kernel<8>, grid, kMoveThreads, 0, st, p); break;
+        default: e = launch_pdl(evict_move_kernel<16>, grid, kMoveThreads, 0, st, p); break;
+    }
+    return e == cudaSuccess ? MI_OK : MI_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace mi
+
+extern "C" size_t mi_paged_kv_evict_workspace_bytes(const mi_dims* dims) {
+    return mi::check_paged_dims(dims) == MI_OK ? mi::list_bytes(*dims) : 0;
+}
+
+extern "C" mi_status mi_paged_kv_evict(const mi_dims* dims, void* k_cache, void* v_cache, float* scores,
+                                       const int32_t* block_tables, const int32_t* context_lens,
+                                       const int32_t* budgets, int32_t recent, const int32_t* dst_tables,
+                                       int32_t* new_lens, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                       mi_stream_t stream) {
+    return mi::evict(dims, k_cache, v_cache, scores, block_tables, context_lens, budgets, recent, dst_tables, new_lens,
+                     workspace, workspace_bytes, dev_err, stream, 2);
+}
+
+extern "C" mi_status mi_paged_kv_evict_fp8(const mi_dims* dims, void* k_cache, void* v_cache, float* scores,
+                                           const int32_t* block_tables, const int32_t* context_lens,
+                                           const int32_t* budgets, int32_t recent, const int32_t* dst_tables,
+                                           int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                                           int32_t* dev_err, mi_stream_t stream) {
+    return mi::evict(dims, k_cache, v_cache, scores, block_tables, context_lens, budgets, recent, dst_tables, new_lens,
+                     workspace, workspace_bytes, dev_err, stream, 1);
+}

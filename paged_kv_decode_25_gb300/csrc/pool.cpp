@@ -150,6 +150,18 @@ extern "C" mi_status mi_kv_pool_free(mi_kv_pool* p, int32_t seq) {
     return MI_OK;
 }
 
+extern "C" mi_status mi_kv_pool_shrink(mi_kv_pool* p, int32_t seq, int32_t num_tokens) {
+    if (!p || num_tokens < 0) return MI_ERR_INVALID_ARG;
+    if (seq < 0 || (size_t)seq >= p->tables.size() || !p->live[(size_t)seq]) return MI_ERR_UNKNOWN_SEQ;
+    if (num_tokens > p->tokens[(size_t)seq]) return MI_ERR_INVALID_ARG;
+    std::vector<int32_t>& t = p->tables[(size_t)seq];
+    const size_t keep = (size_t)(((int64_t)num_tokens + p->block_size - 1) / p->block_size);
+    for (size_t i = keep; i < t.size(); ++i) p->free_stack.push_back(t[i]);
+    t.resize(keep);
+    p->tokens[(size_t)seq] = num_tokens;
+    return MI_OK;
+}
+
 extern "C" int32_t mi_kv_pool_num_free(const mi_kv_pool* p) {
     return p ? (int32_t)p->free_stack.size() : -1;
 }

@@ -38,6 +38,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "prefix.cuh"
 #include "tc.cuh"
 #include "tma.cuh"
 
@@ -63,6 +64,7 @@ struct PrefillParams {
     float sl2;                     // scale * log2(e)
     long long wait_ns;             // bound on every mbarrier wait of the launch
     int withhold;                  // failure-detection test: each producer withholds its first K copy
+    PrefixWork w;                  // attention over shared prefixes only
 };
 
 // The work item of a CTA: row tile k (counted from the request's end) of
@@ -880,6 +882,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // warp 16 issues the MMAs and owns the tensor memory; warp 17 loads Q once
 // and streams K (two stages, a 2 KB copy per block half) and V (two stages,
 // a 4 KB copy per block), K of stage j before V of stage j - 1.
+//
+// With PREFIX the same pipeline computes attention over shared prefixes (the
+// first launch of mi_paged_decode_attention_prefix): the rows are the (request,
+// head) pairs of up to 256 / G requests of a group, every one sees all keys of
+// the item's split, and each row's fp32 output and log-sum-exp go to the
+// item's slot. A group of at most 128 rows runs one Q tile.
 
 constexpr int kT2Keys = 128;                 // keys per stage
 constexpr int kT2Blocks = kT2Keys / kBlock;  // 16-token blocks per stage
@@ -905,7 +913,7 @@ struct Tc2Smem {
     static constexpr int kTotal = kTmem + 16 + 1024;  // slack to align the base to 1024 B
 };
 
-template <int HD>
+template <int HD, bool PREFIX = false>
 __global__ void __launch_bounds__(kT2Threads, 1)
     prefill_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, PrefillParams p) {
@@ -922,7 +930,30 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     // two tiles are consecutive, tr rows apart
     const int tr = (kTcRows / p.G) * p.G;
     Item it;
-    if (!work_item(p, 2 * tr, it)) return;
+    const int32_t* table;  // of the item's keys
+    int slot = 0;
+    bool two = true;       // both Q tiles hold rows
+    if constexpr (PREFIX) {
+        __shared__ long long sums[flat_words(kT2Threads)];
+        PrefixItem x;
+        if (!prefix_item(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, x)) return;
+        it.r = x.g;
+        it.h = x.h;
+        it.q0 = x.b0;
+        it.m = x.count;
+        it.n = x.n;
+        it.first = 0;
+        it.rho0 = 0;
+        it.nrows = it.rows_here = x.count * p.G;
+        it.p_hi = x.n - 1;
+        it.nblk = (x.n + kBlock - 1) / kBlock;
+        table = p.block_tables + (long long)x.g * p.mbps + x.blk0;
+        slot = x.slot;
+        two = it.nrows > tr;
+    } else {
+        if (!work_item(p, 2 * tr, it)) return;
+        table = p.block_tables + (long long)it.r * p.mbps;
+    }
     const int nst = (it.nblk + kT2Blocks - 1) / kT2Blocks;
     const uint32_t bar = sbase + SM::kBar;
     const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
@@ -957,8 +988,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         // ------------------------------------------------ producer warp --
         const uint64_t policy = l2_policy_evict_normal();
         if (lane == 0 && nst > 0) {
-            mbar_arrive_expect_tx(q_full, 2u * kH * (uint32_t)tr * 128u);
-            for (int t = 0; t < 2; ++t)
+            mbar_arrive_expect_tx(q_full, (two ? 2u : 1u) * kH * (uint32_t)tr * 128u);
+            for (int t = 0; t < (two ? 2 : 1); ++t)
                 for (int hh = 0; hh < kH; ++hh)
                     tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
                                 it.q0 + (it.rho0 + t * tr) / p.G, policy);
@@ -985,7 +1016,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         // the slot, so their load latency is hidden
         auto table_entry = [&](int jj) -> int {
             const int x = jj * kT2Blocks + lane;
-            return (lane < kT2Blocks && x < it.nblk) ? __ldg(p.block_tables + (long long)it.r * p.mbps + x) : -1;
+            return (lane < kT2Blocks && x < it.nblk) ? __ldg(table + x) : -1;
         };
         int nblk_next = table_entry(0);
         for (int j = 0; j < nst; ++j) {
@@ -1061,7 +1092,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             if (ok) {
                 tc::fence_after();
                 issue_s(0, 0);
-                issue_s(1, 0);
+                if (two) issue_s(1, 0);
                 tc::commit_elect(k_empty0);  // K(0) read by both tiles
             }
             for (int j = 0; ok && j < nst; ++j) {
@@ -1078,6 +1109,11 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     tc::fence_after();
                     issue_s(0, j + 1);
                 }
+                if (!two) {
+                    tc::commit_elect(v_empty0 + (j & 1) * 8);
+                    if (more) tc::commit_elect(k_empty0 + ((j + 1) % kT2KSlots) * 8);
+                    continue;
+                }
                 if (!(ok = wait_all(p_full0 + 8, ph, p.wait_ns))) break;
                 tc::fence_after();
                 issue_o(1, j);
@@ -1093,7 +1129,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             (void)wait_all(fin, 0, drain_limit(p.wait_ns));
         }
         __syncwarp();
-    } else {
+    } else if (two || ((warp >> 2) & 1) == 0) {
         // ---------------------------------------------------- softmax ----
         // Eight warps per tile. Warp w reads tensor-memory lanes lb ... lb + 15
         // (lb = 32 (w mod 4) + 16 (w / 8)) with the 16-lane shapes: lane i
@@ -1107,7 +1143,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         const int rra = it.rho0 + t * tr + rla, rrb = it.rho0 + t * tr + rlb;
         const bool va = rla < tr && rra < it.nrows, vb = rlb < tr && rrb < it.nrows;
         const int toka = rra / p.G, tokb = rrb / p.G;
-        const int posa = va ? it.first + toka : it.p_hi, posb = vb ? it.first + tokb : it.p_hi;
+        const int posa = va && !PREFIX ? it.first + toka : it.p_hi, posb = vb && !PREFIX ? it.first + tokb : it.p_hi;
         const int mposa = posa < 0 ? 0 : posa, mposb = posb < 0 ? 0 : posb;
         const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
         const uint32_t ts = tl + 128u;                                // S_t / P_t
@@ -1278,6 +1314,31 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         lra += __shfl_xor_sync(0xffffffffu, lra, 2);
         lrb += __shfl_xor_sync(0xffffffffu, lrb, 2);
         const float inva = lra > 0.f ? 1.f / lra : 0.f, invb = lrb > 0.f ? 1.f / lrb : 0.f;
+        if constexpr (PREFIX) {
+            const long long row = (long long)slot * (2 * tr) + t * tr + rla;  // row b: 8 further
+            float* pa = p.w.part + row * HD + 2 * c4;
+#pragma unroll 1
+            for (int ch = 0; ch < HD / 32; ++ch) {
+                uint32_t y[16];
+                if (!ok) break;
+                tc::ld16x256_x4(tl + 32u * ch, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float* at = pa + 32 * ch + 8 * k;
+                    if (va)
+                        *reinterpret_cast<float2*>(at) =
+                            make_float2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva);
+                    if (vb)
+                        *reinterpret_cast<float2*>(at + 8 * HD) =
+                            make_float2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb);
+                }
+            }
+            if (c4 == 0 && ok) {
+                if (va) p.w.part_lse[row] = lra > 0.f ? mra_run + log2f(lra) : -INFINITY;
+                if (vb) p.w.part_lse[row + 8] = lrb > 0.f ? mrb_run + log2f(lrb) : -INFINITY;
+            }
+        } else {
         const uint32_t keepa = posa >= 0 ? 0xFFFFFFFFu : 0u, keepb = posb >= 0 ? 0xFFFFFFFFu : 0u;  // rows before position 0 are +0
         uint16_t* orowa = p.out + ((long long)(it.q0 + toka) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
         uint16_t* orowb = p.out + ((long long)(it.q0 + tokb) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
@@ -1304,6 +1365,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                             keepb;
                 }
             }
+        }
         }
     }
     tc::fence_before();
@@ -1336,11 +1398,11 @@ bool prepare_tc() {
     return raise_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<HD>), TcSmem<HD>::kTotal, done, mu);
 }
 
-template <int HD>
+template <int HD, bool PREFIX = false>
 bool prepare_tc2() {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD>), Tc2Smem<HD>::kTotal, done, mu);
+    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD, PREFIX>), Tc2Smem<HD>::kTotal, done, mu);
 }
 
 template <int HD>
@@ -1441,6 +1503,45 @@ mi_status prefill(const mi_dims* dims, int32_t total_q, int32_t max_query_len, c
 }
 
 }  // namespace
+
+mi_status prefix_partials(const mi_dims* dims, int32_t max_prefix_blocks, const void* q, const void* k_cache,
+                          const void* v_cache, const int32_t* prefix_tables, float scale, const PrefixWork& work,
+                          long long slots, int32_t* dev_err, mi_stream_t stream) {
+    const mi_dims D = *dims;
+    const int G = D.Hq / D.Hkv, HD = D.head_dim;
+    PrefillParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.block_tables = prefix_tables;
+    p.context_lens = nullptr;
+    p.query_start = nullptr;
+    p.out = nullptr;
+    p.dev_err = dev_err;
+    p.R = work.P;
+    p.Hq = D.Hq;
+    p.Hkv = D.Hkv;
+    p.G = G;
+    p.num_blocks = D.num_blocks;
+    p.mbps = max_prefix_blocks;
+    p.T = D.B;
+    p.max_q = 0;
+    p.sl2 = scale * 1.4426950408889634f;
+    p.wait_ns = test_wait_limit_ns();
+    p.withhold = test_withhold_copy() ? 1 : 0;
+    p.w = work;
+    const long long rows = (long long)D.num_blocks * D.Hkv * kBlock;
+    if (!(HD == 64 ? prepare_tc2<64, true>() : prepare_tc2<128, true>())) return MI_ERR_CUDA;
+    CUtensorMap tq, tk, tv;
+    if (!make_tmap_q_group(&tq, q, D.B, D.Hq, HD, G, (kTcRows / G) * G) ||
+        !make_tmap_kv_halves(&tk, k_cache, rows, HD) || !make_tmap_kv_blocks(&tv, v_cache, rows, HD))
+        return MI_ERR_CUDA;
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e =
+        HD == 64 ? launch_pdl(prefill_tc2_kernel<64, true>, (int)slots, kT2Threads, Tc2Smem<64>::kTotal, st, tq, tk, tv, p)
+                 : launch_pdl(prefill_tc2_kernel<128, true>, (int)slots, kT2Threads, Tc2Smem<128>::kTotal, st, tq, tk,
+                              tv, p);
+    return e == cudaSuccess ? MI_OK : MI_ERR_CUDA;
+}
+
 }  // namespace mi
 
 extern "C" mi_status mi_paged_prefill_attention(const mi_dims* dims, int32_t total_q, int32_t max_query_len,

@@ -6,25 +6,26 @@
 //
 // A weight needs its row's log-sum-exp over all keys, so the logits x are
 // computed twice: the first launch reduces them over the keys of each row, the
-// second over the rows of each key. (Kept in memory they would be 4 bytes a
+// last over the rows of each key (a small one between merges split rows). (Kept in memory they would be 4 bytes a
 // pair each way, 0.5 GB for 16 windows of 64 tokens over 85,000 keys; the second
 // product costs a tenth of that time.) V is never read.
 //
-// Both launches are one pipeline on the fifth-generation tensor cores. An item
+// The two are one pipeline on the fifth-generation tensor cores. An item
 // holds up to two 128-row tiles X of one operand in shared memory and streams
 // 128-row tiles Y of the other past them, S = X . Y^T (tcgen05.mma, M 128, N 128):
 //   * kLse: X = (query token, head) rows of a request, Y = its keys; a row's
 //     keys may be split over several items (partial log-sum-exps);
 //   * kSum: X = keys, Y = query rows, from the first that sees a key.
-// A thread then owns one row of S (a tensor-memory lane) and half its columns,
-// so both reductions are private to a thread until the item's end.
-//   warps 0-15   softmax: group (warp / 8) takes every second S tile; warp w
-//                reads lanes 32 (w mod 4) .. + 31, columns 64 (w / 4 mod 2) .. + 63
+// A thread then owns one row of an S tile (a tensor-memory lane), so both
+// reductions are private to a thread until the item's end.
+//   warps 0-15   softmax: group g (four warps, one per scheduler) takes every
+//                fourth S tile, warp w its lanes 32 (w mod 4) .. + 31
 //   warp 16      issues the MMAs and owns the tensor memory (four S tiles)
-//   warp 17      streams X (two slots, so the next item's X lands early) and Y
-//   warp 18      kSum: the Y rows' log-sum-exps, merged from their splits
-// The exponentials bound both launches: 16 a clock and SM, against 28 pairs a
-// clock for the product.
+//   warp 17      picks the items, streams X (two slots, so the next item's X
+//                lands early) and Y
+//   warp 18      kSum: the Y rows' log-sum-exps
+// An S tile costs about 530 clocks of tensor core, 512 of exponentials (32 a
+// clock and SM) and 400 issue slots a scheduler at 3 instructions a logit.
 #include <cmath>
 
 #include "batch.cuh"
@@ -35,10 +36,11 @@ namespace {
 
 constexpr int kLse = 0, kSum = 1;
 constexpr int kTile = 128;
-constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kLseWarp = 18;
+constexpr int kSoftWarps = 16, kGroups = 4, kMmaWarp = 16, kLoadWarp = 17, kLseWarp = 18;
 constexpr int kThreads = 19 * 32;
-constexpr int kYSlots = 2, kSBufs = 4, kMaskSlots = 8, kLseSlots = 4;
+constexpr int kYSlots = 2, kMaskSlots = 8, kLseSlots = 8, kItemSlots = 4;
 constexpr uint32_t kCols = 512;
+constexpr int kMergeThreads = 256;
 
 template <int HD>
 struct WinSmem {
@@ -47,11 +49,12 @@ struct WinSmem {
     static constexpr int kX = 0;                          // [2 slots][2 tiles]
     static constexpr int kY = 4 * kT;                     // [kYSlots]
     static constexpr int kLses = kY + kYSlots * kT;       // [kLseSlots][128] fp32
-    static constexpr int kComb = kLses + kLseSlots * kTile * 4;  // [2][2][2][128] float2
-    static constexpr int kSums = kComb + 8 * kTile * 8;
+    static constexpr int kComb = kLses + kLseSlots * kTile * 4;  // [2][kGroups][128] float2
+    static constexpr int kItems = kComb + 2 * kGroups * kTile * 8;
+    static constexpr int kSums = kItems + kItemSlots * 64;
     static constexpr int kMask = kSums + flat_words(kThreads) * 8;
     static constexpr int kBar = (kMask + kMaskSlots * 4 + 7) / 8 * 8;
-    static constexpr int kNBar = 4 + 2 * kYSlots + 2 * kSBufs + 2 * kLseSlots + 1;
+    static constexpr int kNBar = 4 + 2 * kYSlots + 2 * kGroups + 2 * kLseSlots + 2 * kItemSlots + 1;
     static constexpr int kTmem = kBar + kNBar * 8;        // the tensor-memory base, then two words: a wait ran out
     static constexpr int kTotal = kTmem + 16 + 1024;      // slack to align the base to 1024 B
 };
@@ -61,6 +64,8 @@ struct WindowParams {
     const int32_t* lens;           // [R]
     const int32_t* query_start;    // [R + 1]
     float* part;                   // [T][Hq][splits] partial log-sum-exps, base 2
+    float* nlse;                   // [Hkv][T][G] the rows' negated log-sum-exps (-inf: no key)
+    unsigned int* next;            // kSum: the next item
     float* scores;                 // [num_blocks][Hkv][16]
     int32_t* dev_err;
     int R, Hq, Hkv, G, num_blocks, mbps, T, max_q, fresh;
@@ -124,11 +129,12 @@ __device__ int split_tiles(const WindowParams& p, long long* sums, int* shared_m
     return max(step, 4);
 }
 
-// One work item: X tiles xt (0: nothing to do), Y tiles y0 .. y1-1.
-struct Item {
-    int r, h, xt, y0, y1, row0, split;  // row0: the first query row (kLse) or key (kSum) of X
+// One work item: X tiles xt (0: the list is over), Y tiles y0 .. y1-1.
+struct __align__(16) Item {
+    int r, h, xt, y0, y1, row0, split, pad;  // row0: the first query row (kLse) or key (kSum) of X
     Request x;
 };
+static_assert(sizeof(Item) <= 64, "an item's place in shared memory");
 
 template <int MODE>
 __device__ __forceinline__ long long item_count(const WindowParams& p, int r, int step, int xtiles) {
@@ -148,7 +154,7 @@ __device__ __forceinline__ Item item_at(const WindowParams& p, const long long* 
     it.h = o % p.Hkv;
     it.split = 0;
     if (MODE == kLse) {
-        const int pairs = row_pairs(p, it.x), pt = o / p.Hkv % pairs;
+        const int pairs = row_pairs(p, it.x), pt = pairs - 1 - o / p.Hkv % pairs;  // the longest first
         it.split = o / p.Hkv / pairs;
         it.row0 = pt * 2 * tr;
         it.xt = rows - it.row0 > tr ? 2 : 1;
@@ -178,12 +184,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
     unsigned char* base = smem_raw + (sbase - raw);
     long long* sums = reinterpret_cast<long long*>(base + SM::kSums);
-    float* lses = reinterpret_cast<float*>(base + SM::kLses);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t bar = sbase + SM::kBar;
     const uint32_t x_full = bar, x_empty = bar + 16, y_full = bar + 32, y_empty = y_full + 8 * kYSlots;
-    const uint32_t s_full = y_empty + 8 * kYSlots, s_empty = s_full + 8 * kSBufs;
-    const uint32_t l_full = s_empty + 8 * kSBufs, l_empty = l_full + 8 * kLseSlots, fin = l_empty + 8 * kLseSlots;
+    const uint32_t s_full = y_empty + 8 * kYSlots, s_empty = s_full + 8 * kGroups;
+    const uint32_t l_full = s_empty + 8 * kGroups, l_empty = l_full + 8 * kLseSlots;
+    const uint32_t i_full = l_empty + 8 * kLseSlots, i_empty = i_full + 8 * kItemSlots, fin = i_empty + 8 * kItemSlots;
     volatile int* failed = reinterpret_cast<volatile int*>(base + SM::kTmem + 4);
     const uint32_t mask0 = sbase + SM::kMask;
 
@@ -196,13 +202,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(y_full + 8 * i, 1);
             mbar_init(y_empty + 8 * i, 1);
         }
-        for (int i = 0; i < kSBufs; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
             mbar_init(s_full + 8 * i, 2);   // the MMAs' commit, and the issuing warp (for what it has seen)
-            mbar_init(s_empty + 8 * i, 8);  // the warps of a group
+            mbar_init(s_empty + 8 * i, 4);  // the warps of a group
         }
         for (int i = 0; i < kLseSlots; ++i) {
-            mbar_init(l_full + 8 * i, 1);
+            mbar_init(l_full + 8 * i, 32);  // the copying lanes
             mbar_init(l_empty + 8 * i, kSoftWarps);
+        }
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(i_full + 8 * i, 1);
+            mbar_init(i_empty + 8 * i, kSoftWarps + 1 + (MODE == kSum ? 1 : 0));  // every warp that reads items
         }
         mbar_init(fin, 1);
         failed[0] = failed[1] = 0;
@@ -235,16 +245,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ascend) {
         step = split_tiles(p, sums, reinterpret_cast<int*>(base + SM::kMask));
         if (MODE == kSum) {
-            // single tiles of keys while pairs would leave SMs without one
+            // single tiles of keys while pairs would leave SMs with few
             total = flat_scan(p.R, [&](int r) { return item_count<MODE>(p, r, step, 2); }, sums);
-            if (total < 2LL * p.sms) xtiles = 1;
+            if (total < 4LL * p.sms) xtiles = 1;
         }
         __syncthreads();
         if (MODE == kLse || xtiles == 1)
             total = flat_scan(p.R, [&](int r) { return item_count<MODE>(p, r, step, xtiles); }, sums);
     }
     const int tr = kTile / p.G * p.G;
-    auto item = [&](long long i) { return item_at<MODE>(p, sums, i, step, xtiles); };
+    // the k-th item of the list as every other warp sees it
+    auto take = [&](uint32_t k, Item& it) -> bool {
+        const uint32_t sl = k % kItemSlots;
+        if (!wait_warp(i_full + 8 * sl, (k / kItemSlots) & 1, p.wait_ns)) return false;
+        it = *reinterpret_cast<const Item*>(base + SM::kItems + sl * 64);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i_empty + 8 * sl);
+        return true;
+    };
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------- loads ----
@@ -253,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t xc = 0, yc = 0;
         bool ok = true;
         // key tile j of the item's request to dst: 16-token blocks, each as kH
-        // 64-column halves; returns the tile's mask of blocks in the cache
+        // 64-column halves; kLse posts the tile's mask of blocks in the cache
         auto load_keys = [&](const Item& it, uint32_t dst, uint32_t fb, int j, int tiles) {
             const int b0 = j * (kTile / kBlock), x = b0 + lane;
             bool have = lane < tiles * (kTile / kBlock) && x * kBlock < it.x.n;
@@ -285,9 +303,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-            const Item it = item(i);
-            if (it.xt == 0 || it.y0 >= it.y1) continue;
+        // kLse deals the list out back and forth (it goes from long to short);
+        // kSum's items are taken from a counter as blocks get free
+        auto pick = [&](long long k) -> long long {
+            if (MODE == kLse) return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            unsigned int i = 0;
+            if (lane == 0) i = atomicAdd(p.next, 1u);
+            return (long long)__shfl_sync(0xffffffffu, i, 0);
+        };
+        long long k = 0, i = pick(0);
+        uint32_t ic = 0;
+        for (;;) {
+            Item it;
+            it.xt = 0;
+            if (i < total) {
+                it = item_at<MODE>(p, sums, i, step, xtiles);
+                if (MODE == kLse && it.y0 >= it.y1) {  // keys past what the rows see
+                    i = pick(++k);
+                    continue;
+                }
+            }
+            const uint32_t sl = ic % kItemSlots;
+            if (!(ok = wait_warp(i_empty + 8 * sl, ((ic / kItemSlots) & 1) ^ 1, p.wait_ns))) break;
+            if (lane == 0) {
+                *reinterpret_cast<Item*>(base + SM::kItems + sl * 64) = it;
+                mbar_arrive(i_full + 8 * sl);
+            }
+            __syncwarp();
+            ++ic;
+            if (it.xt == 0) break;
+            i = pick(++k);
+            if (it.y0 >= it.y1) continue;
             const uint32_t xs = xc & 1;
             if (!(ok = wait_warp(x_empty + 8 * xs, ((xc >> 1) & 1) ^ 1, p.wait_ns))) break;
             const uint32_t xd = sbase + SM::kX + xs * 2 * SM::kT;
@@ -306,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else
                     load_rows(it, yd, y_full + 8 * ys, j * tr, 1);
             }
+            if (!ok) break;
         }
         if (!ok) {
             if (lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
@@ -320,16 +367,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id = tc::idesc_bf16(kTile, kTile, false);
         uint32_t xc = 0, yc = 0, sc = 0;
         bool ok = true;
-        for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-            const Item it = item(i);
-            if (it.xt == 0 || it.y0 >= it.y1) continue;
+        for (uint32_t ic = 0; ok; ++ic) {
+            Item it;
+            if (!(ok = take(ic, it)) || it.xt == 0) break;
+            if (it.y0 >= it.y1) continue;
             if (!(ok = wait_warp(x_full + 8 * (xc & 1), (xc >> 1) & 1, p.wait_ns))) break;
             for (int j = it.y0; ok && j < it.y1; ++j, ++yc) {
                 if (!(ok = wait_warp(y_full + 8 * (yc % kYSlots), (yc / kYSlots) & 1, p.wait_ns))) break;
                 const uint32_t ya = sbase + SM::kY + (yc % kYSlots) * SM::kT;
                 for (int t = 0; t < it.xt; ++t, ++sc) {
-                    const uint32_t b = sc % kSBufs;
-                    if (!(ok = wait_warp(s_empty + 8 * b, ((sc / kSBufs) & 1) ^ 1, p.wait_ns))) break;
+                    const uint32_t b = sc % kGroups;
+                    if (!(ok = wait_warp(s_empty + 8 * b, ((sc / kGroups) & 1) ^ 1, p.wait_ns))) break;
                     tc::fence_after();
                     const uint32_t xa = sbase + SM::kX + ((xc & 1) * 2 + t) * SM::kT;
 #pragma unroll
@@ -356,55 +404,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------- the rows' log-sum-exps ----
             uint32_t yc = 0;
             bool ok = true;
-            for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-                const Item it = item(i);
+            for (uint32_t ic = 0; ok; ++ic) {
+                Item it;
+                if (!(ok = take(ic, it)) || it.xt == 0) break;
                 const int rows = it.x.m * p.G;
+                const float* at = p.nlse + ((long long)it.h * p.T + it.x.q0) * p.G;
                 for (int j = it.y0; j < it.y1; ++j, ++yc) {
-                    const int nsp = ceil_div(seen_tiles(p, it.x, j >> 1), step);
-                    float l[kTile / 32];
-#pragma unroll
-                    for (int u = 0; u < kTile / 32; ++u) {
-                        const int c = u * 32 + lane, rho = j * tr + c;
-                        float M = -INFINITY, sum = 0.f;
-                        if (c < tr && rho < rows) {
-                            const float* at = p.part + ((long long)(it.x.q0 + rho / p.G) * p.Hq + (long long)it.h * p.G + rho % p.G) * p.splits;
-                            for (int s = 0; s < nsp; ++s) {
-                                const float v = __ldcg(at + s);
-                                const float n = fmaxf(M, v);
-                                if (n != -INFINITY) sum = sum * exp2f(M - n) + exp2f(v - n);
-                                M = n;
-                            }
-                        }
-                        // a row without keys: every weight is 2^-inf
-                        l[u] = sum > 0.f ? -(M + log2f(sum)) : -INFINITY;
-                    }
+                    // copied without a wait, so the ring is filled ahead; zero
+                    // past the tile's rows
                     const uint32_t ls = yc % kLseSlots;
                     if (!(ok = wait_warp(l_empty + 8 * ls, ((yc / kLseSlots) & 1) ^ 1, p.wait_ns))) break;
 #pragma unroll
-                    for (int u = 0; u < kTile / 32; ++u) lses[ls * kTile + u * 32 + lane] = l[u];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(l_full + 8 * ls);
+                    for (int u = 0; u < kTile / 32; ++u) {
+                        const int c = u * 32 + lane, rho = j * tr + c;
+                        const bool in = c < tr && rho < rows;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                         sbase + SM::kLses + (ls * kTile + c) * 4),
+                                     "l"(at + (in ? rho : 0)), "r"(in ? 4 : 0)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(l_full + 8 * ls) : "memory");
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
         }
     } else {
         // ---------------------------------------------------- softmax ----
-        const int group = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+        const int group = warp >> 2, quad = warp & 3;
         const int my = quad * 32 + lane;  // row of a tile, tensor-memory lane
-        const uint32_t ts = tbase + ((uint32_t)(quad * 32) << 16) + 64u * half;
+        const uint32_t ts = tbase + ((uint32_t)(quad * 32) << 16) + (uint32_t)(group * kTile);
         const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
         const bool pos_scale = p.sl2 > 0.f;
         const float off_value = pos_scale ? -INFINITY : INFINITY;  // a masked logit, before the scale
-        uint32_t yc = 0, sc = 0, ic = 0;
+        uint32_t yc = 0, sc = 0;
         bool ok = true;
-        for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-            const Item it = item(i);
-            if (it.xt == 0) continue;
+        for (uint32_t ic = 0;; ++ic) {
+            Item it;
+            if (!take(ic, it)) {
+                ok = false;
+                it.xt = 1;
+                it.y0 = it.y1 = 0;
+                it.x.m = it.x.n = 0;
+            }
+            if (it.xt == 0) break;
             const int rows = it.x.m * p.G;
             // kLse: the last key this thread's row sees; kSum: the first row
             // that sees this thread's key
-            const int tile = it.xt == 2 ? group ^ (int)(sc & 1) : 0;  // this group's S tiles of the item
+            const int tile = it.xt == 2 ? (group ^ (int)sc) & 1 : 0;  // this group's S tiles of the item
             int bound;
             bool mine;
             if (MODE == kLse) {
@@ -416,106 +463,135 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mine = t < it.x.n;
                 bound = mine ? max(0, t - it.x.first) * p.G : 0;
             }
-            float m = -INFINITY;
-            uint64_t acc[2] = {0ull, 0ull};
+            float m = -INFINITY, total_sum = 0.f;  // kLse: the sum is relative to 2^m
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+            // f(x, q) for the S tile's four chunks of 32 columns, the next one
+            // loaded under the arithmetic of the one at hand
+            auto sweep = [&](auto f) {
+                uint32_t xa[32], xb[32];
+                tc::ld32(ts, xa);
+#pragma unroll 1
+                for (int q = 0; q < 4; q += 2) {
+                    tc::wait_ld();
+                    tc::ld32(ts + 32u * q + 32u, xb);
+                    f(xa, q);
+                    tc::wait_ld();
+                    if (q == 0) tc::ld32(ts + 64u, xa);
+                    f(xb, q + 1);
+                }
+            };
+            // columns lo .. hi - 1 of a chunk count
+            auto cut = [&](uint32_t (&x)[32], int lo, int hi) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < lo || c >= hi) x[c] = __float_as_uint(off_value);
+            };
             for (int j = it.y0; ok && j < it.y1; ++j, ++yc) {
                 if (MODE == kSum &&
                     !(ok = wait_warp(l_full + 8 * (yc % kLseSlots), (yc / kLseSlots) & 1, p.wait_ns)))
                     break;
-                for (int t = 0; t < it.xt; ++t, ++sc) {
-                    if ((int)(sc & 1) != group) continue;
-                    const uint32_t b = sc % kSBufs;
-                    if (!(ok = wait_warp(s_full + 8 * b, (sc / kSBufs) & 1, p.wait_ns))) break;
+                // this group's S tile of the stage, if it has one
+                const int t = (group - (int)sc) & (kGroups - 1);
+                if (t < it.xt) {
+                    if (!(ok = wait_warp(s_full + 8 * group, ((sc + t) / kGroups) & 1, p.wait_ns))) break;
                     tc::fence_after();
-                    uint32_t x[64];
-                    tc::ld32(ts + b * kTile, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-                    tc::ld32(ts + b * kTile + 32u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-                    tc::wait_ld();
-                    tc::fence_before();
-                    __syncwarp();
                     if (MODE == kLse) {
-                        const uint32_t msk = (lds32(mask0 + (yc % kMaskSlots) * 4) >> (4 * half)) & 0xFu;
-                        if (lane == 0) mbar_arrive(s_empty + 8 * b);
-                        const int key0 = j * kTile + 64 * half;
-                        if (!__all_sync(0xffffffffu, msk == 0xFu && key0 + 63 <= bound)) {
+                        const uint32_t msk = lds32(mask0 + (yc % kMaskSlots) * 4);
+                        const bool part = __any_sync(0xffffffffu, msk != 0xFFu || j * kTile + kTile - 1 > bound);
+                        auto mask = [&](uint32_t (&x)[32], int q) {
+                            if (!part) return;
+                            const uint32_t have = (msk >> (2 * q)) & 3u;
+                            const int hi = bound - (j * kTile + 32 * q) + 1;
+                            cut(x, have & 1u ? 0 : 16, have & 2u ? hi : min(hi, 16));
+                        };
+                        // The sum is relative to m, the largest of the first
+                        // tile's logits: fp32 holds it however far later ones
+                        // lie below, and above until it nears overflow. Only
+                        // then, and at first, is a maximum taken and the sum
+                        // moved to it.
+                        bool top = __any_sync(0xffffffffu, m == -INFINITY);
+                        for (;;) {
+                            if (top) {
+                                float e4[4] = {off_value, off_value, off_value, off_value};
+                                sweep([&](uint32_t (&x)[32], int q) {
+                                    mask(x, q);
 #pragma unroll
-                            for (int c = 0; c < 64; ++c)
-                                if (!((msk >> (c >> 4)) & 1u) || key0 + c > bound) x[c] = __float_as_uint(off_value);
-                        }
-                        float e4[4];
+                                    for (int c = 0; c < 32; ++c)
+                                        e4[c & 3] = pos_scale ? fmaxf(e4[c & 3], __uint_as_float(x[c]))
+                                                              : fminf(e4[c & 3], __uint_as_float(x[c]));
+                                });
+                                const float best = (pos_scale ? fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]))
+                                                              : fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]))) * p.sl2;
+                                total_sum *= best > m ? ex2(m - best) : 1.f;
+                                m = fmaxf(m, best);
+                            }
+                            const float nu = m == -INFINITY ? 0.f : -m;
+                            const uint64_t nu2 = tc::f2(nu, nu);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) e4[c] = off_value;
-                        if (pos_scale) {
+                            for (int c = 0; c < 4; ++c) acc[c] = 0ull;
+                            sweep([&](uint32_t (&x)[32], int q) {
+                                mask(x, q);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                e4[c & 3] = tc::max3(e4[c & 3], __uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) e4[c & 3] = fminf(e4[c & 3], __uint_as_float(x[c]));
-                        }
-                        const float ext = pos_scale ? fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]))
-                                                    : fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
-                        const float mn = fmaxf(m, ext * p.sl2);
-                        const float u = mn == -INFINITY ? 0.f : mn;
-                        const float al = ex2(m - u);
-                        m = mn;
-                        const uint64_t al2 = tc::f2(al, al), nu2 = tc::f2(-u, -u);
-                        acc[0] = tc::fma2(acc[0], al2, 0ull);
-                        acc[1] = tc::fma2(acc[1], al2, 0ull);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const uint64_t a = tc::fma2(tc::f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nu2);
-                            acc[c & 1] = tc::add2(acc[c & 1], tc::f2(ex2(tc::f2_lo(a)), ex2(tc::f2_hi(a))));
+                                for (int c = 0; c < 16; ++c) {
+                                    const uint64_t a = tc::fma2(tc::f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nu2);
+                                    acc[c & 3] = tc::add2(acc[c & 3], tc::f2(ex2(tc::f2_lo(a)), ex2(tc::f2_hi(a))));
+                                }
+                            });
+                            const uint64_t a2 = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
+                            const float now = total_sum + (tc::f2_lo(a2) + tc::f2_hi(a2));
+                            if (top || !__any_sync(0xffffffffu, now > 0x1p100f)) {
+                                total_sum = now;
+                                break;
+                            }
+                            top = true;
                         }
                     } else {
-                        if (lane == 0) mbar_arrive(s_empty + 8 * b);
-                        const uint32_t la = sbase + SM::kLses + ((yc % kLseSlots) * kTile + 64 * half) * 4;
-                        const int rho0 = j * tr + 64 * half, end = min(rows, (j + 1) * tr);
-                        if (__all_sync(0xffffffffu, bound <= rho0) && rho0 + 64 <= end) {
+                        const int end = min(rows, (j + 1) * tr);
+                        const bool part = __any_sync(0xffffffffu, bound > j * tr || j * tr + kTile > end);
+                        const uint32_t la = sbase + SM::kLses + (yc % kLseSlots) * kTile * 4;
+                        sweep([&](uint32_t (&x)[32], int q) {
+                            if (part) cut(x, bound - (j * tr + 32 * q), end - (j * tr + 32 * q));
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) {
+                            for (int c = 0; c < 8; ++c) {
                                 uint32_t l0, l1, l2, l3;
-                                lds128(la + 16 * c, l0, l1, l2, l3);
+                                lds128(la + 128 * q + 16 * c, l0, l1, l2, l3);
                                 const uint64_t a0 = tc::fma2(tc::f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sc2,
                                                              tc::f2(__uint_as_float(l0), __uint_as_float(l1)));
                                 const uint64_t a1 = tc::fma2(tc::f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sc2,
                                                              tc::f2(__uint_as_float(l2), __uint_as_float(l3)));
-                                acc[0] = tc::add2(acc[0], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
-                                acc[1] = tc::add2(acc[1], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
+                                acc[(2 * c) & 3] = tc::add2(acc[(2 * c) & 3], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
+                                acc[(2 * c + 1) & 3] = tc::add2(acc[(2 * c + 1) & 3], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
                             }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const float l0 = __uint_as_float(lds32(la + 8 * c)), l1 = __uint_as_float(lds32(la + 8 * c + 4));
-                                const int r0 = rho0 + 2 * c, r1 = r0 + 1;
-                                const float w0 = r0 >= bound && r0 < end ? ex2(__fmaf_rn(__uint_as_float(x[2 * c]), p.sl2, l0)) : 0.f;
-                                const float w1 = r1 >= bound && r1 < end ? ex2(__fmaf_rn(__uint_as_float(x[2 * c + 1]), p.sl2, l1)) : 0.f;
-                                acc[c & 1] = tc::add2(acc[c & 1], tc::f2(w0, w1));
-                            }
-                        }
+                        });
                     }
+                    // the tile has been read: hand it back
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty + 8 * group);
                 }
+                sc += it.xt;
                 if (MODE == kSum) {
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(l_empty + 8 * (yc % kLseSlots));
                 }
             }
-            // the threads that share a row: two column halves, and for a
-            // single tile the two groups
-            const uint64_t a = tc::add2(acc[0], acc[1]);
-            const float sum = tc::f2_lo(a) + tc::f2_hi(a);
-            float2* comb = reinterpret_cast<float2*>(base + SM::kComb) + (ic & 1) * 4 * kTile;
-            // a warp whose wait ran out still meets the others here, and all
-            // of them leave together
+            // the groups that share a row: every second one, or all four for a
+            // single tile. A warp whose wait ran out still meets the others
+            // here, and all of them leave together.
+            float sum = total_sum;
+            if (MODE == kSum) {
+                const uint64_t a = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
+                sum = tc::f2_lo(a) + tc::f2_hi(a);
+            }
+            float2* comb = reinterpret_cast<float2*>(base + SM::kComb) + (ic & 1) * kGroups * kTile;
             if (!ok && lane == 0) failed[ic & 1] = 1;
-            comb[(half * 2 + group) * kTile + my] = make_float2(m, sum);
+            comb[group * kTile + my] = make_float2(m, sum);
             asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
             if (failed[ic & 1]) {
                 ok = false;
                 break;
             }
-            ++ic;
-            if (half == 0 && mine && (it.xt == 2 || group == 0)) {
+            if (mine && group < it.xt) {
                 float2 q[4];
                 const int parts = it.xt == 2 ? 2 : 4;
 #pragma unroll
@@ -528,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     (q[2].y * exp2f(q[2].x - v) + q[3].y * exp2f(q[3].x - v));
                     const int rho = it.row0 + tile * tr + my;
                     p.part[((long long)(it.x.q0 + rho / p.G) * p.Hq + (long long)it.h * p.G + rho % p.G) * p.splits + it.split] =
-                        l > 0.f ? M + log2f(l) : -INFINITY;
+                        l == 0.f ? -INFINITY : M + log2f(l);
                 } else {
                     const float w = (q[0].y + q[1].y) + (q[2].y + q[3].y);
                     const int t = it.row0 + tile * kTile + my;
@@ -550,6 +626,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Each row's log-sum-exp from its splits (one launch between the two: the
+// second reads every row once per 256 keys), and kSum's item counter back to
+// zero. A thread merges one row.
+__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p) {
+    __shared__ long long sums[flat_words(kMergeThreads)];
+    __shared__ int most;
+    pdl_wait();
+    pdl_trigger();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0u;
+    if (!starts_ascend(p.query_start, p.R, p.T)) return;
+    const int step = split_tiles(p, sums, &most);
+    const long long row = (long long)blockIdx.x * kMergeThreads + threadIdx.x;
+    const int i = (int)(row / p.Hq);
+    if (i < __ldg(p.query_start) || i >= __ldg(p.query_start + p.R)) return;
+    int lo = 0, hi = p.R;  // query_start[lo] <= i < query_start[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.query_start + mid) <= i) lo = mid;
+        else hi = mid;
+    }
+    const Request x = request_of(p, lo);
+    if (x.m < 0) return;
+    const int n = ceil_div(seen_tiles(p, x, (i - x.q0) / (2 * (kTile / p.G))), step);
+    const float* at = p.part + row * p.splits;
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) M = fmaxf(M, __ldcg(at + s));
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+        const float v = __ldcg(at + s);
+        sum += v == -INFINITY ? 0.f : exp2f(v - M);
+    }
+    p.nlse[((long long)(row % p.Hq / p.G) * p.T + i) * p.G + row % p.G] = sum == 0.f ? -INFINITY : -(M + log2f(sum));
+}
+
 // Places for partial log-sum-exps per row: enough splits that few row tiles
 // still fill the GPU, fewer where the rows themselves are many.
 int split_places(const mi_dims& D, int32_t total_q) {
@@ -557,8 +668,10 @@ int split_places(const mi_dims& D, int32_t total_q) {
     return rows <= (1LL << 20) ? 32 : rows <= (1LL << 23) ? 8 : 2;
 }
 
+size_t lse_bytes(const mi_dims& D, int32_t total_q) { return ((size_t)total_q * D.Hq * 4 + 255) / 256 * 256; }
+
 size_t window_bytes(const mi_dims& D, int32_t total_q) {
-    return ((size_t)total_q * D.Hq * split_places(D, total_q) * 4 + 255) / 256 * 256 + 256;
+    return lse_bytes(D, total_q) * (1 + split_places(D, total_q)) + 256;
 }
 
 bool window_sizes_ok(const mi_dims& D, int32_t total_q, int32_t max_query_len) {
@@ -606,7 +719,9 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     p.tables = block_tables;
     p.lens = context_lens;
     p.query_start = query_start;
-    p.part = static_cast<float*>(workspace);
+    p.next = static_cast<unsigned int*>(workspace);
+    p.nlse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256 + lse_bytes(D, total_q));
     p.scores = scores;
     p.dev_err = dev_err;
     p.R = D.B;
@@ -632,7 +747,12 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
         !make_tmap_kv_halves(&tk, k_cache, (long long)D.num_blocks * D.Hkv * kBlock, HD))
         return MI_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
-    const bool ok = HD == 128 ? launch_window<128, kLse>(tq, tk, p, st) && launch_window<128, kSum>(tq, tk, p, st)
-                              : launch_window<64, kLse>(tq, tk, p, st) && launch_window<64, kSum>(tq, tk, p, st);
+    const long long rows = (long long)total_q * D.Hq;
+    const bool wide = HD == 128;
+    bool ok = wide ? launch_window<128, kLse>(tq, tk, p, st) : launch_window<64, kLse>(tq, tk, p, st);
+    if (ok)
+        ok = launch_pdl(window_merge_kernel, (int)((rows + kMergeThreads) / kMergeThreads), kMergeThreads, 0, st, p) ==
+             cudaSuccess;
+    if (ok) ok = wide ? launch_window<128, kSum>(tq, tk, p, st) : launch_window<64, kSum>(tq, tk, p, st);
     return ok ? MI_OK : MI_ERR_CUDA;
 }

@@ -14,27 +14,45 @@ namespace mi {
 //
 // Entry b of B contributes count(b) items (a count never depends on anything
 // but device data that stays fixed during the launch), laid end to end in the
-// order of b. Every block scans the counts itself: thread t sums a contiguous
-// chunk of entries, and sums[t] holds the items before chunk t, sums[nt] the
-// total. B counts cost B / nt loads a thread and two barriers, which is less
-// than a launch that would write the list.
+// order of b. Every block scans the counts itself, which is less than a launch
+// that would write the list: the entries are cut into equal chunks, and sums[t]
+// holds the items before chunk t, sums[chunks] the total. Up to 512 entries one
+// warp does it (32 chunks, one barrier: the usual batch, where three barriers of
+// a wide block were most of the plan's time); larger batches take the whole
+// block, a chunk per thread.
 
 constexpr int kFlatWarps = 32;
+constexpr int kFlatOneWarp = 512;
 __host__ __device__ constexpr int flat_words(int threads) { return threads + 1 + kFlatWarps; }
 
+__device__ __forceinline__ int flat_chunks(int B) { return B <= kFlatOneWarp ? 32 : (int)blockDim.x; }
+
+// Ends with a barrier; the caller makes sure nobody still reads `sums`.
 template <typename Count>
 __device__ long long flat_scan(int B, Count count, long long* sums) {
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5, nw = (nt + 31) >> 5;
-    const int per = (B + nt - 1) / nt;
-    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    long long v = 0;
-    for (int b = b0; b < b1; ++b) v += count(b);
-    long long x = v;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int chunks = flat_chunks(B), per = (B + chunks - 1) / chunks;
+    const bool one = B <= kFlatOneWarp;
+    long long v = 0, x = 0;
+    if (!one || wid == 0) {
+        const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+        for (int b = b0; b < b1; ++b) v += count(b);
+        x = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
     }
+    if (one) {
+        if (wid == 0) {
+            sums[lane] = x - v;
+            if (lane == 31) sums[32] = x;
+        }
+        __syncthreads();
+        return sums[32];
+    }
+    const int nt = blockDim.x, nw = (nt + 31) >> 5;
     long long* wsum = sums + nt + 1;
     if (lane == 31) wsum[wid] = x;
     __syncthreads();
@@ -59,8 +77,8 @@ __device__ long long flat_scan(int B, Count count, long long* sums) {
 // `first`. Reads `sums` only, so any thread may call it at any time.
 template <typename Count>
 __device__ int flat_find(int B, Count count, const long long* sums, long long x, long long& first) {
-    const int nt = blockDim.x, per = (B + nt - 1) / nt;
-    int lo = 0, hi = nt;  // sums[lo] <= x < sums[hi]
+    const int chunks = flat_chunks(B), per = (B + chunks - 1) / chunks;
+    int lo = 0, hi = chunks;  // sums[lo] <= x < sums[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (sums[mid] <= x) lo = mid;
@@ -76,6 +94,15 @@ __device__ int flat_find(int B, Count count, const long long* sums, long long x,
     }
     first = acc;
     return b;
+}
+
+// The items before entry b.
+template <typename Count>
+__device__ long long flat_before(int B, Count count, const long long* sums, int b) {
+    const int chunks = flat_chunks(B), per = (B + chunks - 1) / chunks;
+    long long acc = sums[b / per];
+    for (int c = b / per * per; c < b; ++c) acc += count(c);
+    return acc;
 }
 
 // Whether starts[0 .. count] ascends within [0, limit]; the same answer in

@@ -68,7 +68,7 @@ __device__ inline bool prefix_item(const PrefixWork& w, int Hkv, int G, int mbps
     for (int g = gtid; g < w.P; g += nthreads)
         if (__ldg(w.lens + g) > mbps * kBlock) raise_err(dev_err, MI_DEVERR_BAD_CONTEXT);
     // each request's slots; those outside every group have none
-    const int chunk = (w.P + nt - 1) / nt, b_first = __ldg(w.starts), b_last = __ldg(w.starts + w.P);
+    const int b_first = __ldg(w.starts), b_last = __ldg(w.starts + w.P);
     for (int b = gtid; b < w.B; b += nthreads) {
         int4 at = make_int4(0, 0, 0, 0);
         if (b >= b_first && b < b_last) {
@@ -80,8 +80,7 @@ __device__ inline bool prefix_item(const PrefixWork& w, int Hkv, int G, int mbps
             }
             const int splits = (int)((blocks(lo) + step - 1) / step);
             if (splits > 0) {
-                long long first = sums[lo / chunk];
-                for (int g = lo / chunk * chunk; g < lo; ++g) first += items(g);
+                const long long first = flat_before(w.P, items, sums, lo);
                 const int i = b - __ldg(w.starts + lo);
                 at = make_int4((int)first + (i / per) * splits * Hkv, splits, (i % per) * G, 0);
             }

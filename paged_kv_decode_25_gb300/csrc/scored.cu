@@ -41,19 +41,13 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const ScoreParams 
     __shared__ long long bsums[flat_words(kScoreThreads)];
     const long long total = flat_scan(p.B, items, sums);
     if (!p.by_block) flat_scan(p.B, blocks, bsums);
-    const int per_thread = (p.B + kScoreThreads - 1) / kScoreThreads;
     for (long long x = blockIdx.x; x < total; x += gridDim.x) {
         long long first;
         const int b = flat_find(p.B, items, sums, x, first);
         const int n = tokens(b), nblk = (n + kBlock - 1) / kBlock, per = (n + kScoreTokens - 1) / kScoreTokens;
         const int o = (int)(x - first), h = o / per, j0 = (o % per) * kItemBlocks;
         long long e0 = 0;  // flat place of the (request, head)'s first block
-        if (!p.by_block) {
-            const int t = b / per_thread;
-            long long acc = bsums[t];
-            for (int c = t * per_thread; c < b; ++c) acc += blocks(c);
-            e0 = acc + (long long)h * nblk;
-        }
+        if (!p.by_block) e0 = flat_before(p.B, blocks, bsums, b) + (long long)h * nblk;
         float lse[8];
 #pragma unroll
         for (int g = 0; g < 8; ++g)

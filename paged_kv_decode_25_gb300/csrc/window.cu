@@ -15,7 +15,11 @@
 // 128-row tiles Y of the other past them, S = X . Y^T (tcgen05.mma, M 128, N 128):
 //   * kLse: X = (query token, head) rows of a request, Y = its keys; a row's
 //     keys may be split over several items (partial log-sum-exps);
-//   * kSum: X = keys, Y = query rows, from the first that sees a key.
+//   * kSum: X = keys, Y = query rows, from the first that sees a key;
+//   * kWindow, where no request has more than two tiles of rows: X = those
+//     rows, Y = keys with S = Y . X^T, so that a key is finished with its tile
+//     and K streams past resident rows (with K resident, every 256 keys would
+//     stream the rows again: twice the traffic of the product's own).
 // A thread then owns one row of an S tile (a tensor-memory lane), so both
 // reductions are private to a thread until the item's end.
 //   warps 0-15   softmax: group g (four warps, one per scheduler) takes every
@@ -23,7 +27,7 @@
 //   warp 16      issues the MMAs and owns the tensor memory (four S tiles)
 //   warp 17      picks the items, streams X (two slots, so the next item's X
 //                lands early) and Y
-//   warp 18      kSum: the Y rows' log-sum-exps
+//   warp 18      the query rows' log-sum-exps (kSum, kWindow)
 // An S tile costs about 530 clocks of tensor core, 512 of exponentials (32 a
 // clock and SM) and 400 issue slots a scheduler at 3 instructions a logit.
 #include <cmath>
@@ -34,7 +38,7 @@
 namespace mi {
 namespace {
 
-constexpr int kLse = 0, kSum = 1;
+constexpr int kLse = 0, kSum = 1, kWindow = 2;
 constexpr int kTile = 128;
 constexpr int kSoftWarps = 16, kGroups = 4, kMmaWarp = 16, kLoadWarp = 17, kLseWarp = 18;
 constexpr int kThreads = 19 * 32;
@@ -54,7 +58,7 @@ struct WinSmem {
     static constexpr int kSums = kItems + kItemSlots * 64;
     static constexpr int kMask = kSums + flat_words(kThreads) * 8;
     static constexpr int kBar = (kMask + kMaskSlots * 4 + 7) / 8 * 8;
-    static constexpr int kNBar = 4 + 2 * kYSlots + 2 * kGroups + 2 * kLseSlots + 2 * kItemSlots + 1;
+    static constexpr int kNBar = 4 + 2 * kYSlots + 2 * kGroups + 2 * kLseSlots + 2 * kItemSlots + 1 + 4;
     static constexpr int kTmem = kBar + kNBar * 8;        // the tensor-memory base, then two words: a wait ran out
     static constexpr int kTotal = kTmem + 16 + 1024;      // slack to align the base to 1024 B
 };
@@ -65,10 +69,11 @@ struct WindowParams {
     const int32_t* query_start;    // [R + 1]
     float* part;                   // [T][Hq][splits] partial log-sum-exps, base 2
     float* nlse;                   // [Hkv][T][G] the rows' negated log-sum-exps (-inf: no key)
-    unsigned int* next;            // kSum: the next item
+    unsigned int* next;            // [0] kSum: the next item, [1] the key tiles per split (0: bad query_start)
     float* scores;                 // [num_blocks][Hkv][16]
     int32_t* dev_err;
     int R, Hq, Hkv, G, num_blocks, mbps, T, max_q, fresh;
+    int xt;                        // kWindow: tiles of rows of every item
     int splits, sms;               // most splits of a row's keys
     float sl2;                     // scale * log2(e), never 0
     long long wait_ns;
@@ -105,9 +110,9 @@ __device__ __forceinline__ int seen_tiles(const WindowParams& p, const Request& 
     return last >= 0 ? last / kTile + 1 : 0;
 }
 
-// Key tiles per split, the same in every block of both launches: about eight
-// items per SM, and no more splits of a row than the workspace has places for.
-__device__ int split_tiles(const WindowParams& p, long long* sums, int* shared_max) {
+// Key tiles per split: about four items per SM, and no more splits of a row
+// than the workspace has places for. `most` is a shared word.
+__device__ int split_tiles(const WindowParams& p, long long* sums, int* most) {
     const long long total = flat_scan(
         p.R,
         [&](int r) {
@@ -115,17 +120,17 @@ __device__ int split_tiles(const WindowParams& p, long long* sums, int* shared_m
             return (long long)p.Hkv * row_pairs(p, x) * ceil_div(x.n, kTile);
         },
         sums);
-    int most = 0;
+    if (threadIdx.x == 0) *most = 0;
+    __syncthreads();
+    int mine = 0;
     for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
         const Request x = request_of(p, r);
-        if (x.m > 0) most = max(most, ceil_div(x.n, kTile));
+        if (x.m > 0) mine = max(mine, ceil_div(x.n, kTile));
     }
-    if (threadIdx.x == 0) *shared_max = 0;
+    if (mine > 0) atomicMax(most, mine);
     __syncthreads();
-    if (most > 0) atomicMax(shared_max, most);
-    __syncthreads();
-    const long long even = (total + 8LL * p.sms - 1) / (8LL * p.sms);
-    const int step = max((int)min(even, 1LL << 24), ceil_div(*shared_max, p.splits));
+    const long long even = (total + 4LL * p.sms - 1) / (4LL * p.sms);
+    const int step = max((int)min(even, 1LL << 24), ceil_div(*most, p.splits));
     return max(step, 4);
 }
 
@@ -140,6 +145,7 @@ template <int MODE>
 __device__ __forceinline__ long long item_count(const WindowParams& p, int r, int step, int xtiles) {
     const Request x = request_of(p, r);
     if (MODE == kLse) return (long long)p.Hkv * row_pairs(p, x) * ceil_div(ceil_div(x.n, kTile), step);
+    if (MODE == kWindow) return x.m >= 0 ? (long long)p.Hkv * ceil_div(ceil_div(x.n, kTile), step) : 0ll;
     return x.m >= 0 ? (long long)p.Hkv * ceil_div(x.n, xtiles * kTile) : 0ll;
 }
 
@@ -160,7 +166,11 @@ __device__ __forceinline__ Item item_at(const WindowParams& p, const long long* 
         it.xt = rows - it.row0 > tr ? 2 : 1;
         it.y0 = it.split * step;
         it.y1 = min(it.y0 + step, seen_tiles(p, it.x, pt));
-        if (it.y0 >= it.y1) it.xt = 0;
+    } else if (MODE == kWindow) {
+        it.row0 = 0;
+        it.xt = p.xt;
+        it.y0 = o / p.Hkv * step;
+        it.y1 = min(it.y0 + step, ceil_div(it.x.n, kTile));
     } else {
         it.row0 = o / p.Hkv * xtiles * kTile;
         it.xt = min(xtiles, ceil_div(it.x.n - it.row0, kTile));
@@ -190,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_full = y_empty + 8 * kYSlots, s_empty = s_full + 8 * kGroups;
     const uint32_t l_full = s_empty + 8 * kGroups, l_empty = l_full + 8 * kLseSlots;
     const uint32_t i_full = l_empty + 8 * kLseSlots, i_empty = i_full + 8 * kItemSlots, fin = i_empty + 8 * kItemSlots;
+    const uint32_t c_full = fin + 8;  // kWindow: [2 pairs of groups][2] the second group's sums
     volatile int* failed = reinterpret_cast<volatile int*>(base + SM::kTmem + 4);
     const uint32_t mask0 = sbase + SM::kMask;
 
@@ -212,9 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItemSlots; ++i) {
             mbar_init(i_full + 8 * i, 1);
-            mbar_init(i_empty + 8 * i, kSoftWarps + 1 + (MODE == kSum ? 1 : 0));  // every warp that reads items
+            mbar_init(i_empty + 8 * i, kSoftWarps + 1 + (MODE != kLse ? 1 : 0));  // every warp that reads items
         }
         mbar_init(fin, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(c_full + 8 * i, 4);
         failed[0] = failed[1] = 0;
         fence_mbar_init();
     }
@@ -231,9 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---------------------------------------------------------- the plan --
     long long total = 0;
-    int step = 1, xtiles = 2;
-    const bool ascend = starts_ascend(p.query_start, p.R, p.T);
+    int step = 0, xtiles = 2;
     if (MODE == kLse) {
+        const bool ascend = starts_ascend(p.query_start, p.R, p.T);
         const int g = blockIdx.x * kThreads + threadIdx.x;
         if (!ascend && g == 0) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
         for (int r = g; ascend && r < p.R; r += gridDim.x * kThreads) {
@@ -241,17 +253,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.m < 0 || x.m > x.n) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
             if (__ldg(p.lens + r) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
         }
+        if (ascend) step = split_tiles(p, sums, reinterpret_cast<int*>(base + SM::kMask));
+        if (g == 0) p.next[1] = (unsigned int)step;
+    } else {
+        step = (int)__ldcg(p.next + 1);
     }
-    if (ascend) {
-        step = split_tiles(p, sums, reinterpret_cast<int*>(base + SM::kMask));
-        if (MODE == kSum) {
+    if (step > 0) {
+        auto items = [&](int r) { return item_count<MODE>(p, r, step, xtiles); };
+        total = flat_scan(p.R, items, sums);
+        if (MODE == kSum && total < 4LL * p.sms) {
             // single tiles of keys while pairs would leave SMs with few
-            total = flat_scan(p.R, [&](int r) { return item_count<MODE>(p, r, step, 2); }, sums);
-            if (total < 4LL * p.sms) xtiles = 1;
+            xtiles = 1;
+            __syncthreads();
+            total = flat_scan(p.R, items, sums);
         }
-        __syncthreads();
-        if (MODE == kLse || xtiles == 1)
-            total = flat_scan(p.R, [&](int r) { return item_count<MODE>(p, r, step, xtiles); }, sums);
     }
     const int tr = kTile / p.G * p.G;
     // the k-th item of the list as every other warp sees it
@@ -270,24 +285,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
         uint32_t xc = 0, yc = 0;
         bool ok = true;
-        // key tile j of the item's request to dst: 16-token blocks, each as kH
-        // 64-column halves; kLse posts the tile's mask of blocks in the cache
-        auto load_keys = [&](const Item& it, uint32_t dst, uint32_t fb, int j, int tiles) {
-            const int b0 = j * (kTile / kBlock), x = b0 + lane;
-            bool have = lane < tiles * (kTile / kBlock) && x * kBlock < it.x.n;
-            int blk = -1;
-            if (have) {
-                blk = __ldg(p.tables + (long long)it.r * p.mbps + x);
-                have = blk >= 0 && blk < p.num_blocks;
-                if (!have && MODE == kLse) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
-            }
-            const uint32_t msk = __ballot_sync(0xffffffffu, have);
+        // the lane's block of key tiles j .. j + tiles - 1 (-1: none; -2: not in the cache)
+        auto entry = [&](const Item& it, int j, int tiles) -> int {
+            const int x = j * (kTile / kBlock) + lane;
+            if (lane >= tiles * (kTile / kBlock) || x * kBlock >= it.x.n) return -1;
+            const int blk = __ldg(p.tables + (long long)it.r * p.mbps + x);
+            return blk >= 0 && blk < p.num_blocks ? blk : -2;
+        };
+        // those blocks to dst, each as kH 64-column halves; kLse posts the
+        // tile's mask of blocks in the cache
+        auto load_keys = [&](const Item& it, uint32_t dst, uint32_t fb, int blk) {
+            if (MODE == kLse && blk == -2) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+            const uint32_t msk = __ballot_sync(0xffffffffu, blk >= 0);
             if (lane == 0) {
                 if (MODE == kLse) sts32(mask0 + (yc % kMaskSlots) * 4, msk);
                 mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
             }
             __syncwarp();
-            if (have) {
+            if (blk >= 0) {
                 const uint32_t kd = dst + (lane >> 3) * SM::kT + (lane & 7) * kBlock * 128;
                 const int row0 = (blk * p.Hkv + it.h) * kBlock;
                 for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kTile * 128, &tmk, fb, 0, hh, row0, policy);
@@ -303,10 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        // kLse deals the list out back and forth (it goes from long to short);
-        // kSum's items are taken from a counter as blocks get free
+        // kLse and kWindow deal the list out back and forth (it goes from long
+        // to short); kSum's items are taken from a counter as blocks get free
         auto pick = [&](long long k) -> long long {
-            if (MODE == kLse) return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (MODE != kSum) return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             unsigned int i = 0;
             if (lane == 0) i = atomicAdd(p.next, 1u);
             return (long long)__shfl_sync(0xffffffffu, i, 0);
@@ -337,20 +352,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t xs = xc & 1;
             if (!(ok = wait_warp(x_empty + 8 * xs, ((xc >> 1) & 1) ^ 1, p.wait_ns))) break;
             const uint32_t xd = sbase + SM::kX + xs * 2 * SM::kT;
-            if (MODE == kLse)
-                load_rows(it, xd, x_full + 8 * xs, it.row0, it.xt);
+            if (MODE == kSum)
+                load_keys(it, xd, x_full + 8 * xs, entry(it, it.row0 / kTile, it.xt));
             else
-                load_keys(it, xd, x_full + 8 * xs, it.row0 / kTile, it.xt);
+                load_rows(it, xd, x_full + 8 * xs, it.row0, it.xt);
             ++xc;
+            // table entries are read a tile ahead of their use
+            int blk = MODE == kSum ? 0 : entry(it, it.y0, 1);
             for (int j = it.y0; j < it.y1; ++j, ++yc) {
+                const int now = blk;
+                if (MODE != kSum && j + 1 < it.y1) blk = entry(it, j + 1, 1);
                 const uint32_t ys = yc % kYSlots;
                 if (!(ok = wait_warp(y_empty + 8 * ys, ((yc / kYSlots) & 1) ^ 1, p.wait_ns))) break;
                 if (p.withhold && yc == 0) continue;
                 const uint32_t yd = sbase + SM::kY + ys * SM::kT;
-                if (MODE == kLse)
-                    load_keys(it, yd, y_full + 8 * ys, j, 1);
-                else
+                if (MODE == kSum)
                     load_rows(it, yd, y_full + 8 * ys, j * tr, 1);
+                else
+                    load_keys(it, yd, y_full + 8 * ys, now);
             }
             if (!ok) break;
         }
@@ -383,8 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kTile * 128 + (kk & 3) * 32;
-                        tc::mma_ss_elect(tbase + b * kTile, tc::sdesc_sw128(xa + off, 16, 1024),
-                                         tc::sdesc_sw128(ya + off, 16, 1024), id, kk > 0);
+                        const uint64_t xd = tc::sdesc_sw128(xa + off, 16, 1024), yd = tc::sdesc_sw128(ya + off, 16, 1024);
+                        tc::mma_ss_elect(tbase + b * kTile, MODE == kWindow ? yd : xd, MODE == kWindow ? xd : yd, id,
+                                         kk > 0);
                     }
                     tc::commit_elect(s_full + 8 * b);
                     if (lane == 0) mbar_arrive(s_full + 8 * b);
@@ -400,27 +420,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::commit_elect(fin);
         (void)wait_warp(fin, 0, drain_limit(p.wait_ns));
     } else if (warp == kLseWarp) {
-        if (MODE == kSum) {
+        if (MODE != kLse) {
             // -------------------------------- the rows' log-sum-exps ----
-            uint32_t yc = 0;
+            // Copied without a wait, so the ring is filled ahead; zero past a
+            // tile's rows. kSum: one slot per Y tile; kWindow: two per item,
+            // its X tiles.
+            uint32_t lc = 0;
             bool ok = true;
             for (uint32_t ic = 0; ok; ++ic) {
                 Item it;
                 if (!(ok = take(ic, it)) || it.xt == 0) break;
                 const int rows = it.x.m * p.G;
                 const float* at = p.nlse + ((long long)it.h * p.T + it.x.q0) * p.G;
-                for (int j = it.y0; j < it.y1; ++j, ++yc) {
-                    // copied without a wait, so the ring is filled ahead; zero
-                    // past the tile's rows
-                    const uint32_t ls = yc % kLseSlots;
-                    if (!(ok = wait_warp(l_empty + 8 * ls, ((yc / kLseSlots) & 1) ^ 1, p.wait_ns))) break;
+                const int j0 = MODE == kSum ? it.y0 : 0, j1 = MODE == kSum ? it.y1 : 2;
+                for (int j = j0; j < j1; ++j, ++lc) {
+                    const uint32_t ls = lc % kLseSlots;
+                    if (!(ok = wait_warp(l_empty + 8 * ls, ((lc / kLseSlots) & 1) ^ 1, p.wait_ns))) break;
 #pragma unroll
                     for (int u = 0; u < kTile / 32; ++u) {
                         const int c = u * 32 + lane, rho = j * tr + c;
                         const bool in = c < tr && rho < rows;
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
                                          sbase + SM::kLses + (ls * kTile + c) * 4),
-                                     "l"(at + (in ? rho : 0)), "r"(in ? 4 : 0)
+                                     "l"(in ? at + rho : p.nlse), "r"(in ? 4 : 0)
                                      : "memory");
                     }
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(l_full + 8 * ls) : "memory");
@@ -437,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
         const bool pos_scale = p.sl2 > 0.f;
         const float off_value = pos_scale ? -INFINITY : INFINITY;  // a masked logit, before the scale
-        uint32_t yc = 0, sc = 0;
+        uint32_t yc = 0, sc = 0, wc = 0;
         bool ok = true;
         for (uint32_t ic = 0;; ++ic) {
             Item it;
@@ -452,13 +474,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // kLse: the last key this thread's row sees; kSum: the first row
             // that sees this thread's key
             const int tile = it.xt == 2 ? (group ^ (int)sc) & 1 : 0;  // this group's S tiles of the item
-            int bound;
-            bool mine;
+            int bound = 0;
+            bool mine = false;
             if (MODE == kLse) {
                 const int rho = it.row0 + tile * tr + my;
                 mine = my < tr && rho < rows;
                 bound = mine ? it.x.first + rho / p.G : 0x3FFFFFFF;
-            } else {
+            } else if (MODE == kSum) {
                 const int t = it.row0 + tile * kTile + my;
                 mine = t < it.x.n;
                 bound = mine ? max(0, t - it.x.first) * p.G : 0;
@@ -466,8 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, total_sum = 0.f;  // kLse: the sum is relative to 2^m
             uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
             // f(x, q) for the S tile's four chunks of 32 columns, the next one
-            // loaded under the arithmetic of the one at hand
-            auto sweep = [&](auto f) {
+            // loaded under the arithmetic of the one at hand; stops after
+            // `cols` columns
+            auto sweep = [&](int cols, auto f) {
                 uint32_t xa[32], xb[32];
                 tc::ld32(ts, xa);
 #pragma unroll 1
@@ -476,8 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::ld32(ts + 32u * q + 32u, xb);
                     f(xa, q);
                     tc::wait_ld();
-                    if (q == 0) tc::ld32(ts + 64u, xa);
-                    f(xb, q + 1);
+                    const bool more = 32 * q + 64 < cols;
+                    if (q == 0 && more) tc::ld32(ts + 64u, xa);
+                    if (32 * q + 32 < cols) f(xb, q + 1);
+                    if (!more) break;
                 }
             };
             // columns lo .. hi - 1 of a chunk count
@@ -486,10 +511,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 32; ++c)
                     if (c < lo || c >= hi) x[c] = __float_as_uint(off_value);
             };
+            if (MODE == kWindow)
+                ok = ok && wait_warp(l_full + 8 * (2 * ic % kLseSlots), (2 * ic / kLseSlots) & 1, p.wait_ns) &&
+                     wait_warp(l_full + 8 * ((2 * ic + 1) % kLseSlots), (2 * ic / kLseSlots) & 1, p.wait_ns);
             for (int j = it.y0; ok && j < it.y1; ++j, ++yc) {
                 if (MODE == kSum &&
                     !(ok = wait_warp(l_full + 8 * (yc % kLseSlots), (yc / kLseSlots) & 1, p.wait_ns)))
                     break;
+                const int key = j * kTile + my;  // kWindow: this thread's key of the stage, its block and row there
+                int blk = -1;
                 // this group's S tile of the stage, if it has one
                 const int t = (group - (int)sc) & (kGroups - 1);
                 if (t < it.xt) {
@@ -513,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (;;) {
                             if (top) {
                                 float e4[4] = {off_value, off_value, off_value, off_value};
-                                sweep([&](uint32_t (&x)[32], int q) {
+                                sweep(kTile, [&](uint32_t (&x)[32], int q) {
                                     mask(x, q);
 #pragma unroll
                                     for (int c = 0; c < 32; ++c)
@@ -529,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint64_t nu2 = tc::f2(nu, nu);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) acc[c] = 0ull;
-                            sweep([&](uint32_t (&x)[32], int q) {
+                            sweep(kTile, [&](uint32_t (&x)[32], int q) {
                                 mask(x, q);
 #pragma unroll
                                 for (int c = 0; c < 16; ++c) {
@@ -546,34 +576,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                             top = true;
                         }
                     } else {
-                        const int end = min(rows, (j + 1) * tr);
-                        const bool part = __any_sync(0xffffffffu, bound > j * tr || j * tr + kTile > end);
-                        const uint32_t la = sbase + SM::kLses + (yc % kLseSlots) * kTile * 4;
-                        sweep([&](uint32_t (&x)[32], int q) {
-                            if (part) cut(x, bound - (j * tr + 32 * q), end - (j * tr + 32 * q));
+                        // the Y rows of kSum, the X rows of kWindow: columns
+                        // from `first` on see the thread's key, `cols` hold rows
+                        const int row0 = (MODE == kSum ? j : tile) * tr, cols = min(tr, rows - row0);
+                        if (MODE == kWindow) {
+                            if (t == 0 && key < it.x.n) blk = __ldg(p.tables + (long long)it.r * p.mbps + key / kBlock);
+                            bound = (key - it.x.first) * p.G;
+                        }
+                        const int first = bound - row0;
+                        const bool part = __any_sync(0xffffffffu, first > 0) || (cols & 31) != 0;
+                        const uint32_t la = sbase + SM::kLses + ((MODE == kSum ? yc : 2 * ic + tile) % kLseSlots) * kTile * 4;
+                        if (MODE == kWindow) {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t l0, l1, l2, l3;
-                                lds128(la + 128 * q + 16 * c, l0, l1, l2, l3);
-                                const uint64_t a0 = tc::fma2(tc::f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sc2,
-                                                             tc::f2(__uint_as_float(l0), __uint_as_float(l1)));
-                                const uint64_t a1 = tc::fma2(tc::f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sc2,
-                                                             tc::f2(__uint_as_float(l2), __uint_as_float(l3)));
-                                acc[(2 * c) & 3] = tc::add2(acc[(2 * c) & 3], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
-                                acc[(2 * c + 1) & 3] = tc::add2(acc[(2 * c + 1) & 3], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
-                            }
-                        });
+                            for (int c = 0; c < 4; ++c) acc[c] = 0ull;
+                        }
+                        if (cols > 0)
+                            sweep(cols, [&](uint32_t (&x)[32], int q) {
+                                if (part) cut(x, first - 32 * q, cols - 32 * q);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    uint32_t l0, l1, l2, l3;
+                                    lds128(la + 128 * q + 16 * c, l0, l1, l2, l3);
+                                    const uint64_t a0 = tc::fma2(tc::f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sc2,
+                                                                 tc::f2(__uint_as_float(l0), __uint_as_float(l1)));
+                                    const uint64_t a1 = tc::fma2(tc::f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sc2,
+                                                                 tc::f2(__uint_as_float(l2), __uint_as_float(l3)));
+                                    acc[(2 * c) & 3] = tc::add2(acc[(2 * c) & 3], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
+                                    acc[(2 * c + 1) & 3] = tc::add2(acc[(2 * c + 1) & 3], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
+                                }
+                            });
                     }
                     // the tile has been read: hand it back
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_empty + 8 * group);
+                    if (MODE == kWindow) {
+                        // the second tile's group hands its sums to the first's
+                        // through one of two places (the first group's S tile of
+                        // two stages on waits for it to be done with this one)
+                        const uint64_t a = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
+                        float w = tc::f2_lo(a) + tc::f2_hi(a);
+                        const int place = (group & 2) + (int)(wc & 1);
+                        float* comb = reinterpret_cast<float*>(base + SM::kComb) + place * kTile;
+                        if (t == 1) {
+                            comb[my] = w;
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(c_full + 8 * place);
+                        } else {
+                            if (it.xt == 2) {
+                                if (!(ok = wait_warp(c_full + 8 * place, (wc >> 1) & 1, p.wait_ns))) break;
+                                w += comb[my];
+                            }
+                            if (blk >= 0 && blk < p.num_blocks) {
+                                float* at = p.scores + ((long long)blk * p.Hkv + it.h) * kBlock + key % kBlock;
+                                *at = p.fresh || key >= it.x.first ? w : *at + w;
+                            }
+                        }
+                        ++wc;
+                    }
                 }
                 sc += it.xt;
                 if (MODE == kSum) {
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(l_empty + 8 * (yc % kLseSlots));
                 }
+            }
+            if (MODE == kWindow) {
+                if (!ok) break;
+                __syncwarp();
+                if (lane < 2) mbar_arrive(l_empty + 8 * ((2 * ic + lane) % kLseSlots));
+                continue;
             }
             // the groups that share a row: every second one, or all four for a
             // single tile. A warp whose wait ran out still meets the others
@@ -630,13 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // second reads every row once per 256 keys), and kSum's item counter back to
 // zero. A thread merges one row.
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p) {
-    __shared__ long long sums[flat_words(kMergeThreads)];
-    __shared__ int most;
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0u;
-    if (!starts_ascend(p.query_start, p.R, p.T)) return;
-    const int step = split_tiles(p, sums, &most);
+    const int step = (int)__ldcg(p.next + 1);
+    if (step == 0) return;
     const long long row = (long long)blockIdx.x * kMergeThreads + threadIdx.x;
     const int i = (int)(row / p.Hq);
     if (i < __ldg(p.query_start) || i >= __ldg(p.query_start + p.R)) return;
@@ -733,6 +803,7 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     p.T = total_q;
     p.max_q = max_query_len;
     p.fresh = fresh != 0;
+    p.xt = 0;
     p.splits = split_places(D, total_q);
     p.sms = sms;
     p.sl2 = scale * 1.4426950408889634f;
@@ -753,6 +824,11 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     if (ok)
         ok = launch_pdl(window_merge_kernel, (int)((rows + kMergeThreads) / kMergeThreads), kMergeThreads, 0, st, p) ==
              cudaSuccess;
-    if (ok) ok = wide ? launch_window<128, kSum>(tq, tk, p, st) : launch_window<64, kSum>(tq, tk, p, st);
+    // rows that fit in two tiles stay resident while the keys stream
+    const int tr = kTile / G * G;
+    const bool few = (long long)max_query_len * G <= 2 * tr;
+    p.xt = max_query_len * G <= tr ? 1 : 2;
+    if (ok && few) ok = wide ? launch_window<128, kWindow>(tq, tk, p, st) : launch_window<64, kWindow>(tq, tk, p, st);
+    if (ok && !few) ok = wide ? launch_window<128, kSum>(tq, tk, p, st) : launch_window<64, kSum>(tq, tk, p, st);
     return ok ? MI_OK : MI_ERR_CUDA;
 }

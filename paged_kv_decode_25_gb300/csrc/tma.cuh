@@ -135,6 +135,25 @@ inline bool make_tmap_kv_blocks(CUtensorMap* m, const void* base, long long rows
     return r == CUDA_SUCCESS;
 }
 
+// 4-D map over a bf16 cache for whole blocks as K-major operands: dims {64, 8,
+// HD/64, rows/8} (rows in groups of 8, a token row's 128-byte halves outside
+// the group), box {64, 8, HD/64, 2}: a block's 16 token rows in one copy,
+// landing as [2 groups][HD/64][8 rows][128 B] with 128-byte swizzle. The
+// groups of consecutive blocks lie HD/64 * 1024 bytes apart, a uniform stride
+// for a matrix descriptor over any number of blocks.
+inline bool make_tmap_kv_groups(CUtensorMap* m, const void* base, long long rows, int HD) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {64, 8, (cuuint64_t)(HD / 64), (cuuint64_t)(rows / 8)};
+    cuuint64_t strides[3] = {(cuuint64_t)HD * 2, 128, (cuuint64_t)HD * 16};
+    cuuint32_t box[4] = {64, 8, (cuuint32_t)(HD / 64), (cuuint32_t)(kBlock / 8)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // 4-D map over q [T][Hq][HD] bf16: dims {64, HD/64, Hq, T}, box {64, 1, G,
 // rows / G}: one 128-byte half of `rows` (token, head) rows of a GQA group,
 // landing as [rows][128 B] with 128-byte swizzle; tokens past T read as zero.

@@ -6,30 +6,36 @@
 //
 // A weight needs its row's log-sum-exp over all keys, so the logits x are
 // computed twice: the first launch reduces them over the keys of each row, the
-// last over the rows of each key (a small one between merges split rows). (Kept in memory they would be 4 bytes a
-// pair each way, 0.5 GB for 16 windows of 64 tokens over 85,000 keys; the second
-// product costs a tenth of that time.) V is never read.
+// last over the rows of each key (a small one between merges split rows). (Kept
+// in memory they would be 4 bytes a pair each way, 0.5 GB for 16 windows of 64
+// tokens over 85,000 keys; the second product costs a tenth of that time.) V is
+// never read.
 //
-// The two are one pipeline on the fifth-generation tensor cores. An item
-// holds up to two 128-row tiles X of one operand in shared memory and streams
-// 128-row tiles Y of the other past them, S = X . Y^T (tcgen05.mma, M 128, N 128):
-//   * kLse: X = (query token, head) rows of a request, Y = its keys; a row's
-//     keys may be split over several items (partial log-sum-exps);
-//   * kSum: X = keys, Y = query rows, from the first that sees a key;
-//   * kWindow, where no request has more than two tiles of rows: X = those
-//     rows, Y = keys with S = Y . X^T, so that a key is finished with its tile
-//     and K streams past resident rows (with K resident, every 256 keys would
-//     stream the rows again: twice the traffic of the product's own).
-// A thread then owns one row of an S tile (a tensor-memory lane), so both
-// reductions are private to a thread until the item's end.
-//   warps 0-15   softmax: group g (four warps, one per scheduler) takes every
-//                fourth S tile, warp w its lanes 32 (w mod 4) .. + 31
-//   warp 16      issues the MMAs and owns the tensor memory (four S tiles)
-//   warp 17      picks the items, streams X (two slots, so the next item's X
-//                lands early) and Y
+// The two are one pipeline on the fifth-generation tensor cores: an item keeps
+// X in shared memory and streams Y past it, S = A . B^T in tiles of 128 x 256:
+//   * kLse: X = up to 256 (query token, head) rows of a request (A, 128 a
+//     tile), Y = its keys (B, 256 a stage); a row's keys may be split over
+//     several items (partial log-sum-exps);
+//   * kSum: X = up to 256 keys (A, 128 a tile), Y = query rows (B, 256 a
+//     stage), from the first that sees a key;
+//   * kWindow, where no request has more than 256 rows: X = those rows (B), Y =
+//     keys (A, 128 a stage), so that a key is finished with its stage and K
+//     streams past resident rows (with K resident the rows would be streamed
+//     again for every 256 keys, twice the traffic).
+// A thread owns a row of S (a tensor-memory lane) and a quarter of its columns,
+// so both reductions are private to a thread until the item's end (kWindow: the
+// stage's).
+//   warps 0-15   softmax, all on the same S tile while the tensor cores fill the
+//                other: warp w takes lanes 32 (w mod 4) .. + 31 and columns
+//                64 (w / 4) .. + 63 (with a tile per eight warps, each half
+//                waited for its own next tile a third of the time)
+//   warp 16      issues the MMAs and owns the tensor memory (two S tiles)
+//   warp 17      picks the items, streams X and Y
 //   warp 18      the query rows' log-sum-exps (kSum, kWindow)
-// An S tile costs about 530 clocks of tensor core, 512 of exponentials (32 a
-// clock and SM) and 400 issue slots a scheduler at 3 instructions a logit.
+// Why 256 columns: an MMA of 128 x 128 x 16 takes 63 clocks to issue whatever
+// its size, and a tile's waits and commits another 360, so tiles of 128
+// columns ran at 868 clocks against 512 of tensor core; one of 256 takes 1,038
+// against 1,024 (measured apart from the softmax).
 #include <cmath>
 
 #include "batch.cuh"
@@ -39,26 +45,34 @@ namespace mi {
 namespace {
 
 constexpr int kLse = 0, kSum = 1, kWindow = 2;
-constexpr int kTile = 128;
-constexpr int kSoftWarps = 16, kGroups = 4, kMmaWarp = 16, kLoadWarp = 17, kLseWarp = 18;
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kRows = 256;     // rows of a block of query rows: whole tokens, kRows / G of them
+constexpr int kSoftWarps = 16, kQuarters = 4, kMmaWarp = 16, kLoadWarp = 17, kLseWarp = 18;
 constexpr int kThreads = 19 * 32;
-constexpr int kYSlots = 2, kMaskSlots = 8, kLseSlots = 8, kItemSlots = 4;
+constexpr int kMaskSlots = 16, kLseSlots = 4, kItemSlots = 4;
 constexpr uint32_t kCols = 512;
 constexpr int kMergeThreads = 256;
 
-template <int HD>
+template <int HD, int MODE>
 struct WinSmem {
     static constexpr int kH = HD / 64;
-    static constexpr int kT = kH * kTile * 128;          // one tile: kH x [128 rows][128 B], 128-byte swizzle
-    static constexpr int kX = 0;                          // [2 slots][2 tiles]
-    static constexpr int kY = 4 * kT;                     // [kYSlots]
-    static constexpr int kLses = kY + kYSlots * kT;       // [kLseSlots][128] fp32
-    static constexpr int kComb = kLses + kLseSlots * kTile * 4;  // [2][kGroups][128] float2
-    static constexpr int kItems = kComb + 2 * kGroups * kTile * 8;
+    // Both layouts with 128-byte swizzle. Query rows: [kH][256 rows][128 B].
+    // Keys: [groups of 8 rows][kH][8 rows][128 B], so that one copy brings a
+    // block whole (with the halves apart it takes kH copies, 72 clocks each to
+    // issue: 1,150 for 128 keys, more than their products).
+    static constexpr int kRowBytes = kH * kRows * 128, kKeyBytes = kH * kKeys * 128;
+    static constexpr int kXBytes = kRowBytes;             // 256 rows or 256 keys
+    static constexpr int kYBytes = MODE == kWindow ? kKeyBytes : kRowBytes;
+    static constexpr int kXSlots = 65536 / kXBytes, kYSlots = 131072 / kYBytes;
+    static constexpr int kX = 0;
+    static constexpr int kY = 65536;
+    static constexpr int kLses = kY + 131072;             // [kLseSlots][256] fp32
+    static constexpr int kComb = kLses + kLseSlots * kRows * 4;  // [2][2 tiles][kQuarters][128] float2
+    static constexpr int kItems = kComb + 4 * kQuarters * kKeys * 8;
     static constexpr int kSums = kItems + kItemSlots * 64;
     static constexpr int kMask = kSums + flat_words(kThreads) * 8;
     static constexpr int kBar = (kMask + kMaskSlots * 4 + 7) / 8 * 8;
-    static constexpr int kNBar = 4 + 2 * kYSlots + 2 * kGroups + 2 * kLseSlots + 2 * kItemSlots + 1 + 4;
+    static constexpr int kNBar = 2 * kXSlots + 2 * kYSlots + 4 + 2 * kLseSlots + 2 * kItemSlots + 1 + 4;
     static constexpr int kTmem = kBar + kNBar * 8;        // the tensor-memory base, then two words: a wait ran out
     static constexpr int kTotal = kTmem + 16 + 1024;      // slack to align the base to 1024 B
 };
@@ -69,11 +83,11 @@ struct WindowParams {
     const int32_t* query_start;    // [R + 1]
     float* part;                   // [T][Hq][splits] partial log-sum-exps, base 2
     float* nlse;                   // [Hkv][T][G] the rows' negated log-sum-exps (-inf: no key)
-    unsigned int* next;            // [0] kSum: the next item, [1] the key tiles per split (0: bad query_start)
+    unsigned int* next;            // [0] kSum: the next item, [1] the key stages per split (0: bad query_start)
     float* scores;                 // [num_blocks][Hkv][16]
     int32_t* dev_err;
     int R, Hq, Hkv, G, num_blocks, mbps, T, max_q, fresh;
-    int xt;                        // kWindow: tiles of rows of every item
+    int xt;                        // kWindow: 128-row halves that hold rows
     int splits, sms;               // most splits of a row's keys
     float sl2;                     // scale * log2(e), never 0
     long long wait_ns;
@@ -99,42 +113,70 @@ __device__ __forceinline__ Request request_of(const WindowParams& p, int r) {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// A Y or X tile of query rows holds whole tokens: tr = (128 / G) * G rows.
-__device__ __forceinline__ int row_pairs(const WindowParams& p, const Request& x) {
-    const int pr = 2 * (kTile / p.G);  // tokens of two tiles
-    return x.m > 0 ? ceil_div(x.m, pr) : 0;
+// Blocks of query rows.
+__device__ __forceinline__ int row_blocks(const WindowParams& p, const Request& x) {
+    return x.m > 0 ? ceil_div(x.m, kRows / p.G) : 0;
 }
-// Key tiles that the rows of pair pt see.
-__device__ __forceinline__ int seen_tiles(const WindowParams& p, const Request& x, int pt) {
-    const int last = x.first + min(x.m, (pt + 1) * 2 * (kTile / p.G)) - 1;
-    return last >= 0 ? last / kTile + 1 : 0;
+// 256-key stages that the rows of block rb see.
+__device__ __forceinline__ int seen_stages(const WindowParams& p, const Request& x, int rb) {
+    const int last = x.first + min(x.m, (rb + 1) * (kRows / p.G)) - 1;
+    return last >= 0 ? last / (2 * kKeys) + 1 : 0;
 }
+__device__ __forceinline__ int key_stages(const Request& x) { return ceil_div(x.n, 2 * kKeys); }
 
-// Key tiles per split: about four items per SM, and no more splits of a row
-// than the workspace has places for. `most` is a shared word.
-__device__ int split_tiles(const WindowParams& p, long long* sums, int* most) {
-    const long long total = flat_scan(
-        p.R,
-        [&](int r) {
+// 256-key stages per split, no more splits of a row than the workspace has
+// places for. A block's share of the items comes in whole ones, so among 32
+// lengths from the shortest allowed on the one with the least work for the
+// busiest block is taken (a split's own cost: about a stage and a half). Any
+// length is right; more than 512 requests take an even share.
+__device__ int split_stages(const WindowParams& p, int* found) {
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        long long total = 0;
+        int most = 0;
+        for (int r = lane; r < p.R; r += 32) {
             const Request x = request_of(p, r);
-            return (long long)p.Hkv * row_pairs(p, x) * ceil_div(x.n, kTile);
-        },
-        sums);
-    if (threadIdx.x == 0) *most = 0;
-    __syncthreads();
-    int mine = 0;
-    for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
-        const Request x = request_of(p, r);
-        if (x.m > 0) mine = max(mine, ceil_div(x.n, kTile));
+            if (x.m <= 0) continue;
+            total += (long long)p.Hkv * row_blocks(p, x) * key_stages(x);
+            most = max(most, key_stages(x));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        }
+        const int least = max(ceil_div(most, p.splits), 2);
+        const int even = (int)min((total + p.sms - 1) / p.sms, 1LL << 24);
+        int step = max(least, max(even / 4, 1));
+        if (p.R <= kFlatOneWarp) {
+            // lane i tries a share of (i + 1) / 32 of 1.5 times the even one
+            const int mine = max(least, (int)((long long)(lane + 1) * 3 * even / 64));
+            long long items = 0;
+            for (int r = 0; r < p.R; ++r) {
+                const Request x = request_of(p, r);
+                if (x.m > 0) items += (long long)p.Hkv * row_blocks(p, x) * ceil_div(key_stages(x), mine);
+            }
+            const long long rounds = (items + p.sms - 1) / p.sms;
+            long long cost = rounds * (2 * min(mine, max(most, 1)) + 3);
+            int best = mine;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const long long c = __shfl_xor_sync(0xffffffffu, cost, o);
+                const int s = __shfl_xor_sync(0xffffffffu, best, o);
+                if (c < cost || (c == cost && s < best)) {
+                    cost = c;
+                    best = s;
+                }
+            }
+            step = best;
+        }
+        if (lane == 0) *found = step;
     }
-    if (mine > 0) atomicMax(most, mine);
     __syncthreads();
-    const long long even = (total + 4LL * p.sms - 1) / (4LL * p.sms);
-    const int step = max((int)min(even, 1LL << 24), ceil_div(*most, p.splits));
-    return max(step, 4);
+    return *found;
 }
 
-// One work item: X tiles xt (0: the list is over), Y tiles y0 .. y1-1.
+// One work item: X of xt tiles of 128 (0: the list is over), Y stages y0 .. y1-1.
 struct __align__(16) Item {
     int r, h, xt, y0, y1, row0, split, pad;  // row0: the first query row (kLse) or key (kSum) of X
     Request x;
@@ -142,70 +184,90 @@ struct __align__(16) Item {
 static_assert(sizeof(Item) <= 64, "an item's place in shared memory");
 
 template <int MODE>
-__device__ __forceinline__ long long item_count(const WindowParams& p, int r, int step, int xtiles) {
+__device__ __forceinline__ long long item_count(const WindowParams& p, int r, int step, int xkeys) {
     const Request x = request_of(p, r);
-    if (MODE == kLse) return (long long)p.Hkv * row_pairs(p, x) * ceil_div(ceil_div(x.n, kTile), step);
-    if (MODE == kWindow) return x.m >= 0 ? (long long)p.Hkv * ceil_div(ceil_div(x.n, kTile), step) : 0ll;
-    return x.m >= 0 ? (long long)p.Hkv * ceil_div(x.n, xtiles * kTile) : 0ll;
+    if (MODE == kLse) return (long long)p.Hkv * row_blocks(p, x) * ceil_div(key_stages(x), step);
+    if (x.m < 0) return 0;
+    return (long long)p.Hkv * (MODE == kWindow ? ceil_div(key_stages(x), step) : ceil_div(x.n, xkeys * kKeys));
 }
 
 template <int MODE>
 __device__ __forceinline__ Item item_at(const WindowParams& p, const long long* sums, long long i, int step,
-                                        int xtiles) {
+                                        int xkeys) {
     Item it;
     long long first;
-    it.r = flat_find(p.R, [&](int r) { return item_count<MODE>(p, r, step, xtiles); }, sums, i, first);
+    it.r = flat_find(p.R, [&](int r) { return item_count<MODE>(p, r, step, xkeys); }, sums, i, first);
     it.x = request_of(p, it.r);
-    const int o = (int)(i - first), tr = kTile / p.G * p.G, rows = it.x.m * p.G;
+    const int o = (int)(i - first), rp = kRows / p.G * p.G, rows = it.x.m * p.G;
     it.h = o % p.Hkv;
     it.split = 0;
+    it.row0 = 0;
     if (MODE == kLse) {
-        const int pairs = row_pairs(p, it.x), pt = pairs - 1 - o / p.Hkv % pairs;  // the longest first
-        it.split = o / p.Hkv / pairs;
-        it.row0 = pt * 2 * tr;
-        it.xt = rows - it.row0 > tr ? 2 : 1;
+        const int blocks = row_blocks(p, it.x), rb = blocks - 1 - o / p.Hkv % blocks;  // the longest first
+        it.split = o / p.Hkv / blocks;
+        it.row0 = rb * rp;
+        it.xt = rows - it.row0 > kKeys ? 2 : 1;
         it.y0 = it.split * step;
-        it.y1 = min(it.y0 + step, seen_tiles(p, it.x, pt));
+        it.y1 = min(it.y0 + step, seen_stages(p, it.x, rb));
     } else if (MODE == kWindow) {
-        it.row0 = 0;
-        it.xt = p.xt;
-        it.y0 = o / p.Hkv * step;
-        it.y1 = min(it.y0 + step, ceil_div(it.x.n, kTile));
+        it.xt = 1;
+        it.y0 = o / p.Hkv * step * 2;
+        it.y1 = min(it.y0 + step * 2, ceil_div(it.x.n, kKeys));
     } else {
-        it.row0 = o / p.Hkv * xtiles * kTile;
-        it.xt = min(xtiles, ceil_div(it.x.n - it.row0, kTile));
-        it.y0 = max(0, it.row0 - it.x.first) * p.G / tr;  // rows before it see none of the keys
-        it.y1 = max(it.y0, ceil_div(rows, tr));
+        it.row0 = o / p.Hkv * xkeys * kKeys;
+        it.xt = min(xkeys, ceil_div(it.x.n - it.row0, kKeys));
+        it.y0 = max(0, it.row0 - it.x.first) * p.G / rp;  // rows before it see none of the keys
+        it.y1 = max(it.y0, ceil_div(rows, rp));
     }
     return it;
 }
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit_ns) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns, kWaitSleepNs));
+    // One vote decides the common case for the whole warp: a branch on each
+    // lane's own answer costs about 130 clocks for its reconvergence alone.
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, kWaitSleepNs))) return true;
+        if (__any_sync(0xffffffffu, (long long)(globaltimer() - t0) > limit_ns)) return false;
+    }
+}
+
+// Whether phase `parity` of the barrier has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 template <int HD, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     window_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const WindowParams p) {
-    using SM = WinSmem<HD>;
-    constexpr int kH = SM::kH;
+    using SM = WinSmem<HD, MODE>;
+    constexpr int kH = SM::kH, kXSlots = SM::kXSlots, kYSlots = SM::kYSlots;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
     unsigned char* base = smem_raw + (sbase - raw);
     long long* sums = reinterpret_cast<long long*>(base + SM::kSums);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t bar = sbase + SM::kBar;
-    const uint32_t x_full = bar, x_empty = bar + 16, y_full = bar + 32, y_empty = y_full + 8 * kYSlots;
-    const uint32_t s_full = y_empty + 8 * kYSlots, s_empty = s_full + 8 * kGroups;
-    const uint32_t l_full = s_empty + 8 * kGroups, l_empty = l_full + 8 * kLseSlots;
+    const uint32_t x_full = bar, x_empty = x_full + 8 * kXSlots, y_full = x_empty + 8 * kXSlots;
+    const uint32_t y_empty = y_full + 8 * kYSlots, s_full = y_empty + 8 * kYSlots, s_empty = s_full + 16;
+    const uint32_t l_full = s_empty + 16, l_empty = l_full + 8 * kLseSlots;
     const uint32_t i_full = l_empty + 8 * kLseSlots, i_empty = i_full + 8 * kItemSlots, fin = i_empty + 8 * kItemSlots;
-    const uint32_t c_full = fin + 8;  // kWindow: [2 pairs of groups][2] the second group's sums
+    const uint32_t c_full = fin + 8;  // kWindow: [4 places] the other quarters' sums
     volatile int* failed = reinterpret_cast<volatile int*>(base + SM::kTmem + 4);
     const uint32_t mask0 = sbase + SM::kMask;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kXSlots; ++i) {
             mbar_init(x_full + 8 * i, 1);
             mbar_init(x_empty + 8 * i, 1);
         }
@@ -213,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(y_full + 8 * i, 1);
             mbar_init(y_empty + 8 * i, 1);
         }
-        for (int i = 0; i < kGroups; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 2);   // the MMAs' commit, and the issuing warp (for what it has seen)
-            mbar_init(s_empty + 8 * i, 4);  // the warps of a group
+            mbar_init(s_empty + 8 * i, kSoftWarps);
         }
         for (int i = 0; i < kLseSlots; ++i) {
             mbar_init(l_full + 8 * i, 32);  // the copying lanes
@@ -226,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(i_empty + 8 * i, kSoftWarps + 1 + (MODE != kLse ? 1 : 0));  // every warp that reads items
         }
         mbar_init(fin, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(c_full + 8 * i, 4);
+        for (int i = 0; i < 4; ++i) mbar_init(c_full + 8 * i, kSoftWarps - 4);
         failed[0] = failed[1] = 0;
         fence_mbar_init();
     }
@@ -243,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---------------------------------------------------------- the plan --
     long long total = 0;
-    int step = 0, xtiles = 2;
+    int step = 0, xkeys = 2;
     if (MODE == kLse) {
         const bool ascend = starts_ascend(p.query_start, p.R, p.T);
         const int g = blockIdx.x * kThreads + threadIdx.x;
@@ -253,22 +315,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.m < 0 || x.m > x.n) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
             if (__ldg(p.lens + r) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
         }
-        if (ascend) step = split_tiles(p, sums, reinterpret_cast<int*>(base + SM::kMask));
+        if (ascend) step = split_stages(p, reinterpret_cast<int*>(base + SM::kMask));
         if (g == 0) p.next[1] = (unsigned int)step;
     } else {
         step = (int)__ldcg(p.next + 1);
     }
     if (step > 0) {
-        auto items = [&](int r) { return item_count<MODE>(p, r, step, xtiles); };
+        auto items = [&](int r) { return item_count<MODE>(p, r, step, xkeys); };
         total = flat_scan(p.R, items, sums);
-        if (MODE == kSum && total < 4LL * p.sms) {
-            // single tiles of keys while pairs would leave SMs with few
-            xtiles = 1;
+        if (MODE == kSum && total < 2LL * p.sms) {
+            // 128 keys an item while 256 would leave SMs with few
+            xkeys = 1;
             __syncthreads();
             total = flat_scan(p.R, items, sums);
         }
     }
-    const int tr = kTile / p.G * p.G;
+    const int rp = kRows / p.G * p.G;
     // the k-th item of the list as every other warp sees it
     auto take = [&](uint32_t k, Item& it) -> bool {
         const uint32_t sl = k % kItemSlots;
@@ -285,15 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
         uint32_t xc = 0, yc = 0;
         bool ok = true;
-        // the lane's block of key tiles j .. j + tiles - 1 (-1: none; -2: not in the cache)
+        // the lane's block of `tiles` key tiles from tile j on (-1: none; -2: not in the cache)
         auto entry = [&](const Item& it, int j, int tiles) -> int {
-            const int x = j * (kTile / kBlock) + lane;
-            if (lane >= tiles * (kTile / kBlock) || x * kBlock >= it.x.n) return -1;
+            const int x = j * (kKeys / kBlock) + lane;
+            if (lane >= tiles * (kKeys / kBlock) || x * kBlock >= it.x.n) return -1;
             const int blk = __ldg(p.tables + (long long)it.r * p.mbps + x);
             return blk >= 0 && blk < p.num_blocks ? blk : -2;
         };
-        // those blocks to dst, each as kH 64-column halves; kLse posts the
-        // tile's mask of blocks in the cache
+        // those blocks to dst; kLse posts the stage's mask of blocks in the cache
         auto load_keys = [&](const Item& it, uint32_t dst, uint32_t fb, int blk) {
             if (MODE == kLse && blk == -2) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
             const uint32_t msk = __ballot_sync(0xffffffffu, blk >= 0);
@@ -302,19 +363,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
             }
             __syncwarp();
-            if (blk >= 0) {
-                const uint32_t kd = dst + (lane >> 3) * SM::kT + (lane & 7) * kBlock * 128;
-                const int row0 = (blk * p.Hkv + it.h) * kBlock;
-                for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kTile * 128, &tmk, fb, 0, hh, row0, policy);
-            }
+            if (blk >= 0)
+                tma_load_4d(dst + lane * kH * kBlock * 128, &tmk, fb, 0, 0, 0, (blk * p.Hkv + it.h) * (kBlock / 8), policy);
         };
-        auto load_rows = [&](const Item& it, uint32_t dst, uint32_t fb, int row0, int tiles) {
+        // the block of query rows from row0 on
+        auto load_rows = [&](const Item& it, uint32_t dst, uint32_t fb, int row0) {
             if (lane == 0) {
-                mbar_arrive_expect_tx(fb, (uint32_t)(tiles * kH * tr) * 128u);
-                for (int t = 0; t < tiles; ++t)
-                    for (int hh = 0; hh < kH; ++hh)
-                        tma_load_4d(dst + t * SM::kT + hh * kTile * 128, &tmq, fb, 0, hh, it.h * p.G,
-                                    it.x.q0 + row0 / p.G + t * (tr / p.G), policy);
+                mbar_arrive_expect_tx(fb, (uint32_t)(kH * rp) * 128u);
+                for (int hh = 0; hh < kH; ++hh)
+                    tma_load_4d(dst + hh * kRows * 128, &tmq, fb, 0, hh, it.h * p.G, it.x.q0 + row0 / p.G, policy);
             }
             __syncwarp();
         };
@@ -332,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item it;
             it.xt = 0;
             if (i < total) {
-                it = item_at<MODE>(p, sums, i, step, xtiles);
+                it = item_at<MODE>(p, sums, i, step, xkeys);
                 if (MODE == kLse && it.y0 >= it.y1) {  // keys past what the rows see
                     i = pick(++k);
                     continue;
@@ -349,70 +406,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.xt == 0) break;
             i = pick(++k);
             if (it.y0 >= it.y1) continue;
-            const uint32_t xs = xc & 1;
-            if (!(ok = wait_warp(x_empty + 8 * xs, ((xc >> 1) & 1) ^ 1, p.wait_ns))) break;
-            const uint32_t xd = sbase + SM::kX + xs * 2 * SM::kT;
-            if (MODE == kSum)
-                load_keys(it, xd, x_full + 8 * xs, entry(it, it.row0 / kTile, it.xt));
-            else
-                load_rows(it, xd, x_full + 8 * xs, it.row0, it.xt);
-            ++xc;
-            // table entries are read a tile ahead of their use
-            int blk = MODE == kSum ? 0 : entry(it, it.y0, 1);
+            // X goes out at the latest before a wait for Y's ring: an item's
+            // first Y stages may land while the last item still holds X
+            const uint32_t xs = xc % kXSlots, xd = sbase + SM::kX + xs * SM::kXBytes;
+            const int xblk = MODE == kSum ? entry(it, it.row0 / kKeys, it.xt) : 0;
+            bool have_x = false;
+            auto load_x = [&]() -> bool {
+                have_x = true;
+                if (!wait_warp(x_empty + 8 * xs, ((xc / kXSlots) & 1) ^ 1, p.wait_ns)) return false;
+                if (MODE == kSum)
+                    load_keys(it, xd, x_full + 8 * xs, xblk);
+                else
+                    load_rows(it, xd, x_full + 8 * xs, it.row0);
+                ++xc;
+                return true;
+            };
+            // table entries are read a stage ahead of their use
+            constexpr int yt = MODE == kLse ? 2 : 1;  // key tiles of a stage
+            int blk = MODE == kSum ? 0 : entry(it, it.y0 * yt, yt);
             for (int j = it.y0; j < it.y1; ++j, ++yc) {
                 const int now = blk;
-                if (MODE != kSum && j + 1 < it.y1) blk = entry(it, j + 1, 1);
-                const uint32_t ys = yc % kYSlots;
-                if (!(ok = wait_warp(y_empty + 8 * ys, ((yc / kYSlots) & 1) ^ 1, p.wait_ns))) break;
+                if (MODE != kSum && j + 1 < it.y1) blk = entry(it, (j + 1) * yt, yt);
+                const uint32_t ys = yc % kYSlots, yp = ((yc / kYSlots) & 1) ^ 1;
+                if (!have_x && !__all_sync(0xffffffffu, mbar_test_wait(y_empty + 8 * ys, yp)) && !(ok = load_x())) break;
+                if (!(ok = wait_warp(y_empty + 8 * ys, yp, p.wait_ns))) break;
                 if (p.withhold && yc == 0) continue;
-                const uint32_t yd = sbase + SM::kY + ys * SM::kT;
+                const uint32_t yd = sbase + SM::kY + ys * SM::kYBytes;
                 if (MODE == kSum)
-                    load_rows(it, yd, y_full + 8 * ys, j * tr, 1);
+                    load_rows(it, yd, y_full + 8 * ys, j * rp);
                 else
                     load_keys(it, yd, y_full + 8 * ys, now);
             }
+            if (ok && !have_x) ok = load_x();
             if (!ok) break;
         }
         if (!ok) {
             if (lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             // copies issued land before the block's shared memory goes away
-            for (uint32_t s = 0; s < 2; ++s)
-                if (xc > s) (void)wait_warp(x_full + 8 * s, ((xc - 1 - s) / 2) & 1, drain_limit(p.wait_ns));
+            for (uint32_t s = 0; s < kXSlots; ++s)
+                if (xc > s) (void)wait_warp(x_full + 8 * s, ((xc - 1 - s) / kXSlots) & 1, drain_limit(p.wait_ns));
             for (uint32_t s = p.withhold ? 1 : 0; s < kYSlots; ++s)
                 if (yc > s) (void)wait_warp(y_full + 8 * s, ((yc - 1 - s) / kYSlots) & 1, drain_limit(p.wait_ns));
         }
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------- MMA issuer ----
-        constexpr uint32_t id = tc::idesc_bf16(kTile, kTile, false);
+        const uint32_t id = tc::idesc_bf16(kKeys, MODE == kWindow ? kKeys * p.xt : kRows, false);
         uint32_t xc = 0, yc = 0, sc = 0;
         bool ok = true;
         for (uint32_t ic = 0; ok; ++ic) {
             Item it;
             if (!(ok = take(ic, it)) || it.xt == 0) break;
             if (it.y0 >= it.y1) continue;
-            if (!(ok = wait_warp(x_full + 8 * (xc & 1), (xc >> 1) & 1, p.wait_ns))) break;
+            const uint32_t xs = xc % kXSlots, xa = sbase + SM::kX + xs * SM::kXBytes;
+            if (!(ok = wait_warp(x_full + 8 * xs, (xc / kXSlots) & 1, p.wait_ns))) break;
             for (int j = it.y0; ok && j < it.y1; ++j, ++yc) {
-                if (!(ok = wait_warp(y_full + 8 * (yc % kYSlots), (yc / kYSlots) & 1, p.wait_ns))) break;
-                const uint32_t ya = sbase + SM::kY + (yc % kYSlots) * SM::kT;
+                const uint32_t ys = yc % kYSlots, ya = sbase + SM::kY + ys * SM::kYBytes;
+                if (!(ok = wait_warp(y_full + 8 * ys, (yc / kYSlots) & 1, p.wait_ns))) break;
                 for (int t = 0; t < it.xt; ++t, ++sc) {
-                    const uint32_t b = sc % kGroups;
-                    if (!(ok = wait_warp(s_empty + 8 * b, ((sc / kGroups) & 1) ^ 1, p.wait_ns))) break;
+                    const uint32_t b = sc & 1;
+                    if (!(ok = wait_warp(s_empty + 8 * b, ((sc >> 1) & 1) ^ 1, p.wait_ns))) break;
                     tc::fence_after();
-                    const uint32_t xa = sbase + SM::kX + ((xc & 1) * 2 + t) * SM::kT;
+                    // query rows: 8-row groups 1024 B apart, halves 256 rows;
+                    // keys: groups kH * 1024 B apart, halves 1024 B
+                    const uint32_t ra = MODE == kSum ? ya : MODE == kLse ? xa + t * kKeys * 128 : xa;
+                    const uint32_t ka = MODE == kSum ? xa + t * SM::kKeyBytes : ya;
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kTile * 128 + (kk & 3) * 32;
-                        const uint64_t xd = tc::sdesc_sw128(xa + off, 16, 1024), yd = tc::sdesc_sw128(ya + off, 16, 1024);
-                        tc::mma_ss_elect(tbase + b * kTile, MODE == kWindow ? yd : xd, MODE == kWindow ? xd : yd, id,
-                                         kk > 0);
+                        const uint32_t in = (kk & 3) * 32;  // 16 bf16 of a 128-byte row
+                        const uint64_t rd = tc::sdesc_sw128(ra + (kk >> 2) * kRows * 128 + in, 16, 1024);
+                        const uint64_t kd = tc::sdesc_sw128(ka + (kk >> 2) * 1024 + in, 16, kH * 1024);
+                        tc::mma_ss_elect(tbase + b * kRows, MODE == kLse ? rd : kd, MODE == kLse ? kd : rd, id, kk > 0);
                     }
                     tc::commit_elect(s_full + 8 * b);
                     if (lane == 0) mbar_arrive(s_full + 8 * b);
                     __syncwarp();
                 }
-                if (ok) tc::commit_elect(y_empty + 8 * (yc % kYSlots));
+                if (ok) tc::commit_elect(y_empty + 8 * ys);
             }
-            if (ok) tc::commit_elect(x_empty + 8 * (xc & 1));
+            if (ok) tc::commit_elect(x_empty + 8 * xs);
             ++xc;
         }
         if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
@@ -423,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MODE != kLse) {
             // -------------------------------- the rows' log-sum-exps ----
             // Copied without a wait, so the ring is filled ahead; zero past a
-            // tile's rows. kSum: one slot per Y tile; kWindow: two per item,
-            // its X tiles.
+            // block's rows. kSum: a slot per Y stage; kWindow: one per item.
             uint32_t lc = 0;
             bool ok = true;
             for (uint32_t ic = 0; ok; ++ic) {
@@ -432,16 +502,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = take(ic, it)) || it.xt == 0) break;
                 const int rows = it.x.m * p.G;
                 const float* at = p.nlse + ((long long)it.h * p.T + it.x.q0) * p.G;
-                const int j0 = MODE == kSum ? it.y0 : 0, j1 = MODE == kSum ? it.y1 : 2;
+                const int j0 = MODE == kSum ? it.y0 : 0, j1 = MODE == kSum ? it.y1 : 1;
                 for (int j = j0; j < j1; ++j, ++lc) {
                     const uint32_t ls = lc % kLseSlots;
                     if (!(ok = wait_warp(l_empty + 8 * ls, ((lc / kLseSlots) & 1) ^ 1, p.wait_ns))) break;
 #pragma unroll
-                    for (int u = 0; u < kTile / 32; ++u) {
-                        const int c = u * 32 + lane, rho = j * tr + c;
-                        const bool in = c < tr && rho < rows;
+                    for (int u = 0; u < kRows / 32; ++u) {
+                        const int c = u * 32 + lane, rho = j * rp + c;
+                        const bool in = c < rp && rho < rows;
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                         sbase + SM::kLses + (ls * kTile + c) * 4),
+                                         sbase + SM::kLses + (ls * kRows + c) * 4),
                                      "l"(in ? at + rho : p.nlse), "r"(in ? 4 : 0)
                                      : "memory");
                     }
@@ -453,14 +523,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------- softmax ----
-        const int group = warp >> 2, quad = warp & 3;
+        const int quarter = warp >> 2, quad = warp & 3;
         const int my = quad * 32 + lane;  // row of a tile, tensor-memory lane
-        const uint32_t ts = tbase + ((uint32_t)(quad * 32) << 16) + (uint32_t)(group * kTile);
+        const int col0 = quarter * 64;    // of this warp's columns
+        const uint32_t ts0 = tbase + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
         const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
         const bool pos_scale = p.sl2 > 0.f;
         const float off_value = pos_scale ? -INFINITY : INFINITY;  // a masked logit, before the scale
-        uint32_t yc = 0, sc = 0, wc = 0;
+        uint32_t yc = 0, sc = 0;
         bool ok = true;
+        // columns lo .. hi - 1 of a chunk count
+        auto cut = [&](uint32_t (&x)[32], int lo, int hi) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (c < lo || c >= hi) x[c] = __float_as_uint(off_value);
+        };
+        auto give_back = [&](uint32_t b) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty + 8 * b);
+        };
+        // f(x, q) for the two chunks of 32 columns, the second loaded under the
+        // arithmetic of the first; with `give` the tile is handed back as soon
+        // as it is in registers
+        auto sweep = [&](uint32_t b, bool give, auto f) {
+            uint32_t xa[32], xb[32];
+            const uint32_t ts = ts0 + b * kRows;
+            tc::ld32(ts, xa);
+            tc::wait_ld();
+            tc::ld32(ts + 32u, xb);
+            f(xa, 0);
+            tc::wait_ld();
+            if (give) give_back(b);
+            f(xb, 1);
+        };
         for (uint32_t ic = 0;; ++ic) {
             Item it;
             if (!take(ic, it)) {
@@ -471,67 +567,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (it.xt == 0) break;
             const int rows = it.x.m * p.G;
-            // kLse: the last key this thread's row sees; kSum: the first row
-            // that sees this thread's key
-            const int tile = it.xt == 2 ? (group ^ (int)sc) & 1 : 0;  // this group's S tiles of the item
-            int bound = 0;
-            bool mine = false;
-            if (MODE == kLse) {
-                const int rho = it.row0 + tile * tr + my;
-                mine = my < tr && rho < rows;
-                bound = mine ? it.x.first + rho / p.G : 0x3FFFFFFF;
-            } else if (MODE == kSum) {
-                const int t = it.row0 + tile * kTile + my;
-                mine = t < it.x.n;
-                bound = mine ? max(0, t - it.x.first) * p.G : 0;
-            }
-            float m = -INFINITY, total_sum = 0.f;  // kLse: the sum is relative to 2^m
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-            // f(x, q) for the S tile's four chunks of 32 columns, the next one
-            // loaded under the arithmetic of the one at hand; stops after
-            // `cols` columns
-            auto sweep = [&](int cols, auto f) {
-                uint32_t xa[32], xb[32];
-                tc::ld32(ts, xa);
-#pragma unroll 1
-                for (int q = 0; q < 4; q += 2) {
-                    tc::wait_ld();
-                    tc::ld32(ts + 32u * q + 32u, xb);
-                    f(xa, q);
-                    tc::wait_ld();
-                    const bool more = 32 * q + 64 < cols;
-                    if (q == 0 && more) tc::ld32(ts + 64u, xa);
-                    if (32 * q + 32 < cols) f(xb, q + 1);
-                    if (!more) break;
-                }
-            };
-            // columns lo .. hi - 1 of a chunk count
-            auto cut = [&](uint32_t (&x)[32], int lo, int hi) {
+            // per tile: kLse: the last key this thread's row sees; kSum: the
+            // first row that sees this thread's key
+            int bound[2] = {0, 0};
+            bool mine[2] = {false, false};
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < lo || c >= hi) x[c] = __float_as_uint(off_value);
-            };
+            for (int t = 0; t < 2; ++t) {
+                if (MODE == kLse) {
+                    const int rho = it.row0 + t * kKeys + my;
+                    mine[t] = t < it.xt && t * kKeys + my < rp && rho < rows;
+                    bound[t] = mine[t] ? it.x.first + rho / p.G : 0x3FFFFFFF;
+                } else if (MODE == kSum) {
+                    const int key = it.row0 + t * kKeys + my;
+                    mine[t] = t < it.xt && key < it.x.n;
+                    bound[t] = mine[t] ? max(0, key - it.x.first) * p.G : 0;
+                }
+            }
+            float m[2] = {-INFINITY, -INFINITY};  // kLse: the sums are relative to 2^m
+            float sum[2] = {0.f, 0.f};
             if (MODE == kWindow)
-                ok = ok && wait_warp(l_full + 8 * (2 * ic % kLseSlots), (2 * ic / kLseSlots) & 1, p.wait_ns) &&
-                     wait_warp(l_full + 8 * ((2 * ic + 1) % kLseSlots), (2 * ic / kLseSlots) & 1, p.wait_ns);
+                ok = ok && wait_warp(l_full + 8 * (ic % kLseSlots), (ic / kLseSlots) & 1, p.wait_ns);
             for (int j = it.y0; ok && j < it.y1; ++j, ++yc) {
                 if (MODE == kSum &&
                     !(ok = wait_warp(l_full + 8 * (yc % kLseSlots), (yc / kLseSlots) & 1, p.wait_ns)))
                     break;
-                const int key = j * kTile + my;  // kWindow: this thread's key of the stage, its block and row there
+                const int key = j * kKeys + my;  // kWindow: this thread's key of the stage, and its block
                 int blk = -1;
-                // this group's S tile of the stage, if it has one
-                const int t = (group - (int)sc) & (kGroups - 1);
-                if (t < it.xt) {
-                    if (!(ok = wait_warp(s_full + 8 * group, ((sc + t) / kGroups) & 1, p.wait_ns))) break;
+                if (MODE == kWindow && quarter == 0 && key < it.x.n)
+                    blk = __ldg(p.tables + (long long)it.r * p.mbps + key / kBlock);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= it.xt || !ok) continue;
+                    const uint32_t b = sc & 1;
+                    if (!(ok = wait_warp(s_full + 8 * b, (sc >> 1) & 1, p.wait_ns))) continue;
                     tc::fence_after();
+                    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                    auto total = [&]() {
+                        const uint64_t a = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
+                        return tc::f2_lo(a) + tc::f2_hi(a);
+                    };
                     if (MODE == kLse) {
-                        const uint32_t msk = lds32(mask0 + (yc % kMaskSlots) * 4);
-                        const bool part = __any_sync(0xffffffffu, msk != 0xFFu || j * kTile + kTile - 1 > bound);
+                        const int key0 = j * 2 * kKeys + col0;
+                        const uint32_t msk = (lds32(mask0 + (yc % kMaskSlots) * 4) >> (4 * quarter)) & 0xFu;
+                        const bool part = __any_sync(0xffffffffu, msk != 0xFu || key0 + 63 > bound[t]);
                         auto mask = [&](uint32_t (&x)[32], int q) {
-                            if (!part) return;
                             const uint32_t have = (msk >> (2 * q)) & 3u;
-                            const int hi = bound - (j * kTile + 32 * q) + 1;
+                            const int hi = bound[t] - (key0 + 32 * q) + 1;
                             cut(x, have & 1u ? 0 : 16, have & 2u ? hi : min(hi, 16));
                         };
                         // The sum is relative to m, the largest of the first
@@ -539,12 +620,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // lie below, and above until it nears overflow. Only
                         // then, and at first, is a maximum taken and the sum
                         // moved to it.
-                        bool top = __any_sync(0xffffffffu, m == -INFINITY);
+                        bool top = __any_sync(0xffffffffu, m[t] == -INFINITY);
                         for (;;) {
                             if (top) {
                                 float e4[4] = {off_value, off_value, off_value, off_value};
-                                sweep(kTile, [&](uint32_t (&x)[32], int q) {
-                                    mask(x, q);
+                                sweep(b, false, [&](uint32_t (&x)[32], int q) {
+                                    if (part) mask(x, q);
 #pragma unroll
                                     for (int c = 0; c < 32; ++c)
                                         e4[c & 3] = pos_scale ? fmaxf(e4[c & 3], __uint_as_float(x[c]))
@@ -552,90 +633,90 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 });
                                 const float best = (pos_scale ? fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]))
                                                               : fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]))) * p.sl2;
-                                total_sum *= best > m ? ex2(m - best) : 1.f;
-                                m = fmaxf(m, best);
+                                sum[t] *= best > m[t] ? ex2(m[t] - best) : 1.f;
+                                m[t] = fmaxf(m[t], best);
                             }
-                            const float nu = m == -INFINITY ? 0.f : -m;
+                            const float nu = m[t] == -INFINITY ? 0.f : -m[t];
                             const uint64_t nu2 = tc::f2(nu, nu);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) acc[c] = 0ull;
-                            sweep(kTile, [&](uint32_t (&x)[32], int q) {
-                                mask(x, q);
+                            auto add = [&](uint32_t (&x)[32]) {
 #pragma unroll
                                 for (int c = 0; c < 16; ++c) {
                                     const uint64_t a = tc::fma2(tc::f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nu2);
                                     acc[c & 3] = tc::add2(acc[c & 3], tc::f2(ex2(tc::f2_lo(a)), ex2(tc::f2_hi(a))));
                                 }
-                            });
-                            const uint64_t a2 = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
-                            const float now = total_sum + (tc::f2_lo(a2) + tc::f2_hi(a2));
+                            };
+                            if (part)
+                                sweep(b, false, [&](uint32_t (&x)[32], int q) { mask(x, q); add(x); });
+                            else
+                                sweep(b, false, [&](uint32_t (&x)[32], int) { add(x); });
+                            const float now = sum[t] + total();
                             if (top || !__any_sync(0xffffffffu, now > 0x1p100f)) {
-                                total_sum = now;
+                                sum[t] = now;
                                 break;
                             }
                             top = true;
                         }
+                        give_back(b);
                     } else {
-                        // the Y rows of kSum, the X rows of kWindow: columns
-                        // from `first` on see the thread's key, `cols` hold rows
-                        const int row0 = (MODE == kSum ? j : tile) * tr, cols = min(tr, rows - row0);
-                        if (MODE == kWindow) {
-                            if (t == 0 && key < it.x.n) blk = __ldg(p.tables + (long long)it.r * p.mbps + key / kBlock);
-                            bound = (key - it.x.first) * p.G;
-                        }
-                        const int first = bound - row0;
-                        const bool part = __any_sync(0xffffffffu, first > 0) || (cols & 31) != 0;
-                        const uint32_t la = sbase + SM::kLses + ((MODE == kSum ? yc : 2 * ic + tile) % kLseSlots) * kTile * 4;
-                        if (MODE == kWindow) {
+                        // the Y rows of kSum, the X rows of kWindow: of this
+                        // warp's columns those from `first` on see the thread's
+                        // key, and `cols` hold rows
+                        const int row0 = (MODE == kSum ? j * rp : 0) + col0;
+                        const int cols = min(min(rp - col0, 64), rows - row0);
+                        const int first = (MODE == kSum ? bound[t] : (key - it.x.first) * p.G) - row0;
+                        const bool part = __any_sync(0xffffffffu, first > 0) || cols < 64;
+                        const uint32_t la = sbase + SM::kLses + (((MODE == kSum ? yc : ic) % kLseSlots) * kRows + col0) * 4;
+                        auto add = [&](uint32_t (&x)[32], int q) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) acc[c] = 0ull;
-                        }
-                        if (cols > 0)
-                            sweep(cols, [&](uint32_t (&x)[32], int q) {
-                                if (part) cut(x, first - 32 * q, cols - 32 * q);
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    uint32_t l0, l1, l2, l3;
-                                    lds128(la + 128 * q + 16 * c, l0, l1, l2, l3);
-                                    const uint64_t a0 = tc::fma2(tc::f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sc2,
-                                                                 tc::f2(__uint_as_float(l0), __uint_as_float(l1)));
-                                    const uint64_t a1 = tc::fma2(tc::f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sc2,
-                                                                 tc::f2(__uint_as_float(l2), __uint_as_float(l3)));
-                                    acc[(2 * c) & 3] = tc::add2(acc[(2 * c) & 3], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
-                                    acc[(2 * c + 1) & 3] = tc::add2(acc[(2 * c + 1) & 3], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
-                                }
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t l0, l1, l2, l3;
+                                lds128(la + 128 * q + 16 * c, l0, l1, l2, l3);
+                                const uint64_t a0 = tc::fma2(tc::f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sc2,
+                                                             tc::f2(__uint_as_float(l0), __uint_as_float(l1)));
+                                const uint64_t a1 = tc::fma2(tc::f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sc2,
+                                                             tc::f2(__uint_as_float(l2), __uint_as_float(l3)));
+                                acc[(2 * c) & 3] = tc::add2(acc[(2 * c) & 3], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
+                                acc[(2 * c + 1) & 3] = tc::add2(acc[(2 * c + 1) & 3], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
+                            }
+                        };
+                        if (cols <= 0)
+                            give_back(b);
+                        else if (part)
+                            sweep(b, true, [&](uint32_t (&x)[32], int q) {
+                                if (32 * q >= cols) return;
+                                cut(x, first - 32 * q, cols - 32 * q);
+                                add(x, q);
                             });
+                        else
+                            sweep(b, true, [&](uint32_t (&x)[32], int q) { add(x, q); });
+                        if (MODE == kSum) sum[t] += total();
                     }
-                    // the tile has been read: hand it back
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_empty + 8 * group);
                     if (MODE == kWindow) {
-                        // the second tile's group hands its sums to the first's
-                        // through one of two places (the first group's S tile of
-                        // two stages on waits for it to be done with this one)
-                        const uint64_t a = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
-                        float w = tc::f2_lo(a) + tc::f2_hi(a);
-                        const int place = (group & 2) + (int)(wc & 1);
-                        float* comb = reinterpret_cast<float*>(base + SM::kComb) + place * kTile;
-                        if (t == 1) {
-                            comb[my] = w;
+                        // the other quarters hand their sums to the first one
+                        // through one of four places: they come to a place
+                        // again four S tiles on, and the tile before the last
+                        // of these is given back by the first quarter only
+                        // once it is done with this place
+                        const int place = (int)(sc & 3);
+                        float* comb = reinterpret_cast<float*>(base + SM::kComb) + place * 3 * kKeys;
+                        float w = total();
+                        if (quarter > 0) {
+                            comb[(quarter - 1) * kKeys + my] = w;
                             __syncwarp();
                             if (lane == 0) mbar_arrive(c_full + 8 * place);
                         } else {
-                            if (it.xt == 2) {
-                                if (!(ok = wait_warp(c_full + 8 * place, (wc >> 1) & 1, p.wait_ns))) break;
-                                w += comb[my];
-                            }
+                            if (!(ok = wait_warp(c_full + 8 * place, (sc >> 2) & 1, p.wait_ns))) continue;
+                            w = (w + comb[my]) + (comb[kKeys + my] + comb[2 * kKeys + my]);
                             if (blk >= 0 && blk < p.num_blocks) {
                                 float* at = p.scores + ((long long)blk * p.Hkv + it.h) * kBlock + key % kBlock;
                                 *at = p.fresh || key >= it.x.first ? w : *at + w;
                             }
                         }
-                        ++wc;
                     }
+                    ++sc;
                 }
-                sc += it.xt;
                 if (MODE == kSum) {
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(l_empty + 8 * (yc % kLseSlots));
@@ -644,46 +725,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (MODE == kWindow) {
                 if (!ok) break;
                 __syncwarp();
-                if (lane < 2) mbar_arrive(l_empty + 8 * ((2 * ic + lane) % kLseSlots));
+                if (lane == 0) mbar_arrive(l_empty + 8 * (ic % kLseSlots));
                 continue;
             }
-            // the groups that share a row: every second one, or all four for a
-            // single tile. A warp whose wait ran out still meets the others
-            // here, and all of them leave together.
-            float sum = total_sum;
-            if (MODE == kSum) {
-                const uint64_t a = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
-                sum = tc::f2_lo(a) + tc::f2_hi(a);
-            }
-            float2* comb = reinterpret_cast<float2*>(base + SM::kComb) + (ic & 1) * kGroups * kTile;
+            // the quarters of a row. A warp whose wait ran out still meets the
+            // others here, and all of them leave together.
+            float2* comb = reinterpret_cast<float2*>(base + SM::kComb) + (ic & 1) * 2 * kQuarters * kKeys;
             if (!ok && lane == 0) failed[ic & 1] = 1;
-            comb[group * kTile + my] = make_float2(m, sum);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) comb[(t * kQuarters + quarter) * kKeys + my] = make_float2(m[t], sum[t]);
             asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
             if (failed[ic & 1]) {
                 ok = false;
                 break;
             }
-            if (mine && group < it.xt) {
-                float2 q[4];
-                const int parts = it.xt == 2 ? 2 : 4;
+            if (quarter < 2 && (quarter == 0 ? mine[0] : mine[1])) {
+                const int t = quarter;  // this warp finishes tile t
+                float2 q[kQuarters];
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    q[u] = u < parts ? comb[(it.xt == 2 ? u * 2 + group : u) * kTile + my] : make_float2(-INFINITY, 0.f);
+                for (int u = 0; u < kQuarters; ++u) q[u] = comb[(t * kQuarters + u) * kKeys + my];
                 if (MODE == kLse) {
                     const float M = fmaxf(fmaxf(q[0].x, q[1].x), fmaxf(q[2].x, q[3].x));
                     const float v = M == -INFINITY ? 0.f : M;
                     const float l = (q[0].y * exp2f(q[0].x - v) + q[1].y * exp2f(q[1].x - v)) +
                                     (q[2].y * exp2f(q[2].x - v) + q[3].y * exp2f(q[3].x - v));
-                    const int rho = it.row0 + tile * tr + my;
+                    const int rho = it.row0 + t * kKeys + my;
                     p.part[((long long)(it.x.q0 + rho / p.G) * p.Hq + (long long)it.h * p.G + rho % p.G) * p.splits + it.split] =
                         l == 0.f ? -INFINITY : M + log2f(l);
                 } else {
                     const float w = (q[0].y + q[1].y) + (q[2].y + q[3].y);
-                    const int t = it.row0 + tile * kTile + my;
-                    const int blk = __ldg(p.tables + (long long)it.r * p.mbps + t / kBlock);
+                    const int key = it.row0 + t * kKeys + my;
+                    const int blk = __ldg(p.tables + (long long)it.r * p.mbps + key / kBlock);
                     if (blk >= 0 && blk < p.num_blocks) {
-                        float* at = p.scores + ((long long)blk * p.Hkv + it.h) * kBlock + t % kBlock;
-                        *at = p.fresh || t >= it.x.first ? w : *at + w;
+                        float* at = p.scores + ((long long)blk * p.Hkv + it.h) * kBlock + key % kBlock;
+                        *at = p.fresh || key >= it.x.first ? w : *at + w;
                     }
                 }
             }
@@ -718,7 +793,7 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Windo
     }
     const Request x = request_of(p, lo);
     if (x.m < 0) return;
-    const int n = ceil_div(seen_tiles(p, x, (i - x.q0) / (2 * (kTile / p.G))), step);
+    const int n = ceil_div(seen_stages(p, x, (i - x.q0) / (kRows / p.G)), step);
     const float* at = p.part + row * p.splits;
     float M = -INFINITY, sum = 0.f;
 #pragma unroll 8
@@ -753,8 +828,8 @@ template <int HD, int MODE>
 bool launch_window(const CUtensorMap& tq, const CUtensorMap& tk, const WindowParams& p, cudaStream_t st) {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    if (!raise_smem(reinterpret_cast<const void*>(window_kernel<HD, MODE>), WinSmem<HD>::kTotal, done, mu)) return false;
-    return launch_pdl(window_kernel<HD, MODE>, p.sms, kThreads, WinSmem<HD>::kTotal, st, tq, tk, p) == cudaSuccess;
+    if (!raise_smem(reinterpret_cast<const void*>(window_kernel<HD, MODE>), WinSmem<HD, MODE>::kTotal, done, mu)) return false;
+    return launch_pdl(window_kernel<HD, MODE>, p.sms, kThreads, WinSmem<HD, MODE>::kTotal, st, tq, tk, p) == cudaSuccess;
 }
 
 }  // namespace
@@ -814,20 +889,19 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     p.withhold = test_withhold_copy() ? 1 : 0;
     CUtensorMap tq, tk;
     // without queries nothing is loaded through the first map; it may name any tensor
-    if (!make_tmap_q_group(&tq, total_q > 0 ? q : k_cache, total_q > 0 ? total_q : 1, D.Hq, HD, G, kTile / G * G) ||
-        !make_tmap_kv_halves(&tk, k_cache, (long long)D.num_blocks * D.Hkv * kBlock, HD))
+    if (!make_tmap_q_group(&tq, total_q > 0 ? q : k_cache, total_q > 0 ? total_q : 1, D.Hq, HD, G, kRows / G * G) ||
+        !make_tmap_kv_groups(&tk, k_cache, (long long)D.num_blocks * D.Hkv * kBlock, HD))
         return MI_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
     const long long rows = (long long)total_q * D.Hq;
     const bool wide = HD == 128;
+    // few enough rows stay resident while the keys stream
+    const bool few = max_query_len <= kRows / G;
+    p.xt = (long long)max_query_len * G <= kKeys ? 1 : 2;
     bool ok = wide ? launch_window<128, kLse>(tq, tk, p, st) : launch_window<64, kLse>(tq, tk, p, st);
     if (ok)
         ok = launch_pdl(window_merge_kernel, (int)((rows + kMergeThreads) / kMergeThreads), kMergeThreads, 0, st, p) ==
              cudaSuccess;
-    // rows that fit in two tiles stay resident while the keys stream
-    const int tr = kTile / G * G;
-    const bool few = (long long)max_query_len * G <= 2 * tr;
-    p.xt = max_query_len * G <= tr ? 1 : 2;
     if (ok && few) ok = wide ? launch_window<128, kWindow>(tq, tk, p, st) : launch_window<64, kWindow>(tq, tk, p, st);
     if (ok && !few) ok = wide ? launch_window<128, kSum>(tq, tk, p, st) : launch_window<64, kSum>(tq, tk, p, st);
     return ok ? MI_OK : MI_ERR_CUDA;

@@ -532,8 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float off_value = pos_scale ? -INFINITY : INFINITY;  // a masked logit, before the scale
         uint32_t yc = 0, sc = 0;
         bool ok = true;
-        // columns lo .. hi - 1 of a chunk count
+        // Columns lo .. hi - 1 of a chunk count. The empty statement keeps the
+        // masked loops apart from the plain ones: merged into one, with the
+        // mask as selects on every logit, they took a fifth longer.
         auto cut = [&](uint32_t (&x)[32], int lo, int hi) {
+            asm volatile("" ::: "memory");
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 if (c < lo || c >= hi) x[c] = __float_as_uint(off_value);

@@ -59,6 +59,7 @@ constexpr int kMaxG = 8;
 // batch)
 constexpr int kUnitCostE4m3 = 10;
 constexpr int kUnitCostBf16 = 6;
+constexpr int kUnitCostPrefix = 12;  // bf16 and the merge of the prefix's partial results
 // Fewest blocks a CTA's range is cut to (measured on one layer of 8 requests
 // of 200 tokens, 4 KV heads: 11 us with 32 CTAs against 17 us on all 304;
 // larger batches keep the whole grid).
@@ -451,27 +452,45 @@ __device__ __forceinline__ void store_logits(float* lg, int gp, int lane, float 
 
 // Shared-prefix step: folds the prefix's partial results of head h's row g of
 // a request (`at`: its entry of DecodeExt::rows) into four of its own outputs
-// v, whose log2-sum-exp is lse (-inf: no own tokens). Partials are taken in order.
+// v, whose log2-sum-exp is lse (-inf: no own tokens). The HD / 4 lanes that
+// hold the row call it together: each fetches the log-sum-exp of one split,
+// so the weights cost one load for up to HD / 4 splits, and the outputs are
+// then independent loads. Partials are taken in order.
 template <int HD>
 __device__ __forceinline__ float4 merge_prefix(const DecodeExt& x, int4 at, int Hkv, int h, int g, int dcol, float lse,
                                                float4 v) {
+    constexpr int L = HD / 4;
+    const int lane = threadIdx.x & 31, sub = lane & (L - 1);
+    const unsigned lanes = L == 32 ? 0xffffffffu : 0xffffu << (lane & ~(L - 1));
     auto row = [&](int s) { return (long long)(at.x + s * Hkv + h) * x.slot_rows + at.z + g; };
-    float M = lse;
-    for (int s = 0; s < at.y; ++s) M = fmaxf(M, __ldcg(x.part_lse + row(s)));
-    if (M == kNegInf) return make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = exp2f(lse - M);
-    float4 num = den > 0.f ? make_float4(den * v.x, den * v.y, den * v.z, den * v.w) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < at.y; ++s) {
-        const float w = exp2f(__ldcg(x.part_lse + row(s)) - M);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part + row(s) * HD + dcol));
-        den += w;
-        num.x += w * o.x;
-        num.y += w * o.y;
-        num.z += w * o.z;
-        num.w += w * o.w;
+    float M = lse, den = lse > kNegInf ? 1.f : 0.f;
+    float4 num = den > 0.f ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < at.y; s0 += L) {
+        const int cnt = min(at.y - s0, L);
+        const float mine = sub < cnt ? __ldcg(x.part_lse + row(s0 + sub)) : kNegInf;
+        float top = mine;
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
+        top = fmaxf(top, M);
+        if (top == kNegInf) continue;
+        const float old = exp2f(M - top), w = exp2f(mine - top);
+        M = top;
+        float ws = w;
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) ws += __shfl_xor_sync(lanes, ws, o);
+        den = den * old + ws;
+        num = make_float4(num.x * old, num.y * old, num.z * old, num.w * old);
+#pragma unroll 8
+        for (int k = 0; k < cnt; ++k) {
+            const float wk = __shfl_sync(lanes, w, (lane & ~(L - 1)) + k);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part + row(s0 + k) * HD + dcol));
+            num.x += wk * o.x;
+            num.y += wk * o.y;
+            num.z += wk * o.z;
+            num.w += wk * o.w;
+        }
     }
-    const float r = 1.f / den;
+    const float r = den > 0.f ? 1.f / den : 0.f;
     return make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
 }
 
@@ -1235,7 +1254,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
     // Ranges are cut by cost: a unit weighs its blocks plus a fixed number of
     // blocks for its per-unit work (q, the merge, the pipeline restart at its
     // boundary), which weighs more against the half-size one-byte blocks.
-    constexpr int uc = kOneByte ? kUnitCostE4m3 : kUnitCostBf16;
+    constexpr int uc = EXT == kExtPrefix ? kUnitCostPrefix : kOneByte ? kUnitCostE4m3 : kUnitCostBf16;
     const int cta = blockIdx.x;
     RangePlan* rp = reinterpret_cast<RangePlan*>(base + sp.rplan);
     long long TB = 0, TC = 0;
@@ -1279,7 +1298,9 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
         // kMinBlocksPerCta blocks each (a small batch): every CTA's fixed cost
         // (the plan, the first copies, a merge) then outweighs its share of
         // streaming, and fewer, longer ranges finish sooner.
-        const long long Pw = (TB + kMinBlocksPerCta - 1) / kMinBlocksPerCta;
+        // (A shared-prefix step's units are mostly that fixed cost: they count
+        // with it.)
+        const long long Pw = ((EXT == kExtPrefix ? TC : TB) + kMinBlocksPerCta - 1) / kMinBlocksPerCta;
         P = (int)(Pw < (long long)gridDim.x ? Pw : (long long)gridDim.x);
         plan_ranges(p, uc, scan, TB, TC, P, rp);  // (ends with a barrier of all warps)
         if (pe) {
@@ -1486,17 +1507,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                 const int n = __ldg(p.context_lens + b);
                 if (n > p.mbps * kBlock && lane == W) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
                 if (n <= 0) {
-                    if constexpr (EXT == kExtPrefix) {
-                        const int4 at = __ldcg(p.ext.rows + b);
-                        uint2* row = reinterpret_cast<uint2*>(p.out + (long long)b * p.Hq * HD);
-                        for (int i = lane - W; i < p.Hq * HD / 4; i += nl) {
-                            const int j = i / (HD / 4);
-                            row[i] = pack_bf16x4(merge_prefix<HD>(p.ext, at, p.Hkv, j / p.G, j % p.G,
-                                                                  (i % (HD / 4)) * 4, kNegInf,
-                                                                  make_float4(0.f, 0.f, 0.f, 0.f)));
-                        }
-                        continue;
-                    }
+                    if constexpr (EXT == kExtPrefix) continue;  // (the consumer warps write them)
                     uint4* row = reinterpret_cast<uint4*>(p.out + (long long)b * p.Hq * HD);
                     for (int i = lane - W; i < p.Hq * HD / 8; i += nl) row[i] = make_uint4(0, 0, 0, 0);
                 }
@@ -1617,6 +1628,19 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
     }
 
     // ---------------------------------------------------- consumer warps --
+    if constexpr (EXT == kExtPrefix) {
+        // requests without tokens of their own: the prefix's result alone
+        for (long long u = cta; u < (long long)p.B * p.Hkv; u += gridDim.x) {
+            const int b = (int)(u / p.Hkv), h = (int)(u % p.Hkv);
+            if (ctx_clamped(p, b) > 0) continue;
+            const int4 at = __ldcg(p.ext.rows + b);
+            for (int idx = 4 * tid; idx < p.G * HD; idx += 4 * W * 32) {
+                const int g = idx / HD, dcol = idx - g * HD;
+                const float4 v = merge_prefix<HD>(p.ext, at, p.Hkv, h, g, dcol, kNegInf, make_float4(0.f, 0.f, 0.f, 0.f));
+                *reinterpret_cast<uint2*>(p.out + ((long long)b * p.Hq + (long long)h * p.G) * HD + idx) = pack_bf16x4(v);
+            }
+        }
+    }
     if (cta >= P) return;
     float* mbuf = reinterpret_cast<float*>(base + sp.mbuf);
     float* lbuf = reinterpret_cast<float*>(base + sp.lbuf);

@@ -887,7 +887,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // first launch of mi_paged_decode_attention_prefix): the rows are the (request,
 // head) pairs of up to 256 / G requests of a group, every one sees all keys of
 // the item's split, and each row's fp32 output and log-sum-exp go to the
-// item's slot. A group of at most 128 rows runs one Q tile.
+// item's slot. A group of at most 128 rows runs one Q tile. A block runs
+// its share of the items one after another (one block per SM: blocks without
+// an item would each wait for an SM of their own).
 
 constexpr int kT2Keys = 128;                 // keys per stage
 constexpr int kT2Blocks = kT2Keys / kBlock;  // 16-token blocks per stage
@@ -929,444 +931,463 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     // a Q tile holds whole tokens: 128 / G of them, G rows each; the CTA's
     // two tiles are consecutive, tr rows apart
     const int tr = (kTcRows / p.G) * p.G;
-    Item it;
-    const int32_t* table;  // of the item's keys
-    int slot = 0;
-    bool two = true;       // both Q tiles hold rows
+    long long items = 1, item = 0, step = 0;  // PREFIX: the plan's, and this block's
+    __shared__ long long sums[PREFIX ? flat_words(kT2Threads) : 1];
     if constexpr (PREFIX) {
-        __shared__ long long sums[flat_words(kT2Threads)];
-        PrefixItem x;
-        if (!prefix_item(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, x)) return;
-        it.r = x.g;
-        it.h = x.h;
-        it.q0 = x.b0;
-        it.m = x.count;
-        it.n = x.n;
-        it.first = 0;
-        it.rho0 = 0;
-        it.nrows = it.rows_here = x.count * p.G;
-        it.p_hi = x.n - 1;
-        it.nblk = (x.n + kBlock - 1) / kBlock;
-        table = p.block_tables + (long long)x.g * p.mbps + x.blk0;
-        slot = x.slot;
-        two = it.nrows > tr;
-    } else {
-        if (!work_item(p, 2 * tr, it)) return;
-        table = p.block_tables + (long long)it.r * p.mbps;
+        items = prefix_plan(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, step);
+        item = blockIdx.x;
+        if (item >= items) return;
     }
-    const int nst = (it.nblk + kT2Blocks - 1) / kT2Blocks;
-    const uint32_t bar = sbase + SM::kBar;
-    const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
-    const uint32_t v_empty0 = v_full0 + 16, s_full0 = v_empty0 + 16, p_full0 = s_full0 + 16;
-    const uint32_t o_done0 = p_full0 + 16, fin = o_done0 + 16;
-    const uint32_t mask0 = sbase + SM::kMask;
+    uint32_t tbase = 0;
+    bool bad = false;  // a wait ran out
+    for (bool first = true; item < items; item += gridDim.x, first = false) {
+        Item it;
+        const int32_t* table;  // of the item's keys
+        int slot = 0;
+        bool two = true;       // both Q tiles hold rows
+        if constexpr (PREFIX) {
+            const PrefixItem x = prefix_item(p.w, p.Hkv, p.mbps, 2 * tr / p.G, sums, step, item);
+            it.r = x.g;
+            it.h = x.h;
+            it.q0 = x.b0;
+            it.m = x.count;
+            it.n = x.n;
+            it.first = 0;
+            it.rho0 = 0;
+            it.nrows = it.rows_here = x.count * p.G;
+            it.p_hi = x.n - 1;
+            it.nblk = (x.n + kBlock - 1) / kBlock;
+            table = p.block_tables + (long long)x.g * p.mbps + x.blk0;
+            slot = x.slot;
+            two = it.nrows > tr;
+        } else {
+            if (!work_item(p, 2 * tr, it)) return;
+            table = p.block_tables + (long long)it.r * p.mbps;
+        }
+        const int nst = (it.nblk + kT2Blocks - 1) / kT2Blocks;
+        const uint32_t bar = sbase + SM::kBar;
+        const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
+        const uint32_t v_empty0 = v_full0 + 16, s_full0 = v_empty0 + 16, p_full0 = s_full0 + 16;
+        const uint32_t o_done0 = p_full0 + 16, fin = o_done0 + 16;
+        const uint32_t mask0 = sbase + SM::kMask;
 
-    if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(k_full0 + i * 8, 1);
-        for (int i = 0; i < kT2KSlots; ++i) mbar_init(k_empty0 + i * 8, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(v_full0 + i * 8, 1);
-            mbar_init(v_empty0 + i * 8, 1);
-            mbar_init(s_full0 + i * 8, 1);
-            mbar_init(p_full0 + i * 8, 256);  // every softmax thread of the tile
-            mbar_init(o_done0 + i * 8, 1);
+        if (threadIdx.x == 0) {
+            if (!first)
+                for (int i = 0; i < SM::kNBar; ++i) mbar_inval(bar + i * 8);
+            mbar_init(q_full, 1);
+            for (int i = 0; i < 4; ++i) mbar_init(k_full0 + i * 8, 1);
+            for (int i = 0; i < kT2KSlots; ++i) mbar_init(k_empty0 + i * 8, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(v_full0 + i * 8, 1);
+                mbar_init(v_empty0 + i * 8, 1);
+                mbar_init(s_full0 + i * 8, 1);
+                mbar_init(p_full0 + i * 8, 256);  // every softmax thread of the tile
+                mbar_init(o_done0 + i * 8, 1);
+            }
+            mbar_init(fin, 1);
+            fence_mbar_init();
         }
-        mbar_init(fin, 1);
-        fence_mbar_init();
-    }
-    if (warp == kT2MmaWarp) {
-        tc::alloc(sbase + SM::kTmem, kT2Cols);
-        tc::relinquish();
-    }
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    const uint32_t tbase = lds_u32(sbase + SM::kTmem);
+        if (first && warp == kT2MmaWarp) {
+            tc::alloc(sbase + SM::kTmem, kT2Cols);
+            tc::relinquish();
+        }
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+        tbase = lds_u32(sbase + SM::kTmem);
 
-    if (warp == kT2MmaWarp + 1) {
-        // ------------------------------------------------ producer warp --
-        const uint64_t policy = l2_policy_evict_normal();
-        if (lane == 0 && nst > 0) {
-            mbar_arrive_expect_tx(q_full, (two ? 2u : 1u) * kH * (uint32_t)tr * 128u);
-            for (int t = 0; t < (two ? 2 : 1); ++t)
-                for (int hh = 0; hh < kH; ++hh)
-                    tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
-                                it.q0 + (it.rho0 + t * tr) / p.G, policy);
-        }
-        int pblk = -1;
-        bool pok = false;
-        auto load_v = [&](int jv) -> bool {
-            const int sl = jv & 1, u = jv >> 1;
-            if (!wait_all(v_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) return false;
-            const uint32_t msk = __ballot_sync(0xffffffffu, pok);
-            const uint32_t fb = v_full0 + sl * 8;
-            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
-            __syncwarp();
-            if (pok) {
-                // one copy per block: both 128-byte halves of its 16 rows
-                const uint32_t vd = sbase + SM::kRingV + sl * SM::kKV + lane * kH * kBlock * 128;
-                const int row0 = (pblk * p.Hkv + it.h) * kBlock;
-                tma_load_3d(vd, &tmv, fb, 0, row0, 0, policy);
+        if (warp == kT2MmaWarp + 1) {
+            // ------------------------------------------------ producer warp --
+            const uint64_t policy = l2_policy_evict_normal();
+            if (lane == 0 && nst > 0) {
+                mbar_arrive_expect_tx(q_full, (two ? 2u : 1u) * kH * (uint32_t)tr * 128u);
+                for (int t = 0; t < (two ? 2 : 1); ++t)
+                    for (int hh = 0; hh < kH; ++hh)
+                        tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
+                                    it.q0 + (it.rho0 + t * tr) / p.G, policy);
             }
-            return true;
-        };
-        bool pgood = true;
-        // block-table entries are read a stage ahead, before the wait for
-        // the slot, so their load latency is hidden
-        auto table_entry = [&](int jj) -> int {
-            const int x = jj * kT2Blocks + lane;
-            return (lane < kT2Blocks && x < it.nblk) ? __ldg(table + x) : -1;
-        };
-        int nblk_next = table_entry(0);
-        for (int j = 0; j < nst; ++j) {
-            const int sl = j % kT2KSlots, u = j / kT2KSlots;
-            const int x = j * kT2Blocks + lane;
-            const int blk = nblk_next;
-            if (j + 1 < nst) nblk_next = table_entry(j + 1);
-            if (!wait_all(k_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) {
-                pgood = false;
-                break;
-            }
-            bool ok = false;
-            if (lane < kT2Blocks && x < it.nblk) {
-                ok = blk >= 0 && blk < p.num_blocks;
-                if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
-            }
-            const uint32_t msk = __ballot_sync(0xffffffffu, ok);
-            const uint32_t fb = k_full0 + (j & 3) * 8;
-            // failure-detection test: stage 0's K is neither copied nor
-            // announced, so every wait on it runs out
-            const bool held = p.withhold != 0 && j == 0;
-            if (lane == 0 && !held) {
-                sts32(mask0 + (j & 3) * 4, msk);
-                mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
-            }
-            __syncwarp();
-            if (ok && !held) {
-                const uint32_t kd = sbase + SM::kRingK + sl * SM::kKV + lane * kBlock * 128;
-                const int row0 = (blk * p.Hkv + it.h) * kBlock;
-                for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kT2Keys * 128, &tmk, fb, 0, hh, row0, policy);
-            }
-            if (j > 0 && !load_v(j - 1)) {
-                pgood = false;
-                break;
-            }
-            pblk = blk;
-            pok = ok;
-        }
-        if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
-        if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
-    } else if (warp == kT2MmaWarp) {
-        // -------------------------------------------------- MMA issuer --
-        // The whole warp runs the loop; one elected lane issues each MMA
-        // and commit.
-        if (nst > 0) {
-            constexpr uint32_t idS = tc::idesc_bf16(kTcRows, kT2Keys, false);
-            constexpr uint32_t idO = tc::idesc_bf16(kTcRows, HD, true);
-            auto issue_s = [&](int t, int j) {
-                const uint32_t kbase = sbase + SM::kRingK + (j % kT2KSlots) * SM::kKV;
-                const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
-                    const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
-                    const uint64_t bd = tc::sdesc_sw128(kbase + (kk >> 2) * kT2Keys * 128 + off, 16, 1024);
-                    tc::mma_ss_elect(tbase + 256u * t + 128u, a, bd, idS, kk > 0);
+            int pblk = -1;
+            bool pok = false;
+            auto load_v = [&](int jv) -> bool {
+                const int sl = jv & 1, u = jv >> 1;
+                if (!wait_all(v_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) return false;
+                const uint32_t msk = __ballot_sync(0xffffffffu, pok);
+                const uint32_t fb = v_full0 + sl * 8;
+                if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
+                __syncwarp();
+                if (pok) {
+                    // one copy per block: both 128-byte halves of its 16 rows
+                    const uint32_t vd = sbase + SM::kRingV + sl * SM::kKV + lane * kH * kBlock * 128;
+                    const int row0 = (pblk * p.Hkv + it.h) * kBlock;
+                    tma_load_3d(vd, &tmv, fb, 0, row0, 0, policy);
                 }
-                tc::commit_elect(s_full0 + t * 8);
+                return true;
             };
-            auto issue_o = [&](int t, int j) {
-                const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
-                const uint32_t pcol = tbase + 256u * t + 128u;  // P_t(j): bf16 pairs over S_t's first 64 columns
-#pragma unroll
-                for (int l = 0; l < kT2Blocks; ++l) {
-                    // block l: [kH][16 keys][128 B]; the 64-column halves of V
-                    // are kBlock * 128 bytes apart
-                    const uint64_t bd = tc::sdesc_sw128(vbase + l * kH * kBlock * 128, kBlock * 128, 1024);
-                    tc::mma_ts_elect(tbase + 256u * t, pcol + 8u * l, bd, idO, j > 0 || l > 0);
+            bool pgood = true;
+            // block-table entries are read a stage ahead, before the wait for
+            // the slot, so their load latency is hidden
+            auto table_entry = [&](int jj) -> int {
+                const int x = jj * kT2Blocks + lane;
+                return (lane < kT2Blocks && x < it.nblk) ? __ldg(table + x) : -1;
+            };
+            int nblk_next = table_entry(0);
+            for (int j = 0; j < nst; ++j) {
+                const int sl = j % kT2KSlots, u = j / kT2KSlots;
+                const int x = j * kT2Blocks + lane;
+                const int blk = nblk_next;
+                if (j + 1 < nst) nblk_next = table_entry(j + 1);
+                if (!wait_all(k_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) {
+                    pgood = false;
+                    break;
                 }
-                tc::commit_elect(o_done0 + t * 8);
-            };
-            bool ok = wait_all(q_full, 0, p.wait_ns) && wait_all(k_full0, 0, p.wait_ns);
-            if (ok) {
-                tc::fence_after();
-                issue_s(0, 0);
-                if (two) issue_s(1, 0);
-                tc::commit_elect(k_empty0);  // K(0) read by both tiles
+                bool ok = false;
+                if (lane < kT2Blocks && x < it.nblk) {
+                    ok = blk >= 0 && blk < p.num_blocks;
+                    if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+                }
+                const uint32_t msk = __ballot_sync(0xffffffffu, ok);
+                const uint32_t fb = k_full0 + (j & 3) * 8;
+                // failure-detection test: stage 0's K is neither copied nor
+                // announced, so every wait on it runs out
+                const bool held = p.withhold != 0 && j == 0;
+                if (lane == 0 && !held) {
+                    sts32(mask0 + (j & 3) * 4, msk);
+                    mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
+                }
+                __syncwarp();
+                if (ok && !held) {
+                    const uint32_t kd = sbase + SM::kRingK + sl * SM::kKV + lane * kBlock * 128;
+                    const int row0 = (blk * p.Hkv + it.h) * kBlock;
+                    for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kT2Keys * 128, &tmk, fb, 0, hh, row0, policy);
+                }
+                if (j > 0 && !load_v(j - 1)) {
+                    pgood = false;
+                    break;
+                }
+                pblk = blk;
+                pok = ok;
             }
-            for (int j = 0; ok && j < nst; ++j) {
-                const uint32_t ph = (uint32_t)(j & 1);
-                ok = wait_all(p_full0, ph, p.wait_ns) &&
-                     wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns);
-                if (!ok) break;
-                tc::fence_after();
-                issue_o(0, j);
-                const bool more = j + 1 < nst;
-                if (more) {
-                    if (!(ok = wait_all(k_full0 + ((j + 1) & 3) * 8, (uint32_t)(((j + 1) >> 2) & 1), p.wait_ns)))
-                        break;
+            if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
+            bad |= !pgood;
+            if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
+        } else if (warp == kT2MmaWarp) {
+            // -------------------------------------------------- MMA issuer --
+            // The whole warp runs the loop; one elected lane issues each MMA
+            // and commit.
+            if (nst > 0) {
+                constexpr uint32_t idS = tc::idesc_bf16(kTcRows, kT2Keys, false);
+                constexpr uint32_t idO = tc::idesc_bf16(kTcRows, HD, true);
+                auto issue_s = [&](int t, int j) {
+                    const uint32_t kbase = sbase + SM::kRingK + (j % kT2KSlots) * SM::kKV;
+                    const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
+    #pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
+                        const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
+                        const uint64_t bd = tc::sdesc_sw128(kbase + (kk >> 2) * kT2Keys * 128 + off, 16, 1024);
+                        tc::mma_ss_elect(tbase + 256u * t + 128u, a, bd, idS, kk > 0);
+                    }
+                    tc::commit_elect(s_full0 + t * 8);
+                };
+                auto issue_o = [&](int t, int j) {
+                    const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
+                    const uint32_t pcol = tbase + 256u * t + 128u;  // P_t(j): bf16 pairs over S_t's first 64 columns
+    #pragma unroll
+                    for (int l = 0; l < kT2Blocks; ++l) {
+                        // block l: [kH][16 keys][128 B]; the 64-column halves of V
+                        // are kBlock * 128 bytes apart
+                        const uint64_t bd = tc::sdesc_sw128(vbase + l * kH * kBlock * 128, kBlock * 128, 1024);
+                        tc::mma_ts_elect(tbase + 256u * t, pcol + 8u * l, bd, idO, j > 0 || l > 0);
+                    }
+                    tc::commit_elect(o_done0 + t * 8);
+                };
+                bool ok = wait_all(q_full, 0, p.wait_ns) && wait_all(k_full0, 0, p.wait_ns);
+                if (ok) {
                     tc::fence_after();
-                    issue_s(0, j + 1);
+                    issue_s(0, 0);
+                    if (two) issue_s(1, 0);
+                    tc::commit_elect(k_empty0);  // K(0) read by both tiles
                 }
-                if (!two) {
-                    tc::commit_elect(v_empty0 + (j & 1) * 8);
-                    if (more) tc::commit_elect(k_empty0 + ((j + 1) % kT2KSlots) * 8);
-                    continue;
-                }
-                if (!(ok = wait_all(p_full0 + 8, ph, p.wait_ns))) break;
-                tc::fence_after();
-                issue_o(1, j);
-                tc::commit_elect(v_empty0 + (j & 1) * 8);  // V(j) read by both tiles
-                if (more) {
-                    issue_s(1, j + 1);
-                    tc::commit_elect(k_empty0 + ((j + 1) % kT2KSlots) * 8);
-                }
-            }
-            if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
-            // every MMA issued has finished before tensor memory is released
-            tc::commit_elect(fin);
-            (void)wait_all(fin, 0, drain_limit(p.wait_ns));
-        }
-        __syncwarp();
-    } else if (two || ((warp >> 2) & 1) == 0) {
-        // ---------------------------------------------------- softmax ----
-        // Eight warps per tile. Warp w reads tensor-memory lanes lb ... lb + 15
-        // (lb = 32 (w mod 4) + 16 (w / 8)) with the 16-lane shapes: lane i
-        // holds rows a = lb + i/4 and b = a + 8, keys 8k + 2 (i mod 4) and the
-        // next one of each 8-key group k, so a quad of lanes shares two rows'
-        // scores (32 keys each per lane) and reduces them with shuffles.
-        const int t = (warp >> 2) & 1;  // tile
-        const int c4 = lane & 3;
-        const int lb = (warp & 3) * 32 + (warp >> 3) * 16;
-        const int rla = lb + (lane >> 2), rlb = rla + 8;  // rows of the tile
-        const int rra = it.rho0 + t * tr + rla, rrb = it.rho0 + t * tr + rlb;
-        const bool va = rla < tr && rra < it.nrows, vb = rlb < tr && rrb < it.nrows;
-        const int toka = rra / p.G, tokb = rrb / p.G;
-        const int posa = va && !PREFIX ? it.first + toka : it.p_hi, posb = vb && !PREFIX ? it.first + tokb : it.p_hi;
-        const int mposa = posa < 0 ? 0 : posa, mposb = posb < 0 ? 0 : posb;
-        const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
-        const uint32_t ts = tl + 128u;                                // S_t / P_t
-        const int nb_ctx = (it.n + kBlock - 1) / kBlock;
-        const int tail = it.n - (nb_ctx - 1) * kBlock;
-        const bool fold = p.sl2 > 0.f;
-        float mra_run = -INFINITY, mrb_run = -INFINITY, lra = 0.f, lrb = 0.f;  // per lane: its 32 keys of the row
-        bool ok = true;
-        for (int j = 0; j < nst; ++j) {
-            ok = wait_all(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns) &&
-                 wait_all(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns);
-            if (!ok) break;
-            tc::fence_after();
-            uint32_t x[2 * kT2Keys / 4];  // x[4k + e]: e = 0, 1 row a; e = 2, 3 row b
-            tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-            tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-            tc::wait_ld();
-            const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
-            const int kbase = j * kT2Keys;
-            const bool nomask = __all_sync(0xffffffffu, present == (1u << kT2Blocks) - 1u &&
-                                                            kbase + kT2Keys - 1 <= min(mposa, mposb));
-            float alpha_a = 1.f, alpha_b = 1.f, psa, psb;
-            bool need = false;
-            float ma[4], mb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ma[i] = mb[i] = -INFINITY;
-            if (fold && nomask) {
-#pragma unroll
-                for (int k = 0; k < kT2Keys / 8; ++k) {
-                    ma[k & 3] = tc::max3(ma[k & 3], __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
-                    mb[k & 3] = tc::max3(mb[k & 3], __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kT2Keys / 8; ++k) {
-                    const bool blk = (present >> (k >> 1)) & 1u;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = kbase + 8 * k + 2 * c4 + (e & 1);
-                        const bool keep = blk && key <= (e < 2 ? mposa : mposb);
-                        const float v = keep ? (fold ? __uint_as_float(x[4 * k + e])
-                                                     : __uint_as_float(x[4 * k + e]) * p.sl2)
-                                             : -INFINITY;
-                        x[4 * k + e] = __float_as_uint(v);
-                        if (e < 2)
-                            ma[k & 3] = fmaxf(ma[k & 3], v);
-                        else
-                            mb[k & 3] = fmaxf(mb[k & 3], v);
+                for (int j = 0; ok && j < nst; ++j) {
+                    const uint32_t ph = (uint32_t)(j & 1);
+                    ok = wait_all(p_full0, ph, p.wait_ns) &&
+                         wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns);
+                    if (!ok) break;
+                    tc::fence_after();
+                    issue_o(0, j);
+                    const bool more = j + 1 < nst;
+                    if (more) {
+                        if (!(ok = wait_all(k_full0 + ((j + 1) & 3) * 8, (uint32_t)(((j + 1) >> 2) & 1), p.wait_ns)))
+                            break;
+                        tc::fence_after();
+                        issue_s(0, j + 1);
+                    }
+                    if (!two) {
+                        tc::commit_elect(v_empty0 + (j & 1) * 8);
+                        if (more) tc::commit_elect(k_empty0 + ((j + 1) % kT2KSlots) * 8);
+                        continue;
+                    }
+                    if (!(ok = wait_all(p_full0 + 8, ph, p.wait_ns))) break;
+                    tc::fence_after();
+                    issue_o(1, j);
+                    tc::commit_elect(v_empty0 + (j & 1) * 8);  // V(j) read by both tiles
+                    if (more) {
+                        issue_s(1, j + 1);
+                        tc::commit_elect(k_empty0 + ((j + 1) % kT2KSlots) * 8);
                     }
                 }
+                bad |= !ok;
+                if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
+                // every MMA issued has finished before tensor memory is released
+                tc::commit_elect(fin);
+                (void)wait_all(fin, 0, drain_limit(p.wait_ns));
             }
-            float mxa = fmaxf(fmaxf(ma[0], ma[1]), fmaxf(ma[2], ma[3]));
-            float mxb = fmaxf(fmaxf(mb[0], mb[1]), fmaxf(mb[2], mb[3]));
-            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
-            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
-            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-            if (fold) {
-                mxa *= p.sl2;
-                mxb *= p.sl2;
-            }
-            // lazy rescaling, per row: the reference max moves only when the
-            // new max exceeds it by more than 2^8; O and l are rescaled
-            // together (the four lanes of a quad take the same decision)
-            if (mra_run == -INFINITY) {
-                mra_run = mxa;
-            } else if (mxa > mra_run + 8.f) {
-                alpha_a = exp2f(mra_run - mxa);
-                mra_run = mxa;
-                need = true;
-            }
-            if (mrb_run == -INFINITY) {
-                mrb_run = mxb;
-            } else if (mxb > mrb_run + 8.f) {
-                alpha_b = exp2f(mrb_run - mxb);
-                mrb_run = mxb;
-                need = true;
-            }
-            const float una = mra_run == -INFINITY ? 0.f : mra_run;
-            const float unb = mrb_run == -INFINITY ? 0.f : mrb_run;
-            if (fold) {
-                const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
-                const uint64_t nua = tc::f2(-una, -una), nub = tc::f2(-unb, -unb);
-                uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
-#pragma unroll
-                for (int k = 0; k < kT2Keys / 8; ++k) {
-                    const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
-                                                 sc2, nua);
-                    const uint64_t b2 = tc::fma2(
-                        tc::f2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), sc2, nub);
-                    const float ea0 = ex2(tc::f2_lo(a2)), ea1 = ex2(tc::f2_hi(a2));
-                    const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
-                    acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
-                    accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
-                    // P words (column 4k + i mod 4 of rows a and b) over the
-                    // consumed scores
-                    x[2 * k] = pack_bf16x2(ea0, ea1);
-                    x[2 * k + 1] = pack_bf16x2(eb0, eb1);
-                }
-                const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
-                psa = tc::f2_lo(sa) + tc::f2_hi(sa);
-                psb = tc::f2_lo(sb) + tc::f2_hi(sb);
-            } else {
-                float pa[2] = {0.f, 0.f}, pb[2] = {0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < kT2Keys / 8; ++k) {
-                    const float ea0 = ex2(__uint_as_float(x[4 * k]) - una);
-                    const float ea1 = ex2(__uint_as_float(x[4 * k + 1]) - una);
-                    const float eb0 = ex2(__uint_as_float(x[4 * k + 2]) - unb);
-                    const float eb1 = ex2(__uint_as_float(x[4 * k + 3]) - unb);
-                    pa[k & 1] += ea0 + ea1;
-                    pb[k & 1] += eb0 + eb1;
-                    x[2 * k] = pack_bf16x2(ea0, ea1);
-                    x[2 * k + 1] = pack_bf16x2(eb0, eb1);
-                }
-                psa = pa[0] + pa[1];
-                psb = pb[0] + pb[1];
-            }
-            lra = lra * alpha_a + psa;
-            lrb = lrb * alpha_b + psb;
-            if (__any_sync(0xffffffffu, need)) {
-                // O_t may be touched once its previous P . V has finished
-                if (!(ok = wait_all(o_done0 + t * 8, (uint32_t)((j - 1) & 1), p.wait_ns))) break;
+            __syncwarp();
+        } else if (two || ((warp >> 2) & 1) == 0) {
+            // ---------------------------------------------------- softmax ----
+            // Eight warps per tile. Warp w reads tensor-memory lanes lb ... lb + 15
+            // (lb = 32 (w mod 4) + 16 (w / 8)) with the 16-lane shapes: lane i
+            // holds rows a = lb + i/4 and b = a + 8, keys 8k + 2 (i mod 4) and the
+            // next one of each 8-key group k, so a quad of lanes shares two rows'
+            // scores (32 keys each per lane) and reduces them with shuffles.
+            const int t = (warp >> 2) & 1;  // tile
+            const int c4 = lane & 3;
+            const int lb = (warp & 3) * 32 + (warp >> 3) * 16;
+            const int rla = lb + (lane >> 2), rlb = rla + 8;  // rows of the tile
+            const int rra = it.rho0 + t * tr + rla, rrb = it.rho0 + t * tr + rlb;
+            const bool va = rla < tr && rra < it.nrows, vb = rlb < tr && rrb < it.nrows;
+            const int toka = rra / p.G, tokb = rrb / p.G;
+            const int posa = va && !PREFIX ? it.first + toka : it.p_hi, posb = vb && !PREFIX ? it.first + tokb : it.p_hi;
+            const int mposa = posa < 0 ? 0 : posa, mposb = posb < 0 ? 0 : posb;
+            const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
+            const uint32_t ts = tl + 128u;                                // S_t / P_t
+            const int nb_ctx = (it.n + kBlock - 1) / kBlock;
+            const int tail = it.n - (nb_ctx - 1) * kBlock;
+            const bool fold = p.sl2 > 0.f;
+            float mra_run = -INFINITY, mrb_run = -INFINITY, lra = 0.f, lrb = 0.f;  // per lane: its 32 keys of the row
+            bool ok = true;
+            for (int j = 0; j < nst; ++j) {
+                ok = wait_all(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns) &&
+                     wait_all(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns);
+                if (!ok) break;
                 tc::fence_after();
-#pragma unroll 1
-                for (int ch = 0; ch < HD / 32; ++ch) {
-                    uint32_t y[16];
-                    tc::ld16x256_x4(tl + 32u * ch, y);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        y[i] = __float_as_uint(__uint_as_float(y[i]) * ((i & 2) ? alpha_b : alpha_a));
-                    tc::st16x256_x4(tl + 32u * ch, y);
-                }
-            }
-            // P_t(j): the A operand of O_t += P_t(j) . V(j)
-            tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
-            tc::wait_st();
-            if (warp == 1) {
-                // V rows of keys outside the context (missing blocks, the
-                // last block's tail) may hold any bits: zero them once the
-                // stage's V copies have landed, before tile 0's P . V (tile
-                // 1's is issued after it). A warp of tile 0 off the MMA
-                // warp's scheduler does it.
-                const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
-                const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
-                if (any) {
-                    if (!(ok = wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns))) break;
-                    const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
-                    for (int l = 0; l < kT2Blocks; ++l) {
-                        const int from = !((present >> l) & 1u) ? 0 : (l == last && tail < kBlock ? tail : kBlock);
-                        for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
-                            const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
-                            st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
+                uint32_t x[2 * kT2Keys / 4];  // x[4k + e]: e = 0, 1 row a; e = 2, 3 row b
+                tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                tc::wait_ld();
+                const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
+                const int kbase = j * kT2Keys;
+                const bool nomask = __all_sync(0xffffffffu, present == (1u << kT2Blocks) - 1u &&
+                                                                kbase + kT2Keys - 1 <= min(mposa, mposb));
+                float alpha_a = 1.f, alpha_b = 1.f, psa, psb;
+                bool need = false;
+                float ma[4], mb[4];
+    #pragma unroll
+                for (int i = 0; i < 4; ++i) ma[i] = mb[i] = -INFINITY;
+                if (fold && nomask) {
+    #pragma unroll
+                    for (int k = 0; k < kT2Keys / 8; ++k) {
+                        ma[k & 3] = tc::max3(ma[k & 3], __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+                        mb[k & 3] = tc::max3(mb[k & 3], __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+                    }
+                } else {
+    #pragma unroll
+                    for (int k = 0; k < kT2Keys / 8; ++k) {
+                        const bool blk = (present >> (k >> 1)) & 1u;
+    #pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = kbase + 8 * k + 2 * c4 + (e & 1);
+                            const bool keep = blk && key <= (e < 2 ? mposa : mposb);
+                            const float v = keep ? (fold ? __uint_as_float(x[4 * k + e])
+                                                         : __uint_as_float(x[4 * k + e]) * p.sl2)
+                                                 : -INFINITY;
+                            x[4 * k + e] = __float_as_uint(v);
+                            if (e < 2)
+                                ma[k & 3] = fmaxf(ma[k & 3], v);
+                            else
+                                mb[k & 3] = fmaxf(mb[k & 3], v);
                         }
                     }
-                    fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
                 }
+                float mxa = fmaxf(fmaxf(ma[0], ma[1]), fmaxf(ma[2], ma[3]));
+                float mxb = fmaxf(fmaxf(mb[0], mb[1]), fmaxf(mb[2], mb[3]));
+                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+                if (fold) {
+                    mxa *= p.sl2;
+                    mxb *= p.sl2;
+                }
+                // lazy rescaling, per row: the reference max moves only when the
+                // new max exceeds it by more than 2^8; O and l are rescaled
+                // together (the four lanes of a quad take the same decision)
+                if (mra_run == -INFINITY) {
+                    mra_run = mxa;
+                } else if (mxa > mra_run + 8.f) {
+                    alpha_a = exp2f(mra_run - mxa);
+                    mra_run = mxa;
+                    need = true;
+                }
+                if (mrb_run == -INFINITY) {
+                    mrb_run = mxb;
+                } else if (mxb > mrb_run + 8.f) {
+                    alpha_b = exp2f(mrb_run - mxb);
+                    mrb_run = mxb;
+                    need = true;
+                }
+                const float una = mra_run == -INFINITY ? 0.f : mra_run;
+                const float unb = mrb_run == -INFINITY ? 0.f : mrb_run;
+                if (fold) {
+                    const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
+                    const uint64_t nua = tc::f2(-una, -una), nub = tc::f2(-unb, -unb);
+                    uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
+    #pragma unroll
+                    for (int k = 0; k < kT2Keys / 8; ++k) {
+                        const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
+                                                     sc2, nua);
+                        const uint64_t b2 = tc::fma2(
+                            tc::f2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), sc2, nub);
+                        const float ea0 = ex2(tc::f2_lo(a2)), ea1 = ex2(tc::f2_hi(a2));
+                        const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
+                        acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
+                        accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
+                        // P words (column 4k + i mod 4 of rows a and b) over the
+                        // consumed scores
+                        x[2 * k] = pack_bf16x2(ea0, ea1);
+                        x[2 * k + 1] = pack_bf16x2(eb0, eb1);
+                    }
+                    const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
+                    psa = tc::f2_lo(sa) + tc::f2_hi(sa);
+                    psb = tc::f2_lo(sb) + tc::f2_hi(sb);
+                } else {
+                    float pa[2] = {0.f, 0.f}, pb[2] = {0.f, 0.f};
+    #pragma unroll
+                    for (int k = 0; k < kT2Keys / 8; ++k) {
+                        const float ea0 = ex2(__uint_as_float(x[4 * k]) - una);
+                        const float ea1 = ex2(__uint_as_float(x[4 * k + 1]) - una);
+                        const float eb0 = ex2(__uint_as_float(x[4 * k + 2]) - unb);
+                        const float eb1 = ex2(__uint_as_float(x[4 * k + 3]) - unb);
+                        pa[k & 1] += ea0 + ea1;
+                        pb[k & 1] += eb0 + eb1;
+                        x[2 * k] = pack_bf16x2(ea0, ea1);
+                        x[2 * k + 1] = pack_bf16x2(eb0, eb1);
+                    }
+                    psa = pa[0] + pa[1];
+                    psb = pb[0] + pb[1];
+                }
+                lra = lra * alpha_a + psa;
+                lrb = lrb * alpha_b + psb;
+                if (__any_sync(0xffffffffu, need)) {
+                    // O_t may be touched once its previous P . V has finished
+                    if (!(ok = wait_all(o_done0 + t * 8, (uint32_t)((j - 1) & 1), p.wait_ns))) break;
+                    tc::fence_after();
+    #pragma unroll 1
+                    for (int ch = 0; ch < HD / 32; ++ch) {
+                        uint32_t y[16];
+                        tc::ld16x256_x4(tl + 32u * ch, y);
+                        tc::wait_ld();
+    #pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            y[i] = __float_as_uint(__uint_as_float(y[i]) * ((i & 2) ? alpha_b : alpha_a));
+                        tc::st16x256_x4(tl + 32u * ch, y);
+                    }
+                }
+                // P_t(j): the A operand of O_t += P_t(j) . V(j)
+                tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
+                tc::wait_st();
+                if (warp == 1) {
+                    // V rows of keys outside the context (missing blocks, the
+                    // last block's tail) may hold any bits: zero them once the
+                    // stage's V copies have landed, before tile 0's P . V (tile
+                    // 1's is issued after it). A warp of tile 0 off the MMA
+                    // warp's scheduler does it.
+                    const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
+                    const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
+                    if (any) {
+                        if (!(ok = wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns))) break;
+                        const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
+                        for (int l = 0; l < kT2Blocks; ++l) {
+                            const int from = !((present >> l) & 1u) ? 0 : (l == last && tail < kBlock ? tail : kBlock);
+                            for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
+                                const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
+                                st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
+                            }
+                        }
+                        fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
+                    }
+                }
+                tc::fence_before();
+                mbar_arrive(p_full0 + t * 8);
             }
-            tc::fence_before();
-            mbar_arrive(p_full0 + t * 8);
-        }
-        if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
-        if (ok && nst > 0) ok = wait_all(o_done0 + t * 8, (uint32_t)((nst - 1) & 1), p.wait_ns);
-        tc::fence_after();
-        lra += __shfl_xor_sync(0xffffffffu, lra, 1);
-        lrb += __shfl_xor_sync(0xffffffffu, lrb, 1);
-        lra += __shfl_xor_sync(0xffffffffu, lra, 2);
-        lrb += __shfl_xor_sync(0xffffffffu, lrb, 2);
-        const float inva = lra > 0.f ? 1.f / lra : 0.f, invb = lrb > 0.f ? 1.f / lrb : 0.f;
-        if constexpr (PREFIX) {
-            const long long row = (long long)slot * (2 * tr) + t * tr + rla;  // row b: 8 further
-            float* pa = p.w.part + row * HD + 2 * c4;
-#pragma unroll 1
+            bad |= !ok;
+            if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
+            if (ok && nst > 0) ok = wait_all(o_done0 + t * 8, (uint32_t)((nst - 1) & 1), p.wait_ns);
+            bad |= !ok;
+            tc::fence_after();
+            lra += __shfl_xor_sync(0xffffffffu, lra, 1);
+            lrb += __shfl_xor_sync(0xffffffffu, lrb, 1);
+            lra += __shfl_xor_sync(0xffffffffu, lra, 2);
+            lrb += __shfl_xor_sync(0xffffffffu, lrb, 2);
+            const float inva = lra > 0.f ? 1.f / lra : 0.f, invb = lrb > 0.f ? 1.f / lrb : 0.f;
+            if constexpr (PREFIX) {
+                const long long row = (long long)slot * (2 * tr) + t * tr + rla;  // row b: 8 further
+                float* pa = p.w.part + row * HD + 2 * c4;
+    #pragma unroll 1
+                for (int ch = 0; ch < HD / 32; ++ch) {
+                    uint32_t y[16];
+                    if (!ok) break;
+                    tc::ld16x256_x4(tl + 32u * ch, y);
+                    tc::wait_ld();
+    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float* at = pa + 32 * ch + 8 * k;
+                        if (va)
+                            *reinterpret_cast<float2*>(at) =
+                                make_float2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva);
+                        if (vb)
+                            *reinterpret_cast<float2*>(at + 8 * HD) =
+                                make_float2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb);
+                    }
+                }
+                if (c4 == 0 && ok) {
+                    if (va) p.w.part_lse[row] = lra > 0.f ? mra_run + log2f(lra) : -INFINITY;
+                    if (vb) p.w.part_lse[row + 8] = lrb > 0.f ? mrb_run + log2f(lrb) : -INFINITY;
+                }
+            } else {
+            const uint32_t keepa = posa >= 0 ? 0xFFFFFFFFu : 0u, keepb = posb >= 0 ? 0xFFFFFFFFu : 0u;  // rows before position 0 are +0
+            uint16_t* orowa = p.out + ((long long)(it.q0 + toka) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
+            uint16_t* orowb = p.out + ((long long)(it.q0 + tokb) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
+    #pragma unroll 1
             for (int ch = 0; ch < HD / 32; ++ch) {
                 uint32_t y[16];
-                if (!ok) break;
-                tc::ld16x256_x4(tl + 32u * ch, y);
-                tc::wait_ld();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float* at = pa + 32 * ch + 8 * k;
-                    if (va)
-                        *reinterpret_cast<float2*>(at) =
-                            make_float2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva);
-                    if (vb)
-                        *reinterpret_cast<float2*>(at + 8 * HD) =
-                            make_float2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb);
+                if (nst > 0 && ok) {
+                    tc::ld16x256_x4(tl + 32u * ch, y);
+                    tc::wait_ld();
+                } else {
+    #pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = 0u;
+                }
+                if (ok) {
+    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int col = 32 * ch + 8 * k + 2 * c4;
+                        if (va)
+                            *reinterpret_cast<uint32_t*>(orowa + col) =
+                                pack_bf16x2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva) & keepa;
+                        if (vb)
+                            *reinterpret_cast<uint32_t*>(orowb + col) =
+                                pack_bf16x2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb) &
+                                keepb;
+                    }
                 }
             }
-            if (c4 == 0 && ok) {
-                if (va) p.w.part_lse[row] = lra > 0.f ? mra_run + log2f(lra) : -INFINITY;
-                if (vb) p.w.part_lse[row + 8] = lrb > 0.f ? mrb_run + log2f(lrb) : -INFINITY;
-            }
-        } else {
-        const uint32_t keepa = posa >= 0 ? 0xFFFFFFFFu : 0u, keepb = posb >= 0 ? 0xFFFFFFFFu : 0u;  // rows before position 0 are +0
-        uint16_t* orowa = p.out + ((long long)(it.q0 + toka) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
-        uint16_t* orowb = p.out + ((long long)(it.q0 + tokb) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
-#pragma unroll 1
-        for (int ch = 0; ch < HD / 32; ++ch) {
-            uint32_t y[16];
-            if (nst > 0 && ok) {
-                tc::ld16x256_x4(tl + 32u * ch, y);
-                tc::wait_ld();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = 0u;
-            }
-            if (ok) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int col = 32 * ch + 8 * k + 2 * c4;
-                    if (va)
-                        *reinterpret_cast<uint32_t*>(orowa + col) =
-                            pack_bf16x2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva) & keepa;
-                    if (vb)
-                        *reinterpret_cast<uint32_t*>(orowb + col) =
-                            pack_bf16x2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb) &
-                            keepb;
-                }
             }
         }
-        }
+        // the next item starts its barriers afresh; after a wait that ran out
+        // copies may still be under way, and nothing more is started
+        tc::fence_before();
+        if (!PREFIX || __syncthreads_or(bad)) break;
     }
     tc::fence_before();
     __syncthreads();
@@ -1534,10 +1555,11 @@ mi_status prefix_partials(const mi_dims* dims, int32_t max_prefix_blocks, const 
     if (!make_tmap_q_group(&tq, q, D.B, D.Hq, HD, G, (kTcRows / G) * G) ||
         !make_tmap_kv_halves(&tk, k_cache, rows, HD) || !make_tmap_kv_blocks(&tv, v_cache, rows, HD))
         return MI_ERR_CUDA;
+    const int grid = (int)(slots < work.sms ? slots : work.sms);
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e =
-        HD == 64 ? launch_pdl(prefill_tc2_kernel<64, true>, (int)slots, kT2Threads, Tc2Smem<64>::kTotal, st, tq, tk, tv, p)
-                 : launch_pdl(prefill_tc2_kernel<128, true>, (int)slots, kT2Threads, Tc2Smem<128>::kTotal, st, tq, tk,
+        HD == 64 ? launch_pdl(prefill_tc2_kernel<64, true>, grid, kT2Threads, Tc2Smem<64>::kTotal, st, tq, tk, tv, p)
+                 : launch_pdl(prefill_tc2_kernel<128, true>, grid, kT2Threads, Tc2Smem<128>::kTotal, st, tq, tk,
                               tv, p);
     return e == cudaSuccess ? MI_OK : MI_ERR_CUDA;
 }

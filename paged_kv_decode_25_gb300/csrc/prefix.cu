@@ -24,13 +24,13 @@ namespace {
 
 // The workspace after the decode attention's own: the rows' entries, the
 // slots' log-sum-exps and outputs.
-struct PrefixPlan {
+struct PrefixSpace {
     size_t rows, lse, part, total;
     long long slots;
     int slot_rows, sms;
 };
 
-bool prefix_plan(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks, PrefixPlan* s) {
+bool prefix_space(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks, PrefixSpace* s) {
     if (check_paged_dims(dims) != MI_OK || num_prefixes < 0 || num_prefixes > 65535 || max_prefix_blocks < 1 ||
         (long long)max_prefix_blocks * kBlock > 0x7FFFFFFFLL)
         return false;
@@ -55,8 +55,8 @@ bool prefix_plan(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_b
 
 extern "C" size_t mi_paged_prefix_workspace_bytes(const mi_dims* dims, int32_t num_prefixes,
                                                   int32_t max_prefix_blocks) {
-    mi::PrefixPlan s;
-    return mi::prefix_plan(dims, num_prefixes, max_prefix_blocks, &s) ? s.total : 0;
+    mi::PrefixSpace s;
+    return mi::prefix_space(dims, num_prefixes, max_prefix_blocks, &s) ? s.total : 0;
 }
 
 extern "C" mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32_t num_prefixes,
@@ -80,8 +80,8 @@ extern "C" mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32
     if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
         !aligned_to(workspace, 16))
         return MI_ERR_INVALID_ARG;
-    PrefixPlan s;
-    if (!prefix_plan(dims, num_prefixes, max_prefix_blocks, &s)) return MI_ERR_CUDA;
+    PrefixSpace s;
+    if (!prefix_space(dims, num_prefixes, max_prefix_blocks, &s)) return MI_ERR_CUDA;
     if (workspace_bytes < s.total) return MI_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PrefixWork w;

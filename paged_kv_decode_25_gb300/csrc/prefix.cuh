@@ -1,6 +1,6 @@
-// The work items of attention over shared prefixes: which (group, tile of
-// requests, split of the prefix, KV head) a block computes, found by every
-// block itself from the groups and lengths on the device.
+// The work items of attention over shared prefixes, (group, tile of requests,
+// split of the prefix, KV head), found by every block itself from the groups
+// and lengths on the device.
 #pragma once
 
 #include "batch.cuh"
@@ -25,36 +25,43 @@ struct PrefixItem {
 };
 
 // Slots for B requests in P groups, `per` requests a tile: the items of
-// prefix_items, whose splits are at least total / (2 sms) blocks long, are at
+// prefix_plan, whose splits are at least total / (2 sms) blocks long, are at
 // most 2 sms and one more for every (tile, head).
 inline long long prefix_slots(int B, int Hkv, int P, int per, int sms) {
     return 2LL * sms + (long long)Hkv * ((B + per - 1) / per + P);
 }
 
-// Plans the call (in every block, with all its threads), writes the requests'
-// rows, and returns true with this block's item, false when it has none.
-__device__ inline bool prefix_item(const PrefixWork& w, int Hkv, int G, int mbps, int per, int32_t* dev_err,
-                                   long long* sums, PrefixItem& it) {
+__device__ __forceinline__ int prefix_tokens(const PrefixWork& w, int mbps, int g) {
+    return min(max(__ldg(w.lens + g), 0), mbps * kBlock);
+}
+// Items of group g for splits of `step` blocks.
+__device__ __forceinline__ long long prefix_items(const PrefixWork& w, int Hkv, int mbps, int per, long long step, int g) {
+    const int tiles = (__ldg(w.starts + g + 1) - __ldg(w.starts + g) + per - 1) / per;
+    return (long long)Hkv * tiles * (((prefix_tokens(w, mbps, g) + kBlock - 1) / kBlock + step - 1) / step);
+}
+
+// Plans the call in every block, with all its threads: the blocks of a split
+// in `step`, the items laid end to end in `sums`, their number returned.
+// Writes the requests' rows.
+__device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int mbps, int per, int32_t* dev_err,
+                                        long long* sums, long long& step) {
     const int tid = threadIdx.x, nt = blockDim.x;
     const int gtid = blockIdx.x * nt + tid, nthreads = gridDim.x * nt;
     if (!starts_ascend(w.starts, w.P, w.B)) {
         // no request's prefix is known
         if (gtid == 0) raise_err(dev_err, MI_DEVERR_BAD_QUERY);
         for (int b = gtid; b < w.B; b += nthreads) w.rows[b] = make_int4(0, 0, 0, 0);
-        return false;
+        return 0;
     }
-    auto tokens = [&](int g) { return min(max(__ldg(w.lens + g), 0), mbps * kBlock); };
-    auto blocks = [&](int g) { return (tokens(g) + kBlock - 1) / kBlock; };
-    auto tiles = [&](int g) { return (__ldg(w.starts + g + 1) - __ldg(w.starts + g) + per - 1) / per; };
     // The split length: short enough that the grid has work, long enough that
     // one wave takes it all. Start from an even share; a share that leaves
     // more items than SMs (each group rounds up) grows by that ratio.
-    const long long cost = flat_scan(w.P, [&](int g) { return (long long)Hkv * tiles(g) * blocks(g); }, sums);
-    __syncthreads();
-    long long step = cost;
-    auto items = [&](int g) { return (long long)Hkv * tiles(g) * ((blocks(g) + step - 1) / step); };
     auto rounded = [](long long x) { return max((x + kSplitStep - 1) / kSplitStep, 1ll) * kSplitStep; };
-    step = rounded(cost);
+    auto items = [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); };
+    step = 1;
+    const long long cost = flat_scan(w.P, items, sums);  // blocks times tiles and heads
+    __syncthreads();
+    step = 1ll << 40;
     const long long units = flat_scan(w.P, items, sums);
     const long long target = units < w.sms ? w.sms : 2LL * w.sms;
     step = rounded((cost + target - 1) / target);
@@ -78,7 +85,7 @@ __device__ inline bool prefix_item(const PrefixWork& w, int Hkv, int G, int mbps
                 if (__ldg(w.starts + mid) <= b) lo = mid;
                 else hi = mid;
             }
-            const int splits = (int)((blocks(lo) + step - 1) / step);
+            const int splits = (int)(((prefix_tokens(w, mbps, lo) + kBlock - 1) / kBlock + step - 1) / step);
             if (splits > 0) {
                 const long long first = flat_before(w.P, items, sums, lo);
                 const int i = b - __ldg(w.starts + lo);
@@ -87,18 +94,25 @@ __device__ inline bool prefix_item(const PrefixWork& w, int Hkv, int G, int mbps
         }
         w.rows[b] = at;
     }
-    if (blockIdx.x >= total) return false;
+    return total;
+}
+
+// Item x of the plan.
+__device__ inline PrefixItem prefix_item(const PrefixWork& w, int Hkv, int mbps, int per, const long long* sums,
+                                         long long step, long long x) {
+    PrefixItem it;
     long long first;
-    it.g = flat_find(w.P, items, sums, blockIdx.x, first);
-    it.slot = blockIdx.x;
-    const int nblk = blocks(it.g), splits = (int)((nblk + step - 1) / step), o = (int)(blockIdx.x - first);
+    it.g = flat_find(w.P, [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); }, sums, x, first);
+    it.slot = (int)x;
+    const int n = prefix_tokens(w, mbps, it.g), o = (int)(x - first);
+    const int splits = (int)(((n + kBlock - 1) / kBlock + step - 1) / step);
     const int s = o / Hkv % splits, tile = o / Hkv / splits;
     it.h = o % Hkv;
     it.b0 = __ldg(w.starts + it.g) + tile * per;
     it.count = min(__ldg(w.starts + it.g + 1) - it.b0, per);
     it.blk0 = (int)(s * step);
-    it.n = (int)min((long long)tokens(it.g) - (long long)it.blk0 * kBlock, step * kBlock);
-    return true;
+    it.n = (int)min((long long)n - (long long)it.blk0 * kBlock, step * kBlock);
+    return it;
 }
 
 // The prefix part of a shared-prefix decode step: each slot's partial outputs

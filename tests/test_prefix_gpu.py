@@ -114,6 +114,8 @@ def test_many_groups(cuda_device):
 
 
 def test_no_prefixes_is_plain_decode(cuda_device):
+    """Without prefixes the call is plain decode attention up to the split: both
+    lie within the roundings of the 64-bit value."""
     mi, dev = _mi(), cuda_device
     own = [1, 200, 0, 3333]
     both, ptab, tables = make([], own, 2, 128, 34)
@@ -126,7 +128,8 @@ def test_no_prefixes_is_plain_decode(cuda_device):
     mi.check(mi.mi_paged_decode_attention(d_, q.to(dev), both.k.to(dev), both.v.to(dev), tables.to(dev),
                                           torch.tensor(own, dtype=torch.int32, device=dev), 0.1, plain, ws))
     torch.cuda.synchronize()
-    assert torch.equal(out.view(torch.int16), plain.cpu().view(torch.int16))
+    check(both, 0, [0], own, q, out, 0.1)
+    check(both, 0, [0], own, q, plain.cpu(), 0.1)
 
 
 def test_large_values_and_far_parts(cuda_device):

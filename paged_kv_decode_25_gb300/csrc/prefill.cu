@@ -925,20 +925,25 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    if (PREFIX && warp == kT2MmaWarp) {  // ahead of the plan
+        tc::alloc(sbase + SM::kTmem, kT2Cols);
+        tc::relinquish();
+    }
     pdl_wait();
     pdl_trigger();
 
     // a Q tile holds whole tokens: 128 / G of them, G rows each; the CTA's
     // two tiles are consecutive, tr rows apart
     const int tr = (kTcRows / p.G) * p.G;
-    long long items = 1, item = 0, step = 0;  // PREFIX: the plan's, and this block's
-    __shared__ long long sums[PREFIX ? flat_words(kT2Threads) : 1];
+    long long items = 1, item = 0;  // PREFIX: the plan's, and this block's
+    int step = 0;
+    __shared__ long long sums[PREFIX ? flat_words(kT2Threads) + 2 : 1];
+    __shared__ PrefixItem pick;
     if constexpr (PREFIX) {
-        items = prefix_plan(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, step);
+        items = prefix_plan(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, step, &pick);
         item = blockIdx.x;
-        if (item >= items) return;
     }
-    uint32_t tbase = 0;
+    uint32_t tbase = PREFIX ? lds_u32(sbase + SM::kTmem) : 0u;
     bool bad = false;  // a wait ran out
     for (bool first = true; item < items; item += gridDim.x, first = false) {
         Item it;
@@ -946,7 +951,11 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         int slot = 0;
         bool two = true;       // both Q tiles hold rows
         if constexpr (PREFIX) {
-            const PrefixItem x = prefix_item(p.w, p.Hkv, p.mbps, 2 * tr / p.G, sums, step, item);
+            if (!first) {
+                if (threadIdx.x == 0) pick = prefix_item(p.w, p.Hkv, p.mbps, 2 * tr / p.G, sums, step, item);
+                __syncthreads();
+            }
+            const PrefixItem x = pick;
             it.r = x.g;
             it.h = x.h;
             it.q0 = x.b0;
@@ -987,7 +996,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             mbar_init(fin, 1);
             fence_mbar_init();
         }
-        if (first && warp == kT2MmaWarp) {
+        if (!PREFIX && warp == kT2MmaWarp) {
             tc::alloc(sbase + SM::kTmem, kT2Cols);
             tc::relinquish();
         }

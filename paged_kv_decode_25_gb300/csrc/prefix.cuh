@@ -34,60 +34,148 @@ inline long long prefix_slots(int B, int Hkv, int P, int per, int sms) {
 __device__ __forceinline__ int prefix_tokens(const PrefixWork& w, int mbps, int g) {
     return min(max(__ldg(w.lens + g), 0), mbps * kBlock);
 }
+__device__ __forceinline__ int prefix_blocks(const PrefixWork& w, int mbps, int g) {
+    return (prefix_tokens(w, mbps, g) + kBlock - 1) / kBlock;
+}
+// Tiles of group g's requests, all KV heads counted.
+__device__ __forceinline__ int prefix_units(const PrefixWork& w, int Hkv, int per, int g) {
+    return Hkv * ((__ldg(w.starts + g + 1) - __ldg(w.starts + g) + per - 1) / per);
+}
+__device__ __forceinline__ int prefix_splits(int blocks, int step) { return (blocks + step - 1) / step; }
 // Items of group g for splits of `step` blocks.
-__device__ __forceinline__ long long prefix_items(const PrefixWork& w, int Hkv, int mbps, int per, long long step, int g) {
-    const int tiles = (__ldg(w.starts + g + 1) - __ldg(w.starts + g) + per - 1) / per;
-    return (long long)Hkv * tiles * (((prefix_tokens(w, mbps, g) + kBlock - 1) / kBlock + step - 1) / step);
+__device__ __forceinline__ long long prefix_items(const PrefixWork& w, int Hkv, int mbps, int per, int step, int g) {
+    return (long long)prefix_units(w, Hkv, per, g) * prefix_splits(prefix_blocks(w, mbps, g), step);
+}
+
+// Item x of the plan, whose items lie end to end in `sums`.
+__device__ inline PrefixItem prefix_item(const PrefixWork& w, int Hkv, int mbps, int per, const long long* sums,
+                                         int step, long long x) {
+    PrefixItem it;
+    long long first;
+    it.g = flat_find(w.P, [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); }, sums, x, first);
+    it.slot = (int)x;
+    const int n = prefix_tokens(w, mbps, it.g), o = (int)(x - first), splits = prefix_splits((n + kBlock - 1) / kBlock, step);
+    const int st = o / Hkv, tile = st / splits;
+    it.h = o - st * Hkv;
+    it.b0 = __ldg(w.starts + it.g) + tile * per;
+    it.count = min(__ldg(w.starts + it.g + 1) - it.b0, per);
+    it.blk0 = (st - tile * splits) * step;
+    it.n = (int)min((long long)n - (long long)it.blk0 * kBlock, (long long)step * kBlock);
+    return it;
+}
+
+// The split length: short enough that the grid has work, long enough that one
+// wave takes it all where the tiles alone do not fill it. An even share of
+// the blocks comes first; a share that leaves more items than SMs (each group
+// rounds up) grows by that ratio.
+__device__ __forceinline__ int prefix_share(long long blocks, long long items) {
+    const long long share = (blocks + items - 1) / items;
+    const long long up = (share + kSplitStep - 1) / kSplitStep * kSplitStep;
+    return (int)(up < kSplitStep ? kSplitStep : up > (1 << 27) ? 1 << 27 : up);  // a table has at most 2^27 blocks
 }
 
 // Plans the call in every block, with all its threads: the blocks of a split
-// in `step`, the items laid end to end in `sums`, their number returned.
-// Writes the requests' rows.
+// in `step`, the items laid end to end in `sums` (two words more than
+// flat_words), their number returned, this block's first one in *mine (shared).
+// Writes the requests' rows. Up to 32 groups one warp does it from one load of
+// each group's numbers: the block's other way, four scans of the list, took
+// 3 us of a call.
 __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int mbps, int per, int32_t* dev_err,
-                                        long long* sums, long long& step) {
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const int gtid = blockIdx.x * nt + tid, nthreads = gridDim.x * nt;
-    if (!starts_ascend(w.starts, w.P, w.B)) {
-        // no request's prefix is known
-        if (gtid == 0) raise_err(dev_err, MI_DEVERR_BAD_QUERY);
-        for (int b = gtid; b < w.B; b += nthreads) w.rows[b] = make_int4(0, 0, 0, 0);
-        return 0;
-    }
-    // The split length: short enough that the grid has work, long enough that
-    // one wave takes it all. Start from an even share; a share that leaves
-    // more items than SMs (each group rounds up) grows by that ratio.
-    auto rounded = [](long long x) { return max((x + kSplitStep - 1) / kSplitStep, 1ll) * kSplitStep; };
-    auto items = [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); };
-    step = 1;
-    const long long cost = flat_scan(w.P, items, sums);  // blocks times tiles and heads
-    __syncthreads();
-    step = 1ll << 40;
-    const long long units = flat_scan(w.P, items, sums);
-    const long long target = units < w.sms ? w.sms : 2LL * w.sms;
-    step = rounded((cost + target - 1) / target);
-    __syncthreads();
-    long long total = flat_scan(w.P, items, sums);
-    for (int round = 0; round < 3 && units < w.sms && total > w.sms; ++round) {
-        step = rounded((step * total + w.sms - 1) / w.sms);
+                                        long long* sums, int& step, PrefixItem* mine) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+    auto no_prefix = [&]() {  // no request's prefix is known
+        if (blockIdx.x == 0 && tid == 0) raise_err(dev_err, MI_DEVERR_BAD_QUERY);
+        for (int b = blockIdx.x * nt + tid; b < w.B; b += gridDim.x * nt) w.rows[b] = make_int4(0, 0, 0, 0);
+    };
+    long long total = 0;
+    if (w.P <= 32) {
+        if (tid < 32) {
+            const bool in = lane < w.P;
+            const int s0 = __ldg(w.starts + min(lane, w.P)), len = in ? __ldg(w.lens + lane) : 0;
+            int s1 = __shfl_down_sync(0xffffffffu, s0, 1);
+            if (lane == 31) s1 = __ldg(w.starts + w.P);  // (read by lane 31 alone when there are 32 groups)
+            const bool bad = s0 < 0 || s0 > w.B || (in && (s1 < s0 || s1 > w.B));
+            if (__any_sync(0xffffffffu, bad)) {
+                step = 0;
+            } else {
+                const int units = in ? Hkv * ((s1 - s0 + per - 1) / per) : 0;
+                const int blocks = (min(max(len, 0), mbps * kBlock) + kBlock - 1) / kBlock;
+                if (blockIdx.x == 0 && in && len > mbps * kBlock) raise_err(dev_err, MI_DEVERR_BAD_CONTEXT);
+                auto sum = [](long long v) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    return v;
+                };
+                const long long cost = sum((long long)units * blocks), busy = sum(blocks > 0 ? units : 0);
+                step = prefix_share(cost, busy < w.sms ? w.sms : 2LL * w.sms);
+                long long items = (long long)units * prefix_splits(blocks, step);
+                total = sum(items);
+                for (int round = 0; round < 3 && busy < w.sms && total > w.sms; ++round) {
+                    step = prefix_share((long long)step * total, w.sms);
+                    items = (long long)units * prefix_splits(blocks, step);
+                    total = sum(items);
+                }
+                long long x = items;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                sums[lane] = x - items;
+                if (lane == 31) sums[32] = x;
+                __syncwarp();
+                if (lane == 0 && blockIdx.x < total) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
+            }
+            if (lane == 0) {
+                sums[33] = step;
+                sums[34] = total;
+            }
+        }
+        __syncthreads();
+        step = (int)sums[33];
+        total = sums[34];
+        if (step == 0) {
+            no_prefix();
+            return 0;
+        }
+    } else {
+        if (!starts_ascend(w.starts, w.P, w.B)) {
+            no_prefix();
+            return 0;
+        }
+        const long long cost = flat_scan(
+            w.P, [&](int g) { return (long long)prefix_units(w, Hkv, per, g) * prefix_blocks(w, mbps, g); }, sums);
+        __syncthreads();
+        auto items = [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); };
+        step = 1 << 27;
+        const long long busy = flat_scan(w.P, items, sums);
+        step = prefix_share(cost, busy < w.sms ? w.sms : 2LL * w.sms);
         __syncthreads();
         total = flat_scan(w.P, items, sums);
+        for (int round = 0; round < 3 && busy < w.sms && total > w.sms; ++round) {
+            step = prefix_share((long long)step * total, w.sms);
+            __syncthreads();
+            total = flat_scan(w.P, items, sums);
+        }
+        for (int g = blockIdx.x * nt + tid; g < w.P; g += gridDim.x * nt)
+            if (__ldg(w.lens + g) > mbps * kBlock) raise_err(dev_err, MI_DEVERR_BAD_CONTEXT);
+        if (tid == 0 && blockIdx.x < total) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
+        __syncthreads();
     }
-    for (int g = gtid; g < w.P; g += nthreads)
-        if (__ldg(w.lens + g) > mbps * kBlock) raise_err(dev_err, MI_DEVERR_BAD_CONTEXT);
     // each request's slots; those outside every group have none
-    const int b_first = __ldg(w.starts), b_last = __ldg(w.starts + w.P);
-    for (int b = gtid; b < w.B; b += nthreads) {
+    for (int b = blockIdx.x + gridDim.x * tid; b < w.B; b += gridDim.x * nt) {
         int4 at = make_int4(0, 0, 0, 0);
-        if (b >= b_first && b < b_last) {
+        if (b >= __ldg(w.starts) && b < __ldg(w.starts + w.P)) {
             int lo = 0, hi = w.P;  // starts[lo] <= b < starts[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (__ldg(w.starts + mid) <= b) lo = mid;
                 else hi = mid;
             }
-            const int splits = (int)(((prefix_tokens(w, mbps, lo) + kBlock - 1) / kBlock + step - 1) / step);
+            const int splits = prefix_splits(prefix_blocks(w, mbps, lo), step);
             if (splits > 0) {
-                const long long first = flat_before(w.P, items, sums, lo);
+                const long long first =
+                    flat_before(w.P, [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); }, sums, lo);
                 const int i = b - __ldg(w.starts + lo);
                 at = make_int4((int)first + (i / per) * splits * Hkv, splits, (i % per) * G, 0);
             }
@@ -95,24 +183,6 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
         w.rows[b] = at;
     }
     return total;
-}
-
-// Item x of the plan.
-__device__ inline PrefixItem prefix_item(const PrefixWork& w, int Hkv, int mbps, int per, const long long* sums,
-                                         long long step, long long x) {
-    PrefixItem it;
-    long long first;
-    it.g = flat_find(w.P, [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); }, sums, x, first);
-    it.slot = (int)x;
-    const int n = prefix_tokens(w, mbps, it.g), o = (int)(x - first);
-    const int splits = (int)(((n + kBlock - 1) / kBlock + step - 1) / step);
-    const int s = o / Hkv % splits, tile = o / Hkv / splits;
-    it.h = o % Hkv;
-    it.b0 = __ldg(w.starts + it.g) + tile * per;
-    it.count = min(__ldg(w.starts + it.g + 1) - it.b0, per);
-    it.blk0 = (int)(s * step);
-    it.n = (int)min((long long)n - (long long)it.blk0 * kBlock, step * kBlock);
-    return it;
 }
 
 // The prefix part of a shared-prefix decode step: each slot's partial outputs

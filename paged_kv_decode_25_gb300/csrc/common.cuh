@@ -361,4 +361,25 @@ inline cudaError_t launch_pdl(void (*fn)(Args...), int grid, int block, int smem
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// The same with thread-block clusters of `cluster` blocks.
+template <typename... Args>
+inline cudaError_t launch_cluster(void (*fn)(Args...), int grid, int block, int smem, int cluster, cudaStream_t s,
+                                  Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 }  // namespace mi

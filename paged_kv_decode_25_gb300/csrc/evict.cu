@@ -10,7 +10,11 @@
 // Two launches:
 //   * evict_select_kernel finds the (k - r)-th largest score of every (b, h)
 //     by a radix select over an order-preserving 32-bit key, and writes the
-//     kept older tokens' indices in ascending order;
+//     kept older tokens' indices in ascending order. Where the (b, h) do not
+//     fill the GPU, a cluster of up to 8 blocks shares one: each holds a
+//     stretch of the tokens and adds up the others' digit counts through
+//     distributed shared memory (16 (b, h) of 57,000 tokens: one block each
+//     73 us);
 //   * evict_move_kernel copies the kept rows of K and V and their scores.
 // Both only move bytes: the floor is the scores once, the kept rows in and
 // out.
@@ -24,6 +28,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;                // digits of 11, 11 and 10 bits
+constexpr int kSelKeys = 24576;            // keys a block holds in shared memory (96 KB: two blocks an SM)
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 64;              // destination rows per work item
 
@@ -108,20 +113,47 @@ __device__ __forceinline__ uint32_t block_sum_before(uint32_t v, uint32_t* wsum,
     return (wid ? wsum[wid - 1] : 0u) + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+// A word of the block `rank` of the cluster, at this block's shared address.
+__device__ __forceinline__ uint32_t cluster_word(const uint32_t* mine, uint32_t rank) {
+    uint32_t addr, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One cluster of `ranks` blocks per (b, h); block `rank` of it takes the
+// stretch of quads (four tokens) [rank * share, (rank + 1) * share). Its keys
+// stay in shared memory (`held` of them; the rest is read again). Every block
+// of a cluster takes the same way through the kernel.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, int ranks, int held) {
+    extern __shared__ uint4 keys[];  // [held / 4]
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t wsum[32];
     __shared__ uint32_t found[2];
+    __shared__ uint32_t counts[2];
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, tid = threadIdx.x;
+    const int unit = blockIdx.x / ranks, rank = blockIdx.x % ranks;
+    const int b = unit / p.Hkv, h = unit % p.Hkv, tid = threadIdx.x;
     const Share s = share_of(p, b);
-    if (h == 0 && tid == 0) {
+    if (h == 0 && rank == 0 && tid == 0) {
         p.new_lens[b] = s.kept;
         if (__ldg(p.lens + b) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
     }
     if (s.heavy == 0) return;
-    const int quads = (s.old + 3) / 4;
+    const int all = (s.old + 3) / 4, share = (all + ranks - 1) / ranks;
+    const int q0 = min(all, rank * share), quads = min(all, q0 + share) - q0;
+    auto quad = [&](int i, bool first) -> uint4 {  // the keys of quad q0 + i; 0 past the older tokens
+        if (!first && 4 * i < held) return keys[i];
+        uint32_t k[4];
+        load_keys(p, b, h, q0 + i, k, first);
+        const uint4 v = make_uint4(k[0], k[1], k[2], k[3]);
+        if (first && 4 * i < held) keys[i] = v;
+        return v;
+    };
     uint32_t prefix = 0, need = (uint32_t)s.heavy;  // of the tokens whose key starts with `prefix`, take the top `need`
     int low = 32;                                   // key bits below the prefix
 #pragma unroll 1
@@ -130,18 +162,30 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         low -= bits;
         for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
         __syncthreads();
-        for (int t4 = tid; t4 < quads; t4 += kSelThreads) {
-            uint32_t key[4];
-            load_keys(p, b, h, t4, key, pass == 0);
+        for (int i = tid; i < quads; i += kSelThreads) {
+            const uint4 v = quad(i, pass == 0);
+            const uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (4 * t4 + e < s.old && (pass == 0 || (key[e] >> up) == prefix))
+                if (4 * (q0 + i) + e < s.old && (pass == 0 || (key[e] >> up) == prefix))
                     atomicAdd(&hist[(key[e] >> low) & ((1u << bits) - 1u)], 1u);
         }
-        __syncthreads();
+        if (ranks > 1) cluster_sync();
+        else __syncthreads();
         // thread i counts bins top - 2i and top - 2i - 1, from the largest down
         const int hi = (1 << bits) - 1 - 2 * tid;
-        const uint32_t c0 = hi >= 0 ? hist[hi] : 0u, c1 = hi >= 1 ? hist[hi - 1] : 0u;
+        uint32_t c0 = 0, c1 = 0;
+        if (hi >= 1) {
+            if (ranks == 1) {
+                c0 = hist[hi];
+                c1 = hist[hi - 1];
+            } else {
+                for (int r = 0; r < ranks; ++r) {
+                    c0 += cluster_word(hist + hi, r);
+                    c1 += cluster_word(hist + hi - 1, r);
+                }
+            }
+        }
         uint32_t total;
         const uint32_t before = block_sum_before(c0 + c1, wsum, total);
         if (before < need && need <= before + c0 + c1) {
@@ -149,24 +193,55 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             found[0] = (uint32_t)(first ? hi : hi - 1);
             found[1] = first ? before : before + c0;
         }
-        __syncthreads();
+        if (ranks > 1) cluster_sync();  // (nobody's counts are read any more)
+        else __syncthreads();
         prefix = (prefix << bits) | found[0];
         need -= found[1];
         __syncthreads();
     }
     // every token with a larger key, and the first `need` of those with the
     // key itself, in ascending order
-    int32_t* list = p.list + ((long long)b * p.Hkv + h) * p.mbps * kBlock;
-    uint32_t above = 0, equal = 0;  // seen so far
-    for (int base = 0; base < quads; base += kSelThreads) {
-        const int t4 = base + tid;
-        uint32_t key[4] = {0u, 0u, 0u, 0u};
+    uint32_t above = 0, equal = 0;  // in the stretches before this one, then seen so far
+    if (ranks > 1) {
         uint32_t gt = 0, eq = 0;
-        if (t4 < quads) {
-            load_keys(p, b, h, t4, key, false);
+        for (int i = tid; i < quads; i += kSelThreads) {
+            const uint4 v = quad(i, false);
+            const uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (4 * t4 + e >= s.old) continue;
+                if (4 * (q0 + i) + e >= s.old) continue;
+                gt += key[e] > prefix;
+                eq += key[e] == prefix;
+            }
+        }
+        uint32_t gt_all, eq_all;
+        block_sum_before(gt, wsum, gt_all);
+        block_sum_before(eq, wsum, eq_all);
+        if (tid == 0) {
+            counts[0] = gt_all;
+            counts[1] = eq_all;
+        }
+        cluster_sync();
+        for (int r = 0; r < rank; ++r) {
+            above += cluster_word(counts, r);
+            equal += cluster_word(counts + 1, r);
+        }
+        cluster_sync();  // no block leaves while another reads its shared memory
+    }
+    int32_t* list = p.list + ((long long)b * p.Hkv + h) * p.mbps * kBlock;
+    for (int base = 0; base < quads; base += kSelThreads) {
+        const int i = base + tid;
+        uint32_t key[4] = {0u, 0u, 0u, 0u};
+        uint32_t gt = 0, eq = 0;
+        if (i < quads) {
+            const uint4 v = quad(i, false);
+            key[0] = v.x;
+            key[1] = v.y;
+            key[2] = v.z;
+            key[3] = v.w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (4 * (q0 + i) + e >= s.old) continue;
                 gt += key[e] > prefix;
                 eq += key[e] == prefix;
             }
@@ -174,10 +249,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         uint32_t total;
         const uint32_t before = block_sum_before((gt << 16) | eq, wsum, total);
         uint32_t g = above + (before >> 16), q = equal + (before & 0xFFFFu);
-        if (t4 < quads) {
+        if (i < quads) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int t = 4 * t4 + e;
+                const int t = 4 * (q0 + i) + e;
                 if (t >= s.old) continue;
                 if (key[e] > prefix) {
                     list[g + min(q, need)] = t;
@@ -299,7 +374,7 @@ mi_status evict(const mi_dims* dims, void* k_cache, void* v_cache, float* scores
         return MI_ERR_INVALID_ARG;
     if (dst_tables != block_tables && overlaps(dst_tables, table_bytes, block_tables, table_bytes))
         return MI_ERR_INVALID_ARG;
-    if ((long long)D.B * D.Hkv > 0x7FFFFFFFLL) return MI_ERR_INVALID_ARG;
+    if ((long long)D.B * D.Hkv > 0x7FFFFFFFLL / 8) return MI_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms <= 0) return MI_ERR_CUDA;
     EvictParams p;
@@ -321,7 +396,18 @@ mi_status evict(const mi_dims* dims, void* k_cache, void* v_cache, float* scores
     p.in_place = dst_tables == block_tables ? 1 : 0;
     cudaStream_t st = (cudaStream_t)stream;
     const int units = D.B * D.Hkv;
-    if (launch_pdl(evict_select_kernel, units, kSelThreads, 0, st, p) != cudaSuccess) return MI_ERR_CUDA;
+    // blocks per (b, h): one where they fill the GPU, else up to 8 with at
+    // least 2,048 of the longest request's tokens each
+    const long long longest = (long long)D.max_blocks_per_seq * kBlock;
+    int ranks = 1;
+    while (ranks < 8 && 2LL * ranks * units <= 2LL * sms && longest / (2 * ranks) >= 2048) ranks *= 2;
+    const long long stretch = (longest / 4 + ranks - 1) / ranks * 4 + 4;
+    const int held = (int)(stretch < kSelKeys ? (stretch + 3) / 4 * 4 : kSelKeys);
+    static std::mutex mu;
+    static CUcontext done[256] = {};
+    if (!raise_smem(reinterpret_cast<const void*>(evict_select_kernel), kSelKeys * 4, done, mu)) return MI_ERR_CUDA;
+    if (launch_cluster(evict_select_kernel, units * ranks, kSelThreads, held * 4, ranks, st, p, ranks, held) != cudaSuccess)
+        return MI_ERR_CUDA;
     const int grid = p.in_place ? units : 8 * sms;
     cudaError_t e;
     switch (D.head_dim * elem / 16) {

@@ -27,18 +27,20 @@ struct ScoreParams {
     int B, Hq, Hkv, G, gp, num_blocks, mbps, by_block, fresh;
 };
 
+// GP: floats of a token's logits. A thread takes four consecutive tokens of a
+// block, so that all its loads (4 GP floats of logits, a table entry, four
+// scores) are wide and, but for the scores, independent.
+template <int GP>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(const ScoreParams p) {
-    __shared__ long long sums[flat_words(kScoreThreads)];
+    __shared__ long long sums[flat_words(kScoreThreads)], bsums[flat_words(kScoreThreads)];
     pdl_wait();
     pdl_trigger();
     auto tokens = [&](int b) { return min(max(__ldg(p.lens + b), 0), p.mbps * kBlock); };
-    // work items tile the flat (request, head, block) order, whose place of a
-    // block is also where its logits are: count in blocks, item = 64 blocks
-    // of one (request, head)
+    // work items are 64 blocks of one (request, head); the logits of the
+    // flat order lie in blocks of (request, head) laid end to end
     constexpr int kItemBlocks = kScoreTokens / kBlock;
     auto items = [&](int b) { return (long long)p.Hkv * ((tokens(b) + kScoreTokens - 1) / kScoreTokens); };
     auto blocks = [&](int b) { return (long long)p.Hkv * ((tokens(b) + kBlock - 1) / kBlock); };
-    __shared__ long long bsums[flat_words(kScoreThreads)];
     const long long total = flat_scan(p.B, items, sums);
     if (!p.by_block) flat_scan(p.B, blocks, bsums);
     for (long long x = blockIdx.x; x < total; x += gridDim.x) {
@@ -46,31 +48,41 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const ScoreParams 
         const int b = flat_find(p.B, items, sums, x, first);
         const int n = tokens(b), nblk = (n + kBlock - 1) / kBlock, per = (n + kScoreTokens - 1) / kScoreTokens;
         const int o = (int)(x - first), h = o / per, j0 = (o % per) * kItemBlocks;
-        long long e0 = 0;  // flat place of the (request, head)'s first block
-        if (!p.by_block) e0 = flat_before(p.B, blocks, bsums, b) + (long long)h * nblk;
-        float lse[8];
+        const long long e0 = p.by_block ? 0 : flat_before(p.B, blocks, bsums, b) + (long long)h * nblk;
+        const int j = j0 + threadIdx.x / 4, i0 = threadIdx.x % 4 * 4, t0 = j * kBlock + i0;
+        if (t0 >= n) continue;
+        const int blk = __ldg(p.tables + (long long)b * p.mbps + j);
+        const bool in = blk >= 0 && blk < p.num_blocks;  // (else reported by the attention)
+        if (!in && p.by_block) continue;
+        const long long e = p.by_block ? (long long)blk * p.Hkv + h : e0 + j;
+        const float* lg = p.logits + (e * kBlock + i0) * GP;
+        float l[4 * GP], lse[GP];
 #pragma unroll
-        for (int g = 0; g < 8; ++g)
-            lse[g] = g < p.G ? p.lse[(long long)b * p.Hq + (long long)h * p.G + g] : 0.f;
-#pragma unroll
-        for (int u = 0; u < kScoreTokens / kScoreThreads; ++u) {
-            const int i = u * kScoreThreads + threadIdx.x, j = j0 + i / kBlock, t = j * kBlock + i % kBlock;
-            if (t >= n) continue;
-            const int blk = __ldg(p.tables + (long long)b * p.mbps + j);
-            if (blk < 0 || blk >= p.num_blocks) continue;  // (reported by the attention)
-            const long long e = p.by_block ? (long long)blk * p.Hkv + h : e0 + j;
-            const float* lg = p.logits + (e * kBlock + i % kBlock) * p.gp;
-            float w = 0.f;
-#pragma unroll
-            for (int g = 0; g < 8; g += 2) {
-                if (g >= p.G) break;
-                const float2 xx = *reinterpret_cast<const float2*>(lg + g);
-                w += exp2f(xx.x - lse[g]);
-                if (g + 1 < p.G) w += exp2f(xx.y - lse[g + 1]);
-            }
-            float* at = p.scores + ((long long)blk * p.Hkv + h) * kBlock + i % kBlock;
-            *at = p.fresh || t == n - 1 ? w : *at + w;
+        for (int c = 0; c < GP; ++c) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(lg) + c);
+            l[4 * c] = v.x;
+            l[4 * c + 1] = v.y;
+            l[4 * c + 2] = v.z;
+            l[4 * c + 3] = v.w;
         }
+#pragma unroll
+        for (int g = 0; g < GP; ++g)
+            lse[g] = g < p.G ? __ldcg(p.lse + (long long)b * p.Hq + (long long)h * p.G + g) : INFINITY;
+        if (!in) continue;
+        float4* at = reinterpret_cast<float4*>(p.scores + ((long long)blk * p.Hkv + h) * kBlock + i0);
+        const bool whole = p.fresh && t0 + 4 <= n;
+        const float4 old = whole ? make_float4(0.f, 0.f, 0.f, 0.f) : *at;
+        float w[4], was[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float v = 0.f;
+#pragma unroll
+            for (int g = 0; g < GP; ++g)
+                if (g < p.G) v += exp2f(l[c * GP + g] - lse[g]);
+            const int t = t0 + c;
+            w[c] = t >= n ? was[c] : p.fresh || t == n - 1 ? v : was[c] + v;
+        }
+        *at = make_float4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -140,7 +152,9 @@ mi_status scored(const mi_dims* dims, const void* q, const void* k_cache, const 
     p.fresh = fresh != 0;
     const long long most = (long long)D.B * D.Hkv * (((long long)D.max_blocks_per_seq * kBlock + kScoreTokens - 1) / kScoreTokens);
     const int grid = (int)(most < 8LL * sms ? most : 8LL * sms);
-    return launch_pdl(score_kernel, grid, kScoreThreads, 0, (cudaStream_t)stream, p) == cudaSuccess ? MI_OK : MI_ERR_CUDA;
+    void (*const kernel[4])(ScoreParams) = {score_kernel<2>, score_kernel<4>, score_kernel<6>, score_kernel<8>};
+    return launch_pdl(kernel[s.gp / 2 - 1], grid, kScoreThreads, 0, (cudaStream_t)stream, p) == cudaSuccess ? MI_OK
+                                                                                                           : MI_ERR_CUDA;
 }
 
 }  // namespace

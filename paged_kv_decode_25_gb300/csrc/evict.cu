@@ -26,7 +26,6 @@
 namespace mi {
 namespace {
 
-constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;                // digits of 11, 11 and 10 bits
 constexpr int kSelKeys = 24576;            // keys a block holds in shared memory (96 KB: two blocks an SM)
 constexpr int kMoveThreads = 256;
@@ -115,20 +114,22 @@ __device__ __forceinline__ uint32_t block_sum_before(uint32_t v, uint32_t* wsum,
 
 // A word of the block `rank` of the cluster, at this block's shared address.
 __device__ __forceinline__ uint32_t cluster_word(const uint32_t* mine, uint32_t rank) {
-    uint32_t addr, v;
+    uint32_t addr, v;  // (volatile orders it among the cluster barriers and leaves the loads in flight together)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One cluster of `ranks` blocks per (b, h); block `rank` of it takes the
+// One cluster of RANKS blocks per (b, h); block `rank` of it takes the
 // stretch of quads (four tokens) [rank * share, (rank + 1) * share). Its keys
 // stay in shared memory (`held` of them; the rest is read again). Every block
 // of a cluster takes the same way through the kernel.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p, int ranks, int held) {
+template <int RANKS, int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p, int held) {
+    constexpr int kPer = kBins / THREADS;  // bins a thread counts
     extern __shared__ uint4 keys[];  // [held / 4]
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t wsum[32];
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     __shared__ uint32_t counts[2];
     pdl_wait();
     pdl_trigger();
-    const int unit = blockIdx.x / ranks, rank = blockIdx.x % ranks;
+    const int unit = blockIdx.x / RANKS, rank = blockIdx.x % RANKS;
     const int b = unit / p.Hkv, h = unit % p.Hkv, tid = threadIdx.x;
     const Share s = share_of(p, b);
     if (h == 0 && rank == 0 && tid == 0) {
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         if (__ldg(p.lens + b) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
     }
     if (s.heavy == 0) return;
-    const int all = (s.old + 3) / 4, share = (all + ranks - 1) / ranks;
+    const int all = (s.old + 3) / 4, share = (all + RANKS - 1) / RANKS;
     const int q0 = min(all, rank * share), quads = min(all, q0 + share) - q0;
     auto quad = [&](int i, bool first) -> uint4 {  // the keys of quad q0 + i; 0 past the older tokens
         if (!first && 4 * i < held) return keys[i];
@@ -160,9 +161,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     for (int pass = 0; pass < 3; ++pass) {
         const int bits = pass < 2 ? 11 : 10, up = low;
         low -= bits;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
+        for (int i = tid; i < kBins; i += THREADS) hist[i] = 0u;
         __syncthreads();
-        for (int i = tid; i < quads; i += kSelThreads) {
+        for (int i = tid; i < quads; i += THREADS) {
             const uint4 v = quad(i, pass == 0);
             const uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -170,30 +171,44 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
                 if (4 * (q0 + i) + e < s.old && (pass == 0 || (key[e] >> up) == prefix))
                     atomicAdd(&hist[(key[e] >> low) & ((1u << bits) - 1u)], 1u);
         }
-        if (ranks > 1) cluster_sync();
+        if (RANKS > 1) cluster_sync();
         else __syncthreads();
-        // thread i counts bins top - 2i and top - 2i - 1, from the largest down
-        const int hi = (1 << bits) - 1 - 2 * tid;
-        uint32_t c0 = 0, c1 = 0;
-        if (hi >= 1) {
-            if (ranks == 1) {
-                c0 = hist[hi];
-                c1 = hist[hi - 1];
+        // thread i counts the kPer bins from top - kPer * i on, down
+        const int hi = (1 << bits) - 1 - kPer * tid;
+        uint32_t c[kPer], n = 0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) c[u] = 0u;
+        if (hi >= kPer - 1) {
+            if constexpr (RANKS == 1) {
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) c[u] = hist[hi - u];
             } else {
-                for (int r = 0; r < ranks; ++r) {
-                    c0 += cluster_word(hist + hi, r);
-                    c1 += cluster_word(hist + hi - 1, r);
-                }
+                uint32_t all_c[RANKS][kPer];
+#pragma unroll
+                for (int r = 0; r < RANKS; ++r)
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u) all_c[r][u] = cluster_word(hist + hi - u, r);
+#pragma unroll
+                for (int r = 0; r < RANKS; ++r)
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u) c[u] += all_c[r][u];
             }
         }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) n += c[u];
         uint32_t total;
-        const uint32_t before = block_sum_before(c0 + c1, wsum, total);
-        if (before < need && need <= before + c0 + c1) {
-            const bool first = need <= before + c0;
-            found[0] = (uint32_t)(first ? hi : hi - 1);
-            found[1] = first ? before : before + c0;
+        uint32_t before = block_sum_before(n, wsum, total);
+        if (before < need && need <= before + n) {
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                if (before < need && need <= before + c[u]) {
+                    found[0] = (uint32_t)(hi - u);
+                    found[1] = before;
+                }
+                before += c[u];
+            }
         }
-        if (ranks > 1) cluster_sync();  // (nobody's counts are read any more)
+        if (RANKS > 1) cluster_sync();  // (nobody's counts are read any more)
         else __syncthreads();
         prefix = (prefix << bits) | found[0];
         need -= found[1];
@@ -202,9 +217,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     // every token with a larger key, and the first `need` of those with the
     // key itself, in ascending order
     uint32_t above = 0, equal = 0;  // in the stretches before this one, then seen so far
-    if (ranks > 1) {
+    if (RANKS > 1) {
         uint32_t gt = 0, eq = 0;
-        for (int i = tid; i < quads; i += kSelThreads) {
+        for (int i = tid; i < quads; i += THREADS) {
             const uint4 v = quad(i, false);
             const uint32_t key[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -229,7 +244,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
         cluster_sync();  // no block leaves while another reads its shared memory
     }
     int32_t* list = p.list + ((long long)b * p.Hkv + h) * p.mbps * kBlock;
-    for (int base = 0; base < quads; base += kSelThreads) {
+    for (int base = 0; base < quads; base += THREADS) {
         const int i = base + tid;
         uint32_t key[4] = {0u, 0u, 0u, 0u};
         uint32_t gt = 0, eq = 0;
@@ -350,6 +365,15 @@ size_t list_bytes(const mi_dims& D) {
     return ((size_t)D.B * D.Hkv * D.max_blocks_per_seq * kBlock * 4 + 255) / 256 * 256;
 }
 
+template <int RANKS, int THREADS>
+bool launch_select(const EvictParams& p, int units, int held, cudaStream_t st) {
+    static std::mutex mu;
+    static CUcontext done[256] = {};
+    auto* kernel = evict_select_kernel<RANKS, THREADS>;
+    return raise_smem(reinterpret_cast<const void*>(kernel), kSelKeys * 4, done, mu) &&
+           launch_cluster(kernel, units * RANKS, THREADS, held * 4, RANKS, st, p, held) == cudaSuccess;
+}
+
 mi_status evict(const mi_dims* dims, void* k_cache, void* v_cache, float* scores, const int32_t* block_tables,
                 const int32_t* context_lens, const int32_t* budgets, int32_t recent, const int32_t* dst_tables,
                 int32_t* new_lens, void* workspace, size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream,
@@ -403,11 +427,11 @@ mi_status evict(const mi_dims* dims, void* k_cache, void* v_cache, float* scores
     while (ranks < 8 && 2LL * ranks * units <= 2LL * sms && longest / (2 * ranks) >= 2048) ranks *= 2;
     const long long stretch = (longest / 4 + ranks - 1) / ranks * 4 + 4;
     const int held = (int)(stretch < kSelKeys ? (stretch + 3) / 4 * 4 : kSelKeys);
-    static std::mutex mu;
-    static CUcontext done[256] = {};
-    if (!raise_smem(reinterpret_cast<const void*>(evict_select_kernel), kSelKeys * 4, done, mu)) return MI_ERR_CUDA;
-    if (launch_cluster(evict_select_kernel, units * ranks, kSelThreads, held * 4, ranks, st, p, ranks, held) != cudaSuccess)
-        return MI_ERR_CUDA;
+    const bool sel = ranks == 1   ? launch_select<1, 512>(p, units, held, st)
+                     : ranks == 2 ? launch_select<2, 1024>(p, units, held, st)
+                     : ranks == 4 ? launch_select<4, 1024>(p, units, held, st)
+                                  : launch_select<8, 1024>(p, units, held, st);
+    if (!sel) return MI_ERR_CUDA;
     const int grid = p.in_place ? units : 8 * sms;
     cudaError_t e;
     switch (D.head_dim * elem / 16) {

@@ -44,6 +44,7 @@
 #include <mutex>
 #include <random>
 
+#include "batch.cuh"
 #include "common.cuh"
 #include "decode.cuh"
 #include "rope.cuh"
@@ -59,7 +60,6 @@ constexpr int kMaxG = 8;
 // batch)
 constexpr int kUnitCostE4m3 = 10;
 constexpr int kUnitCostBf16 = 6;
-constexpr int kUnitCostPrefix = 12;  // bf16 and the merge of the prefix's partial results
 // Fewest blocks a CTA's range is cut to (measured on one layer of 8 requests
 // of 200 tokens, 4 KV heads: 11 us with 32 CTAs against 17 us on all 304;
 // larger batches keep the whole grid).
@@ -101,7 +101,7 @@ struct AttnParams {
     long long wait_ns;             // bound on every mbarrier wait of the launch
     int early;                     // fused step: plan and first copies before the wait on the kernel before
     int withhold;                  // failure-detection test: each producer withholds its first copy
-    DecodeExt ext;                 // scored and shared-prefix steps only
+    DecodeExt ext;                 // scored step only
 };
 
 // ------------------------------------------------------------- the plan ---
@@ -448,50 +448,6 @@ __device__ __forceinline__ void store_logits(float* lg, int gp, int lane, float 
         *reinterpret_cast<float2*>(at) = make_float2(s0, s1);
         *reinterpret_cast<float2*>(at + 8 * gp) = make_float2(s2, s3);
     }
-}
-
-// Shared-prefix step: folds the prefix's partial results of head h's row g of
-// a request (`at`: its entry of DecodeExt::rows) into four of its own outputs
-// v, whose log2-sum-exp is lse (-inf: no own tokens). The HD / 4 lanes that
-// hold the row call it together: each fetches the log-sum-exp of one split,
-// so the weights cost one load for up to HD / 4 splits, and the outputs are
-// then independent loads. Partials are taken in order.
-template <int HD>
-__device__ __forceinline__ float4 merge_prefix(const DecodeExt& x, int4 at, int Hkv, int h, int g, int dcol, float lse,
-                                               float4 v) {
-    constexpr int L = HD / 4;
-    const int lane = threadIdx.x & 31, sub = lane & (L - 1);
-    const unsigned lanes = L == 32 ? 0xffffffffu : 0xffffu << (lane & ~(L - 1));
-    auto row = [&](int s) { return (long long)(at.x + s * Hkv + h) * x.slot_rows + at.z + g; };
-    float M = lse, den = lse > kNegInf ? 1.f : 0.f;
-    float4 num = den > 0.f ? v : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < at.y; s0 += L) {
-        const int cnt = min(at.y - s0, L);
-        const float mine = sub < cnt ? __ldcg(x.part_lse + row(s0 + sub)) : kNegInf;
-        float top = mine;
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
-        top = fmaxf(top, M);
-        if (top == kNegInf) continue;
-        const float old = exp2f(M - top), w = exp2f(mine - top);
-        M = top;
-        float ws = w;
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) ws += __shfl_xor_sync(lanes, ws, o);
-        den = den * old + ws;
-        num = make_float4(num.x * old, num.y * old, num.z * old, num.w * old);
-#pragma unroll 8
-        for (int k = 0; k < cnt; ++k) {
-            const float wk = __shfl_sync(lanes, w, (lane & ~(L - 1)) + k);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part + row(s0 + k) * HD + dcol));
-            num.x += wk * o.x;
-            num.y += wk * o.y;
-            num.z += wk * o.z;
-            num.w += wk * o.w;
-        }
-    }
-    const float r = den > 0.f ? 1.f / den : 0.f;
-    return make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
 }
 
 __device__ __forceinline__ uint2 pack_bf16x4(float4 v) {
@@ -1191,8 +1147,7 @@ __device__ __forceinline__ void consumer_sync(int nthreads) {
 // consumer warp that streams that block copies the two rows into its staged
 // tiles.
 // EXT (MMA and e4m3 tiles; not FUSED): kExtScored also keeps every logit and
-// each row's log-sum-exp for the score pass; kExtPrefix merges partial results
-// over a shared prefix into each row where the row is finished.
+// each row's log-sum-exp for the score pass.
 template <int HD, int VAR, int GP, int W, bool FUSED = false, int EXT = kExtNone>
 __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 || VAR == kVarInt8) && !FUSED ? 3 : 2)
     attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -1254,7 +1209,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
     // Ranges are cut by cost: a unit weighs its blocks plus a fixed number of
     // blocks for its per-unit work (q, the merge, the pipeline restart at its
     // boundary), which weighs more against the half-size one-byte blocks.
-    constexpr int uc = EXT == kExtPrefix ? kUnitCostPrefix : kOneByte ? kUnitCostE4m3 : kUnitCostBf16;
+    constexpr int uc = kOneByte ? kUnitCostE4m3 : kUnitCostBf16;
     const int cta = blockIdx.x;
     RangePlan* rp = reinterpret_cast<RangePlan*>(base + sp.rplan);
     long long TB = 0, TC = 0;
@@ -1298,9 +1253,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
         // kMinBlocksPerCta blocks each (a small batch): every CTA's fixed cost
         // (the plan, the first copies, a merge) then outweighs its share of
         // streaming, and fewer, longer ranges finish sooner.
-        // (A shared-prefix step's units are mostly that fixed cost: they count
-        // with it.)
-        const long long Pw = ((EXT == kExtPrefix ? TC : TB) + kMinBlocksPerCta - 1) / kMinBlocksPerCta;
+        const long long Pw = (TB + kMinBlocksPerCta - 1) / kMinBlocksPerCta;
         P = (int)(Pw < (long long)gridDim.x ? Pw : (long long)gridDim.x);
         plan_ranges(p, uc, scan, TB, TC, P, rp);  // (ends with a barrier of all warps)
         if (pe) {
@@ -1507,7 +1460,6 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                 const int n = __ldg(p.context_lens + b);
                 if (n > p.mbps * kBlock && lane == W) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
                 if (n <= 0) {
-                    if constexpr (EXT == kExtPrefix) continue;  // (the consumer warps write them)
                     uint4* row = reinterpret_cast<uint4*>(p.out + (long long)b * p.Hq * HD);
                     for (int i = lane - W; i < p.Hq * HD / 8; i += nl) row[i] = make_uint4(0, 0, 0, 0);
                 }
@@ -1628,19 +1580,6 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
     }
 
     // ---------------------------------------------------- consumer warps --
-    if constexpr (EXT == kExtPrefix) {
-        // requests without tokens of their own: the prefix's result alone
-        for (long long u = cta; u < (long long)p.B * p.Hkv; u += gridDim.x) {
-            const int b = (int)(u / p.Hkv), h = (int)(u % p.Hkv);
-            if (ctx_clamped(p, b) > 0) continue;
-            const int4 at = __ldcg(p.ext.rows + b);
-            for (int idx = 4 * tid; idx < p.G * HD; idx += 4 * W * 32) {
-                const int g = idx / HD, dcol = idx - g * HD;
-                const float4 v = merge_prefix<HD>(p.ext, at, p.Hkv, h, g, dcol, kNegInf, make_float4(0.f, 0.f, 0.f, 0.f));
-                *reinterpret_cast<uint2*>(p.out + ((long long)b * p.Hq + (long long)h * p.G) * HD + idx) = pack_bf16x4(v);
-            }
-        }
-    }
     if (cta >= P) return;
     float* mbuf = reinterpret_cast<float*>(base + sp.mbuf);
     float* lbuf = reinterpret_cast<float*>(base + sp.lbuf);
@@ -1777,8 +1716,6 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
         const bool whole = (sa == cu.start) && (se == cu.start + cu.len);
         const int slot = (sa == ra) ? 0 : 1;
         float* part = p.part + ((long long)cta * 2 + slot) * p.slot_floats;
-        int4 pfx = make_int4(0, 0, 0, 0);
-        if constexpr (EXT == kExtPrefix) pfx = __ldcg(p.ext.rows + cu.b);
         // four consecutive outputs per thread (16-byte shared and global
         // accesses); each thread weighs the warps' states of its head itself
         for (int idx = 4 * tid; idx < p.G * HD; idx += 4 * nc) {
@@ -1803,11 +1740,9 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                 }
             }
             const float r = L > 0.f ? 1.f / L : 0.f;
-            float4 v = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+            const float4 v = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
             if (whole) {
                 const long long row = (long long)cu.b * p.Hq + (long long)cu.h * p.G + g;
-                if constexpr (EXT == kExtPrefix)
-                    v = merge_prefix<HD>(p.ext, pfx, p.Hkv, cu.h, g, dcol, L > 0.f ? M + log2f(L) : kNegInf, v);
                 if constexpr (EXT == kExtScored)
                     if (dcol == 0) p.ext.lse[row] = L > 0.f ? M + log2f(L) : kNegInf;
                 *reinterpret_cast<uint2*>(p.out + row * HD + dcol) = pack_bf16x4(v);
@@ -1878,9 +1813,7 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
                     const float r = den > 0.f ? 1.f / den : 0.f;
                     const long long row = (long long)cu.b * p.Hq + (long long)cu.h * p.G + g;
                     const int dcol = idx - g * HD;
-                    float4 v = make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
-                    if constexpr (EXT == kExtPrefix)
-                        v = merge_prefix<HD>(p.ext, pfx, p.Hkv, cu.h, g, dcol, den > 0.f ? M + log2f(den) : kNegInf, v);
+                    const float4 v = make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
                     if constexpr (EXT == kExtScored)
                         if (dcol == 0) p.ext.lse[row] = den > 0.f ? M + log2f(den) : kNegInf;
                     *reinterpret_cast<uint2*>(p.out + row * HD + dcol) = pack_bf16x4(v);
@@ -1899,6 +1832,195 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
             (void)mbar_wait_bounded(full0 + si * 8, s2 < (int)cstage ? cphase ^ 1u : cphase, drain_limit(p.wait_ns));
         }
     }
+}
+
+// ------------------------------------- requests behind a shared prefix ----
+//
+// The requests' own tokens of a shared-prefix step. They are few to a request
+// (an answer begun, a chat turn), so the unit of attn_kernel, four warps on one
+// (request, head) with a merge of their states at its end, spends most of its
+// time on that end (44 us for 85 MB). Here a warp takes a piece of up to `step`
+// blocks of a (request, head) by itself: it looks the blocks up, issues their
+// copies into a ring of its own, and writes the piece's normalised output and
+// log-sum-exp; prefix.cu merges the pieces with the prefix's partial results.
+// step is such that every warp of the grid has about one piece.
+//
+// Launch order: this kernel follows the one that computes the prefix part and
+// depends on nothing it writes, so it starts on SMs that one leaves idle. Its
+// inputs and its part of the workspace are free: the kernel before had
+// waited for everything ahead of it. It waits for that kernel last, so that
+// whoever waits for this one has both.
+constexpr int kTailWarps = 4;
+
+template <int HD>
+struct TailSmem {
+    static constexpr int kTile = Tile<HD, 2>::kBytes;
+    static constexpr int kStages = HD == 128 ? 3 : 6;
+    static constexpr int kTotal = kTailWarps * kStages * 2 * kTile + 1024;  // slack to align the tiles
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kTailWarps * 32, 2)
+    tail_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const AttnParams p,
+                const TailWork t) {
+    constexpr int S = TailSmem<HD>::kStages, kTile = TailSmem<HD>::kTile;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) unsigned long long bars[kTailWarps * S];
+    __shared__ long long sums[flat_words(kTailWarps * 32)];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
+    const uint32_t full = smem_u32(bars) + warp * S * 8;
+    const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + (uint32_t)(warp * S * 2 * kTile);
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(full + 8 * i, 1);
+        fence_mbar_init();
+    }
+    // ---------------------------------------------------------- the plan --
+    int step = 1;
+    auto pieces = [&](int b) { return (long long)p.Hkv * ((unit_blocks(p, b) + step - 1) / step); };
+    const long long blocks = flat_scan(p.B, pieces, sums);
+    __syncthreads();
+    step = 1 << 27;
+    const long long units = flat_scan(p.B, pieces, sums);
+    auto share = [](long long x, long long parts) {
+        const long long v = (x + parts - 1) / parts;
+        return (int)(v < kTailLeast ? kTailLeast : v > (1 << 27) ? 1 << 27 : v);
+    };
+    step = share(blocks, t.target);
+    __syncthreads();
+    long long total = flat_scan(p.B, pieces, sums);
+    for (int round = 0; round < 3 && units < t.target && total > t.target; ++round) {
+        step = share((long long)step * total, t.target);
+        __syncthreads();
+        total = flat_scan(p.B, pieces, sums);
+    }
+    for (int b = blockIdx.x + gridDim.x * tid; b < p.B; b += gridDim.x * kTailWarps * 32) {
+        if (__ldg(p.context_lens + b) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
+        t.rows[b] = make_int2((int)flat_before(p.B, pieces, sums, b), (unit_blocks(p, b) + step - 1) / step);
+    }
+    // ---------------------------------------------------------- the pieces --
+    struct Piece {
+        long long x;
+        int b, h, j, j1, n;  // blocks j .. j1 - 1 of a request of n tokens
+    };
+    const long long stride = (long long)gridDim.x * kTailWarps;
+    auto piece = [&](long long x) {
+        Piece c;
+        long long first;
+        c.x = x;
+        c.b = c.h = c.j = c.j1 = c.n = 0;
+        if (x < total) {
+            c.b = flat_find(p.B, pieces, sums, x, first);
+            c.n = ctx_clamped(p, c.b);
+            const int nblk = (c.n + kBlock - 1) / kBlock, np = (nblk + step - 1) / step, o = (int)(x - first);
+            c.h = o / np;
+            c.j = (o - c.h * np) * step;
+            c.j1 = min(nblk, c.j + step);
+        }
+        return c;
+    };
+    const uint64_t policy = l2_policy_evict_first();
+    // the issuing side runs up to S blocks ahead, across pieces; table entries
+    // come 32 at a time
+    Piece in = piece((long long)blockIdx.x * kTailWarps + warp);
+    int entry = 0, base = 0;
+    auto fetch = [&]() {
+        base = in.j;
+        entry = in.x < total && in.j + lane < in.j1 ? __ldg(p.block_tables + (long long)in.b * p.mbps + in.j + lane) : -1;
+    };
+    fetch();
+    uint32_t issued = 0, copied = 0, phase = 0;  // stages used; bit i: stage i holds a block; its parity
+    bool withhold = p.withhold != 0;
+    auto issue = [&]() {
+        if (in.x >= total) return;
+        const uint32_t st = issued % S;
+        const int blk = __shfl_sync(0xffffffffu, entry, in.j - base);
+        const bool ok = blk >= 0 && blk < p.num_blocks;
+        if (lane == 0) {
+            if (!ok) {
+                raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+            } else if (!withhold) {
+                const uint32_t bar = full + 8 * st, dst = ring + st * 2 * kTile;
+                const int y = (blk * p.Hkv + in.h) * (kTile / 128);
+                mbar_arrive_expect_tx(bar, 2 * kTile);
+                tma_load_2d(dst, &tmk, bar, 0, y, policy);
+                tma_load_2d(dst + kTile, &tmv, bar, 0, y, policy);
+            }
+        }
+        withhold = false;
+        copied = ok ? copied | (1u << st) : copied & ~(1u << st);
+        ++issued;
+        if (++in.j == in.j1) {
+            in = piece(in.x + stride);
+            fetch();
+        } else if (in.j - base == 32) {
+            fetch();
+        }
+    };
+    __syncwarp();
+    Piece c = in;
+    for (int i = 0; i < S; ++i) issue();
+    uint32_t taken = 0;
+    bool dead = false;
+    MmaState<HD> st;
+    while (!dead && c.x < total) {
+        st.begin_unit(p, c.b, c.h, lane);
+        for (int j = c.j; j < c.j1; ++j, ++taken) {
+            const uint32_t sg = taken % S;
+            if ((copied >> sg) & 1u) {
+                if (!wait_all_warp(full + 8 * sg, (phase >> sg) & 1u, p.wait_ns, 0u)) {
+                    if (lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
+                    dead = true;
+                    break;
+                }
+                phase ^= 1u << sg;
+                const uint32_t kt = ring + sg * 2 * kTile, vt = kt + kTile;
+                const int valid = min(kBlock, c.n - j * kBlock);
+                if (valid < kBlock) {  // rows past the context may hold any bits: zero V there
+                    for (int i = lane; i < (kBlock - valid) * (HD / 8); i += 32)
+                        st_shared_zero16(vt + swz<HD>(valid + i / (HD / 8), i % (HD / 8)));
+                    __syncwarp();
+                }
+                st.block(kt, vt, valid, p.sl2, lane);
+                __syncwarp();
+                if (lane == 0) fence_proxy_async_smem();
+            }
+            issue();
+        }
+        if (dead) break;
+        float l0 = st.l[0], l1 = st.l[1];
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
+        }
+        const int h0 = (lane & 3) * 2, h1 = h0 + 1, r = lane >> 2;
+        const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+        float* o = t.part + c.x * p.G * HD + r;
+#pragma unroll
+        for (int mt = 0; mt < HD / 16; ++mt) {
+            if (h0 < p.G) {
+                o[h0 * HD + mt * 16] = st.o[mt][0] * i0;
+                o[h0 * HD + mt * 16 + 8] = st.o[mt][2] * i0;
+            }
+            if (h1 < p.G) {
+                o[h1 * HD + mt * 16] = st.o[mt][1] * i1;
+                o[h1 * HD + mt * 16 + 8] = st.o[mt][3] * i1;
+            }
+        }
+        if (lane < 4) {
+            if (h0 < p.G) t.lse[c.x * p.G + h0] = l0 > 0.f ? st.m[0] + log2f(l0) : kNegInf;
+            if (h1 < p.G) t.lse[c.x * p.G + h1] = l1 > 0.f ? st.m[1] + log2f(l1) : kNegInf;
+        }
+        c = piece(c.x + stride);
+    }
+    // after a wait that ran out, the copies in flight land first
+    if (dead && lane == 0)
+        for (; taken < issued; ++taken) {
+            const uint32_t sg = taken % S;
+            if ((copied >> sg) & 1u) (void)mbar_wait_bounded(full + 8 * sg, (phase >> sg) & 1u, drain_limit(p.wait_ns));
+        }
+    pdl_wait();
 }
 
 // ------------------------------------------------------------- host side --
@@ -1954,7 +2076,7 @@ KernelFn pick_kernel(int HD, int var, int G) {
     return HD == 64 ? fma_kernel_for<64>(gp_of(G)) : fma_kernel_for<128>(gp_of(G));
 }
 
-// The kernels of the scored and the shared-prefix step (null: not built).
+// The kernels of the scored step (null: not built).
 KernelFn pick_ext_kernel(int HD, int var, int kind) {
     if (kind == kExtScored && var == kVarMma)
         return HD == 64 ? attn_kernel<64, kVarMma, 8, kWarps, false, kExtScored>
@@ -1962,9 +2084,6 @@ KernelFn pick_ext_kernel(int HD, int var, int kind) {
     if (kind == kExtScored && var == kVarFp8)
         return HD == 64 ? attn_kernel<64, kVarFp8, 8, kWarps, false, kExtScored>
                         : attn_kernel<128, kVarFp8, 8, kWarps, false, kExtScored>;
-    if (kind == kExtPrefix && var == kVarMma)
-        return HD == 64 ? attn_kernel<64, kVarMma, 8, kWarps, false, kExtPrefix>
-                        : attn_kernel<128, kVarMma, 8, kWarps, false, kExtPrefix>;
     return nullptr;
 }
 
@@ -2223,7 +2342,45 @@ mi_status attention(const mi_dims* dims, const void* q, const void* k_cache, con
     return launch_pdl(fn, grid, threads, smem, s, tk, tv, p) == cudaSuccess ? MI_OK : MI_ERR_CUDA;
 }
 
+template <int HD>
+cudaError_t launch_tail(int grid, cudaStream_t st, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p,
+                        const TailWork& t) {
+    static std::mutex mu;
+    static CUcontext done[256] = {};
+    if (!raise_smem(reinterpret_cast<const void*>(tail_kernel<HD>), TailSmem<HD>::kTotal, done, mu))
+        return cudaErrorInvalidValue;
+    return launch_pdl(tail_kernel<HD>, grid, kTailWarps * 32, TailSmem<HD>::kTotal, st, tk, tv, p, t);
+}
+
 }  // namespace
+
+mi_status prefix_tail(const mi_dims* dims, const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, const int32_t* context_lens, float scale, const TailWork& work,
+                      int32_t* dev_err, mi_stream_t stream) {
+    const mi_dims D = *dims;
+    CUtensorMap tk, tv;
+    const long long rows = (long long)D.num_blocks * D.Hkv * kBlock;
+    if (!make_tmap(&tk, k_cache, rows, D.head_dim) || !make_tmap(&tv, v_cache, rows, D.head_dim)) return MI_ERR_CUDA;
+    AttnParams p = {};
+    p.q = static_cast<const uint16_t*>(q);
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.dev_err = dev_err;
+    p.B = D.B;
+    p.Hq = D.Hq;
+    p.Hkv = D.Hkv;
+    p.G = D.Hq / D.Hkv;
+    p.num_blocks = D.num_blocks;
+    p.mbps = D.max_blocks_per_seq;
+    p.sl2 = scale * 1.4426950408889634f;
+    p.wait_ns = test_wait_limit_ns();
+    p.withhold = test_withhold_copy() ? 1 : 0;
+    const int grid = work.target / kTailWarps;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = D.head_dim == 64 ? launch_tail<64>(grid, st, tk, tv, p, work)
+                                           : launch_tail<128>(grid, st, tk, tv, p, work);
+    return e == cudaSuccess ? MI_OK : MI_ERR_CUDA;
+}
 
 mi_status decode_attention_ext(const mi_dims* dims, const void* q, const void* k_cache, const void* v_cache,
                                const float* k_scale, const float* v_scale, const int32_t* block_tables,

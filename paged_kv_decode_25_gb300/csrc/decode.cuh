@@ -1,5 +1,6 @@
-// What the decode attention kernel does on top of plain attention for the
-// entry points built on it (the scored step and the shared-prefix step).
+// What the decode attention file offers to the entry points built on it: the
+// scored step's extension of the attention kernel, and the requests' own
+// tokens of the shared-prefix step.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -8,7 +9,7 @@
 
 namespace mi {
 
-enum DecodeExtKind { kExtNone = 0, kExtScored = 1, kExtPrefix = 2 };
+enum DecodeExtKind { kExtNone = 0, kExtScored = 1 };
 
 struct DecodeExt {
     int kind = kExtNone;
@@ -19,14 +20,6 @@ struct DecodeExt {
     float* logits = nullptr;
     float* lse = nullptr;
     int by_block = 0, gp = 0;
-    // kExtPrefix: what to merge into the rows of request b: rows[b] = {first
-    // slot, splits, row in the slot, 0}; split s of KV head h is slot first +
-    // s * Hkv + h, whose row i holds a normalised output part[(slot *
-    // slot_rows + i) * HD ..] and its log2-sum-exp part_lse[slot * slot_rows + i]
-    const int4* rows = nullptr;
-    const float* part = nullptr;
-    const float* part_lse = nullptr;
-    int slot_rows = 0;
 };
 
 // mi_paged_decode_attention (or the e4m3 call with `fp8`) with an extension;
@@ -36,5 +29,20 @@ mi_status decode_attention_ext(const mi_dims* dims, const void* q, const void* k
                                const int32_t* context_lens, float scale, void* out, void* workspace,
                                size_t workspace_bytes, int32_t* dev_err, mi_stream_t stream, bool fp8,
                                const DecodeExt& ext);
+
+// Attention over the requests' own tokens in pieces: request b's piece c of KV
+// head h is piece rows[b].x + h * rows[b].y + c, whose G rows of normalised
+// output are part[piece][G][HD] and their log2-sum-exps lse[piece][G]. About
+// `target` pieces (a multiple of 8), at most target + B * Hkv.
+struct TailWork {
+    int2* rows = nullptr;  // [B] {first piece, pieces per head}
+    float* part = nullptr;
+    float* lse = nullptr;
+    int target = 0;
+};
+constexpr int kTailLeast = 4;  // blocks: a shorter piece does not pay for its result
+mi_status prefix_tail(const mi_dims* dims, const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, const int32_t* context_lens, float scale, const TailWork& work,
+                      int32_t* dev_err, mi_stream_t stream);
 
 }  // namespace mi

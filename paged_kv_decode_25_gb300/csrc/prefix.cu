@@ -7,8 +7,8 @@
 //   * prefix_partials (prefill.cu): the group's queries against the prefix on
 //     the fifth-generation tensor cores, as one tall matrix of (request, head)
 //     rows per KV head: a staged K / V tile serves up to 256 of them;
-//   * the decode kernel (decode.cu) over the requests' own blocks, which
-//     merges the prefix's partial results into each row as it finishes it.
+//   * prefix_tail (decode.cu): the requests' own blocks, a warp per piece;
+//   * prefix_merge_kernel puts each row together from the two.
 //
 // The rows of (group, KV head) are cut into tiles of whole requests, the
 // prefix's blocks into equal splits; a (group, tile, split, head) is a work
@@ -22,31 +22,105 @@
 namespace mi {
 namespace {
 
-// The workspace after the decode attention's own: the rows' entries, the
-// slots' log-sum-exps and outputs.
+constexpr int kMergeThreads = 256;
+
+struct MergeParams {
+    const int4* prefix_rows;       // [B] see PrefixWork
+    const float* prefix_part;
+    const float* prefix_lse;
+    const int2* tail_rows;         // [B] see TailWork
+    const float* tail_part;
+    const float* tail_lse;
+    uint16_t* out;                 // [B][Hq][HD]
+    int B, Hq, Hkv, G, slot_rows;
+};
+
+// out = sum 2^(lse_i - M) o_i / sum 2^(lse_i - M) over a row's partial results,
+// the prefix's splits first, in order. HD / 4 lanes hold a row: each fetches
+// the log-sum-exps of every (HD / 4)-th part, so that the weights cost one
+// round of loads, and the outputs are then independent of one another.
+template <int HD>
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const MergeParams p) {
+    constexpr int L = HD / 4, kRows = kMergeThreads / L;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, sub = threadIdx.x & (L - 1), src = lane & ~(L - 1);
+    const unsigned lanes = L == 32 ? 0xffffffffu : 0xffffu << src;
+    const long long row = (long long)blockIdx.x * kRows + threadIdx.x / L;
+    if (row >= (long long)p.B * p.Hq) return;
+    const int b = (int)(row / p.Hq), j = (int)(row % p.Hq), h = j / p.G, g = j % p.G;
+    const int4 at = __ldcg(p.prefix_rows + b);
+    const int2 own = __ldcg(p.tail_rows + b);
+    const int parts = at.y + own.y;
+    // where part i's row lies, in rows of its array
+    auto place = [&](int i) {
+        return i < at.y ? (long long)(at.x + i * p.Hkv + h) * p.slot_rows + at.z + g
+                        : (long long)(own.x + h * own.y + (i - at.y)) * p.G + g;
+    };
+    float M = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += L) {
+        const int cnt = min(parts - i0, L);
+        float mine = -INFINITY;
+        if (sub < cnt) mine = __ldcg((i0 + sub < at.y ? p.prefix_lse : p.tail_lse) + place(i0 + sub));
+        float top = mine;
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
+        top = fmaxf(top, M);
+        if (top == -INFINITY) continue;
+        const float old = exp2f(M - top), w = exp2f(mine - top);
+        M = top;
+        float ws = w;
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) ws += __shfl_xor_sync(lanes, ws, o);
+        den = den * old + ws;
+        num = make_float4(num.x * old, num.y * old, num.z * old, num.w * old);
+#pragma unroll 8
+        for (int k = 0; k < cnt; ++k) {
+            const float wk = __shfl_sync(lanes, w, src + k);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>((i0 + k < at.y ? p.prefix_part : p.tail_part) +
+                                                                    place(i0 + k) * HD + sub * 4));
+            num.x += wk * o.x;
+            num.y += wk * o.y;
+            num.z += wk * o.z;
+            num.w += wk * o.w;
+        }
+    }
+    const float r = den > 0.f ? 1.f / den : 0.f;
+    *reinterpret_cast<uint2*>(p.out + row * HD + sub * 4) =
+        make_uint2(pack_bf16x2(num.x * r, num.y * r), pack_bf16x2(num.z * r, num.w * r));
+}
+
+// The workspace: the requests' entries of both parts, the log-sum-exps and
+// outputs of the prefix's slots and of the pieces.
 struct PrefixSpace {
-    size_t rows, lse, part, total;
+    size_t rows, tail_rows, lse, tail_lse, part, tail_part, total;
     long long slots;
-    int slot_rows, sms;
+    int slot_rows, sms, target;
 };
 
 bool prefix_space(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks, PrefixSpace* s) {
     if (check_paged_dims(dims) != MI_OK || num_prefixes < 0 || num_prefixes > 65535 || max_prefix_blocks < 1 ||
         (long long)max_prefix_blocks * kBlock > 0x7FFFFFFFLL)
         return false;
-    const size_t base = mi_paged_decode_workspace_bytes(dims);
     const int sms = sm_count();
-    if (base == 0 || sms <= 0) return false;
+    if (sms <= 0) return false;
     const mi_dims& D = *dims;
     const int G = D.Hq / D.Hkv, per = prefix_tile_requests(G);
     s->sms = sms;
     s->slot_rows = per * G;
     s->slots = prefix_slots(D.B, D.Hkv, num_prefixes, per, sms);
-    if (s->slots * s->slot_rows > 0x7FFFFFFFLL) return false;
-    s->rows = (base + 255) / 256 * 256;
-    s->lse = s->rows + ((size_t)D.B * 16 + 255) / 256 * 256;
-    s->part = s->lse + ((size_t)s->slots * s->slot_rows * 4 + 255) / 256 * 256;
-    s->total = s->part + (size_t)s->slots * s->slot_rows * D.head_dim * 4;
+    s->target = 8 * sms;  // two blocks of four warps an SM
+    const long long pieces = s->target + (long long)D.B * D.Hkv;
+    if (s->slots * s->slot_rows > 0x7FFFFFFFLL || pieces * G > 0x7FFFFFFFLL) return false;
+    auto next = [](size_t at, size_t bytes) { return (at + bytes + 255) / 256 * 256; };
+    s->rows = 0;
+    s->tail_rows = next(s->rows, (size_t)D.B * 16);
+    s->lse = next(s->tail_rows, (size_t)D.B * 8);
+    s->tail_lse = next(s->lse, (size_t)s->slots * s->slot_rows * 4);
+    s->part = next(s->tail_lse, (size_t)pieces * G * 4);
+    s->tail_part = next(s->part, (size_t)s->slots * s->slot_rows * D.head_dim * 4);
+    s->total = next(s->tail_part, (size_t)pieces * G * D.head_dim * 4);
     return true;
 }
 
@@ -93,15 +167,34 @@ extern "C" mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32
     w.P = num_prefixes;
     w.B = D.B;
     w.sms = s.sms;
-    const mi_status st = prefix_partials(dims, max_prefix_blocks, q, k_cache, v_cache, prefix_tables, scale, w, s.slots,
+    mi_status st = prefix_partials(dims, max_prefix_blocks, q, k_cache, v_cache, prefix_tables, scale, w, s.slots,
                                          dev_err, stream);
     if (st != MI_OK) return st;
-    DecodeExt ext;
-    ext.kind = kExtPrefix;
-    ext.rows = w.rows;
-    ext.part = w.part;
-    ext.part_lse = w.part_lse;
-    ext.slot_rows = s.slot_rows;
-    return decode_attention_ext(dims, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale, out,
-                                workspace, s.rows, dev_err, stream, false, ext);
+    TailWork t;
+    t.rows = reinterpret_cast<int2*>(ws + s.tail_rows);
+    t.part = reinterpret_cast<float*>(ws + s.tail_part);
+    t.lse = reinterpret_cast<float*>(ws + s.tail_lse);
+    t.target = s.target;
+    st = prefix_tail(dims, q, k_cache, v_cache, block_tables, context_lens, scale, t, dev_err, stream);
+    if (st != MI_OK) return st;
+    MergeParams m;
+    m.prefix_rows = w.rows;
+    m.prefix_part = w.part;
+    m.prefix_lse = w.part_lse;
+    m.tail_rows = t.rows;
+    m.tail_part = t.part;
+    m.tail_lse = t.lse;
+    m.out = static_cast<uint16_t*>(out);
+    m.B = D.B;
+    m.Hq = D.Hq;
+    m.Hkv = D.Hkv;
+    m.G = D.Hq / D.Hkv;
+    m.slot_rows = s.slot_rows;
+    const int HD = D.head_dim, per = kMergeThreads / (HD / 4);
+    const long long grid = ((long long)D.B * D.Hq + per - 1) / per;
+    if (grid > 0x7FFFFFFFLL) return MI_ERR_INVALID_ARG;
+    return launch_pdl(HD == 128 ? prefix_merge_kernel<128> : prefix_merge_kernel<64>, (int)grid, kMergeThreads, 0,
+                      (cudaStream_t)stream, m) == cudaSuccess
+               ? MI_OK
+               : MI_ERR_CUDA;
 }

@@ -12,9 +12,11 @@ constexpr int kSplitStep = 8;  // blocks: a split is whole 128-key stages
 struct PrefixWork {
     const int32_t* lens = nullptr;    // [P] tokens of each prefix
     const int32_t* starts = nullptr;  // [P + 1] the groups' requests
-    int4* rows = nullptr;             // [B] see DecodeExt
-    float* part = nullptr;            // [slots][slot_rows][HD]
-    float* part_lse = nullptr;        // [slots][slot_rows]
+    // [B] {first slot, splits, row in the slot, 0}: split s of KV head h is slot
+    // first + s * Hkv + h
+    int4* rows = nullptr;
+    float* part = nullptr;            // [slots][slot_rows][HD], normalised
+    float* part_lse = nullptr;        // [slots][slot_rows] log2-sum-exps
     int P = 0, B = 0, sms = 0;
 };
 

@@ -1839,34 +1839,44 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
 // The requests' own tokens of a shared-prefix step. They are few to a request
 // (an answer begun, a chat turn), so the unit of attn_kernel, four warps on one
 // (request, head) with a merge of their states at its end, spends most of its
-// time on that end (44 us for 85 MB). Here a warp takes a piece of up to `step`
+// time on that end (44 us for 139 MB). Here a warp takes a piece of up to `step`
 // blocks of a (request, head) by itself: it looks the blocks up, issues their
 // copies into a ring of its own, and writes the piece's normalised output and
-// log-sum-exp; prefix.cu merges the pieces with the prefix's partial results.
-// step is such that every warp of the grid has about one piece.
+// log-sum-exp; prefix.cu merges the pieces with the prefix's partial results
+// (139 MB in 20 us with every SM at it, 6.8 TB/s).
+//
+// A warp spends about 1,000 clocks on a block's products and softmax and 400 on
+// its copies, all of it latency, so an SM holds twelve warps of two stages
+// rather than eight of three (40 us for a step against 45).
 //
 // Launch order: this kernel follows the one that computes the prefix part and
 // depends on nothing it writes, so it starts on SMs that one leaves idle. Its
 // inputs and its part of the workspace are free: the kernel before had
-// waited for everything ahead of it. It waits for that kernel last, so that
-// whoever waits for this one has both.
-constexpr int kTailWarps = 4;
+// waited for everything ahead of it. Its first block waits for that kernel at
+// its end, so that whoever waits for this one has both (with every block
+// waiting, those that were done kept their SMs from the rest).
+constexpr int kTailWarps = 4, kTailBlocks = 3;  // a block's, an SM's
+// pieces of an early warp: requests differ in length, so one piece a warp would
+// leave the SMs waiting for the longest (128 requests of 16 to 512 tokens: 107
+// us for two pieces, 94 for four, 93 for eight)
+constexpr int kTailPieces = 8;
 
 template <int HD>
 struct TailSmem {
     static constexpr int kTile = Tile<HD, 2>::kBytes;
-    static constexpr int kStages = HD == 128 ? 3 : 6;
+    static constexpr int kStages = HD == 128 ? 2 : 4;
     static constexpr int kTotal = kTailWarps * kStages * 2 * kTile + 1024;  // slack to align the tiles
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kTailWarps * 32, 2)
+__global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
     tail_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const AttnParams p,
                 const TailWork t) {
     constexpr int S = TailSmem<HD>::kStages, kTile = TailSmem<HD>::kTile;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long bars[kTailWarps * S];
-    __shared__ long long sums[flat_words(kTailWarps * 32)];
+    __shared__ long long sums[flat_words(kTailWarps * 32)], red[2][kTailWarps];
+    __shared__ int own[kFlatOneWarp], first_piece[kFlatOneWarp + 1];  // usual batches: tokens, pieces before
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     const uint32_t full = smem_u32(bars) + warp * S * 8;
@@ -1876,43 +1886,108 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2)
         fence_mbar_init();
     }
     // ---------------------------------------------------------- the plan --
-    int step = 1;
-    auto pieces = [&](int b) { return (long long)p.Hkv * ((unit_blocks(p, b) + step - 1) / step); };
-    const long long blocks = flat_scan(p.B, pieces, sums);
+    // Early warps, on the SMs that the prefix part leaves, take the pieces they
+    // can finish while it runs; the others, started as it ends, take the rest.
+    const bool small = p.B <= kFlatOneWarp;
+    long long blocks = 0, prefix = 0;  // (head, block)s of own tokens, (tile, block)s of the prefixes
+    for (int b = tid; b < p.B; b += kTailWarps * 32) {
+        if (b % (int)gridDim.x == (int)blockIdx.x && __ldg(p.context_lens + b) > p.mbps * kBlock)
+            raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
+        const int n = ctx_clamped(p, b);
+        if (small) own[b] = n;
+        blocks += (long long)p.Hkv * ((n + kBlock - 1) / kBlock);
+    }
+    // groups that do not ascend give a number as good as any: it sets shares
+    // of the work, never an index
+    for (int g = tid; g < t.prefix.P; g += kTailWarps * 32)
+        prefix += (long long)min(max(prefix_units(t.prefix, p.Hkv, prefix_tile_requests(p.G), g), 0), p.B * p.Hkv) *
+                  prefix_blocks(t.prefix, t.prefix_mbps, g);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+        prefix += __shfl_xor_sync(0xffffffffu, prefix, o);
+    }
+    if (lane == 0) {
+        red[0][warp] = blocks;
+        red[1][warp] = prefix;
+    }
     __syncthreads();
-    step = 1 << 27;
-    const long long units = flat_scan(p.B, pieces, sums);
-    auto share = [](long long x, long long parts) {
-        const long long v = (x + parts - 1) / parts;
-        return (int)(v < kTailLeast ? kTailLeast : v > (1 << 27) ? 1 << 27 : v);
-    };
-    step = share(blocks, t.target);
-    __syncthreads();
-    long long total = flat_scan(p.B, pieces, sums);
-    for (int round = 0; round < 3 && units < t.target && total > t.target; ++round) {
-        step = share((long long)step * total, t.target);
+    blocks = prefix = 0;
+    for (int i = 0; i < kTailWarps; ++i) {
+        blocks += red[0][i];
+        prefix += red[1][i];
+    }
+    const int active = prefix_budget(t.prefix, prefix, blocks);
+    const int warps = gridDim.x * kTailWarps;
+    const int early = prefix > 0 ? (t.prefix.sms - active) * kTailBlocks * kTailWarps : 0;
+    // the early warps' part of the blocks
+    float part = early > 0 ? (float)(t.prefix.sms - active) / (float)active * (float)prefix * kTileBlock / (float)blocks : 0.f;
+    if (!(part < 0.875f)) part = 1.f;
+    auto pieces_of = [&](int n, int step) { return p.Hkv * (((n + kBlock - 1) / kBlock + step - 1) / step); };
+    constexpr int kWhole = 1 << 27;  // a table's blocks are no more
+    int step = (int)min((long long)kWhole, max((long long)kTailLeast, (blocks + t.most - 1) / t.most));
+    if (part > 0.f) step = max(step, (int)ceilf((float)blocks * part / (float)(kTailPieces * early)));
+    if (part < 1.f) step = max(step, (int)ceilf((float)blocks * (1.f - part) / (float)(warps - early)));
+    step = min(step, kWhole);
+    auto pieces = [&](int b) { return (long long)pieces_of(ctx_clamped(p, b), step); };
+    int total;
+    if (small) {
+        if (warp == 0) {
+            const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+            int v = 0;
+            for (int b = b0; b < b1; ++b) v += pieces_of(own[b], step);
+            int x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) first_piece[p.B] = x;
+            x -= v;
+            for (int b = b0; b < b1; ++b) {
+                first_piece[b] = x;
+                x += pieces_of(own[b], step);
+            }
+        }
         __syncthreads();
-        total = flat_scan(p.B, pieces, sums);
+        total = first_piece[p.B];
+    } else {
+        total = (int)flat_scan(p.B, pieces, sums);
     }
-    for (int b = blockIdx.x + gridDim.x * tid; b < p.B; b += gridDim.x * kTailWarps * 32) {
-        if (__ldg(p.context_lens + b) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
-        t.rows[b] = make_int2((int)flat_before(p.B, pieces, sums, b), (unit_blocks(p, b) + step - 1) / step);
-    }
+    const int split = part < 1.f ? min(total, (int)((float)total * part)) : total;
+    for (int b = blockIdx.x + gridDim.x * tid; b < p.B; b += gridDim.x * kTailWarps * 32)
+        t.rows[b] = make_int2(small ? first_piece[b] : (int)flat_before(p.B, pieces, sums, b),
+                              pieces_of(ctx_clamped(p, b), step) / p.Hkv);
     // ---------------------------------------------------------- the pieces --
     struct Piece {
-        long long x;
-        int b, h, j, j1, n;  // blocks j .. j1 - 1 of a request of n tokens
+        int x, b, h, j, j1, n;  // blocks j .. j1 - 1 of a request of n tokens
     };
-    const long long stride = (long long)gridDim.x * kTailWarps;
-    auto piece = [&](long long x) {
+    const int self = blockIdx.x * kTailWarps + warp;
+    const bool is_early = self < early;
+    const int stride = is_early ? early : warps - early, end = is_early ? split : total;
+    auto piece = [&](int x) {
         Piece c;
-        long long first;
         c.x = x;
         c.b = c.h = c.j = c.j1 = c.n = 0;
-        if (x < total) {
-            c.b = flat_find(p.B, pieces, sums, x, first);
-            c.n = ctx_clamped(p, c.b);
-            const int nblk = (c.n + kBlock - 1) / kBlock, np = (nblk + step - 1) / step, o = (int)(x - first);
+        if (x < end) {
+            int o;
+            if (small) {
+                int lo = 0, hi = p.B;  // first_piece[lo] <= x < first_piece[hi]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (first_piece[mid] <= x) lo = mid;
+                    else hi = mid;
+                }
+                c.b = lo;
+                c.n = own[lo];
+                o = x - first_piece[lo];
+            } else {
+                long long first;
+                c.b = flat_find(p.B, pieces, sums, x, first);
+                c.n = ctx_clamped(p, c.b);
+                o = (int)(x - first);
+            }
+            const int nblk = (c.n + kBlock - 1) / kBlock, np = (nblk + step - 1) / step;
             c.h = o / np;
             c.j = (o - c.h * np) * step;
             c.j1 = min(nblk, c.j + step);
@@ -1922,17 +1997,17 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2)
     const uint64_t policy = l2_policy_evict_first();
     // the issuing side runs up to S blocks ahead, across pieces; table entries
     // come 32 at a time
-    Piece in = piece((long long)blockIdx.x * kTailWarps + warp);
+    Piece in = piece(is_early ? self : split + self - early);
     int entry = 0, base = 0;
     auto fetch = [&]() {
         base = in.j;
-        entry = in.x < total && in.j + lane < in.j1 ? __ldg(p.block_tables + (long long)in.b * p.mbps + in.j + lane) : -1;
+        entry = in.x < end && in.j + lane < in.j1 ? __ldg(p.block_tables + (long long)in.b * p.mbps + in.j + lane) : -1;
     };
     fetch();
     uint32_t issued = 0, copied = 0, phase = 0;  // stages used; bit i: stage i holds a block; its parity
     bool withhold = p.withhold != 0;
     auto issue = [&]() {
-        if (in.x >= total) return;
+        if (in.x >= end) return;
         const uint32_t st = issued % S;
         const int blk = __shfl_sync(0xffffffffu, entry, in.j - base);
         const bool ok = blk >= 0 && blk < p.num_blocks;
@@ -1963,7 +2038,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2)
     uint32_t taken = 0;
     bool dead = false;
     MmaState<HD> st;
-    while (!dead && c.x < total) {
+    while (!dead && c.x < end) {
         st.begin_unit(p, c.b, c.h, lane);
         for (int j = c.j; j < c.j1; ++j, ++taken) {
             const uint32_t sg = taken % S;
@@ -1996,7 +2071,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2)
         }
         const int h0 = (lane & 3) * 2, h1 = h0 + 1, r = lane >> 2;
         const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-        float* o = t.part + c.x * p.G * HD + r;
+        float* o = t.part + (long long)c.x * p.G * HD + r;
 #pragma unroll
         for (int mt = 0; mt < HD / 16; ++mt) {
             if (h0 < p.G) {
@@ -2009,8 +2084,8 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2)
             }
         }
         if (lane < 4) {
-            if (h0 < p.G) t.lse[c.x * p.G + h0] = l0 > 0.f ? st.m[0] + log2f(l0) : kNegInf;
-            if (h1 < p.G) t.lse[c.x * p.G + h1] = l1 > 0.f ? st.m[1] + log2f(l1) : kNegInf;
+            if (h0 < p.G) t.lse[(long long)c.x * p.G + h0] = l0 > 0.f ? st.m[0] + log2f(l0) : kNegInf;
+            if (h1 < p.G) t.lse[(long long)c.x * p.G + h1] = l1 > 0.f ? st.m[1] + log2f(l1) : kNegInf;
         }
         c = piece(c.x + stride);
     }
@@ -2020,7 +2095,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2)
             const uint32_t sg = taken % S;
             if ((copied >> sg) & 1u) (void)mbar_wait_bounded(full + 8 * sg, (phase >> sg) & 1u, drain_limit(p.wait_ns));
         }
-    pdl_wait();
+    if (blockIdx.x == 0) pdl_wait();
 }
 
 // ------------------------------------------------------------- host side --
@@ -2375,7 +2450,7 @@ mi_status prefix_tail(const mi_dims* dims, const void* q, const void* k_cache, c
     p.sl2 = scale * 1.4426950408889634f;
     p.wait_ns = test_wait_limit_ns();
     p.withhold = test_withhold_copy() ? 1 : 0;
-    const int grid = work.target / kTailWarps;
+    const int grid = kTailBlocks * work.prefix.sms;
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = D.head_dim == 64 ? launch_tail<64>(grid, st, tk, tv, p, work)
                                            : launch_tail<128>(grid, st, tk, tv, p, work);

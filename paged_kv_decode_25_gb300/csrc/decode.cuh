@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "mi.h"
+#include "prefix.cuh"
 
 namespace mi {
 
@@ -32,13 +33,16 @@ mi_status decode_attention_ext(const mi_dims* dims, const void* q, const void* k
 
 // Attention over the requests' own tokens in pieces: request b's piece c of KV
 // head h is piece rows[b].x + h * rows[b].y + c, whose G rows of normalised
-// output are part[piece][G][HD] and their log2-sum-exps lse[piece][G]. About
-// `target` pieces (a multiple of 8), at most target + B * Hkv.
+// output are part[piece][G][HD] and their log2-sum-exps lse[piece][G]; at most
+// `most` + B * Hkv pieces. `prefix`, `prefix_mbps`: the prefix part that runs
+// at the same time.
 struct TailWork {
     int2* rows = nullptr;  // [B] {first piece, pieces per head}
     float* part = nullptr;
     float* lse = nullptr;
-    int target = 0;
+    long long most = 0;
+    PrefixWork prefix;
+    int prefix_mbps = 0;
 };
 constexpr int kTailLeast = 4;  // blocks: a shorter piece does not pay for its result
 mi_status prefix_tail(const mi_dims* dims, const void* q, const void* k_cache, const void* v_cache,

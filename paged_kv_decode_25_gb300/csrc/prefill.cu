@@ -936,16 +936,16 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     // two tiles are consecutive, tr rows apart
     const int tr = (kTcRows / p.G) * p.G;
     long long items = 1, item = 0;  // PREFIX: the plan's, and this block's
-    int step = 0;
+    int step = 0, stride = 1;
     __shared__ long long sums[PREFIX ? flat_words(kT2Threads) + 2 : 1];
     __shared__ PrefixItem pick;
     if constexpr (PREFIX) {
-        items = prefix_plan(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, step, &pick);
-        item = blockIdx.x;
+        items = prefix_plan(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, step, stride, &pick);
+        item = blockIdx.x < stride ? blockIdx.x : items;
     }
     uint32_t tbase = PREFIX ? lds_u32(sbase + SM::kTmem) : 0u;
     bool bad = false;  // a wait ran out
-    for (bool first = true; item < items; item += gridDim.x, first = false) {
+    for (bool first = true; item < items; item += stride, first = false) {
         Item it;
         const int32_t* table;  // of the item's keys
         int slot = 0;

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
 struct PrefixSpace {
     size_t rows, tail_rows, lse, tail_lse, part, tail_part, total;
     long long slots;
-    int slot_rows, sms, target;
+    int slot_rows, sms, most;
 };
 
 bool prefix_space(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks, PrefixSpace* s) {
@@ -110,9 +110,9 @@ bool prefix_space(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_
     s->sms = sms;
     s->slot_rows = per * G;
     s->slots = prefix_slots(D.B, D.Hkv, num_prefixes, per, sms);
-    s->target = 8 * sms;  // two blocks of four warps an SM
-    const long long pieces = s->target + (long long)D.B * D.Hkv;
-    if (s->slots * s->slot_rows > 0x7FFFFFFFLL || pieces * G > 0x7FFFFFFFLL) return false;
+    s->most = 32 * sms;
+    const long long pieces = s->most + (long long)D.B * D.Hkv;
+    if (s->slots * s->slot_rows > 0x7FFFFFFFLL || pieces * G > 0x3FFFFFFFLL) return false;
     auto next = [](size_t at, size_t bytes) { return (at + bytes + 255) / 256 * 256; };
     s->rows = 0;
     s->tail_rows = next(s->rows, (size_t)D.B * 16);
@@ -164,6 +164,8 @@ extern "C" mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32
     w.rows = reinterpret_cast<int4*>(ws + s.rows);
     w.part = reinterpret_cast<float*>(ws + s.part);
     w.part_lse = reinterpret_cast<float*>(ws + s.lse);
+    w.own = context_lens;
+    w.own_blocks = D.max_blocks_per_seq;
     w.P = num_prefixes;
     w.B = D.B;
     w.sms = s.sms;
@@ -174,7 +176,9 @@ extern "C" mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32
     t.rows = reinterpret_cast<int2*>(ws + s.tail_rows);
     t.part = reinterpret_cast<float*>(ws + s.tail_part);
     t.lse = reinterpret_cast<float*>(ws + s.tail_lse);
-    t.target = s.target;
+    t.most = s.most;
+    t.prefix = w;
+    t.prefix_mbps = max_prefix_blocks;
     st = prefix_tail(dims, q, k_cache, v_cache, block_tables, context_lens, scale, t, dev_err, stream);
     if (st != MI_OK) return st;
     MergeParams m;

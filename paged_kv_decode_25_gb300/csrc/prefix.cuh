@@ -17,7 +17,8 @@ struct PrefixWork {
     int4* rows = nullptr;
     float* part = nullptr;            // [slots][slot_rows][HD], normalised
     float* part_lse = nullptr;        // [slots][slot_rows] log2-sum-exps
-    int P = 0, B = 0, sms = 0;
+    const int32_t* own = nullptr;     // [B] the requests' own tokens (at most own_blocks blocks each)
+    int P = 0, B = 0, sms = 0, own_blocks = 0;
 };
 
 // Item: prefix g's keys from its block blk0 on (n tokens there), against the
@@ -66,24 +67,47 @@ __device__ inline PrefixItem prefix_item(const PrefixWork& w, int Hkv, int mbps,
     return it;
 }
 
-// The split length: short enough that the grid has work, long enough that one
-// wave takes it all where the tiles alone do not fill it. An even share of
-// the blocks comes first; a share that leaves more items than SMs (each group
-// rounds up) grows by that ratio.
+// Blocks of a split for an even share of `blocks` among `items`, in whole stages.
 __device__ __forceinline__ int prefix_share(long long blocks, long long items) {
     const long long share = (blocks + items - 1) / items;
     const long long up = (share + kSplitStep - 1) / kSplitStep * kSplitStep;
     return (int)(up < kSplitStep ? kSplitStep : up > (1 << 27) ? 1 << 27 : up);  // a table has at most 2^27 blocks
 }
 
+// The SMs that the prefix part takes. The requests' own tokens are read by a
+// launch that fills the SMs this one leaves (decode.cu). The two are bound by
+// different things, tensor cores and memory, and share the SMs in proportion
+// to their work, so that both end together: a (tile, block) of the prefix takes
+// an SM as long as kTileBlock blocks of own tokens. Own tokens get three
+// quarters of the SMs at most: where they are most of the work they are bound by
+// memory, and the prefix part should not wait for them. Measured with 64 chats
+// of 32 to 1,024 tokens behind 4,100, 128 of 16 to 512 behind 32,000, and 90 in
+// six groups: 37, 93 and 37 us; one after the other 44, 96 and 41; kTileBlock 1
+// or 3: 45, 93, 37 and 38, 126, 44.
+constexpr int kTileBlock = 2;
+__device__ __forceinline__ int prefix_budget(const PrefixWork& w, long long tile_blocks, long long own_blocks) {
+    const long long a = tile_blocks * kTileBlock, b = own_blocks;
+    if (a + b <= 0) return w.sms;
+    const long long least = w.sms - (long long)w.sms * 3 / 4;
+    const long long x = (w.sms * a + (a + b) / 2) / (a + b);
+    return (int)(x < least ? least : x < 1 ? 1 : x);
+}
+__device__ __forceinline__ long long own_blocks_of(const PrefixWork& w, int b) {
+    return (min(max(__ldg(w.own + b), 0), w.own_blocks * kBlock) + kBlock - 1) / kBlock;
+}
+
+// An item's prologue and end count as much as this many blocks of its prefix
+// (7 us, and 2.1 us for 8 blocks).
+constexpr int kItemBlocks = 27;
+
 // Plans the call in every block, with all its threads: the blocks of a split
-// in `step`, the items laid end to end in `sums` (two words more than
+// in `step`, the grid's blocks that take items (the first ones) in `active`, the items laid end to end in `sums` (two words more than
 // flat_words), their number returned, this block's first one in *mine (shared).
 // Writes the requests' rows. Up to 32 groups one warp does it from one load of
 // each group's numbers: the block's other way, four scans of the list, took
 // 3 us of a call.
 __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int mbps, int per, int32_t* dev_err,
-                                        long long* sums, int& step, PrefixItem* mine) {
+                                        long long* sums, int& step, int& active, PrefixItem* mine) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
     auto no_prefix = [&]() {  // no request's prefix is known
         if (blockIdx.x == 0 && tid == 0) raise_err(dev_err, MI_DEVERR_BAD_QUERY);
@@ -108,15 +132,35 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
                     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                     return v;
                 };
-                const long long cost = sum((long long)units * blocks), busy = sum(blocks > 0 ? units : 0);
-                step = prefix_share(cost, busy < w.sms ? w.sms : 2LL * w.sms);
-                long long items = (long long)units * prefix_splits(blocks, step);
-                total = sum(items);
-                for (int round = 0; round < 3 && busy < w.sms && total > w.sms; ++round) {
-                    step = prefix_share((long long)step * total, w.sms);
-                    items = (long long)units * prefix_splits(blocks, step);
-                    total = sum(items);
+                long long own = 0;
+                for (int b = lane; b < w.B; b += 32) own += Hkv * own_blocks_of(w, b);
+                const long long cost = sum((long long)units * blocks);
+                active = prefix_budget(w, cost, sum(own));
+                // lane i tries a share of 0.5 + i / 20 of the even one, made
+                // as short as its number of splits of the longest prefix allows
+                const long long share = prefix_share(cost, active), least = prefix_share(cost, 2LL * w.sms);
+                int longest = blocks;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+                longest = max(longest, 1);
+                const int tried = prefix_share(share * (10 + lane), 20);
+                step = (int)max(least, (long long)prefix_share(longest, prefix_splits(longest, tried)));
+                long long items = 0;
+                for (int g = 0; g < w.P; ++g)
+                    items += (long long)__shfl_sync(0xffffffffu, units, g) *
+                             prefix_splits(__shfl_sync(0xffffffffu, blocks, g), step);
+                long long time = (items + active - 1) / active * (min(step, longest) + kItemBlocks);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const long long t = __shfl_xor_sync(0xffffffffu, time, o);
+                    const int other = __shfl_xor_sync(0xffffffffu, step, o);
+                    if (t < time || (t == time && other > step)) {
+                        time = t;
+                        step = other;
+                    }
                 }
+                items = (long long)units * prefix_splits(blocks, step);
+                total = sum(items);
                 long long x = items;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -126,16 +170,18 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
                 sums[lane] = x - items;
                 if (lane == 31) sums[32] = x;
                 __syncwarp();
-                if (lane == 0 && blockIdx.x < total) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
+                if (lane == 0 && blockIdx.x < min(total, (long long)active)) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
             }
             if (lane == 0) {
                 sums[33] = step;
                 sums[34] = total;
+                sums[35] = active;
             }
         }
         __syncthreads();
         step = (int)sums[33];
         total = sums[34];
+        active = (int)sums[35];
         if (step == 0) {
             no_prefix();
             return 0;
@@ -148,20 +194,15 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
         const long long cost = flat_scan(
             w.P, [&](int g) { return (long long)prefix_units(w, Hkv, per, g) * prefix_blocks(w, mbps, g); }, sums);
         __syncthreads();
-        auto items = [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); };
-        step = 1 << 27;
-        const long long busy = flat_scan(w.P, items, sums);
-        step = prefix_share(cost, busy < w.sms ? w.sms : 2LL * w.sms);
+        active = prefix_budget(w, cost, Hkv * flat_scan(w.B, [&](int b) { return own_blocks_of(w, b); }, sums));
         __syncthreads();
+        auto items = [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); };
+        // an even share
+        step = prefix_share(cost, active);
         total = flat_scan(w.P, items, sums);
-        for (int round = 0; round < 3 && busy < w.sms && total > w.sms; ++round) {
-            step = prefix_share((long long)step * total, w.sms);
-            __syncthreads();
-            total = flat_scan(w.P, items, sums);
-        }
         for (int g = blockIdx.x * nt + tid; g < w.P; g += gridDim.x * nt)
             if (__ldg(w.lens + g) > mbps * kBlock) raise_err(dev_err, MI_DEVERR_BAD_CONTEXT);
-        if (tid == 0 && blockIdx.x < total) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
+        if (tid == 0 && blockIdx.x < min(total, (long long)active)) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
         __syncthreads();
     }
     // each request's slots; those outside every group have none
@@ -190,7 +231,7 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
 // The prefix part of a shared-prefix decode step: each slot's partial outputs
 // and log-sum-exps (prefill.cu). `slots` as prefix_slots for tiles of
 // prefix_tile_requests(G) requests.
-constexpr int prefix_tile_requests(int G) { return 2 * (128 / G); }
+__host__ __device__ constexpr int prefix_tile_requests(int G) { return 2 * (128 / G); }
 mi_status prefix_partials(const mi_dims* dims, int32_t max_prefix_blocks, const void* q, const void* k_cache,
                           const void* v_cache, const int32_t* prefix_tables, float scale, const PrefixWork& work,
                           long long slots, int32_t* dev_err, mi_stream_t stream);

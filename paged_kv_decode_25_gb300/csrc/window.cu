@@ -81,14 +81,15 @@ struct WindowParams {
     const int32_t* tables;         // [R][mbps]
     const int32_t* lens;           // [R]
     const int32_t* query_start;    // [R + 1]
-    float* part;                   // [T][Hq][splits] partial log-sum-exps, base 2
+    float* part;                   // [slots][kRows] partial log-sum-exps, base 2 (see Cost)
     float* nlse;                   // [Hkv][T][G] the rows' negated log-sum-exps (-inf: no key)
-    unsigned int* next;            // [0] kSum: the next item, [1] the key stages per split (0: bad query_start)
+    unsigned int* next;            // kSum: the next item
+    long long* begin;              // [R + 1] the cost before each request, then a block's share (0: bad query_start)
     float* scores;                 // [num_blocks][Hkv][16]
     int32_t* dev_err;
     int R, Hq, Hkv, G, num_blocks, mbps, T, max_q, fresh;
     int xt;                        // kWindow: 128-row halves that hold rows
-    int splits, sms;               // most splits of a row's keys
+    int grid;
     float sl2;                     // scale * log2(e), never 0
     long long wait_ns;
     int withhold;                  // failure-detection test: the first Y tile of every block is not announced
@@ -122,103 +123,130 @@ __device__ __forceinline__ int seen_stages(const WindowParams& p, const Request&
     const int last = x.first + min(x.m, (rb + 1) * (kRows / p.G)) - 1;
     return last >= 0 ? last / (2 * kKeys) + 1 : 0;
 }
-__device__ __forceinline__ int key_stages(const Request& x) { return ceil_div(x.n, 2 * kKeys); }
 
-// 256-key stages per split, no more splits of a row than the workspace has
-// places for. A block's share of the items comes in whole ones, so among 32
-// lengths from the shortest allowed on the one with the least work for the
-// busiest block is taken (a split's own cost: about a stage and a half). Any
-// length is right; more than 512 requests take an even share.
-__device__ int split_stages(const WindowParams& p, int* found) {
-    const int lane = threadIdx.x & 31;
-    if (threadIdx.x < 32) {
-        long long total = 0;
-        int most = 0;
-        for (int r = lane; r < p.R; r += 32) {
-            const Request x = request_of(p, r);
-            if (x.m <= 0) continue;
-            total += (long long)p.Hkv * row_blocks(p, x) * key_stages(x);
-            most = max(most, key_stages(x));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        }
-        const int least = max(ceil_div(most, p.splits), 2);
-        const int even = (int)min((total + p.sms - 1) / p.sms, 1LL << 24);
-        int step = max(least, max(even / 4, 1));
-        if (p.R <= kFlatOneWarp) {
-            // lane i tries a share of (i + 1) / 32 of 1.5 times the even one
-            const int mine = max(least, (int)((long long)(lane + 1) * 3 * even / 64));
-            long long items = 0;
-            for (int r = 0; r < p.R; ++r) {
-                const Request x = request_of(p, r);
-                if (x.m > 0) items += (long long)p.Hkv * row_blocks(p, x) * ceil_div(key_stages(x), mine);
-            }
-            const long long rounds = (items + p.sms - 1) / p.sms;
-            long long cost = rounds * (2 * min(mine, max(most, 1)) + 3);
-            int best = mine;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const long long c = __shfl_xor_sync(0xffffffffu, cost, o);
-                const int s = __shfl_xor_sync(0xffffffffu, best, o);
-                if (c < cost || (c == cost && s < best)) {
-                    cost = c;
-                    best = s;
-                }
-            }
-            step = best;
-        }
-        if (lane == 0) *found = step;
+// The shares of kLse and kWindow. Their work lies end to end as units (request,
+// row block, head), each costing its products and its own start; block b of the
+// grid takes the cost from b to b + 1 shares, wherever that begins and ends
+// within a unit. So all blocks end together (whole splits of equal length, dealt
+// out, left some with a quarter more than the mean), and a row's keys are split
+// only where a share ends. Units and blocks both ascend along the work, so
+// u + b numbers the pairs that meet: the slots of partial log-sum-exps.
+//
+// The cost of kLse is in keys times row tiles, closed in form over a request's
+// row blocks: a prompt has thousands. (Stages round it up; a share may be off by
+// one.)
+constexpr int kUnitCost = 1050;   // X's copy, the pipeline's start, the first maximum, the last tiles' masks: 7,000
+                                  // clocks, where a tile of 256 keys takes 1,700
+constexpr int kUnitTiles = 2;     // kWindow: X's copy and the pipeline's start, in stages
+constexpr int kLeastCost = 1024, kLeastTiles = 6;  // of a share
+static_assert(kLeastCost > 4 * kKeys, "a share has part of a stage's end wherever it begins");
+
+__device__ __forceinline__ int block_tokens(const WindowParams& p) { return kRows / p.G; }
+// Row tiles of a request's last row block.
+__device__ __forceinline__ int last_tiles(const WindowParams& p, const Request& x) {
+    const int t = block_tokens(p), rest = x.m % t;
+    return rest > 0 && rest * p.G <= kKeys ? 1 : 2;
+}
+// Cost of one head's first k row blocks.
+__device__ __forceinline__ long long cost_before(const WindowParams& p, const Request& x, int k) {
+    const long long t = block_tokens(p), f = max(x.first, 0), full = min(k, x.m / (int)t);
+    long long v = full * (kUnitCost + 2 * f) + t * full * (full + 1);
+    if (k > full) v += kUnitCost + last_tiles(p, x) * (f + x.m);
+    return v;
+}
+// A unit: its cost from `at` on, `keys` cost units to a stage after `start`.
+struct Cost {
+    long long at, end;
+    int start, per, stages;
+    // the stage that the work up to c reaches
+    __device__ int reaches(long long c) const {
+        const long long q = c - at - start;
+        return q <= 0 ? 0 : (int)min((long long)stages, (q + per - 1) / per);
     }
-    __syncthreads();
-    return *found;
+};
+__device__ __forceinline__ Cost lse_cost(const WindowParams& p, const Request& x, int rb, int h, long long begin) {
+    Cost c;
+    const long long before = cost_before(p, x, rb), w = cost_before(p, x, rb + 1) - before;
+    c.at = begin + p.Hkv * before + h * w;
+    c.end = c.at + w;
+    c.start = kUnitCost;
+    c.per = 2 * kKeys * (rb == x.m / block_tokens(p) ? last_tiles(p, x) : 2);
+    c.stages = seen_stages(p, x, rb);
+    return c;
+}
+__device__ __forceinline__ int lse_unit(const WindowParams& p, const Request& x, int r, int rb, int h) {
+    // (q0 / tokens + r bounds the row blocks of the requests before)
+    return h + p.Hkv * (rb + x.q0 / block_tokens(p) + r);
+}
+template <int MODE>
+__device__ __forceinline__ long long request_cost(const WindowParams& p, int r) {
+    const Request x = request_of(p, r);
+    if (MODE == kLse) return x.m > 0 ? p.Hkv * cost_before(p, x, row_blocks(p, x)) : 0;
+    return x.m < 0 ? 0 : (long long)p.Hkv * (kUnitTiles + ceil_div(x.n, kKeys));
 }
 
 // One work item: X of xt tiles of 128 (0: the list is over), Y stages y0 .. y1-1.
 struct __align__(16) Item {
-    int r, h, xt, y0, y1, row0, split, pad;  // row0: the first query row (kLse) or key (kSum) of X
+    int r, h, xt, y0, y1, row0, slot, pad;  // row0: the first query row (kLse) or key (kSum) of X
     Request x;
 };
 static_assert(sizeof(Item) <= 64, "an item's place in shared memory");
 
-template <int MODE>
-__device__ __forceinline__ long long item_count(const WindowParams& p, int r, int step, int xkeys) {
+// kSum's items: 128 xkeys keys of a head.
+__device__ __forceinline__ long long sum_items(const WindowParams& p, int r, int xkeys) {
     const Request x = request_of(p, r);
-    if (MODE == kLse) return (long long)p.Hkv * row_blocks(p, x) * ceil_div(key_stages(x), step);
-    if (x.m < 0) return 0;
-    return (long long)p.Hkv * (MODE == kWindow ? ceil_div(key_stages(x), step) : ceil_div(x.n, xkeys * kKeys));
+    return x.m < 0 ? 0 : (long long)p.Hkv * ceil_div(x.n, xkeys * kKeys);
 }
-
-template <int MODE>
-__device__ __forceinline__ Item item_at(const WindowParams& p, const long long* sums, long long i, int step,
-                                        int xkeys) {
+__device__ __forceinline__ Item sum_item(const WindowParams& p, const long long* sums, long long i, int xkeys) {
     Item it;
     long long first;
-    it.r = flat_find(p.R, [&](int r) { return item_count<MODE>(p, r, step, xkeys); }, sums, i, first);
+    it.r = flat_find(p.R, [&](int r) { return sum_items(p, r, xkeys); }, sums, i, first);
     it.x = request_of(p, it.r);
-    const int o = (int)(i - first), rp = kRows / p.G * p.G, rows = it.x.m * p.G;
+    const int o = (int)(i - first), rp = block_tokens(p) * p.G;
     it.h = o % p.Hkv;
-    it.split = 0;
-    it.row0 = 0;
+    it.slot = 0;
+    it.row0 = o / p.Hkv * xkeys * kKeys;
+    it.xt = min(xkeys, ceil_div(it.x.n - it.row0, kKeys));
+    it.y0 = max(0, it.row0 - it.x.first) * p.G / rp;  // rows before it see none of the keys
+    it.y1 = max(it.y0, ceil_div(it.x.m * p.G, rp));
+    return it;
+}
+// The unit at cost `pos`, as far as the share that ends at `stop` goes; `pos`
+// moves to its end.
+template <int MODE>
+__device__ __forceinline__ Item share_item(const WindowParams& p, const long long* sums, long long& pos, long long stop) {
+    Item it;
+    long long first;
+    it.r = flat_find(p.R, [&](int r) { return request_cost<MODE>(p, r); }, sums, pos, first);
+    it.x = request_of(p, it.r);
+    Cost c;
     if (MODE == kLse) {
-        const int blocks = row_blocks(p, it.x), rb = blocks - 1 - o / p.Hkv % blocks;  // the longest first
-        it.split = o / p.Hkv / blocks;
-        it.row0 = rb * rp;
-        it.xt = rows - it.row0 > kKeys ? 2 : 1;
-        it.y0 = it.split * step;
-        it.y1 = min(it.y0 + step, seen_stages(p, it.x, rb));
-    } else if (MODE == kWindow) {
-        it.xt = 1;
-        it.y0 = o / p.Hkv * step * 2;
-        it.y1 = min(it.y0 + step * 2, ceil_div(it.x.n, kKeys));
+        int lo = 0, hi = row_blocks(p, it.x);
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first + p.Hkv * cost_before(p, it.x, mid) <= pos) lo = mid;
+            else hi = mid;
+        }
+        c = lse_cost(p, it.x, lo, 0, first);
+        it.h = (int)((pos - c.at) / (c.end - c.at));
+        c = lse_cost(p, it.x, lo, it.h, first);
+        it.row0 = lo * block_tokens(p) * p.G;
+        it.xt = it.x.m * p.G - it.row0 > kKeys ? 2 : 1;
+        it.slot = lse_unit(p, it.x, it.r, lo, it.h) + (int)blockIdx.x;
     } else {
-        it.row0 = o / p.Hkv * xkeys * kKeys;
-        it.xt = min(xkeys, ceil_div(it.x.n - it.row0, kKeys));
-        it.y0 = max(0, it.row0 - it.x.first) * p.G / rp;  // rows before it see none of the keys
-        it.y1 = max(it.y0, ceil_div(rows, rp));
+        c.start = kUnitTiles;
+        c.per = 1;
+        c.stages = ceil_div(it.x.n, kKeys);
+        const int w = c.start + c.stages;
+        it.h = (int)((pos - first) / w);
+        c.at = first + (long long)it.h * w;
+        c.end = c.at + w;
+        it.row0 = it.slot = 0;
+        it.xt = 1;
     }
+    it.y0 = c.reaches(pos);
+    it.y1 = c.reaches(min(stop, c.end));
+    pos = c.end;
     return it;
 }
 
@@ -244,6 +272,92 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+// f(x, q) for the two chunks of 32 columns of a warp's quarter at ts, the second
+// loaded under the arithmetic of the first; done() once both are in registers.
+template <typename F, typename D>
+__device__ __forceinline__ void sweep(uint32_t ts, F f, D done) {
+    uint32_t xa[32], xb[32];
+    tc::ld32(ts, xa);
+    tc::wait_ld();
+    tc::ld32(ts + 32u, xb);
+    f(xa, 0);
+    tc::wait_ld();
+    done();
+    f(xb, 1);
+}
+
+// Columns outside lo .. hi - 1 of a chunk take the value `off`.
+__device__ __forceinline__ void cut(uint32_t (&x)[32], int lo, int hi, float off) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        if (c < lo || c >= hi) x[c] = __float_as_uint(off);
+}
+
+// acc += 2^(x sc2 + b) over a chunk.
+__device__ __forceinline__ void add_chunk(const uint32_t (&x)[32], uint64_t sc2, uint64_t b, uint64_t (&acc)[4]) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const uint64_t a = tc::fma2(tc::f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, b);
+        acc[c & 3] = tc::add2(acc[c & 3], tc::f2(ex2(tc::f2_lo(a)), ex2(tc::f2_hi(a))));
+    }
+}
+// As above with b the 32 values at shared address la.
+__device__ __forceinline__ void add_chunk_rows(const uint32_t (&x)[32], uint64_t sc2, uint32_t la, uint64_t (&acc)[4]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint32_t l0, l1, l2, l3;
+        lds128(la + 16 * c, l0, l1, l2, l3);
+        const uint64_t a0 = tc::fma2(tc::f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sc2,
+                                     tc::f2(__uint_as_float(l0), __uint_as_float(l1)));
+        const uint64_t a1 = tc::fma2(tc::f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sc2,
+                                     tc::f2(__uint_as_float(l2), __uint_as_float(l3)));
+        acc[(2 * c) & 3] = tc::add2(acc[(2 * c) & 3], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
+        acc[(2 * c + 1) & 3] = tc::add2(acc[(2 * c + 1) & 3], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
+    }
+}
+__device__ __forceinline__ float total_of(const uint64_t (&acc)[4]) {
+    const uint64_t a = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
+    return tc::f2_lo(a) + tc::f2_hi(a);
+}
+
+// The sweeps that few tiles need (a mask, a first maximum) are functions of
+// their own: inlined, the mask's selects and their registers slowed the plain
+// sweep by a fifth. `have`: bit i: the quarter's columns 16 i .. + 15 hold keys;
+// the row sees columns below `hi`.
+__device__ __noinline__ float masked_top(uint32_t ts, uint32_t have, int hi, bool highest) {
+    const float off = highest ? -INFINITY : INFINITY;
+    float e4[4] = {off, off, off, off};
+    sweep(ts, [&](uint32_t (&x)[32], int q) {
+        const uint32_t two = have >> (2 * q);
+        cut(x, two & 1u ? 0 : 16, two & 2u ? hi - 32 * q : min(hi - 32 * q, 16), off);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            e4[c & 3] = highest ? fmaxf(e4[c & 3], __uint_as_float(x[c])) : fminf(e4[c & 3], __uint_as_float(x[c]));
+    }, [] {});
+    return highest ? fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])) : fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
+}
+__device__ __noinline__ float masked_keys(uint32_t ts, uint32_t have, int hi, float sl2, float nu) {
+    const float off = sl2 > 0.f ? -INFINITY : INFINITY;
+    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+    sweep(ts, [&](uint32_t (&x)[32], int q) {
+        const uint32_t two = have >> (2 * q);
+        cut(x, two & 1u ? 0 : 16, two & 2u ? hi - 32 * q : min(hi - 32 * q, 16), off);
+        add_chunk(x, tc::f2(sl2, sl2), tc::f2(nu, nu), acc);
+    }, [] {});
+    return total_of(acc);
+}
+// Columns from `first` on see the thread's key, `cols` hold rows.
+__device__ __noinline__ float masked_rows(uint32_t ts, uint32_t la, int first, int cols, float sl2) {
+    const float off = sl2 > 0.f ? -INFINITY : INFINITY;
+    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+    sweep(ts, [&](uint32_t (&x)[32], int q) {
+        if (32 * q >= cols) return;
+        cut(x, first - 32 * q, cols - 32 * q, off);
+        add_chunk_rows(x, tc::f2(sl2, sl2), la + 128 * q, acc);
+    }, [] {});
+    return total_of(acc);
 }
 
 template <int HD, int MODE>
@@ -304,10 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
 
     // ---------------------------------------------------------- the plan --
-    long long total = 0;
-    int step = 0, xkeys = 2;
+    long long total = 0, pos = 0, stop = 0;
+    int xkeys = 2;
+    bool ascend = true;
     if (MODE == kLse) {
-        const bool ascend = starts_ascend(p.query_start, p.R, p.T);
+        ascend = starts_ascend(p.query_start, p.R, p.T);
         const int g = blockIdx.x * kThreads + threadIdx.x;
         if (!ascend && g == 0) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
         for (int r = g; ascend && r < p.R; r += gridDim.x * kThreads) {
@@ -315,19 +430,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x.m < 0 || x.m > x.n) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
             if (__ldg(p.lens + r) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
         }
-        if (ascend) step = split_stages(p, reinterpret_cast<int*>(base + SM::kMask));
-        if (g == 0) p.next[1] = (unsigned int)step;
+        if (!ascend && g == 0) p.begin[p.R] = 0;
     } else {
-        step = (int)__ldcg(p.next + 1);
+        ascend = __ldcg(p.begin + p.R) != 0;
     }
-    if (step > 0) {
-        auto items = [&](int r) { return item_count<MODE>(p, r, step, xkeys); };
-        total = flat_scan(p.R, items, sums);
-        if (MODE == kSum && total < 2LL * p.sms) {
+    if (ascend && MODE == kSum) {
+        total = flat_scan(p.R, [&](int r) { return sum_items(p, r, xkeys); }, sums);
+        if (total < 2LL * gridDim.x) {
             // 128 keys an item while 256 would leave SMs with few
             xkeys = 1;
             __syncthreads();
-            total = flat_scan(p.R, items, sums);
+            total = flat_scan(p.R, [&](int r) { return sum_items(p, r, xkeys); }, sums);
+        }
+    } else if (ascend) {
+        auto cost = [&](int r) { return request_cost<MODE>(p, r); };
+        total = flat_scan(p.R, cost, sums);
+        const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)(MODE == kLse ? kLeastCost : kLeastTiles));
+        pos = blockIdx.x * share;
+        stop = min(pos + share, total);
+        if (MODE == kLse) {
+            for (int r = blockIdx.x + gridDim.x * threadIdx.x; r < p.R; r += gridDim.x * kThreads)
+                p.begin[r] = flat_before(p.R, cost, sums, r);
+            if (blockIdx.x == 0 && threadIdx.x == 0) p.begin[p.R] = share;
         }
     }
     const int rp = kRows / p.G * p.G;
@@ -375,26 +499,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        // kLse and kWindow deal the list out back and forth (it goes from long
-        // to short); kSum's items are taken from a counter as blocks get free
-        auto pick = [&](long long k) -> long long {
-            if (MODE != kSum) return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            unsigned int i = 0;
-            if (lane == 0) i = atomicAdd(p.next, 1u);
-            return (long long)__shfl_sync(0xffffffffu, i, 0);
-        };
-        long long k = 0, i = pick(0);
-        uint32_t ic = 0;
-        for (;;) {
+        // kSum's items (of very different lengths, the longest first) are taken
+        // from a counter, each when the last stage of the one before is out:
+        // taken earlier, long ones wait behind others (a third of the time)
+        auto pick = [&]() -> Item {
             Item it;
             it.xt = 0;
-            if (i < total) {
-                it = item_at<MODE>(p, sums, i, step, xkeys);
-                if (MODE == kLse && it.y0 >= it.y1) {  // keys past what the rows see
-                    i = pick(++k);
-                    continue;
+            if (MODE == kSum) {
+                unsigned int i = 0;
+                if (lane == 0) i = atomicAdd(p.next, 1u);
+                i = __shfl_sync(0xffffffffu, i, 0);
+                if (i < total) it = sum_item(p, sums, i, xkeys);
+            } else {
+                while (pos < stop) {
+                    it = share_item<MODE>(p, sums, pos, stop);
+                    if (it.y0 < it.y1) break;
+                    it.xt = 0;
                 }
             }
+            return it;
+        };
+        uint32_t ic = 0;
+        for (;;) {
+            const Item it = pick();
             const uint32_t sl = ic % kItemSlots;
             if (!(ok = wait_warp(i_empty + 8 * sl, ((ic / kItemSlots) & 1) ^ 1, p.wait_ns))) break;
             if (lane == 0) {
@@ -404,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++ic;
             if (it.xt == 0) break;
-            i = pick(++k);
             if (it.y0 >= it.y1) continue;
             // X goes out at the latest before a wait for Y's ring: an item's
             // first Y stages may land while the last item still holds X
@@ -529,36 +655,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts0 = tbase + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
         const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
         const bool pos_scale = p.sl2 > 0.f;
-        const float off_value = pos_scale ? -INFINITY : INFINITY;  // a masked logit, before the scale
         uint32_t yc = 0, sc = 0;
         bool ok = true;
-        // Columns lo .. hi - 1 of a chunk count. The empty statement keeps the
-        // masked loops apart from the plain ones: merged into one, with the
-        // mask as selects on every logit, they took a fifth longer.
-        auto cut = [&](uint32_t (&x)[32], int lo, int hi) {
-            asm volatile("" ::: "memory");
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-                if (c < lo || c >= hi) x[c] = __float_as_uint(off_value);
-        };
         auto give_back = [&](uint32_t b) {
             tc::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_empty + 8 * b);
-        };
-        // f(x, q) for the two chunks of 32 columns, the second loaded under the
-        // arithmetic of the first; with `give` the tile is handed back as soon
-        // as it is in registers
-        auto sweep = [&](uint32_t b, bool give, auto f) {
-            uint32_t xa[32], xb[32];
-            const uint32_t ts = ts0 + b * kRows;
-            tc::ld32(ts, xa);
-            tc::wait_ld();
-            tc::ld32(ts + 32u, xb);
-            f(xa, 0);
-            tc::wait_ld();
-            if (give) give_back(b);
-            f(xb, 1);
         };
         for (uint32_t ic = 0;; ++ic) {
             Item it;
@@ -604,20 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t b = sc & 1;
                     if (!(ok = wait_warp(s_full + 8 * b, (sc >> 1) & 1, p.wait_ns))) continue;
                     tc::fence_after();
-                    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-                    auto total = [&]() {
-                        const uint64_t a = tc::add2(tc::add2(acc[0], acc[1]), tc::add2(acc[2], acc[3]));
-                        return tc::f2_lo(a) + tc::f2_hi(a);
-                    };
+                    const uint32_t ts = ts0 + b * kRows;
+                    float got = 0.f;  // the tile's sum
                     if (MODE == kLse) {
                         const int key0 = j * 2 * kKeys + col0;
                         const uint32_t msk = (lds32(mask0 + (yc % kMaskSlots) * 4) >> (4 * quarter)) & 0xFu;
                         const bool part = __any_sync(0xffffffffu, msk != 0xFu || key0 + 63 > bound[t]);
-                        auto mask = [&](uint32_t (&x)[32], int q) {
-                            const uint32_t have = (msk >> (2 * q)) & 3u;
-                            const int hi = bound[t] - (key0 + 32 * q) + 1;
-                            cut(x, have & 1u ? 0 : 16, have & 2u ? hi : min(hi, 16));
-                        };
+                        const int hi = bound[t] - key0 + 1;
                         // The sum is relative to m, the largest of the first
                         // tile's logits: fp32 holds it however far later ones
                         // lie below, and above until it nears overflow. Only
@@ -626,35 +721,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bool top = __any_sync(0xffffffffu, m[t] == -INFINITY);
                         for (;;) {
                             if (top) {
-                                float e4[4] = {off_value, off_value, off_value, off_value};
-                                sweep(b, false, [&](uint32_t (&x)[32], int q) {
-                                    if (part) mask(x, q);
-#pragma unroll
-                                    for (int c = 0; c < 32; ++c)
-                                        e4[c & 3] = pos_scale ? fmaxf(e4[c & 3], __uint_as_float(x[c]))
-                                                              : fminf(e4[c & 3], __uint_as_float(x[c]));
-                                });
-                                const float best = (pos_scale ? fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3]))
-                                                              : fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]))) * p.sl2;
+                                const float best = masked_top(ts, msk, hi, pos_scale) * p.sl2;
                                 sum[t] *= best > m[t] ? ex2(m[t] - best) : 1.f;
                                 m[t] = fmaxf(m[t], best);
                             }
                             const float nu = m[t] == -INFINITY ? 0.f : -m[t];
-                            const uint64_t nu2 = tc::f2(nu, nu);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) acc[c] = 0ull;
-                            auto add = [&](uint32_t (&x)[32]) {
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) {
-                                    const uint64_t a = tc::fma2(tc::f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nu2);
-                                    acc[c & 3] = tc::add2(acc[c & 3], tc::f2(ex2(tc::f2_lo(a)), ex2(tc::f2_hi(a))));
-                                }
-                            };
-                            if (part)
-                                sweep(b, false, [&](uint32_t (&x)[32], int q) { mask(x, q); add(x); });
-                            else
-                                sweep(b, false, [&](uint32_t (&x)[32], int) { add(x); });
-                            const float now = sum[t] + total();
+                            if (part) {
+                                got = masked_keys(ts, msk, hi, p.sl2, nu);
+                            } else {
+                                const uint64_t nu2 = tc::f2(nu, nu);
+                                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                                sweep(ts, [&](uint32_t (&x)[32], int) { add_chunk(x, sc2, nu2, acc); }, [] {});
+                                got = total_of(acc);
+                            }
+                            const float now = sum[t] + got;
                             if (top || !__any_sync(0xffffffffu, now > 0x1p100f)) {
                                 sum[t] = now;
                                 break;
@@ -671,30 +751,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int first = (MODE == kSum ? bound[t] : (key - it.x.first) * p.G) - row0;
                         const bool part = __any_sync(0xffffffffu, first > 0) || cols < 64;
                         const uint32_t la = sbase + SM::kLses + (((MODE == kSum ? yc : ic) % kLseSlots) * kRows + col0) * 4;
-                        auto add = [&](uint32_t (&x)[32], int q) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                uint32_t l0, l1, l2, l3;
-                                lds128(la + 128 * q + 16 * c, l0, l1, l2, l3);
-                                const uint64_t a0 = tc::fma2(tc::f2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), sc2,
-                                                             tc::f2(__uint_as_float(l0), __uint_as_float(l1)));
-                                const uint64_t a1 = tc::fma2(tc::f2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), sc2,
-                                                             tc::f2(__uint_as_float(l2), __uint_as_float(l3)));
-                                acc[(2 * c) & 3] = tc::add2(acc[(2 * c) & 3], tc::f2(ex2(tc::f2_lo(a0)), ex2(tc::f2_hi(a0))));
-                                acc[(2 * c + 1) & 3] = tc::add2(acc[(2 * c + 1) & 3], tc::f2(ex2(tc::f2_lo(a1)), ex2(tc::f2_hi(a1))));
-                            }
-                        };
-                        if (cols <= 0)
+                        if (cols <= 0) {
                             give_back(b);
-                        else if (part)
-                            sweep(b, true, [&](uint32_t (&x)[32], int q) {
-                                if (32 * q >= cols) return;
-                                cut(x, first - 32 * q, cols - 32 * q);
-                                add(x, q);
-                            });
-                        else
-                            sweep(b, true, [&](uint32_t (&x)[32], int q) { add(x, q); });
-                        if (MODE == kSum) sum[t] += total();
+                        } else if (part) {
+                            got = masked_rows(ts, la, first, cols, p.sl2);
+                            give_back(b);
+                        } else {
+                            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                            sweep(ts, [&](uint32_t (&x)[32], int q) { add_chunk_rows(x, sc2, la + 128 * q, acc); },
+                                  [&] { give_back(b); });  // as soon as it is in registers
+                            got = total_of(acc);
+                        }
+                        if (MODE == kSum) sum[t] += got;
                     }
                     if (MODE == kWindow) {
                         // the other quarters hand their sums to the first one
@@ -704,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // once it is done with this place
                         const int place = (int)(sc & 3);
                         float* comb = reinterpret_cast<float*>(base + SM::kComb) + place * 3 * kKeys;
-                        float w = total();
+                        float w = got;
                         if (quarter > 0) {
                             comb[(quarter - 1) * kKeys + my] = w;
                             __syncwarp();
@@ -752,8 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float v = M == -INFINITY ? 0.f : M;
                     const float l = (q[0].y * exp2f(q[0].x - v) + q[1].y * exp2f(q[1].x - v)) +
                                     (q[2].y * exp2f(q[2].x - v) + q[3].y * exp2f(q[3].x - v));
-                    const int rho = it.row0 + t * kKeys + my;
-                    p.part[((long long)(it.x.q0 + rho / p.G) * p.Hq + (long long)it.h * p.G + rho % p.G) * p.splits + it.split] =
+                    p.part[(long long)it.slot * kRows + t * kKeys + my] =
                         l == 0.f ? -INFINITY : M + log2f(l);
                 } else {
                     const float w = (q[0].y + q[1].y) + (q[2].y + q[3].y);
@@ -776,17 +843,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Each row's log-sum-exp from its splits (one launch between the two: the
-// second reads every row once per 256 keys), and kSum's item counter back to
-// zero. A thread merges one row.
+// Each row's log-sum-exp from the blocks that had keys of it (one launch between
+// the two: the second reads every row once per 256 keys), and kSum's item
+// counter back to zero. A thread merges one row.
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p) {
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0u;
-    const int step = (int)__ldcg(p.next + 1);
-    if (step == 0) return;
+    const long long share = __ldcg(p.begin + p.R);
+    if (share == 0) return;
     const long long row = (long long)blockIdx.x * kMergeThreads + threadIdx.x;
-    const int i = (int)(row / p.Hq);
+    const int i = (int)(row / p.Hq), j = (int)(row % p.Hq);
     if (i < __ldg(p.query_start) || i >= __ldg(p.query_start + p.R)) return;
     int lo = 0, hi = p.R;  // query_start[lo] <= i < query_start[hi]
     while (hi - lo > 1) {
@@ -796,30 +863,34 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Windo
     }
     const Request x = request_of(p, lo);
     if (x.m < 0) return;
-    const int n = ceil_div(seen_stages(p, x, (i - x.q0) / (kRows / p.G)), step);
-    const float* at = p.part + row * p.splits;
+    const int rb = (i - x.q0) / block_tokens(p), h = j / p.G;
+    const Cost c = lse_cost(p, x, rb, h, __ldcg(p.begin + lo));
+    // the blocks of its first and last stage; all between have some (a share is
+    // longer than a stage)
+    const int b0 = (int)((c.at + c.start) / share);
+    const int n = c.stages > 0 ? (int)((c.at + c.start + (c.stages - 1LL) * c.per) / share) - b0 + 1 : 0;
+    const float* at = p.part + (long long)(lse_unit(p, x, lo, rb, h) + b0) * kRows +
+                      (i - x.q0 - rb * block_tokens(p)) * p.G + j % p.G;
     float M = -INFINITY, sum = 0.f;
 #pragma unroll 8
-    for (int s = 0; s < n; ++s) M = fmaxf(M, __ldcg(at + s));
+    for (int s = 0; s < n; ++s) M = fmaxf(M, __ldcg(at + s * kRows));
 #pragma unroll 8
     for (int s = 0; s < n; ++s) {
-        const float v = __ldcg(at + s);
+        const float v = __ldcg(at + s * kRows);
         sum += v == -INFINITY ? 0.f : exp2f(v - M);
     }
-    p.nlse[((long long)(row % p.Hq / p.G) * p.T + i) * p.G + row % p.G] = sum == 0.f ? -INFINITY : -(M + log2f(sum));
+    p.nlse[((long long)h * p.T + i) * p.G + j % p.G] = sum == 0.f ? -INFINITY : -(M + log2f(sum));
 }
 
-// Places for partial log-sum-exps per row: enough splits that few row tiles
-// still fill the GPU, fewer where the rows themselves are many.
-int split_places(const mi_dims& D, int32_t total_q) {
-    const long long rows = (long long)total_q * D.Hq;
-    return rows <= (1LL << 20) ? 32 : rows <= (1LL << 23) ? 8 : 2;
-}
+constexpr int kMostBlocks = 256;  // of the grid, whatever the device has
 
 size_t lse_bytes(const mi_dims& D, int32_t total_q) { return ((size_t)total_q * D.Hq * 4 + 255) / 256 * 256; }
 
+size_t begin_bytes(const mi_dims& D) { return ((size_t)(D.B + 1) * 8 + 255) / 256 * 256; }
+
 size_t window_bytes(const mi_dims& D, int32_t total_q) {
-    return lse_bytes(D, total_q) * (1 + split_places(D, total_q)) + 256;
+    const size_t blocks = (size_t)total_q / (kRows / (D.Hq / D.Hkv)) + D.B;
+    return 256 + begin_bytes(D) + lse_bytes(D, total_q) + (D.Hkv * blocks + kMostBlocks) * kRows * 4;
 }
 
 bool window_sizes_ok(const mi_dims& D, int32_t total_q, int32_t max_query_len) {
@@ -832,7 +903,7 @@ bool launch_window(const CUtensorMap& tq, const CUtensorMap& tk, const WindowPar
     static std::mutex mu;
     static CUcontext done[256] = {};
     if (!raise_smem(reinterpret_cast<const void*>(window_kernel<HD, MODE>), WinSmem<HD, MODE>::kTotal, done, mu)) return false;
-    return launch_pdl(window_kernel<HD, MODE>, p.sms, kThreads, WinSmem<HD, MODE>::kTotal, st, tq, tk, p) == cudaSuccess;
+    return launch_pdl(window_kernel<HD, MODE>, p.grid, kThreads, WinSmem<HD, MODE>::kTotal, st, tq, tk, p) == cudaSuccess;
 }
 
 }  // namespace
@@ -868,8 +939,10 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     p.lens = context_lens;
     p.query_start = query_start;
     p.next = static_cast<unsigned int*>(workspace);
-    p.nlse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
-    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256 + lse_bytes(D, total_q));
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + 256;
+    p.begin = reinterpret_cast<long long*>(ws);
+    p.nlse = reinterpret_cast<float*>(ws += begin_bytes(D));
+    p.part = reinterpret_cast<float*>(ws + lse_bytes(D, total_q));
     p.scores = scores;
     p.dev_err = dev_err;
     p.R = D.B;
@@ -882,8 +955,7 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     p.max_q = max_query_len;
     p.fresh = fresh != 0;
     p.xt = 0;
-    p.splits = split_places(D, total_q);
-    p.sms = sms;
+    p.grid = sms < kMostBlocks ? sms : kMostBlocks;
     p.sl2 = scale * 1.4426950408889634f;
     // a scale of 0 weighs every key the same, and so does one that leaves
     // every logit far below 2^-24 (a masked logit times 0 would be NaN)

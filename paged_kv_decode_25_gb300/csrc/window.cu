@@ -211,44 +211,68 @@ __device__ __forceinline__ Item sum_item(const WindowParams& p, const long long*
     it.y1 = max(it.y0, ceil_div(it.x.m * p.G, rp));
     return it;
 }
-// The unit at cost `pos`, as far as the share that ends at `stop` goes; `pos`
-// moves to its end.
+// A share's units in order, from the one at cost `pos` on.
 template <int MODE>
-__device__ __forceinline__ Item share_item(const WindowParams& p, const long long* sums, long long& pos, long long stop) {
+struct Units {
     Item it;
-    long long first;
-    it.r = flat_find(p.R, [&](int r) { return request_cost<MODE>(p, r); }, sums, pos, first);
-    it.x = request_of(p, it.r);
     Cost c;
-    if (MODE == kLse) {
-        int lo = 0, hi = row_blocks(p, it.x);
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (first + p.Hkv * cost_before(p, it.x, mid) <= pos) lo = mid;
-            else hi = mid;
+    long long first;  // the cost before the request
+    int rb;
+
+    __device__ __forceinline__ void row_block(const WindowParams& p, int h) {
+        it.h = h;
+        if (MODE == kLse) {
+            c = lse_cost(p, it.x, rb, h, first);
+            it.row0 = rb * block_tokens(p) * p.G;
+            it.xt = it.x.m * p.G - it.row0 > kKeys ? 2 : 1;
+        } else {
+            const int w = kUnitTiles + ceil_div(it.x.n, kKeys);
+            c.at = first + (long long)h * w;
+            c.end = c.at + w;
+            c.start = kUnitTiles;
+            c.per = 1;
+            c.stages = w - kUnitTiles;
+            it.row0 = it.slot = 0;
+            it.xt = 1;
         }
-        c = lse_cost(p, it.x, lo, 0, first);
-        it.h = (int)((pos - c.at) / (c.end - c.at));
-        c = lse_cost(p, it.x, lo, it.h, first);
-        it.row0 = lo * block_tokens(p) * p.G;
-        it.xt = it.x.m * p.G - it.row0 > kKeys ? 2 : 1;
-        it.slot = lse_unit(p, it.x, it.r, lo, it.h) + (int)blockIdx.x;
-    } else {
-        c.start = kUnitTiles;
-        c.per = 1;
-        c.stages = ceil_div(it.x.n, kKeys);
-        const int w = c.start + c.stages;
-        it.h = (int)((pos - first) / w);
-        c.at = first + (long long)it.h * w;
-        c.end = c.at + w;
-        it.row0 = it.slot = 0;
-        it.xt = 1;
     }
-    it.y0 = c.reaches(pos);
-    it.y1 = c.reaches(min(stop, c.end));
-    pos = c.end;
-    return it;
-}
+    __device__ __forceinline__ void seek(const WindowParams& p, const long long* sums, long long pos) {
+        it.r = flat_find(p.R, [&](int r) { return request_cost<MODE>(p, r); }, sums, pos, first);
+        it.x = request_of(p, it.r);
+        rb = 0;
+        if (MODE == kLse) {
+            int hi = row_blocks(p, it.x);
+            while (hi - rb > 1) {
+                const int mid = (rb + hi) >> 1;
+                if (first + p.Hkv * cost_before(p, it.x, mid) <= pos) rb = mid;
+                else hi = mid;
+            }
+        }
+        row_block(p, 0);
+        const int h = (int)((pos - c.at) / (c.end - c.at));
+        if (h > 0) row_block(p, h);
+    }
+    // The unit's stages up to the share's end.
+    __device__ __forceinline__ void stages(const WindowParams& p, long long pos, long long stop) {
+        it.y0 = c.reaches(pos);
+        it.y1 = c.reaches(min(stop, c.end));
+        if (MODE == kLse) it.slot = lse_unit(p, it.x, it.r, rb, it.h) + (int)blockIdx.x;
+    }
+    // The next unit, which begins where this one ends (before the share does).
+    __device__ __forceinline__ void advance(const WindowParams& p, const long long* sums) {
+        const long long w = c.end - c.at;
+        if (it.h + 1 < p.Hkv) {
+            ++it.h;
+            c.at = c.end;
+            c.end += w;
+        } else if (MODE == kLse && rb + 1 < row_blocks(p, it.x)) {
+            ++rb;
+            row_block(p, 0);
+        } else {
+            seek(p, sums, c.end);
+        }
+    }
+};
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit_ns) {
     // One vote decides the common case for the whole warp: a branch on each
@@ -288,11 +312,28 @@ __device__ __forceinline__ void sweep(uint32_t ts, F f, D done) {
     f(xb, 1);
 }
 
-// Columns outside lo .. hi - 1 of a chunk take the value `off`.
-__device__ __forceinline__ void cut(uint32_t (&x)[32], int lo, int hi, float off) {
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n > 0 ? (1u << n) - 1u : 0u; }
+// Columns of a chunk without their bit in `keep` take the value `off`.
+__device__ __forceinline__ void cut(uint32_t (&x)[32], uint32_t keep, float off) {
 #pragma unroll
     for (int c = 0; c < 32; ++c)
-        if (c < lo || c >= hi) x[c] = __float_as_uint(off);
+        if (!(keep & (1u << c))) x[c] = __float_as_uint(off);
+}
+// kLse: bit i of `have`: the quarter's columns 16 i .. + 15 hold keys; the row
+// sees columns below `hi`. The columns of chunk q that count.
+__device__ __forceinline__ uint32_t seen_columns(uint32_t have, int hi, int q) {
+    const uint32_t two = have >> (2 * q);
+    return low_bits(hi - 32 * q) & ((two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u));
+}
+template <bool HIGHEST>
+__device__ __forceinline__ float chunk_top(const uint32_t (&x)[32]) {
+    auto pick = [](float a, float b) { return HIGHEST ? fmaxf(a, b) : fminf(a, b); };
+    float e4[4];
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        e4[c & 3] = c < 4 ? __uint_as_float(x[c]) : pick(e4[c & 3], __uint_as_float(x[c]));
+    return pick(pick(e4[0], e4[1]), pick(e4[2], e4[3]));
 }
 
 // acc += 2^(x sc2 + b) over a chunk.
@@ -324,29 +365,38 @@ __device__ __forceinline__ float total_of(const uint64_t (&acc)[4]) {
 
 // The sweeps that few tiles need (a mask, a first maximum) are functions of
 // their own: inlined, the mask's selects and their registers slowed the plain
-// sweep by a fifth. `have`: bit i: the quarter's columns 16 i .. + 15 hold keys;
-// the row sees columns below `hi`.
-__device__ __noinline__ float masked_top(uint32_t ts, uint32_t have, int hi, bool highest) {
-    const float off = highest ? -INFINITY : INFINITY;
-    float e4[4] = {off, off, off, off};
+// sweep by a fifth.
+__device__ __noinline__ float masked_top(uint32_t ts, uint32_t have, int hi, float sl2) {
+    const float off = sl2 > 0.f ? -INFINITY : INFINITY;
+    float best = off;
     sweep(ts, [&](uint32_t (&x)[32], int q) {
-        const uint32_t two = have >> (2 * q);
-        cut(x, two & 1u ? 0 : 16, two & 2u ? hi - 32 * q : min(hi - 32 * q, 16), off);
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-            e4[c & 3] = highest ? fmaxf(e4[c & 3], __uint_as_float(x[c])) : fminf(e4[c & 3], __uint_as_float(x[c]));
+        cut(x, seen_columns(have, hi, q), off);
+        best = sl2 > 0.f ? fmaxf(best, chunk_top<true>(x)) : fminf(best, chunk_top<false>(x));
     }, [] {});
-    return highest ? fmaxf(fmaxf(e4[0], e4[1]), fmaxf(e4[2], e4[3])) : fminf(fminf(e4[0], e4[1]), fminf(e4[2], e4[3]));
+    return best * sl2;
 }
 __device__ __noinline__ float masked_keys(uint32_t ts, uint32_t have, int hi, float sl2, float nu) {
     const float off = sl2 > 0.f ? -INFINITY : INFINITY;
     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
     sweep(ts, [&](uint32_t (&x)[32], int q) {
-        const uint32_t two = have >> (2 * q);
-        cut(x, two & 1u ? 0 : 16, two & 2u ? hi - 32 * q : min(hi - 32 * q, 16), off);
+        cut(x, seen_columns(have, hi, q), off);
         add_chunk(x, tc::f2(sl2, sl2), tc::f2(nu, nu), acc);
     }, [] {});
     return total_of(acc);
+}
+// A row's first tile: {m, the sum relative to 2^m}. A row without an m takes the
+// largest logit of the first 32 columns, or of the others where those hold none
+// of it.
+__device__ __noinline__ float2 first_keys(uint32_t ts, uint32_t have, int hi, float sl2, float m) {
+    const float off = sl2 > 0.f ? -INFINITY : INFINITY;
+    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+    sweep(ts, [&](uint32_t (&x)[32], int q) {
+        cut(x, seen_columns(have, hi, q), off);
+        if (m == -INFINITY) m = (sl2 > 0.f ? chunk_top<true>(x) : chunk_top<false>(x)) * sl2;
+        const float nu = m == -INFINITY ? 0.f : -m;
+        add_chunk(x, tc::f2(sl2, sl2), tc::f2(nu, nu), acc);
+    }, [] {});
+    return make_float2(m, total_of(acc));
 }
 // Columns from `first` on see the thread's key, `cols` hold rows.
 __device__ __noinline__ float masked_rows(uint32_t ts, uint32_t la, int first, int cols, float sl2) {
@@ -354,7 +404,7 @@ __device__ __noinline__ float masked_rows(uint32_t ts, uint32_t la, int first, i
     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
     sweep(ts, [&](uint32_t (&x)[32], int q) {
         if (32 * q >= cols) return;
-        cut(x, first - 32 * q, cols - 32 * q, off);
+        cut(x, low_bits(cols - 32 * q) & ~low_bits(first - 32 * q), off);
         add_chunk_rows(x, tc::f2(sl2, sl2), la + 128 * q, acc);
     }, [] {});
     return total_of(acc);
@@ -502,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // kSum's items (of very different lengths, the longest first) are taken
         // from a counter, each when the last stage of the one before is out:
         // taken earlier, long ones wait behind others (a third of the time)
+        Units<MODE> units;
+        units.c.end = -1;  // none yet
         auto pick = [&]() -> Item {
             Item it;
             it.xt = 0;
@@ -512,9 +564,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i < total) it = sum_item(p, sums, i, xkeys);
             } else {
                 while (pos < stop) {
-                    it = share_item<MODE>(p, sums, pos, stop);
-                    if (it.y0 < it.y1) break;
-                    it.xt = 0;
+                    if (units.c.end < 0) units.seek(p, sums, pos);
+                    else units.advance(p, sums);
+                    units.stages(p, pos, stop);
+                    pos = units.c.end;
+                    if (units.it.y0 < units.it.y1) {
+                        it = units.it;
+                        break;
+                    }
                 }
             }
             return it;
@@ -654,7 +711,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int col0 = quarter * 64;    // of this warp's columns
         const uint32_t ts0 = tbase + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
         const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
-        const bool pos_scale = p.sl2 > 0.f;
         uint32_t yc = 0, sc = 0;
         bool ok = true;
         auto give_back = [&](uint32_t b) {
@@ -713,34 +769,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t msk = (lds32(mask0 + (yc % kMaskSlots) * 4) >> (4 * quarter)) & 0xFu;
                         const bool part = __any_sync(0xffffffffu, msk != 0xFu || key0 + 63 > bound[t]);
                         const int hi = bound[t] - key0 + 1;
-                        // The sum is relative to m, the largest of the first
-                        // tile's logits: fp32 holds it however far later ones
-                        // lie below, and above until it nears overflow. Only
-                        // then, and at first, is a maximum taken and the sum
-                        // moved to it.
-                        bool top = __any_sync(0xffffffffu, m[t] == -INFINITY);
-                        for (;;) {
-                            if (top) {
-                                const float best = masked_top(ts, msk, hi, pos_scale) * p.sl2;
-                                sum[t] *= best > m[t] ? ex2(m[t] - best) : 1.f;
-                                m[t] = fmaxf(m[t], best);
-                            }
-                            const float nu = m[t] == -INFINITY ? 0.f : -m[t];
-                            if (part) {
-                                got = masked_keys(ts, msk, hi, p.sl2, nu);
-                            } else {
-                                const uint64_t nu2 = tc::f2(nu, nu);
-                                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-                                sweep(ts, [&](uint32_t (&x)[32], int) { add_chunk(x, sc2, nu2, acc); }, [] {});
-                                got = total_of(acc);
-                            }
-                            const float now = sum[t] + got;
-                            if (top || !__any_sync(0xffffffffu, now > 0x1p100f)) {
-                                sum[t] = now;
-                                break;
-                            }
-                            top = true;
+                        // The sum is relative to m, a large logit of the row's
+                        // first tile: fp32 holds it however far others lie
+                        // below, and above until it nears overflow. Only then
+                        // is a maximum taken and the sum moved to it.
+                        if (__any_sync(0xffffffffu, m[t] == -INFINITY)) {
+                            const float2 v = first_keys(ts, msk, hi, p.sl2, m[t]);
+                            m[t] = v.x;
+                            got = v.y;
+                        } else if (part) {
+                            got = masked_keys(ts, msk, hi, p.sl2, -m[t]);
+                        } else {
+                            const uint64_t nu2 = tc::f2(-m[t], -m[t]);
+                            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                            sweep(ts, [&](uint32_t (&x)[32], int) { add_chunk(x, sc2, nu2, acc); }, [] {});
+                            got = total_of(acc);
                         }
+                        if (__any_sync(0xffffffffu, sum[t] + got > 0x1p100f)) {
+                            const float best = masked_top(ts, msk, hi, p.sl2);
+                            if (best > m[t]) {
+                                sum[t] *= ex2(m[t] - best);
+                                m[t] = best;
+                            }
+                            got = masked_keys(ts, msk, hi, p.sl2, m[t] == -INFINITY ? 0.f : -m[t]);
+                        }
+                        sum[t] += got;
                         give_back(b);
                     } else {
                         // the Y rows of kSum, the X rows of kWindow: of this

@@ -6,7 +6,7 @@
 //
 // A weight needs its row's log-sum-exp over all keys, so the logits x are
 // computed twice: the first launch reduces them over the keys of each row, the
-// last over the rows of each key (a small one between merges split rows). (Kept
+// second over the rows of each key. (Kept
 // in memory they would be 4 bytes a pair each way, 0.5 GB for 16 windows of 64
 // tokens over 85,000 keys; the second product costs a tenth of that time.) V is
 // never read.
@@ -17,7 +17,8 @@
 //     tile), Y = its keys (B, 256 a stage); a row's keys may be split over
 //     several items (partial log-sum-exps);
 //   * kSum: X = up to 256 keys (A, 128 a tile), Y = query rows (B, 256 a
-//     stage), from the first that sees a key;
+//     stage), from the first that sees a key; a small launch before it merges
+//     the rows' partial log-sum-exps, which it reads once per 256 keys;
 //   * kWindow, where no request has more than 256 rows: X = those rows (B), Y =
 //     keys (A, 128 a stage), so that a key is finished with its stage and K
 //     streams past resident rows (with K resident the rows would be streamed
@@ -191,6 +192,49 @@ struct __align__(16) Item {
     Request x;
 };
 static_assert(sizeof(Item) <= 64, "an item's place in shared memory");
+
+// The negated log-sum-exp (-inf: no key) of row `row` of a row block, from the
+// blocks that had keys of it: those of its first and last stage, and all between
+// (a share is longer than a stage).
+struct RowParts {
+    const float* at;
+    int n;
+};
+__device__ __forceinline__ RowParts row_parts(const WindowParams& p, const Request& x, int r, int rb, int h,
+                                              long long share) {
+    const Cost c = lse_cost(p, x, rb, h, __ldcg(p.begin + r));
+    const int b0 = (int)((c.at + c.start) / share);
+    RowParts v;
+    v.n = c.stages > 0 ? (int)((c.at + c.start + (c.stages - 1LL) * c.per) / share) - b0 + 1 : 0;
+    v.at = p.part + (long long)(lse_unit(p, x, r, rb, h) + b0) * kRows;
+    return v;
+}
+// Rows row, row + 32, ..: all of a part's loads at once.
+template <int N>
+__device__ __forceinline__ void merge_rows(const RowParts& v, int row, float (&out)[N]) {
+    float M[N], sum[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        M[u] = -INFINITY;
+        sum[u] = 0.f;
+    }
+#pragma unroll 2
+    for (int s = 0; s < v.n; ++s) {
+        float l[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) l[u] = __ldcg(v.at + s * kRows + row + 32 * u);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const float top = fmaxf(M[u], l[u]);
+            if (top > -INFINITY) {
+                sum[u] = sum[u] * exp2f(M[u] - top) + exp2f(l[u] - top);
+                M[u] = top;
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) out[u] = sum[u] == 0.f ? -INFINITY : -(M[u] + log2f(sum[u]));
+}
 
 // kSum's items: 128 xkeys keys of a head.
 __device__ __forceinline__ long long sum_items(const WindowParams& p, int r, int xkeys) {
@@ -468,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
 
     // ---------------------------------------------------------- the plan --
-    long long total = 0, pos = 0, stop = 0;
+    long long total = 0, pos = 0, stop = 0, share = 0;  // share: kLse's
     int xkeys = 2;
     bool ascend = true;
     if (MODE == kLse) {
@@ -482,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ascend && g == 0) p.begin[p.R] = 0;
     } else {
-        ascend = __ldcg(p.begin + p.R) != 0;
+        share = __ldcg(p.begin + p.R);
+        ascend = share != 0;
     }
     if (ascend && MODE == kSum) {
         total = flat_scan(p.R, [&](int r) { return sum_items(p, r, xkeys); }, sums);
@@ -495,13 +540,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (ascend) {
         auto cost = [&](int r) { return request_cost<MODE>(p, r); };
         total = flat_scan(p.R, cost, sums);
-        const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)(MODE == kLse ? kLeastCost : kLeastTiles));
-        pos = blockIdx.x * share;
-        stop = min(pos + share, total);
+        const long long mine = max((total + gridDim.x - 1) / gridDim.x, (long long)(MODE == kLse ? kLeastCost : kLeastTiles));
+        pos = blockIdx.x * mine;
+        stop = min(pos + mine, total);
         if (MODE == kLse) {
             for (int r = blockIdx.x + gridDim.x * threadIdx.x; r < p.R; r += gridDim.x * kThreads)
                 p.begin[r] = flat_before(p.R, cost, sums, r);
-            if (blockIdx.x == 0 && threadIdx.x == 0) p.begin[p.R] = share;
+            if (blockIdx.x == 0 && threadIdx.x == 0) p.begin[p.R] = mine;
         }
     }
     const int rp = kRows / p.G * p.G;
@@ -676,17 +721,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLseWarp) {
         if (MODE != kLse) {
             // -------------------------------- the rows' log-sum-exps ----
-            // Copied without a wait, so the ring is filled ahead; zero past a
-            // block's rows. kSum: a slot per Y stage; kWindow: one per item.
+            // Zero past a block's rows. kSum: a slot per Y stage, copied without
+            // a wait, so the ring is filled ahead; kWindow: one per item, put
+            // together here (a launch for it took 8 us of a step, and a row is
+            // wanted a few times only).
             uint32_t lc = 0;
             bool ok = true;
             for (uint32_t ic = 0; ok; ++ic) {
                 Item it;
                 if (!(ok = take(ic, it)) || it.xt == 0) break;
                 const int rows = it.x.m * p.G;
+                if (MODE == kWindow) {
+                    const uint32_t ls = lc++ % kLseSlots;
+                    if (!(ok = wait_warp(l_empty + 8 * ls, (((lc - 1) / kLseSlots) & 1) ^ 1, p.wait_ns))) break;
+                    float v[kRows / 32];
+                    merge_rows(row_parts(p, it.x, it.r, 0, it.h, share), lane, v);
+#pragma unroll
+                    for (int u = 0; u < kRows / 32; ++u) {
+                        const int c = u * 32 + lane;
+                        sts32(sbase + SM::kLses + (ls * kRows + c) * 4, __float_as_uint(c < rows ? v[u] : 0.f));
+                    }
+                    mbar_arrive(l_full + 8 * ls);
+                    continue;
+                }
                 const float* at = p.nlse + ((long long)it.h * p.T + it.x.q0) * p.G;
-                const int j0 = MODE == kSum ? it.y0 : 0, j1 = MODE == kSum ? it.y1 : 1;
-                for (int j = j0; j < j1; ++j, ++lc) {
+                for (int j = it.y0; j < it.y1; ++j, ++lc) {
                     const uint32_t ls = lc % kLseSlots;
                     if (!(ok = wait_warp(l_empty + 8 * ls, ((lc / kLseSlots) & 1) ^ 1, p.wait_ns))) break;
 #pragma unroll
@@ -896,9 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Each row's log-sum-exp from the blocks that had keys of it (one launch between
-// the two: the second reads every row once per 256 keys), and kSum's item
-// counter back to zero. A thread merges one row.
+// For kSum: every row's log-sum-exp, a thread each, and its item counter back to
+// zero.
 __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const WindowParams p) {
     pdl_wait();
     pdl_trigger();
@@ -917,22 +975,9 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Windo
     const Request x = request_of(p, lo);
     if (x.m < 0) return;
     const int rb = (i - x.q0) / block_tokens(p), h = j / p.G;
-    const Cost c = lse_cost(p, x, rb, h, __ldcg(p.begin + lo));
-    // the blocks of its first and last stage; all between have some (a share is
-    // longer than a stage)
-    const int b0 = (int)((c.at + c.start) / share);
-    const int n = c.stages > 0 ? (int)((c.at + c.start + (c.stages - 1LL) * c.per) / share) - b0 + 1 : 0;
-    const float* at = p.part + (long long)(lse_unit(p, x, lo, rb, h) + b0) * kRows +
-                      (i - x.q0 - rb * block_tokens(p)) * p.G + j % p.G;
-    float M = -INFINITY, sum = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) M = fmaxf(M, __ldcg(at + s * kRows));
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-        const float v = __ldcg(at + s * kRows);
-        sum += v == -INFINITY ? 0.f : exp2f(v - M);
-    }
-    p.nlse[((long long)h * p.T + i) * p.G + j % p.G] = sum == 0.f ? -INFINITY : -(M + log2f(sum));
+    float v[1];
+    merge_rows(row_parts(p, x, lo, rb, h, share), (i - x.q0 - rb * block_tokens(p)) * p.G + j % p.G, v);
+    p.nlse[((long long)h * p.T + i) * p.G + j % p.G] = v[0];
 }
 
 constexpr int kMostBlocks = 256;  // of the grid, whatever the device has
@@ -1027,7 +1072,7 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     const bool few = max_query_len <= kRows / G;
     p.xt = (long long)max_query_len * G <= kKeys ? 1 : 2;
     bool ok = wide ? launch_window<128, kLse>(tq, tk, p, st) : launch_window<64, kLse>(tq, tk, p, st);
-    if (ok)
+    if (ok && !few)
         ok = launch_pdl(window_merge_kernel, (int)((rows + kMergeThreads) / kMergeThreads), kMergeThreads, 0, st, p) ==
              cudaSuccess;
     if (ok && few) ok = wide ? launch_window<128, kWindow>(tq, tk, p, st) : launch_window<64, kWindow>(tq, tk, p, st);

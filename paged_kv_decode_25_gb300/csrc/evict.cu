@@ -359,19 +359,23 @@ template <int V16>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
     __shared__ long long sums[flat_words(kMoveThreads)];
     __shared__ int2 rows[kMoveRows];
-    pdl_wait();
-    pdl_trigger();
+    // lengths and budgets were there before the selection: the plan is made
+    // while it runs
     if (p.in_place) {
         // a kept row never moves up, so items in ascending order never
         // overwrite a row that is still to be read: one block per (b, h)
         const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
         const Share s = share_of(p, b);
+        pdl_wait();
+        pdl_trigger();
         if (s.kept == s.n) return;
         for (int i0 = 0; i0 < s.kept; i0 += kMoveRows) move_rows<V16>(p, s, b, h, i0, rows);
         return;
     }
     auto items = [&](int b) { return (long long)p.Hkv * ((share_of(p, b).kept + kMoveRows - 1) / kMoveRows); };
     const long long total = flat_scan(p.B, items, sums);
+    pdl_wait();
+    pdl_trigger();
     for (long long x = blockIdx.x; x < total; x += gridDim.x) {
         long long first;
         const int b = flat_find(p.B, items, sums, x, first);

@@ -33,8 +33,15 @@ struct ScoreParams {
 template <int GP>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(const ScoreParams p) {
     __shared__ long long sums[flat_words(kScoreThreads)], bsums[flat_words(kScoreThreads)];
-    pdl_wait();
-    pdl_trigger();
+    // the plan and the first item's table entries need nothing of the attention,
+    // which had waited for all before it
+    bool waited = false;
+    auto wait = [&]() {
+        if (waited) return;
+        pdl_wait();
+        pdl_trigger();
+        waited = true;
+    };
     auto tokens = [&](int b) { return min(max(__ldg(p.lens + b), 0), p.mbps * kBlock); };
     // work items are 64 blocks of one (request, head); the logits of the
     // flat order lie in blocks of (request, head) laid end to end
@@ -54,6 +61,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const ScoreParams 
         const int blk = __ldg(p.tables + (long long)b * p.mbps + j);
         const bool in = blk >= 0 && blk < p.num_blocks;  // (else reported by the attention)
         if (!in && p.by_block) continue;
+        wait();
         const long long e = p.by_block ? (long long)blk * p.Hkv + h : e0 + j;
         const float* lg = p.logits + (e * kBlock + i0) * GP;
         float l[4 * GP], lse[GP];
@@ -84,6 +92,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const ScoreParams 
         }
         *at = make_float4(w[0], w[1], w[2], w[3]);
     }
+    wait();  // (whoever waits for this launch has the attention too)
 }
 
 // The workspace after the decode attention's own: each row's log-sum-exp,

@@ -508,10 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after();
     const uint32_t tbase = lds32(sbase + SM::kTmem);
-    pdl_wait();
-    pdl_trigger();
-
     // ---------------------------------------------------------- the plan --
+    // the launches after kLse plan while the one before them ends: the requests
+    // were there before the first
+    if (MODE == kLse) {
+        pdl_wait();
+        pdl_trigger();
+    }
     long long total = 0, pos = 0, stop = 0, share = 0;  // share: kLse's
     int xkeys = 2;
     bool ascend = true;
@@ -525,9 +528,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__ldg(p.lens + r) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
         }
         if (!ascend && g == 0) p.begin[p.R] = 0;
-    } else {
-        share = __ldcg(p.begin + p.R);
-        ascend = share != 0;
     }
     if (ascend && MODE == kSum) {
         total = flat_scan(p.R, [&](int r) { return sum_items(p, r, xkeys); }, sums);
@@ -548,6 +548,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.begin[r] = flat_before(p.R, cost, sums, r);
             if (blockIdx.x == 0 && threadIdx.x == 0) p.begin[p.R] = mine;
         }
+    }
+    if (MODE != kLse) {
+        pdl_wait();
+        pdl_trigger();
+        share = __ldcg(p.begin + p.R);
+        if (share == 0) total = stop = 0;
     }
     const int rp = kRows / p.G * p.G;
     // the k-th item of the list as every other warp sees it

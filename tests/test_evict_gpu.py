@@ -99,6 +99,21 @@ def test_long(cuda_device, in_place):
     run([70001, 40], [20011, 40], 500, 2, 64, True, "spread", in_place, cuda=cuda_device)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+@pytest.mark.parametrize("lens,Hkv", [([4500, 100], 2), ([9000, 0, 8999, 3], 1), ([16500, 16493, 5, 700], 2), ([16401, 2049, 2048, 2047, 900], 8)])
+def test_several_blocks_a_request(cuda_device, lens, Hkv, kind):
+    """Tables of 4,096, 8,192 and 16,384 tokens and more are shared by 2, 4 and
+    8 blocks where few (request, head) pairs stand for them."""
+    run(lens, [max(1, n // 3) for n in lens], 20, Hkv, 64, True, kind, False, cuda=cuda_device)
+    run(lens, [n - 1 for n in lens], 0, Hkv, 64, True, kind, True, cuda=cuda_device)
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+def test_more_keys_than_shared_memory(cuda_device, kind):
+    """Eight blocks hold 24,576 keys each; the rest is read again."""
+    run([200500], [90001], 500, 1, 64, True, kind, False, cuda=cuda_device)
+
+
 def test_bad_blocks_and_lengths(cuda_device):
     """A bad source block drops out of the choice, a bad destination block
     drops its rows, a length past the table is cut: reported, nothing else moves."""

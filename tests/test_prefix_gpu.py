@@ -113,6 +113,31 @@ def test_many_groups(cuda_device):
     check(both, P, starts, own, q, out, 0.125)
 
 
+def test_many_requests_in_few_groups(cuda_device):
+    """More requests than one warp plans for, lengths from none to many blocks."""
+    rng = np.random.default_rng(5)
+    B = 700
+    own = [int(x) for x in rng.integers(0, 60, B)]
+    own[3], own[699], own[350] = 900, 500, 0
+    starts = [0, 0, 300, 640]
+    both, ptab, tables = make([90, 700, 33], own, 1, 64, 35)
+    q = both.queries(B, 4)
+    out, err = call(_mi(), cuda_device, both, ptab, [90, 700, 33], starts, tables, own, q, 0.125)
+    assert err == 0
+    check(both, 3, starts, own, q, out, 0.125)
+
+
+@pytest.mark.parametrize("prefix,own", [(5, [9000, 0, 3, 17000, 40]), (9000, [1, 0, 17, 40, 3]), (3000, [3000] * 9),
+                                        (0, [700, 16, 0, 33])])
+def test_parts_of_unequal_length(cuda_device, prefix, own):
+    """Own tokens that outweigh the prefix, the reverse, and a prefix without tokens."""
+    both, ptab, tables = make([prefix], own, 2, 128, 36)
+    q = both.queries(len(own), 8)
+    out, err = call(_mi(), cuda_device, both, ptab, [prefix], [0, len(own)], tables, own, q, 0.08)
+    assert err == 0
+    check(both, 1, [0, len(own)], own, q, out, 0.08)
+
+
 def test_no_prefixes_is_plain_decode(cuda_device):
     """Without prefixes the call is plain decode attention up to the split: both
     lie within the roundings of the 64-bit value."""

@@ -95,6 +95,49 @@ def test_long_window(cuda_device):
     check(batch, q, 8, starts_of(m), before, got.cpu(), True)
 
 
+def test_shares_end_anywhere(cuda_device):
+    """One head and unequal requests: shares of the work end within a request's
+    rows and keys, windows and prompts alike."""
+    for lens, m in (([9000, 40, 5100, 1], [64, 3, 64, 1]), ([2500, 40, 1100], [2500, 40, 700])):
+        batch = Batch(lens, 1, 64, 25)
+        q = batch.queries(sum(m), 3)
+        before = torch.rand(batch.num_blocks, 1, BLOCK, generator=batch.gen)
+        got = before.to(cuda_device)
+        assert call(_mi(), cuda_device, batch, q, 3, starts_of(m), max(m), got, False) == 0
+        check(batch, q, 3, starts_of(m), before, got.cpu(), False)
+
+
+def test_many_short_requests(cuda_device):
+    """More requests than one warp plans for."""
+    g = torch.Generator().manual_seed(6)
+    lens = torch.randint(0, 50, (600,), generator=g).tolist()
+    m = [min(n, 1 + i % 5) for i, n in enumerate(lens)]
+    batch = Batch(lens, 1, 64, 26)
+    q = batch.queries(sum(m), 2)
+    before = torch.rand(batch.num_blocks, 1, BLOCK, generator=batch.gen)
+    for most in (5, 300):  # resident rows, resident keys
+        got = before.to(cuda_device)
+        assert call(_mi(), cuda_device, batch, q, 2, starts_of(m), most, got, False) == 0
+        check(batch, q, 2, starts_of(m), before, got.cpu(), False)
+
+
+@pytest.mark.parametrize("step", [60.0, -60.0])
+def test_logits_far_apart(cuda_device, step):
+    """Logits that climb or fall by hundreds along the keys, so that the first
+    ones say nothing about the size of a row's sum."""
+    lens, m = [700, 300], [20, 300]
+    batch = Batch(lens, 1, 64, 27)
+    q = batch.queries(sum(m), 2)
+    q[:, :, 0] = 2.0
+    for r, n in enumerate(lens):
+        blk, off = batch.rows(r)
+        batch.k[blk, 0, off, 0] = (torch.arange(n) // 50 * step).to(torch.bfloat16)
+    before = torch.rand(batch.num_blocks, 1, BLOCK, generator=batch.gen)
+    got = before.to(cuda_device)
+    assert call(_mi(), cuda_device, batch, q, 2, starts_of(m), 300, got, True, scale=0.5) == 0
+    check(batch, q, 2, starts_of(m), before, got.cpu(), True, scale=0.5)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
 def test_scales(cuda_device, scale):
     batch = Batch([200, 90], 1, 64, 23)

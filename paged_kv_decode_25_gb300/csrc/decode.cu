@@ -1856,10 +1856,8 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
 // its end, so that whoever waits for this one has both (with every block
 // waiting, those that were done kept their SMs from the rest).
 constexpr int kTailWarps = 4, kTailBlocks = 3;  // a block's, an SM's
-// pieces of an early warp: requests differ in length, so one piece a warp would
-// leave the SMs waiting for the longest (128 requests of 16 to 512 tokens: 107
-// us for two pieces, 94 for four, 93 for eight)
-constexpr int kTailPieces = 8;
+// A piece's own cost (its queries, its output, finding the next), in blocks.
+constexpr float kTailCost = 2.f;
 
 template <int HD>
 struct TailSmem {
@@ -1875,7 +1873,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
     constexpr int S = TailSmem<HD>::kStages, kTile = TailSmem<HD>::kTile;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long bars[kTailWarps * S];
-    __shared__ long long sums[flat_words(kTailWarps * 32)], red[2][kTailWarps];
+    __shared__ long long sums[flat_words(kTailWarps * 32)], red[3][kTailWarps];
     __shared__ int own[kFlatOneWarp], first_piece[kFlatOneWarp + 1];  // usual batches: tokens, pieces before
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
@@ -1890,12 +1888,14 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
     // can finish while it runs; the others, started as it ends, take the rest.
     const bool small = p.B <= kFlatOneWarp;
     long long blocks = 0, prefix = 0;  // (head, block)s of own tokens, (tile, block)s of the prefixes
+    int units = 0;                     // (request, head)s with tokens
     for (int b = tid; b < p.B; b += kTailWarps * 32) {
         if (b % (int)gridDim.x == (int)blockIdx.x && __ldg(p.context_lens + b) > p.mbps * kBlock)
             raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
         const int n = ctx_clamped(p, b);
         if (small) own[b] = n;
         blocks += (long long)p.Hkv * ((n + kBlock - 1) / kBlock);
+        units += n > 0 ? p.Hkv : 0;
     }
     // groups that do not ascend give a number as good as any: it sets shares
     // of the work, never an index
@@ -1906,16 +1906,19 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
     for (int o = 16; o > 0; o >>= 1) {
         blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
         prefix += __shfl_xor_sync(0xffffffffu, prefix, o);
+        units += __shfl_xor_sync(0xffffffffu, units, o);
     }
     if (lane == 0) {
         red[0][warp] = blocks;
         red[1][warp] = prefix;
+        red[2][warp] = units;
     }
     __syncthreads();
-    blocks = prefix = 0;
+    blocks = prefix = units = 0;
     for (int i = 0; i < kTailWarps; ++i) {
         blocks += red[0][i];
         prefix += red[1][i];
+        units += (int)red[2][i];
     }
     const int active = prefix_budget(t.prefix, prefix, blocks);
     const int warps = gridDim.x * kTailWarps;
@@ -1924,11 +1927,32 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
     float part = early > 0 ? (float)(t.prefix.sms - active) / (float)active * (float)prefix * kTileBlock / (float)blocks : 0.f;
     if (!(part < 0.875f)) part = 1.f;
     auto pieces_of = [&](int n, int step) { return p.Hkv * (((n + kBlock - 1) / kBlock + step - 1) / step); };
+    // The blocks of a piece: lane i tries (i + 1) / 16 of a warp's even share.
+    // Warps take whole pieces in turn (about blocks / step, and half a piece
+    // more for every unit's end), so the share comes out in rounds of them; long
+    // pieces differ more from one another. (64 chats, 9 blocks a warp: 32 us
+    // with pieces of 12, 37 with 4 or 8; 128 requests, 44 a warp: 99, 93, 90.)
     constexpr int kWhole = 1 << 27;  // a table's blocks are no more
-    int step = (int)min((long long)kWhole, max((long long)kTailLeast, (blocks + t.most - 1) / t.most));
-    if (part > 0.f) step = max(step, (int)ceilf((float)blocks * part / (float)(kTailPieces * early)));
-    if (part < 1.f) step = max(step, (int)ceilf((float)blocks * (1.f - part) / (float)(warps - early)));
-    step = min(step, kWhole);
+    int step = 1;
+    {
+        const float be = (float)blocks * part, bl = (float)blocks - be, we = (float)early, wl = (float)(warps - early);
+        const float even = be > 0.f ? be / we : bl / wl;
+        const float s = ceilf(fmaxf((float)kTailLeast, even * (float)(lane + 1) / 16.f));
+        float cost = (be > 0.f ? ceilf((be / s + 0.5f * (float)units * part) / we) : 0.f) +
+                     (bl > 0.f ? ceilf((bl / s + 0.5f * (float)units * (1.f - part)) / wl) : 0.f);
+        cost = cost * (s + kTailCost) + 0.5f * s;
+        float best = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float c = __shfl_xor_sync(0xffffffffu, cost, o), t = __shfl_xor_sync(0xffffffffu, best, o);
+            if (c < cost || (c == cost && t < best)) {
+                cost = c;
+                best = t;
+            }
+        }
+        step = (int)fminf(best, (float)kWhole);
+    }
+    step = (int)min((long long)kWhole, max((long long)step, (blocks + t.most - 1) / t.most));
     auto pieces = [&](int b) { return (long long)pieces_of(ctx_clamped(p, b), step); };
     int total;
     if (small) {

@@ -65,7 +65,8 @@ typedef enum mi_status {
 #define MI_DEVERR_BAD_QUERY    0x20 /* prefill: query_start not within [0, total_q] and ascending,
                                        a request longer than max_query_len, or more
                                        new tokens than context; shared prefixes:
-                                       group_start not within [0, B] and ascending */
+                                       group_start not within [0, B], or its entries
+                                       before the last not ascending */
 
 /* Short human-readable name of a status. */
 const char* mi_status_string(mi_status s);
@@ -579,9 +580,10 @@ mi_status mi_kv_copy_rows(const void* src, int64_t src_count, const int32_t* src
 /* One decode step of attention for such a batch: every prefix's K and V are
  * read once for all its requests. num_prefixes groups; group g is the requests
  * group_start[g] .. group_start[g+1]-1 of the batch, all behind prefix g, whose
- * first prefix_lens[g] tokens prefix_tables[g] holds. Requests before
- * group_start[0] or from group_start[num_prefixes] on have no prefix. For
- * request b of group g with p = prefix_lens[g] and n = context_lens[b] own
+ * first prefix_lens[g] tokens prefix_tables[g] holds. A group may be empty; the
+ * last one also is when group_start[num_prefixes] lies before its start (a
+ * batch with fewer requests than prefixes). Requests in no group have no
+ * prefix. For request b of group g with p = prefix_lens[g] and n = context_lens[b] own
  * tokens (counting the new one; append it with positions[b] = p + n - 1):
  *   out[b][j] = sum_t softmax_t(scale * <q[b][j], K_t>) V_t
  * over the p tokens of the prefix and the n of the request. The result is that
@@ -597,8 +599,8 @@ mi_status mi_kv_copy_rows(const void* src, int64_t src_count, const int32_t* src
  * bytes, 16-byte aligned, contents and graph replay as for
  * mi_paged_decode_attention; calls that may run at the same time take
  * different ones.
- * Device errors: group_start not ascending within [0, B] (MI_DEVERR_BAD_QUERY):
- * every request attends to its own tokens only; a prefix length above a table
+ * Device errors: an entry of group_start outside [0, B], or one before the last
+ * below the one ahead of it (MI_DEVERR_BAD_QUERY): every request attends to its own tokens only; a prefix length above a table
  * row clamps to it (MI_DEVERR_BAD_CONTEXT); a bad block id of a prefix drops
  * that block's keys (MI_DEVERR_BAD_BLOCK); the others as
  * mi_paged_decode_attention. num_prefixes 0 .. 65535, max_prefix_blocks >= 1. */

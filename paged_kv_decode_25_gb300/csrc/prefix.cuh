@@ -40,9 +40,14 @@ __device__ __forceinline__ int prefix_tokens(const PrefixWork& w, int mbps, int 
 __device__ __forceinline__ int prefix_blocks(const PrefixWork& w, int mbps, int g) {
     return (prefix_tokens(w, mbps, g) + kBlock - 1) / kBlock;
 }
-// Tiles of group g's requests, all KV heads counted.
+// Tiles of group g's requests, all KV heads counted. (The last group may end
+// before it starts: it is empty.)
 __device__ __forceinline__ int prefix_units(const PrefixWork& w, int Hkv, int per, int g) {
-    return Hkv * ((__ldg(w.starts + g + 1) - __ldg(w.starts + g) + per - 1) / per);
+    return Hkv * ((max(__ldg(w.starts + g + 1) - __ldg(w.starts + g), 0) + per - 1) / per);
+}
+// The first request behind all groups.
+__device__ __forceinline__ int prefix_end(const PrefixWork& w) {
+    return max(__ldg(w.starts + w.P), __ldg(w.starts + max(w.P - 1, 0)));
 }
 __device__ __forceinline__ int prefix_splits(int blocks, int step) { return (blocks + step - 1) / step; }
 // Items of group g for splits of `step` blocks.
@@ -120,7 +125,8 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
             const int s0 = __ldg(w.starts + min(lane, w.P)), len = in ? __ldg(w.lens + lane) : 0;
             int s1 = __shfl_down_sync(0xffffffffu, s0, 1);
             if (lane == 31) s1 = __ldg(w.starts + w.P);  // (read by lane 31 alone when there are 32 groups)
-            const bool bad = s0 < 0 || s0 > w.B || (in && (s1 < s0 || s1 > w.B));
+            const bool bad = s0 < 0 || s0 > w.B || (in && (s1 < 0 || s1 > w.B || (s1 < s0 && lane < w.P - 1)));
+            s1 = max(s1, s0);
             if (__any_sync(0xffffffffu, bad)) {
                 step = 0;
             } else {
@@ -187,7 +193,8 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
             return 0;
         }
     } else {
-        if (!starts_ascend(w.starts, w.P, w.B)) {
+        const int end = __ldg(w.starts + w.P);
+        if (!starts_ascend(w.starts, w.P - 1, w.B) || end < 0 || end > w.B) {
             no_prefix();
             return 0;
         }
@@ -208,7 +215,7 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
     // each request's slots; those outside every group have none
     for (int b = blockIdx.x + gridDim.x * tid; b < w.B; b += gridDim.x * nt) {
         int4 at = make_int4(0, 0, 0, 0);
-        if (b >= __ldg(w.starts) && b < __ldg(w.starts + w.P)) {
+        if (b >= __ldg(w.starts) && b < prefix_end(w)) {
             int lo = 0, hi = w.P;  // starts[lo] <= b < starts[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;

@@ -176,7 +176,7 @@ def test_device_errors(cuda_device):
     both, ptab, tables = make([100, 64], own, 2, 64, 36)
     q = both.queries(3, 4)
     # groups out of order or out of range: own tokens only
-    for starts in ([0, 2, 1], [0, 4, 4], [-1, 2, 3]):
+    for starts in ([2, 1, 3], [0, 4, 4], [-1, 2, 3], [0, 2, -1], [0, 2, 4]):
         out, err = call(mi, dev, both, ptab, [100, 64], starts, tables, own, q, 0.125)
         assert err == mi.MI_DEVERR_BAD_QUERY
         check(both, 2, [0, 0, 0], own, q, out, 0.125)
@@ -198,6 +198,20 @@ def test_device_errors(cuda_device):
                                     torch.cat([both.tokens(both.v, 1, h), both.tokens(both.v, 4, h)]), 0.125)
                       for h in range(2)])
     assert torch.all((out[2].double() - torch.cat(want)).abs() <= torch.cat(tol))
+
+
+@pytest.mark.parametrize("P", [3, 32, 33, 60])
+def test_last_group_ends_before_it_starts(cuda_device, P):
+    """It is empty; the groups before it are as given."""
+    B = P + 2
+    own, prefixes = [b % 7 for b in range(B)], [20 + g % 50 for g in range(P)]
+    both, ptab, tables = make(prefixes, own, 1, 64, 37)
+    q = both.queries(B, 2)
+    for end in (0, 1, P - 2, P - 1):
+        starts = list(range(P)) + [end]
+        out, err = call(_mi(), cuda_device, both, ptab, prefixes, starts, tables, own, q, 0.125)
+        assert err == 0
+        check(both, P, starts, own, q, out, 0.125)
 
 
 def test_paging_does_not_matter_and_repeat(cuda_device):

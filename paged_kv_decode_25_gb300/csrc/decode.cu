@@ -1839,11 +1839,11 @@ __global__ void __launch_bounds__((W + (FUSED ? 2 : 1)) * 32, (VAR == kVarFp8 ||
 // The requests' own tokens of a shared-prefix step. They are few to a request
 // (an answer begun, a chat turn), so the unit of attn_kernel, four warps on one
 // (request, head) with a merge of their states at its end, spends most of its
-// time on that end (44 us for 139 MB). Here a warp takes a piece of up to `step`
+// time on that end (44 us for 92 MB). Here a warp takes a piece of up to `step`
 // blocks of a (request, head) by itself: it looks the blocks up, issues their
 // copies into a ring of its own, and writes the piece's normalised output and
 // log-sum-exp; prefix.cu merges the pieces with the prefix's partial results
-// (139 MB in 20 us with every SM at it, 6.8 TB/s).
+// (92 MB in 20 us with every SM at it, 4.6 TB/s).
 //
 // A warp spends about 1,000 clocks on a block's products and softmax and 400 on
 // its copies, all of it latency, so an SM holds twelve warps of two stages
@@ -1930,8 +1930,8 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
     // The blocks of a piece: lane i tries (i + 1) / 16 of a warp's even share.
     // Warps take whole pieces in turn (about blocks / step, and half a piece
     // more for every unit's end), so the share comes out in rounds of them; long
-    // pieces differ more from one another. (64 chats, 9 blocks a warp: 32 us
-    // with pieces of 12, 37 with 4 or 8; 128 requests, 44 a warp: 99, 93, 90.)
+    // pieces differ more from one another. (64 chats, 8 blocks a warp: 32 us
+    // with pieces of 12, 37 with 4 or 8; 128 requests, 41 a warp: 99, 93, 90.)
     constexpr int kWhole = 1 << 27;  // a table's blocks are no more
     int step = 1;
     {

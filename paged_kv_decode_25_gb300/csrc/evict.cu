@@ -13,11 +13,13 @@
 //     kept older tokens' indices in ascending order. Where the (b, h) do not
 //     fill the GPU, a cluster of up to 8 blocks shares one: each holds a
 //     stretch of the tokens and adds up the others' digit counts through
-//     distributed shared memory (16 (b, h) of 57,000 tokens: one block each
-//     73 us);
+//     distributed shared memory (16 (b, h) of 30,000 to 120,000 tokens: 22 us,
+//     with one block each 73);
 //   * evict_move_kernel copies the kept rows of K and V and their scores.
 // Both only move bytes: the floor is the scores once, the kept rows in and
-// out.
+// out. 64 requests of 2,000 to 8,192 tokens cut to 2,048: the selection 22 us
+// (the keys are read from shared memory three times more, the digit counts are
+// atomics on a few hot bins), the move 172 us for 1.08 GB (6.3 TB/s).
 #include <algorithm>
 #include <mutex>
 

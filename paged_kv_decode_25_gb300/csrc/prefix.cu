@@ -7,7 +7,8 @@
 //   * prefix_partials (prefill.cu): the group's queries against the prefix on
 //     the fifth-generation tensor cores, as one tall matrix of (request, head)
 //     rows per KV head: a staged K / V tile serves up to 256 of them;
-//   * prefix_tail (decode.cu): the requests' own blocks, a warp per piece;
+//   * prefix_tail (decode.cu): the requests' own blocks, a warp per piece, at
+//     the same time on the SMs that the first part leaves;
 //   * prefix_merge_kernel puts each row together from the two.
 //
 // The rows of (group, KV head) are cut into tiles of whole requests, the

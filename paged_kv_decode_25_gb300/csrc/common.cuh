@@ -382,4 +382,16 @@ inline cudaError_t launch_cluster(void (*fn)(Args...), int grid, int block, int 
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// A warp's wait for a barrier's phase, bounded.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit_ns) {
+    // One vote decides the common case for the whole warp: a branch on each
+    // lane's own answer costs about 130 clocks for its reconvergence alone.
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, kWaitSleepNs))) return true;
+        if (__any_sync(0xffffffffu, (long long)(globaltimer() - t0) > limit_ns)) return false;
+    }
+}
+
 }  // namespace mi

@@ -1920,7 +1920,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
         prefix += red[1][i];
         units += (int)red[2][i];
     }
-    const int active = prefix_budget(t.prefix, prefix, blocks);
+    const int active = prefix_budget(t.prefix, (float)prefix, (float)blocks);
     const int warps = gridDim.x * kTailWarps;
     const int early = prefix > 0 ? (t.prefix.sms - active) * kTailBlocks * kTailWarps : 0;
     // the early warps' part of the blocks

@@ -915,6 +915,93 @@ struct Tc2Smem {
     static constexpr int kTotal = kTmem + 16 + 1024;  // slack to align the base to 1024 B
 };
 
+// Two rows' running reference exponent and sum (per lane: its 32 keys).
+struct RowSums {
+    float ma, mb, la, lb;
+    bool ok;
+};
+
+// PREFIX: a stage whose rows have no reference yet, or have outgrown it, or
+// with keys that do not count (all but the first `left`, and those of absent
+// blocks): masks, takes the maximum, moves O and the sums to it and writes P.
+// A function of its own, as few stages need it and the plain stage's loop is
+// the faster without its registers and selects; and in short loops, as every
+// item's first stage runs it out of a cold instruction cache (unrolled over the
+// 128 keys it took 10 us there).
+template <int HD>
+__device__ __noinline__ RowSums whole_stage(uint32_t tl, uint32_t present, int left, float sl2, RowSums r,
+                                            uint32_t o_done, uint32_t parity, long long wait_ns) {
+    const int c4 = threadIdx.x & 3;
+    const uint32_t ts = tl + 128u;
+    uint32_t y[16];  // y[4k + e] of 32 keys: e = 0, 1 row a; e = 2, 3 row b
+    const bool masked = present != (1u << kT2Blocks) - 1u || left < kT2Keys;
+    auto scores = [&](int ch) {
+        tc::ld16x256_x4(ts + 32u * ch, y);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * sl2);
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int k = 4 * ch + (i >> 2);
+                if (!((present >> (k >> 1)) & 1u) || 8 * k + 2 * c4 + (i & 1) >= left) y[i] = __float_as_uint(-INFINITY);
+            }
+        }
+    };
+    float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll 1
+    for (int ch = 0; ch < kT2Keys / 32; ++ch) {
+        scores(ch);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) (i & 2 ? mb : ma) = fmaxf(i & 2 ? mb : ma, __uint_as_float(y[i]));
+    }
+#pragma unroll 1
+    for (int o = 1; o < 4; o <<= 1) {
+        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    }
+    // (all four lanes of a row take the same decision)
+    const bool move_a = ma > r.ma && r.ma != -INFINITY, move_b = mb > r.mb && r.mb != -INFINITY;
+    const float alpha_a = move_a ? ex2(r.ma - ma) : 1.f, alpha_b = move_b ? ex2(r.mb - mb) : 1.f;
+    r.ma = fmaxf(r.ma, ma);
+    r.mb = fmaxf(r.mb, mb);
+    r.ok = true;
+    if (__any_sync(0xffffffffu, move_a || move_b)) {
+        // O may be touched once its previous P . V has finished
+        r.ok = wait_warp(o_done, parity, wait_ns);
+        tc::fence_after();
+#pragma unroll 1
+        for (int ch = 0; r.ok && ch < HD / 32; ++ch) {
+            tc::ld16x256_x4(tl + 32u * ch, y);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                y[i] = __float_as_uint(__uint_as_float(y[i]) * (i & 2 ? alpha_b : alpha_a));
+            tc::st16x256_x4(tl + 32u * ch, y);
+        }
+    }
+    const float una = r.ma == -INFINITY ? 0.f : r.ma, unb = r.mb == -INFINITY ? 0.f : r.mb;
+    r.la *= alpha_a;
+    r.lb *= alpha_b;
+#pragma unroll 1
+    for (int ch = 0; ch < kT2Keys / 32; ++ch) {
+        scores(ch);
+        uint32_t pk[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float ea0 = ex2(__uint_as_float(y[4 * k]) - una), ea1 = ex2(__uint_as_float(y[4 * k + 1]) - una);
+            const float eb0 = ex2(__uint_as_float(y[4 * k + 2]) - unb), eb1 = ex2(__uint_as_float(y[4 * k + 3]) - unb);
+            r.la += ea0 + ea1;
+            r.lb += eb0 + eb1;
+            pk[2 * k] = pack_bf16x2(ea0, ea1);
+            pk[2 * k + 1] = pack_bf16x2(eb0, eb1);
+        }
+        tc::st16x128_x4(ts + 16u * ch, pk);  // over scores read already
+    }
+    tc::wait_st();
+    return r;
+}
+
 template <int HD, bool PREFIX = false>
 __global__ void __launch_bounds__(kT2Threads, 1)
     prefill_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -990,7 +1077,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 mbar_init(v_full0 + i * 8, 1);
                 mbar_init(v_empty0 + i * 8, 1);
                 mbar_init(s_full0 + i * 8, 1);
-                mbar_init(p_full0 + i * 8, 256);  // every softmax thread of the tile
+                mbar_init(p_full0 + i * 8, PREFIX ? 8 : 256);  // every softmax warp or thread of the tile
                 mbar_init(o_done0 + i * 8, 1);
             }
             mbar_init(fin, 1);
@@ -1089,7 +1176,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 auto issue_s = [&](int t, int j) {
                     const uint32_t kbase = sbase + SM::kRingK + (j % kT2KSlots) * SM::kKV;
                     const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
-    #pragma unroll
+    #pragma unroll(PREFIX ? 2 : HD / 16)
                     for (int kk = 0; kk < HD / 16; ++kk) {
                         const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
                         const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
@@ -1101,7 +1188,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 auto issue_o = [&](int t, int j) {
                     const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
                     const uint32_t pcol = tbase + 256u * t + 128u;  // P_t(j): bf16 pairs over S_t's first 64 columns
-    #pragma unroll
+    #pragma unroll(PREFIX ? 2 : kT2Blocks)
                     for (int l = 0; l < kT2Blocks; ++l) {
                         // block l: [kH][16 keys][128 B]; the 64-column halves of V
                         // are kBlock * 128 bytes apart
@@ -1175,7 +1262,90 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             const bool fold = p.sl2 > 0.f;
             float mra_run = -INFINITY, mrb_run = -INFINITY, lra = 0.f, lrb = 0.f;  // per lane: its 32 keys of the row
             bool ok = true;
-            for (int j = 0; j < nst; ++j) {
+            // V rows of keys outside the context (missing blocks, the last
+            // block's tail) may hold any bits: zero them once the stage's V
+            // copies have landed, before tile 0's P . V (tile 1's is issued
+            // after it). A warp of tile 0 off the MMA warp's scheduler does it.
+            auto zero_v = [&](int j, uint32_t present) -> bool {
+                const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
+                const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
+                if (any) {
+                    if (!wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns)) return false;
+                    const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
+                    for (int l = 0; l < kT2Blocks; ++l) {
+                        const int from = !((present >> l) & 1u) ? 0 : (l == last && tail < kBlock ? tail : kBlock);
+                        for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
+                            const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
+                            st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
+                        }
+                    }
+                    fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
+                }
+                return true;
+            };
+            if constexpr (PREFIX) {
+                // Every row sees every key, so a stage is plain but for an
+                // item's last: exponentials relative to the row's reference,
+                // no maximum. The reference is the first stage's maximum; it
+                // moves when a sum passes 2^60 (bf16 and fp32 hold the
+                // probabilities and sums below that as well as below 1).
+                RowSums r = {-INFINITY, -INFINITY, 0.f, 0.f, true};
+                bool steady = false;  // the warp's rows have references
+                const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
+                for (int j = 0; j < nst; ++j) {
+                    ok = wait_warp(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns) &&
+                         wait_warp(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns);  // (the mask's)
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
+                    const int left = it.n - j * kT2Keys;
+                    bool done = false;
+                    if (steady && present == (1u << kT2Blocks) - 1u && left >= kT2Keys) {
+                        uint32_t x[2 * kT2Keys / 4];
+                        tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                        tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                        tc::wait_ld();
+                        const uint64_t nua = tc::f2(-r.ma, -r.ma), nub = tc::f2(-r.mb, -r.mb);
+                        uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
+    #pragma unroll
+                        for (int k = 0; k < kT2Keys / 8; ++k) {
+                            const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
+                                                         sc2, nua);
+                            const uint64_t b2 = tc::fma2(
+                                tc::f2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), sc2, nub);
+                            const float ea0 = ex2(tc::f2_lo(a2)), ea1 = ex2(tc::f2_hi(a2));
+                            const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
+                            acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
+                            accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
+                            x[2 * k] = pack_bf16x2(ea0, ea1);
+                            x[2 * k + 1] = pack_bf16x2(eb0, eb1);
+                        }
+                        const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
+                        const float psa = tc::f2_lo(sa) + tc::f2_hi(sa), psb = tc::f2_lo(sb) + tc::f2_hi(sb);
+                        if (!__any_sync(0xffffffffu, (va && psa > 0x1p60f) || (vb && psb > 0x1p60f))) {
+                            r.la += psa;
+                            r.lb += psb;
+                            tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
+                            tc::wait_st();
+                            done = true;
+                        }
+                    }
+                    if (!done) {
+                        r = whole_stage<HD>(tl, present, left, p.sl2, r, o_done0 + t * 8, (uint32_t)((j - 1) & 1), p.wait_ns);
+                        if (!(ok = r.ok)) break;
+                        steady = fold && !__any_sync(0xffffffffu, (va && r.ma == -INFINITY) || (vb && r.mb == -INFINITY));
+                    }
+                    if (warp == 1 && !(ok = zero_v(j, present))) break;
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full0 + t * 8);
+                }
+                mra_run = r.ma;
+                mrb_run = r.mb;
+                lra = r.la;
+                lrb = r.lb;
+            }
+            for (int j = 0; !PREFIX && j < nst; ++j) {
                 ok = wait_all(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns) &&
                      wait_all(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns);
                 if (!ok) break;
@@ -1305,27 +1475,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 // P_t(j): the A operand of O_t += P_t(j) . V(j)
                 tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
                 tc::wait_st();
-                if (warp == 1) {
-                    // V rows of keys outside the context (missing blocks, the
-                    // last block's tail) may hold any bits: zero them once the
-                    // stage's V copies have landed, before tile 0's P . V (tile
-                    // 1's is issued after it). A warp of tile 0 off the MMA
-                    // warp's scheduler does it.
-                    const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
-                    const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
-                    if (any) {
-                        if (!(ok = wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns))) break;
-                        const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
-                        for (int l = 0; l < kT2Blocks; ++l) {
-                            const int from = !((present >> l) & 1u) ? 0 : (l == last && tail < kBlock ? tail : kBlock);
-                            for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
-                                const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
-                                st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
-                            }
-                        }
-                        fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
-                    }
-                }
+                if (warp == 1 && !(ok = zero_v(j, present))) break;
                 tc::fence_before();
                 mbar_arrive(p_full0 + t * 8);
             }

@@ -72,11 +72,10 @@ __device__ inline PrefixItem prefix_item(const PrefixWork& w, int Hkv, int mbps,
     return it;
 }
 
-// Blocks of a split for an even share of `blocks` among `items`, in whole stages.
-__device__ __forceinline__ int prefix_share(long long blocks, long long items) {
-    const long long share = (blocks + items - 1) / items;
-    const long long up = (share + kSplitStep - 1) / kSplitStep * kSplitStep;
-    return (int)(up < kSplitStep ? kSplitStep : up > (1 << 27) ? 1 << 27 : up);  // a table has at most 2^27 blocks
+// Blocks of a split, of whole stages, no shorter than `share`.
+__device__ __forceinline__ int prefix_step(float share) {
+    // (a table has at most 2^27 blocks)
+    return (int)fminf(fmaxf(ceilf(share * (1.f / kSplitStep)), 1.f), (float)((1 << 27) / kSplitStep)) * kSplitStep;
 }
 
 // The SMs that the prefix part takes. The requests' own tokens are read by a
@@ -90,14 +89,13 @@ __device__ __forceinline__ int prefix_share(long long blocks, long long items) {
 // six groups: 37, 93 and 37 us; one after the other 44, 96 and 41; kTileBlock 1
 // or 3: 45, 93, 37 and 38, 126, 44.
 constexpr int kTileBlock = 2;
-__device__ __forceinline__ int prefix_budget(const PrefixWork& w, long long tile_blocks, long long own_blocks) {
-    const long long a = tile_blocks * kTileBlock, b = own_blocks;
-    if (a + b <= 0) return w.sms;
-    const long long least = w.sms - (long long)w.sms * 3 / 4;
-    const long long x = (w.sms * a + (a + b) / 2) / (a + b);
-    return (int)(x < least ? least : x < 1 ? 1 : x);
+__device__ __forceinline__ int prefix_budget(const PrefixWork& w, float tile_blocks, float own_blocks) {
+    const float a = tile_blocks * (float)kTileBlock, b = own_blocks;
+    if (a + b <= 0.f) return w.sms;
+    const int least = max(w.sms - w.sms * 3 / 4, 1), x = (int)((float)w.sms * (a / (a + b)) + 0.5f);
+    return min(max(x, least), w.sms);
 }
-__device__ __forceinline__ long long own_blocks_of(const PrefixWork& w, int b) {
+__device__ __forceinline__ int own_blocks_of(const PrefixWork& w, int b) {
     return (min(max(__ldg(w.own + b), 0), w.own_blocks * kBlock) + kBlock - 1) / kBlock;
 }
 
@@ -133,44 +131,36 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
                 const int units = in ? Hkv * ((s1 - s0 + per - 1) / per) : 0;
                 const int blocks = (min(max(len, 0), mbps * kBlock) + kBlock - 1) / kBlock;
                 if (blockIdx.x == 0 && in && len > mbps * kBlock) raise_err(dev_err, MI_DEVERR_BAD_CONTEXT);
-                auto sum = [](long long v) {
-#pragma unroll
+                auto sum = [](float v) {
+#pragma unroll 1
                     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                     return v;
                 };
-                long long own = 0;
-                for (int b = lane; b < w.B; b += 32) own += Hkv * own_blocks_of(w, b);
-                const long long cost = sum((long long)units * blocks);
-                active = prefix_budget(w, cost, sum(own));
+                float own = 0.f;
+                for (int b = lane; b < w.B; b += 32) own += (float)own_blocks_of(w, b);
+                const float cost = sum((float)units * (float)blocks);
+                active = prefix_budget(w, cost, sum(own) * (float)Hkv);
                 // lane i tries a share of 0.5 + i / 20 of the even one, made
-                // as short as its number of splits of the longest prefix allows
-                const long long share = prefix_share(cost, active), least = prefix_share(cost, 2LL * w.sms);
-                int longest = blocks;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-                longest = max(longest, 1);
-                const int tried = prefix_share(share * (10 + lane), 20);
-                step = (int)max(least, (long long)prefix_share(longest, prefix_splits(longest, tried)));
-                long long items = 0;
+                // as short as its number of splits of the longest prefix
+                // allows; never so short that the slots would not do (the
+                // factor is for the rounding of `cost`)
+                const int longest = max(__reduce_max_sync(0xffffffffu, blocks), 1);
+                const int least = prefix_step(cost * 1.00001f / (float)(2 * w.sms));
+                const int tried = prefix_step(cost / (float)active * (float)(10 + lane) * 0.05f);
+                step = max(least, prefix_step((float)((longest + prefix_splits(longest, tried) - 1) / prefix_splits(longest, tried))));
+                int items = 0;
                 for (int g = 0; g < w.P; ++g)
-                    items += (long long)__shfl_sync(0xffffffffu, units, g) *
-                             prefix_splits(__shfl_sync(0xffffffffu, blocks, g), step);
-                long long time = (items + active - 1) / active * (min(step, longest) + kItemBlocks);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const long long t = __shfl_xor_sync(0xffffffffu, time, o);
-                    const int other = __shfl_xor_sync(0xffffffffu, step, o);
-                    if (t < time || (t == time && other > step)) {
-                        time = t;
-                        step = other;
-                    }
-                }
-                items = (long long)units * prefix_splits(blocks, step);
-                total = sum(items);
-                long long x = items;
-#pragma unroll
+                    items += __shfl_sync(0xffffffffu, units, g) * prefix_splits(__shfl_sync(0xffffffffu, blocks, g), step);
+                // the least time, then the longest split
+                const float time = (float)((items + active - 1) / active) * (float)(min(step, longest) + kItemBlocks);
+                const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(time));
+                step = (int)__reduce_max_sync(0xffffffffu, __float_as_uint(time) == best ? (unsigned)step : 0u);
+                items = units * prefix_splits(blocks, step);
+                total = __reduce_add_sync(0xffffffffu, items);
+                int x = items;
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
                     if (lane >= o) x += y;
                 }
                 sums[lane] = x - items;
@@ -201,11 +191,12 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
         const long long cost = flat_scan(
             w.P, [&](int g) { return (long long)prefix_units(w, Hkv, per, g) * prefix_blocks(w, mbps, g); }, sums);
         __syncthreads();
-        active = prefix_budget(w, cost, Hkv * flat_scan(w.B, [&](int b) { return own_blocks_of(w, b); }, sums));
+        active = prefix_budget(
+            w, (float)cost, (float)(Hkv * flat_scan(w.B, [&](int b) { return (long long)own_blocks_of(w, b); }, sums)));
         __syncthreads();
         auto items = [&](int g) { return prefix_items(w, Hkv, mbps, per, step, g); };
         // an even share
-        step = prefix_share(cost, active);
+        step = prefix_step((float)cost * 1.00001f / (float)active);
         total = flat_scan(w.P, items, sums);
         for (int g = blockIdx.x * nt + tid; g < w.P; g += gridDim.x * nt)
             if (__ldg(w.lens + g) > mbps * kBlock) raise_err(dev_err, MI_DEVERR_BAD_CONTEXT);

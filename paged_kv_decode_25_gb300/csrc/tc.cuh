@@ -192,6 +192,10 @@ __device__ __forceinline__ void st16x128_x16(uint32_t taddr, const uint32_t (&r)
         MI_TC_W8(0), MI_TC_W8(8), MI_TC_W8(16), MI_TC_W8(24)
         : "memory");
 }
+__device__ __forceinline__ void st16x128_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), MI_TC_W8(0)
+                 : "memory");
+}
 #undef MI_TC_R8
 #undef MI_TC_W8
 

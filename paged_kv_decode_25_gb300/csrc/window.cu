@@ -326,17 +326,6 @@ struct Units {
     }
 };
 
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit_ns) {
-    // One vote decides the common case for the whole warp: a branch on each
-    // lane's own answer costs about 130 clocks for its reconvergence alone.
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const unsigned long long t0 = globaltimer();
-    for (;;) {
-        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, kWaitSleepNs))) return true;
-        if (__any_sync(0xffffffffu, (long long)(globaltimer() - t0) > limit_ns)) return false;
-    }
-}
-
 // Whether phase `parity` of the barrier has completed, without waiting.
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;

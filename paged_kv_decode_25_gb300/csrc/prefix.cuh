@@ -84,13 +84,13 @@ __device__ __forceinline__ int prefix_step(float share) {
 // to their work, so that both end together: a (tile, block) of the prefix takes
 // an SM as long as kTileBlock blocks of own tokens. Own tokens get three
 // quarters of the SMs at most: where they are most of the work they are bound by
-// memory, and the prefix part should not wait for them. Measured with 64 chats
-// of 32 to 1,024 tokens behind 4,100, 128 of 16 to 512 behind 32,000, and 90 in
-// six groups: 37, 93 and 37 us; one after the other 44, 96 and 41; kTileBlock 1
-// or 3: 45, 93, 37 and 38, 126, 44.
-constexpr int kTileBlock = 2;
+// memory, and the prefix part should not wait for them. Measured on the device
+// with 64 chats of 32 to 1,024 tokens behind 4,100, 128 of 16 to 512 behind
+// 32,000, and 90 in six groups: 33-36, 86 and 33 us (one part after the other 44,
+// 96 and 41); kTileBlock 1: 35-38, 87, 34; 2: 33-36, 89, 33.
+constexpr float kTileBlock = 1.8f;
 __device__ __forceinline__ int prefix_budget(const PrefixWork& w, float tile_blocks, float own_blocks) {
-    const float a = tile_blocks * (float)kTileBlock, b = own_blocks;
+    const float a = tile_blocks * kTileBlock, b = own_blocks;
     if (a + b <= 0.f) return w.sms;
     const int least = max(w.sms - w.sms * 3 / 4, 1), x = (int)((float)w.sms * (a / (a + b)) + 0.5f);
     return min(max(x, least), w.sms);
@@ -100,15 +100,15 @@ __device__ __forceinline__ int own_blocks_of(const PrefixWork& w, int b) {
 }
 
 // An item's prologue and end count as much as this many blocks of its prefix
-// (7 us, and 2.1 us for 8 blocks).
+// (6 us, and 1.7 us for 8 blocks).
 constexpr int kItemBlocks = 27;
 
 // Plans the call in every block, with all its threads: the blocks of a split
-// in `step`, the grid's blocks that take items (the first ones) in `active`, the items laid end to end in `sums` (two words more than
-// flat_words), their number returned, this block's first one in *mine (shared).
-// Writes the requests' rows. Up to 32 groups one warp does it from one load of
-// each group's numbers: the block's other way, four scans of the list, took
-// 3 us of a call.
+// in `step`, the grid's blocks that take items (the first ones) in `active`,
+// the items laid end to end in `sums` (two words more than flat_words), their
+// number returned, this block's first one in *mine (shared). Writes the
+// requests' rows. Up to 32 groups one warp does it from one load of each group's
+// numbers: the block's other way, four scans of the list, took 3 us of a call.
 __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int mbps, int per, int32_t* dev_err,
                                         long long* sums, int& step, int& active, PrefixItem* mine) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;

@@ -170,6 +170,32 @@ def test_large_values_and_far_parts(cuda_device):
         check(both, 1, [0, 2], [40, 40], q, out, 0.5)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0])
+def test_scales(cuda_device, scale):
+    own = [40, 0, 3, 129]
+    both, ptab, tables = make([700], own, 2, 64, 38)
+    q = both.queries(4, 8)
+    out, err = call(_mi(), cuda_device, both, ptab, [700], [0, 4], tables, own, q, scale)
+    assert err == 0
+    check(both, 1, [0, 4], own, q, out, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("step", [60.0, -60.0, 6.0])
+def test_logits_far_apart(cuda_device, d, step):
+    """Logits that climb or fall along a prefix by hundreds: the reference of a
+    row's sums moves many times, not at all, or once in a while."""
+    own = [5, 200] + [1] * 40
+    both, ptab, tables = make([3000], own, 1, d, 39)
+    q = both.queries(len(own), 8)
+    q[:, :, 0] = 2.0
+    blk, off = both.rows(0)
+    both.k[blk, 0, off, 0] = (torch.arange(3000) // 100 * step).to(torch.bfloat16)
+    out, err = call(_mi(), cuda_device, both, ptab, [3000], [0, len(own)], tables, own, q, 0.5)
+    assert err == 0
+    check(both, 1, [0, len(own)], own, q, out, 0.5)
+
+
 def test_device_errors(cuda_device):
     mi, dev = _mi(), cuda_device
     own = [10, 20, 30]

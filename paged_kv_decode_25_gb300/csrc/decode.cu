@@ -1926,6 +1926,10 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
     // the early warps' part of the blocks
     float part = early > 0 ? (float)(t.prefix.sms - active) / (float)active * (float)prefix * kTileBlock / (float)blocks : 0.f;
     if (!(part < 0.875f)) part = 1.f;
+    // blocks without a piece leave at once: the last of them start when the
+    // prefix part ends, and the merge waits for them all
+    const int doers = part < 1.f ? (int)gridDim.x : early / kTailWarps;
+    if ((int)blockIdx.x >= doers) return;
     auto pieces_of = [&](int n, int step) { return p.Hkv * (((n + kBlock - 1) / kBlock + step - 1) / step); };
     // The blocks of a piece: lane i tries (i + 1) / 16 of a warp's even share.
     // Warps take whole pieces in turn (about blocks / step, and half a piece
@@ -1979,7 +1983,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, kTailBlocks)
         total = (int)flat_scan(p.B, pieces, sums);
     }
     const int split = part < 1.f ? min(total, (int)((float)total * part)) : total;
-    for (int b = blockIdx.x + gridDim.x * tid; b < p.B; b += gridDim.x * kTailWarps * 32)
+    for (int b = blockIdx.x + doers * tid; b < p.B; b += doers * kTailWarps * 32)
         t.rows[b] = make_int2(small ? first_piece[b] : (int)flat_before(p.B, pieces, sums, b),
                               pieces_of(ctx_clamped(p, b), step) / p.Hkv);
     // ---------------------------------------------------------- the pieces --

@@ -140,33 +140,36 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
                 for (int b = lane; b < w.B; b += 32) own += (float)own_blocks_of(w, b);
                 const float cost = sum((float)units * (float)blocks);
                 active = prefix_budget(w, cost, sum(own) * (float)Hkv);
-                // lane i tries a share of 0.5 + i / 20 of the even one, made
-                // as short as its number of splits of the longest prefix
-                // allows; never so short that the slots would not do (the
-                // factor is for the rounding of `cost`)
-                const int longest = max(__reduce_max_sync(0xffffffffu, blocks), 1);
-                const int least = prefix_step(cost * 1.00001f / (float)(2 * w.sms));
-                const int tried = prefix_step(cost / (float)active * (float)(10 + lane) * 0.05f);
-                step = max(least, prefix_step((float)((longest + prefix_splits(longest, tried) - 1) / prefix_splits(longest, tried))));
-                int items = 0;
-                for (int g = 0; g < w.P; ++g)
-                    items += __shfl_sync(0xffffffffu, units, g) * prefix_splits(__shfl_sync(0xffffffffu, blocks, g), step);
-                // the least time, then the longest split
-                const float time = (float)((items + active - 1) / active) * (float)(min(step, longest) + kItemBlocks);
-                const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(time));
-                step = (int)__reduce_max_sync(0xffffffffu, __float_as_uint(time) == best ? (unsigned)step : 0u);
-                items = units * prefix_splits(blocks, step);
-                total = __reduce_add_sync(0xffffffffu, items);
-                int x = items;
+                step = kSplitStep;
+                if ((int)blockIdx.x < active) {  // the others are done, and make room
+                    // lane i tries a share of 0.5 + i / 20 of the even one, made
+                    // as short as its number of splits of the longest prefix
+                    // allows; never so short that the slots would not do (the
+                    // factor is for the rounding of `cost`)
+                    const int longest = max(__reduce_max_sync(0xffffffffu, blocks), 1);
+                    const int least = prefix_step(cost * 1.00001f / (float)(2 * w.sms));
+                    const int tried = prefix_step(cost / (float)active * (float)(10 + lane) * 0.05f);
+                    step = max(least, prefix_step((float)((longest + prefix_splits(longest, tried) - 1) / prefix_splits(longest, tried))));
+                    int items = 0;
+                    for (int g = 0; g < w.P; ++g)
+                        items += __shfl_sync(0xffffffffu, units, g) * prefix_splits(__shfl_sync(0xffffffffu, blocks, g), step);
+                    // the least time, then the longest split
+                    const float time = (float)((items + active - 1) / active) * (float)(min(step, longest) + kItemBlocks);
+                    const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(time));
+                    step = (int)__reduce_max_sync(0xffffffffu, __float_as_uint(time) == best ? (unsigned)step : 0u);
+                    items = units * prefix_splits(blocks, step);
+                    total = __reduce_add_sync(0xffffffffu, items);
+                    int x = items;
 #pragma unroll 1
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, x, o);
+                        if (lane >= o) x += y;
+                    }
+                    sums[lane] = x - items;
+                    if (lane == 31) sums[32] = x;
+                    __syncwarp();
+                    if (lane == 0 && blockIdx.x < total) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
                 }
-                sums[lane] = x - items;
-                if (lane == 31) sums[32] = x;
-                __syncwarp();
-                if (lane == 0 && blockIdx.x < min(total, (long long)active)) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
             }
             if (lane == 0) {
                 sums[33] = step;
@@ -203,8 +206,9 @@ __device__ inline long long prefix_plan(const PrefixWork& w, int Hkv, int G, int
         if (tid == 0 && blockIdx.x < min(total, (long long)active)) *mine = prefix_item(w, Hkv, mbps, per, sums, step, blockIdx.x);
         __syncthreads();
     }
+    if ((int)blockIdx.x >= active) return 0;
     // each request's slots; those outside every group have none
-    for (int b = blockIdx.x + gridDim.x * tid; b < w.B; b += gridDim.x * nt) {
+    for (int b = blockIdx.x + active * tid; b < w.B; b += active * nt) {
         int4 at = make_int4(0, 0, 0, 0);
         if (b >= __ldg(w.starts) && b < prefix_end(w)) {
             int lo = 0, hi = w.P;  // starts[lo] <= b < starts[hi]

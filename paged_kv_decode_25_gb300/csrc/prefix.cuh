@@ -82,17 +82,18 @@ __device__ __forceinline__ int prefix_step(float share) {
 // launch that fills the SMs this one leaves (decode.cu). The two are bound by
 // different things, tensor cores and memory, and share the SMs in proportion
 // to their work, so that both end together: a (tile, block) of the prefix takes
-// an SM as long as kTileBlock blocks of own tokens. Own tokens get three
-// quarters of the SMs at most: where they are most of the work they are bound by
-// memory, and the prefix part should not wait for them. Measured on the device
-// with 64 chats of 32 to 1,024 tokens behind 4,100, 128 of 16 to 512 behind
-// 32,000, and 90 in six groups: 33-36, 86 and 33 us (one part after the other 44,
-// 96 and 41); kTileBlock 1: 35-38, 87, 34; 2: 33-36, 89, 33.
+// an SM as long as kTileBlock blocks of own tokens. Own tokens get 11 of 15 SMs
+// at most: where they are most of the work they are bound by memory, and the
+// prefix part's start alone is 12 us. Measured on the device with 64 chats of 32
+// to 1,024 tokens behind 4,100, 128 of 16 to 512 behind 32,000, and 90 in six
+// groups: 34, 83 and 33 us (one part after the other 44, 96 and 41); kTileBlock
+// 1: 35-38, 87, 34; 2: 34, 90, 33; with 3 of 4 SMs the chats take 37, with 2 of
+// 3 40.
 constexpr float kTileBlock = 1.8f;
 __device__ __forceinline__ int prefix_budget(const PrefixWork& w, float tile_blocks, float own_blocks) {
     const float a = tile_blocks * kTileBlock, b = own_blocks;
     if (a + b <= 0.f) return w.sms;
-    const int least = max(w.sms - w.sms * 3 / 4, 1), x = (int)((float)w.sms * (a / (a + b)) + 0.5f);
+    const int least = max(w.sms - w.sms * 11 / 15, 1), x = (int)((float)w.sms * (a / (a + b)) + 0.5f);
     return min(max(x, least), w.sms);
 }
 __device__ __forceinline__ int own_blocks_of(const PrefixWork& w, int b) {

@@ -890,6 +890,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // item's slot. A group of at most 128 rows runs one Q tile. A block runs
 // its share of the items one after another (one block per SM: blocks without
 // an item would each wait for an SM of their own).
+// A plain stage takes 1.65 us (81 % of the tensor peak; 2.1 with a maximum and
+// masks in its loop), the first one of an item 6 on top of a plan of 4.
 
 constexpr int kT2Keys = 128;                 // keys per stage
 constexpr int kT2Blocks = kT2Keys / kBlock;  // 16-token blocks per stage

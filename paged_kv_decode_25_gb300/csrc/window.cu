@@ -97,6 +97,7 @@ struct WindowParams {
     float* scores;                 // [num_blocks][Hkv][16]
     int32_t* dev_err;
     int R, Hq, Hkv, G, num_blocks, mbps, T, max_q, fresh;
+    int tokens;                    // of a row block: kRows / G
     int xt;                        // kWindow: 128-row halves that hold rows
     int grid;
     float sl2;                     // scale * log2(e), never 0
@@ -107,8 +108,12 @@ struct WindowParams {
 // Request r: n tokens, the last m of them with queries in rows q0 .. q0+m-1;
 // first = n - m (negative: the rows before position 0 see nothing). A request
 // with more queries than the call allows has m = -1 and is left alone.
+// (Divisions by the tokens of a row block are made once: the plans ran for 3 and
+// 5 us with them where they are used.)
 struct Request {
     int n, m, q0, first;
+    int full, rest;  // whole row blocks, tokens of the last one besides
+    int before;      // bounds the row blocks of the requests before this one
 };
 
 __device__ __forceinline__ Request request_of(const WindowParams& p, int r) {
@@ -118,6 +123,9 @@ __device__ __forceinline__ Request request_of(const WindowParams& p, int r) {
     x.n = min(max(__ldg(p.lens + r), 0), p.mbps * kBlock);
     x.first = x.n - x.m;
     if (x.m < 0 || x.m > p.max_q) x.m = -1;
+    x.full = max(x.m, 0) / p.tokens;
+    x.rest = max(x.m, 0) - x.full * p.tokens;
+    x.before = x.q0 / p.tokens + r;
     return x;
 }
 
@@ -125,11 +133,11 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 
 // Blocks of query rows.
 __device__ __forceinline__ int row_blocks(const WindowParams& p, const Request& x) {
-    return x.m > 0 ? ceil_div(x.m, kRows / p.G) : 0;
+    return x.full + (x.rest > 0);
 }
 // 256-key stages that the rows of block rb see.
 __device__ __forceinline__ int seen_stages(const WindowParams& p, const Request& x, int rb) {
-    const int last = x.first + min(x.m, (rb + 1) * (kRows / p.G)) - 1;
+    const int last = x.first + min(x.m, (rb + 1) * p.tokens) - 1;
     return last >= 0 ? last / (2 * kKeys) + 1 : 0;
 }
 
@@ -150,18 +158,23 @@ constexpr int kUnitTiles = 2;     // kWindow: X's copy and the pipeline's start,
 constexpr int kLeastCost = 1024, kLeastTiles = 6;  // of a share
 static_assert(kLeastCost > 4 * kKeys, "a share has part of a stage's end wherever it begins");
 
-__device__ __forceinline__ int block_tokens(const WindowParams& p) { return kRows / p.G; }
 // Row tiles of a request's last row block.
 __device__ __forceinline__ int last_tiles(const WindowParams& p, const Request& x) {
-    const int t = block_tokens(p), rest = x.m % t;
-    return rest > 0 && rest * p.G <= kKeys ? 1 : 2;
+    return x.rest > 0 && x.rest * p.G <= kKeys ? 1 : 2;
 }
 // Cost of one head's first k row blocks.
 __device__ __forceinline__ long long cost_before(const WindowParams& p, const Request& x, int k) {
-    const long long t = block_tokens(p), f = max(x.first, 0), full = min(k, x.m / (int)t);
+    const long long t = p.tokens, f = max(x.first, 0), full = min(k, x.full);
     long long v = full * (kUnitCost + 2 * f) + t * full * (full + 1);
     if (k > full) v += kUnitCost + last_tiles(p, x) * (f + x.m);
     return v;
+}
+// a / d, at most a few hundred
+__device__ __forceinline__ int small_quotient(long long a, long long d) {
+    int q = (int)((float)a / (float)d);
+    while ((q + 1) * d <= a) ++q;
+    while (q * d > a) --q;
+    return q;
 }
 // A unit: its cost from `at` on, `keys` cost units to a stage after `start`.
 struct Cost {
@@ -179,13 +192,12 @@ __device__ __forceinline__ Cost lse_cost(const WindowParams& p, const Request& x
     c.at = begin + p.Hkv * before + h * w;
     c.end = c.at + w;
     c.start = kUnitCost;
-    c.per = 2 * kKeys * (rb == x.m / block_tokens(p) ? last_tiles(p, x) : 2);
+    c.per = 2 * kKeys * (rb == x.full ? last_tiles(p, x) : 2);
     c.stages = seen_stages(p, x, rb);
     return c;
 }
-__device__ __forceinline__ int lse_unit(const WindowParams& p, const Request& x, int r, int rb, int h) {
-    // (q0 / tokens + r bounds the row blocks of the requests before)
-    return h + p.Hkv * (rb + x.q0 / block_tokens(p) + r);
+__device__ __forceinline__ int lse_unit(const WindowParams& p, const Request& x, int rb, int h) {
+    return h + p.Hkv * (rb + x.before);
 }
 template <int MODE>
 __device__ __forceinline__ long long request_cost(const WindowParams& p, int r) {
@@ -211,10 +223,10 @@ struct RowParts {
 __device__ __forceinline__ RowParts row_parts(const WindowParams& p, const Request& x, int r, int rb, int h,
                                               long long share) {
     const Cost c = lse_cost(p, x, rb, h, __ldcg(p.begin + r));
-    const int b0 = (int)((c.at + c.start) / share);
+    const int b0 = small_quotient(c.at + c.start, share);
     RowParts v;
-    v.n = c.stages > 0 ? (int)((c.at + c.start + (c.stages - 1LL) * c.per) / share) - b0 + 1 : 0;
-    v.at = p.part + (long long)(lse_unit(p, x, r, rb, h) + b0) * kRows;
+    v.n = c.stages > 0 ? small_quotient(c.at + c.start + (c.stages - 1LL) * c.per, share) - b0 + 1 : 0;
+    v.at = p.part + (long long)(lse_unit(p, x, rb, h) + b0) * kRows;
     return v;
 }
 // Rows row, row + 32, ..: all of a part's loads at once.
@@ -254,7 +266,7 @@ __device__ __forceinline__ Item sum_item(const WindowParams& p, const long long*
     long long first;
     it.r = flat_find(p.R, [&](int r) { return sum_items(p, r, xkeys); }, sums, i, first);
     it.x = request_of(p, it.r);
-    const int o = (int)(i - first), rp = block_tokens(p) * p.G;
+    const int o = (int)(i - first), rp = p.tokens * p.G;
     it.h = o % p.Hkv;
     it.slot = 0;
     it.row0 = o / p.Hkv * xkeys * kKeys;
@@ -275,7 +287,7 @@ struct Units {
         it.h = h;
         if (MODE == kLse) {
             c = lse_cost(p, it.x, rb, h, first);
-            it.row0 = rb * block_tokens(p) * p.G;
+            it.row0 = rb * p.tokens * p.G;
             it.xt = it.x.m * p.G - it.row0 > kKeys ? 2 : 1;
         } else {
             const int w = kUnitTiles + ceil_div(it.x.n, kKeys);
@@ -301,14 +313,14 @@ struct Units {
             }
         }
         row_block(p, 0);
-        const int h = (int)((pos - c.at) / (c.end - c.at));
+        const int h = small_quotient(pos - c.at, c.end - c.at);
         if (h > 0) row_block(p, h);
     }
     // The unit's stages up to the share's end.
     __device__ __forceinline__ void stages(const WindowParams& p, long long pos, long long stop) {
         it.y0 = c.reaches(pos);
         it.y1 = c.reaches(min(stop, c.end));
-        if (MODE == kLse) it.slot = lse_unit(p, it.x, it.r, rb, it.h) + (int)blockIdx.x;
+        if (MODE == kLse) it.slot = lse_unit(p, it.x, rb, it.h) + (int)blockIdx.x;
     }
     // The next unit, which begins where this one ends (before the share does).
     __device__ __forceinline__ void advance(const WindowParams& p, const long long* sums) {
@@ -537,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (ascend) {
         auto cost = [&](int r) { return request_cost<MODE>(p, r); };
         total = flat_scan(p.R, cost, sums);
-        const long long mine = max((total + gridDim.x - 1) / gridDim.x, (long long)(MODE == kLse ? kLeastCost : kLeastTiles));
+        const long long mine = max((long long)((float)total / (float)gridDim.x * 1.000001f) + 1, (long long)(MODE == kLse ? kLeastCost : kLeastTiles));
         pos = blockIdx.x * mine;
         stop = min(pos + mine, total);
         if (MODE == kLse) {
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         share = __ldcg(p.begin + p.R);
         if (share == 0) total = stop = 0;
     }
-    const int rp = kRows / p.G * p.G;
+    const int rp = p.tokens * p.G;
     // the k-th item of the list as every other warp sees it
     auto take = [&](uint32_t k, Item& it) -> bool {
         const uint32_t sl = k % kItemSlots;
@@ -977,9 +989,9 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Windo
     }
     const Request x = request_of(p, lo);
     if (x.m < 0) return;
-    const int rb = (i - x.q0) / block_tokens(p), h = j / p.G;
+    const int rb = (i - x.q0) / p.tokens, h = j / p.G;
     float v[1];
-    merge_rows(row_parts(p, x, lo, rb, h, share), (i - x.q0 - rb * block_tokens(p)) * p.G + j % p.G, v);
+    merge_rows(row_parts(p, x, lo, rb, h, share), (i - x.q0 - rb * p.tokens) * p.G + j % p.G, v);
     p.nlse[((long long)h * p.T + i) * p.G + j % p.G] = v[0];
 }
 
@@ -1050,6 +1062,7 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     p.Hq = D.Hq;
     p.Hkv = D.Hkv;
     p.G = G;
+    p.tokens = kRows / G;
     p.num_blocks = D.num_blocks;
     p.mbps = D.max_blocks_per_seq;
     p.T = total_q;

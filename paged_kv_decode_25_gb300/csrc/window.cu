@@ -649,8 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++ic;
             if (it.xt == 0) break;
             if (it.y0 >= it.y1) continue;
-            // X goes out at the latest before a wait for Y's ring: an item's
-            // first Y stages may land while the last item still holds X
+            // X goes out first where its place is free, and at the latest
+            // before a wait for Y's ring: an item's first Y stages may land
+            // while the last item still holds X
             const uint32_t xs = xc % kXSlots, xd = sbase + SM::kX + xs * SM::kXBytes;
             const int xblk = MODE == kSum ? entry(it, it.row0 / kKeys, it.xt) : 0;
             bool have_x = false;
@@ -667,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // table entries are read a stage ahead of their use
             constexpr int yt = MODE == kLse ? 2 : 1;  // key tiles of a stage
             int blk = MODE == kSum ? 0 : entry(it, it.y0 * yt, yt);
+            if (__all_sync(0xffffffffu, mbar_test_wait(x_empty + 8 * xs, ((xc / kXSlots) & 1) ^ 1)) && !(ok = load_x())) break;
             for (int j = it.y0; j < it.y1; ++j, ++yc) {
                 const int now = blk;
                 if (MODE != kSum && j + 1 < it.y1) blk = entry(it, (j + 1) * yt, yt);

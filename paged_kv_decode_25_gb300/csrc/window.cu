@@ -49,13 +49,13 @@
 
 #include "batch.cuh"
 #include "tc.cuh"
+#include "window.cuh"
 
 namespace mi {
 namespace {
 
-constexpr int kLse = 0, kSum = 1, kWindow = 2;
-constexpr int kKeys = 128;     // keys of a tile
-constexpr int kRows = 256;     // rows of a block of query rows: whole tokens, kRows / G of them
+using namespace window;
+
 constexpr int kSoftWarps = 16, kQuarters = 4, kMmaWarp = 16, kLoadWarp = 17, kLseWarp = 18;
 constexpr int kThreads = 19 * 32;
 constexpr int kMaskSlots = 16, kLseSlots = 4, kItemSlots = 4;
@@ -86,126 +86,6 @@ struct WinSmem {
     static constexpr int kTotal = kTmem + 16 + 1024;      // slack to align the base to 1024 B
 };
 
-struct WindowParams {
-    const int32_t* tables;         // [R][mbps]
-    const int32_t* lens;           // [R]
-    const int32_t* query_start;    // [R + 1]
-    float* part;                   // [slots][kRows] partial log-sum-exps, base 2 (see Cost)
-    float* nlse;                   // [Hkv][T][G] the rows' negated log-sum-exps (-inf: no key)
-    unsigned int* next;            // kSum: the next item
-    long long* begin;              // [R + 1] the cost before each request, then a block's share (0: bad query_start)
-    float* scores;                 // [num_blocks][Hkv][16]
-    int32_t* dev_err;
-    int R, Hq, Hkv, G, num_blocks, mbps, T, max_q, fresh;
-    int tokens;                    // of a row block: kRows / G
-    int xt;                        // kWindow: 128-row halves that hold rows
-    int grid;
-    float sl2;                     // scale * log2(e), never 0
-    long long wait_ns;
-    int withhold;                  // failure-detection test: the first Y tile of every block is not announced
-};
-
-// Request r: n tokens, the last m of them with queries in rows q0 .. q0+m-1;
-// first = n - m (negative: the rows before position 0 see nothing). A request
-// with more queries than the call allows has m = -1 and is left alone.
-// (Divisions by the tokens of a row block are made once: the plans ran for 3 and
-// 5 us with them where they are used.)
-struct Request {
-    int n, m, q0, first;
-    int full, rest;  // whole row blocks, tokens of the last one besides
-    int before;      // bounds the row blocks of the requests before this one
-};
-
-__device__ __forceinline__ Request request_of(const WindowParams& p, int r) {
-    Request x;
-    x.q0 = __ldg(p.query_start + r);
-    x.m = __ldg(p.query_start + r + 1) - x.q0;
-    x.n = min(max(__ldg(p.lens + r), 0), p.mbps * kBlock);
-    x.first = x.n - x.m;
-    if (x.m < 0 || x.m > p.max_q) x.m = -1;
-    x.full = max(x.m, 0) / p.tokens;
-    x.rest = max(x.m, 0) - x.full * p.tokens;
-    x.before = x.q0 / p.tokens + r;
-    return x;
-}
-
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// Blocks of query rows.
-__device__ __forceinline__ int row_blocks(const WindowParams& p, const Request& x) {
-    return x.full + (x.rest > 0);
-}
-// 256-key stages that the rows of block rb see.
-__device__ __forceinline__ int seen_stages(const WindowParams& p, const Request& x, int rb) {
-    const int last = x.first + min(x.m, (rb + 1) * p.tokens) - 1;
-    return last >= 0 ? last / (2 * kKeys) + 1 : 0;
-}
-
-// The shares of kLse and kWindow. Their work lies end to end as units (request,
-// row block, head), each costing its products and its own start; block b of the
-// grid takes the cost from b to b + 1 shares, wherever that begins and ends
-// within a unit. So all blocks end together (whole splits of equal length, dealt
-// out, left some with a quarter more than the mean), and a row's keys are split
-// only where a share ends. Units and blocks both ascend along the work, so
-// u + b numbers the pairs that meet: the slots of partial log-sum-exps.
-//
-// The cost of kLse is in keys times row tiles, closed in form over a request's
-// row blocks: a prompt has thousands. (Stages round it up; a share may be off by
-// one.)
-constexpr int kUnitCost = 1050;   // X's copy, the pipeline's start, the first maximum, the last tiles' masks: 7,000
-                                  // clocks, where a tile of 256 keys takes 1,700
-constexpr int kUnitTiles = 2;     // kWindow: X's copy and the pipeline's start, in stages
-constexpr int kLeastCost = 1024, kLeastTiles = 6;  // of a share
-static_assert(kLeastCost > 4 * kKeys, "a share has part of a stage's end wherever it begins");
-
-// Row tiles of a request's last row block.
-__device__ __forceinline__ int last_tiles(const WindowParams& p, const Request& x) {
-    return x.rest > 0 && x.rest * p.G <= kKeys ? 1 : 2;
-}
-// Cost of one head's first k row blocks.
-__device__ __forceinline__ long long cost_before(const WindowParams& p, const Request& x, int k) {
-    const long long t = p.tokens, f = max(x.first, 0), full = min(k, x.full);
-    long long v = full * (kUnitCost + 2 * f) + t * full * (full + 1);
-    if (k > full) v += kUnitCost + last_tiles(p, x) * (f + x.m);
-    return v;
-}
-// a / d, at most a few hundred
-__device__ __forceinline__ int small_quotient(long long a, long long d) {
-    int q = (int)((float)a / (float)d);
-    while ((q + 1) * d <= a) ++q;
-    while (q * d > a) --q;
-    return q;
-}
-// A unit: its cost from `at` on, `keys` cost units to a stage after `start`.
-struct Cost {
-    long long at, end;
-    int start, per, stages;
-    // the stage that the work up to c reaches
-    __device__ int reaches(long long c) const {
-        const long long q = c - at - start;
-        return q <= 0 ? 0 : (int)min((long long)stages, (q + per - 1) / per);
-    }
-};
-__device__ __forceinline__ Cost lse_cost(const WindowParams& p, const Request& x, int rb, int h, long long begin) {
-    Cost c;
-    const long long before = cost_before(p, x, rb), w = cost_before(p, x, rb + 1) - before;
-    c.at = begin + p.Hkv * before + h * w;
-    c.end = c.at + w;
-    c.start = kUnitCost;
-    c.per = 2 * kKeys * (rb == x.full ? last_tiles(p, x) : 2);
-    c.stages = seen_stages(p, x, rb);
-    return c;
-}
-__device__ __forceinline__ int lse_unit(const WindowParams& p, const Request& x, int rb, int h) {
-    return h + p.Hkv * (rb + x.before);
-}
-template <int MODE>
-__device__ __forceinline__ long long request_cost(const WindowParams& p, int r) {
-    const Request x = request_of(p, r);
-    if (MODE == kLse) return x.m > 0 ? p.Hkv * cost_before(p, x, row_blocks(p, x)) : 0;
-    return x.m < 0 ? 0 : (long long)p.Hkv * (kUnitTiles + ceil_div(x.n, kKeys));
-}
-
 // One work item: X of xt tiles of 128 (0: the list is over), Y stages y0 .. y1-1.
 struct __align__(16) Item {
     int r, h, xt, y0, y1, row0, slot, pad;  // row0: the first query row (kLse) or key (kSum) of X
@@ -213,22 +93,6 @@ struct __align__(16) Item {
 };
 static_assert(sizeof(Item) <= 64, "an item's place in shared memory");
 
-// The negated log-sum-exp (-inf: no key) of row `row` of a row block, from the
-// blocks that had keys of it: those of its first and last stage, and all between
-// (a share is longer than a stage).
-struct RowParts {
-    const float* at;
-    int n;
-};
-__device__ __forceinline__ RowParts row_parts(const WindowParams& p, const Request& x, int r, int rb, int h,
-                                              long long share) {
-    const Cost c = lse_cost(p, x, rb, h, __ldcg(p.begin + r));
-    const int b0 = small_quotient(c.at + c.start, share);
-    RowParts v;
-    v.n = c.stages > 0 ? small_quotient(c.at + c.start + (c.stages - 1LL) * c.per, share) - b0 + 1 : 0;
-    v.at = p.part + (long long)(lse_unit(p, x, rb, h) + b0) * kRows;
-    return v;
-}
 // Rows row, row + 32, ..: all of a part's loads at once.
 template <int N>
 __device__ __forceinline__ void merge_rows(const RowParts& v, int row, float (&out)[N]) {
@@ -549,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (ascend) {
         auto cost = [&](int r) { return request_cost<MODE>(p, r); };
         total = flat_scan(p.R, cost, sums);
-        const long long mine = max((long long)((float)total / (float)gridDim.x * 1.000001f) + 1, (long long)(MODE == kLse ? kLeastCost : kLeastTiles));
+        const long long mine = even_share(total, gridDim.x, MODE);
         pos = blockIdx.x * mine;
         stop = min(pos + mine, total);
         if (MODE == kLse) {
@@ -997,15 +861,12 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Windo
     p.nlse[((long long)h * p.T + i) * p.G + j % p.G] = v[0];
 }
 
-constexpr int kMostBlocks = 256;  // of the grid, whatever the device has
-
 size_t lse_bytes(const mi_dims& D, int32_t total_q) { return ((size_t)total_q * D.Hq * 4 + 255) / 256 * 256; }
 
 size_t begin_bytes(const mi_dims& D) { return ((size_t)(D.B + 1) * 8 + 255) / 256 * 256; }
 
 size_t window_bytes(const mi_dims& D, int32_t total_q) {
-    const size_t blocks = (size_t)total_q / (kRows / (D.Hq / D.Hkv)) + D.B;
-    return 256 + begin_bytes(D) + lse_bytes(D, total_q) + (D.Hkv * blocks + kMostBlocks) * kRows * 4;
+    return 256 + begin_bytes(D) + lse_bytes(D, total_q) + slots(D.Hkv, D.Hq / D.Hkv, D.B, total_q) * kRows * 4;
 }
 
 bool window_sizes_ok(const mi_dims& D, int32_t total_q, int32_t max_query_len) {
@@ -1079,7 +940,9 @@ extern "C" mi_status mi_paged_prefill_scores(const mi_dims* dims, int32_t total_
     p.wait_ns = test_wait_limit_ns();
     p.withhold = test_withhold_copy() ? 1 : 0;
     CUtensorMap tq, tk;
-    // without queries nothing is loaded through the first map; it may name any tensor
+    // without queries the first map may name any tensor that holds a row of q:
+    // kWindow still loads X for requests that have keys only, and no product of
+    // it is used
     if (!make_tmap_q_group(&tq, total_q > 0 ? q : k_cache, total_q > 0 ? total_q : 1, D.Hq, HD, G, kRows / G * G) ||
         !make_tmap_kv_groups(&tk, k_cache, (long long)D.num_blocks * D.Hkv * kBlock, HD))
         return MI_ERR_CUDA;

@@ -247,3 +247,17 @@ def test_repeat_and_graph(cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(scores, first)
+
+
+@pytest.mark.parametrize("fresh", [False, True])
+@pytest.mark.parametrize("lens,m", [([20000, 40, 30001, 900], [0, 8, 0, 32]), ([40000], [0])])
+def test_long_contexts_without_queries(cuda_device, lens, m, fresh):
+    """Requests with keys and no query tokens, alone (total_q 0) and beside
+    windows: their weights are 0, on both paths."""
+    batch = Batch(lens, 8, 64, 29)
+    q = batch.queries(sum(m), 32)
+    before = torch.rand(batch.num_blocks, 8, BLOCK, generator=batch.gen)
+    for most in (max(m), 300):  # resident rows, resident keys
+        got = before.to(cuda_device)
+        assert call(_mi(), cuda_device, batch, q, 32, starts_of(m), most, got, fresh) == 0
+        check(batch, q, 32, starts_of(m), before, got.cpu(), fresh)

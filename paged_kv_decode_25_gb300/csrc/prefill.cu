@@ -64,7 +64,6 @@ struct PrefillParams {
     float sl2;                     // scale * log2(e)
     long long wait_ns;             // bound on every mbarrier wait of the launch
     int withhold;                  // failure-detection test: each producer withholds its first K copy
-    PrefixWork w;                  // attention over shared prefixes only
 };
 
 // The work item of a CTA: row tile k (counted from the request's end) of
@@ -882,16 +881,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // warp 16 issues the MMAs and owns the tensor memory; warp 17 loads Q once
 // and streams K (two stages, a 2 KB copy per block half) and V (two stages,
 // a 4 KB copy per block), K of stage j before V of stage j - 1.
-//
-// With PREFIX the same pipeline computes attention over shared prefixes (the
-// first launch of mi_paged_decode_attention_prefix): the rows are the (request,
-// head) pairs of up to 256 / G requests of a group, every one sees all keys of
-// the item's split, and each row's fp32 output and log-sum-exp go to the
-// item's slot. A group of at most 128 rows runs one Q tile. A block runs
-// its share of the items one after another (one block per SM: blocks without
-// an item would each wait for an SM of their own).
-// A plain stage takes 1.65 us (81 % of the tensor peak; 2.1 with a maximum and
-// masks in its loop), the first one of an item 6 on top of a plan of 4.
 
 constexpr int kT2Keys = 128;                 // keys per stage
 constexpr int kT2Blocks = kT2Keys / kBlock;  // 16-token blocks per stage
@@ -917,13 +906,448 @@ struct Tc2Smem {
     static constexpr int kTotal = kTmem + 16 + 1024;  // slack to align the base to 1024 B
 };
 
+template <int HD>
+__global__ void __launch_bounds__(kT2Threads, 1)
+    prefill_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv, PrefillParams p) {
+    using SM = Tc2Smem<HD>;
+    constexpr int kH = SM::kH;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    pdl_wait();
+    pdl_trigger();
+
+    // a Q tile holds whole tokens: 128 / G of them, G rows each; the CTA's
+    // two tiles are consecutive, tr rows apart
+    const int tr = (kTcRows / p.G) * p.G;
+    Item it;
+    if (!work_item(p, 2 * tr, it)) return;
+    const int nst = (it.nblk + kT2Blocks - 1) / kT2Blocks;
+    const uint32_t bar = sbase + SM::kBar;
+    const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
+    const uint32_t v_empty0 = v_full0 + 16, s_full0 = v_empty0 + 16, p_full0 = s_full0 + 16;
+    const uint32_t o_done0 = p_full0 + 16, fin = o_done0 + 16;
+    const uint32_t mask0 = sbase + SM::kMask;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(k_full0 + i * 8, 1);
+        for (int i = 0; i < kT2KSlots; ++i) mbar_init(k_empty0 + i * 8, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(v_full0 + i * 8, 1);
+            mbar_init(v_empty0 + i * 8, 1);
+            mbar_init(s_full0 + i * 8, 1);
+            mbar_init(p_full0 + i * 8, 256);  // every softmax thread of the tile
+            mbar_init(o_done0 + i * 8, 1);
+        }
+        mbar_init(fin, 1);
+        fence_mbar_init();
+    }
+    if (warp == kT2MmaWarp) {
+        tc::alloc(sbase + SM::kTmem, kT2Cols);
+        tc::relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tbase = lds_u32(sbase + SM::kTmem);
+
+    if (warp == kT2MmaWarp + 1) {
+        // ------------------------------------------------ producer warp --
+        const uint64_t policy = l2_policy_evict_normal();
+        if (lane == 0 && nst > 0) {
+            mbar_arrive_expect_tx(q_full, 2u * kH * (uint32_t)tr * 128u);
+            for (int t = 0; t < 2; ++t)
+                for (int hh = 0; hh < kH; ++hh)
+                    tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
+                                it.q0 + (it.rho0 + t * tr) / p.G, policy);
+        }
+        int pblk = -1;
+        bool pok = false;
+        auto load_v = [&](int jv) -> bool {
+            const int sl = jv & 1, u = jv >> 1;
+            if (!wait_all(v_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) return false;
+            const uint32_t msk = __ballot_sync(0xffffffffu, pok);
+            const uint32_t fb = v_full0 + sl * 8;
+            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
+            __syncwarp();
+            if (pok) {
+                // one copy per block: both 128-byte halves of its 16 rows
+                const uint32_t vd = sbase + SM::kRingV + sl * SM::kKV + lane * kH * kBlock * 128;
+                const int row0 = (pblk * p.Hkv + it.h) * kBlock;
+                tma_load_3d(vd, &tmv, fb, 0, row0, 0, policy);
+            }
+            return true;
+        };
+        bool pgood = true;
+        // block-table entries are read a stage ahead, before the wait for
+        // the slot, so their load latency is hidden
+        auto table_entry = [&](int jj) -> int {
+            const int x = jj * kT2Blocks + lane;
+            return (lane < kT2Blocks && x < it.nblk) ? __ldg(p.block_tables + (long long)it.r * p.mbps + x) : -1;
+        };
+        int nblk_next = table_entry(0);
+        for (int j = 0; j < nst; ++j) {
+            const int sl = j % kT2KSlots, u = j / kT2KSlots;
+            const int x = j * kT2Blocks + lane;
+            const int blk = nblk_next;
+            if (j + 1 < nst) nblk_next = table_entry(j + 1);
+            if (!wait_all(k_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) {
+                pgood = false;
+                break;
+            }
+            bool ok = false;
+            if (lane < kT2Blocks && x < it.nblk) {
+                ok = blk >= 0 && blk < p.num_blocks;
+                if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+            }
+            const uint32_t msk = __ballot_sync(0xffffffffu, ok);
+            const uint32_t fb = k_full0 + (j & 3) * 8;
+            // failure-detection test: stage 0's K is neither copied nor
+            // announced, so every wait on it runs out
+            const bool held = p.withhold != 0 && j == 0;
+            if (lane == 0 && !held) {
+                sts32(mask0 + (j & 3) * 4, msk);
+                mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
+            }
+            __syncwarp();
+            if (ok && !held) {
+                const uint32_t kd = sbase + SM::kRingK + sl * SM::kKV + lane * kBlock * 128;
+                const int row0 = (blk * p.Hkv + it.h) * kBlock;
+                for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kT2Keys * 128, &tmk, fb, 0, hh, row0, policy);
+            }
+            if (j > 0 && !load_v(j - 1)) {
+                pgood = false;
+                break;
+            }
+            pblk = blk;
+            pok = ok;
+        }
+        if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
+        if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
+    } else if (warp == kT2MmaWarp) {
+        // -------------------------------------------------- MMA issuer --
+        // The whole warp runs the loop; one elected lane issues each MMA
+        // and commit.
+        if (nst > 0) {
+            constexpr uint32_t idS = tc::idesc_bf16(kTcRows, kT2Keys, false);
+            constexpr uint32_t idO = tc::idesc_bf16(kTcRows, HD, true);
+            auto issue_s = [&](int t, int j) {
+                const uint32_t kbase = sbase + SM::kRingK + (j % kT2KSlots) * SM::kKV;
+                const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
+                    const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
+                    const uint64_t bd = tc::sdesc_sw128(kbase + (kk >> 2) * kT2Keys * 128 + off, 16, 1024);
+                    tc::mma_ss_elect(tbase + 256u * t + 128u, a, bd, idS, kk > 0);
+                }
+                tc::commit_elect(s_full0 + t * 8);
+            };
+            auto issue_o = [&](int t, int j) {
+                const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
+                const uint32_t pcol = tbase + 256u * t + 128u;  // P_t(j): bf16 pairs over S_t's first 64 columns
+#pragma unroll
+                for (int l = 0; l < kT2Blocks; ++l) {
+                    // block l: [kH][16 keys][128 B]; the 64-column halves of V
+                    // are kBlock * 128 bytes apart
+                    const uint64_t bd = tc::sdesc_sw128(vbase + l * kH * kBlock * 128, kBlock * 128, 1024);
+                    tc::mma_ts_elect(tbase + 256u * t, pcol + 8u * l, bd, idO, j > 0 || l > 0);
+                }
+                tc::commit_elect(o_done0 + t * 8);
+            };
+            bool ok = wait_all(q_full, 0, p.wait_ns) && wait_all(k_full0, 0, p.wait_ns);
+            if (ok) {
+                tc::fence_after();
+                issue_s(0, 0);
+                issue_s(1, 0);
+                tc::commit_elect(k_empty0);  // K(0) read by both tiles
+            }
+            for (int j = 0; ok && j < nst; ++j) {
+                const uint32_t ph = (uint32_t)(j & 1);
+                ok = wait_all(p_full0, ph, p.wait_ns) &&
+                     wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns);
+                if (!ok) break;
+                tc::fence_after();
+                issue_o(0, j);
+                const bool more = j + 1 < nst;
+                if (more) {
+                    if (!(ok = wait_all(k_full0 + ((j + 1) & 3) * 8, (uint32_t)(((j + 1) >> 2) & 1), p.wait_ns)))
+                        break;
+                    tc::fence_after();
+                    issue_s(0, j + 1);
+                }
+                if (!(ok = wait_all(p_full0 + 8, ph, p.wait_ns))) break;
+                tc::fence_after();
+                issue_o(1, j);
+                tc::commit_elect(v_empty0 + (j & 1) * 8);  // V(j) read by both tiles
+                if (more) {
+                    issue_s(1, j + 1);
+                    tc::commit_elect(k_empty0 + ((j + 1) % kT2KSlots) * 8);
+                }
+            }
+            if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
+            // every MMA issued has finished before tensor memory is released
+            tc::commit_elect(fin);
+            (void)wait_all(fin, 0, drain_limit(p.wait_ns));
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- softmax ----
+        // Eight warps per tile. Warp w reads tensor-memory lanes lb ... lb + 15
+        // (lb = 32 (w mod 4) + 16 (w / 8)) with the 16-lane shapes: lane i
+        // holds rows a = lb + i/4 and b = a + 8, keys 8k + 2 (i mod 4) and the
+        // next one of each 8-key group k, so a quad of lanes shares two rows'
+        // scores (32 keys each per lane) and reduces them with shuffles.
+        const int t = (warp >> 2) & 1;  // tile
+        const int c4 = lane & 3;
+        const int lb = (warp & 3) * 32 + (warp >> 3) * 16;
+        const int rla = lb + (lane >> 2), rlb = rla + 8;  // rows of the tile
+        const int rra = it.rho0 + t * tr + rla, rrb = it.rho0 + t * tr + rlb;
+        const bool va = rla < tr && rra < it.nrows, vb = rlb < tr && rrb < it.nrows;
+        const int toka = rra / p.G, tokb = rrb / p.G;
+        const int posa = va ? it.first + toka : it.p_hi, posb = vb ? it.first + tokb : it.p_hi;
+        const int mposa = posa < 0 ? 0 : posa, mposb = posb < 0 ? 0 : posb;
+        const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
+        const uint32_t ts = tl + 128u;                                // S_t / P_t
+        const int nb_ctx = (it.n + kBlock - 1) / kBlock;
+        const int tail = it.n - (nb_ctx - 1) * kBlock;
+        const bool fold = p.sl2 > 0.f;
+        float mra_run = -INFINITY, mrb_run = -INFINITY, lra = 0.f, lrb = 0.f;  // per lane: its 32 keys of the row
+        bool ok = true;
+        for (int j = 0; j < nst; ++j) {
+            ok = wait_all(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns) &&
+                 wait_all(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns);
+            if (!ok) break;
+            tc::fence_after();
+            uint32_t x[2 * kT2Keys / 4];  // x[4k + e]: e = 0, 1 row a; e = 2, 3 row b
+            tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+            tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+            tc::wait_ld();
+            const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
+            const int kbase = j * kT2Keys;
+            const bool nomask = __all_sync(0xffffffffu, present == (1u << kT2Blocks) - 1u &&
+                                                            kbase + kT2Keys - 1 <= min(mposa, mposb));
+            float alpha_a = 1.f, alpha_b = 1.f, psa, psb;
+            bool need = false;
+            float ma[4], mb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ma[i] = mb[i] = -INFINITY;
+            if (fold && nomask) {
+#pragma unroll
+                for (int k = 0; k < kT2Keys / 8; ++k) {
+                    ma[k & 3] = tc::max3(ma[k & 3], __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+                    mb[k & 3] = tc::max3(mb[k & 3], __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kT2Keys / 8; ++k) {
+                    const bool blk = (present >> (k >> 1)) & 1u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = kbase + 8 * k + 2 * c4 + (e & 1);
+                        const bool keep = blk && key <= (e < 2 ? mposa : mposb);
+                        const float v = keep ? (fold ? __uint_as_float(x[4 * k + e])
+                                                     : __uint_as_float(x[4 * k + e]) * p.sl2)
+                                             : -INFINITY;
+                        x[4 * k + e] = __float_as_uint(v);
+                        if (e < 2)
+                            ma[k & 3] = fmaxf(ma[k & 3], v);
+                        else
+                            mb[k & 3] = fmaxf(mb[k & 3], v);
+                    }
+                }
+            }
+            float mxa = fmaxf(fmaxf(ma[0], ma[1]), fmaxf(ma[2], ma[3]));
+            float mxb = fmaxf(fmaxf(mb[0], mb[1]), fmaxf(mb[2], mb[3]));
+            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+            if (fold) {
+                mxa *= p.sl2;
+                mxb *= p.sl2;
+            }
+            // lazy rescaling, per row: the reference max moves only when the
+            // new max exceeds it by more than 2^8; O and l are rescaled
+            // together (the four lanes of a quad take the same decision)
+            if (mra_run == -INFINITY) {
+                mra_run = mxa;
+            } else if (mxa > mra_run + 8.f) {
+                alpha_a = exp2f(mra_run - mxa);
+                mra_run = mxa;
+                need = true;
+            }
+            if (mrb_run == -INFINITY) {
+                mrb_run = mxb;
+            } else if (mxb > mrb_run + 8.f) {
+                alpha_b = exp2f(mrb_run - mxb);
+                mrb_run = mxb;
+                need = true;
+            }
+            const float una = mra_run == -INFINITY ? 0.f : mra_run;
+            const float unb = mrb_run == -INFINITY ? 0.f : mrb_run;
+            if (fold) {
+                const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
+                const uint64_t nua = tc::f2(-una, -una), nub = tc::f2(-unb, -unb);
+                uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
+#pragma unroll
+                for (int k = 0; k < kT2Keys / 8; ++k) {
+                    const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
+                                                 sc2, nua);
+                    const uint64_t b2 = tc::fma2(
+                        tc::f2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), sc2, nub);
+                    const float ea0 = ex2(tc::f2_lo(a2)), ea1 = ex2(tc::f2_hi(a2));
+                    const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
+                    acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
+                    accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
+                    // P words (column 4k + i mod 4 of rows a and b) over the
+                    // consumed scores
+                    x[2 * k] = pack_bf16x2(ea0, ea1);
+                    x[2 * k + 1] = pack_bf16x2(eb0, eb1);
+                }
+                const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
+                psa = tc::f2_lo(sa) + tc::f2_hi(sa);
+                psb = tc::f2_lo(sb) + tc::f2_hi(sb);
+            } else {
+                float pa[2] = {0.f, 0.f}, pb[2] = {0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < kT2Keys / 8; ++k) {
+                    const float ea0 = ex2(__uint_as_float(x[4 * k]) - una);
+                    const float ea1 = ex2(__uint_as_float(x[4 * k + 1]) - una);
+                    const float eb0 = ex2(__uint_as_float(x[4 * k + 2]) - unb);
+                    const float eb1 = ex2(__uint_as_float(x[4 * k + 3]) - unb);
+                    pa[k & 1] += ea0 + ea1;
+                    pb[k & 1] += eb0 + eb1;
+                    x[2 * k] = pack_bf16x2(ea0, ea1);
+                    x[2 * k + 1] = pack_bf16x2(eb0, eb1);
+                }
+                psa = pa[0] + pa[1];
+                psb = pb[0] + pb[1];
+            }
+            lra = lra * alpha_a + psa;
+            lrb = lrb * alpha_b + psb;
+            if (__any_sync(0xffffffffu, need)) {
+                // O_t may be touched once its previous P . V has finished
+                if (!(ok = wait_all(o_done0 + t * 8, (uint32_t)((j - 1) & 1), p.wait_ns))) break;
+                tc::fence_after();
+#pragma unroll 1
+                for (int ch = 0; ch < HD / 32; ++ch) {
+                    uint32_t y[16];
+                    tc::ld16x256_x4(tl + 32u * ch, y);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = __float_as_uint(__uint_as_float(y[i]) * ((i & 2) ? alpha_b : alpha_a));
+                    tc::st16x256_x4(tl + 32u * ch, y);
+                }
+            }
+            // P_t(j): the A operand of O_t += P_t(j) . V(j)
+            tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
+            tc::wait_st();
+            if (warp == 1) {
+                // V rows of keys outside the context (missing blocks, the
+                // last block's tail) may hold any bits: zero them once the
+                // stage's V copies have landed, before tile 0's P . V (tile
+                // 1's is issued after it). A warp of tile 0 off the MMA
+                // warp's scheduler does it.
+                const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
+                const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
+                if (any) {
+                    if (!(ok = wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns))) break;
+                    const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
+                    for (int l = 0; l < kT2Blocks; ++l) {
+                        const int from = !((present >> l) & 1u) ? 0 : (l == last && tail < kBlock ? tail : kBlock);
+                        for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
+                            const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
+                            st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
+                        }
+                    }
+                    fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
+                }
+            }
+            tc::fence_before();
+            mbar_arrive(p_full0 + t * 8);
+        }
+        if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
+        if (ok && nst > 0) ok = wait_all(o_done0 + t * 8, (uint32_t)((nst - 1) & 1), p.wait_ns);
+        tc::fence_after();
+        lra += __shfl_xor_sync(0xffffffffu, lra, 1);
+        lrb += __shfl_xor_sync(0xffffffffu, lrb, 1);
+        lra += __shfl_xor_sync(0xffffffffu, lra, 2);
+        lrb += __shfl_xor_sync(0xffffffffu, lrb, 2);
+        const float inva = lra > 0.f ? 1.f / lra : 0.f, invb = lrb > 0.f ? 1.f / lrb : 0.f;
+        const uint32_t keepa = posa >= 0 ? 0xFFFFFFFFu : 0u, keepb = posb >= 0 ? 0xFFFFFFFFu : 0u;  // rows before position 0 are +0
+        uint16_t* orowa = p.out + ((long long)(it.q0 + toka) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
+        uint16_t* orowb = p.out + ((long long)(it.q0 + tokb) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
+#pragma unroll 1
+        for (int ch = 0; ch < HD / 32; ++ch) {
+            uint32_t y[16];
+            if (nst > 0 && ok) {
+                tc::ld16x256_x4(tl + 32u * ch, y);
+                tc::wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = 0u;
+            }
+            if (ok) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int col = 32 * ch + 8 * k + 2 * c4;
+                    if (va)
+                        *reinterpret_cast<uint32_t*>(orowa + col) =
+                            pack_bf16x2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva) & keepa;
+                    if (vb)
+                        *reinterpret_cast<uint32_t*>(orowb + col) =
+                            pack_bf16x2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb) &
+                            keepb;
+                }
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kT2MmaWarp) {
+        tc::fence_after();
+        tc::dealloc(tbase, kT2Cols);
+    }
+}
+
+// ---------------------------------------------- shared-prefix attention ----
+//
+// The pipeline of prefill_tc2_kernel for the first launch of
+// mi_paged_decode_attention_prefix: the rows are the (request, head) pairs of up
+// to 256 / G requests of a group, every one sees all keys of the item's split,
+// and each row's fp32 output and log-sum-exp go to the item's slot. A group of
+// at most 128 rows runs one Q tile. A block runs its share of the items one
+// after another (one block per SM: blocks without an item would each wait for an
+// SM of their own).
+// A plain stage takes 1.65 us (81 % of the tensor peak; 2.1 with a maximum and
+// masks in its loop), the first one of an item 6 on top of a plan of 4.
+// (A kernel of its own: as one template with the causal one, whose launches then
+// carried this plan's arguments too, it cost that one 1.1 % of its time: 0.3828 to
+// 0.3872 ms for a layer of 8 prompts of 512 to 2,048 tokens and 8 chunks of 512
+// behind 1,024 to 8,192; the arguments alone 0.7 %.)
+
+struct PrefixParams {
+    const int32_t* tables;         // [P][mbps] the prefixes' blocks
+    int32_t* dev_err;
+    int Hkv, G, num_blocks, mbps;
+    float sl2;                     // scale * log2(e)
+    long long wait_ns;             // bound on every mbarrier wait of the launch
+    int withhold;                  // failure-detection test: each item's producer withholds its first K copy
+    PrefixWork w;
+};
+
 // Two rows' running reference exponent and sum (per lane: its 32 keys).
 struct RowSums {
     float ma, mb, la, lb;
     bool ok;
 };
 
-// PREFIX: a stage whose rows have no reference yet, or have outgrown it, or
+// A stage whose rows have no reference yet, or have outgrown it, or
 // with keys that do not count (all but the first `left`, and those of absent
 // blocks): masks, takes the maximum, moves O and the sums to it and writes P.
 // A function of its own, as few stages need it and the plain stage's loop is
@@ -1004,65 +1428,44 @@ __device__ __noinline__ RowSums whole_stage(uint32_t tl, uint32_t present, int l
     return r;
 }
 
-template <int HD, bool PREFIX = false>
+template <int HD>
 __global__ void __launch_bounds__(kT2Threads, 1)
-    prefill_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, PrefillParams p) {
+    prefix_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, PrefixParams p) {
     using SM = Tc2Smem<HD>;
     constexpr int kH = SM::kH;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (PREFIX && warp == kT2MmaWarp) {  // ahead of the plan
+    if (warp == kT2MmaWarp) {  // ahead of the plan
         tc::alloc(sbase + SM::kTmem, kT2Cols);
         tc::relinquish();
     }
     pdl_wait();
     pdl_trigger();
 
-    // a Q tile holds whole tokens: 128 / G of them, G rows each; the CTA's
+    // a Q tile holds whole requests: 128 / G of them, G rows each; an item's
     // two tiles are consecutive, tr rows apart
     const int tr = (kTcRows / p.G) * p.G;
-    long long items = 1, item = 0;  // PREFIX: the plan's, and this block's
-    int step = 0, stride = 1;
-    __shared__ long long sums[PREFIX ? flat_words(kT2Threads) + 2 : 1];
+    int step, stride;
+    __shared__ long long sums[flat_words(kT2Threads) + 2];
     __shared__ PrefixItem pick;
-    if constexpr (PREFIX) {
-        items = prefix_plan(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, step, stride, &pick);
-        item = blockIdx.x < stride ? blockIdx.x : items;
-    }
-    uint32_t tbase = PREFIX ? lds_u32(sbase + SM::kTmem) : 0u;
+    const long long items = prefix_plan(p.w, p.Hkv, p.G, p.mbps, 2 * tr / p.G, p.dev_err, sums, step, stride, &pick);
+    long long item = blockIdx.x < stride ? blockIdx.x : items;
+    uint32_t tbase = lds_u32(sbase + SM::kTmem);
     bool bad = false;  // a wait ran out
     for (bool first = true; item < items; item += stride, first = false) {
-        Item it;
-        const int32_t* table;  // of the item's keys
-        int slot = 0;
-        bool two = true;       // both Q tiles hold rows
-        if constexpr (PREFIX) {
-            if (!first) {
-                if (threadIdx.x == 0) pick = prefix_item(p.w, p.Hkv, p.mbps, 2 * tr / p.G, sums, step, item);
-                __syncthreads();
-            }
-            const PrefixItem x = pick;
-            it.r = x.g;
-            it.h = x.h;
-            it.q0 = x.b0;
-            it.m = x.count;
-            it.n = x.n;
-            it.first = 0;
-            it.rho0 = 0;
-            it.nrows = it.rows_here = x.count * p.G;
-            it.p_hi = x.n - 1;
-            it.nblk = (x.n + kBlock - 1) / kBlock;
-            table = p.block_tables + (long long)x.g * p.mbps + x.blk0;
-            slot = x.slot;
-            two = it.nrows > tr;
-        } else {
-            if (!work_item(p, 2 * tr, it)) return;
-            table = p.block_tables + (long long)it.r * p.mbps;
+        if (!first) {
+            if (threadIdx.x == 0) pick = prefix_item(p.w, p.Hkv, p.mbps, 2 * tr / p.G, sums, step, item);
+            __syncthreads();
         }
-        const int nst = (it.nblk + kT2Blocks - 1) / kT2Blocks;
+        const PrefixItem it = pick;
+        const int32_t* table = p.tables + (long long)it.g * p.mbps + it.blk0;  // of the item's keys
+        const int nrows = it.count * p.G;
+        const bool two = nrows > tr;  // both Q tiles hold rows
+        const int nblk = (it.n + kBlock - 1) / kBlock;
+        const int nst = (nblk + kT2Blocks - 1) / kT2Blocks;
         const uint32_t bar = sbase + SM::kBar;
         const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
         const uint32_t v_empty0 = v_full0 + 16, s_full0 = v_empty0 + 16, p_full0 = s_full0 + 16;
@@ -1079,15 +1482,11 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 mbar_init(v_full0 + i * 8, 1);
                 mbar_init(v_empty0 + i * 8, 1);
                 mbar_init(s_full0 + i * 8, 1);
-                mbar_init(p_full0 + i * 8, PREFIX ? 8 : 256);  // every softmax warp or thread of the tile
+                mbar_init(p_full0 + i * 8, 8);  // every softmax warp of the tile
                 mbar_init(o_done0 + i * 8, 1);
             }
             mbar_init(fin, 1);
             fence_mbar_init();
-        }
-        if (!PREFIX && warp == kT2MmaWarp) {
-            tc::alloc(sbase + SM::kTmem, kT2Cols);
-            tc::relinquish();
         }
         tc::fence_before();
         __syncthreads();
@@ -1102,7 +1501,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 for (int t = 0; t < (two ? 2 : 1); ++t)
                     for (int hh = 0; hh < kH; ++hh)
                         tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
-                                    it.q0 + (it.rho0 + t * tr) / p.G, policy);
+                                    it.b0 + t * tr / p.G, policy);
             }
             int pblk = -1;
             bool pok = false;
@@ -1126,7 +1525,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             // the slot, so their load latency is hidden
             auto table_entry = [&](int jj) -> int {
                 const int x = jj * kT2Blocks + lane;
-                return (lane < kT2Blocks && x < it.nblk) ? __ldg(table + x) : -1;
+                return (lane < kT2Blocks && x < nblk) ? __ldg(table + x) : -1;
             };
             int nblk_next = table_entry(0);
             for (int j = 0; j < nst; ++j) {
@@ -1139,7 +1538,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     break;
                 }
                 bool ok = false;
-                if (lane < kT2Blocks && x < it.nblk) {
+                if (lane < kT2Blocks && x < nblk) {
                     ok = blk >= 0 && blk < p.num_blocks;
                     if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
                 }
@@ -1178,7 +1577,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 auto issue_s = [&](int t, int j) {
                     const uint32_t kbase = sbase + SM::kRingK + (j % kT2KSlots) * SM::kKV;
                     const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
-    #pragma unroll(PREFIX ? 2 : HD / 16)
+#pragma unroll 2
                     for (int kk = 0; kk < HD / 16; ++kk) {
                         const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
                         const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
@@ -1190,7 +1589,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 auto issue_o = [&](int t, int j) {
                     const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
                     const uint32_t pcol = tbase + 256u * t + 128u;  // P_t(j): bf16 pairs over S_t's first 64 columns
-    #pragma unroll(PREFIX ? 2 : kT2Blocks)
+#pragma unroll 2
                     for (int l = 0; l < kT2Blocks; ++l) {
                         // block l: [kH][16 keys][128 B]; the 64-column halves of V
                         // are kBlock * 128 bytes apart
@@ -1252,24 +1651,18 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             const int c4 = lane & 3;
             const int lb = (warp & 3) * 32 + (warp >> 3) * 16;
             const int rla = lb + (lane >> 2), rlb = rla + 8;  // rows of the tile
-            const int rra = it.rho0 + t * tr + rla, rrb = it.rho0 + t * tr + rlb;
-            const bool va = rla < tr && rra < it.nrows, vb = rlb < tr && rrb < it.nrows;
-            const int toka = rra / p.G, tokb = rrb / p.G;
-            const int posa = va && !PREFIX ? it.first + toka : it.p_hi, posb = vb && !PREFIX ? it.first + tokb : it.p_hi;
-            const int mposa = posa < 0 ? 0 : posa, mposb = posb < 0 ? 0 : posb;
+            const bool va = rla < tr && t * tr + rla < nrows, vb = rlb < tr && t * tr + rlb < nrows;
             const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
             const uint32_t ts = tl + 128u;                                // S_t / P_t
-            const int nb_ctx = (it.n + kBlock - 1) / kBlock;
-            const int tail = it.n - (nb_ctx - 1) * kBlock;
+            const int tail = it.n - (nblk - 1) * kBlock;
             const bool fold = p.sl2 > 0.f;
-            float mra_run = -INFINITY, mrb_run = -INFINITY, lra = 0.f, lrb = 0.f;  // per lane: its 32 keys of the row
             bool ok = true;
             // V rows of keys outside the context (missing blocks, the last
             // block's tail) may hold any bits: zero them once the stage's V
             // copies have landed, before tile 0's P . V (tile 1's is issued
             // after it). A warp of tile 0 off the MMA warp's scheduler does it.
             auto zero_v = [&](int j, uint32_t present) -> bool {
-                const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
+                const int last = nblk - 1 - j * kT2Blocks;  // the context's last block, stage-local
                 const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
                 if (any) {
                     if (!wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns)) return false;
@@ -1285,145 +1678,30 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 }
                 return true;
             };
-            if constexpr (PREFIX) {
-                // Every row sees every key, so a stage is plain but for an
-                // item's last: exponentials relative to the row's reference,
-                // no maximum. The reference is the first stage's maximum; it
-                // moves when a sum passes 2^60 (bf16 and fp32 hold the
-                // probabilities and sums below that as well as below 1).
-                RowSums r = {-INFINITY, -INFINITY, 0.f, 0.f, true};
-                bool steady = false;  // the warp's rows have references
-                const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
-                for (int j = 0; j < nst; ++j) {
-                    ok = wait_warp(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns) &&
-                         wait_warp(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns);  // (the mask's)
-                    if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
-                    const int left = it.n - j * kT2Keys;
-                    bool done = false;
-                    if (steady && present == (1u << kT2Blocks) - 1u && left >= kT2Keys) {
-                        uint32_t x[2 * kT2Keys / 4];
-                        tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-                        tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-                        tc::wait_ld();
-                        const uint64_t nua = tc::f2(-r.ma, -r.ma), nub = tc::f2(-r.mb, -r.mb);
-                        uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
-    #pragma unroll
-                        for (int k = 0; k < kT2Keys / 8; ++k) {
-                            const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
-                                                         sc2, nua);
-                            const uint64_t b2 = tc::fma2(
-                                tc::f2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), sc2, nub);
-                            const float ea0 = ex2(tc::f2_lo(a2)), ea1 = ex2(tc::f2_hi(a2));
-                            const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
-                            acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
-                            accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
-                            x[2 * k] = pack_bf16x2(ea0, ea1);
-                            x[2 * k + 1] = pack_bf16x2(eb0, eb1);
-                        }
-                        const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
-                        const float psa = tc::f2_lo(sa) + tc::f2_hi(sa), psb = tc::f2_lo(sb) + tc::f2_hi(sb);
-                        if (!__any_sync(0xffffffffu, (va && psa > 0x1p60f) || (vb && psb > 0x1p60f))) {
-                            r.la += psa;
-                            r.lb += psb;
-                            tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
-                            tc::wait_st();
-                            done = true;
-                        }
-                    }
-                    if (!done) {
-                        r = whole_stage<HD>(tl, present, left, p.sl2, r, o_done0 + t * 8, (uint32_t)((j - 1) & 1), p.wait_ns);
-                        if (!(ok = r.ok)) break;
-                        steady = fold && !__any_sync(0xffffffffu, (va && r.ma == -INFINITY) || (vb && r.mb == -INFINITY));
-                    }
-                    if (warp == 1 && !(ok = zero_v(j, present))) break;
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full0 + t * 8);
-                }
-                mra_run = r.ma;
-                mrb_run = r.mb;
-                lra = r.la;
-                lrb = r.lb;
-            }
-            for (int j = 0; !PREFIX && j < nst; ++j) {
-                ok = wait_all(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns) &&
-                     wait_all(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns);
+            // Every row sees every key, so a stage is plain but for an
+            // item's last: exponentials relative to the row's reference,
+            // no maximum. The reference is the first stage's maximum; it
+            // moves when a sum passes 2^60 (bf16 and fp32 hold the
+            // probabilities and sums below that as well as below 1).
+            RowSums r = {-INFINITY, -INFINITY, 0.f, 0.f, true};
+            bool steady = false;  // the warp's rows have references
+            const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
+            for (int j = 0; j < nst; ++j) {
+                ok = wait_warp(s_full0 + t * 8, (uint32_t)(j & 1), p.wait_ns) &&
+                     wait_warp(k_full0 + (j & 3) * 8, (uint32_t)((j >> 2) & 1), p.wait_ns);  // (the mask's)
                 if (!ok) break;
                 tc::fence_after();
-                uint32_t x[2 * kT2Keys / 4];  // x[4k + e]: e = 0, 1 row a; e = 2, 3 row b
-                tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-                tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-                tc::wait_ld();
                 const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
-                const int kbase = j * kT2Keys;
-                const bool nomask = __all_sync(0xffffffffu, present == (1u << kT2Blocks) - 1u &&
-                                                                kbase + kT2Keys - 1 <= min(mposa, mposb));
-                float alpha_a = 1.f, alpha_b = 1.f, psa, psb;
-                bool need = false;
-                float ma[4], mb[4];
-    #pragma unroll
-                for (int i = 0; i < 4; ++i) ma[i] = mb[i] = -INFINITY;
-                if (fold && nomask) {
-    #pragma unroll
-                    for (int k = 0; k < kT2Keys / 8; ++k) {
-                        ma[k & 3] = tc::max3(ma[k & 3], __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
-                        mb[k & 3] = tc::max3(mb[k & 3], __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
-                    }
-                } else {
-    #pragma unroll
-                    for (int k = 0; k < kT2Keys / 8; ++k) {
-                        const bool blk = (present >> (k >> 1)) & 1u;
-    #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = kbase + 8 * k + 2 * c4 + (e & 1);
-                            const bool keep = blk && key <= (e < 2 ? mposa : mposb);
-                            const float v = keep ? (fold ? __uint_as_float(x[4 * k + e])
-                                                         : __uint_as_float(x[4 * k + e]) * p.sl2)
-                                                 : -INFINITY;
-                            x[4 * k + e] = __float_as_uint(v);
-                            if (e < 2)
-                                ma[k & 3] = fmaxf(ma[k & 3], v);
-                            else
-                                mb[k & 3] = fmaxf(mb[k & 3], v);
-                        }
-                    }
-                }
-                float mxa = fmaxf(fmaxf(ma[0], ma[1]), fmaxf(ma[2], ma[3]));
-                float mxb = fmaxf(fmaxf(mb[0], mb[1]), fmaxf(mb[2], mb[3]));
-                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
-                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
-                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-                if (fold) {
-                    mxa *= p.sl2;
-                    mxb *= p.sl2;
-                }
-                // lazy rescaling, per row: the reference max moves only when the
-                // new max exceeds it by more than 2^8; O and l are rescaled
-                // together (the four lanes of a quad take the same decision)
-                if (mra_run == -INFINITY) {
-                    mra_run = mxa;
-                } else if (mxa > mra_run + 8.f) {
-                    alpha_a = exp2f(mra_run - mxa);
-                    mra_run = mxa;
-                    need = true;
-                }
-                if (mrb_run == -INFINITY) {
-                    mrb_run = mxb;
-                } else if (mxb > mrb_run + 8.f) {
-                    alpha_b = exp2f(mrb_run - mxb);
-                    mrb_run = mxb;
-                    need = true;
-                }
-                const float una = mra_run == -INFINITY ? 0.f : mra_run;
-                const float unb = mrb_run == -INFINITY ? 0.f : mrb_run;
-                if (fold) {
-                    const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
-                    const uint64_t nua = tc::f2(-una, -una), nub = tc::f2(-unb, -unb);
+                const int left = it.n - j * kT2Keys;
+                bool done = false;
+                if (steady && present == (1u << kT2Blocks) - 1u && left >= kT2Keys) {
+                    uint32_t x[2 * kT2Keys / 4];
+                    tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                    tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                    tc::wait_ld();
+                    const uint64_t nua = tc::f2(-r.ma, -r.ma), nub = tc::f2(-r.mb, -r.mb);
                     uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < kT2Keys / 8; ++k) {
                         const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
                                                      sc2, nua);
@@ -1433,122 +1711,67 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                         const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
                         acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
                         accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
-                        // P words (column 4k + i mod 4 of rows a and b) over the
-                        // consumed scores
                         x[2 * k] = pack_bf16x2(ea0, ea1);
                         x[2 * k + 1] = pack_bf16x2(eb0, eb1);
                     }
                     const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
-                    psa = tc::f2_lo(sa) + tc::f2_hi(sa);
-                    psb = tc::f2_lo(sb) + tc::f2_hi(sb);
-                } else {
-                    float pa[2] = {0.f, 0.f}, pb[2] = {0.f, 0.f};
-    #pragma unroll
-                    for (int k = 0; k < kT2Keys / 8; ++k) {
-                        const float ea0 = ex2(__uint_as_float(x[4 * k]) - una);
-                        const float ea1 = ex2(__uint_as_float(x[4 * k + 1]) - una);
-                        const float eb0 = ex2(__uint_as_float(x[4 * k + 2]) - unb);
-                        const float eb1 = ex2(__uint_as_float(x[4 * k + 3]) - unb);
-                        pa[k & 1] += ea0 + ea1;
-                        pb[k & 1] += eb0 + eb1;
-                        x[2 * k] = pack_bf16x2(ea0, ea1);
-                        x[2 * k + 1] = pack_bf16x2(eb0, eb1);
-                    }
-                    psa = pa[0] + pa[1];
-                    psb = pb[0] + pb[1];
-                }
-                lra = lra * alpha_a + psa;
-                lrb = lrb * alpha_b + psb;
-                if (__any_sync(0xffffffffu, need)) {
-                    // O_t may be touched once its previous P . V has finished
-                    if (!(ok = wait_all(o_done0 + t * 8, (uint32_t)((j - 1) & 1), p.wait_ns))) break;
-                    tc::fence_after();
-    #pragma unroll 1
-                    for (int ch = 0; ch < HD / 32; ++ch) {
-                        uint32_t y[16];
-                        tc::ld16x256_x4(tl + 32u * ch, y);
-                        tc::wait_ld();
-    #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            y[i] = __float_as_uint(__uint_as_float(y[i]) * ((i & 2) ? alpha_b : alpha_a));
-                        tc::st16x256_x4(tl + 32u * ch, y);
+                    const float psa = tc::f2_lo(sa) + tc::f2_hi(sa), psb = tc::f2_lo(sb) + tc::f2_hi(sb);
+                    if (!__any_sync(0xffffffffu, (va && psa > 0x1p60f) || (vb && psb > 0x1p60f))) {
+                        r.la += psa;
+                        r.lb += psb;
+                        tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
+                        tc::wait_st();
+                        done = true;
                     }
                 }
-                // P_t(j): the A operand of O_t += P_t(j) . V(j)
-                tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
-                tc::wait_st();
+                if (!done) {
+                    r = whole_stage<HD>(tl, present, left, p.sl2, r, o_done0 + t * 8, (uint32_t)((j - 1) & 1), p.wait_ns);
+                    if (!(ok = r.ok)) break;
+                    steady = fold && !__any_sync(0xffffffffu, (va && r.ma == -INFINITY) || (vb && r.mb == -INFINITY));
+                }
                 if (warp == 1 && !(ok = zero_v(j, present))) break;
                 tc::fence_before();
-                mbar_arrive(p_full0 + t * 8);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full0 + t * 8);
             }
             bad |= !ok;
             if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             if (ok && nst > 0) ok = wait_all(o_done0 + t * 8, (uint32_t)((nst - 1) & 1), p.wait_ns);
             bad |= !ok;
             tc::fence_after();
-            lra += __shfl_xor_sync(0xffffffffu, lra, 1);
-            lrb += __shfl_xor_sync(0xffffffffu, lrb, 1);
-            lra += __shfl_xor_sync(0xffffffffu, lra, 2);
-            lrb += __shfl_xor_sync(0xffffffffu, lrb, 2);
-            const float inva = lra > 0.f ? 1.f / lra : 0.f, invb = lrb > 0.f ? 1.f / lrb : 0.f;
-            if constexpr (PREFIX) {
-                const long long row = (long long)slot * (2 * tr) + t * tr + rla;  // row b: 8 further
-                float* pa = p.w.part + row * HD + 2 * c4;
-    #pragma unroll 1
-                for (int ch = 0; ch < HD / 32; ++ch) {
-                    uint32_t y[16];
-                    if (!ok) break;
-                    tc::ld16x256_x4(tl + 32u * ch, y);
-                    tc::wait_ld();
-    #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float* at = pa + 32 * ch + 8 * k;
-                        if (va)
-                            *reinterpret_cast<float2*>(at) =
-                                make_float2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva);
-                        if (vb)
-                            *reinterpret_cast<float2*>(at + 8 * HD) =
-                                make_float2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb);
-                    }
-                }
-                if (c4 == 0 && ok) {
-                    if (va) p.w.part_lse[row] = lra > 0.f ? mra_run + log2f(lra) : -INFINITY;
-                    if (vb) p.w.part_lse[row + 8] = lrb > 0.f ? mrb_run + log2f(lrb) : -INFINITY;
-                }
-            } else {
-            const uint32_t keepa = posa >= 0 ? 0xFFFFFFFFu : 0u, keepb = posb >= 0 ? 0xFFFFFFFFu : 0u;  // rows before position 0 are +0
-            uint16_t* orowa = p.out + ((long long)(it.q0 + toka) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
-            uint16_t* orowb = p.out + ((long long)(it.q0 + tokb) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
-    #pragma unroll 1
+            r.la += __shfl_xor_sync(0xffffffffu, r.la, 1);
+            r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 1);
+            r.la += __shfl_xor_sync(0xffffffffu, r.la, 2);
+            r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 2);
+            const float inva = r.la > 0.f ? 1.f / r.la : 0.f, invb = r.lb > 0.f ? 1.f / r.lb : 0.f;
+            const long long row = (long long)it.slot * (2 * tr) + t * tr + rla;  // row b: 8 further
+            float* pa = p.w.part + row * HD + 2 * c4;
+#pragma unroll 1
             for (int ch = 0; ch < HD / 32; ++ch) {
                 uint32_t y[16];
-                if (nst > 0 && ok) {
-                    tc::ld16x256_x4(tl + 32u * ch, y);
-                    tc::wait_ld();
-                } else {
-    #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = 0u;
-                }
-                if (ok) {
-    #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int col = 32 * ch + 8 * k + 2 * c4;
-                        if (va)
-                            *reinterpret_cast<uint32_t*>(orowa + col) =
-                                pack_bf16x2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva) & keepa;
-                        if (vb)
-                            *reinterpret_cast<uint32_t*>(orowb + col) =
-                                pack_bf16x2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb) &
-                                keepb;
-                    }
+                if (!ok) break;
+                tc::ld16x256_x4(tl + 32u * ch, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float* at = pa + 32 * ch + 8 * k;
+                    if (va)
+                        *reinterpret_cast<float2*>(at) =
+                            make_float2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva);
+                    if (vb)
+                        *reinterpret_cast<float2*>(at + 8 * HD) =
+                            make_float2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb);
                 }
             }
+            if (c4 == 0 && ok) {
+                if (va) p.w.part_lse[row] = r.la > 0.f ? r.ma + log2f(r.la) : -INFINITY;
+                if (vb) p.w.part_lse[row + 8] = r.lb > 0.f ? r.mb + log2f(r.lb) : -INFINITY;
             }
         }
         // the next item starts its barriers afresh; after a wait that ran out
         // copies may still be under way, and nothing more is started
         tc::fence_before();
-        if (!PREFIX || __syncthreads_or(bad)) break;
+        if (__syncthreads_or(bad)) break;
     }
     tc::fence_before();
     __syncthreads();
@@ -1580,11 +1803,18 @@ bool prepare_tc() {
     return raise_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<HD>), TcSmem<HD>::kTotal, done, mu);
 }
 
-template <int HD, bool PREFIX = false>
+template <int HD>
 bool prepare_tc2() {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD, PREFIX>), Tc2Smem<HD>::kTotal, done, mu);
+    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD>), Tc2Smem<HD>::kTotal, done, mu);
+}
+
+template <int HD>
+bool prepare_prefix() {
+    static std::mutex mu;
+    static CUcontext done[256] = {};
+    return raise_smem_once(reinterpret_cast<const void*>(prefix_tc2_kernel<HD>), Tc2Smem<HD>::kTotal, done, mu);
 }
 
 template <int HD>
@@ -1691,27 +1921,19 @@ mi_status prefix_partials(const mi_dims* dims, int32_t max_prefix_blocks, const 
                           long long slots, int32_t* dev_err, mi_stream_t stream) {
     const mi_dims D = *dims;
     const int G = D.Hq / D.Hkv, HD = D.head_dim;
-    PrefillParams p;
-    p.q = static_cast<const uint16_t*>(q);
-    p.block_tables = prefix_tables;
-    p.context_lens = nullptr;
-    p.query_start = nullptr;
-    p.out = nullptr;
+    PrefixParams p;
+    p.tables = prefix_tables;
     p.dev_err = dev_err;
-    p.R = work.P;
-    p.Hq = D.Hq;
     p.Hkv = D.Hkv;
     p.G = G;
     p.num_blocks = D.num_blocks;
     p.mbps = max_prefix_blocks;
-    p.T = D.B;
-    p.max_q = 0;
     p.sl2 = scale * 1.4426950408889634f;
     p.wait_ns = test_wait_limit_ns();
     p.withhold = test_withhold_copy() ? 1 : 0;
     p.w = work;
     const long long rows = (long long)D.num_blocks * D.Hkv * kBlock;
-    if (!(HD == 64 ? prepare_tc2<64, true>() : prepare_tc2<128, true>())) return MI_ERR_CUDA;
+    if (!(HD == 64 ? prepare_prefix<64>() : prepare_prefix<128>())) return MI_ERR_CUDA;
     CUtensorMap tq, tk, tv;
     if (!make_tmap_q_group(&tq, q, D.B, D.Hq, HD, G, (kTcRows / G) * G) ||
         !make_tmap_kv_halves(&tk, k_cache, rows, HD) || !make_tmap_kv_blocks(&tv, v_cache, rows, HD))
@@ -1719,9 +1941,8 @@ mi_status prefix_partials(const mi_dims* dims, int32_t max_prefix_blocks, const 
     const int grid = (int)(slots < work.sms ? slots : work.sms);
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e =
-        HD == 64 ? launch_pdl(prefill_tc2_kernel<64, true>, grid, kT2Threads, Tc2Smem<64>::kTotal, st, tq, tk, tv, p)
-                 : launch_pdl(prefill_tc2_kernel<128, true>, grid, kT2Threads, Tc2Smem<128>::kTotal, st, tq, tk,
-                              tv, p);
+        HD == 64 ? launch_pdl(prefix_tc2_kernel<64>, grid, kT2Threads, Tc2Smem<64>::kTotal, st, tq, tk, tv, p)
+                 : launch_pdl(prefix_tc2_kernel<128>, grid, kT2Threads, Tc2Smem<128>::kTotal, st, tq, tk, tv, p);
     return e == cudaSuccess ? MI_OK : MI_ERR_CUDA;
 }
 

@@ -141,6 +141,16 @@ __device__ __forceinline__ bool wait_pf(uint32_t bar, uint32_t parity, long long
     return mbar_wait_bounded(bar, parity, limit_ns, kWaitSleepNs);
 }
 
+// The end of a CTA in which some wait ran out: copies may be under way that no
+// warp waits for any more, and none may outlive the shared memory it writes. They
+// take microseconds and get 10 ms. (Waiting on the barriers of those announced
+// needs their numbers kept in the producer's loop, which cost these kernels 0.3
+// to 1.5 % of their time in four forms tried; this costs 0.1 %.)
+__device__ __forceinline__ void let_copies_land() {
+    const unsigned long long t0 = globaltimer();
+    while ((long long)(globaltimer() - t0) < kDrainMinNs) __nanosleep(20000);
+}
+
 template <int HD>
 __global__ void __launch_bounds__((kPWarps + 1) * 32, kMT == 1 ? 2 : 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -547,6 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncthreads();
     tc::fence_after();
     const uint32_t tbase = lds_u32(sbase + SM::kTmem);
+    bool bad = false;  // a wait ran out
 
     if (warp == 5) {
         // ------------------------------------------------ producer warp --
@@ -613,6 +624,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             pok = ok;
         }
         if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
+        bad = !pgood;
         if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
     } else if (warp == 4) {
         // ------------------------------------------------- MMA issuer ----
@@ -642,6 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 tc::fence_after();
                 issue_s(jj);
             }
+            bad = !ok;
             if (!ok) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             // every MMA issued has finished before tensor memory is released
             tc::commit(fin);
@@ -671,6 +684,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 tc::commit(s_free0 + (j & 1) * 8);  // the buffer's P has been read
                 tc::commit(v_empty0 + (j % kTcV) * 8);
             }
+            bad = !ok;
             if (!ok) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             tc::commit(fin_o);
             (void)wait_pf(fin_o, 0, drain_limit(p.wait_ns));
@@ -825,6 +839,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
         if (!ok && threadIdx.x == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
         if (ok && nst > 0) ok = wait_all(o_done0 + ((nst - 1) & 1) * 8, (uint32_t)(((nst - 1) >> 1) & 1), p.wait_ns);
+        bad = !ok;
         tc::fence_after();
         const float inv = lrow > 0.f ? 1.f / lrow : 0.f;
         const uint32_t keep = pos >= 0 ? 0xFFFFFFFFu : 0u;  // rows before position 0 are +0
@@ -854,7 +869,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
     }
     tc::fence_before();
-    __syncthreads();
+    if (__syncthreads_or(bad)) let_copies_land();
     if (warp == 4) {
         tc::fence_after();
         tc::dealloc(tbase, kTcCols);
@@ -953,6 +968,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     __syncthreads();
     tc::fence_after();
     const uint32_t tbase = lds_u32(sbase + SM::kTmem);
+    bool bad = false;  // a wait ran out
 
     if (warp == kT2MmaWarp + 1) {
         // ------------------------------------------------ producer warp --
@@ -1026,6 +1042,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             pok = ok;
         }
         if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
+        bad = !pgood;
         if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
     } else if (warp == kT2MmaWarp) {
         // -------------------------------------------------- MMA issuer --
@@ -1088,6 +1105,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     tc::commit_elect(k_empty0 + ((j + 1) % kT2KSlots) * 8);
                 }
             }
+            bad = !ok;
             if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             // every MMA issued has finished before tensor memory is released
             tc::commit_elect(fin);
@@ -1273,6 +1291,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         }
         if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
         if (ok && nst > 0) ok = wait_all(o_done0 + t * 8, (uint32_t)((nst - 1) & 1), p.wait_ns);
+        bad = !ok;
         tc::fence_after();
         lra += __shfl_xor_sync(0xffffffffu, lra, 1);
         lrb += __shfl_xor_sync(0xffffffffu, lrb, 1);
@@ -1308,7 +1327,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         }
     }
     tc::fence_before();
-    __syncthreads();
+    if (__syncthreads_or(bad)) let_copies_land();
     if (warp == kT2MmaWarp) {
         tc::fence_after();
         tc::dealloc(tbase, kT2Cols);
@@ -1769,9 +1788,12 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             }
         }
         // the next item starts its barriers afresh; after a wait that ran out
-        // copies may still be under way, and nothing more is started
+        // nothing more is started
         tc::fence_before();
-        if (__syncthreads_or(bad)) break;
+        if (__syncthreads_or(bad)) {
+            let_copies_land();
+            break;
+        }
     }
     tc::fence_before();
     __syncthreads();

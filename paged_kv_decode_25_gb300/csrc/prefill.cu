@@ -141,12 +141,15 @@ __device__ __forceinline__ bool wait_pf(uint32_t bar, uint32_t parity, long long
     return mbar_wait_bounded(bar, parity, limit_ns, kWaitSleepNs);
 }
 
-// The end of a CTA in which some wait ran out: copies may be under way that no
-// warp waits for any more, and none may outlive the shared memory it writes. They
-// take microseconds and get 10 ms. (Waiting on the barriers of those announced
-// needs their numbers kept in the producer's loop, which cost these kernels 0.3
-// to 1.5 % of their time in four forms tried; this costs 0.1 %.)
-__device__ __forceinline__ void let_copies_land() {
+// The end of a CTA in which some wait ran out (any thread's): reports it, once,
+// and lets copies land that may be under way and that no warp waits for any more,
+// as none may outlive the shared memory it writes. They take microseconds and get
+// 10 ms. (Waiting on the barriers of those announced needs their numbers kept in
+// the producer's loop, which cost these kernels 0.3 to 1.5 % of their time in four
+// forms tried. A report at each wait kept its code within the loops: 0.3830 ms a
+// layer of 8 prompts and 8 chunks, 0.3795 like this.)
+__device__ __forceinline__ void give_up(int32_t* dev_err) {
+    if (threadIdx.x == 0) raise_err(dev_err, MI_DEVERR_TIMEOUT);
     const unsigned long long t0 = globaltimer();
     while ((long long)(globaltimer() - t0) < kDrainMinNs) __nanosleep(20000);
 }
@@ -625,7 +628,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
         if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
         bad = !pgood;
-        if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
     } else if (warp == 4) {
         // ------------------------------------------------- MMA issuer ----
         if (lane == 0 && nst > 0) {
@@ -655,7 +657,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 issue_s(jj);
             }
             bad = !ok;
-            if (!ok) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             // every MMA issued has finished before tensor memory is released
             tc::commit(fin);
             (void)wait_pf(fin, 0, drain_limit(p.wait_ns));
@@ -685,7 +686,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 tc::commit(v_empty0 + (j % kTcV) * 8);
             }
             bad = !ok;
-            if (!ok) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             tc::commit(fin_o);
             (void)wait_pf(fin_o, 0, drain_limit(p.wait_ns));
         }
@@ -837,7 +837,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             tc::fence_before();
             mbar_arrive(p_full0 + (j & 1) * 8);
         }
-        if (!ok && threadIdx.x == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
         if (ok && nst > 0) ok = wait_all(o_done0 + ((nst - 1) & 1) * 8, (uint32_t)(((nst - 1) >> 1) & 1), p.wait_ns);
         bad = !ok;
         tc::fence_after();
@@ -869,7 +868,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
     }
     tc::fence_before();
-    if (__syncthreads_or(bad)) let_copies_land();
+    if (__syncthreads_or(bad)) give_up(p.dev_err);
     if (warp == 4) {
         tc::fence_after();
         tc::dealloc(tbase, kTcCols);
@@ -1043,7 +1042,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         }
         if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
         bad = !pgood;
-        if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
     } else if (warp == kT2MmaWarp) {
         // -------------------------------------------------- MMA issuer --
         // The whole warp runs the loop; one elected lane issues each MMA
@@ -1106,7 +1104,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 }
             }
             bad = !ok;
-            if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             // every MMA issued has finished before tensor memory is released
             tc::commit_elect(fin);
             (void)wait_all(fin, 0, drain_limit(p.wait_ns));
@@ -1289,7 +1286,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             tc::fence_before();
             mbar_arrive(p_full0 + t * 8);
         }
-        if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
         if (ok && nst > 0) ok = wait_all(o_done0 + t * 8, (uint32_t)((nst - 1) & 1), p.wait_ns);
         bad = !ok;
         tc::fence_after();
@@ -1327,7 +1323,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         }
     }
     tc::fence_before();
-    if (__syncthreads_or(bad)) let_copies_land();
+    if (__syncthreads_or(bad)) give_up(p.dev_err);
     if (warp == kT2MmaWarp) {
         tc::fence_after();
         tc::dealloc(tbase, kT2Cols);
@@ -1585,7 +1581,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             }
             if (pgood && nst > 0 && !load_v(nst - 1)) pgood = false;
             bad |= !pgood;
-            if (!pgood && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
         } else if (warp == kT2MmaWarp) {
             // -------------------------------------------------- MMA issuer --
             // The whole warp runs the loop; one elected lane issues each MMA
@@ -1653,7 +1648,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     }
                 }
                 bad |= !ok;
-                if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
                 // every MMA issued has finished before tensor memory is released
                 tc::commit_elect(fin);
                 (void)wait_all(fin, 0, drain_limit(p.wait_ns));
@@ -1753,8 +1747,6 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full0 + t * 8);
             }
-            bad |= !ok;
-            if (!ok && lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
             if (ok && nst > 0) ok = wait_all(o_done0 + t * 8, (uint32_t)((nst - 1) & 1), p.wait_ns);
             bad |= !ok;
             tc::fence_after();
@@ -1791,7 +1783,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         // nothing more is started
         tc::fence_before();
         if (__syncthreads_or(bad)) {
-            let_copies_land();
+            give_up(p.dev_err);
             break;
         }
     }

@@ -1356,6 +1356,15 @@ struct PrefixParams {
     PrefixWork w;
 };
 
+// A row's exponentials are relative to a reference 2^16 above its largest logit
+// so far; it moves there again when a logit comes within 2^8 of it, so no
+// exponential passes 1. (The plain stage takes no maximum, and the row may grow
+// under it. With references at the maximum and growth up to 2^60, values above
+// 2^68 overflowed the fp32 output where one softmax over both parts has them
+// finite. 16 bits below 1 cost nothing: a weight of 2^-110 of the largest still
+// counts, and products of the smallest values keep more bits than bf16 has.)
+constexpr float kAhead = 16.f, kNear = 8.f;
+
 // Two rows' running reference exponent and sum (per lane: its 32 keys).
 struct RowSums {
     float ma, mb, la, lb;
@@ -1402,10 +1411,12 @@ __device__ __noinline__ RowSums whole_stage(uint32_t tl, uint32_t present, int l
         mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     }
     // (all four lanes of a row take the same decision)
+    ma = ma + kNear > r.ma ? ma + kAhead : r.ma;
+    mb = mb + kNear > r.mb ? mb + kAhead : r.mb;
     const bool move_a = ma > r.ma && r.ma != -INFINITY, move_b = mb > r.mb && r.mb != -INFINITY;
     const float alpha_a = move_a ? ex2(r.ma - ma) : 1.f, alpha_b = move_b ? ex2(r.mb - mb) : 1.f;
-    r.ma = fmaxf(r.ma, ma);
-    r.mb = fmaxf(r.mb, mb);
+    r.ma = ma;
+    r.mb = mb;
     r.ok = true;
     if (__any_sync(0xffffffffu, move_a || move_b)) {
         // O may be touched once its previous P . V has finished
@@ -1693,9 +1704,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             };
             // Every row sees every key, so a stage is plain but for an
             // item's last: exponentials relative to the row's reference,
-            // no maximum. The reference is the first stage's maximum; it
-            // moves when a sum passes 2^60 (bf16 and fp32 hold the
-            // probabilities and sums below that as well as below 1).
+            // no maximum. A lane's sum of 32 above 1 has one above 2^-5: the
+            // stage is done again with the reference moved.
             RowSums r = {-INFINITY, -INFINITY, 0.f, 0.f, true};
             bool steady = false;  // the warp's rows have references
             const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
@@ -1729,7 +1739,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     }
                     const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
                     const float psa = tc::f2_lo(sa) + tc::f2_hi(sa), psb = tc::f2_lo(sb) + tc::f2_hi(sb);
-                    if (!__any_sync(0xffffffffu, (va && psa > 0x1p60f) || (vb && psb > 0x1p60f))) {
+                    if (!__any_sync(0xffffffffu, (va && psa > 1.f) || (vb && psb > 1.f))) {
                         r.la += psa;
                         r.lb += psb;
                         tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));

@@ -287,3 +287,26 @@ def test_shared_blocks(cuda_device):
     assert err == 0
     both.tables[1], both.tables[2] = tables[0], tables[1]
     check(both, 1, [0, 2], [48, 40], q, out, 0.125)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("step", [1.0, 5.0, 30.0, -5.0])
+@pytest.mark.parametrize("size", [0, 80, 110, -110])
+def test_large_and_small_values(cuda_device, d, step, size):
+    """Values of 2^size while the logits climb or fall by `step` every 100
+    tokens (24 prefixes of 8 heads, so that one block takes many keys): sums of
+    weights times values stay in range wherever one softmax over both parts has
+    them there."""
+    P, prefixes, own = 24, [700] * 24, [30] + [0] * 23
+    both, ptab, tables = make(prefixes, own, 8, d, 32)
+    q = both.queries(P, 16)
+    q[:, :, 0] = 2.0
+    for s in range(P):
+        blk, off = both.rows(s, 700)
+        both.k[blk, :, off, 0] = (torch.arange(700) // 100 * step).to(torch.bfloat16)[:, None]
+    plain = both.v
+    both.v = both.v * 2.0 ** size  # (exact)
+    out, err = call(_mi(), cuda_device, both, ptab, prefixes, list(range(P + 1)), tables, own, q, 0.5)
+    assert err == 0
+    both.v = plain
+    check(both, P, list(range(P + 1)), own, q, out.double() * 2.0 ** -size, 0.5)

@@ -1792,13 +1792,10 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         // the next item starts its barriers afresh; after a wait that ran out
         // nothing more is started
         tc::fence_before();
-        if (__syncthreads_or(bad)) {
-            give_up(p.dev_err);
-            break;
-        }
+        if ((bad = __syncthreads_or(bad))) break;
     }
-    tc::fence_before();
-    __syncthreads();
+    // (that barrier, or the plan's, is the last: no warp is in tensor memory any more)
+    if (bad) give_up(p.dev_err);
     if (warp == kT2MmaWarp) {
         tc::fence_after();
         tc::dealloc(tbase, kT2Cols);

@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // key, and `cols` hold rows
                         const int row0 = (MODE == kSum ? j * rp : 0) + col0;
                         const int cols = min(min(rp - col0, 64), rows - row0);
-                        const int first = (MODE == kSum ? bound[t] : (key - it.x.first) * p.G) - row0;
+                        const int first = (MODE == kSum ? bound[t] : max(key - it.x.first, 0) * p.G) - row0;
                         const bool part = __any_sync(0xffffffffu, first > 0) || cols < 64;
                         const uint32_t la = sbase + SM::kLses + (((MODE == kSum ? yc : ic) % kLseSlots) * kRows + col0) * 4;
                         if (cols <= 0) {

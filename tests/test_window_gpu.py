@@ -261,3 +261,29 @@ def test_long_contexts_without_queries(cuda_device, lens, m, fresh):
         got = before.to(cuda_device)
         assert call(_mi(), cuda_device, batch, q, 32, starts_of(m), most, got, fresh) == 0
         check(batch, q, 32, starts_of(m), before, got.cpu(), fresh)
+
+
+@pytest.mark.parametrize("most", [1, 300])  # resident rows, resident keys
+def test_context_of_268_million(cuda_device, most):
+    """More than 2^31 / G tokens (most of them in one block, again and again):
+    the first and the last block's scores."""
+    mi, dev = _mi(), cuda_device
+    n, G, d = (1 << 28) + 4096, 8, 64
+    batch = Batch([48], 1, d, 30, spare=0)
+    q = batch.queries(1, G)
+    first, many, last = batch.tables[0].tolist()
+    tables = torch.full((1, n // BLOCK), many, dtype=torch.int32)
+    tables[0, 0], tables[0, -1] = first, last
+    got = torch.rand(3, 1, BLOCK, generator=batch.gen).to(dev)
+    assert call(mi, dev, batch, q, G, [0, 1], most, got, True, tables=tables, lens=[n]) == 0
+    k = batch.tokens(batch.k, 0, 0)
+    x = (q[0].double() @ k.T * d ** -0.5).exp()  # [G][48]: the first block, one of the many, the last
+    times = torch.ones(48, dtype=torch.float64)
+    times[16:32] = n // BLOCK - 2
+    w = (x / (x * times).sum(-1, keepdim=True)).sum(0)
+    w = torch.cat([w[:16], w[32:]])
+    have = torch.cat([got[first, 0], got[last, 0]]).cpu().double()
+    # sums in sequence: 2^20 stages over at least 100 blocks, 64 columns, the
+    # blocks: fewer than 2^14 roundings
+    tol = 2 ** 14 * 2.0 ** -24 + 2 * logit_slack(q[0].double(), k, d ** -0.5) + 2.0 ** -20
+    assert torch.all((have - w).abs() <= tol * w), float((have / w - 1).abs().max())

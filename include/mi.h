@@ -572,7 +572,10 @@ mi_status mi_kv_copy_rows(const void* src, int64_t src_count, const int32_t* src
                           int32_t* dev_err, mi_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
-/* Shared prefixes. Requests that begin with the same tokens (a system prompt,
+/* The calls of this section and the next take tables of at most 2^27 - 128
+ * blocks (max_blocks_per_seq, max_prefix_blocks).
+ *
+ * Shared prefixes. Requests that begin with the same tokens (a system prompt,
  * a document many questions are asked about) keep those tokens once: the
  * prefix is a sequence of its own in the pool, and each request's table holds
  * only the tokens after it. */
@@ -600,10 +603,10 @@ mi_status mi_kv_copy_rows(const void* src, int64_t src_count, const int32_t* src
  * mi_paged_decode_attention; calls that may run at the same time take
  * different ones.
  * Device errors: an entry of group_start outside [0, B], or one before the last
- * below the one ahead of it (MI_DEVERR_BAD_QUERY): every request attends to its own tokens only; a prefix length above a table
- * row clamps to it (MI_DEVERR_BAD_CONTEXT); a bad block id of a prefix drops
- * that block's keys (MI_DEVERR_BAD_BLOCK); the others as
- * mi_paged_decode_attention. num_prefixes 0 .. 65535, max_prefix_blocks >= 1. */
+ * below the one ahead of it (MI_DEVERR_BAD_QUERY): every request attends to its
+ * own tokens only; a prefix length above a table row clamps to it
+ * (MI_DEVERR_BAD_CONTEXT); a bad block id of a prefix drops that block's keys
+ * (MI_DEVERR_BAD_BLOCK); the others as mi_paged_decode_attention. num_prefixes 0 .. 65535, max_prefix_blocks >= 1. */
 mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks,
                                            const void* q, const void* k_cache, const void* v_cache,
                                            const int32_t* prefix_tables, const int32_t* prefix_lens,

@@ -125,7 +125,11 @@ inline bool overlaps(const void* a, size_t a_bytes, const void* b, size_t b_byte
     return x < y + b_bytes && y < x + a_bytes;
 }
 
-// The dims every paged entry point of this library accepts (B up to 65535).
+// Blocks of the longest table: token indices of a work item that begins in the
+// context (up to 1,024 tokens) stay within 32 bits.
+constexpr int kLongestTable = (1 << 27) - 128;
+
+// The dims the cache operators accept (B up to 65535).
 inline mi_status check_paged_dims(const mi_dims* dims) {
     if (!dims) return MI_ERR_INVALID_ARG;
     const mi_dims& D = *dims;
@@ -134,7 +138,7 @@ inline mi_status check_paged_dims(const mi_dims* dims) {
     if (D.block_size != kBlock || (D.head_dim != 64 && D.head_dim != 128) || D.Hq % D.Hkv != 0 || D.Hq / D.Hkv > 8)
         return MI_ERR_UNSUPPORTED;
     if ((long long)D.num_blocks * D.Hkv * kBlock * (D.head_dim / 64) > 0x7FFFFFFFLL) return MI_ERR_INVALID_ARG;
-    if ((long long)D.max_blocks_per_seq * kBlock > 0x7FFFFFFFLL) return MI_ERR_INVALID_ARG;
+    if (D.max_blocks_per_seq > kLongestTable) return MI_ERR_INVALID_ARG;
     return MI_OK;
 }
 

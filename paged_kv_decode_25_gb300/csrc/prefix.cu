@@ -102,7 +102,7 @@ struct PrefixSpace {
 
 bool prefix_space(const mi_dims* dims, int32_t num_prefixes, int32_t max_prefix_blocks, PrefixSpace* s) {
     if (check_paged_dims(dims) != MI_OK || num_prefixes < 0 || num_prefixes > 65535 || max_prefix_blocks < 1 ||
-        (long long)max_prefix_blocks * kBlock > 0x7FFFFFFFLL)
+        max_prefix_blocks > kLongestTable)
         return false;
     const int sms = sm_count();
     if (sms <= 0) return false;
@@ -146,7 +146,7 @@ extern "C" mi_status mi_paged_decode_attention_prefix(const mi_dims* dims, int32
     if (ds != MI_OK) return ds;
     const mi_dims D = *dims;
     if (num_prefixes < 0 || num_prefixes > 65535 || max_prefix_blocks < 1 ||
-        (long long)max_prefix_blocks * kBlock > 0x7FFFFFFFLL || !std::isfinite(scale))
+        max_prefix_blocks > kLongestTable || !std::isfinite(scale))
         return MI_ERR_INVALID_ARG;
     if (D.B == 0) return MI_OK;
     if (!q || !k_cache || !v_cache || !group_start || !block_tables || !context_lens || !out || !workspace ||

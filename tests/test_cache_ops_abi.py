@@ -172,3 +172,15 @@ def test_shrink_among_other_calls(mi):
         blocks = [b for q in held for b in mi.mi_kv_pool_seq_blocks(pool.handle, q)]
         assert len(blocks) == len(set(blocks)) and len(blocks) + pool.num_free() == 60
         assert all(len(mi.mi_kv_pool_seq_blocks(pool.handle, q)) == -(-n // 16) for q, n in held.items())
+
+
+def test_longest_tables(mi):
+    """Tables of 2^27 - 128 blocks at most: the kernels look up to 1,024 tokens
+    past a sequence's end, in 32 bits."""
+    top = (1 << 27) - 128
+    for call in (prefix, scored, window, evict):
+        for width in (top + 1, (1 << 27) - 1):
+            assert call(mi, d=dims(mi, max_blocks_per_seq=width)) == mi.MI_ERR_INVALID_ARG
+    for size in (mi.mi_paged_kv_evict_workspace_bytes, lambda d: mi.mi_paged_prefill_scores_workspace_bytes(d, 4, 4)):
+        assert size(dims(mi, max_blocks_per_seq=top)) > 0 and size(dims(mi, max_blocks_per_seq=top + 1)) == 0
+    assert prefix(mi, width=top + 1) == mi.MI_ERR_INVALID_ARG

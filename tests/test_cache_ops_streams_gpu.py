@@ -116,3 +116,39 @@ def test_two_graphs_over_one_workspace(cuda_device, name):
     torch.cuda.synchronize()
     for (_, outs, _), ref in zip(ops, want):
         assert all(torch.equal(x, y) for x, y in zip(bits(outs), ref))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_replays_write_everything(cuda_device, name):
+    """Two graphs over one workspace, every output poisoned before each replay:
+    a replay leaves the bits that an eager call leaves over the same poison."""
+    _, _, a = operator(name, cuda_device, 1)
+    _, _, b = operator(name, cuda_device, 2)
+    space = torch.empty(max(a.numel(), b.numel()), dtype=torch.uint8, device=cuda_device)
+    ops = [operator(name, cuda_device, seed, space) for seed in (1, 2)]
+
+    def poison(outs):
+        for t in outs:
+            t.view(torch.uint8).fill_(0x3C)
+
+    want, graphs, stream = [], [], torch.cuda.Stream()
+    for call, outs, _ in ops:
+        poison(outs)
+        call()
+        torch.cuda.synchronize()
+        want.append(bits(outs))
+        poison(outs)
+        assert not all(torch.equal(x, y) for x, y in zip(bits(outs), want[-1]))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for call, _, _ in ops:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                call()
+            graphs.append(g)
+        for i in (0, 1, 1, 0, 0, 1, 0, 1):
+            poison(ops[i][1])
+            graphs[i].replay()
+            got = bits(ops[i][1])
+            assert all(torch.equal(x, y) for x, y in zip(got, want[i]))
+    torch.cuda.synchronize()

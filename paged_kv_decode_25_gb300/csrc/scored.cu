@@ -21,10 +21,10 @@ constexpr int kScoreTokens = 1024;  // of one (request, head) per work item
 struct ScoreParams {
     const int32_t* tables;         // [B][mbps]
     const int32_t* lens;           // [B]
-    const float* logits;           // [blocks][16][gp], see DecodeExt
+    const float* logits;           // [blocks][16][GP], see DecodeExt
     const float* lse;              // [B][Hq]
     float* scores;                 // [num_blocks][Hkv][16]
-    int B, Hq, Hkv, G, gp, num_blocks, mbps, by_block, fresh;
+    int B, Hq, Hkv, G, num_blocks, mbps, by_block, fresh;
 };
 
 // GP: floats of a token's logits. A thread takes four consecutive tokens of a
@@ -156,7 +156,6 @@ mi_status scored(const mi_dims* dims, const void* q, const void* k_cache, const 
     p.Hq = D.Hq;
     p.Hkv = D.Hkv;
     p.G = D.Hq / D.Hkv;
-    p.gp = s.gp;
     p.num_blocks = D.num_blocks;
     p.mbps = D.max_blocks_per_seq;
     p.by_block = s.by_block;

@@ -20,6 +20,10 @@
 // out. 64 requests of 2,000 to 8,192 tokens cut to 2,048: the selection 22 us
 // (the keys are read from shared memory three times more, the digit counts are
 // atomics on a few hot bins), the move 172 us for 1.08 GB (6.3 TB/s).
+// In place each (request, head) moves in steps of 64 rows by one block, so that
+// rows are read before they are overwritten: as fast where there are hundreds
+// of them (512: 175 us), but latency by latency where there are few (4 e4m3
+// requests of 30,000 to 120,000 with 4 heads: 189 us, out of place 12).
 #include <algorithm>
 #include <mutex>
 

@@ -1371,13 +1371,13 @@ struct RowSums {
     bool ok;
 };
 
-// A stage whose rows have no reference yet, or have outgrown it, or
-// with keys that do not count (all but the first `left`, and those of absent
-// blocks): masks, takes the maximum, moves O and the sums to it and writes P.
-// A function of its own, as few stages need it and the plain stage's loop is
-// the faster without its registers and selects; and in short loops, as every
-// item's first stage runs it out of a cold instruction cache (unrolled over the
-// 128 keys it took 10 us there).
+// A stage whose rows have no reference yet, or have outgrown it, or with keys
+// that do not count (all but the first `left`, and those of absent blocks):
+// masks, takes the maximum, moves the reference, O and the sums where it has to
+// and writes P. A function of its own, as few stages need it and the plain
+// stage's loop is the faster without its registers and selects; and in short
+// loops: unrolled over the 128 keys an item's first stage took 10 us, like this
+// 4 (3.3 without a mask).
 template <int HD>
 __device__ __noinline__ RowSums whole_stage(uint32_t tl, uint32_t present, int left, float sl2, RowSums r,
                                             uint32_t o_done, uint32_t parity, long long wait_ns) {

@@ -88,7 +88,10 @@ __device__ __forceinline__ int prefix_step(float share) {
 // to 1,024 tokens behind 4,100, 128 of 16 to 512 behind 32,000, and 90 in six
 // groups: 34, 83 and 33 us (one part after the other 44, 96 and 41); kTileBlock
 // 1: 35-38, 87, 34; 2: 34, 90, 33; with 3 of 4 SMs the chats take 37, with 2 of
-// 3 40.
+// 3 40. (On 152 SMs 11 of 15 leave the prefix part 41, room for eight KV heads
+// with one tile in five splits, 40 items; 3 of 4 leave 38 and four splits. The
+// cap fits such counts and is neutral for 2, 4 and 16 units, by the plan's own
+// cost: a number found by trying, not a rule.)
 constexpr float kTileBlock = 1.8f;
 __device__ __forceinline__ int prefix_budget(const PrefixWork& w, float tile_blocks, float own_blocks) {
     const float a = tile_blocks * kTileBlock, b = own_blocks;

@@ -39,12 +39,13 @@
 // against 1,024 (measured apart from the softmax).
 //
 // Measured (head_dim 128, 32 heads over 8): 16 windows of 32 to 64 tokens over
-// 77,600 keys 48 + 49 us, each bound by what two or three items a block cost to
-// start (7,000 clocks, X has one place) on top of 30 tiles; two whole prompts
-// of 5,000 tokens 190 + 10 + 164 us, 565 TFLOP/s of the products it cannot do
-// without, bound by the softmax's issue slots (a tile of 32,768 logits takes
-// 1,300 to 1,500 clocks, its exponentials alone 1,024; tensor cores busy for
-// half of them).
+// 77,600 keys 48 + 49 us, each with two or three items a block that cost 7,000
+// clocks to start (X has one place) on top of 30 tiles; two whole prompts of
+// 5,000 tokens 190 + 10 + 164 us, 565 TFLOP/s of the products it cannot do
+// without. No unit bounds the latter: a tile of 32,768 logits takes 1,300 to
+// 1,500 clocks, of which its exponentials are 1,024, the issue slots are used
+// for 48 to 53 % and the tensor cores for 47 to 54 %; what is lost lies in the
+// hand-over from tile to tile and in the items' starts.
 #include <cmath>
 
 #include "batch.cuh"

@@ -125,8 +125,65 @@ mi_status mi_kv_pool_free(mi_kv_pool* pool, int32_t seq_id);
  * the last of them); the kept blocks stay where they are. Shrinking to 0
  * keeps the sequence, with an empty table. The use clock does not move.
  * MI_ERR_UNKNOWN_SEQ if seq_id is not resident; MI_ERR_INVALID_ARG if
- * num_tokens is negative or above what the sequence holds. */
+ * num_tokens is negative or above what the sequence holds, or its last kept
+ * block was given back (mi_kv_pool_slide) or, with room for more tokens, is held by
+ * another sequence too (mi_kv_pool_fork; with INT8 caches shrink a sequence that
+ * shares blocks to a multiple of 64 tokens only). */
 mi_status mi_kv_pool_shrink(mi_kv_pool* pool, int32_t seq_id, int32_t num_tokens);
+
+/* ---- Forks, windows, compaction: sequences that share blocks, give back blocks
+ * out of the middle, and a pool whose blocks move.
+ * A sequence whose first tokens another one also holds (samples or beams of one
+ * prompt, a chat that branches) shares the blocks of those tokens: a block then
+ * stands in several tables and returns to the free list with the last of them.
+ * Shared blocks are whole groups of tokens, which appends never write again; the
+ * other calls that write cached rows (an eviction in place) want blocks that
+ * mi_kv_pool_block_refs says one table holds. A table column whose block was
+ * given back by mi_kv_pool_slide holds -1 from then on: mi_kv_pool_seq_blocks and
+ * mi_kv_pool_batch_meta show it, mi_kv_pool_token_slots refuses ranges over it,
+ * a swap leaves it out (fewer blocks go and come back) and attention over the
+ * sequence takes the window it was slid with (mi_paged_decode_attention_sliding).
+ * group_tokens is 16, or 64 where the blocks are INT8 caches, whose appends
+ * quantise a sequence's open group of 64 tokens again. */
+
+/* Make sequence dst_seq (not held yet) hold the first num_tokens tokens of
+ * resident src_seq. Blocks of whole groups are shared. The blocks of the last,
+ * open group (at most group_tokens / 16) are new ones of dst_seq's own, popped in
+ * order: their contents are the caller's to copy, copy_src[i] to copy_dst[i] for
+ * i < *n_copies (mi_kv_copy_planes), before either sequence's next append (and
+ * before the copies of a fork of the fork, which read them); with INT8 caches the
+ * open-group rows of its slot too. Both sequences are used now.
+ * MI_ERR_UNKNOWN_SEQ if src_seq is not resident. MI_ERR_INVALID_ARG: dst_seq out
+ * of range, resident or swapped out, more tokens than src_seq holds, group_tokens
+ * not a positive multiple of 16, fewer than *n_copies places in the arrays
+ * (max_copies), or a block of the open group, or of token num_tokens - 1, that
+ * was given back. MI_ERR_OUT_OF_BLOCKS: not enough free blocks. Errors change
+ * nothing. */
+mi_status mi_kv_pool_fork(mi_kv_pool* pool, int32_t src_seq, int32_t dst_seq, int32_t num_tokens, int32_t group_tokens,
+                          int32_t* copy_src, int32_t* copy_dst, int32_t max_copies, int32_t* n_copies);
+
+/* Give back the blocks of resident sequence seq_id that no token from its newest
+ * on sees: those past the first `sinks` tokens that end at or before token
+ * tokens - window, but none of the open group. They leave the table in order
+ * (columns of -1). Call it once the attention of the sequence's newest tokens has
+ * been queued: a chunk's earlier tokens look further back than its last.
+ * *n_released (or NULL) gets their number. The use clock does not move.
+ * MI_ERR_UNKNOWN_SEQ if seq_id is not resident; MI_ERR_INVALID_ARG for window < 1,
+ * sinks < 0 or a group_tokens that is not a positive multiple of 16. */
+mi_status mi_kv_pool_slide(mi_kv_pool* pool, int32_t seq_id, int32_t window, int32_t sinks, int32_t group_tokens,
+                           int32_t* n_released);
+
+/* Move every held block into the first `used` block ids (used = blocks held): the
+ * held blocks with higher ids, ascending, go to the free lower ids, ascending.
+ * Tables change at once; the caller copies the contents src_out[i] to dst_out[i]
+ * for i < *n_out (mi_kv_copy_planes) before anything reads or writes them. No id is
+ * both a source and a destination. Afterwards pops return used, used + 1, ...
+ * If *n_out exceeds max_out: MI_ERR_INVALID_ARG, *n_out set and nothing changed
+ * (so max_out 0 asks for the number). Swapped-out sequences hold no blocks. */
+mi_status mi_kv_pool_compact(mi_kv_pool* pool, int32_t* src_out, int32_t* dst_out, int32_t max_out, int32_t* n_out);
+
+/* Tables that hold the block (0: free), or -1 for a NULL pool or an id out of range. */
+int32_t mi_kv_pool_block_refs(const mi_kv_pool* pool, int32_t block);
 
 /* Number of free blocks, or -1 for a NULL pool. */
 int32_t mi_kv_pool_num_free(const mi_kv_pool* pool);
@@ -260,6 +317,32 @@ mi_status mi_paged_kv_append(const mi_dims* dims, const void* q, const void* k, 
                              const int32_t* positions, const int32_t* slot_mapping,
                              const float* rope_cos_sin, int32_t max_pos, void* q_out,
                              void* k_cache, void* v_cache, int32_t* dev_err, mi_stream_t stream);
+
+/* mi_paged_kv_append for models that norm each query and key head (Qwen3: before
+ * the rotation), in the same pass: for a head's d values x
+ *   y[i] = x[i] / sqrt(sum x^2 / d + eps) * weight[i]
+ * and y is rotated at positions[b], all in fp32 (sums of squares too, so |x| below
+ * 2^60) and rounded once: q_out and k_cache hold bf16, v_cache v as given.
+ * Row b of q, k and v begins q_stride, k_stride, v_stride elements after row b - 1
+ * (multiples of 8, at least Hq * d, Hkv * d, Hkv * d), so all three may be parts of
+ * one projection's rows. q_weight and k_weight are bf16 [head_dim], 16-byte
+ * aligned; eps positive and finite. q_out [B][Hq][d] is q itself (contiguous rows)
+ * or overlaps none of q, k, v. Other arguments and errors as mi_paged_kv_append. */
+mi_status mi_paged_kv_append_norm(const mi_dims* dims, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                                  const int32_t* positions, const int32_t* slot_mapping, const float* rope_cos_sin,
+                                  int32_t max_pos, void* q_out, void* k_cache, void* v_cache, int32_t* dev_err,
+                                  mi_stream_t stream);
+
+/* The same into FP8 caches (below): k8 = e4m3(fp32(y / k_scale[h])) of the normed
+ * and rotated fp32 y itself, one rounding less than a bf16 value in between would
+ * take; v8 and bad scales as mi_paged_kv_append_fp8. */
+mi_status mi_paged_kv_append_norm_fp8(const mi_dims* dims, const void* q, int64_t q_stride, const void* k,
+                                      int64_t k_stride, const void* v, int64_t v_stride, const void* q_weight,
+                                      const void* k_weight, float eps, const int32_t* positions,
+                                      const int32_t* slot_mapping, const float* rope_cos_sin, int32_t max_pos,
+                                      void* q_out, void* k_cache, void* v_cache, const float* k_scale,
+                                      const float* v_scale, int32_t* dev_err, mi_stream_t stream);
 
 /* Device workspace the attention call needs for these dims on the current
  * device (split-KV partials of the persistent grid): a size in bytes, or 0 when
@@ -570,6 +653,23 @@ mi_status mi_kv_copy_blocks(const mi_dims* dims, const void* src_k, const void* 
 mi_status mi_kv_copy_rows(const void* src, int64_t src_count, const int32_t* src_ids, void* dst,
                           int64_t dst_count, const int32_t* dst_ids, int32_t n, int64_t row_bytes,
                           int32_t* dev_err, mi_stream_t stream);
+
+/* Rows moved within caches, in every layer by one launch (forks, compaction):
+ *   plane[dst_ids[i]] = plane[src_ids[i]]   for i < n, for every plane.
+ * A plane is `rows` rows of row_bytes bytes, back to back, in device memory: a
+ * layer's K or V cache (a row is a block, Hkv * 16 * head_dim elements), its scores
+ * or its INT8 maxima. base 4-byte aligned and row_bytes a multiple of 4 (16 and 16
+ * are faster). `planes` is a host array and free again when the call returns;
+ * src_ids, dst_ids int32 [n] on the device. Destinations are distinct and none is a
+ * source (mi_kv_pool_compact and mi_kv_pool_fork give such lists; forks of several
+ * sequences may name one source many times). An id outside a plane's rows skips that
+ * row (MI_DEVERR_BAD_BLOCK). One launch per 144 planes. */
+typedef struct mi_kv_plane {
+    void* base;
+    int64_t rows, row_bytes;
+} mi_kv_plane;
+mi_status mi_kv_copy_planes(const mi_kv_plane* planes, int32_t num_planes, const int32_t* src_ids,
+                            const int32_t* dst_ids, int32_t n, int32_t* dev_err, mi_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* The calls of this section and the next take tables of at most 2^27 - 128

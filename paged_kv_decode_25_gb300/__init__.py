@@ -47,6 +47,8 @@ EXPORTS = (
     "mi_paged_decode_attention_scored", "mi_paged_decode_attention_scored_fp8", "mi_paged_scored_workspace_bytes",
     "mi_paged_prefill_scores", "mi_paged_prefill_scores_workspace_bytes",
     "mi_paged_kv_evict", "mi_paged_kv_evict_fp8", "mi_paged_kv_evict_workspace_bytes",
+    "mi_paged_kv_append_norm", "mi_paged_kv_append_norm_fp8",
+    "mi_kv_pool_fork", "mi_kv_pool_slide", "mi_kv_pool_compact", "mi_kv_pool_block_refs", "mi_kv_copy_planes",
     "mi_paged_decode_step", "mi_paged_decode_step_fp8", "mi_test_set_wait_limit", "mi_test_withhold_copy",
 )
 MI_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -55,6 +57,10 @@ MI_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 class MiDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "Hq", "Hkv", "head_dim", "block_size", "num_blocks", "max_blocks_per_seq")]
+
+
+class MiKvPlane(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("rows", ctypes.c_int64), ("row_bytes", ctypes.c_int64)]
 
 
 class MIError(RuntimeError):
@@ -74,6 +80,7 @@ def load():
                                % LIB_PATH)
         lib = ctypes.CDLL(LIB_PATH)
         P, i32, f32, f64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_double
+        i64 = ctypes.c_int64
         dims_p = ctypes.POINTER(MiDims)
         sig = {
             "mi_status_string": ([i32], ctypes.c_char_p),
@@ -131,6 +138,15 @@ def load():
             "mi_paged_kv_evict_workspace_bytes": ([dims_p], ctypes.c_size_t),
             "mi_paged_kv_evict": ([dims_p, P, P, P, P, P, P, i32, P, P, P, ctypes.c_size_t, P, P], i32),
             "mi_paged_kv_evict_fp8": ([dims_p, P, P, P, P, P, P, i32, P, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_kv_append_norm": (
+                [dims_p, P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32, P, P, P, P, P], i32),
+            "mi_paged_kv_append_norm_fp8": (
+                [dims_p, P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32, P, P, P, P, P, P, P], i32),
+            "mi_kv_pool_fork": ([P, i32, i32, i32, i32, P, P, i32, P], i32),
+            "mi_kv_pool_slide": ([P, i32, i32, i32, i32, P], i32),
+            "mi_kv_pool_compact": ([P, P, P, i32, P], i32),
+            "mi_kv_pool_block_refs": ([P, i32], i32),
+            "mi_kv_copy_planes": ([P, i32, P, P, i32, P, P], i32),
             "mi_test_set_wait_limit": ([ctypes.c_int64], i32),
             "mi_test_withhold_copy": ([i32], i32),
         }
@@ -285,6 +301,40 @@ def mi_kv_pool_seq_blocks(handle, seq_id, max_out=1 << 20):
     return out[:n]
 
 
+def mi_kv_pool_fork(handle, src_seq, dst_seq, num_tokens, group_tokens=16, max_copies=None):
+    """(status, copy_src, copy_dst): dst_seq holds src_seq's first num_tokens
+    tokens; the caller copies blocks copy_src[i] to copy_dst[i]."""
+    most = max(1, int(group_tokens) // 16) if max_copies is None else int(max_copies)
+    src, dst, n = np.empty(most, np.int32), np.empty(most, np.int32), ctypes.c_int32(0)
+    st = load().mi_kv_pool_fork(handle, int(src_seq), int(dst_seq), int(num_tokens), int(group_tokens), _ptr(src),
+                                _ptr(dst), most, ctypes.byref(n))
+    k = n.value if st == MI_OK else 0
+    return st, src[:k], dst[:k]
+
+
+def mi_kv_pool_slide(handle, seq_id, window, sinks, group_tokens=16):
+    """(status, blocks given back)."""
+    n = ctypes.c_int32(0)
+    st = load().mi_kv_pool_slide(handle, int(seq_id), int(window), int(sinks), int(group_tokens), ctypes.byref(n))
+    return st, n.value
+
+
+def mi_kv_pool_compact(handle, max_out=None):
+    """(status, src, dst): blocks to copy, src[i] to dst[i]; with max_out, at most so many."""
+    n = ctypes.c_int32(0)
+    if max_out is None:
+        load().mi_kv_pool_compact(handle, None, None, 0, ctypes.byref(n))
+        max_out = n.value
+    src, dst = np.empty(max(1, max_out), np.int32), np.empty(max(1, max_out), np.int32)
+    st = load().mi_kv_pool_compact(handle, _ptr(src), _ptr(dst), int(max_out), ctypes.byref(n))
+    k = n.value if st == MI_OK else 0
+    return st, src[:k], dst[:k]
+
+
+def mi_kv_pool_block_refs(handle, block):
+    return load().mi_kv_pool_block_refs(handle, int(block))
+
+
 class Pool:
     """Owner of a library pool handle, with the alloc/free/num_free/batch_meta
     calls the workloads expect (each returns the library's status)."""
@@ -309,6 +359,18 @@ class Pool:
 
     def num_free(self):
         return mi_kv_pool_num_free(self.handle)
+
+    def fork(self, src, dst, num_tokens, group_tokens=16):
+        return mi_kv_pool_fork(self.handle, src, dst, num_tokens, group_tokens)
+
+    def slide(self, seq, window, sinks, group_tokens=16):
+        return mi_kv_pool_slide(self.handle, seq, window, sinks, group_tokens)
+
+    def compact(self):
+        return mi_kv_pool_compact(self.handle)
+
+    def block_refs(self, block):
+        return mi_kv_pool_block_refs(self.handle, block)
 
     def token_slots(self, seq, first_token, count):
         st, slots = mi_kv_pool_token_slots(self.handle, seq, first_token, count)
@@ -593,6 +655,59 @@ def mi_paged_kv_evict_fp8(d: MiDims, k_cache, v_cache, scores, block_tables, con
     """mi_paged_kv_evict over e4m3 caches."""
     return _evict(load().mi_paged_kv_evict_fp8, d, k_cache, v_cache, scores, block_tables, context_lens, budgets,
                   recent, dst_tables, new_lens, workspace, workspace_bytes, dev_err, stream)
+
+
+def _rows(x, stride):
+    """Address of rows and the elements between them: of a tensor [rows][...]
+    whose rows may lie apart, or an address with its stride given."""
+    if x is None or isinstance(x, int):
+        return x, int(stride)
+    if stride is None:
+        assert x[:1].is_contiguous(), "a row must be contiguous"
+        stride = x.stride(0)
+        if x.shape[0] <= 1:  # torch leaves the stride of a single row unspecified
+            stride = max(stride, x[:1].numel())
+    return x.data_ptr(), int(stride)
+
+
+def _append_norm(fn, d, q, k, v, q_weight, k_weight, eps, positions, slot_mapping, rope_cos_sin, max_pos, q_out, caches,
+                 strides, dev_err, stream):
+    rows = [y for x, s in zip((q, k, v), strides or (None, None, None)) for y in _rows(x, s)]
+    return fn(ctypes.byref(d), *rows, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(slot_mapping),
+              _ptr(rope_cos_sin), int(max_pos), _ptr(q_out), *(_ptr(x) for x in caches), _ptr(dev_err), _stream(stream))
+
+
+def mi_paged_kv_append_norm(d: MiDims, q, k, v, q_weight, k_weight, eps, positions, slot_mapping, rope_cos_sin, max_pos,
+                            q_out, k_cache, v_cache, dev_err=None, stream=None, strides=None):
+    """mi_paged_kv_append with the RMS norm of every query and key head. Rows of
+    q, k, v may lie apart (slices of one projection); their strides are the
+    tensors', or `strides` in elements."""
+    return _append_norm(load().mi_paged_kv_append_norm, d, q, k, v, q_weight, k_weight, eps, positions, slot_mapping,
+                        rope_cos_sin, max_pos, q_out, (k_cache, v_cache), strides, dev_err, stream)
+
+
+def mi_paged_kv_append_norm_fp8(d: MiDims, q, k, v, q_weight, k_weight, eps, positions, slot_mapping, rope_cos_sin,
+                                max_pos, q_out, k_cache, v_cache, k_scale, v_scale, dev_err=None, stream=None,
+                                strides=None):
+    """mi_paged_kv_append_norm into e4m3 caches."""
+    return _append_norm(load().mi_paged_kv_append_norm_fp8, d, q, k, v, q_weight, k_weight, eps, positions, slot_mapping,
+                        rope_cos_sin, max_pos, q_out, (k_cache, v_cache, k_scale, v_scale), strides, dev_err, stream)
+
+
+def kv_planes(tensors):
+    """The planes of mi_kv_copy_planes: tensors [rows][...], one per layer's K, V,
+    scores or maxima. Holds the tensors' addresses, so keep them."""
+    planes = (MiKvPlane * max(1, len(tensors)))()
+    for p, x in zip(planes, tensors):
+        assert x.is_contiguous(), "tensors must be contiguous"
+        p.base, p.rows, p.row_bytes = x.data_ptr(), x.shape[0], x[0].numel() * x.element_size()
+    return planes, len(tensors)
+
+
+def mi_kv_copy_planes(planes, src_ids, dst_ids, n, dev_err=None, stream=None):
+    """Row src_ids[i] to row dst_ids[i] of every plane (`kv_planes`), in one launch."""
+    array, count = planes
+    return load().mi_kv_copy_planes(array, count, _ptr(src_ids), _ptr(dst_ids), int(n), _ptr(dev_err), _stream(stream))
 
 
 def mi_test_set_wait_limit(ns):

@@ -23,8 +23,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contract=off",
               "-I" + INCLUDE] + ARCH
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-I" + INCLUDE]
-CU_SOURCES = ["append.cu", "decode.cu", "evict.cu", "int8.cu", "noalloc.cu", "prefill.cu", "prefix.cu", "scored.cu",
-              "swap.cu", "window.cu"]
+CU_SOURCES = ["append.cu", "decode.cu", "evict.cu", "int8.cu", "noalloc.cu", "norm.cu", "pages.cu", "prefill.cu",
+              "prefix.cu", "scored.cu", "swap.cu", "window.cu"]
 CPP_SOURCES = ["pool.cpp"]
 
 

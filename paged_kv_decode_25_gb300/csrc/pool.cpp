@@ -7,6 +7,7 @@
 // "KV缓存的内存革命"), but fixed in size: an allocation that does not fit fails
 // and leaves the pool as it was.
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstring>
 #include <new>
@@ -25,8 +26,25 @@ struct mi_kv_pool {
     std::vector<uint8_t> swapped;               // per sequence id: blocks swapped out, tokens kept
     std::vector<int64_t> last_use;              // per sequence id: clock of the last use
     int64_t clock = 0;                          // LRU use counter
+    std::vector<int32_t> refs;                  // per block: sequences whose table holds it (0: free)
+    std::vector<std::vector<int32_t>> released; // per swapped sequence: table columns given back (mi_kv_pool_slide)
 
     void use(int32_t seq) { last_use[(size_t)seq] = clock; }
+    int32_t take() {
+        const int32_t b = free_stack.back();
+        free_stack.pop_back();
+        refs[(size_t)b] = 1;
+        return b;
+    }
+    // one table fewer holds block b (b < 0: a column given back already)
+    void give(int32_t b) {
+        if (b >= 0 && --refs[(size_t)b] == 0) free_stack.push_back(b);
+    }
+    bool resident(int32_t seq) const { return seq >= 0 && (size_t)seq < tables.size() && live[(size_t)seq]; }
+    // whether the block of token n - 1 of a table was given back
+    bool ends_released(const std::vector<int32_t>& t, int32_t n) const {
+        return n > 0 && t[(size_t)((n - 1) / block_size)] < 0;
+    }
 };
 
 extern "C" const char* mi_status_string(mi_status s) {
@@ -75,6 +93,8 @@ extern "C" mi_status mi_kv_pool_create(int32_t num_blocks, int32_t block_size, i
         p->live.assign((size_t)max_seqs, 0);
         p->swapped.assign((size_t)max_seqs, 0);
         p->last_use.assign((size_t)max_seqs, 0);
+        p->refs.assign((size_t)num_blocks, 0);
+        p->released.resize((size_t)max_seqs);
     } catch (...) {
         delete p;
         return MI_ERR_INVALID_ARG;
@@ -94,10 +114,7 @@ extern "C" mi_status mi_kv_pool_alloc(mi_kv_pool* p, int32_t seq, int32_t num_to
     if (need > p->max_blocks_per_seq) return MI_ERR_INVALID_ARG;
     const int64_t extra = need - (int64_t)t.size();
     if (extra > (int64_t)p->free_stack.size()) return MI_ERR_OUT_OF_BLOCKS;
-    for (int64_t i = 0; i < extra; ++i) {
-        t.push_back(p->free_stack.back());
-        p->free_stack.pop_back();
-    }
+    for (int64_t i = 0; i < extra; ++i) t.push_back(p->take());
     p->tokens[(size_t)seq] = num_tokens;
     p->live[(size_t)seq] = 1;
     ++p->clock;
@@ -139,11 +156,12 @@ extern "C" mi_status mi_kv_pool_free(mi_kv_pool* p, int32_t seq) {
     if (seq >= 0 && (size_t)seq < p->tables.size() && p->swapped[(size_t)seq]) {
         p->swapped[(size_t)seq] = 0;  // nothing on the device: just forget it
         p->tokens[(size_t)seq] = 0;
+        p->released[(size_t)seq].clear();
         return MI_OK;
     }
     if (seq < 0 || (size_t)seq >= p->tables.size() || !p->live[(size_t)seq]) return MI_ERR_UNKNOWN_SEQ;
     std::vector<int32_t>& t = p->tables[(size_t)seq];
-    for (int32_t b : t) p->free_stack.push_back(b);
+    for (int32_t b : t) p->give(b);
     t.clear();
     p->tokens[(size_t)seq] = 0;
     p->live[(size_t)seq] = 0;
@@ -156,7 +174,11 @@ extern "C" mi_status mi_kv_pool_shrink(mi_kv_pool* p, int32_t seq, int32_t num_t
     if (num_tokens > p->tokens[(size_t)seq]) return MI_ERR_INVALID_ARG;
     std::vector<int32_t>& t = p->tables[(size_t)seq];
     const size_t keep = (size_t)(((int64_t)num_tokens + p->block_size - 1) / p->block_size);
-    for (size_t i = keep; i < t.size(); ++i) p->free_stack.push_back(t[i]);
+    // the next token goes into the last block if that has room: it must be this
+    // sequence's alone, and there at all
+    if (p->ends_released(t, num_tokens)) return MI_ERR_INVALID_ARG;
+    if (num_tokens % p->block_size != 0 && p->refs[(size_t)t[keep - 1]] > 1) return MI_ERR_INVALID_ARG;
+    for (size_t i = keep; i < t.size(); ++i) p->give(t[i]);
     t.resize(keep);
     p->tokens[(size_t)seq] = num_tokens;
     return MI_OK;
@@ -222,6 +244,8 @@ extern "C" mi_status mi_kv_pool_token_slots(const mi_kv_pool* p, int32_t seq, in
     if ((int64_t)first_token + count > p->tokens[(size_t)seq]) return MI_ERR_INVALID_ARG;
     const std::vector<int32_t>& t = p->tables[(size_t)seq];
     const int32_t BS = p->block_size;
+    for (int32_t i = 0; i < count; ++i)
+        if (t[(size_t)((first_token + i) / BS)] < 0) return MI_ERR_INVALID_ARG;
     for (int32_t i = 0; i < count; ++i) {
         const int32_t tok = first_token + i;
         slots_out[i] = t[(size_t)(tok / BS)] * BS + tok % BS;
@@ -276,12 +300,22 @@ extern "C" mi_status mi_kv_pool_swap_out(mi_kv_pool* p, int32_t seq, int32_t* bl
     if (!p || max_out < 0) return MI_ERR_INVALID_ARG;
     if (seq < 0 || (size_t)seq >= p->tables.size() || !p->live[(size_t)seq]) return MI_ERR_UNKNOWN_SEQ;
     std::vector<int32_t>& t = p->tables[(size_t)seq];
-    if ((int64_t)t.size() > max_out || (!t.empty() && !blocks_out)) return MI_ERR_INVALID_ARG;
-    for (size_t i = 0; i < t.size(); ++i) {
-        blocks_out[i] = t[i];
-        p->free_stack.push_back(t[i]);
+    std::vector<int32_t> gone;
+    try {
+        for (size_t i = 0; i < t.size(); ++i)
+            if (t[i] < 0) gone.push_back((int32_t)i);
+    } catch (...) {
+        return MI_ERR_INVALID_ARG;
     }
-    if (n_out) *n_out = (int32_t)t.size();
+    const size_t held = t.size() - gone.size();
+    if ((int64_t)held > max_out || (held > 0 && !blocks_out)) return MI_ERR_INVALID_ARG;
+    int32_t at = 0;
+    for (int32_t b : t) {
+        if (b >= 0) blocks_out[at++] = b;
+        p->give(b);
+    }
+    p->released[(size_t)seq].swap(gone);
+    if (n_out) *n_out = at;
     t.clear();
     p->live[(size_t)seq] = 0;
     p->swapped[(size_t)seq] = 1;
@@ -292,19 +326,122 @@ extern "C" mi_status mi_kv_pool_swap_in(mi_kv_pool* p, int32_t seq, int32_t* blo
                                         int32_t* n_out) {
     if (!p || max_out < 0) return MI_ERR_INVALID_ARG;
     if (seq < 0 || (size_t)seq >= p->tables.size() || !p->swapped[(size_t)seq]) return MI_ERR_UNKNOWN_SEQ;
-    const int64_t need = ((int64_t)p->tokens[(size_t)seq] + p->block_size - 1) / p->block_size;
+    std::vector<int32_t>& gone = p->released[(size_t)seq];
+    const int64_t cols = ((int64_t)p->tokens[(size_t)seq] + p->block_size - 1) / p->block_size;
+    const int64_t need = cols - (int64_t)gone.size();
     if (need > max_out || (need > 0 && !blocks_out)) return MI_ERR_INVALID_ARG;
     if (need > (int64_t)p->free_stack.size()) return MI_ERR_OUT_OF_BLOCKS;
     std::vector<int32_t>& t = p->tables[(size_t)seq];
-    for (int64_t i = 0; i < need; ++i) {
-        t.push_back(p->free_stack.back());
-        p->free_stack.pop_back();
-        blocks_out[i] = t.back();
+    int32_t at = 0;
+    for (int64_t i = 0, g = 0; i < cols; ++i) {
+        if (g < (int64_t)gone.size() && gone[(size_t)g] == i) {
+            t.push_back(-1);
+            ++g;
+        } else {
+            t.push_back(p->take());
+            blocks_out[at++] = t.back();
+        }
     }
-    if (n_out) *n_out = (int32_t)need;
+    gone.clear();
+    if (n_out) *n_out = at;
     p->swapped[(size_t)seq] = 0;
     p->live[(size_t)seq] = 1;
     ++p->clock;
     p->use(seq);
     return MI_OK;
+}
+
+// ------------------------------------------- forks, windows, compaction ----
+
+extern "C" mi_status mi_kv_pool_fork(mi_kv_pool* p, int32_t src, int32_t dst, int32_t num_tokens, int32_t group_tokens,
+                                     int32_t* copy_src, int32_t* copy_dst, int32_t max_copies, int32_t* n_copies) {
+    if (!p || !n_copies || max_copies < 0 || (max_copies > 0 && (!copy_src || !copy_dst)) || group_tokens < 1 ||
+        group_tokens % p->block_size != 0)
+        return MI_ERR_INVALID_ARG;
+    if (!p->resident(src)) return MI_ERR_UNKNOWN_SEQ;
+    if (dst < 0 || (size_t)dst >= p->tables.size() || p->live[(size_t)dst] || p->swapped[(size_t)dst] ||
+        num_tokens < 0 || num_tokens > p->tokens[(size_t)src])
+        return MI_ERR_INVALID_ARG;
+    const std::vector<int32_t>& s = p->tables[(size_t)src];
+    // whole groups are shared (nobody writes them again), the open one's blocks copied
+    const size_t shared = (size_t)(num_tokens / group_tokens) * (size_t)(group_tokens / p->block_size);
+    const size_t all = (size_t)(((int64_t)num_tokens + p->block_size - 1) / p->block_size);
+    if (p->ends_released(s, num_tokens)) return MI_ERR_INVALID_ARG;
+    for (size_t i = shared; i < all; ++i)
+        if (s[i] < 0) return MI_ERR_INVALID_ARG;
+    if (all - shared > (size_t)max_copies) return MI_ERR_INVALID_ARG;
+    if (all - shared > p->free_stack.size()) return MI_ERR_OUT_OF_BLOCKS;
+    std::vector<int32_t> t;
+    try {
+        t.assign(s.begin(), s.begin() + (std::ptrdiff_t)all);
+    } catch (...) {
+        return MI_ERR_INVALID_ARG;
+    }
+    for (size_t i = 0; i < shared; ++i)
+        if (t[i] >= 0) ++p->refs[(size_t)t[i]];
+    for (size_t i = shared; i < all; ++i) {
+        t[i] = p->take();
+        copy_src[i - shared] = s[i];
+        copy_dst[i - shared] = t[i];
+    }
+    *n_copies = (int32_t)(all - shared);
+    p->tables[(size_t)dst].swap(t);
+    p->tokens[(size_t)dst] = num_tokens;
+    p->live[(size_t)dst] = 1;
+    ++p->clock;
+    p->use(src);
+    p->use(dst);
+    return MI_OK;
+}
+
+extern "C" mi_status mi_kv_pool_slide(mi_kv_pool* p, int32_t seq, int32_t window, int32_t sinks, int32_t group_tokens,
+                                      int32_t* n_released) {
+    if (!p || window < 1 || sinks < 0 || group_tokens < 1 || group_tokens % p->block_size != 0)
+        return MI_ERR_INVALID_ARG;
+    if (!p->resident(seq)) return MI_ERR_UNKNOWN_SEQ;
+    std::vector<int32_t>& t = p->tables[(size_t)seq];
+    const int64_t BS = p->block_size, tokens = p->tokens[(size_t)seq];
+    // no later token sees anything before this but the sinks, and no append writes it
+    const int64_t open = tokens / group_tokens * group_tokens;
+    const int64_t past = tokens - window < open ? tokens - window : open;
+    int32_t n = 0;
+    for (int64_t j = (sinks + BS - 1) / BS; (j + 1) * BS <= past; ++j)
+        if (t[(size_t)j] >= 0) {
+            p->give(t[(size_t)j]);
+            t[(size_t)j] = -1;
+            ++n;
+        }
+    if (n_released) *n_released = n;
+    return MI_OK;
+}
+
+extern "C" mi_status mi_kv_pool_compact(mi_kv_pool* p, int32_t* src_out, int32_t* dst_out, int32_t max_out,
+                                        int32_t* n_out) {
+    if (!p || max_out < 0 || !n_out || (max_out > 0 && (!src_out || !dst_out))) return MI_ERR_INVALID_ARG;
+    const int32_t used = p->num_blocks - (int32_t)p->free_stack.size();
+    int32_t n = 0;
+    for (int32_t b = used; b < p->num_blocks; ++b) n += p->refs[(size_t)b] > 0;
+    *n_out = n;
+    if (n > max_out) return MI_ERR_INVALID_ARG;
+    int32_t to = 0, i = 0;
+    for (int32_t b = used; b < p->num_blocks; ++b) {
+        if (p->refs[(size_t)b] == 0) continue;
+        while (p->refs[(size_t)to] > 0) ++to;
+        src_out[i] = b;
+        dst_out[i++] = to;
+        p->refs[(size_t)to] = p->refs[(size_t)b];
+        p->refs[(size_t)b] = -1 - to;  // where it went, until the tables follow
+    }
+    for (std::vector<int32_t>& t : p->tables)
+        for (int32_t& b : t)
+            if (b >= 0 && p->refs[(size_t)b] < 0) b = -1 - p->refs[(size_t)b];
+    for (int32_t b = used; b < p->num_blocks; ++b) {
+        p->refs[(size_t)b] = 0;
+        p->free_stack[(size_t)(p->num_blocks - 1 - b)] = b;
+    }
+    return MI_OK;
+}
+
+extern "C" int32_t mi_kv_pool_block_refs(const mi_kv_pool* p, int32_t block) {
+    return p && block >= 0 && block < p->num_blocks ? p->refs[(size_t)block] : -1;
 }

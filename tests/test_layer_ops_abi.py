@@ -1,0 +1,92 @@
+"""Argument checks of the normed append and of the page moves, made before
+anything is queued: no GPU, no device pointer is followed."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def mi():
+    import paged_kv_decode_25_gb300 as m
+    from paged_kv_decode_25_gb300 import build
+    build.build()
+    return m
+
+
+P = 1 << 32  # stands for device buffers far apart: aligned, never read
+BAD, UNSUPPORTED = 1, 4
+
+
+def dims(mi, **kw):
+    a = dict(B=2, Hq=8, Hkv=2, head_dim=128, num_blocks=64, max_blocks_per_seq=8, block_size=16)
+    a.update(kw)
+    return mi.dims(**a)
+
+
+def norm(mi, fp8=False, d=None, q=P, k=2 * P, v=3 * P, qw=4 * P, kw=5 * P, eps=1e-6, pos=6 * P, slot=7 * P, rope=8 * P,
+         max_pos=100, q_out=9 * P, kc=10 * P, vc=11 * P, ks=12 * P, vs=13 * P, strides=(1024, 256, 256)):
+    fn = mi.mi_paged_kv_append_norm_fp8 if fp8 else mi.mi_paged_kv_append_norm
+    args = (dims(mi) if d is None else d, q, k, v, qw, kw, eps, pos, slot, rope, max_pos, q_out, kc, vc)
+    return fn(*args, *((ks, vs) if fp8 else ()), stream=0, strides=strides)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_norm_refusals(mi, fp8):
+    for change, st in [(dict(B=-1), BAD), (dict(B=(1 << 24) + 1), BAD), (dict(Hq=0), BAD), (dict(Hkv=0), BAD),
+                       (dict(num_blocks=0), BAD), (dict(head_dim=96), UNSUPPORTED), (dict(block_size=32), UNSUPPORTED),
+                       (dict(Hq=7), UNSUPPORTED), (dict(num_blocks=1 << 27), BAD),
+                       (dict(Hq=1 << 25, Hkv=1 << 25), BAD)]:
+        assert norm(mi, fp8, d=dims(mi, **change)) == st, change
+    assert norm(mi, fp8, d=dims(mi, B=0)) == 0
+    names = "q k v qw kw pos slot rope q_out kc vc".split() + (["ks", "vs"] if fp8 else [])
+    for name in names:
+        assert norm(mi, fp8, **{name: 0}) == BAD, name
+    for name in "q k v qw kw rope q_out kc vc".split():
+        assert norm(mi, fp8, **{name: 20 * P + 8}) == BAD, name
+    for eps in (0.0, -1e-6, float("nan"), float("inf")):
+        assert norm(mi, fp8, eps=eps) == BAD, eps
+    assert norm(mi, fp8, max_pos=0) == BAD
+    for strides in ((1023, 256, 256), (1016, 256, 256), (1024, 248, 256), (1024, 256, 0), (1024, -256, 256),
+                    (1028, 256, 256), (1 << 40, 256, 256)):
+        assert norm(mi, fp8, strides=strides) == BAD, strides
+
+
+def test_norm_overlaps(mi):
+    """q_out may be q row for row, nothing else that is read."""
+    for at in (P + 2048, P + 16, P - 16):  # 2 rows of 1,024 elements
+        assert norm(mi, q_out=at) == BAD
+    for name in "k v".split():
+        assert norm(mi, q_out=3 * P, **{name: 3 * P + 4096 - 16}) == BAD
+        assert norm(mi, q_out=3 * P, **{name: 3 * P}) == BAD
+    assert norm(mi, q_out=P, strides=(1032, 256, 256)) == BAD  # q's rows lie apart, q_out's do not
+    assert norm(mi, q_out=P + 4096, strides=(1 << 20, 256, 256)) == BAD  # between q's rows
+
+
+def planes(mi, rows=((P, 4, 16),), src=2 * P, dst=3 * P, n=1, count=None):
+    a = (mi.MiKvPlane * max(1, len(rows)))(*(mi.MiKvPlane(*r) for r in rows))
+    return mi.mi_kv_copy_planes((a, len(rows) if count is None else count), src, dst, n, stream=0)
+
+
+def test_plane_refusals(mi):
+    assert planes(mi, n=0) == 0 and planes(mi, rows=()) == 0
+    assert planes(mi, n=-1) == BAD and planes(mi, count=-1) == BAD
+    assert mi.load().mi_kv_copy_planes(None, 1, 2 * P, 3 * P, 1, None, None) == BAD
+    assert mi.load().mi_kv_copy_planes(None, 0, 2 * P, 3 * P, 1, None, None) == 0
+    for row in ((0, 4, 16), (P + 2, 4, 16), (P, 0, 16), (P, -1, 16), (P, 1 << 31, 16), (P, 4, 0), (P, 4, 2), (P, 4, 18),
+                (P, 4, -4), (P, 1 << 20, 1 << 21), (P, 1, 1 << 62)):
+        assert planes(mi, rows=((P, 4, 16), row)) == BAD, row
+        assert planes(mi, rows=((P, 4, 16), row), n=0) == BAD, row
+    for name in ("src", "dst"):
+        assert planes(mi, **{name: 0}) == BAD and planes(mi, **{name: P + 2}) == BAD
+
+
+def test_planes_of_tensors(mi):
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(7, 2, 16, 64, dtype=torch.bfloat16)
+    y = torch.zeros(7, 2)
+    a, n = mi.kv_planes([x, y])
+    assert n == 2 and ctypes.sizeof(mi.MiKvPlane) == 24
+    assert (a[0].base, a[0].rows, a[0].row_bytes) == (x.data_ptr(), 7, 2 * 16 * 64 * 2)
+    assert (a[1].base, a[1].rows, a[1].row_bytes) == (y.data_ptr(), 7, 8)
+    with pytest.raises(AssertionError):
+        mi.kv_planes([x.transpose(1, 2)])

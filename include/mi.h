@@ -569,6 +569,49 @@ mi_status mi_paged_decode_attention_int8(const mi_dims* dims, const void* q, con
                                          void* out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
                                          mi_stream_t stream);
 
+/* ---- Sliding windows with sinks. In layers with a window a token sees the newest
+ * `window` tokens up to itself and its sequence's first `sinks` ones (which keep
+ * the softmax where it was trained to be): with p its position, tokens t <= p with
+ * t > p - window or t < sinks. window >= 1 (it counts the token itself), sinks >= 0;
+ * a window no smaller than the context sees all of it. Keys keep the rotation of
+ * the position they were appended at. */
+
+/* mi_paged_decode_attention within the window: with n = context_lens[b],
+ *   out[b][j] = sum_t softmax_t(scale * <q[b][j], K_t>) V_t,
+ *               t < n and (t >= n - window or t < sinks).
+ * Table entries of blocks that hold no such token are not read (they may be -1:
+ * mi_kv_pool_slide gives such blocks back), nor is anything of tokens out of sight.
+ * One launch. The workspace has mi_paged_sliding_workspace_bytes() bytes, 16-byte
+ * aligned; its contents need no initialisation, and a captured call can be replayed
+ * over it; calls that may run at the same time take different ones, and after
+ * MI_DEVERR_TIMEOUT it is zeroed before a replay. B * Hkv up to 2^30. Other
+ * arguments, errors and guarantees as mi_paged_decode_attention. */
+mi_status mi_paged_decode_attention_sliding(const mi_dims* dims, const void* q, const void* k_cache,
+                                            const void* v_cache, const int32_t* block_tables,
+                                            const int32_t* context_lens, int32_t window, int32_t sinks, float scale,
+                                            void* out, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                            mi_stream_t stream);
+
+/* The same over FP8 caches (mi_paged_decode_attention_fp8). */
+mi_status mi_paged_decode_attention_sliding_fp8(const mi_dims* dims, const void* q, const void* k_cache,
+                                                const void* v_cache, const float* k_scale, const float* v_scale,
+                                                const int32_t* block_tables, const int32_t* context_lens,
+                                                int32_t window, int32_t sinks, float scale, void* out,
+                                                void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                                mi_stream_t stream);
+
+/* The same over INT8 caches (mi_paged_decode_attention_int8). */
+mi_status mi_paged_decode_attention_sliding_int8(const mi_dims* dims, const void* q, const void* k_cache,
+                                                 const void* v_cache, const float* k_amax, const float* v_amax,
+                                                 const int32_t* block_tables, const int32_t* context_lens,
+                                                 int32_t window, int32_t sinks, float scale, void* out,
+                                                 void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                                 mi_stream_t stream);
+
+/* Workspace of the three calls in bytes on the current device; 0 when the sizes are
+ * not supported. */
+size_t mi_paged_sliding_workspace_bytes(const mi_dims* dims, int32_t window, int32_t sinks);
+
 /* Causal paged GQA attention for a prefill or chunked-prefill batch (NJU
  * course brief §2.1, the prefill stage of the prefill + decode loop; mini-infer
  * README "项目概述", prefill as its own pass). dims.B = R requests. Request r

@@ -48,6 +48,8 @@ EXPORTS = (
     "mi_paged_prefill_scores", "mi_paged_prefill_scores_workspace_bytes",
     "mi_paged_kv_evict", "mi_paged_kv_evict_fp8", "mi_paged_kv_evict_workspace_bytes",
     "mi_paged_kv_append_norm", "mi_paged_kv_append_norm_fp8",
+    "mi_paged_decode_attention_sliding", "mi_paged_decode_attention_sliding_fp8",
+    "mi_paged_decode_attention_sliding_int8", "mi_paged_sliding_workspace_bytes",
     "mi_kv_pool_fork", "mi_kv_pool_slide", "mi_kv_pool_compact", "mi_kv_pool_block_refs", "mi_kv_copy_planes",
     "mi_paged_decode_step", "mi_paged_decode_step_fp8", "mi_test_set_wait_limit", "mi_test_withhold_copy",
 )
@@ -142,6 +144,13 @@ def load():
                 [dims_p, P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32, P, P, P, P, P], i32),
             "mi_paged_kv_append_norm_fp8": (
                 [dims_p, P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32, P, P, P, P, P, P, P], i32),
+            "mi_paged_sliding_workspace_bytes": ([dims_p, i32, i32], ctypes.c_size_t),
+            "mi_paged_decode_attention_sliding": (
+                [dims_p, P, P, P, P, P, i32, i32, f32, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_decode_attention_sliding_fp8": (
+                [dims_p, P, P, P, P, P, P, P, i32, i32, f32, P, P, ctypes.c_size_t, P, P], i32),
+            "mi_paged_decode_attention_sliding_int8": (
+                [dims_p, P, P, P, P, P, P, P, i32, i32, f32, P, P, ctypes.c_size_t, P, P], i32),
             "mi_kv_pool_fork": ([P, i32, i32, i32, i32, P, P, i32, P], i32),
             "mi_kv_pool_slide": ([P, i32, i32, i32, i32, P], i32),
             "mi_kv_pool_compact": ([P, P, P, i32, P], i32),
@@ -692,6 +701,39 @@ def mi_paged_kv_append_norm_fp8(d: MiDims, q, k, v, q_weight, k_weight, eps, pos
     """mi_paged_kv_append_norm into e4m3 caches."""
     return _append_norm(load().mi_paged_kv_append_norm_fp8, d, q, k, v, q_weight, k_weight, eps, positions, slot_mapping,
                         rope_cos_sin, max_pos, q_out, (k_cache, v_cache, k_scale, v_scale), strides, dev_err, stream)
+
+
+def mi_paged_sliding_workspace_bytes(d: MiDims, window, sinks) -> int:
+    return int(load().mi_paged_sliding_workspace_bytes(ctypes.byref(d), int(window), int(sinks)))
+
+
+def mi_paged_decode_attention_sliding(d: MiDims, q, k_cache, v_cache, block_tables, context_lens, window, sinks, scale,
+                                      out, workspace, workspace_bytes=None, dev_err=None, stream=None):
+    """Decode attention over each request's first `sinks` and newest `window` tokens."""
+    return load().mi_paged_decode_attention_sliding(
+        ctypes.byref(d), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), int(window),
+        int(sinks), float(scale), _ptr(out), _ptr(workspace), _nbytes(workspace, workspace_bytes), _ptr(dev_err),
+        _stream(stream))
+
+
+def mi_paged_decode_attention_sliding_fp8(d: MiDims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                                          window, sinks, scale, out, workspace, workspace_bytes=None, dev_err=None,
+                                          stream=None):
+    """mi_paged_decode_attention_sliding over e4m3 caches."""
+    return load().mi_paged_decode_attention_sliding_fp8(
+        ctypes.byref(d), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        _ptr(context_lens), int(window), int(sinks), float(scale), _ptr(out), _ptr(workspace),
+        _nbytes(workspace, workspace_bytes), _ptr(dev_err), _stream(stream))
+
+
+def mi_paged_decode_attention_sliding_int8(d: MiDims, q, k_cache, v_cache, k_amax, v_amax, block_tables, context_lens,
+                                           window, sinks, scale, out, workspace, workspace_bytes=None, dev_err=None,
+                                           stream=None):
+    """mi_paged_decode_attention_sliding over INT8 caches."""
+    return load().mi_paged_decode_attention_sliding_int8(
+        ctypes.byref(d), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_amax), _ptr(v_amax), _ptr(block_tables),
+        _ptr(context_lens), int(window), int(sinks), float(scale), _ptr(out), _ptr(workspace),
+        _nbytes(workspace, workspace_bytes), _ptr(dev_err), _stream(stream))
 
 
 def kv_planes(tensors):

@@ -24,7 +24,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contra
               "-I" + INCLUDE] + ARCH
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-I" + INCLUDE]
 CU_SOURCES = ["append.cu", "decode.cu", "evict.cu", "int8.cu", "noalloc.cu", "norm.cu", "pages.cu", "prefill.cu",
-              "prefix.cu", "scored.cu", "swap.cu", "window.cu"]
+              "prefix.cu", "scored.cu", "sliding.cu", "swap.cu", "window.cu"]
 CPP_SOURCES = ["pool.cpp"]
 
 

@@ -90,3 +90,36 @@ def test_planes_of_tensors(mi):
     assert (a[1].base, a[1].rows, a[1].row_bytes) == (y.data_ptr(), 7, 8)
     with pytest.raises(AssertionError):
         mi.kv_planes([x.transpose(1, 2)])
+
+
+def sliding(mi, kind="bf16", d=None, q=P, k=2 * P, v=3 * P, ks=4 * P, vs=5 * P, tab=6 * P, lens=7 * P, window=10, sinks=2,
+            scale=0.1, out=8 * P, ws=9 * P, nbytes=1 << 40):
+    fn = {"bf16": mi.mi_paged_decode_attention_sliding, "fp8": mi.mi_paged_decode_attention_sliding_fp8,
+          "int8": mi.mi_paged_decode_attention_sliding_int8}[kind]
+    return fn(dims(mi) if d is None else d, q, k, v, *(() if kind == "bf16" else (ks, vs)), tab, lens, window, sinks, scale,
+              out, ws, workspace_bytes=nbytes, stream=0)
+
+
+BAD_DIMS = [(dict(B=-1), 1), (dict(B=65536), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(num_blocks=0), 1),
+            (dict(max_blocks_per_seq=0), 1), (dict(head_dim=96), 4), (dict(head_dim=256), 4), (dict(block_size=32), 4),
+            (dict(Hq=7, Hkv=2), 4), (dict(Hq=9, Hkv=1), 4), (dict(num_blocks=1 << 27, Hkv=8, Hq=8), 1),
+            (dict(max_blocks_per_seq=(1 << 27) - 127), 1), (dict(B=65535, Hkv=1 << 15, Hq=1 << 15, num_blocks=1), 1)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int8"])
+def test_sliding_refusals(mi, kind):
+    for change, st in BAD_DIMS:
+        assert sliding(mi, kind, d=dims(mi, **change)) == st, change
+    assert sliding(mi, kind, d=dims(mi, B=0)) == 0
+    for kw in (dict(window=0), dict(window=-1), dict(sinks=-1), dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert sliding(mi, kind, **kw) == BAD, kw
+    for name in "q k v tab lens out ws".split() + (["ks", "vs"] if kind != "bf16" else []):
+        assert sliding(mi, kind, **{name: 0}) == BAD, name
+    for name in "q k v out ws".split():
+        assert sliding(mi, kind, **{name: 20 * P + 8}) == BAD, name
+    if kind != "bf16":
+        assert sliding(mi, kind, ks=20 * P + 2) == BAD and sliding(mi, kind, vs=20 * P + 1) == BAD
+    for change, _ in BAD_DIMS:
+        assert mi.mi_paged_sliding_workspace_bytes(dims(mi, **change), 10, 2) == 0
+    assert mi.mi_paged_sliding_workspace_bytes(dims(mi), 0, 2) == 0
+    assert mi.mi_paged_sliding_workspace_bytes(dims(mi), 1, -1) == 0

@@ -12,7 +12,7 @@
 // one mbarrier a stage), runs the decode tiles over them and writes the result,
 // with no barrier among warps. A (request, head) of one piece is done then; of the
 // others the warp that stores the last piece adds all of them up by their
-// log-sum-exps, counted in a word per (request, head).
+// log-sum-exps.
 #include <atomic>
 #include <chrono>
 #include <cmath>
@@ -29,28 +29,38 @@ namespace {
 
 constexpr int kSlideWarps = 4;
 
+// Warps of an SM hide one another's latency: sixteen where registers and tiles allow.
 template <int HD, int VAR>
 struct SlideShape {
     static constexpr int kTile = Tile<HD, elem_bytes(VAR)>::kBytes;
-    static constexpr int kStages = 16384 / (2 * kTile) < 4 ? 16384 / (2 * kTile) : 4;
-    static constexpr int kBlocksPerSm = 3;
+    static constexpr int kBlocksPerSm = VAR == kVarMma ? 3 : 4;
+    static constexpr int kRing = kBlocksPerSm == 3 ? 16384 : 12288;  // bytes of a warp's stages, at most
+    static constexpr int kStages = kRing / (2 * kTile) < 4 ? kRing / (2 * kTile) : 4;
     static constexpr int kSmem = kSlideWarps * kStages * 2 * kTile + 1024;  // slack to align the tiles
 };
 
 // Pieces that have partial results, at most, per warp of the grid.
 constexpr int kSplitPerWarp = 8;
-// A piece's own cost (its queries, its output, finding the next), in blocks, and
-// that of adding up one piece at a (request, head)'s end.
-constexpr float kPieceCost = 2.f, kMergeCost = 0.1f;
+// A piece's own cost (its queries, its output, finding the next), in blocks; that of
+// a split unit's end, and of each piece that is added up there.
+constexpr float kPieceCost = 2.f, kSplitCost = 3.f, kMergeCost = 0.2f;
+
+// Piece i of the np of (request b, head h): blocks in sight j .. j1 - 1; `slot`: the
+// unit's first partial result. b < 0: no more pieces.
+struct SlidePiece {
+    int b, h, i, np, slot, j, j1;
+};
+constexpr int kPieceRing = 8;
+constexpr int kOwed = 8;
 
 struct SlideParams {
     const uint16_t* q;             // [B][Hq][HD]
     const int32_t* block_tables;   // [B][mbps]
     const int32_t* context_lens;   // [B]
     uint16_t* out;                 // [B][Hq][HD]
-    unsigned long long* words;     // [most]: at a split unit's first piece: epoch | pieces stored
+    unsigned long long* words;     // [most]: at a split unit's first piece: tag | pieces done
     float* part;                   // [most][slot_floats] normalised output [G][HD], log2-sum-exps [G]
-    unsigned long long epoch;      // distinct per call
+    unsigned long long tag;        // of the call, in the high 48 bits; never zero
     const float* k_scale;          // [Hkv] e4m3 caches
     const float* v_scale;
     const float* k_amax;           // [num_blocks][Hkv] INT8 caches
@@ -68,126 +78,133 @@ __device__ __forceinline__ Sight sight_of(const SlideParams& p, int b) {
     return Sight(n < 0 ? 0 : (n > cap ? cap : n), p.window, p.sinks);
 }
 
-// The blocks of a piece, chosen by every block of the launch alike: lane i tries
-// i + 1 (and 32 + 15 i) pieces for the largest unit. Warps take whole pieces in
-// turn; full rounds run at the memory's rate, in the last one a warp's own time may
-// show, and so may the end of the unit with the most pieces.
-__device__ int piece_blocks(const SlideParams& p, int warps, float blocks, float units, int largest, int lane) {
+// The blocks of a piece, chosen by every block of the launch alike: a lane tries 1
+// to 16 pieces for the largest unit, or 16 to 448 in steps of a quarter. Warps take
+// whole pieces in turn: full rounds run at the memory's rate, in the last one a
+// warp's own time may show, and so may the end of the unit with the most pieces.
+__device__ int piece_blocks(const SlideParams& p, float warps, float blocks, float units, int largest, int lane) {
     const float all = blocks * p.flow;  // time of all blocks at the memory's rate, in a warp's block times
-    float best = 3.0e38f, step = (float)largest;
-    const float floor_step = fmaxf(1.f, ceilf(2.f * blocks / ((float)kSplitPerWarp * (float)warps)));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float np = i == 0 ? (float)(lane + 1) : (float)(32 + 15 * lane);
-        const float s = fmaxf(floor_step, ceilf((float)largest / np));
-        const float most = ceilf((float)largest / s);
-        // pieces: those of units of the largest size, and half a piece more than their share for the others
-        const float even = units * (float)largest;
-        const float pieces = even > 0.f ? units * most * (blocks / even) + 0.5f * units * (1.f - blocks / even) : 1.f;
-        const float rounds = fmaxf(pieces, units) / (float)warps, full = floorf(rounds);
-        const float cost = (full > 0.f ? full / rounds * all : 0.f) +
-                           fmaxf(s + kPieceCost, (rounds - full) / rounds * all) + (most > 1.f ? kMergeCost * most : 0.f) +
-                           0.01f * kPieceCost * rounds;
-        if (cost < best) {
-            best = cost;
-            step = s;
-        }
-    }
+    const float np = lane < 16 ? (float)(lane + 1) : (float)((16 + 4 * (lane & 3)) << ((lane - 16) >> 2));
+    const float big = (float)largest;
+    const float least = fmaxf(1.f, ceilf(__fdividef(2.f * blocks, (float)kSplitPerWarp * warps)));
+    float step = fmaxf(least, ceilf(__fdividef(big, np)));
+    const float most = ceilf(__fdividef(big, step));
+    // the largest units have `most` pieces, the others half a piece more than their share
+    const float fill = __fdividef(blocks, units * big);
+    const float rounds = __fdividef(fmaxf(units * (most * fill + 0.5f * (1.f - fill)), units), warps);
+    const float part = __fdividef(rounds - floorf(rounds), rounds);
+    float cost = (1.f - part) * all + fmaxf(step + kPieceCost, part * all) + 0.1f * rounds +
+                 (most > 1.f ? kSplitCost + kMergeCost * most : 0.f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float c = __shfl_xor_sync(0xffffffffu, best, o), t = __shfl_xor_sync(0xffffffffu, step, o);
-        if (c < best || (c == best && t < step)) {
-            best = c;
+        const float c = __shfl_xor_sync(0xffffffffu, cost, o), t = __shfl_xor_sync(0xffffffffu, step, o);
+        if (c < cost || (c == cost && t < step)) {
+            cost = c;
             step = t;
         }
     }
-    return (int)step;
+    return max(1, (int)step);
 }
 
-// Whether this warp, its partial result written, is the last one of a unit of np
-// pieces. The count is a word at the unit's first piece: high 48 bits the call's
-// epoch, low 16 the pieces stored, so a word of another call counts as zero; the
-// last piece hands it back as zero, so a captured call can be replayed.
+// A split unit counts its finished pieces in a word: the call's tag in the high 48
+// bits, the pieces in the low 16. A word with another tag (of an earlier call, or
+// whatever the workspace held) counts as zero: the first piece sets it up at its
+// start, so that at their ends an addition is enough. (Counting by compare-and-swap
+// alone lets one piece on per trip to L2: 54 us for a request in 22 pieces a head.)
+// The last piece zeroes the word: a captured call keeps its tag.
+constexpr unsigned long long kCount = 0xFFFFull;
+
+__device__ __forceinline__ void open_count(unsigned long long* word, unsigned long long tag) {
+    const unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+    if ((old & ~kCount) != tag) atomicCAS(word, old, tag);
+}
+
+// Whether the piece whose result lane 0's warp has just written is the unit's last.
 __device__ __forceinline__ bool last_piece(const SlideParams& p, int slot, int np, int lane) {
-    __syncwarp();
+    unsigned long long* word = p.words + slot;
     int last = 0;
+    __syncwarp();
     if (lane == 0) {
-        unsigned long long* wd = p.words + slot;
-        const unsigned long long e48 = p.epoch & 0xFFFFFFFFFFFFull;
-        unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(wd), nw, got;
-        for (;;) {
-            nw = ((old >> 16) == e48) ? old + 1 : ((e48 << 16) | 1ull);
-            // this warp's partial result before the count, the others' after it
-            asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
-                         : "=l"(got) : "l"(wd), "l"(old), "l"(nw) : "memory");
-            if (got == old) break;
-            old = got;
+        // this warp's result before the count, the others' after it
+        unsigned long long old;
+        asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+        while ((old & ~kCount) != p.tag) {
+            unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word), got;
+            if ((seen & ~kCount) == p.tag) {
+                asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+            } else {
+                asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                             : "=l"(got) : "l"(word), "l"(seen), "l"(p.tag | 1ull) : "memory");
+                if (got == seen) old = p.tag;
+            }
         }
-        last = (int)(nw & 0xFFFFull) == np;
-        if (last) *reinterpret_cast<volatile unsigned long long*>(wd) = 0ull;
+        last = (int)(old & kCount) + 1 == np;
+        if (last) *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
     }
     last = __shfl_sync(0xffffffffu, last, 0);
-    __syncwarp();
     return last != 0;
 }
 
-// The unit's output from its np pieces, in order: weights 2^(lse - M) over their
-// sum, a lane per piece; then four outputs a lane and 512 bytes of a piece at a
-// time, sixteen loads in flight.
+// The unit's output from its np pieces, in order: out = sum 2^(lse - M) o over the
+// weights' sum, with a running maximum. A lane has four outputs of each of two
+// groups of 128; four pieces' loads are in flight. (Short code: it runs once or
+// twice in a launch, and instructions come from as far as the data. With the
+// maxima found first, over the lanes, eight heads unrolled, it took 6 us for three
+// pieces and 15 for 22.)
 template <int HD>
 __device__ void merge_unit(const SlideParams& p, int b, int h, int slot, int np, int lane) {
     const float* part = p.part + (long long)slot * p.slot_floats;
     const int outs = p.G * HD;
-    float top[kMaxG], den[kMaxG];
-#pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-        top[g] = kNegInf;
-        if (g < p.G)
-            for (int i = lane; i < np; i += 32) top[g] = fmaxf(top[g], __ldcg(part + (long long)i * p.slot_floats + outs + g));
-    }
-#pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top[g] = fmaxf(top[g], __shfl_xor_sync(0xffffffffu, top[g], o));
-        den[g] = 0.f;
-        if (top[g] == kNegInf) top[g] = 0.f;  // nothing in sight: weights 0
-        if (g < p.G)
-            for (int i = lane; i < np; i += 32) den[g] += exp2f(__ldcg(part + (long long)i * p.slot_floats + outs + g) - top[g]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) den[g] += __shfl_xor_sync(0xffffffffu, den[g], o);
-        den[g] = den[g] > 0.f ? 1.f / den[g] : 0.f;
-    }
     uint16_t* out = p.out + ((long long)b * p.Hq + (long long)h * p.G) * HD;
-    for (int k0 = 4 * lane; k0 < outs; k0 += 512) {  // up to four groups of 128 outputs
-        float4 acc[4];
+#pragma unroll 1
+    for (int x0 = 4 * lane; x0 - 4 * lane < outs; x0 += 256) {
+        float top[2], den[2];
+        float4 acc[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < np; ++i) {
-            const float* at = part + (long long)i * p.slot_floats;
+        for (int k = 0; k < 2; ++k) {
+            top[k] = kNegInf;
+            den[k] = 0.f;
+            acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < np; i0 += 2) {
+            float lse[2][2];
+            float4 v[2][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int x = k0 + 128 * k;
-                if (x < outs) {
-                    const int g = x / HD;
-                    float t = top[0], d = den[0];
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 1; e < kMaxG; ++e)
-                        if (g == e) {
-                            t = top[e];
-                            d = den[e];
-                        }
-                    const float w = exp2f(__ldcg(at + outs + g) - t) * d;
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(at + x));
-                    acc[k].x += w * v.x;
-                    acc[k].y += w * v.y;
-                    acc[k].z += w * v.z;
-                    acc[k].w += w * v.w;
+                for (int k = 0; k < 2; ++k) {
+                    const int x = x0 + 128 * k;
+                    lse[i][k] = kNegInf;
+                    if (i0 + i < np && x < outs) {
+                        const float* at = part + (long long)(i0 + i) * p.slot_floats;
+                        lse[i][k] = __ldcg(at + outs + x / HD);
+                        v[i][k] = __ldcg(reinterpret_cast<const float4*>(at + x));
+                    }
                 }
-            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (lse[i][k] == kNegInf) continue;  // no piece, or nothing of it in sight
+                    const float t = fmaxf(top[k], lse[i][k]);
+                    const float f = ex2(top[k] - t), w = ex2(lse[i][k] - t);
+                    top[k] = t;
+                    den[k] = den[k] * f + w;
+                    acc[k].x = acc[k].x * f + w * v[i][k].x;
+                    acc[k].y = acc[k].y * f + w * v[i][k].y;
+                    acc[k].z = acc[k].z * f + w * v[i][k].z;
+                    acc[k].w = acc[k].w * f + w * v[i][k].w;
+                }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k0 + 128 * k < outs) *reinterpret_cast<uint2*>(out + k0 + 128 * k) = pack_bf16x4(acc[k]);
+        for (int k = 0; k < 2; ++k) {
+            const int x = x0 + 128 * k;
+            const float r = den[k] > 0.f ? 1.f / den[k] : 0.f;
+            if (x < outs)
+                *reinterpret_cast<uint2*>(out + x) =
+                    pack_bf16x4(make_float4(acc[k].x * r, acc[k].y * r, acc[k].z * r, acc[k].w * r));
+        }
     }
 }
 
@@ -208,15 +225,23 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
     constexpr bool kInt8 = VAR == kVarInt8, kFp8 = VAR == kVarFp8;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long bars[kSlideWarps * S];
-    __shared__ long long sums[flat_words(kThreads)], split_sums[flat_words(kThreads)];
+    __shared__ float maxima[kInt8 ? kSlideWarps * S * 2 : 1];  // of a stage's block: K's, V's
+    // usual batches: blocks in sight, pieces before, those of split units; larger ones: chunks' sums
+    __shared__ union {
+        struct {
+            int held[kFlatOneWarp], first[kFlatOneWarp + 1], first_split[kFlatOneWarp];
+        };
+        struct {
+            long long sums[flat_words(kThreads)], split_sums[flat_words(kThreads)];
+        };
+    } plan;
     __shared__ long long red[2][kSlideWarps];
     __shared__ int red_top[kSlideWarps];
-    __shared__ int held[kFlatOneWarp], first[kFlatOneWarp + 1], first_split[kFlatOneWarp];  // usual batches
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t full = smem_u32(bars) + warp * S * 8;
     const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + (uint32_t)(warp * S * 2 * kTile);
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(full + 8 * i, 1);
+        for (int i = 0; i < S; ++i) mbar_init(full + 8 * i, kInt8 ? 2 : 1);  // the tiles; the maxima
         fence_mbar_init();
     }
     pdl_wait();
@@ -228,7 +253,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
     for (int b = tid; b < p.B; b += kThreads) {
         const int n = __ldg(p.context_lens + b);
         const int nb = sight_of(p, b).blocks;
-        if (small) held[b] = nb;
+        if (small) plan.held[b] = nb;
         blocks += (long long)p.Hkv * nb;
         units += nb > 0 ? p.Hkv : 0;
         largest = max(largest, nb);
@@ -260,20 +285,20 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
     }
     if (largest == 0) return;
     const int warps = gridDim.x * kSlideWarps;
-    const int step = piece_blocks(p, warps, (float)blocks, (float)units, largest, lane);
+    const int step = piece_blocks(p, (float)warps, (float)blocks, (float)units, largest, lane);
     auto pieces_of = [&](int nb) { return (nb + step - 1) / step; };
     auto pieces = [&](int b) { return (long long)p.Hkv * pieces_of(sight_of(p, b).blocks); };
     auto splits = [&](int b) {
         const int np = pieces_of(sight_of(p, b).blocks);
         return np > 1 ? (long long)p.Hkv * np : 0LL;
     };
-    long long total;
+    int total;
     if (small) {
         if (warp == 0) {
             const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
             int v = 0, w = 0;
             for (int b = b0; b < b1; ++b) {
-                const int np = pieces_of(held[b]);
+                const int np = pieces_of(plan.held[b]);
                 v += p.Hkv * np;
                 w += np > 1 ? p.Hkv * np : 0;
             }
@@ -286,133 +311,132 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
                     y += t;
                 }
             }
-            if (lane == 31) first[p.B] = x;
+            if (lane == 31) plan.first[p.B] = x;
             x -= v;
             y -= w;
             for (int b = b0; b < b1; ++b) {
-                const int np = pieces_of(held[b]);
-                first[b] = x;
-                first_split[b] = y;
+                const int np = pieces_of(plan.held[b]);
+                plan.first[b] = x;
+                plan.first_split[b] = y;
                 x += p.Hkv * np;
                 y += np > 1 ? p.Hkv * np : 0;
             }
         }
         __syncthreads();
-        total = first[p.B];
+        total = plan.first[p.B];
     } else {
-        total = flat_scan(p.B, pieces, sums);
-        (void)flat_scan(p.B, splits, split_sums);
+        total = (int)flat_scan(p.B, pieces, plan.sums);
+        (void)flat_scan(p.B, splits, plan.split_sums);
     }
     // ---------------------------------------------------------- the pieces --
-    struct Piece {
-        long long x;
-        int b, h, i, np, slot;  // piece i of the np of (request, head); the first one's partial result
-        int j, j1;              // blocks in sight j .. j1 - 1
+    // The issuing side runs up to S blocks ahead, across pieces; it leaves what the
+    // computing side needs of a piece in a ring (S + 2 pieces at most: the one
+    // computed, one for each block ahead, and the next). Table entries come 32 at a time.
+    __shared__ SlidePiece ring_of[kSlideWarps][kPieceRing];
+    static_assert(S + 2 <= kPieceRing, "pieces in flight");
+    SlidePiece* pieces_ahead = ring_of[warp];
+    int x = (int)blockIdx.x * kSlideWarps + warp;  // the issuing side's piece, or past the last
+    int in_b = 0, in_h = 0, in_j = 0, in_j1 = 0, entry = -1, ahead = 0, found = 0;
+    auto fetch = [&]() {
+        ahead = 0;
+        const int j = in_j + lane;
+        entry = j < in_j1 ? __ldg(p.block_tables + (long long)in_b * p.mbps + sight_of(p, in_b).column(j)) : -1;
     };
-    auto piece = [&](long long x) {
-        Piece c;
-        c.x = x;
-        c.b = c.h = c.i = c.j = c.j1 = c.slot = 0;
-        c.np = 1;
+    auto find = [&]() {
+        SlidePiece c;
+        c.b = -1;
+        in_j = in_j1 = 0;
         if (x < total) {
             int o, nb;
             if (small) {
                 int lo = 0, hi = p.B;  // first[lo] <= x < first[hi]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (first[mid] <= (int)x) lo = mid;
+                    if (plan.first[mid] <= x) lo = mid;
                     else hi = mid;
                 }
                 c.b = lo;
-                nb = held[lo];
-                o = (int)x - first[lo];
-                c.slot = first_split[lo];
+                nb = plan.held[lo];
+                o = x - plan.first[lo];
+                c.slot = plan.first_split[lo];
             } else {
                 long long before;
-                c.b = flat_find(p.B, pieces, sums, x, before);
+                c.b = flat_find(p.B, pieces, plan.sums, x, before);
                 nb = sight_of(p, c.b).blocks;
                 o = (int)(x - before);
-                c.slot = (int)flat_before(p.B, splits, split_sums, c.b);
+                c.slot = (int)flat_before(p.B, splits, plan.split_sums, c.b);
             }
             c.np = pieces_of(nb);
             c.h = o / c.np;
             c.i = o - c.h * c.np;
             c.slot += c.h * c.np;
             // equal shares of the unit's blocks
-            c.j = (int)((long long)nb * c.i / c.np);
-            c.j1 = (int)((long long)nb * (c.i + 1) / c.np);
+            c.j = in_j = (int)((long long)nb * c.i / c.np);
+            c.j1 = in_j1 = (int)((long long)nb * (c.i + 1) / c.np);
+            in_b = c.b;
+            in_h = c.h;
         }
-        return c;
+        if (lane == 0) pieces_ahead[found & (kPieceRing - 1)] = c;
+        ++found;
+        __syncwarp();
+        fetch();
     };
     const uint64_t policy = l2_policy_evict_first();
-    // the issuing side runs up to S blocks ahead, across pieces; table entries (and
-    // an INT8 block's maxima) come 32 at a time
-    Piece in = piece((long long)blockIdx.x * kSlideWarps + warp);
-    Sight in_sight = sight_of(p, in.b);
-    int entry = -1, base = 0;
-    float ka = 0.f, va = 0.f;
-    auto fetch = [&]() {
-        base = in.j;
-        entry = -1;
-        ka = va = 0.f;
-        if (in.x < total && in.j + lane < in.j1) {
-            entry = __ldg(p.block_tables + (long long)in.b * p.mbps + in_sight.column(in.j + lane));
-            if (kInt8 && entry >= 0 && entry < p.num_blocks) {
-                ka = __ldg(p.k_amax + (long long)entry * p.Hkv + in.h);
-                va = __ldg(p.v_amax + (long long)entry * p.Hkv + in.h);
-            }
-        }
-    };
-    fetch();
-    uint32_t issued = 0, copied = 0, phase = 0;  // stages used; bit i: stage i holds a block; its parity
-    float ks_of[kInt8 ? S : 1], vs_of[kInt8 ? S : 1];
+    find();
+    uint32_t copied = 0, phase = 0;  // bit i: stage i holds a block, or will; its parity
     bool withhold = p.withhold != 0;
     auto issue = [&](uint32_t st) {
-        if (in.x >= total) return;
-        const int blk = __shfl_sync(0xffffffffu, entry, in.j - base);
-        if constexpr (kInt8) {
-            const float a = __shfl_sync(0xffffffffu, ka, in.j - base), v = __shfl_sync(0xffffffffu, va, in.j - base);
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                if (st == (uint32_t)i) {
-                    ks_of[i] = a;
-                    vs_of[i] = v;
-                }
-        }
+        if (x >= total) return;
+        const int blk = __shfl_sync(0xffffffffu, entry, ahead);
         const bool ok = blk >= 0 && blk < p.num_blocks;
         if (lane == 0) {
             if (!ok) {
                 raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
             } else if (!withhold) {
                 const uint32_t bar = full + 8 * st, dst = ring + st * 2 * kTile;
-                const int y = (blk * p.Hkv + in.h) * (kTile / 128);
+                const int y = (blk * p.Hkv + in_h) * (kTile / 128);
                 mbar_arrive_expect_tx(bar, 2 * kTile);
                 tma_load_2d(dst, &tmk, bar, 0, y, policy);
                 tma_load_2d(dst + kTile, &tmv, bar, 0, y, policy);
+                if constexpr (kInt8) {
+                    // the block's maxima arrive on the same barrier
+                    const uint32_t at = smem_u32(maxima + (warp * S + st) * 2);
+                    const long long e = (long long)blk * p.Hkv + in_h;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(p.k_amax + e) : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 4), "l"(p.v_amax + e) : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+                }
             }
         }
         withhold = false;
-        copied = ok ? copied | (1u << st) : copied & ~(1u << st);
-        ++issued;
-        if (++in.j == in.j1) {
-            in = piece(in.x + warps);
-            in_sight = sight_of(p, in.b);
-            fetch();
-        } else if (in.j - base == 32) {
+        if (ok) copied |= 1u << st;
+        ++ahead;
+        if (++in_j == in_j1) {
+            x += warps;
+            find();
+        } else if (ahead == 32) {
             fetch();
         }
     };
-    __syncwarp();
-    Piece c = in;
     for (int i = 0; i < S; ++i) issue((uint32_t)i);
-    uint32_t taken = 0;
+    uint32_t sg = 0;  // the stage whose block comes next
     bool dead = false;
     typename TileOf<HD, VAR>::T st;
-    while (!dead && c.x < total) {
+    // units whose last piece was this warp's are added up behind its pieces (or when
+    // kOwed of them wait): among the tiles' registers the sums would have spilled
+    __shared__ SlidePiece owed_by[kSlideWarps][kOwed];
+    SlidePiece* owed = owed_by[warp];
+    int done = 0, owes = 0;
+    for (bool more = true; more;) {
+    for (;; ++done) {
+        const SlidePiece& c = pieces_ahead[done & (kPieceRing - 1)];
+        more = !dead && c.b >= 0;
+        if (!more || owes == kOwed) break;
         const Sight sight = sight_of(p, c.b);
         st.begin_unit(p, c.b, c.h, lane);
-        for (int j = c.j; j < c.j1; ++j, ++taken) {
-            const uint32_t sg = taken % S;
+        if (c.np > 1 && c.i == 0 && lane == 0) open_count(p.words + c.slot, p.tag);
+        const int j1 = c.j1;
+        for (int j = c.j; j < j1; ++j) {
             if ((copied >> sg) & 1u) {
                 if (!wait_warp(full + 8 * sg, (phase >> sg) & 1u, p.wait_ns)) {
                     if (lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
@@ -420,6 +444,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
                     break;
                 }
                 phase ^= 1u << sg;
+                copied &= ~(1u << sg);
                 const uint32_t kt = ring + sg * 2 * kTile, vt = kt + kTile;
                 const uint32_t seen = sight.mask(sight.column(j));
                 if (!kInt8 && seen != 0xFFFFu) {
@@ -432,14 +457,8 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
                     __syncwarp();
                 }
                 if constexpr (kInt8) {
-                    float a = ks_of[0], v = vs_of[0];
-#pragma unroll
-                    for (int i = 1; i < S; ++i)
-                        if (sg == (uint32_t)i) {
-                            a = ks_of[i];
-                            v = vs_of[i];
-                        }
-                    st.block(kt, vt, TokenMask{seen}, lane, a, v);
+                    const float* m = maxima + (warp * S + sg) * 2;
+                    st.block(kt, vt, TokenMask{seen}, lane, m[0], m[1]);
                 } else {
                     st.block(kt, vt, TokenMask{seen}, p.sl2, lane);
                 }
@@ -447,6 +466,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
                 if (lane == 0) fence_proxy_async_smem();
             }
             issue(sg);
+            sg = sg + 1 == S ? 0 : sg + 1;
         }
         if (dead) break;
         st.sums();
@@ -479,16 +499,21 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
                 const int g = 2 * (lane & 3) + w;
                 if (lane < 4 && g < p.G) part[p.G * HD + g] = st.l[w] > 0.f ? st.m[w] + log2f(st.l[w]) : kNegInf;
             }
-            if (last_piece(p, c.slot, c.np, lane)) merge_unit<HD>(p, c.b, c.h, c.slot, c.np, lane);
+            if (last_piece(p, c.slot, c.np, lane)) {
+                if (lane == 0) owed[owes] = c;
+                ++owes;
+            }
         }
-        c = piece(c.x + warps);
+    }
+    __syncwarp();
+    for (int i = 0; i < owes; ++i) merge_unit<HD>(p, owed[i].b, owed[i].h, owed[i].slot, owed[i].np, lane);
+    __syncwarp();
+    owes = 0;
     }
     // after a wait that ran out, the copies in flight land first
     if (dead && lane == 0)
-        for (; taken < issued; ++taken) {
-            const uint32_t sg = taken % S;
-            if ((copied >> sg) & 1u) (void)mbar_wait_bounded(full + 8 * sg, (phase >> sg) & 1u, drain_limit(p.wait_ns));
-        }
+        for (int i = 0; i < S; ++i)
+            if ((copied >> i) & 1u) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
 }
 
 // A value per call, never that of an earlier one in this process, nor zero: a
@@ -503,8 +528,8 @@ unsigned long long slide_epoch() {
     return (start + 2 * ctr.fetch_add(1)) | 1ull;
 }
 
-// Blocks per SM of the kernels (their launch bounds; shared memory holds as many).
-constexpr int kSlideBlocks = 3;
+// Blocks per SM of the kernels, at most (their launch bounds; shared memory holds as many).
+constexpr int kSlideBlocks = 4;
 
 mi_status check_sliding(const mi_dims* dims, int32_t window, int32_t sinks) {
     const mi_status st = check_paged_dims(dims);
@@ -520,13 +545,13 @@ size_t slot_floats(const mi_dims& D) { return (size_t)(D.Hq / D.Hkv) * D.head_di
 size_t slide_bytes(const mi_dims& D, int sms) { return (size_t)slide_slots(sms) * (8 + 4 * slot_floats(D)); }
 
 template <int HD, int VAR>
-cudaError_t launch_slide(int grid, cudaStream_t st, const CUtensorMap& tk, const CUtensorMap& tv, const SlideParams& p) {
+cudaError_t launch_slide(int sms, cudaStream_t st, const CUtensorMap& tk, const CUtensorMap& tv, const SlideParams& p) {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    static_assert(SlideShape<HD, VAR>::kBlocksPerSm == kSlideBlocks, "grid");
+    static_assert(SlideShape<HD, VAR>::kBlocksPerSm <= kSlideBlocks, "the workspace holds every warp's pieces");
     constexpr int smem = SlideShape<HD, VAR>::kSmem;
     if (!raise_smem(reinterpret_cast<const void*>(slide_kernel<HD, VAR>), smem, done, mu)) return cudaErrorInvalidValue;
-    return launch_pdl(slide_kernel<HD, VAR>, grid, kSlideWarps * 32, smem, st, tk, tv, p);
+    return launch_pdl(slide_kernel<HD, VAR>, SlideShape<HD, VAR>::kBlocksPerSm * sms, kSlideWarps * 32, smem, st, tk, tv, p);
 }
 
 mi_status attention_sliding(const mi_dims* dims, const void* q, const void* k_cache, const void* v_cache,
@@ -560,7 +585,7 @@ mi_status attention_sliding(const mi_dims* dims, const void* q, const void* k_ca
     p.most = slide_slots(sms);
     p.words = static_cast<unsigned long long*>(workspace);
     p.part = reinterpret_cast<float*>(p.words + p.most);
-    p.epoch = slide_epoch();
+    p.tag = slide_epoch() << 16;
     p.k_scale = var == kVarFp8 ? k_scale : nullptr;
     p.v_scale = var == kVarFp8 ? v_scale : nullptr;
     p.k_amax = var == kVarInt8 ? k_scale : nullptr;
@@ -576,19 +601,18 @@ mi_status attention_sliding(const mi_dims* dims, const void* q, const void* k_ca
     p.sinks = sinks;
     p.slot_floats = (int)slot_floats(D);
     p.sl2 = scale * 1.4426950408889634f;
-    // 6.8 TB/s; a warp's block takes about 0.75 us
-    p.flow = (float)(2 * kBlock * HD * elem_bytes(var)) / 6.8e12f / 0.75e-6f;
+    // 6.8 TB/s; a warp's block takes about 0.75 us (bf16) or 1.1 (one-byte codes, converted)
+    p.flow = (float)(2 * kBlock * HD * elem_bytes(var)) / 6.8e12f / (var == kVarMma ? 0.75e-6f : 1.1e-6f);
     p.wait_ns = test_wait_limit_ns();
     p.withhold = test_withhold_copy() ? 1 : 0;
-    const int grid = kSlideBlocks * sms;
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (var == kVarMma)
-        e = HD == 64 ? launch_slide<64, kVarMma>(grid, st, tk, tv, p) : launch_slide<128, kVarMma>(grid, st, tk, tv, p);
+        e = HD == 64 ? launch_slide<64, kVarMma>(sms, st, tk, tv, p) : launch_slide<128, kVarMma>(sms, st, tk, tv, p);
     else if (var == kVarFp8)
-        e = HD == 64 ? launch_slide<64, kVarFp8>(grid, st, tk, tv, p) : launch_slide<128, kVarFp8>(grid, st, tk, tv, p);
+        e = HD == 64 ? launch_slide<64, kVarFp8>(sms, st, tk, tv, p) : launch_slide<128, kVarFp8>(sms, st, tk, tv, p);
     else
-        e = HD == 64 ? launch_slide<64, kVarInt8>(grid, st, tk, tv, p) : launch_slide<128, kVarInt8>(grid, st, tk, tv, p);
+        e = HD == 64 ? launch_slide<64, kVarInt8>(sms, st, tk, tv, p) : launch_slide<128, kVarInt8>(sms, st, tk, tv, p);
     return e == cudaSuccess ? MI_OK : MI_ERR_CUDA;
 }
 

@@ -11,8 +11,8 @@
 // (request, head), looks the blocks up, copies them through a ring of its own (TMA,
 // one mbarrier a stage), runs the decode tiles over them and writes the result,
 // with no barrier among warps. A (request, head) of one piece is done then; of the
-// others the warp that stores the last piece adds all of them up by their
-// log-sum-exps.
+// others the warp that counts the last piece adds all of them up by their
+// log-sum-exps. (A second launch for that cost 5 us a call more.)
 #include <atomic>
 #include <chrono>
 #include <cmath>
@@ -29,21 +29,22 @@ namespace {
 
 constexpr int kSlideWarps = 4;
 
-// Warps of an SM hide one another's latency: sixteen where registers and tiles allow.
+// Blocks per SM. (Four for one-byte caches, at 128 registers a thread: 116 us instead
+// of 92 for 128 windows of 4,096 tokens, 4 KV heads, e4m3.)
+constexpr int kSlideBlocks = 3;
+
 template <int HD, int VAR>
 struct SlideShape {
     static constexpr int kTile = Tile<HD, elem_bytes(VAR)>::kBytes;
-    static constexpr int kBlocksPerSm = VAR == kVarMma ? 3 : 4;
-    static constexpr int kRing = kBlocksPerSm == 3 ? 16384 : 12288;  // bytes of a warp's stages, at most
-    static constexpr int kStages = kRing / (2 * kTile) < 4 ? kRing / (2 * kTile) : 4;
+    static constexpr int kStages = 16384 / (2 * kTile) < 4 ? 16384 / (2 * kTile) : 4;
     static constexpr int kSmem = kSlideWarps * kStages * 2 * kTile + 1024;  // slack to align the tiles
 };
 
 // Pieces that have partial results, at most, per warp of the grid.
 constexpr int kSplitPerWarp = 8;
-// A piece's own cost (its queries, its output, finding the next), in blocks; that of
-// a split unit's end, and of each piece that is added up there.
-constexpr float kPieceCost = 2.f, kSplitCost = 3.f, kMergeCost = 0.2f;
+// In a warp's block times: a piece's own cost (its queries, its output), that of a
+// split unit's end, and of a round of loads (four pieces, 512 outputs) there.
+constexpr float kPieceCost = 6.f, kSplitCost = 1.f, kMergeCost = 2.5f;
 
 // Piece i of the np of (request b, head h): blocks in sight j .. j1 - 1; `slot`: the
 // unit's first partial result. b < 0: no more pieces.
@@ -51,7 +52,6 @@ struct SlidePiece {
     int b, h, i, np, slot, j, j1;
 };
 constexpr int kPieceRing = 8;
-constexpr int kOwed = 8;
 
 struct SlideParams {
     const uint16_t* q;             // [B][Hq][HD]
@@ -59,8 +59,8 @@ struct SlideParams {
     const int32_t* context_lens;   // [B]
     uint16_t* out;                 // [B][Hq][HD]
     unsigned long long* words;     // [most]: at a split unit's first piece: tag | pieces done
-    float* part;                   // [most][slot_floats] normalised output [G][HD], log2-sum-exps [G]
     unsigned long long tag;        // of the call, in the high 48 bits; never zero
+    float* part;                   // [most][slot_floats] normalised output [G][HD], log2-sum-exps [G]
     const float* k_scale;          // [Hkv] e4m3 caches
     const float* v_scale;
     const float* k_amax;           // [num_blocks][Hkv] INT8 caches
@@ -80,9 +80,9 @@ __device__ __forceinline__ Sight sight_of(const SlideParams& p, int b) {
 
 // The blocks of a piece, chosen by every block of the launch alike: a lane tries 1
 // to 16 pieces for the largest unit, or 16 to 448 in steps of a quarter. Warps take
-// whole pieces in turn: full rounds run at the memory's rate, in the last one a
-// warp's own time may show, and so may the end of the unit with the most pieces.
-__device__ int piece_blocks(const SlideParams& p, float warps, float blocks, float units, int largest, int lane) {
+// whole pieces in turn; the time is that of the rounds, or of all bytes at the memory's rate, and the
+// end of the unit with the most pieces.
+__device__ int piece_blocks(const SlideParams& p, float warps, float blocks, float units, int largest, int hd, int lane) {
     const float all = blocks * p.flow;  // time of all blocks at the memory's rate, in a warp's block times
     const float np = lane < 16 ? (float)(lane + 1) : (float)((16 + 4 * (lane & 3)) << ((lane - 16) >> 2));
     const float big = (float)largest;
@@ -92,9 +92,8 @@ __device__ int piece_blocks(const SlideParams& p, float warps, float blocks, flo
     // the largest units have `most` pieces, the others half a piece more than their share
     const float fill = __fdividef(blocks, units * big);
     const float rounds = __fdividef(fmaxf(units * (most * fill + 0.5f * (1.f - fill)), units), warps);
-    const float part = __fdividef(rounds - floorf(rounds), rounds);
-    float cost = (1.f - part) * all + fmaxf(step + kPieceCost, part * all) + 0.1f * rounds +
-                 (most > 1.f ? kSplitCost + kMergeCost * most : 0.f);
+    float cost = fmaxf(all, ceilf(rounds) * (step + kPieceCost)) + 0.01f * most +
+                 (most > 1.f ? kSplitCost + kMergeCost * ceilf(0.25f * most) * (float)((p.G * hd + 511) / 512) : 0.f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float c = __shfl_xor_sync(0xffffffffu, cost, o), t = __shfl_xor_sync(0xffffffffu, step, o);
@@ -109,7 +108,7 @@ __device__ int piece_blocks(const SlideParams& p, float warps, float blocks, flo
 // A split unit counts its finished pieces in a word: the call's tag in the high 48
 // bits, the pieces in the low 16. A word with another tag (of an earlier call, or
 // whatever the workspace held) counts as zero: the first piece sets it up at its
-// start, so that at their ends an addition is enough. (Counting by compare-and-swap
+// start, so that at the ends an addition is enough. (Counting by compare-and-swap
 // alone lets one piece on per trip to L2: 54 us for a request in 22 pieces a head.)
 // The last piece zeroes the word: a captured call keeps its tag.
 constexpr unsigned long long kCount = 0xFFFFull;
@@ -119,74 +118,66 @@ __device__ __forceinline__ void open_count(unsigned long long* word, unsigned lo
     if ((old & ~kCount) != tag) atomicCAS(word, old, tag);
 }
 
-// Whether the piece whose result lane 0's warp has just written is the unit's last.
-__device__ __forceinline__ bool last_piece(const SlideParams& p, int slot, int np, int lane) {
+// Counts a piece whose result has been written (a lane's call, the warp's results
+// before a __syncwarp); whether it was the unit's last.
+__device__ __forceinline__ bool last_piece(const SlideParams& p, int slot, int np) {
     unsigned long long* word = p.words + slot;
-    int last = 0;
-    __syncwarp();
-    if (lane == 0) {
-        // this warp's result before the count, the others' after it
-        unsigned long long old;
-        asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
-        while ((old & ~kCount) != p.tag) {
-            unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word), got;
-            if ((seen & ~kCount) == p.tag) {
-                asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
-            } else {
-                asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
-                             : "=l"(got) : "l"(word), "l"(seen), "l"(p.tag | 1ull) : "memory");
-                if (got == seen) old = p.tag;
-            }
+    // this warp's result before the count, the others' after it
+    unsigned long long old;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+    while ((old & ~kCount) != p.tag) {
+        unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word), got;
+        if ((seen & ~kCount) == p.tag) {
+            asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+        } else {
+            asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                         : "=l"(got) : "l"(word), "l"(seen), "l"(p.tag | 1ull) : "memory");
+            if (got == seen) old = p.tag;
         }
-        last = (int)(old & kCount) + 1 == np;
-        if (last) *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
     }
-    last = __shfl_sync(0xffffffffu, last, 0);
-    return last != 0;
+    const bool last = (int)(old & kCount) + 1 == np;
+    if (last) *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
+    return last;
 }
 
 // The unit's output from its np pieces, in order: out = sum 2^(lse - M) o over the
-// weights' sum, with a running maximum. A lane has four outputs of each of two
-// groups of 128; four pieces' loads are in flight. (Short code: it runs once or
-// twice in a launch, and instructions come from as far as the data. With the
-// maxima found first, over the lanes, eight heads unrolled, it took 6 us for three
-// pieces and 15 for 22.)
+// weights' sum, with a running maximum. A lane has four outputs of each of four
+// groups of 128; four pieces' loads are in flight.
 template <int HD>
 __device__ void merge_unit(const SlideParams& p, int b, int h, int slot, int np, int lane) {
     const float* part = p.part + (long long)slot * p.slot_floats;
     const int outs = p.G * HD;
     uint16_t* out = p.out + ((long long)b * p.Hq + (long long)h * p.G) * HD;
 #pragma unroll 1
-    for (int x0 = 4 * lane; x0 - 4 * lane < outs; x0 += 256) {
-        float top[2], den[2];
-        float4 acc[2];
+    for (int x0 = 4 * lane; x0 - 4 * lane < outs; x0 += 512) {
+        float top[4], den[4];
+        float4 acc[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
             top[k] = kNegInf;
             den[k] = 0.f;
             acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll 1
-        for (int i0 = 0; i0 < np; i0 += 2) {
-            float lse[2][2];
-            float4 v[2][2];
+        for (int i0 = 0; i0 < np; i0 += 4) {
+            float lse[4][4];
+            float4 v[4][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i) {
+                // (past the last piece or output: the last one again, with no weight)
+                const float* at = part + (long long)min(i0 + i, np - 1) * p.slot_floats;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int x = x0 + 128 * k;
-                    lse[i][k] = kNegInf;
-                    if (i0 + i < np && x < outs) {
-                        const float* at = part + (long long)(i0 + i) * p.slot_floats;
-                        lse[i][k] = __ldcg(at + outs + x / HD);
-                        v[i][k] = __ldcg(reinterpret_cast<const float4*>(at + x));
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int x = min(x0 + 128 * k, outs - 4);
+                    lse[i][k] = __ldcg(at + outs + x / HD);
+                    v[i][k] = __ldcg(reinterpret_cast<const float4*>(at + x));
                 }
+            }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (lse[i][k] == kNegInf) continue;  // no piece, or nothing of it in sight
+                for (int k = 0; k < 4; ++k) {
+                    if (i0 + i >= np || lse[i][k] == kNegInf) continue;  // (-inf: nothing of it in sight)
                     const float t = fmaxf(top[k], lse[i][k]);
                     const float f = ex2(top[k] - t), w = ex2(lse[i][k] - t);
                     top[k] = t;
@@ -198,7 +189,7 @@ __device__ void merge_unit(const SlideParams& p, int b, int h, int slot, int np,
                 }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
             const int x = x0 + 128 * k;
             const float r = den[k] > 0.f ? 1.f / den[k] : 0.f;
             if (x < outs)
@@ -218,7 +209,7 @@ template <int HD>
 struct TileOf<HD, kVarInt8> { using T = Int8State<HD>; };
 
 template <int HD, int VAR>
-__global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocksPerSm)
+__global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     slide_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const SlideParams p) {
     using Shape = SlideShape<HD, VAR>;
     constexpr int S = Shape::kStages, kTile = Shape::kTile, kThreads = kSlideWarps * 32;
@@ -285,7 +276,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
     }
     if (largest == 0) return;
     const int warps = gridDim.x * kSlideWarps;
-    const int step = piece_blocks(p, (float)warps, (float)blocks, (float)units, largest, lane);
+    const int step = piece_blocks(p, (float)warps, (float)blocks, (float)units, largest, HD, lane);
     auto pieces_of = [&](int nb) { return (nb + step - 1) / step; };
     auto pieces = [&](int b) { return (long long)p.Hkv * pieces_of(sight_of(p, b).blocks); };
     auto splits = [&](int b) {
@@ -329,23 +320,24 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
         (void)flat_scan(p.B, splits, plan.split_sums);
     }
     // ---------------------------------------------------------- the pieces --
-    // The issuing side runs up to S blocks ahead, across pieces; it leaves what the
-    // computing side needs of a piece in a ring (S + 2 pieces at most: the one
-    // computed, one for each block ahead, and the next). Table entries come 32 at a time.
+    // The issuing side runs up to S blocks ahead, across pieces, and looks one piece
+    // further: its place and first table entries (32 at a time) are there when the
+    // copies reach it. The computing side finds the pieces in a ring (S + 3 at most:
+    // the one computed, one for each block ahead, the one copied next, the one after).
     __shared__ SlidePiece ring_of[kSlideWarps][kPieceRing];
-    static_assert(S + 2 <= kPieceRing, "pieces in flight");
+    static_assert(S + 3 <= kPieceRing, "pieces in flight");
     SlidePiece* pieces_ahead = ring_of[warp];
-    int x = (int)blockIdx.x * kSlideWarps + warp;  // the issuing side's piece, or past the last
-    int in_b = 0, in_h = 0, in_j = 0, in_j1 = 0, entry = -1, ahead = 0, found = 0;
-    auto fetch = [&]() {
-        ahead = 0;
-        const int j = in_j + lane;
-        entry = j < in_j1 ? __ldg(p.block_tables + (long long)in_b * p.mbps + sight_of(p, in_b).column(j)) : -1;
+    // (neighbouring pieces on different SMs: one-byte tiles keep an SM's warps busy,
+    // so all SMs get the same number of them)
+    int x = warp * (int)gridDim.x + (int)blockIdx.x;  // the piece to be found next
+    int found = 0, next_entry = -1;
+    auto entries = [&](int b, int j, int j1) {
+        return j + lane < j1 ? __ldg(p.block_tables + (long long)b * p.mbps + sight_of(p, b).column(j + lane)) : -1;
     };
-    auto find = [&]() {
+    auto locate = [&](int x) {
         SlidePiece c;
         c.b = -1;
-        in_j = in_j1 = 0;
+        c.np = c.j = c.j1 = 0;
         if (x < total) {
             int o, nb;
             if (small) {
@@ -370,23 +362,39 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
             c.h = o / c.np;
             c.i = o - c.h * c.np;
             c.slot += c.h * c.np;
-            // equal shares of the unit's blocks
-            c.j = in_j = (int)((long long)nb * c.i / c.np);
-            c.j1 = in_j1 = (int)((long long)nb * (c.i + 1) / c.np);
-            in_b = c.b;
-            in_h = c.h;
+            // shares of the unit's blocks that differ by one at most
+            const int share = nb / c.np, rest = nb - share * c.np;
+            c.j = c.i * share + min(c.i, rest);
+            c.j1 = c.j + share + (c.i < rest ? 1 : 0);
         }
+        return c;
+    };
+    auto find = [&]() {
+        const SlidePiece c = locate(x);
+        if (x < total) x += warps;
         if (lane == 0) pieces_ahead[found & (kPieceRing - 1)] = c;
         ++found;
+        next_entry = entries(max(c.b, 0), c.j, c.j1);
+    };
+    int in_b = -1, in_h = 0, in_j = 0, in_j1 = 0, entry = -1, ahead = 0;  // the piece that is copied; b < 0: none
+    auto advance = [&]() {
         __syncwarp();
-        fetch();
+        const SlidePiece& c = pieces_ahead[(found - 1) & (kPieceRing - 1)];
+        in_b = c.b;
+        in_h = c.h;
+        in_j = c.j;
+        in_j1 = c.j1;
+        entry = next_entry;
+        ahead = 0;
+        if (in_b >= 0) find();
     };
     const uint64_t policy = l2_policy_evict_first();
     find();
+    advance();
     uint32_t copied = 0, phase = 0;  // bit i: stage i holds a block, or will; its parity
     bool withhold = p.withhold != 0;
     auto issue = [&](uint32_t st) {
-        if (x >= total) return;
+        if (in_b < 0) return;
         const int blk = __shfl_sync(0xffffffffu, entry, ahead);
         const bool ok = blk >= 0 && blk < p.num_blocks;
         if (lane == 0) {
@@ -412,26 +420,20 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
         if (ok) copied |= 1u << st;
         ++ahead;
         if (++in_j == in_j1) {
-            x += warps;
-            find();
+            advance();
         } else if (ahead == 32) {
-            fetch();
+            ahead = 0;
+            entry = entries(in_b, in_j, in_j1);
         }
     };
     for (int i = 0; i < S; ++i) issue((uint32_t)i);
     uint32_t sg = 0;  // the stage whose block comes next
     bool dead = false;
     typename TileOf<HD, VAR>::T st;
-    // units whose last piece was this warp's are added up behind its pieces (or when
-    // kOwed of them wait): among the tiles' registers the sums would have spilled
-    __shared__ SlidePiece owed_by[kSlideWarps][kOwed];
-    SlidePiece* owed = owed_by[warp];
-    int done = 0, owes = 0;
-    for (bool more = true; more;) {
-    for (;; ++done) {
+    for (int done = 0;; ++done) {
+        __syncwarp();
         const SlidePiece& c = pieces_ahead[done & (kPieceRing - 1)];
-        more = !dead && c.b >= 0;
-        if (!more || owes == kOwed) break;
+        if (dead || c.b < 0) break;
         const Sight sight = sight_of(p, c.b);
         st.begin_unit(p, c.b, c.h, lane);
         if (c.np > 1 && c.i == 0 && lane == 0) open_count(p.words + c.slot, p.tag);
@@ -499,21 +501,34 @@ __global__ void __launch_bounds__(kSlideWarps * 32, SlideShape<HD, VAR>::kBlocks
                 const int g = 2 * (lane & 3) + w;
                 if (lane < 4 && g < p.G) part[p.G * HD + g] = st.l[w] > 0.f ? st.m[w] + log2f(st.l[w]) : kNegInf;
             }
-            if (last_piece(p, c.slot, c.np, lane)) {
-                if (lane == 0) owed[owes] = c;
-                ++owes;
-            }
         }
     }
-    __syncwarp();
-    for (int i = 0; i < owes; ++i) merge_unit<HD>(p, owed[i].b, owed[i].h, owed[i].slot, owed[i].np, lane);
-    __syncwarp();
-    owes = 0;
+    if (dead) {
+        // the copies in flight land first
+        if (lane == 0)
+            for (int i = 0; i < S; ++i)
+                if ((copied >> i) & 1u) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
+        return;
     }
-    // after a wait that ran out, the copies in flight land first
-    if (dead && lane == 0)
-        for (int i = 0; i < S; ++i)
-            if ((copied >> i) & 1u) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
+    // The warp's pieces of split units are counted, a lane each, and units whose last
+    // one was among them added up. (Behind all of its pieces: a count is a trip to L2
+    // and back, and among the tiles' registers the sums spilled, which cost the
+    // e4m3 tiles a third of their rate.)
+    __syncwarp();
+#pragma unroll 1
+    for (int x0 = warp * (int)gridDim.x + (int)blockIdx.x; x0 < total; x0 += 32 * warps) {
+        const bool there = lane < (total - x0 + warps - 1) / warps;
+        const SlidePiece c = locate(there ? x0 + lane * warps : total);
+        uint32_t last = __ballot_sync(0xffffffffu, c.np > 1 && last_piece(p, c.slot, c.np));
+        __syncwarp();
+#pragma unroll 1
+        for (; last; last &= last - 1) {
+            const int i = __ffs(last) - 1;
+            merge_unit<HD>(p, __shfl_sync(0xffffffffu, c.b, i), __shfl_sync(0xffffffffu, c.h, i),
+                           __shfl_sync(0xffffffffu, c.slot, i), __shfl_sync(0xffffffffu, c.np, i), lane);
+        }
+        if (total - x0 <= 32 * warps) break;
+    }
 }
 
 // A value per call, never that of an earlier one in this process, nor zero: a
@@ -527,9 +542,6 @@ unsigned long long slide_epoch() {
     }();
     return (start + 2 * ctr.fetch_add(1)) | 1ull;
 }
-
-// Blocks per SM of the kernels, at most (their launch bounds; shared memory holds as many).
-constexpr int kSlideBlocks = 4;
 
 mi_status check_sliding(const mi_dims* dims, int32_t window, int32_t sinks) {
     const mi_status st = check_paged_dims(dims);
@@ -548,10 +560,9 @@ template <int HD, int VAR>
 cudaError_t launch_slide(int sms, cudaStream_t st, const CUtensorMap& tk, const CUtensorMap& tv, const SlideParams& p) {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    static_assert(SlideShape<HD, VAR>::kBlocksPerSm <= kSlideBlocks, "the workspace holds every warp's pieces");
     constexpr int smem = SlideShape<HD, VAR>::kSmem;
     if (!raise_smem(reinterpret_cast<const void*>(slide_kernel<HD, VAR>), smem, done, mu)) return cudaErrorInvalidValue;
-    return launch_pdl(slide_kernel<HD, VAR>, SlideShape<HD, VAR>::kBlocksPerSm * sms, kSlideWarps * 32, smem, st, tk, tv, p);
+    return launch_pdl(slide_kernel<HD, VAR>, kSlideBlocks * sms, kSlideWarps * 32, smem, st, tk, tv, p);
 }
 
 mi_status attention_sliding(const mi_dims* dims, const void* q, const void* k_cache, const void* v_cache,
@@ -601,8 +612,8 @@ mi_status attention_sliding(const mi_dims* dims, const void* q, const void* k_ca
     p.sinks = sinks;
     p.slot_floats = (int)slot_floats(D);
     p.sl2 = scale * 1.4426950408889634f;
-    // 6.8 TB/s; a warp's block takes about 0.75 us (bf16) or 1.1 (one-byte codes, converted)
-    p.flow = (float)(2 * kBlock * HD * elem_bytes(var)) / 6.8e12f / (var == kVarMma ? 0.75e-6f : 1.1e-6f);
+    // 6.8 TB/s; a warp's block takes about 0.75 us (bf16) or 1 (one-byte codes, converted)
+    p.flow = (float)(2 * kBlock * HD * elem_bytes(var)) / 6.8e12f / (var == kVarMma ? 0.75e-6f : 1e-6f);
     p.wait_ns = test_wait_limit_ns();
     p.withhold = test_withhold_copy() ? 1 : 0;
     const cudaStream_t st = (cudaStream_t)stream;

@@ -641,6 +641,18 @@ mi_status mi_paged_prefill_attention(const mi_dims* dims, int32_t total_q, int32
                                      const int32_t* query_start, float scale, void* out,
                                      int32_t* dev_err, mi_stream_t stream);
 
+/* mi_paged_prefill_attention within a sliding window with sinks (above): new token i
+ * of request r, at position p = n_r - m_r + i, attends to t <= p with t > p - window
+ * or t < sinks. One new token gives mi_paged_decode_attention_sliding. Table entries
+ * of blocks that none of the request's new tokens sees are not read (they may be
+ * -1); tokens that none of them sees may hold any bits. Other arguments, errors and
+ * guarantees as mi_paged_prefill_attention (tables of at most 2^27 - 128 blocks). */
+mi_status mi_paged_prefill_attention_sliding(const mi_dims* dims, int32_t total_q, int32_t max_query_len,
+                                             const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens,
+                                             const int32_t* query_start, int32_t window, int32_t sinks, float scale,
+                                             void* out, int32_t* dev_err, mi_stream_t stream);
+
 /* Kernel of mi_paged_prefill_attention_variant:
  *   MI_PREFILL_MMA      warp-level mma.sync tiles (64 rows per CTA; any G),
  *   MI_PREFILL_TCGEN05  fifth-generation tensor cores (tcgen05.mma with

@@ -49,7 +49,7 @@ EXPORTS = (
     "mi_paged_kv_evict", "mi_paged_kv_evict_fp8", "mi_paged_kv_evict_workspace_bytes",
     "mi_paged_kv_append_norm", "mi_paged_kv_append_norm_fp8",
     "mi_paged_decode_attention_sliding", "mi_paged_decode_attention_sliding_fp8",
-    "mi_paged_decode_attention_sliding_int8", "mi_paged_sliding_workspace_bytes",
+    "mi_paged_decode_attention_sliding_int8", "mi_paged_sliding_workspace_bytes", "mi_paged_prefill_attention_sliding",
     "mi_kv_pool_fork", "mi_kv_pool_slide", "mi_kv_pool_compact", "mi_kv_pool_block_refs", "mi_kv_copy_planes",
     "mi_paged_decode_step", "mi_paged_decode_step_fp8", "mi_test_set_wait_limit", "mi_test_withhold_copy",
 )
@@ -144,6 +144,8 @@ def load():
                 [dims_p, P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32, P, P, P, P, P], i32),
             "mi_paged_kv_append_norm_fp8": (
                 [dims_p, P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32, P, P, P, P, P, P, P], i32),
+            "mi_paged_prefill_attention_sliding": (
+                [dims_p, i32, i32, P, P, P, P, P, P, i32, i32, f32, P, P, P], i32),
             "mi_paged_sliding_workspace_bytes": ([dims_p, i32, i32], ctypes.c_size_t),
             "mi_paged_decode_attention_sliding": (
                 [dims_p, P, P, P, P, P, i32, i32, f32, P, P, ctypes.c_size_t, P, P], i32),
@@ -734,6 +736,15 @@ def mi_paged_decode_attention_sliding_int8(d: MiDims, q, k_cache, v_cache, k_ama
         ctypes.byref(d), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_amax), _ptr(v_amax), _ptr(block_tables),
         _ptr(context_lens), int(window), int(sinks), float(scale), _ptr(out), _ptr(workspace),
         _nbytes(workspace, workspace_bytes), _ptr(dev_err), _stream(stream))
+
+
+def mi_paged_prefill_attention_sliding(d: MiDims, total_q, max_query_len, q, k_cache, v_cache, block_tables,
+                                       context_lens, query_start, window, sinks, scale, out, dev_err=None, stream=None):
+    """Causal attention of new tokens over each one's `window` newest and the sequence's first `sinks` tokens."""
+    return load().mi_paged_prefill_attention_sliding(
+        ctypes.byref(d), int(total_q), int(max_query_len), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        _ptr(context_lens), _ptr(query_start), int(window), int(sinks), float(scale), _ptr(out), _ptr(dev_err),
+        _stream(stream))
 
 
 def kv_planes(tensors):

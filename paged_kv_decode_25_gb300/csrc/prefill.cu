@@ -36,9 +36,11 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "prefix.cuh"
+#include "sliding.cuh"
 #include "tc.cuh"
 #include "tma.cuh"
 
@@ -64,6 +66,12 @@ struct PrefillParams {
     float sl2;                     // scale * log2(e)
     long long wait_ns;             // bound on every mbarrier wait of the launch
     int withhold;                  // failure-detection test: each producer withholds its first K copy
+};
+
+// mi_paged_prefill_attention_sliding. (Apart, so that the causal kernel's launches
+// carry no more arguments: two more cost it 0.7 %.)
+struct SlidingParams : PrefillParams {
+    int window, sinks;
 };
 
 // The work item of a CTA: row tile k (counted from the request's end) of
@@ -920,10 +928,14 @@ struct Tc2Smem {
     static constexpr int kTotal = kTmem + 16 + 1024;  // slack to align the base to 1024 B
 };
 
-template <int HD>
+// With SLIDE a row at position p sees keys t <= p with t > p - window or t < sinks.
+// The stages then hold the blocks in sight of any of the CTA's rows, end to end:
+// those of the sinks, then those from the first row's window to the last row. All
+// but the first and the last of them need no mask where the window is long.
+template <int HD, bool SLIDE = false>
 __global__ void __launch_bounds__(kT2Threads, 1)
     prefill_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, PrefillParams p) {
+                       const __grid_constant__ CUtensorMap tmv, std::conditional_t<SLIDE, SlidingParams, PrefillParams> p) {
     using SM = Tc2Smem<HD>;
     constexpr int kH = SM::kH;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -938,7 +950,18 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     const int tr = (kTcRows / p.G) * p.G;
     Item it;
     if (!work_item(p, 2 * tr, it)) return;
-    const int nst = (it.nblk + kT2Blocks - 1) / kT2Blocks;
+    // blocks 0 .. head - 1 and head + gap .. it.nblk - 1 of the table are in sight
+    int head = 0, gap = 0, lo = 0, sinks = 0;
+    if constexpr (SLIDE) {
+        const int p_lo = max(0, it.first + it.rho0 / p.G);  // the first row's position
+        lo = p_lo >= p.window ? p_lo - p.window + 1 : 0;
+        sinks = min(p.sinks, lo);
+        head = (sinks + kBlock - 1) / kBlock;
+        gap = max(0, min(lo / kBlock, it.nblk) - head);
+    }
+    const int nblk = it.nblk - gap;  // the item's blocks
+    auto column = [&](int x) { return SLIDE && x >= head ? x + gap : x; };
+    const int nst = (nblk + kT2Blocks - 1) / kT2Blocks;
     const uint32_t bar = sbase + SM::kBar;
     const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
     const uint32_t v_empty0 = v_full0 + 16, s_full0 = v_empty0 + 16, p_full0 = s_full0 + 16;
@@ -1001,7 +1024,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         // the slot, so their load latency is hidden
         auto table_entry = [&](int jj) -> int {
             const int x = jj * kT2Blocks + lane;
-            return (lane < kT2Blocks && x < it.nblk) ? __ldg(p.block_tables + (long long)it.r * p.mbps + x) : -1;
+            return (lane < kT2Blocks && x < nblk) ? __ldg(p.block_tables + (long long)it.r * p.mbps + column(x)) : -1;
         };
         int nblk_next = table_entry(0);
         for (int j = 0; j < nst; ++j) {
@@ -1014,7 +1037,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 break;
             }
             bool ok = false;
-            if (lane < kT2Blocks && x < it.nblk) {
+            if (lane < kT2Blocks && x < nblk) {
                 ok = blk >= 0 && blk < p.num_blocks;
                 if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
             }
@@ -1142,9 +1165,11 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
             tc::wait_ld();
             const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
-            const int kbase = j * kT2Keys;
-            const bool nomask = __all_sync(0xffffffffu, present == (1u << kT2Blocks) - 1u &&
-                                                            kbase + kT2Keys - 1 <= min(mposa, mposb));
+            // the stage's first key (with SLIDE: if no sinks are in it)
+            const int kbase = SLIDE ? column(j * kT2Blocks) * kBlock : j * kT2Keys;
+            bool plain = present == (1u << kT2Blocks) - 1u && kbase + kT2Keys - 1 <= min(mposa, mposb);
+            if constexpr (SLIDE) plain = plain && j * kT2Blocks >= head && kbase > max(mposa, mposb) - p.window;
+            const bool nomask = __all_sync(0xffffffffu, plain);
             float alpha_a = 1.f, alpha_b = 1.f, psa, psb;
             bool need = false;
             float ma[4], mb[4];
@@ -1162,8 +1187,14 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     const bool blk = (present >> (k >> 1)) & 1u;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int key = kbase + 8 * k + 2 * c4 + (e & 1);
-                        const bool keep = blk && key <= (e < 2 ? mposa : mposb);
+                        int key = kbase + 8 * k + 2 * c4 + (e & 1);
+                        const int pos = e < 2 ? mposa : mposb;
+                        bool keep = blk;
+                        if constexpr (SLIDE) {
+                            key = column(j * kT2Blocks + (k >> 1)) * kBlock + 8 * (k & 1) + 2 * c4 + (e & 1);
+                            keep = keep && (key > pos - p.window || key < p.sinks);
+                        }
+                        keep = keep && key <= pos;
                         const float v = keep ? (fold ? __uint_as_float(x[4 * k + e])
                                                      : __uint_as_float(x[4 * k + e]) * p.sl2)
                                              : -INFINITY;
@@ -1268,16 +1299,33 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 // stage's V copies have landed, before tile 0's P . V (tile
                 // 1's is issued after it). A warp of tile 0 off the MMA
                 // warp's scheduler does it.
-                const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
-                const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
+                // (With SLIDE also those that no row of the CTA sees.)
+                const int last = nb_ctx - 1 - gap - j * kT2Blocks;  // the context's last block, stage-local
+                bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
+                uint32_t seen = 0xFFFFu;  // lane l: the rows of block l in sight
+                if constexpr (SLIDE) {
+                    const int t0 = column(j * kT2Blocks + lane) * kBlock;
+                    seen = Sight::first_bits(sinks - t0) | (0xFFFFu & ~Sight::first_bits(lo - t0));
+                    any = any || __any_sync(0xffffffffu, lane < kT2Blocks && seen != 0xFFFFu);
+                }
                 if (any) {
                     if (!(ok = wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns))) break;
                     const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
                     for (int l = 0; l < kT2Blocks; ++l) {
                         const int from = !((present >> l) & 1u) ? 0 : (l == last && tail < kBlock ? tail : kBlock);
-                        for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
-                            const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
-                            st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
+                        if constexpr (SLIDE) {
+                            const uint32_t in = __shfl_sync(0xffffffffu, seen, l) & Sight::first_bits(from);
+                            if (in == 0xFFFFu) continue;
+                            for (int i = lane; i < kBlock * kH * 8; i += 32) {
+                                const int r = i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
+                                if (!((in >> r) & 1u))
+                                    st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
+                            }
+                        } else {
+                            for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
+                                const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
+                                st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
+                            }
                         }
                     }
                     fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
@@ -1824,11 +1872,11 @@ bool prepare_tc() {
     return raise_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<HD>), TcSmem<HD>::kTotal, done, mu);
 }
 
-template <int HD>
+template <int HD, bool SLIDE = false>
 bool prepare_tc2() {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD>), Tc2Smem<HD>::kTotal, done, mu);
+    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD, SLIDE>), Tc2Smem<HD>::kTotal, done, mu);
 }
 
 template <int HD>
@@ -1855,8 +1903,10 @@ namespace {
 mi_status prefill(const mi_dims* dims, int32_t total_q, int32_t max_query_len, const void* q, const void* k_cache,
                   const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
                   const int32_t* query_start, float scale, void* out, int32_t* dev_err, mi_stream_t stream,
-                  int32_t variant) {
+                  int32_t variant, const SlidingParams* sliding = nullptr) {
     if (!dims) return MI_ERR_INVALID_ARG;
+    if (sliding && (sliding->window < 1 || sliding->sinks < 0 || dims->max_blocks_per_seq > kLongestTable))
+        return MI_ERR_INVALID_ARG;
     if (variant < MI_PREFILL_DEFAULT || variant > MI_PREFILL_TCGEN05_PAIR) return MI_ERR_INVALID_ARG;
     const mi_dims D = *dims;
     if (D.B < 0 || D.Hq < 1 || D.Hkv < 1 || D.num_blocks < 1 || D.max_blocks_per_seq < 1 || total_q < 0 ||
@@ -1906,7 +1956,20 @@ mi_status prefill(const mi_dims* dims, int32_t total_q, int32_t max_query_len, c
     const long long rows = (long long)D.num_blocks * D.Hkv * kBlock;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    if (use_tc2) {
+    if (sliding) {
+        if (!(HD == 64 ? prepare_tc2<64, true>() : prepare_tc2<128, true>())) return MI_ERR_CUDA;
+        CUtensorMap tq, tk, tv;
+        if (!make_tmap_q_group(&tq, q, total_q, D.Hq, HD, G, tc_rows) ||
+            !make_tmap_kv_halves(&tk, k_cache, rows, HD) || !make_tmap_kv_blocks(&tv, v_cache, rows, HD))
+            return MI_ERR_CUDA;
+        SlidingParams sp;
+        static_cast<PrefillParams&>(sp) = p;
+        sp.window = sliding->window;
+        sp.sinks = sliding->sinks;
+        e = HD == 64 ? launch_pdl(prefill_tc2_kernel<64, true>, (int)grid, kT2Threads, Tc2Smem<64>::kTotal, st, tq, tk, tv, sp)
+                     : launch_pdl(prefill_tc2_kernel<128, true>, (int)grid, kT2Threads, Tc2Smem<128>::kTotal, st, tq, tk,
+                                  tv, sp);
+    } else if (use_tc2) {
         if (!(HD == 64 ? prepare_tc2<64>() : prepare_tc2<128>())) return MI_ERR_CUDA;
         CUtensorMap tq, tk, tv;
         if (!make_tmap_q_group(&tq, q, total_q, D.Hq, HD, G, tc_rows) ||
@@ -1986,4 +2049,16 @@ extern "C" mi_status mi_paged_prefill_attention_variant(const mi_dims* dims, int
                                                         mi_stream_t stream, int32_t variant) {
     return mi::prefill(dims, total_q, max_query_len, q, k_cache, v_cache, block_tables, context_lens, query_start,
                        scale, out, dev_err, stream, variant);
+}
+
+extern "C" mi_status mi_paged_prefill_attention_sliding(const mi_dims* dims, int32_t total_q, int32_t max_query_len,
+                                                        const void* q, const void* k_cache, const void* v_cache,
+                                                        const int32_t* block_tables, const int32_t* context_lens,
+                                                        const int32_t* query_start, int32_t window, int32_t sinks,
+                                                        float scale, void* out, int32_t* dev_err, mi_stream_t stream) {
+    mi::SlidingParams sliding = {};
+    sliding.window = window;
+    sliding.sinks = sinks;
+    return mi::prefill(dims, total_q, max_query_len, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                       scale, out, dev_err, stream, MI_PREFILL_DEFAULT, &sliding);
 }

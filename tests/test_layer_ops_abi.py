@@ -123,3 +123,25 @@ def test_sliding_refusals(mi, kind):
         assert mi.mi_paged_sliding_workspace_bytes(dims(mi, **change), 10, 2) == 0
     assert mi.mi_paged_sliding_workspace_bytes(dims(mi), 0, 2) == 0
     assert mi.mi_paged_sliding_workspace_bytes(dims(mi), 1, -1) == 0
+
+
+def sliding_prefill(mi, d=None, total=4, most=4, q=P, k=2 * P, v=3 * P, tab=4 * P, lens=5 * P, starts=6 * P, window=10,
+                    sinks=2, scale=0.1, out=7 * P):
+    return mi.mi_paged_prefill_attention_sliding(dims(mi) if d is None else d, total, most, q, k, v, tab, lens, starts,
+                                                 window, sinks, scale, out, stream=0)
+
+
+def test_sliding_prefill_refusals(mi):
+    for change, st in BAD_DIMS:
+        if change.get("B", 0) <= 0:  # (any number of requests, and they need not fit 2^30 heads)
+            assert sliding_prefill(mi, d=dims(mi, **change)) == st, change
+    for kw in (dict(window=0), dict(window=-1), dict(sinks=-1), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(total=-1), dict(most=-1), dict(total=1 << 30), dict(most=1 << 30)):
+        assert sliding_prefill(mi, **kw) == BAD, kw
+    for kw in (dict(total=0), dict(most=0), dict(d=dims(mi, B=0))):
+        assert sliding_prefill(mi, **kw) == 0, kw
+    for name in "q k v tab lens starts out".split():
+        assert sliding_prefill(mi, **{name: 0}) == BAD, name
+    for name in "q k v out".split():
+        assert sliding_prefill(mi, **{name: 20 * P + 8}) == BAD, name
+    assert mi.load().mi_paged_prefill_attention_sliding(None, 4, 4, P, P, P, P, P, P, 1, 0, 0.1, P, None, None) == BAD

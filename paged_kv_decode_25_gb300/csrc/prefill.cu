@@ -36,7 +36,6 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
-#include <type_traits>
 
 #include "common.cuh"
 #include "prefix.cuh"
@@ -68,8 +67,7 @@ struct PrefillParams {
     int withhold;                  // failure-detection test: each producer withholds its first K copy
 };
 
-// mi_paged_prefill_attention_sliding. (Apart, so that the causal kernel's launches
-// carry no more arguments: two more cost it 0.7 %.)
+// mi_paged_prefill_attention_sliding
 struct SlidingParams : PrefillParams {
     int window, sinks;
 };
@@ -928,14 +926,10 @@ struct Tc2Smem {
     static constexpr int kTotal = kTmem + 16 + 1024;  // slack to align the base to 1024 B
 };
 
-// With SLIDE a row at position p sees keys t <= p with t > p - window or t < sinks.
-// The stages then hold the blocks in sight of any of the CTA's rows, end to end:
-// those of the sinks, then those from the first row's window to the last row. All
-// but the first and the last of them need no mask where the window is long.
-template <int HD, bool SLIDE = false>
+template <int HD>
 __global__ void __launch_bounds__(kT2Threads, 1)
     prefill_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, std::conditional_t<SLIDE, SlidingParams, PrefillParams> p) {
+                       const __grid_constant__ CUtensorMap tmv, PrefillParams p) {
     using SM = Tc2Smem<HD>;
     constexpr int kH = SM::kH;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -950,18 +944,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     const int tr = (kTcRows / p.G) * p.G;
     Item it;
     if (!work_item(p, 2 * tr, it)) return;
-    // blocks 0 .. head - 1 and head + gap .. it.nblk - 1 of the table are in sight
-    int head = 0, gap = 0, lo = 0, sinks = 0;
-    if constexpr (SLIDE) {
-        const int p_lo = max(0, it.first + it.rho0 / p.G);  // the first row's position
-        lo = p_lo >= p.window ? p_lo - p.window + 1 : 0;
-        sinks = min(p.sinks, lo);
-        head = (sinks + kBlock - 1) / kBlock;
-        gap = max(0, min(lo / kBlock, it.nblk) - head);
-    }
-    const int nblk = it.nblk - gap;  // the item's blocks
-    auto column = [&](int x) { return SLIDE && x >= head ? x + gap : x; };
-    const int nst = (nblk + kT2Blocks - 1) / kT2Blocks;
+    const int nst = (it.nblk + kT2Blocks - 1) / kT2Blocks;
     const uint32_t bar = sbase + SM::kBar;
     const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
     const uint32_t v_empty0 = v_full0 + 16, s_full0 = v_empty0 + 16, p_full0 = s_full0 + 16;
@@ -1024,7 +1007,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         // the slot, so their load latency is hidden
         auto table_entry = [&](int jj) -> int {
             const int x = jj * kT2Blocks + lane;
-            return (lane < kT2Blocks && x < nblk) ? __ldg(p.block_tables + (long long)it.r * p.mbps + column(x)) : -1;
+            return (lane < kT2Blocks && x < it.nblk) ? __ldg(p.block_tables + (long long)it.r * p.mbps + x) : -1;
         };
         int nblk_next = table_entry(0);
         for (int j = 0; j < nst; ++j) {
@@ -1037,7 +1020,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 break;
             }
             bool ok = false;
-            if (lane < kT2Blocks && x < nblk) {
+            if (lane < kT2Blocks && x < it.nblk) {
                 ok = blk >= 0 && blk < p.num_blocks;
                 if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
             }
@@ -1165,11 +1148,9 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
             tc::wait_ld();
             const uint32_t present = lds_u32(mask0 + (j & 3) * 4);
-            // the stage's first key (with SLIDE: if no sinks are in it)
-            const int kbase = SLIDE ? column(j * kT2Blocks) * kBlock : j * kT2Keys;
-            bool plain = present == (1u << kT2Blocks) - 1u && kbase + kT2Keys - 1 <= min(mposa, mposb);
-            if constexpr (SLIDE) plain = plain && j * kT2Blocks >= head && kbase > max(mposa, mposb) - p.window;
-            const bool nomask = __all_sync(0xffffffffu, plain);
+            const int kbase = j * kT2Keys;
+            const bool nomask = __all_sync(0xffffffffu, present == (1u << kT2Blocks) - 1u &&
+                                                            kbase + kT2Keys - 1 <= min(mposa, mposb));
             float alpha_a = 1.f, alpha_b = 1.f, psa, psb;
             bool need = false;
             float ma[4], mb[4];
@@ -1187,14 +1168,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     const bool blk = (present >> (k >> 1)) & 1u;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        int key = kbase + 8 * k + 2 * c4 + (e & 1);
-                        const int pos = e < 2 ? mposa : mposb;
-                        bool keep = blk;
-                        if constexpr (SLIDE) {
-                            key = column(j * kT2Blocks + (k >> 1)) * kBlock + 8 * (k & 1) + 2 * c4 + (e & 1);
-                            keep = keep && (key > pos - p.window || key < p.sinks);
-                        }
-                        keep = keep && key <= pos;
+                        const int key = kbase + 8 * k + 2 * c4 + (e & 1);
+                        const bool keep = blk && key <= (e < 2 ? mposa : mposb);
                         const float v = keep ? (fold ? __uint_as_float(x[4 * k + e])
                                                      : __uint_as_float(x[4 * k + e]) * p.sl2)
                                              : -INFINITY;
@@ -1299,33 +1274,16 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 // stage's V copies have landed, before tile 0's P . V (tile
                 // 1's is issued after it). A warp of tile 0 off the MMA
                 // warp's scheduler does it.
-                // (With SLIDE also those that no row of the CTA sees.)
-                const int last = nb_ctx - 1 - gap - j * kT2Blocks;  // the context's last block, stage-local
-                bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
-                uint32_t seen = 0xFFFFu;  // lane l: the rows of block l in sight
-                if constexpr (SLIDE) {
-                    const int t0 = column(j * kT2Blocks + lane) * kBlock;
-                    seen = Sight::first_bits(sinks - t0) | (0xFFFFu & ~Sight::first_bits(lo - t0));
-                    any = any || __any_sync(0xffffffffu, lane < kT2Blocks && seen != 0xFFFFu);
-                }
+                const int last = nb_ctx - 1 - j * kT2Blocks;  // the context's last block, stage-local
+                const bool any = present != (1u << kT2Blocks) - 1u || (last < kT2Blocks && tail < kBlock);
                 if (any) {
                     if (!(ok = wait_all(v_full0 + (j & 1) * 8, (uint32_t)((j >> 1) & 1), p.wait_ns))) break;
                     const uint32_t vbase = sbase + SM::kRingV + (j & 1) * SM::kKV;
                     for (int l = 0; l < kT2Blocks; ++l) {
                         const int from = !((present >> l) & 1u) ? 0 : (l == last && tail < kBlock ? tail : kBlock);
-                        if constexpr (SLIDE) {
-                            const uint32_t in = __shfl_sync(0xffffffffu, seen, l) & Sight::first_bits(from);
-                            if (in == 0xFFFFu) continue;
-                            for (int i = lane; i < kBlock * kH * 8; i += 32) {
-                                const int r = i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
-                                if (!((in >> r) & 1u))
-                                    st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
-                            }
-                        } else {
-                            for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
-                                const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
-                                st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
-                            }
+                        for (int i = lane; i < (kBlock - from) * kH * 8; i += 32) {
+                            const int r = from + i / (kH * 8), hh = (i / 8) % kH, ch = i % 8;
+                            st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + r * 128 + ch * 16);
                         }
                     }
                     fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
@@ -1850,6 +1808,555 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     }
 }
 
+// ------------------------------------------------- sliding windows, prefill --
+//
+// mi_paged_prefill_attention_sliding on the pipeline of prefill_tc2_kernel. A row at
+// position p sees keys t <= p with t > p - window or t < sinks, so an item (256 rows
+// of a request and KV head) has window / 128 + 2 stages whatever the context: what a
+// block does around its stages (setting up, the first copies, two masked stages, the
+// stores) took 13 of 30 us for windows of 1,024 with a block per item. So
+//   * one block per SM takes items in turn and its barriers run on from item to item:
+//     the next item's K, V and Q are copied, and its first scores computed, while the
+//     rows of the one before are finished;
+//   * an item's stages hold the blocks in sight of any of its rows end to end, those
+//     of the sinks first: sinks cost no stage of their own;
+//   * a stage that every row sees whole takes no mask and no maximum (as in the
+//     shared-prefix kernel); in the others a row's keys are two intervals, tested as
+//     bits of four words;
+//   * rows are stored 16 bytes a lane (as pairs of values the stores took 2.7 us).
+
+template <int HD>
+struct SlideSmem : Tc2Smem<HD> {
+    using Base = Tc2Smem<HD>;
+    // Items described ahead, each of a stage at least: when a stage's copies begin, the
+    // scores three stages before have been computed, and every role is past those
+    // four before.
+    static constexpr int kItems = 8;
+    static constexpr int kBarX = Base::kTmem + 16;  // q_empty, item_full[kItems]
+    static constexpr int kTotal = kBarX + (1 + kItems) * 8 + 1024;
+};
+
+// 256 rows of a request and KV head; r < 0: no more.
+struct SlideItem {
+    int r, h, q0, first, n, nrows, rho0, p_hi;  // as Item
+    int head, gap, lo, sinks, nblk;             // blocks 0 .. head - 1 and head + gap .. head + gap + nblk - head - 1
+};
+
+// A request's tiles of `rows` rows; 0 where it is refused.
+__device__ __forceinline__ int slide_tiles(const PrefillParams& p, int r, int rows) {
+    const int q0 = __ldg(p.query_start + r), q1 = __ldg(p.query_start + r + 1), m = q1 - q0;
+    if (q0 < 0 || q1 > p.T || m < 0 || m > p.max_q) return 0;
+    return (m * p.G + rows - 1) / rows;
+}
+
+__device__ SlideItem slide_item(const SlidingParams& p, const long long* sums, int rows, long long x) {
+    SlideItem it;
+    auto tiles_of = [&](int r) { return (long long)p.Hkv * slide_tiles(p, r, rows); };
+    long long before;
+    it.r = flat_find(p.R, tiles_of, sums, x, before);
+    const int tiles = slide_tiles(p, it.r, rows), o = (int)(x - before);
+    it.h = o / tiles;
+    const int k = o - it.h * tiles;
+    it.q0 = __ldg(p.query_start + it.r);
+    const int m = __ldg(p.query_start + it.r + 1) - it.q0;
+    it.n = min(__ldg(p.context_lens + it.r), p.mbps * kBlock);
+    it.first = it.n - m;
+    it.nrows = m * p.G;
+    it.rho0 = (tiles - 1 - k) * rows;
+    it.p_hi = it.first + (it.rho0 + min(rows, it.nrows - it.rho0) - 1) / p.G;
+    const int p_lo = max(0, it.first + it.rho0 / p.G);  // the first row's position
+    it.lo = p_lo >= p.window ? p_lo - p.window + 1 : 0;
+    it.sinks = min(p.sinks, it.lo);
+    it.head = (it.sinks + kBlock - 1) / kBlock;
+    const int all = it.p_hi >= 0 ? it.p_hi / kBlock + 1 : 0;
+    it.gap = max(0, min(it.lo / kBlock, all) - it.head);
+    it.nblk = all - it.gap;
+    return it;
+}
+
+// The keys of a stage that count for a row, as bits: local keys below `sink` and
+// from `from` to `to` - 1, in blocks that are present.
+struct StageMask {
+    uint32_t w[4];
+    __device__ __forceinline__ static uint32_t below(int k) {  // the first k of 32 bits
+        return k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u);
+    }
+    __device__ __forceinline__ StageMask(int sink, int from, int to, uint32_t present) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t blocks = ((present >> (2 * i)) & 1u ? 0x0000FFFFu : 0u) | ((present >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+            w[i] = (below(sink - 32 * i) | (below(to - 32 * i) & ~below(from - 32 * i))) & blocks;
+        }
+    }
+};
+
+// A stage with a mask, or whose rows have no reference yet or have outgrown it:
+// masks, takes the maximum, moves the reference, O and the sums where it has to and
+// writes P. `a`, `b`: the rows' masks, shifted right by the lane's first key.
+template <int HD>
+__device__ __noinline__ RowSums masked_stage(uint32_t tl, StageMask a, StageMask b, float sl2, RowSums r, uint32_t o_done,
+                                             uint32_t parity, long long wait_ns) {
+    const uint32_t ts = tl + 128u;
+    uint32_t x[2 * kT2Keys / 4];  // x[4k + e]: e = 0, 1 row a; e = 2, 3 row b
+    tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+    tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+    tc::wait_ld();
+    float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kT2Keys / 8; ++k) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t bit = 1u << (8 * (k & 3) + e);
+            const float va = a.w[k >> 2] & bit ? __uint_as_float(x[4 * k + e]) * sl2 : -INFINITY;
+            const float vb = b.w[k >> 2] & bit ? __uint_as_float(x[4 * k + 2 + e]) * sl2 : -INFINITY;
+            x[4 * k + e] = __float_as_uint(va);
+            x[4 * k + 2 + e] = __float_as_uint(vb);
+        }
+        ma = tc::max3(ma, __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+        mb = tc::max3(mb, __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    }
+    // (all four lanes of a row take the same decision)
+    ma = ma + kNear > r.ma ? ma + kAhead : r.ma;
+    mb = mb + kNear > r.mb ? mb + kAhead : r.mb;
+    const bool move_a = ma > r.ma && r.ma != -INFINITY, move_b = mb > r.mb && r.mb != -INFINITY;
+    const float alpha_a = move_a ? ex2(r.ma - ma) : 1.f, alpha_b = move_b ? ex2(r.mb - mb) : 1.f;
+    r.ma = ma;
+    r.mb = mb;
+    r.ok = true;
+    const float una = ma == -INFINITY ? 0.f : ma, unb = mb == -INFINITY ? 0.f : mb;
+    float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kT2Keys / 8; ++k) {
+        const float ea0 = ex2(__uint_as_float(x[4 * k]) - una), ea1 = ex2(__uint_as_float(x[4 * k + 1]) - una);
+        const float eb0 = ex2(__uint_as_float(x[4 * k + 2]) - unb), eb1 = ex2(__uint_as_float(x[4 * k + 3]) - unb);
+        sa[k & 1] += ea0 + ea1;
+        sb[k & 1] += eb0 + eb1;
+        x[2 * k] = pack_bf16x2(ea0, ea1);
+        x[2 * k + 1] = pack_bf16x2(eb0, eb1);
+    }
+    r.la = r.la * alpha_a + (sa[0] + sa[1]);
+    r.lb = r.lb * alpha_b + (sb[0] + sb[1]);
+    tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
+    if (__any_sync(0xffffffffu, move_a || move_b)) {
+        // O may be touched once its previous P . V has finished
+        r.ok = wait_warp(o_done, parity, wait_ns);
+        tc::fence_after();
+#pragma unroll 1
+        for (int ch = 0; r.ok && ch < HD / 32; ++ch) {
+            uint32_t y[16];
+            tc::ld16x256_x4(tl + 32u * ch, y);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * (i & 2 ? alpha_b : alpha_a));
+            tc::st16x256_x4(tl + 32u * ch, y);
+        }
+    }
+    tc::wait_st();
+    return r;
+}
+
+// Word k of lane c of a quad becomes word c of lane k.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int c) {
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (!(i & o)) {
+                const bool up = (c & o) != 0;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i | o], o);
+                (up ? w[i] : w[i | o]) = got;
+            }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kT2Threads, 1)
+    slide_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, const SlidingParams p) {
+    using SM = SlideSmem<HD>;
+    constexpr int kH = SM::kH, kItems = SM::kItems;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ long long sums[flat_words(kT2Threads)];
+    __shared__ SlideItem ring[kItems];
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tr = (kTcRows / p.G) * p.G, rows = 2 * tr;  // rows of a Q tile (whole tokens), of an item
+    // Barriers: as in prefill_tc2_kernel with stages counted over all items (g), and
+    // q_full / q_empty and item_full by items
+    const uint32_t bar = sbase + SM::kBar;
+    const uint32_t q_full = bar, k_full0 = bar + 8, k_empty0 = k_full0 + 32, v_full0 = k_empty0 + 8 * kT2KSlots;
+    const uint32_t v_empty0 = v_full0 + 16, s_full0 = v_empty0 + 16, p_full0 = s_full0 + 16;
+    const uint32_t o_done0 = p_full0 + 16, fin = o_done0 + 16;
+    const uint32_t q_empty = sbase + SM::kBarX, item_full0 = q_empty + 8;
+    const uint32_t mask0 = sbase + SM::kMask;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(k_full0 + i * 8, 1);
+        for (int i = 0; i < kT2KSlots; ++i) mbar_init(k_empty0 + i * 8, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(v_full0 + i * 8, 1);
+            mbar_init(v_empty0 + i * 8, 1);
+            mbar_init(s_full0 + i * 8, 1);
+            mbar_init(p_full0 + i * 8, 8);  // every softmax warp of the tile
+            mbar_init(o_done0 + i * 8, 1);
+        }
+        for (int i = 0; i < kItems; ++i) mbar_init(item_full0 + i * 8, 1);
+        mbar_init(fin, 1);
+        fence_mbar_init();
+    }
+    if (warp == kT2MmaWarp) {
+        tc::alloc(sbase + SM::kTmem, kT2Cols);
+        tc::relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    for (int r = blockIdx.x + gridDim.x * threadIdx.x; r < p.R; r += gridDim.x * kT2Threads) {  // each request once
+        const int q0 = __ldg(p.query_start + r), q1 = __ldg(p.query_start + r + 1), m = q1 - q0;
+        const int n = __ldg(p.context_lens + r);
+        if (q0 < 0 || q1 > p.T || m < 0 || m > p.max_q) {
+            raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
+        } else if (m > 0) {
+            if (n > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
+            if (m > min(n, p.mbps * kBlock)) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
+        }
+    }
+    const long long items =
+        flat_scan(p.R, [&](int r) { return (long long)p.Hkv * slide_tiles(p, r, rows); }, sums);  // (ends with a barrier)
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tbase = lds_u32(sbase + SM::kTmem);
+    bool bad = false;  // a wait ran out
+    auto stages = [](const SlideItem& it) { return (it.nblk + kT2Blocks - 1) / kT2Blocks; };
+
+    if (warp == kT2MmaWarp + 1) {
+        // ------------------------------------------------ producer warp --
+        const uint64_t policy = l2_policy_evict_normal();
+        int g = 0, begun = 0;
+        int pblk = -1, ph = 0;  // the stage before: its V comes behind this stage's K
+        bool pok = false, good = true;
+        auto load_v = [&](int gv) -> bool {
+            const int sl = gv & 1, u = gv >> 1;
+            if (!wait_all(v_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) return false;
+            const uint32_t msk = __ballot_sync(0xffffffffu, pok);
+            const uint32_t fb = v_full0 + sl * 8;
+            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
+            __syncwarp();
+            if (pok) {
+                const uint32_t vd = sbase + SM::kRingV + sl * SM::kKV + lane * kH * kBlock * 128;
+                tma_load_3d(vd, &tmv, fb, 0, (pblk * p.Hkv + ph) * kBlock, 0, policy);
+            }
+            return true;
+        };
+        long long x = blockIdx.x;
+        for (int i = 0; good; x += gridDim.x) {
+            SlideItem it;
+            it.r = -1;
+            if (x < items) it = slide_item(p, sums, rows, x);
+            if (it.r >= 0 && it.nblk == 0) {
+                // every row before position 0: zeros, and nothing for the others to do
+                const int tokens = min(rows, it.nrows - it.rho0) / p.G, words = p.G * HD / 8;
+                for (int k = lane; k < tokens * words; k += 32) {
+                    const long long row = (long long)(it.q0 + it.rho0 / p.G + k / words) * p.Hq + (long long)it.h * p.G;
+                    reinterpret_cast<uint4*>(p.out + row * HD)[k % words] = make_uint4(0, 0, 0, 0);
+                }
+                continue;
+            }
+            if (lane == 0) {
+                ring[i % kItems] = it;
+                mbar_arrive(item_full0 + (i % kItems) * 8);
+            }
+            ++i;
+            if (it.r < 0) break;
+            const int nst = stages(it);
+            // block-table entries are read a stage ahead, before the wait for the slot
+            auto table_entry = [&](int j) -> int {
+                const int y = j * kT2Blocks + lane;
+                return lane < kT2Blocks && y < it.nblk
+                           ? __ldg(p.block_tables + (long long)it.r * p.mbps + (y < it.head ? y : y + it.gap))
+                           : -1;
+            };
+            int blk_next = table_entry(0);
+            for (int j = 0; j < nst; ++j, ++g) {
+                const int sl = g % kT2KSlots, u = g / kT2KSlots, blk = blk_next;
+                if (j + 1 < nst) blk_next = table_entry(j + 1);
+                if (!(good = wait_all(k_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns))) break;
+                bool ok = false;
+                if (lane < kT2Blocks && j * kT2Blocks + lane < it.nblk) {
+                    ok = blk >= 0 && blk < p.num_blocks;
+                    if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+                }
+                const uint32_t msk = __ballot_sync(0xffffffffu, ok);
+                const uint32_t fb = k_full0 + (g & 3) * 8;
+                // failure-detection test: the first K is neither copied nor
+                // announced, so every wait on it runs out
+                const bool held = p.withhold != 0 && g == 0;
+                if (lane == 0 && !held) {
+                    sts32(mask0 + (g & 3) * 4, msk);
+                    mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
+                }
+                __syncwarp();
+                if (ok && !held) {
+                    const uint32_t kd = sbase + SM::kRingK + sl * SM::kKV + lane * kBlock * 128;
+                    const int row0 = (blk * p.Hkv + it.h) * kBlock;
+                    for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kT2Keys * 128, &tmk, fb, 0, hh, row0, policy);
+                }
+                if (g > 0 && !(good = load_v(g - 1))) break;
+                pblk = blk;
+                pok = ok;
+                ph = it.h;
+                if (j == 0) {
+                    // Q, once the item before has no scores to compute any more
+                    if (!(good = wait_all(q_empty, (uint32_t)((begun & 1) ^ 1), p.wait_ns))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full, 2u * kH * (uint32_t)tr * 128u);
+                        for (int t = 0; t < 2; ++t)
+                            for (int hh = 0; hh < kH; ++hh)
+                                tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
+                                            it.q0 + (it.rho0 + t * tr) / p.G, policy);
+                    }
+                    __syncwarp();
+                    ++begun;
+                }
+            }
+        }
+        if (good && g > 0) good = load_v(g - 1);
+        bad = !good;
+    } else if (warp == kT2MmaWarp) {
+        // -------------------------------------------------- MMA issuer --
+        constexpr uint32_t idS = tc::idesc_bf16(kTcRows, kT2Keys, false);
+        constexpr uint32_t idO = tc::idesc_bf16(kTcRows, HD, true);
+        auto issue_s = [&](int t, int g) {
+            const uint32_t kbase = sbase + SM::kRingK + (g % kT2KSlots) * SM::kKV;
+            const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
+                const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
+                const uint64_t bd = tc::sdesc_sw128(kbase + (kk >> 2) * kT2Keys * 128 + off, 16, 1024);
+                tc::mma_ss_elect(tbase + 256u * t + 128u, a, bd, idS, kk > 0);
+            }
+            tc::commit_elect(s_full0 + t * 8);
+        };
+        auto issue_o = [&](int t, int g, bool first) {
+            const uint32_t vbase = sbase + SM::kRingV + (g & 1) * SM::kKV;
+            const uint32_t pcol = tbase + 256u * t + 128u;  // P_t: bf16 pairs over S_t's first 64 columns
+#pragma unroll
+            for (int l = 0; l < kT2Blocks; ++l) {
+                const uint64_t bd = tc::sdesc_sw128(vbase + l * kH * kBlock * 128, kBlock * 128, 1024);
+                tc::mma_ts_elect(tbase + 256u * t, pcol + 8u * l, bd, idO, !first || l > 0);
+            }
+            tc::commit_elect(o_done0 + t * 8);
+        };
+        // the next item's stages, or 0
+        int found = 0;
+        bool ok = true;
+        auto next_item = [&]() -> int {
+            if (!(ok = wait_all(item_full0 + (found % kItems) * 8, (uint32_t)((found / kItems) & 1), p.wait_ns))) return 0;
+            const SlideItem& it = ring[found % kItems];
+            ++found;
+            return it.r < 0 ? 0 : stages(it);
+        };
+        int nst = next_item(), g = 0, begun = 0;
+        // both tiles' scores of an item's first stage
+        auto begin = [&]() -> bool {
+            if (!wait_all(q_full, (uint32_t)(begun & 1), p.wait_ns) ||
+                !wait_all(k_full0 + (g & 3) * 8, (uint32_t)((g >> 2) & 1), p.wait_ns))
+                return false;
+            ++begun;
+            tc::fence_after();
+            issue_s(0, g);
+            issue_s(1, g);
+            tc::commit_elect(k_empty0 + (g % kT2KSlots) * 8);
+            if (nst == 1) tc::commit_elect(q_empty);
+            return true;
+        };
+        if (nst > 0) ok = begin();
+        while (ok && nst > 0) {
+            for (int j = 0; ok && j < nst; ++j, ++g) {
+                const uint32_t ph = (uint32_t)(g & 1);
+                ok = wait_all(p_full0, ph, p.wait_ns) && wait_all(v_full0 + (g & 1) * 8, (uint32_t)((g >> 1) & 1), p.wait_ns);
+                if (!ok) break;
+                tc::fence_after();
+                issue_o(0, g, j == 0);
+                const bool more = j + 1 < nst;
+                if (more) {
+                    if (!(ok = wait_all(k_full0 + ((g + 1) & 3) * 8, (uint32_t)(((g + 1) >> 2) & 1), p.wait_ns))) break;
+                    tc::fence_after();
+                    issue_s(0, g + 1);
+                }
+                if (!(ok = wait_all(p_full0 + 8, ph, p.wait_ns))) break;
+                tc::fence_after();
+                issue_o(1, g, j == 0);
+                tc::commit_elect(v_empty0 + (g & 1) * 8);  // V read by both tiles
+                if (more) {
+                    issue_s(1, g + 1);
+                    tc::commit_elect(k_empty0 + ((g + 1) % kT2KSlots) * 8);
+                    if (j + 2 == nst) tc::commit_elect(q_empty);  // the item's last scores
+                }
+            }
+            if (!ok) break;
+            nst = next_item();
+            if (ok && nst > 0) ok = begin();
+        }
+        bad = !ok;
+        // every MMA issued has finished before tensor memory is released
+        tc::commit_elect(fin);
+        (void)wait_all(fin, 0, drain_limit(p.wait_ns));
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- softmax ----
+        // Lanes and rows as in prefill_tc2_kernel: a quad of lanes has rows a and b of
+        // its tile, a lane the keys 8k + 2 (i mod 4) and the next one of each group.
+        const int t = (warp >> 2) & 1;  // tile
+        const int c4 = lane & 3;
+        const int lb = (warp & 3) * 32 + (warp >> 3) * 16;
+        const int rla = lb + (lane >> 2), rlb = rla + 8;              // rows of the tile
+        const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
+        const uint32_t ts = tl + 128u;                                // S_t / P_t
+        const bool fold = p.sl2 > 0.f;
+        const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
+        int g = 0;
+        bool ok = true;
+        for (int i = 0;; ++i) {
+            if (!(ok = wait_warp(item_full0 + (i % kItems) * 8, (uint32_t)((i / kItems) & 1), p.wait_ns))) break;
+            const SlideItem& it = ring[i % kItems];
+            if (it.r < 0) break;
+            const int nst = stages(it), head = it.head, gap = it.gap;
+            const int rra = it.rho0 + t * tr + rla, rrb = it.rho0 + t * tr + rlb;
+            const bool va = rla < tr && rra < it.nrows, vb = rlb < tr && rrb < it.nrows;
+            const int posa = va ? it.first + rra / p.G : it.p_hi, posb = vb ? it.first + rrb / p.G : it.p_hi;
+            const int mposa = max(posa, 0), mposb = max(posb, 0);
+            // the rows' windows begin here
+            const int wina = mposa >= p.window ? mposa - p.window + 1 : 0, winb = mposb >= p.window ? mposb - p.window + 1 : 0;
+            RowSums r = {-INFINITY, -INFINITY, 0.f, 0.f, true};
+            bool steady = false;  // the warp's rows have references
+            for (int j = 0; j < nst; ++j, ++g) {
+                ok = wait_warp(s_full0 + t * 8, (uint32_t)(g & 1), p.wait_ns) &&
+                     wait_warp(k_full0 + (g & 3) * 8, (uint32_t)((g >> 2) & 1), p.wait_ns);  // (the mask's)
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t present = lds_u32(mask0 + (g & 3) * 4);
+                // key = local key + shift, in the sinks' blocks local key + 128 j
+                const int shift = (j * kT2Blocks + gap) * kBlock;
+                const bool plain = steady && present == (1u << kT2Blocks) - 1u && j * kT2Blocks >= head &&
+                                   shift + kT2Keys - 1 <= min(mposa, mposb) && shift >= max(wina, winb);
+                bool done = false;
+                if (__all_sync(0xffffffffu, plain)) {
+                    uint32_t x[2 * kT2Keys / 4];
+                    tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                    tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                    tc::wait_ld();
+                    const uint64_t nua = tc::f2(-r.ma, -r.ma), nub = tc::f2(-r.mb, -r.mb);
+                    uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int k = 0; k < kT2Keys / 8; ++k) {
+                        const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])),
+                                                     sc2, nua);
+                        const uint64_t b2 = tc::fma2(
+                            tc::f2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), sc2, nub);
+                        const float ea0 = ex2(tc::f2_lo(a2)), ea1 = ex2(tc::f2_hi(a2));
+                        const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
+                        acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
+                        accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
+                        x[2 * k] = pack_bf16x2(ea0, ea1);
+                        x[2 * k + 1] = pack_bf16x2(eb0, eb1);
+                    }
+                    const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
+                    const float psa = tc::f2_lo(sa) + tc::f2_hi(sa), psb = tc::f2_lo(sb) + tc::f2_hi(sb);
+                    // A lane's sum of 32 above 1 has one above 2^-5: the stage is
+                    // done again with the reference moved.
+                    if (!__any_sync(0xffffffffu, (va && psa > 1.f) || (vb && psb > 1.f))) {
+                        r.la += psa;
+                        r.lb += psb;
+                        tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
+                        tc::wait_st();
+                        done = true;
+                    }
+                }
+                if (!done) {
+                    const int done_keys = j * kT2Keys;
+                    StageMask a(min(p.sinks, mposa + 1) - done_keys, wina - shift, mposa + 1 - shift, present);
+                    StageMask b(min(p.sinks, mposb + 1) - done_keys, winb - shift, mposb + 1 - shift, present);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        a.w[k] >>= 2 * c4;
+                        b.w[k] >>= 2 * c4;
+                    }
+                    r = masked_stage<HD>(tl, a, b, p.sl2, r, o_done0 + t * 8, (uint32_t)((g - 1) & 1), p.wait_ns);
+                    if (!(ok = r.ok)) break;
+                    steady = fold && !__any_sync(0xffffffffu, (va && r.ma == -INFINITY) || (vb && r.mb == -INFINITY));
+                }
+                if (warp == 1) {
+                    // V rows that no row of the item sees (missing blocks, the
+                    // context's end, outside the window) may hold any bits: zero them
+                    // once the stage's V copies have landed, before tile 0's P . V
+                    // (tile 1's is issued after it)
+                    const int y = j * kT2Blocks + lane, t0 = (y < head ? y : y + gap) * kBlock;
+                    const uint32_t seen = lane < kT2Blocks && !((present >> lane) & 1u) ? 0u
+                                          : Sight::first_bits(it.n - t0) & (Sight::first_bits(it.sinks - t0) | ~Sight::first_bits(it.lo - t0));
+                    if (__any_sync(0xffffffffu, lane < kT2Blocks && seen != 0xFFFFu)) {
+                        if (!(ok = wait_all(v_full0 + (g & 1) * 8, (uint32_t)((g >> 1) & 1), p.wait_ns))) break;
+                        const uint32_t vbase = sbase + SM::kRingV + (g & 1) * SM::kKV;
+                        for (int l = 0; l < kT2Blocks; ++l) {
+                            const uint32_t in = __shfl_sync(0xffffffffu, seen, l);
+                            if (in == 0xFFFFu) continue;
+                            for (int k = lane; k < kBlock * kH * 8; k += 32) {
+                                const int row = k / (kH * 8), hh = (k / 8) % kH, ch = k % 8;
+                                if (!((in >> row) & 1u))
+                                    st_shared_zero16(vbase + (l * kH + hh) * kBlock * 128 + row * 128 + ch * 16);
+                            }
+                        }
+                        fence_proxy_async_smem();  // generic-proxy writes read by the tensor cores
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full0 + t * 8);
+            }
+            if (!ok) break;
+            if (!(ok = wait_warp(o_done0 + t * 8, (uint32_t)((g - 1) & 1), p.wait_ns))) break;
+            tc::fence_after();
+            r.la += __shfl_xor_sync(0xffffffffu, r.la, 1);
+            r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 1);
+            r.la += __shfl_xor_sync(0xffffffffu, r.la, 2);
+            r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 2);
+            // rows before position 0 are +0, and so is a row without a key
+            const float inva = posa >= 0 && r.la > 0.f ? 1.f / r.la : 0.f, invb = posb >= 0 && r.lb > 0.f ? 1.f / r.lb : 0.f;
+            uint16_t* orowa = p.out + ((long long)(it.q0 + rra / p.G) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
+            uint16_t* orowb = p.out + ((long long)(it.q0 + rrb / p.G) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
+#pragma unroll 1
+            for (int ch = 0; ch < HD / 32; ++ch) {
+                uint32_t y[16], wa[4], wb[4];
+                tc::ld16x256_x4(tl + 32u * ch, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    wa[k] = inva != 0.f ? pack_bf16x2(__uint_as_float(y[4 * k]) * inva, __uint_as_float(y[4 * k + 1]) * inva) : 0u;
+                    wb[k] = invb != 0.f ? pack_bf16x2(__uint_as_float(y[4 * k + 2]) * invb, __uint_as_float(y[4 * k + 3]) * invb) : 0u;
+                }
+                quad_transpose(wa, c4);
+                quad_transpose(wb, c4);
+                if (va) *reinterpret_cast<uint4*>(orowa + 32 * ch + 8 * c4) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                if (vb) *reinterpret_cast<uint4*>(orowb + 32 * ch + 8 * c4) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+            }
+        }
+        bad = !ok;
+    }
+    tc::fence_before();
+    if (__syncthreads_or(bad)) give_up(p.dev_err);
+    if (warp == kT2MmaWarp) {
+        tc::fence_after();
+        tc::dealloc(tbase, kT2Cols);
+    }
+}
+
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 // Raise a kernel's dynamic shared-memory limit once per device and context
@@ -1872,11 +2379,18 @@ bool prepare_tc() {
     return raise_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<HD>), TcSmem<HD>::kTotal, done, mu);
 }
 
-template <int HD, bool SLIDE = false>
+template <int HD>
 bool prepare_tc2() {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD, SLIDE>), Tc2Smem<HD>::kTotal, done, mu);
+    return raise_smem_once(reinterpret_cast<const void*>(prefill_tc2_kernel<HD>), Tc2Smem<HD>::kTotal, done, mu);
+}
+
+template <int HD>
+bool prepare_slide() {
+    static std::mutex mu;
+    static CUcontext done[256] = {};
+    return raise_smem_once(reinterpret_cast<const void*>(slide_tc2_kernel<HD>), SlideSmem<HD>::kTotal, done, mu);
 }
 
 template <int HD>
@@ -1957,18 +2471,22 @@ mi_status prefill(const mi_dims* dims, int32_t total_q, int32_t max_query_len, c
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (sliding) {
-        if (!(HD == 64 ? prepare_tc2<64, true>() : prepare_tc2<128, true>())) return MI_ERR_CUDA;
+        if (!(HD == 64 ? prepare_slide<64>() : prepare_slide<128>())) return MI_ERR_CUDA;
         CUtensorMap tq, tk, tv;
         if (!make_tmap_q_group(&tq, q, total_q, D.Hq, HD, G, tc_rows) ||
             !make_tmap_kv_halves(&tk, k_cache, rows, HD) || !make_tmap_kv_blocks(&tv, v_cache, rows, HD))
             return MI_ERR_CUDA;
+        const int sms = sm_count();
+        if (sms <= 0) return MI_ERR_CUDA;
         SlidingParams sp;
         static_cast<PrefillParams&>(sp) = p;
         sp.window = sliding->window;
         sp.sinks = sliding->sinks;
-        e = HD == 64 ? launch_pdl(prefill_tc2_kernel<64, true>, (int)grid, kT2Threads, Tc2Smem<64>::kTotal, st, tq, tk, tv, sp)
-                     : launch_pdl(prefill_tc2_kernel<128, true>, (int)grid, kT2Threads, Tc2Smem<128>::kTotal, st, tq, tk,
-                                  tv, sp);
+        // one block per SM, which takes items in turn; no more blocks than items
+        const long long most = ((long long)total_q * G / rows_per_tile + D.B) * D.Hkv;
+        const int blocks = (int)(most < sms ? most : sms);
+        e = HD == 64 ? launch_pdl(slide_tc2_kernel<64>, blocks, kT2Threads, SlideSmem<64>::kTotal, st, tq, tk, tv, sp)
+                     : launch_pdl(slide_tc2_kernel<128>, blocks, kT2Threads, SlideSmem<128>::kTotal, st, tq, tk, tv, sp);
     } else if (use_tc2) {
         if (!(HD == 64 ? prepare_tc2<64>() : prepare_tc2<128>())) return MI_ERR_CUDA;
         CUtensorMap tq, tk, tv;

@@ -1839,7 +1839,8 @@ struct SlideSmem : Tc2Smem<HD> {
 // 256 rows of a request and KV head; r < 0: no more.
 struct SlideItem {
     int r, h, q0, first, n, nrows, rho0, p_hi;  // as Item
-    int head, gap, lo, sinks, nblk;             // blocks 0 .. head - 1 and head + gap .. head + gap + nblk - head - 1
+    int head, gap, nblk;  // the blocks 0 .. head - 1 and from head + gap on, nblk in all
+    int lo, sinks;        // tokens that some row of the request sees: below sinks, and from lo on
 };
 
 // A request's tiles of `rows` rows; 0 where it is refused.
@@ -1864,13 +1865,14 @@ __device__ SlideItem slide_item(const SlidingParams& p, const long long* sums, i
     it.nrows = m * p.G;
     it.rho0 = (tiles - 1 - k) * rows;
     it.p_hi = it.first + (it.rho0 + min(rows, it.nrows - it.rho0) - 1) / p.G;
-    const int p_lo = max(0, it.first + it.rho0 / p.G);  // the first row's position
-    it.lo = p_lo >= p.window ? p_lo - p.window + 1 : 0;
-    it.sinks = min(p.sinks, it.lo);
-    it.head = (it.sinks + kBlock - 1) / kBlock;
+    auto window_of = [&](int pos) { return pos >= p.window ? pos - p.window + 1 : 0; };
+    const int from = window_of(max(0, it.first + it.rho0 / p.G));  // the first row's window
+    it.head = (min(p.sinks, from) + kBlock - 1) / kBlock;
     const int all = it.p_hi >= 0 ? it.p_hi / kBlock + 1 : 0;
-    it.gap = max(0, min(it.lo / kBlock, all) - it.head);
+    it.gap = max(0, min(from / kBlock, all) - it.head);
     it.nblk = all - it.gap;
+    it.lo = window_of(max(0, it.first));
+    it.sinks = min(p.sinks, it.lo);
     return it;
 }
 
@@ -1901,16 +1903,19 @@ __device__ __noinline__ RowSums masked_stage(uint32_t tl, StageMask a, StageMask
     tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
     tc::ld16x256_x8(ts + 64u, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
     tc::wait_ld();
+    if (!(sl2 > 0.f)) {  // scaled before the maximum
+#pragma unroll
+        for (int i = 0; i < 2 * kT2Keys / 4; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * sl2);
+        sl2 = 1.f;
+    }
     float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kT2Keys / 8; ++k) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const uint32_t bit = 1u << (8 * (k & 3) + e);
-            const float va = a.w[k >> 2] & bit ? __uint_as_float(x[4 * k + e]) * sl2 : -INFINITY;
-            const float vb = b.w[k >> 2] & bit ? __uint_as_float(x[4 * k + 2 + e]) * sl2 : -INFINITY;
-            x[4 * k + e] = __float_as_uint(va);
-            x[4 * k + 2 + e] = __float_as_uint(vb);
+            x[4 * k + e] = a.w[k >> 2] & bit ? x[4 * k + e] : __float_as_uint(-INFINITY);
+            x[4 * k + 2 + e] = b.w[k >> 2] & bit ? x[4 * k + 2 + e] : __float_as_uint(-INFINITY);
         }
         ma = tc::max3(ma, __uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
         mb = tc::max3(mb, __uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
@@ -1920,6 +1925,8 @@ __device__ __noinline__ RowSums masked_stage(uint32_t tl, StageMask a, StageMask
         ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
         mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
     }
+    ma *= sl2;
+    mb *= sl2;
     // (all four lanes of a row take the same decision)
     ma = ma + kNear > r.ma ? ma + kAhead : r.ma;
     mb = mb + kNear > r.mb ? mb + kAhead : r.mb;
@@ -1929,18 +1936,22 @@ __device__ __noinline__ RowSums masked_stage(uint32_t tl, StageMask a, StageMask
     r.mb = mb;
     r.ok = true;
     const float una = ma == -INFINITY ? 0.f : ma, unb = mb == -INFINITY ? 0.f : mb;
-    float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+    const uint64_t sc2 = tc::f2(sl2, sl2), nua = tc::f2(-una, -una), nub = tc::f2(-unb, -unb);
+    uint64_t acca[2] = {0ull, 0ull}, accb[2] = {0ull, 0ull};
 #pragma unroll
     for (int k = 0; k < kT2Keys / 8; ++k) {
-        const float ea0 = ex2(__uint_as_float(x[4 * k]) - una), ea1 = ex2(__uint_as_float(x[4 * k + 1]) - una);
-        const float eb0 = ex2(__uint_as_float(x[4 * k + 2]) - unb), eb1 = ex2(__uint_as_float(x[4 * k + 3]) - unb);
-        sa[k & 1] += ea0 + ea1;
-        sb[k & 1] += eb0 + eb1;
+        const uint64_t a2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1])), sc2, nua);
+        const uint64_t b2 = tc::fma2(tc::f2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3])), sc2, nub);
+        const float ea0 = ex2(tc::f2_lo(a2)), ea1 = ex2(tc::f2_hi(a2));
+        const float eb0 = ex2(tc::f2_lo(b2)), eb1 = ex2(tc::f2_hi(b2));
+        acca[k & 1] = tc::add2(acca[k & 1], tc::f2(ea0, ea1));
+        accb[k & 1] = tc::add2(accb[k & 1], tc::f2(eb0, eb1));
         x[2 * k] = pack_bf16x2(ea0, ea1);
         x[2 * k + 1] = pack_bf16x2(eb0, eb1);
     }
-    r.la = r.la * alpha_a + (sa[0] + sa[1]);
-    r.lb = r.lb * alpha_b + (sb[0] + sb[1]);
+    const uint64_t sa = tc::add2(acca[0], acca[1]), sb = tc::add2(accb[0], accb[1]);
+    r.la = r.la * alpha_a + (tc::f2_lo(sa) + tc::f2_hi(sa));
+    r.lb = r.lb * alpha_b + (tc::f2_lo(sb) + tc::f2_hi(sb));
     tc::st16x128_x16(ts, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
     if (__any_sync(0xffffffffu, move_a || move_b)) {
         // O may be touched once its previous P . V has finished
@@ -2294,8 +2305,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     steady = fold && !__any_sync(0xffffffffu, (va && r.ma == -INFINITY) || (vb && r.mb == -INFINITY));
                 }
                 if (warp == 1) {
-                    // V rows that no row of the item sees (missing blocks, the
-                    // context's end, outside the window) may hold any bits: zero them
+                    // V rows that no row of the request sees (missing blocks, the
+                    // context's end, outside every window) may hold any bits: zero them
                     // once the stage's V copies have landed, before tile 0's P . V
                     // (tile 1's is issued after it)
                     const int y = j * kT2Blocks + lane, t0 = (y < head ? y : y + gap) * kBlock;
@@ -2331,7 +2342,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             const float inva = posa >= 0 && r.la > 0.f ? 1.f / r.la : 0.f, invb = posb >= 0 && r.lb > 0.f ? 1.f / r.lb : 0.f;
             uint16_t* orowa = p.out + ((long long)(it.q0 + rra / p.G) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
             uint16_t* orowb = p.out + ((long long)(it.q0 + rrb / p.G) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
-#pragma unroll 1
+#pragma unroll 2
             for (int ch = 0; ch < HD / 32; ++ch) {
                 uint32_t y[16], wa[4], wb[4];
                 tc::ld16x256_x4(tl + 32u * ch, y);

@@ -1838,7 +1838,8 @@ struct SlideSmem : Tc2Smem<HD> {
 
 // 256 rows of a request and KV head; r < 0: no more.
 struct SlideItem {
-    int r, h, q0, first, n, nrows, rho0, p_hi;  // as Item
+    int r, h, q0, first, n, p_hi;  // as Item
+    int tok0, m;                   // the item's first of the request's m new tokens
     int head, gap, nblk;  // the blocks 0 .. head - 1 and from head + gap on, nblk in all
     int lo, sinks;        // tokens that some row of the request sees: below sinks, and from lo on
 };
@@ -1861,12 +1862,12 @@ __device__ SlideItem slide_item(const SlidingParams& p, const long long* sums, i
     it.q0 = __ldg(p.query_start + it.r);
     const int m = __ldg(p.query_start + it.r + 1) - it.q0;
     it.n = min(__ldg(p.context_lens + it.r), p.mbps * kBlock);
+    it.m = m;
     it.first = it.n - m;
-    it.nrows = m * p.G;
-    it.rho0 = (tiles - 1 - k) * rows;
-    it.p_hi = it.first + (it.rho0 + min(rows, it.nrows - it.rho0) - 1) / p.G;
+    it.tok0 = (tiles - 1 - k) * (rows / p.G);
+    it.p_hi = it.first + min(it.tok0 + rows / p.G, m) - 1;
     auto window_of = [&](int pos) { return pos >= p.window ? pos - p.window + 1 : 0; };
-    const int from = window_of(max(0, it.first + it.rho0 / p.G));  // the first row's window
+    const int from = window_of(max(0, it.first + it.tok0));  // the first row's window
     it.head = (min(p.sinks, from) + kBlock - 1) / kBlock;
     const int all = it.p_hi >= 0 ? it.p_hi / kBlock + 1 : 0;
     it.gap = max(0, min(from / kBlock, all) - it.head);
@@ -2072,9 +2073,9 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             if (x < items) it = slide_item(p, sums, rows, x);
             if (it.r >= 0 && it.nblk == 0) {
                 // every row before position 0: zeros, and nothing for the others to do
-                const int tokens = min(rows, it.nrows - it.rho0) / p.G, words = p.G * HD / 8;
+                const int tokens = min(rows / p.G, it.m - it.tok0), words = p.G * HD / 8;
                 for (int k = lane; k < tokens * words; k += 32) {
-                    const long long row = (long long)(it.q0 + it.rho0 / p.G + k / words) * p.Hq + (long long)it.h * p.G;
+                    const long long row = (long long)(it.q0 + it.tok0 + k / words) * p.Hq + (long long)it.h * p.G;
                     reinterpret_cast<uint4*>(p.out + row * HD)[k % words] = make_uint4(0, 0, 0, 0);
                 }
                 continue;
@@ -2130,7 +2131,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                         for (int t = 0; t < 2; ++t)
                             for (int hh = 0; hh < kH; ++hh)
                                 tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
-                                            it.q0 + (it.rho0 + t * tr) / p.G, policy);
+                                            it.q0 + it.tok0 + t * (tr / p.G), policy);
                     }
                     __syncwarp();
                     ++begun;
@@ -2174,31 +2175,44 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             ++found;
             return it.r < 0 ? 0 : stages(it);
         };
-        int nst = next_item(), g = 0, begun = 0;
-        // both tiles' scores of an item's first stage
-        auto begin = [&]() -> bool {
-            if (!wait_all(q_full, (uint32_t)(begun & 1), p.wait_ns) ||
-                !wait_all(k_full0 + (g & 3) * 8, (uint32_t)((g >> 2) & 1), p.wait_ns))
-                return false;
+        // whether Q and K of stage g, an item's first, have landed (without a wait: now)
+        int g = 0, begun = 0;
+        auto landed = [&](int gn, bool now) -> bool {
+            const uint32_t kb = k_full0 + (gn & 3) * 8, kp = (uint32_t)((gn >> 2) & 1), qp = (uint32_t)(begun & 1);
+            if (now) return __all_sync(0xffffffffu, mbar_try_wait(q_full, qp) && mbar_try_wait(kb, kp));
+            return wait_all(q_full, qp, p.wait_ns) && wait_all(kb, kp, p.wait_ns);
+        };
+        // An item's stages; behind its last P . V of a tile come the first scores of
+        // the next item, whose rows' softmax then need not wait for the other tile.
+        int nst = next_item();
+        if (nst > 0 && (ok = landed(0, false))) {
             ++begun;
             tc::fence_after();
-            issue_s(0, g);
-            issue_s(1, g);
-            tc::commit_elect(k_empty0 + (g % kT2KSlots) * 8);
+            issue_s(0, 0);
+            issue_s(1, 0);
+            tc::commit_elect(k_empty0);
             if (nst == 1) tc::commit_elect(q_empty);
-            return true;
-        };
-        if (nst > 0) ok = begin();
+        }
         while (ok && nst > 0) {
-            for (int j = 0; ok && j < nst; ++j, ++g) {
+            int after = 0;  // the next item's stages
+            for (int j = 0; j < nst; ++j, ++g) {
                 const uint32_t ph = (uint32_t)(g & 1);
-                ok = wait_all(p_full0, ph, p.wait_ns) && wait_all(v_full0 + (g & 1) * 8, (uint32_t)((g >> 1) & 1), p.wait_ns);
-                if (!ok) break;
+                if (!(ok = wait_all(p_full0, ph, p.wait_ns) && wait_all(v_full0 + (g & 1) * 8, (uint32_t)((g >> 1) & 1), p.wait_ns)))
+                    break;
                 tc::fence_after();
                 issue_o(0, g, j == 0);
-                const bool more = j + 1 < nst;
-                if (more) {
+                const bool last = j + 1 == nst;
+                bool first_tile = false, more = !last;
+                if (!last) {
                     if (!(ok = wait_all(k_full0 + ((g + 1) & 3) * 8, (uint32_t)(((g + 1) >> 2) & 1), p.wait_ns))) break;
+                    first_tile = true;
+                } else {
+                    after = next_item();
+                    if (!ok) break;
+                    more = after > 0;
+                    first_tile = more && landed(g + 1, true);
+                }
+                if (first_tile) {
                     tc::fence_after();
                     issue_s(0, g + 1);
                 }
@@ -2206,15 +2220,18 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 tc::fence_after();
                 issue_o(1, g, j == 0);
                 tc::commit_elect(v_empty0 + (g & 1) * 8);  // V read by both tiles
-                if (more) {
-                    issue_s(1, g + 1);
-                    tc::commit_elect(k_empty0 + ((g + 1) % kT2KSlots) * 8);
-                    if (j + 2 == nst) tc::commit_elect(q_empty);  // the item's last scores
+                if (!more) continue;
+                if (!first_tile) {
+                    if (!(ok = landed(g + 1, false))) break;
+                    tc::fence_after();
+                    issue_s(0, g + 1);
                 }
+                issue_s(1, g + 1);
+                tc::commit_elect(k_empty0 + ((g + 1) % kT2KSlots) * 8);
+                if (last) ++begun;
+                if (last ? after == 1 : j + 2 == nst) tc::commit_elect(q_empty);  // an item's last scores
             }
-            if (!ok) break;
-            nst = next_item();
-            if (ok && nst > 0) ok = begin();
+            nst = after;
         }
         bad = !ok;
         // every MMA issued has finished before tensor memory is released
@@ -2231,6 +2248,9 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         const int rla = lb + (lane >> 2), rlb = rla + 8;              // rows of the tile
         const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
         const uint32_t ts = tl + 128u;                                // S_t / P_t
+        const int toka = (t * tr + rla) / p.G, tokb = (t * tr + rlb) / p.G;  // their tokens in an item
+        const long long outa = ((long long)toka * p.Hq + (t * tr + rla) % p.G) * HD + 8 * c4;
+        const long long outb = ((long long)tokb * p.Hq + (t * tr + rlb) % p.G) * HD + 8 * c4;
         const bool fold = p.sl2 > 0.f;
         const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
         int g = 0;
@@ -2240,9 +2260,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             const SlideItem& it = ring[i % kItems];
             if (it.r < 0) break;
             const int nst = stages(it), head = it.head, gap = it.gap;
-            const int rra = it.rho0 + t * tr + rla, rrb = it.rho0 + t * tr + rlb;
-            const bool va = rla < tr && rra < it.nrows, vb = rlb < tr && rrb < it.nrows;
-            const int posa = va ? it.first + rra / p.G : it.p_hi, posb = vb ? it.first + rrb / p.G : it.p_hi;
+            const bool va = rla < tr && it.tok0 + toka < it.m, vb = rlb < tr && it.tok0 + tokb < it.m;
+            const int posa = va ? it.first + it.tok0 + toka : it.p_hi, posb = vb ? it.first + it.tok0 + tokb : it.p_hi;
             const int mposa = max(posa, 0), mposb = max(posb, 0);
             // the rows' windows begin here
             const int wina = mposa >= p.window ? mposa - p.window + 1 : 0, winb = mposb >= p.window ? mposb - p.window + 1 : 0;
@@ -2340,8 +2359,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 2);
             // rows before position 0 are +0, and so is a row without a key
             const float inva = posa >= 0 && r.la > 0.f ? 1.f / r.la : 0.f, invb = posb >= 0 && r.lb > 0.f ? 1.f / r.lb : 0.f;
-            uint16_t* orowa = p.out + ((long long)(it.q0 + rra / p.G) * p.Hq + (long long)it.h * p.G + rra % p.G) * HD;
-            uint16_t* orowb = p.out + ((long long)(it.q0 + rrb / p.G) * p.Hq + (long long)it.h * p.G + rrb % p.G) * HD;
+            uint16_t* out = p.out + ((long long)(it.q0 + it.tok0) * p.Hq + (long long)it.h * p.G) * HD;
 #pragma unroll 2
             for (int ch = 0; ch < HD / 32; ++ch) {
                 uint32_t y[16], wa[4], wb[4];
@@ -2354,8 +2372,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 }
                 quad_transpose(wa, c4);
                 quad_transpose(wb, c4);
-                if (va) *reinterpret_cast<uint4*>(orowa + 32 * ch + 8 * c4) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-                if (vb) *reinterpret_cast<uint4*>(orowb + 32 * ch + 8 * c4) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                if (va) *reinterpret_cast<uint4*>(out + outa + 32 * ch) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                if (vb) *reinterpret_cast<uint4*>(out + outb + 32 * ch) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
             }
         }
         bad = !ok;

@@ -34,6 +34,7 @@
 //     while the 8 tiles of a group read the same K/V through L2 at about the
 //     same time. Tiles past a request's last row exit at once.
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <mutex>
 
@@ -2248,23 +2249,41 @@ __global__ void __launch_bounds__(kT2Threads, 1)
         const int rla = lb + (lane >> 2), rlb = rla + 8;              // rows of the tile
         const uint32_t tl = tbase + ((uint32_t)lb << 16) + 256u * t;  // O_t of these lanes
         const uint32_t ts = tl + 128u;                                // S_t / P_t
-        const int toka = (t * tr + rla) / p.G, tokb = (t * tr + rlb) / p.G;  // their tokens in an item
-        const long long outa = ((long long)toka * p.Hq + (t * tr + rla) % p.G) * HD + 8 * c4;
-        const long long outb = ((long long)tokb * p.Hq + (t * tr + rlb) % p.G) * HD + 8 * c4;
+        // their tokens in an item; a row past the tile (G does not divide 128, so a request
+        // has fewer than 2^31 / 3 tokens) has none
+        constexpr int kNoToken = 1 << 30;
+        const int toka = rla < tr ? (t * tr + rla) / p.G : kNoToken, tokb = rlb < tr ? (t * tr + rlb) / p.G : kNoToken;
         const bool fold = p.sl2 > 0.f;
         const uint64_t sc2 = tc::f2(p.sl2, p.sl2);
         int g = 0;
         bool ok = true;
         for (int i = 0;; ++i) {
             if (!(ok = wait_warp(item_full0 + (i % kItems) * 8, (uint32_t)((i / kItems) & 1), p.wait_ns))) break;
-            const SlideItem& it = ring[i % kItems];
-            if (it.r < 0) break;
-            const int nst = stages(it), head = it.head, gap = it.gap;
-            const bool va = rla < tr && it.tok0 + toka < it.m, vb = rlb < tr && it.tok0 + tokb < it.m;
-            const int posa = va ? it.first + it.tok0 + toka : it.p_hi, posb = vb ? it.first + it.tok0 + tokb : it.p_hi;
-            const int mposa = max(posa, 0), mposb = max(posb, 0);
-            // the rows' windows begin here
-            const int wina = mposa >= p.window ? mposa - p.window + 1 : 0, winb = mposb >= p.window ? mposb - p.window + 1 : 0;
+            // (The item's numbers are read where they are used: 64 scores leave no
+            // registers for them, and what spilled from the plain stage's loop cost it 15 %.)
+            const uint32_t item = smem_u32(&ring[i % kItems]);
+            auto it = [&](size_t field) { return (int)lds_u32(item + (uint32_t)field); };
+            if (it(offsetof(SlideItem, r)) < 0) break;
+            const int nst = (it(offsetof(SlideItem, nblk)) + kT2Blocks - 1) / kT2Blocks;
+            // a row's position, of one that does not count the item's last
+            auto position = [&](int tok) {
+                const int x = it(offsetof(SlideItem, tok0)) + tok;
+                return x < it(offsetof(SlideItem, m)) ? it(offsetof(SlideItem, first)) + x : it(offsetof(SlideItem, p_hi));
+            };
+            auto window_of = [&](int pos) { return pos >= p.window ? pos - p.window + 1 : 0; };
+            bool va, vb;
+            int whole_from, whole_to;  // the stages that both rows see whole, if all blocks are there
+            {
+                const int left = it(offsetof(SlideItem, m)) - it(offsetof(SlideItem, tok0));
+                va = toka < left;
+                vb = tokb < left;
+                const int mposa = max(position(toka), 0), mposb = max(position(tokb), 0);
+                // stage j's keys: j * 128 + skipped and 127 more
+                const int skipped = it(offsetof(SlideItem, gap)) * kBlock, from = window_of(max(mposa, mposb)) - skipped;
+                whole_from = max((it(offsetof(SlideItem, head)) + kT2Blocks - 1) / kT2Blocks,
+                                 from <= 0 ? 0 : from / kT2Keys + (from % kT2Keys != 0));
+                whole_to = max(0, min(mposa, mposb) + 1 - skipped) / kT2Keys;
+            }
             RowSums r = {-INFINITY, -INFINITY, 0.f, 0.f, true};
             bool steady = false;  // the warp's rows have references
             for (int j = 0; j < nst; ++j, ++g) {
@@ -2273,10 +2292,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 if (!ok) break;
                 tc::fence_after();
                 const uint32_t present = lds_u32(mask0 + (g & 3) * 4);
-                // key = local key + shift, in the sinks' blocks local key + 128 j
-                const int shift = (j * kT2Blocks + gap) * kBlock;
-                const bool plain = steady && present == (1u << kT2Blocks) - 1u && j * kT2Blocks >= head &&
-                                   shift + kT2Keys - 1 <= min(mposa, mposb) && shift >= max(wina, winb);
+                const bool plain = steady && present == (1u << kT2Blocks) - 1u && j >= whole_from && j < whole_to;
                 bool done = false;
                 if (__all_sync(0xffffffffu, plain)) {
                     uint32_t x[2 * kT2Keys / 4];
@@ -2311,9 +2327,11 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     }
                 }
                 if (!done) {
-                    const int done_keys = j * kT2Keys;
-                    StageMask a(min(p.sinks, mposa + 1) - done_keys, wina - shift, mposa + 1 - shift, present);
-                    StageMask b(min(p.sinks, mposb + 1) - done_keys, winb - shift, mposb + 1 - shift, present);
+                    // key = local key + shift, in the sinks' blocks local key + before
+                    const int before = j * kT2Keys, shift = before + it(offsetof(SlideItem, gap)) * kBlock;
+                    const int mposa = max(position(toka), 0), mposb = max(position(tokb), 0);
+                    StageMask a(min(p.sinks, mposa + 1) - before, window_of(mposa) - shift, mposa + 1 - shift, present);
+                    StageMask b(min(p.sinks, mposb + 1) - before, window_of(mposb) - shift, mposb + 1 - shift, present);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         a.w[k] >>= 2 * c4;
@@ -2328,9 +2346,13 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                     // context's end, outside every window) may hold any bits: zero them
                     // once the stage's V copies have landed, before tile 0's P . V
                     // (tile 1's is issued after it)
-                    const int y = j * kT2Blocks + lane, t0 = (y < head ? y : y + gap) * kBlock;
-                    const uint32_t seen = lane < kT2Blocks && !((present >> lane) & 1u) ? 0u
-                                          : Sight::first_bits(it.n - t0) & (Sight::first_bits(it.sinks - t0) | ~Sight::first_bits(it.lo - t0));
+                    const int y = j * kT2Blocks + lane;
+                    const int t0 = (y < it(offsetof(SlideItem, head)) ? y : y + it(offsetof(SlideItem, gap))) * kBlock;
+                    uint32_t seen = 0u;
+                    if (lane < kT2Blocks && ((present >> lane) & 1u))
+                        seen = Sight::first_bits(it(offsetof(SlideItem, n)) - t0) &
+                               (Sight::first_bits(it(offsetof(SlideItem, sinks)) - t0) |
+                                ~Sight::first_bits(it(offsetof(SlideItem, lo)) - t0));
                     if (__any_sync(0xffffffffu, lane < kT2Blocks && seen != 0xFFFFu)) {
                         if (!(ok = wait_all(v_full0 + (g & 1) * 8, (uint32_t)((g >> 1) & 1), p.wait_ns))) break;
                         const uint32_t vbase = sbase + SM::kRingV + (g & 1) * SM::kKV;
@@ -2358,8 +2380,12 @@ __global__ void __launch_bounds__(kT2Threads, 1)
             r.la += __shfl_xor_sync(0xffffffffu, r.la, 2);
             r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 2);
             // rows before position 0 are +0, and so is a row without a key
-            const float inva = posa >= 0 && r.la > 0.f ? 1.f / r.la : 0.f, invb = posb >= 0 && r.lb > 0.f ? 1.f / r.lb : 0.f;
-            uint16_t* out = p.out + ((long long)(it.q0 + it.tok0) * p.Hq + (long long)it.h * p.G) * HD;
+            const float inva = position(toka) >= 0 && r.la > 0.f ? 1.f / r.la : 0.f;
+            const float invb = position(tokb) >= 0 && r.lb > 0.f ? 1.f / r.lb : 0.f;
+            uint16_t* out = p.out + ((long long)(it(offsetof(SlideItem, q0)) + it(offsetof(SlideItem, tok0))) * p.Hq +
+                                     (long long)it(offsetof(SlideItem, h)) * p.G) * HD + 8 * c4;
+            uint16_t* outa = out + ((long long)toka * p.Hq + (t * tr + rla) % p.G) * HD;
+            uint16_t* outb = out + ((long long)tokb * p.Hq + (t * tr + rlb) % p.G) * HD;
 #pragma unroll 2
             for (int ch = 0; ch < HD / 32; ++ch) {
                 uint32_t y[16], wa[4], wb[4];
@@ -2372,8 +2398,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
                 }
                 quad_transpose(wa, c4);
                 quad_transpose(wb, c4);
-                if (va) *reinterpret_cast<uint4*>(out + outa + 32 * ch) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-                if (vb) *reinterpret_cast<uint4*>(out + outb + 32 * ch) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                if (va) *reinterpret_cast<uint4*>(outa + 32 * ch) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                if (vb) *reinterpret_cast<uint4*>(outb + 32 * ch) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
             }
         }
         bad = !ok;

@@ -669,23 +669,30 @@ def mi_paged_kv_evict_fp8(d: MiDims, k_cache, v_cache, scores, block_tables, con
 
 
 def _rows(x, stride):
-    """Address of rows and the elements between them: of a tensor [rows][...]
-    whose rows may lie apart, or an address with its stride given."""
+    """Address of rows and the elements between them: of a tensor [rows][width]
+    or [rows][heads][head_dim] whose rows may lie apart, or an address with its
+    stride given."""
     if x is None or isinstance(x, int):
         return x, int(stride)
-    if stride is None:
-        assert x[:1].is_contiguous(), "a row must be contiguous"
-        stride = x.stride(0)
-        if x.shape[0] <= 1:  # torch leaves the stride of a single row unspecified
-            stride = max(stride, x[:1].numel())
-    return x.data_ptr(), int(stride)
+    if stride is not None:
+        return x.data_ptr(), int(stride)
+    st, shape = x.stride(), x.shape
+    assert st[-1] == 1 and (len(st) == 2 or (len(st) == 3 and (shape[1] == 1 or st[1] == shape[2]))), \
+        "a row must be contiguous"
+    if shape[0] > 1:
+        return x.data_ptr(), st[0]
+    return x.data_ptr(), max(st[0], x.numel())  # torch leaves a single row's stride unspecified
 
 
 def _append_norm(fn, d, q, k, v, q_weight, k_weight, eps, positions, slot_mapping, rope_cos_sin, max_pos, q_out, caches,
                  strides, dev_err, stream):
-    rows = [y for x, s in zip((q, k, v), strides or (None, None, None)) for y in _rows(x, s)]
-    return fn(ctypes.byref(d), *rows, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(slot_mapping),
-              _ptr(rope_cos_sin), int(max_pos), _ptr(q_out), *(_ptr(x) for x in caches), _ptr(dev_err), _stream(stream))
+    sq, sk, sv = strides or (None, None, None)
+    q, sq = _rows(q, sq)
+    k, sk = _rows(k, sk)
+    v, sv = _rows(v, sv)
+    return fn(ctypes.byref(d), q, sq, k, sk, v, sv, _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions),
+              _ptr(slot_mapping), _ptr(rope_cos_sin), max_pos, _ptr(q_out), *map(_ptr, caches), _ptr(dev_err),
+              _stream(stream))
 
 
 def mi_paged_kv_append_norm(d: MiDims, q, k, v, q_weight, k_weight, eps, positions, slot_mapping, rope_cos_sin, max_pos,

@@ -67,7 +67,7 @@ __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
 }
 
 template <int HD, bool FP8>
-__global__ void __launch_bounds__(kNormWarps * 32) norm_append_kernel(const NormParams a) {
+__global__ void __launch_bounds__(kNormWarps * 32, 5) norm_append_kernel(const NormParams a) {
     constexpr int kLanes = HD / 16;      // of a head
     constexpr int kHeads = 32 / kLanes;  // of a group
     constexpr int kChunks = HD / 8;      // 16-byte pieces of a v head

@@ -78,31 +78,50 @@ __device__ __forceinline__ Sight sight_of(const SlideParams& p, int b) {
     return Sight(n < 0 ? 0 : (n > cap ? cap : n), p.window, p.sinks);
 }
 
-// The blocks of a piece, chosen by every block of the launch alike: a lane tries 1
-// to 16 pieces for the largest unit, or 16 to 448 in steps of a quarter. Warps take
-// whole pieces in turn; the time is that of the rounds, or of all bytes at the memory's rate, and the
-// end of the unit with the most pieces.
-__device__ int piece_blocks(const SlideParams& p, float warps, float blocks, float units, int largest, int hd, int lane) {
+// The blocks of a piece, for requests before b0 and for those from it on.
+struct Cut {
+    int step, tail_step, b0;
+};
+
+// Chosen by every block of the launch alike: a lane tries 1 to 16 pieces for the
+// largest unit, or 16 to 448 in steps of a quarter. Warps take whole pieces in turn;
+// what the last round leaves over is cut so that every warp has some of it. The time
+// is that of the rounds, or of all bytes at the memory's rate, and the end of the
+// unit with the most pieces.
+__device__ Cut cut_units(const SlideParams& p, float warps, float blocks, float units, int largest, int hd, int lane) {
     const float all = blocks * p.flow;  // time of all blocks at the memory's rate, in a warp's block times
     const float np = lane < 16 ? (float)(lane + 1) : (float)((16 + 4 * (lane & 3)) << ((lane - 16) >> 2));
     const float big = (float)largest;
     const float least = fmaxf(1.f, ceilf(__fdividef(2.f * blocks, (float)kSplitPerWarp * warps)));
-    float step = fmaxf(least, ceilf(__fdividef(big, np)));
-    const float most = ceilf(__fdividef(big, step));
+    const float step = fmaxf(least, ceilf(__fdividef(big, np)));
+    float most = ceilf(__fdividef(big, step));
     // the largest units have `most` pieces, the others half a piece more than their share
     const float fill = __fdividef(blocks, units * big);
     const float rounds = __fdividef(fmaxf(units * (most * fill + 0.5f * (1.f - fill)), units), warps);
-    float cost = fmaxf(all, ceilf(rounds) * (step + kPieceCost)) + 0.01f * most +
+    const float whole = floorf(rounds), over = rounds - whole;
+    float tail_step = step, time = ceilf(rounds) * (step + kPieceCost), part = 1.f;  // part: of the requests, before b0
+    if (whole > 0.f && over > 0.01f) {
+        part = __fdividef(whole, rounds);
+        const float tail_np = fminf(16.f, __fdividef(most * fill, over));  // so that they fill a round
+        tail_step = fminf(step, fmaxf(least, ceilf(__fdividef(big, fmaxf(1.f, tail_np)))));
+        time = whole * (step + kPieceCost) + tail_step + kPieceCost;
+        most = fmaxf(most, ceilf(__fdividef(big, tail_step)));
+    }
+    float cost = fmaxf(all, time) + 0.01f * most +
                  (most > 1.f ? kSplitCost + kMergeCost * ceilf(0.25f * most) * (float)((p.G * hd + 511) / 512) : 0.f);
+    int who = lane;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float c = __shfl_xor_sync(0xffffffffu, cost, o), t = __shfl_xor_sync(0xffffffffu, step, o);
-        if (c < cost || (c == cost && t < step)) {
+        const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+        const int w = __shfl_xor_sync(0xffffffffu, who, o);
+        if (c < cost || (c == cost && w < who)) {
             cost = c;
-            step = t;
+            who = w;
         }
     }
-    return max(1, (int)step);
+    const float b0 = part < 1.f ? part * (float)p.B : (float)p.B;
+    return {max(1, (int)__shfl_sync(0xffffffffu, step, who)), max(1, (int)__shfl_sync(0xffffffffu, tail_step, who)),
+            min(p.B, (int)__shfl_sync(0xffffffffu, b0, who))};
 }
 
 // A split unit counts its finished pieces in a word: the call's tag in the high 48
@@ -227,7 +246,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
         };
     } plan;
     __shared__ long long red[2][kSlideWarps];
-    __shared__ int red_top[kSlideWarps];
+    __shared__ int red_ends[2][kSlideWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t full = smem_u32(bars) + warp * S * 8;
     const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + (uint32_t)(warp * S * 2 * kTile);
@@ -240,7 +259,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     // ---------------------------------------------------------- the plan --
     const bool small = p.B <= kFlatOneWarp;
     long long blocks = 0, units = 0;  // (head, block)s in sight; (request, head)s with any
-    int largest = 0;
+    int largest = 0, smallest = 0x7FFFFFFF;
     for (int b = tid; b < p.B; b += kThreads) {
         const int n = __ldg(p.context_lens + b);
         const int nb = sight_of(p, b).blocks;
@@ -248,6 +267,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
         blocks += (long long)p.Hkv * nb;
         units += nb > 0 ? p.Hkv : 0;
         largest = max(largest, nb);
+        smallest = min(smallest, nb);
         if (b % (int)gridDim.x == (int)blockIdx.x) {
             if (n > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
             if (n <= 0) {  // no token: a zero row
@@ -261,35 +281,48 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
         blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
         units += __shfl_xor_sync(0xffffffffu, units, o);
         largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+        smallest = min(smallest, __shfl_xor_sync(0xffffffffu, smallest, o));
     }
     if (lane == 0) {
         red[0][warp] = blocks;
         red[1][warp] = units;
-        red_top[warp] = largest;
+        red_ends[0][warp] = largest;
+        red_ends[1][warp] = smallest;
     }
     __syncthreads();
     blocks = units = 0;
     for (int i = 0; i < kSlideWarps; ++i) {
         blocks += red[0][i];
         units += red[1][i];
-        largest = max(largest, red_top[i]);
+        largest = max(largest, red_ends[0][i]);
+        smallest = min(smallest, red_ends[1][i]);
     }
     if (largest == 0) return;
     const int warps = gridDim.x * kSlideWarps;
-    const int step = piece_blocks(p, (float)warps, (float)blocks, (float)units, largest, HD, lane);
-    auto pieces_of = [&](int nb) { return (nb + step - 1) / step; };
-    auto pieces = [&](int b) { return (long long)p.Hkv * pieces_of(sight_of(p, b).blocks); };
+    const Cut cut = cut_units(p, (float)warps, (float)blocks, (float)units, largest, HD, lane);
+    auto pieces_of = [&](int b, int nb) {
+        const int step = b < cut.b0 ? cut.step : cut.tail_step;
+        return (nb + step - 1) / step;
+    };
+    auto pieces = [&](int b) { return (long long)p.Hkv * pieces_of(b, sight_of(p, b).blocks); };
     auto splits = [&](int b) {
-        const int np = pieces_of(sight_of(p, b).blocks);
+        const int np = pieces_of(b, sight_of(p, b).blocks);
         return np > 1 ? (long long)p.Hkv * np : 0LL;
     };
+    // As a rule every context is longer than the window, and every request before b0
+    // has as many pieces as any other, and so from it on: then places are divisions.
+    const int even0 = pieces_of(0, largest), even1 = pieces_of(p.B, largest);  // (b0 0: the first is not used)
+    const bool even = pieces_of(0, smallest) == even0 && pieces_of(p.B, smallest) == even1 && smallest > 0;
+    const int per0 = p.Hkv * even0, per1 = p.Hkv * even1, head_pieces = cut.b0 * per0;
     int total;
-    if (small) {
+    if (even) {
+        total = head_pieces + (p.B - cut.b0) * per1;
+    } else if (small) {
         if (warp == 0) {
             const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
             int v = 0, w = 0;
             for (int b = b0; b < b1; ++b) {
-                const int np = pieces_of(plan.held[b]);
+                const int np = pieces_of(b, plan.held[b]);
                 v += p.Hkv * np;
                 w += np > 1 ? p.Hkv * np : 0;
             }
@@ -306,7 +339,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
             x -= v;
             y -= w;
             for (int b = b0; b < b1; ++b) {
-                const int np = pieces_of(plan.held[b]);
+                const int np = pieces_of(b, plan.held[b]);
                 plan.first[b] = x;
                 plan.first_split[b] = y;
                 x += p.Hkv * np;
@@ -340,7 +373,14 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
         c.np = c.j = c.j1 = 0;
         if (x < total) {
             int o, nb;
-            if (small) {
+            if (even) {
+                const bool tail = x >= head_pieces;
+                const int y = tail ? x - head_pieces : x, per = tail ? per1 : per0, r = y / per;
+                c.b = tail ? cut.b0 + r : r;
+                o = y - r * per;
+                nb = small ? plan.held[c.b] : sight_of(p, c.b).blocks;
+                c.slot = x - o - (tail && even0 == 1 ? head_pieces : 0);  // (unused without a split)
+            } else if (small) {
                 int lo = 0, hi = p.B;  // first[lo] <= x < first[hi]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
@@ -358,7 +398,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
                 o = (int)(x - before);
                 c.slot = (int)flat_before(p.B, splits, plan.split_sums, c.b);
             }
-            c.np = pieces_of(nb);
+            c.np = pieces_of(c.b, nb);
             c.h = o / c.np;
             c.i = o - c.h * c.np;
             c.slot += c.h * c.np;

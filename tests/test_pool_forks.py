@@ -300,3 +300,28 @@ def test_compact_empty_and_full(mi):
     assert pool.alloc(0, 64) == 0
     st, src, dst = pool.compact()
     assert st == 0 and len(src) == 0 and pool.num_free() == 0
+
+
+def test_a_slid_sequence_that_shrinks_keeps_its_window():
+    """Slid with window + k, a sequence that takes k tokens back still has all its
+    window; slid with the window alone its table shows what is missing."""
+    import paged_kv_decode_25_gb300 as mi
+    for k, whole in ((20, True), (0, False)):
+        pool = mi.Pool(32, 2, 16)
+        assert pool.alloc(0, 150) == 0
+        assert pool.slide(0, 40 + k, 3)[0] == 0
+        assert mi.mi_kv_pool_shrink(pool.handle, 0, 130) == 0
+        blocks = mi.mi_kv_pool_seq_blocks(pool.handle, 0)
+        assert (blocks[(130 - 40) // 16:] >= 0).all() == whole
+
+
+def test_token_slots_over_released_blocks():
+    import paged_kv_decode_25_gb300 as mi
+    pool = mi.Pool(32, 2, 16)
+    assert pool.alloc(0, 150) == 0 and pool.slide(0, 40, 3)[0] == 0  # columns 1 .. 5 are gone
+    for first, count in ((96, 54), (0, 16), (15, 1), (149, 1)):
+        assert mi.mi_kv_pool_token_slots(pool.handle, 0, first, count)[0] == 0
+    for first in (16, 95, 150):
+        assert mi.mi_kv_pool_token_slots(pool.handle, 0, first, 0)[0] == 0
+    for first, count in ((95, 55), (0, 17), (15, 2), (16, 1), (50, 60)):
+        assert mi.mi_kv_pool_token_slots(pool.handle, 0, first, count)[0] == mi.MI_ERR_INVALID_ARG

@@ -415,9 +415,9 @@ mi_status mi_paged_decode_step(const mi_dims* dims, const void* q, const void* k
  * early-start calls take different workspaces (two, used in turn, suffice:
  * the step lets the next launch start only after its own wait, so a
  * launch never runs beside the one two before it), and a call directly
- * after mi_kv_copy_blocks, mi_kv_copy_rows, mi_paged_kv_evict or an append
- * into the same caches, or after a kernel of the caller's that fills the tables or
- * lengths, does not set the flag. */
+ * after mi_kv_copy_blocks, mi_kv_copy_rows, mi_kv_copy_planes, mi_paged_kv_evict or
+ * an append into the same caches, or after a kernel of the caller's that fills the
+ * tables or lengths, does not set the flag. */
 #define MI_STEP_EARLY_START 1u
 
 /* Kernel variant used by mi_paged_decode_attention_variant:

@@ -1833,6 +1833,15 @@ __global__ void __launch_bounds__(kT2Threads, 1)
 // to 16,000 behind 4,096 (28/4) 1,135 us, 1.22 PFLOP/s; a prompt of 700 behind 256 17 us. A
 // block per item: 207, 1,272, 19.5.
 
+// Warps 0 .. 15 softmax, 16 MMA, 17 producer, and two that only fill up their warpgroup:
+// the four give registers to the sixteen, whose 64 scores leave 96 too few. (With 18
+// warps of 96 and the masked stage a function of its own 159 us for the chunks below,
+// now 151; with shares of 32 and 112 the small roles spill: 167.)
+constexpr int kSlideThreads = (kT2MmaWarp + 4) * 32, kSlideRegs = 96;  // at launch
+constexpr int kSlideFewRegs = 64, kSlideManyRegs = 104;
+static_assert(128 * kSlideFewRegs + 32 * kT2MmaWarp * kSlideManyRegs <= kSlideThreads * kSlideRegs,
+              "the shares come out of the launch's registers");
+
 template <int HD>
 struct SlideSmem : Tc2Smem<HD> {
     using Base = Tc2Smem<HD>;
@@ -1905,8 +1914,8 @@ struct StageMask {
 // masks, takes the maximum, moves the reference, O and the sums where it has to and
 // writes P. `a`, `b`: the rows' masks, shifted right by the lane's first key.
 template <int HD>
-__device__ __noinline__ RowSums masked_stage(uint32_t tl, StageMask a, StageMask b, float sl2, RowSums r, uint32_t o_done,
-                                             uint32_t parity, long long wait_ns) {
+__device__ __forceinline__ RowSums masked_stage(uint32_t tl, StageMask a, StageMask b, float sl2, RowSums r,
+                                                uint32_t o_done, uint32_t parity, long long wait_ns) {
     const uint32_t ts = tl + 128u;
     uint32_t x[2 * kT2Keys / 4];  // x[4k + e]: e = 0, 1 row a; e = 2, 3 row b
     tc::ld16x256_x8(ts, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
@@ -1994,13 +2003,13 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int c) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kT2Threads, 1)
+__global__ void __launch_bounds__(kSlideThreads, 1)
     slide_tc2_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const SlidingParams p) {
     using SM = SlideSmem<HD>;
     constexpr int kH = SM::kH, kItems = SM::kItems;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ long long sums[flat_words(kT2Threads)];
+    __shared__ long long sums[flat_words(kSlideThreads)];
     __shared__ SlideItem ring[kItems];
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -2036,7 +2045,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    for (int r = blockIdx.x + gridDim.x * threadIdx.x; r < p.R; r += gridDim.x * kT2Threads) {  // each request once
+    // each request once
+    for (int r = blockIdx.x + gridDim.x * threadIdx.x; r < p.R; r += gridDim.x * kSlideThreads) {
         const int q0 = __ldg(p.query_start + r), q1 = __ldg(p.query_start + r + 1), m = q1 - q0;
         const int n = __ldg(p.context_lens + r);
         if (q0 < 0 || q1 > p.T || m < 0 || m > p.max_q) {
@@ -2055,199 +2065,204 @@ __global__ void __launch_bounds__(kT2Threads, 1)
     bool bad = false;  // a wait ran out
     auto stages = [](const SlideItem& it) { return (it.nblk + kT2Blocks - 1) / kT2Blocks; };
 
-    if (warp == kT2MmaWarp + 1) {
-        // ------------------------------------------------ producer warp --
-        const uint64_t policy = l2_policy_evict_normal();
-        int g = 0, begun = 0;
-        int pblk = -1, ph = 0;  // the stage before: its V comes behind this stage's K
-        bool pok = false, good = true;
-        auto load_v = [&](int gv) -> bool {
-            const int sl = gv & 1, u = gv >> 1;
-            if (!wait_all(v_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) return false;
-            const uint32_t msk = __ballot_sync(0xffffffffu, pok);
-            const uint32_t fb = v_full0 + sl * 8;
-            if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
-            __syncwarp();
-            if (pok) {
-                const uint32_t vd = sbase + SM::kRingV + sl * SM::kKV + lane * kH * kBlock * 128;
-                tma_load_3d(vd, &tmv, fb, 0, (pblk * p.Hkv + ph) * kBlock, 0, policy);
-            }
-            return true;
-        };
-        long long x = blockIdx.x;
-        for (int i = 0; good; x += gridDim.x) {
-            SlideItem it;
-            it.r = -1;
-            if (x < items) it = slide_item(p, sums, rows, x);
-            if (it.r >= 0 && it.nblk == 0) {
-                // every row before position 0: zeros, and nothing for the others to do
-                const int tokens = min(rows / p.G, it.m - it.tok0), words = p.G * HD / 8;
-                for (int k = lane; k < tokens * words; k += 32) {
-                    const long long row = (long long)(it.q0 + it.tok0 + k / words) * p.Hq + (long long)it.h * p.G;
-                    reinterpret_cast<uint4*>(p.out + row * HD)[k % words] = make_uint4(0, 0, 0, 0);
-                }
-                continue;
-            }
-            if (lane == 0) {
-                ring[i % kItems] = it;
-                mbar_arrive(item_full0 + (i % kItems) * 8);
-            }
-            ++i;
-            if (it.r < 0) break;
-            const int nst = stages(it);
-            // block-table entries are read a stage ahead, before the wait for the slot
-            auto table_entry = [&](int j) -> int {
-                const int y = j * kT2Blocks + lane;
-                return lane < kT2Blocks && y < it.nblk
-                           ? __ldg(p.block_tables + (long long)it.r * p.mbps + (y < it.head ? y : y + it.gap))
-                           : -1;
-            };
-            int blk_next = table_entry(0);
-            for (int j = 0; j < nst; ++j, ++g) {
-                const int sl = g % kT2KSlots, u = g / kT2KSlots, blk = blk_next;
-                if (j + 1 < nst) blk_next = table_entry(j + 1);
-                if (!(good = wait_all(k_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns))) break;
-                bool ok = false;
-                if (lane < kT2Blocks && j * kT2Blocks + lane < it.nblk) {
-                    ok = blk >= 0 && blk < p.num_blocks;
-                    if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
-                }
-                const uint32_t msk = __ballot_sync(0xffffffffu, ok);
-                const uint32_t fb = k_full0 + (g & 3) * 8;
-                // failure-detection test: the first K is neither copied nor
-                // announced, so every wait on it runs out
-                const bool held = p.withhold != 0 && g == 0;
-                if (lane == 0 && !held) {
-                    sts32(mask0 + (g & 3) * 4, msk);
-                    mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
-                }
+    if (warp >= kT2MmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSlideFewRegs));
+        if (warp == kT2MmaWarp + 1) {
+            // ------------------------------------------------ producer warp --
+            const uint64_t policy = l2_policy_evict_normal();
+            int g = 0, begun = 0;
+            int pblk = -1, ph = 0;  // the stage before: its V comes behind this stage's K
+            bool pok = false, good = true;
+            auto load_v = [&](int gv) -> bool {
+                const int sl = gv & 1, u = gv >> 1;
+                if (!wait_all(v_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns)) return false;
+                const uint32_t msk = __ballot_sync(0xffffffffu, pok);
+                const uint32_t fb = v_full0 + sl * 8;
+                if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
                 __syncwarp();
-                if (ok && !held) {
-                    const uint32_t kd = sbase + SM::kRingK + sl * SM::kKV + lane * kBlock * 128;
-                    const int row0 = (blk * p.Hkv + it.h) * kBlock;
-                    for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kT2Keys * 128, &tmk, fb, 0, hh, row0, policy);
+                if (pok) {
+                    const uint32_t vd = sbase + SM::kRingV + sl * SM::kKV + lane * kH * kBlock * 128;
+                    tma_load_3d(vd, &tmv, fb, 0, (pblk * p.Hkv + ph) * kBlock, 0, policy);
                 }
-                if (g > 0 && !(good = load_v(g - 1))) break;
-                pblk = blk;
-                pok = ok;
-                ph = it.h;
-                if (j == 0) {
-                    // Q, once the item before has no scores to compute any more
-                    if (!(good = wait_all(q_empty, (uint32_t)((begun & 1) ^ 1), p.wait_ns))) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(q_full, 2u * kH * (uint32_t)tr * 128u);
-                        for (int t = 0; t < 2; ++t)
-                            for (int hh = 0; hh < kH; ++hh)
-                                tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
-                                            it.q0 + it.tok0 + t * (tr / p.G), policy);
+                return true;
+            };
+            long long x = blockIdx.x;
+            for (int i = 0; good; x += gridDim.x) {
+                SlideItem it;
+                it.r = -1;
+                if (x < items) it = slide_item(p, sums, rows, x);
+                if (it.r >= 0 && it.nblk == 0) {
+                    // every row before position 0: zeros, and nothing for the others to do
+                    const int tokens = min(rows / p.G, it.m - it.tok0), words = p.G * HD / 8;
+                    for (int k = lane; k < tokens * words; k += 32) {
+                        const long long row = (long long)(it.q0 + it.tok0 + k / words) * p.Hq + (long long)it.h * p.G;
+                        reinterpret_cast<uint4*>(p.out + row * HD)[k % words] = make_uint4(0, 0, 0, 0);
+                    }
+                    continue;
+                }
+                if (lane == 0) {
+                    ring[i % kItems] = it;
+                    mbar_arrive(item_full0 + (i % kItems) * 8);
+                }
+                ++i;
+                if (it.r < 0) break;
+                const int nst = stages(it);
+                // block-table entries are read a stage ahead, before the wait for the slot
+                auto table_entry = [&](int j) -> int {
+                    const int y = j * kT2Blocks + lane;
+                    return lane < kT2Blocks && y < it.nblk
+                               ? __ldg(p.block_tables + (long long)it.r * p.mbps + (y < it.head ? y : y + it.gap))
+                               : -1;
+                };
+                int blk_next = table_entry(0);
+                for (int j = 0; j < nst; ++j, ++g) {
+                    const int sl = g % kT2KSlots, u = g / kT2KSlots, blk = blk_next;
+                    if (j + 1 < nst) blk_next = table_entry(j + 1);
+                    if (!(good = wait_all(k_empty0 + sl * 8, (uint32_t)((u & 1) ^ 1), p.wait_ns))) break;
+                    bool ok = false;
+                    if (lane < kT2Blocks && j * kT2Blocks + lane < it.nblk) {
+                        ok = blk >= 0 && blk < p.num_blocks;
+                        if (!ok) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+                    }
+                    const uint32_t msk = __ballot_sync(0xffffffffu, ok);
+                    const uint32_t fb = k_full0 + (g & 3) * 8;
+                    // failure-detection test: the first K is neither copied nor
+                    // announced, so every wait on it runs out
+                    const bool held = p.withhold != 0 && g == 0;
+                    if (lane == 0 && !held) {
+                        sts32(mask0 + (g & 3) * 4, msk);
+                        mbar_arrive_expect_tx(fb, (uint32_t)__popc(msk) * kH * kBlock * 128u);
                     }
                     __syncwarp();
-                    ++begun;
+                    if (ok && !held) {
+                        const uint32_t kd = sbase + SM::kRingK + sl * SM::kKV + lane * kBlock * 128;
+                        const int row0 = (blk * p.Hkv + it.h) * kBlock;
+                        for (int hh = 0; hh < kH; ++hh) tma_load_3d(kd + hh * kT2Keys * 128, &tmk, fb, 0, hh, row0, policy);
+                    }
+                    if (g > 0 && !(good = load_v(g - 1))) break;
+                    pblk = blk;
+                    pok = ok;
+                    ph = it.h;
+                    if (j == 0) {
+                        // Q, once the item before has no scores to compute any more
+                        if (!(good = wait_all(q_empty, (uint32_t)((begun & 1) ^ 1), p.wait_ns))) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(q_full, 2u * kH * (uint32_t)tr * 128u);
+                            for (int t = 0; t < 2; ++t)
+                                for (int hh = 0; hh < kH; ++hh)
+                                    tma_load_4d(sbase + SM::kQ + t * SM::kQT + hh * kTcRows * 128, &tmq, q_full, 0, hh, it.h * p.G,
+                                                it.q0 + it.tok0 + t * (tr / p.G), policy);
+                        }
+                        __syncwarp();
+                        ++begun;
+                    }
                 }
             }
-        }
-        if (good && g > 0) good = load_v(g - 1);
-        bad = !good;
-    } else if (warp == kT2MmaWarp) {
-        // -------------------------------------------------- MMA issuer --
-        constexpr uint32_t idS = tc::idesc_bf16(kTcRows, kT2Keys, false);
-        constexpr uint32_t idO = tc::idesc_bf16(kTcRows, HD, true);
-        auto issue_s = [&](int t, int g) {
-            const uint32_t kbase = sbase + SM::kRingK + (g % kT2KSlots) * SM::kKV;
-            const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
+            if (good && g > 0) good = load_v(g - 1);
+            bad = !good;
+        } else if (warp == kT2MmaWarp) {
+            // -------------------------------------------------- MMA issuer --
+            constexpr uint32_t idS = tc::idesc_bf16(kTcRows, kT2Keys, false);
+            constexpr uint32_t idO = tc::idesc_bf16(kTcRows, HD, true);
+            auto issue_s = [&](int t, int g) {
+                const uint32_t kbase = sbase + SM::kRingK + (g % kT2KSlots) * SM::kKV;
+                const uint32_t qbase = sbase + SM::kQ + t * SM::kQT;
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
-                const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
-                const uint64_t bd = tc::sdesc_sw128(kbase + (kk >> 2) * kT2Keys * 128 + off, 16, 1024);
-                tc::mma_ss_elect(tbase + 256u * t + 128u, a, bd, idS, kk > 0);
-            }
-            tc::commit_elect(s_full0 + t * 8);
-        };
-        auto issue_o = [&](int t, int g, bool first) {
-            const uint32_t vbase = sbase + SM::kRingV + (g & 1) * SM::kKV;
-            const uint32_t pcol = tbase + 256u * t + 128u;  // P_t: bf16 pairs over S_t's first 64 columns
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t off = (kk & 3) * 32;  // 16 bf16 of the 128-byte row
+                    const uint64_t a = tc::sdesc_sw128(qbase + (kk >> 2) * kTcRows * 128 + off, 16, 1024);
+                    const uint64_t bd = tc::sdesc_sw128(kbase + (kk >> 2) * kT2Keys * 128 + off, 16, 1024);
+                    tc::mma_ss_elect(tbase + 256u * t + 128u, a, bd, idS, kk > 0);
+                }
+                tc::commit_elect(s_full0 + t * 8);
+            };
+            auto issue_o = [&](int t, int g, bool first) {
+                const uint32_t vbase = sbase + SM::kRingV + (g & 1) * SM::kKV;
+                const uint32_t pcol = tbase + 256u * t + 128u;  // P_t: bf16 pairs over S_t's first 64 columns
 #pragma unroll
-            for (int l = 0; l < kT2Blocks; ++l) {
-                const uint64_t bd = tc::sdesc_sw128(vbase + l * kH * kBlock * 128, kBlock * 128, 1024);
-                tc::mma_ts_elect(tbase + 256u * t, pcol + 8u * l, bd, idO, !first || l > 0);
-            }
-            tc::commit_elect(o_done0 + t * 8);
-        };
-        // the next item's stages, or 0
-        int found = 0;
-        bool ok = true;
-        auto next_item = [&]() -> int {
-            if (!(ok = wait_all(item_full0 + (found % kItems) * 8, (uint32_t)((found / kItems) & 1), p.wait_ns))) return 0;
-            const SlideItem& it = ring[found % kItems];
-            ++found;
-            return it.r < 0 ? 0 : stages(it);
-        };
-        // whether Q and K of stage g, an item's first, have landed (without a wait: now)
-        int g = 0, begun = 0;
-        auto landed = [&](int gn, bool now) -> bool {
-            const uint32_t kb = k_full0 + (gn & 3) * 8, kp = (uint32_t)((gn >> 2) & 1), qp = (uint32_t)(begun & 1);
-            if (now) return __all_sync(0xffffffffu, mbar_try_wait(q_full, qp) && mbar_try_wait(kb, kp));
-            return wait_all(q_full, qp, p.wait_ns) && wait_all(kb, kp, p.wait_ns);
-        };
-        // An item's stages; behind its last P . V of a tile come the first scores of
-        // the next item, whose rows' softmax then need not wait for the other tile.
-        int nst = next_item();
-        if (nst > 0 && (ok = landed(0, false))) {
-            ++begun;
-            tc::fence_after();
-            issue_s(0, 0);
-            issue_s(1, 0);
-            tc::commit_elect(k_empty0);
-            if (nst == 1) tc::commit_elect(q_empty);
-        }
-        while (ok && nst > 0) {
-            int after = 0;  // the next item's stages
-            for (int j = 0; j < nst; ++j, ++g) {
-                const uint32_t ph = (uint32_t)(g & 1);
-                if (!(ok = wait_all(p_full0, ph, p.wait_ns) && wait_all(v_full0 + (g & 1) * 8, (uint32_t)((g >> 1) & 1), p.wait_ns)))
-                    break;
+                for (int l = 0; l < kT2Blocks; ++l) {
+                    const uint64_t bd = tc::sdesc_sw128(vbase + l * kH * kBlock * 128, kBlock * 128, 1024);
+                    tc::mma_ts_elect(tbase + 256u * t, pcol + 8u * l, bd, idO, !first || l > 0);
+                }
+                tc::commit_elect(o_done0 + t * 8);
+            };
+            // the next item's stages, or 0
+            int found = 0;
+            bool ok = true;
+            auto next_item = [&]() -> int {
+                if (!(ok = wait_all(item_full0 + (found % kItems) * 8, (uint32_t)((found / kItems) & 1), p.wait_ns))) return 0;
+                const SlideItem& it = ring[found % kItems];
+                ++found;
+                return it.r < 0 ? 0 : stages(it);
+            };
+            // whether Q and K of stage g, an item's first, have landed (without a wait: now)
+            int g = 0, begun = 0;
+            auto landed = [&](int gn, bool now) -> bool {
+                const uint32_t kb = k_full0 + (gn & 3) * 8, kp = (uint32_t)((gn >> 2) & 1), qp = (uint32_t)(begun & 1);
+                if (now) return __all_sync(0xffffffffu, mbar_try_wait(q_full, qp) && mbar_try_wait(kb, kp));
+                return wait_all(q_full, qp, p.wait_ns) && wait_all(kb, kp, p.wait_ns);
+            };
+            // An item's stages; behind its last P . V of a tile come the first scores of
+            // the next item, whose rows' softmax then need not wait for the other tile.
+            int nst = next_item();
+            if (nst > 0 && (ok = landed(0, false))) {
+                ++begun;
                 tc::fence_after();
-                issue_o(0, g, j == 0);
-                const bool last = j + 1 == nst;
-                bool first_tile = false, more = !last;
-                if (!last) {
-                    if (!(ok = wait_all(k_full0 + ((g + 1) & 3) * 8, (uint32_t)(((g + 1) >> 2) & 1), p.wait_ns))) break;
-                    first_tile = true;
-                } else {
-                    after = next_item();
-                    if (!ok) break;
-                    more = after > 0;
-                    first_tile = more && landed(g + 1, true);
-                }
-                if (first_tile) {
-                    tc::fence_after();
-                    issue_s(0, g + 1);
-                }
-                if (!(ok = wait_all(p_full0 + 8, ph, p.wait_ns))) break;
-                tc::fence_after();
-                issue_o(1, g, j == 0);
-                tc::commit_elect(v_empty0 + (g & 1) * 8);  // V read by both tiles
-                if (!more) continue;
-                if (!first_tile) {
-                    if (!(ok = landed(g + 1, false))) break;
-                    tc::fence_after();
-                    issue_s(0, g + 1);
-                }
-                issue_s(1, g + 1);
-                tc::commit_elect(k_empty0 + ((g + 1) % kT2KSlots) * 8);
-                if (last) ++begun;
-                if (last ? after == 1 : j + 2 == nst) tc::commit_elect(q_empty);  // an item's last scores
+                issue_s(0, 0);
+                issue_s(1, 0);
+                tc::commit_elect(k_empty0);
+                if (nst == 1) tc::commit_elect(q_empty);
             }
-            nst = after;
+            while (ok && nst > 0) {
+                int after = 0;  // the next item's stages
+                for (int j = 0; j < nst; ++j, ++g) {
+                    const uint32_t ph = (uint32_t)(g & 1);
+                    if (!(ok = wait_all(p_full0, ph, p.wait_ns) &&
+                               wait_all(v_full0 + (g & 1) * 8, (uint32_t)((g >> 1) & 1), p.wait_ns)))
+                        break;
+                    tc::fence_after();
+                    issue_o(0, g, j == 0);
+                    const bool last = j + 1 == nst;
+                    bool first_tile = false, more = !last;
+                    if (!last) {
+                        if (!(ok = wait_all(k_full0 + ((g + 1) & 3) * 8, (uint32_t)(((g + 1) >> 2) & 1), p.wait_ns))) break;
+                        first_tile = true;
+                    } else {
+                        after = next_item();
+                        if (!ok) break;
+                        more = after > 0;
+                        first_tile = more && landed(g + 1, true);
+                    }
+                    if (first_tile) {
+                        tc::fence_after();
+                        issue_s(0, g + 1);
+                    }
+                    if (!(ok = wait_all(p_full0 + 8, ph, p.wait_ns))) break;
+                    tc::fence_after();
+                    issue_o(1, g, j == 0);
+                    tc::commit_elect(v_empty0 + (g & 1) * 8);  // V read by both tiles
+                    if (!more) continue;
+                    if (!first_tile) {
+                        if (!(ok = landed(g + 1, false))) break;
+                        tc::fence_after();
+                        issue_s(0, g + 1);
+                    }
+                    issue_s(1, g + 1);
+                    tc::commit_elect(k_empty0 + ((g + 1) % kT2KSlots) * 8);
+                    if (last) ++begun;
+                    if (last ? after == 1 : j + 2 == nst) tc::commit_elect(q_empty);  // an item's last scores
+                }
+                nst = after;
+            }
+            bad = !ok;
+            // every MMA issued has finished before tensor memory is released
+            tc::commit_elect(fin);
+            (void)wait_all(fin, 0, drain_limit(p.wait_ns));
+            __syncwarp();
         }
-        bad = !ok;
-        // every MMA issued has finished before tensor memory is released
-        tc::commit_elect(fin);
-        (void)wait_all(fin, 0, drain_limit(p.wait_ns));
-        __syncwarp();
     } else {
         // ---------------------------------------------------- softmax ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSlideManyRegs));
         // Lanes and rows as in prefill_tc2_kernel: a quad of lanes has rows a and b of
         // its tile, a lane the keys 8k + 2 (i mod 4) and the next one of each group.
         const int t = (warp >> 2) & 1;  // tile
@@ -2452,7 +2467,14 @@ template <int HD>
 bool prepare_slide() {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    return raise_smem_once(reinterpret_cast<const void*>(slide_tc2_kernel<HD>), SlideSmem<HD>::kTotal, done, mu);
+    // registers that the launch does not have would be waited for without end
+    static const bool enough = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(slide_tc2_kernel<HD>)) == cudaSuccess &&
+               a.numRegs == kSlideRegs;
+    }();
+    return enough &&
+           raise_smem_once(reinterpret_cast<const void*>(slide_tc2_kernel<HD>), SlideSmem<HD>::kTotal, done, mu);
 }
 
 template <int HD>
@@ -2547,8 +2569,8 @@ mi_status prefill(const mi_dims* dims, int32_t total_q, int32_t max_query_len, c
         // one block per SM, which takes items in turn; no more blocks than items
         const long long most = ((long long)total_q * G / rows_per_tile + D.B) * D.Hkv;
         const int blocks = (int)(most < sms ? most : sms);
-        e = HD == 64 ? launch_pdl(slide_tc2_kernel<64>, blocks, kT2Threads, SlideSmem<64>::kTotal, st, tq, tk, tv, sp)
-                     : launch_pdl(slide_tc2_kernel<128>, blocks, kT2Threads, SlideSmem<128>::kTotal, st, tq, tk, tv, sp);
+        e = HD == 64 ? launch_pdl(slide_tc2_kernel<64>, blocks, kSlideThreads, SlideSmem<64>::kTotal, st, tq, tk, tv, sp)
+                     : launch_pdl(slide_tc2_kernel<128>, blocks, kSlideThreads, SlideSmem<128>::kTotal, st, tq, tk, tv, sp);
     } else if (use_tc2) {
         if (!(HD == 64 ? prepare_tc2<64>() : prepare_tc2<128>())) return MI_ERR_CUDA;
         CUtensorMap tq, tk, tv;

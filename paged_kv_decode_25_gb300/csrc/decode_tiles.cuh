@@ -358,6 +358,90 @@ struct Fp8State {
         }
     }
 
+    // Two blocks at once, the second's tiles `next` bytes behind the first's; seen(t):
+    // token t of the 32. One maximum and one rescaling for both, and twice as many
+    // products that do not depend on one another.
+    template <class Seen>
+    __device__ __forceinline__ void pair(uint32_t kt, uint32_t vt, uint32_t next, Seen seen, int lane) {
+        float s[2][4];
+        {
+            const int mi = lane >> 3;
+            const int tok = (lane & 7) + (mi & 1) * 8;
+            float c[2][4] = {}, c1[2][4] = {};
+#pragma unroll
+            for (int kp = 0; kp < kK / 2; ++kp) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t r0, r1, r2, r3;
+                    ldsm_x4(kt + x * next + swz8<HD>(tok, 2 * kp + (mi >> 1)), r0, r1, r2, r3);
+                    mma_f16_16816(c[x], e4m3x2_to_f16x2(r0), e4m3x2_to_f16x2(r1), e4m3x2_to_f16x2(r0 >> 16),
+                                  e4m3x2_to_f16x2(r1 >> 16), qb[2 * kp][0], qb[2 * kp][1]);
+                    mma_f16_16816(c1[x], e4m3x2_to_f16x2(r2), e4m3x2_to_f16x2(r3), e4m3x2_to_f16x2(r2 >> 16),
+                                  e4m3x2_to_f16x2(r3 >> 16), qb[2 * kp + 1][0], qb[2 * kp + 1][1]);
+                }
+            }
+            const int t0 = lane >> 2;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[x][i] = seen(16 * x + t0 + 8 * (i >> 1)) ? (c[x][i] + c1[x][i]) * sl2 : kNegInf;
+        }
+        float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+        float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+        }
+        const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
+        const float r0 = mn0 == kNegInf ? 0.f : mn0, r1 = mn1 == kNegInf ? 0.f : mn1;
+        const float al0 = ex2(m[0] - r0), al1 = ex2(m[1] - r1);
+        m[0] = mn0;
+        m[1] = mn1;
+        uint32_t b[2][2];
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t x0 = pack_f16x2(ex2(s[x][0] - r0), ex2(s[x][1] - r1));
+            const uint32_t x1 = pack_f16x2(ex2(s[x][2] - r0), ex2(s[x][3] - r1));
+            l0 += f16_lo(x0) + f16_lo(x1);
+            l1 += f16_hi(x0) + f16_hi(x1);
+            b[x][0] = movmatrix_trans(x0);
+            b[x][1] = movmatrix_trans(x1);
+        }
+        l[0] = l[0] * al0 + l0;
+        l[1] = l[1] * al1 + l1;
+        if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+#pragma unroll
+            for (int mt = 0; mt < kK; ++mt) {
+                o[mt][0] *= al0;
+                o[mt][1] *= al1;
+                o[mt][2] *= al0;
+                o[mt][3] *= al1;
+            }
+        }
+        const int g = lane >> 2, cc = lane & 3;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t v = vt + x * next;
+#pragma unroll
+            for (int t = 0; t < kK / 2; ++t) {
+                const int chunk = 2 * t + (g >> 2), inb = (g & 3) * 4;
+                const uint32_t w0 = lds32(v + swz8<HD>(2 * cc, chunk) + inb);
+                const uint32_t w1 = lds32(v + swz8<HD>(2 * cc + 1, chunk) + inb);
+                const uint32_t w2 = lds32(v + swz8<HD>(2 * cc + 8, chunk) + inb);
+                const uint32_t w3 = lds32(v + swz8<HD>(2 * cc + 9, chunk) + inb);
+                const uint32_t lo01 = __byte_perm(w0, w1, 0x5140), hi01 = __byte_perm(w0, w1, 0x7362);
+                const uint32_t lo89 = __byte_perm(w2, w3, 0x5140), hi89 = __byte_perm(w2, w3, 0x7362);
+                mma_f16_16816(o[2 * t], e4m3x2_to_f16x2(lo01), e4m3x2_to_f16x2(lo01 >> 16), e4m3x2_to_f16x2(lo89),
+                              e4m3x2_to_f16x2(lo89 >> 16), b[x][0], b[x][1]);
+                mma_f16_16816(o[2 * t + 1], e4m3x2_to_f16x2(hi01), e4m3x2_to_f16x2(hi01 >> 16),
+                              e4m3x2_to_f16x2(hi89), e4m3x2_to_f16x2(hi89 >> 16), b[x][0], b[x][1]);
+            }
+        }
+    }
+
     // The warp's sums in every lane; then each() hands out this lane's outputs, not
     // yet divided by the sums: f(0 or 1 (head 2 (lane & 3) or the next), first
     // dim, kRun consecutive values).
@@ -565,6 +649,113 @@ struct Int8State {
                               i8x2_to_f16x2_biased(lo89, kLo), i8x2_to_f16x2_biased(lo89, kHi), b0, b1);
                 mma_f16_16816(o[2 * t + 1], i8x2_to_f16x2_biased(hi01, kLo), i8x2_to_f16x2_biased(hi01, kHi),
                               i8x2_to_f16x2_biased(hi89, kLo), i8x2_to_f16x2_biased(hi89, kHi), b0, b1);
+            }
+        }
+    }
+
+    // Two blocks at once, as Fp8State::pair; each with its own factors (av 0 where a
+    // block is absent: none of its tokens is seen).
+    template <class Seen>
+    __device__ __forceinline__ void pair(uint32_t kt, uint32_t vt, uint32_t next, Seen seen, int lane, float ak0, float ak1,
+                                         float av0, float av1) {
+        float s[2][4];
+        {
+            const int mi = lane >> 3;
+            const int tok = (lane & 7) + (mi & 1) * 8;
+            float c[2][4] = {}, c1[2][4] = {};
+#pragma unroll
+            for (int kp = 0; kp < kK / 2; ++kp) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t r0, r1, r2, r3;
+                    ldsm_x4(kt + x * next + swz8<HD>(tok, 2 * kp + (mi >> 1)), r0, r1, r2, r3);
+                    r0 ^= kFlip;
+                    r1 ^= kFlip;
+                    r2 ^= kFlip;
+                    r3 ^= kFlip;
+                    mma_f16_16816(c[x], i8x2_to_f16x2_biased(r0, kLo), i8x2_to_f16x2_biased(r1, kLo),
+                                  i8x2_to_f16x2_biased(r0, kHi), i8x2_to_f16x2_biased(r1, kHi), qb[2 * kp][0],
+                                  qb[2 * kp][1]);
+                    mma_f16_16816(c1[x], i8x2_to_f16x2_biased(r2, kLo), i8x2_to_f16x2_biased(r3, kLo),
+                                  i8x2_to_f16x2_biased(r2, kHi), i8x2_to_f16x2_biased(r3, kHi), qb[2 * kp + 1][0],
+                                  qb[2 * kp + 1][1]);
+                }
+            }
+            const int t0 = lane >> 2;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float ks = sl2 * (x ? ak1 : ak0);  // scale * log2(e) * a_k / 127
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[x][i] = seen(16 * x + t0 + 8 * (i >> 1)) ? fmaf(c[x][i] + c1[x][i], ks, -(ks * koff[i & 1])) : kNegInf;
+            }
+        }
+        float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+        float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+        }
+        const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
+        const float r0 = mn0 == kNegInf ? 0.f : mn0, r1 = mn1 == kNegInf ? 0.f : mn1;
+        const float al0 = ex2(m[0] - r0), al1 = ex2(m[1] - r1);
+        m[0] = mn0;
+        m[1] = mn1;
+        // the larger of the blocks' V factors moves the reference (the same for every lane)
+        const float fv = fmaxf(av0, av1) * (1.f / 127.f);
+        float ov0 = al0, ov1 = al1;  // O's factors for these blocks
+        if (fv > vref * 256.f) {
+            const float f = vref * (1.f / fv);  // 0 for the first nonzero factor (O is still 0)
+            ov0 *= f;
+            ov1 *= f;
+            vref = fv;
+            rvref = 1.f / fv;
+        }
+        uint32_t b[2][2];
+        float l0 = 0.f, l1 = 0.f, sp0 = 0.f, sp1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float p0 = ex2(s[x][0] - r0), p1 = ex2(s[x][1] - r1), p2 = ex2(s[x][2] - r0), p3 = ex2(s[x][3] - r1);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            const float rel = (x ? av1 : av0) * (1.f / 127.f) * rvref;
+            const uint32_t x0 = pack_f16x2(p0 * rel, p1 * rel), x1 = pack_f16x2(p2 * rel, p3 * rel);
+            sp0 += f16_lo(x0) + f16_lo(x1);
+            sp1 += f16_hi(x0) + f16_hi(x1);
+            b[x][0] = movmatrix_trans(x0);
+            b[x][1] = movmatrix_trans(x1);
+        }
+        l[0] = l[0] * al0 + l0;
+        l[1] = l[1] * al1 + l1;
+        sp[0] = sp[0] * ov0 + sp0;
+        sp[1] = sp[1] * ov1 + sp1;
+        if (__any_sync(0xffffffffu, ov0 != 1.f || ov1 != 1.f)) {
+#pragma unroll
+            for (int mt = 0; mt < kK; ++mt) {
+                o[mt][0] *= ov0;
+                o[mt][1] *= ov1;
+                o[mt][2] *= ov0;
+                o[mt][3] *= ov1;
+            }
+        }
+        const int g = lane >> 2, cc = lane & 3;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t v = vt + x * next;
+#pragma unroll
+            for (int t = 0; t < kK / 2; ++t) {
+                const int chunk = 2 * t + (g >> 2), inb = (g & 3) * 4;
+                const uint32_t w0 = lds32(v + swz8<HD>(2 * cc, chunk) + inb);
+                const uint32_t w1 = lds32(v + swz8<HD>(2 * cc + 1, chunk) + inb);
+                const uint32_t w2 = lds32(v + swz8<HD>(2 * cc + 8, chunk) + inb);
+                const uint32_t w3 = lds32(v + swz8<HD>(2 * cc + 9, chunk) + inb);
+                const uint32_t lo01 = __byte_perm(w0, w1, 0x5140) ^ kFlip, hi01 = __byte_perm(w0, w1, 0x7362) ^ kFlip;
+                const uint32_t lo89 = __byte_perm(w2, w3, 0x5140) ^ kFlip, hi89 = __byte_perm(w2, w3, 0x7362) ^ kFlip;
+                mma_f16_16816(o[2 * t], i8x2_to_f16x2_biased(lo01, kLo), i8x2_to_f16x2_biased(lo01, kHi),
+                              i8x2_to_f16x2_biased(lo89, kLo), i8x2_to_f16x2_biased(lo89, kHi), b[x][0], b[x][1]);
+                mma_f16_16816(o[2 * t + 1], i8x2_to_f16x2_biased(hi01, kLo), i8x2_to_f16x2_biased(hi01, kHi),
+                              i8x2_to_f16x2_biased(hi89, kLo), i8x2_to_f16x2_biased(hi89, kHi), b[x][0], b[x][1]);
             }
         }
     }

@@ -15,11 +15,12 @@
 // log-sum-exps. (A second launch for that cost 5 us a call more.)
 //
 // Measured, bytes in sight over the whole call: 64 requests behind windows of 1,024
-// (32/8 heads of 128, bf16) 49 us, 5.0 TB/s, of which the stream itself runs at 7 between
+// (32/8 heads of 128, bf16) 48 us, 5.1 TB/s, of which the stream itself runs at 7 between
 // 6 us of plan and first copies and 4 to 5 of last pieces; 128 behind 4,096 (28/4, e4m3)
-// 98 us, 5.3 TB/s, and 256 behind 128 (16/8, INT8) 28 us, 2.2 TB/s: an SM takes 0.1 us
-// for a one-byte block (its conversions) whatever its number of warps; a single request
-// 12 us, latency from end to end.
+// 93 us, 5.6 TB/s, and 256 behind 128 (16/8, INT8) 24 us, 2.5 TB/s: there no pipe is busy
+// above 40 % (issue 37, integer 36, tensor 13), the warps wait for their own results. So
+// one-byte blocks go two to a stage: 97 us with one. A single request takes 12 us, latency
+// from end to end.
 #include <atomic>
 #include <chrono>
 #include <cmath>
@@ -43,17 +44,23 @@ constexpr int kSlideBlocks = 3;
 template <int HD, int VAR>
 struct SlideShape {
     static constexpr int kTile = Tile<HD, elem_bytes(VAR)>::kBytes;
-    static constexpr int kStages = 16384 / (2 * kTile) < 4 ? 16384 / (2 * kTile) : 4;
-    static constexpr int kSmem = kSlideWarps * kStages * 2 * kTile + 1024;  // slack to align the tiles
+    // blocks of a stage: what surrounds a tile (waiting, masks, the next copies, the
+    // running maximum) is half of a one-byte block's instructions
+    static constexpr int kBlocks = elem_bytes(VAR) == 1 ? 2 : 1;
+    static constexpr int kStage = kBlocks * 2 * kTile;
+    static constexpr int kStages = 16384 / kStage < 4 ? 16384 / kStage : 4;
+    static constexpr int kSmem = kSlideWarps * kStages * kStage + 1024;  // slack to align the tiles
 };
 
 // Pieces that have partial results, at most, per warp of the grid.
 constexpr int kSplitPerWarp = 8;
 // In a warp's block times: a piece's own cost (its queries, its output), that of a
-// split unit's end, and of adding up 512 outputs of a piece there. (Fitted to sweeps of
-// forced plans; several rounds of pieces lose to one round, 2.2 us a piece: results and
+// split unit's end, and of adding up 512 outputs of a piece there. Fitted, with
+// SlideParams::alone, to 15 shapes (1 to 256 requests, windows of 128 to 4,096, the three
+// types) cut into 1 to 24 pieces: the plan's choice is within 0.9 % of the best one on
+// average. (More rounds of shorter pieces lose to one round: each costs its results and
 // counts, and the additions fall to the blocks that end last.)
-constexpr float kPieceCost = 12.f, kSplitCost = 3.f, kMergeCost = 0.5f;
+constexpr float kPieceCost = 16.f, kSplitCost = 1.f, kMergeCost = 0.1f;
 
 // Piece i of the np of (request b, head h): blocks in sight j .. j1 - 1; `slot`: the
 // unit's first partial result. b < 0: no more pieces.
@@ -82,6 +89,7 @@ struct SlideParams {
     int B, Hq, Hkv, G, num_blocks, mbps, window, sinks, most, slot_floats;
     float sl2;                     // scale * log2(e)
     float flow;                    // a block's time at full memory rate over its time in a warp, times all warps
+    float alone;                   // a warp's share of that time which others on its SM do not lengthen
     long long wait_ns;
     int withhold;                  // failure-detection test: each warp withholds its first copy
 };
@@ -114,7 +122,8 @@ __device__ Cut cut_units(const SlideParams& p, float warps, float blocks, float 
     const float rounds = __fdividef(fmaxf(units * (most * fill + 0.5f * (1.f - fill)), units), warps);
     const float whole = floorf(rounds), over = rounds - whole;
     float tail_step = step, part = 1.f;  // part: of the requests, before b0
-    float cost = fmaxf(all, ceilf(rounds) * (step + kPieceCost)) + end_cost(most);
+    const float last = over > 0.f ? p.alone + (1.f - p.alone) * over : 0.f;
+    float cost = fmaxf(all, (whole + last) * (step + kPieceCost)) + end_cost(most);
     if (whole > 0.f && over > 0.01f) {
         const float tail_np = fminf(16.f, __fdividef(most * fill, over));  // so that they fill a round
         const float s = fminf(step, fmaxf(least, ceilf(__fdividef(big, fmaxf(1.f, tail_np)))));
@@ -240,10 +249,11 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     slide_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const SlideParams p) {
     using Shape = SlideShape<HD, VAR>;
     constexpr int S = Shape::kStages, kTile = Shape::kTile, kThreads = kSlideWarps * 32;
+    constexpr int kBlocks = Shape::kBlocks, kStage = Shape::kStage;
     constexpr bool kInt8 = VAR == kVarInt8, kFp8 = VAR == kVarFp8;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) unsigned long long bars[kSlideWarps * S];
-    __shared__ float maxima[kInt8 ? kSlideWarps * S * 2 : 1];  // of a stage's block: K's, V's
+    __shared__ float maxima[kInt8 ? kSlideWarps * S * 2 * kBlocks : 1];  // of a stage's blocks: K's, V's
     // usual batches: blocks in sight, pieces before, those of split units; larger ones: chunks' sums
     __shared__ union {
         struct {
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     __shared__ int red_ends[2][kSlideWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t full = smem_u32(bars) + warp * S * 8;
-    const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + (uint32_t)(warp * S * 2 * kTile);
+    const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + (uint32_t)(warp * S * kStage);
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(full + 8 * i, kInt8 ? 2 : 1);  // the tiles; the maxima
         fence_mbar_init();
@@ -439,35 +449,50 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     const uint64_t policy = l2_policy_evict_first();
     find();
     advance();
-    uint32_t copied = 0, phase = 0;  // bit i: stage i holds a block, or will; its parity
+    uint32_t copied = 0, phase = 0;  // bits kBlocks i ..: stage i's blocks that it holds, or will; bit i: its parity
     bool withhold = p.withhold != 0;
     auto issue = [&](uint32_t st) {
         if (in_b < 0) return;
-        const int blk = __shfl_sync(0xffffffffu, entry, ahead);
-        const bool ok = blk >= 0 && blk < p.num_blocks;
+        const int n = kBlocks == 1 ? 1 : min(kBlocks, in_j1 - in_j);
+        uint32_t have = 0;
+        int blk[kBlocks];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+            blk[i] = __shfl_sync(0xffffffffu, entry, ahead + i);  // (`ahead` a multiple of kBlocks)
+            if (i < n && blk[i] >= 0 && blk[i] < p.num_blocks) have |= 1u << i;
+        }
         if (lane == 0) {
-            if (!ok) {
-                raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
-            } else if (!withhold) {
-                const uint32_t bar = full + 8 * st, dst = ring + st * 2 * kTile;
-                const int y = (blk * p.Hkv + in_h) * (kTile / 128);
-                mbar_arrive_expect_tx(bar, 2 * kTile);
-                tma_load_2d(dst, &tmk, bar, 0, y, policy);
-                tma_load_2d(dst + kTile, &tmv, bar, 0, y, policy);
+            if (have != (1u << n) - 1u) raise_err(p.dev_err, MI_DEVERR_BAD_BLOCK);
+            if (have && !withhold) {
+                const uint32_t bar = full + 8 * st;
+                mbar_arrive_expect_tx(bar, (uint32_t)__popc(have) * 2 * kTile);
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+                    if (!((have >> i) & 1u)) continue;
+                    const uint32_t dst = ring + st * kStage + i * 2 * kTile;
+                    const int y = (blk[i] * p.Hkv + in_h) * (kTile / 128);
+                    tma_load_2d(dst, &tmk, bar, 0, y, policy);
+                    tma_load_2d(dst + kTile, &tmv, bar, 0, y, policy);
+                }
                 if constexpr (kInt8) {
-                    // the block's maxima arrive on the same barrier
-                    const uint32_t at = smem_u32(maxima + (warp * S + st) * 2);
-                    const long long e = (long long)blk * p.Hkv + in_h;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(p.k_amax + e) : "memory");
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 4), "l"(p.v_amax + e) : "memory");
+                    // the blocks' maxima arrive on the same barrier
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i) {
+                        if (!((have >> i) & 1u)) continue;
+                        const uint32_t at = smem_u32(maxima + ((warp * S + st) * kBlocks + i) * 2);
+                        const long long e = (long long)blk[i] * p.Hkv + in_h;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(p.k_amax + e) : "memory");
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 4), "l"(p.v_amax + e) : "memory");
+                    }
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
                 }
             }
         }
         withhold = false;
-        if (ok) copied |= 1u << st;
-        ++ahead;
-        if (++in_j == in_j1) {
+        copied |= have << (kBlocks * st);
+        ahead += n;
+        in_j += n;
+        if (in_j == in_j1) {
             advance();
         } else if (ahead == 32) {
             ahead = 0;
@@ -492,29 +517,38 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
         st.begin_unit(p, c.b, c.h, lane);
         if (c.np > 1 && c.i == 0 && lane == 0) open_count(p.words + c.slot, p.tag);
         const int j1 = c.j1;
-        for (int j = c.j; j < j1; ++j) {
-            if ((copied >> sg) & 1u) {
+        for (int j = c.j; j < j1; j += kBlocks) {
+            const uint32_t have = (copied >> (kBlocks * sg)) & ((1u << kBlocks) - 1u);
+            if (have) {
                 if (!wait_warp(full + 8 * sg, (phase >> sg) & 1u, p.wait_ns)) {
                     if (lane == 0) raise_err(p.dev_err, MI_DEVERR_TIMEOUT);
                     dead = true;
                     break;
                 }
                 phase ^= 1u << sg;
-                copied &= ~(1u << sg);
-                const uint32_t kt = ring + sg * 2 * kTile, vt = kt + kTile;
-                const uint32_t seen = sight.mask(sight.column(j));
-                if (!kInt8 && seen != 0xFFFFu) {
+                copied &= ~(have << (kBlocks * sg));
+                const uint32_t kt = ring + sg * kStage, vt = kt + kTile;
+                uint32_t seen = 0;
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i)
+                    if ((have >> i) & 1u) seen |= sight.mask(sight.column(j + i)) << (kBlock * i);
+                if (!kInt8 && seen != (kBlocks == 2 ? 0xFFFFFFFFu : 0xFFFFu)) {
                     // rows out of sight may hold any bits: zero V there (INT8 codes are always finite)
                     constexpr int kChunks = HD * elem_bytes(VAR) / 16;
-                    for (int i = lane; i < kBlock * kChunks; i += 32) {
-                        const int row = i / kChunks, ch = i % kChunks;
-                        if (!((seen >> row) & 1u)) st_shared_zero16(vt + (kFp8 ? swz8<HD>(row, ch) : swz<HD>(row, ch)));
+                    for (int i = lane; i < kBlocks * kBlock * kChunks; i += 32) {
+                        const int at = i / kChunks, row = at % kBlock, ch = i % kChunks;
+                        const uint32_t tile = vt + at / kBlock * 2 * kTile;
+                        if (!((seen >> at) & 1u)) st_shared_zero16(tile + (kFp8 ? swz8<HD>(row, ch) : swz<HD>(row, ch)));
                     }
                     __syncwarp();
                 }
                 if constexpr (kInt8) {
-                    const float* m = maxima + (warp * S + sg) * 2;
-                    st.block(kt, vt, TokenMask{seen}, lane, m[0], m[1]);
+                    const float* m = maxima + (warp * S + sg) * kBlocks * 2;
+                    // (an absent block's maxima are an earlier one's)
+                    st.pair(kt, vt, 2 * kTile, TokenMask{seen}, lane, have & 1u ? m[0] : 0.f, have & 2u ? m[2] : 0.f,
+                            have & 1u ? m[1] : 0.f, have & 2u ? m[3] : 0.f);
+                } else if constexpr (kFp8) {
+                    st.pair(kt, vt, 2 * kTile, TokenMask{seen}, lane);
                 } else {
                     st.block(kt, vt, TokenMask{seen}, p.sl2, lane);
                 }
@@ -570,7 +604,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     }
     if (dead && lane == 0)  // the copies in flight land first
         for (int i = 0; i < S; ++i)
-            if ((copied >> i) & 1u) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
+            if ((copied >> (kBlocks * i)) & ((1u << kBlocks) - 1u)) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
     if (even0 == 1 && even1 == 1) return;  // no unit is split
     // All of the block's warps add up what they owe. (One warp a unit took 12 us for two
     // units of 7 pieces and 7 heads. Counting all pieces only here left most units to
@@ -693,8 +727,12 @@ mi_status attention_sliding(const mi_dims* dims, const void* q, const void* k_ca
     p.sinks = sinks;
     p.slot_floats = (int)slot_floats(D);
     p.sl2 = scale * 1.4426950408889634f;
-    // 6.8 TB/s; a warp's block takes about 0.75 us (bf16) or 1 (one-byte codes, converted)
+    // 6.8 TB/s; a warp's block takes about 0.75 us (bf16: its ring's latency, whoever else
+    // is there) or 1 (one-byte codes, of which an SM's warps share the time: 128 windows of
+    // 4,096 in e4m3 take 0.65 us a block with 3.4 warps an SM, 0.88 with 6.7, 1.05 with 10.1,
+    // 1.3 with 12)
     p.flow = (float)(2 * kBlock * HD * elem_bytes(var)) / 6.8e12f / (var == kVarMma ? 0.75e-6f : 1e-6f);
+    p.alone = var == kVarMma ? 1.f : 0.6f;
     p.wait_ns = test_wait_limit_ns();
     p.withhold = test_withhold_copy() ? 1 : 0;
     const cudaStream_t st = (cudaStream_t)stream;

@@ -145,3 +145,21 @@ def test_sliding_prefill_refusals(mi):
     for name in "q k v out".split():
         assert sliding_prefill(mi, **{name: 20 * P + 8}) == BAD, name
     assert mi.load().mi_paged_prefill_attention_sliding(None, 4, 4, P, P, P, P, P, P, 1, 0, 0.1, P, None, None) == BAD
+
+
+def test_pieces_stay_within_the_places():
+    """The plan's cuts, in fp32 as every block of the launch computes them: pieces of split
+    units never outnumber the workspace's places (8 per warp and 64)."""
+    import random
+
+    import numpy as np
+    f, r = np.float32, random.Random(74)
+    for _ in range(300):
+        warps = f(r.choice((12, 1776, 1824)))
+        units = int(np.exp(r.uniform(0, np.log(60000))))
+        hi = int(np.exp(r.uniform(0, np.log(20000))))
+        nb = np.random.default_rng(r.randrange(1 << 30)).integers(r.choice((1, max(1, hi // 2), hi)), hi + 1, units)
+        least = max(f(1), np.ceil(f(2) * f(nb.sum()) / (f(8) * warps)))
+        for step in (least, least + 1, 2 * least):  # no cut is finer than the first
+            pieces = -(-nb // int(step))
+            assert pieces[pieces > 1].sum() <= 8 * warps + 64

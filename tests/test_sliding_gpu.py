@@ -357,3 +357,59 @@ def test_units_that_end_in_the_same_two_warps(cuda_device, kind):
     tol = (BF16_HALF * (2 * ref.abs() + mag) + ((2 * slack + 64 * FP32_HALF) * 2)[:, None] * mag) * 1.01 + 1e-30
     more = fp8_slack(x * seen, slack, vv.abs().amax((1, 2)))
     assert torch.all((out[short] - ref).abs() <= tol + more[:, None])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (7, 1, 128)])
+def test_bad_blocks_on_either_side_of_a_pair(cuda_device, kind, Hq, Hkv, d):
+    """One block of a request has a bad id, request by request another one, in windows
+    of an odd and an even number of blocks: its tokens alone carry no weight."""
+    mi = _mi()
+    n, blocks = 16 * 9 + 5, 10
+    for window in (16 * 5, 16 * 6, 1 << 20):
+        c = Case([n] * blocks, Hq, Hkv, d, window, 4, 71, kind, hide=False)
+        for s in range(blocks):
+            c.b.tables[s, s] = -1 if s % 2 else c.b.num_blocks
+        out, err = c.call(cuda_device)
+        assert err.item() == mi.MI_DEVERR_BAD_BLOCK
+        assert torch.all(torch.isfinite(out.float()))
+        out = out.cpu()
+        for s in range(blocks):
+            t = sight(n, window, 4)
+            t = t[t // BLOCK != s]
+            for h in range(Hkv):
+                k, v = (x[t] for x in c.kv[s][h])
+                q = c.q[s, h * Hq // Hkv:(h + 1) * Hq // Hkv].double()
+                ref, tol = attention_ref(q, k, v, c.scale)
+                if kind == "int8":
+                    tol = tol + int8_slack(q, v, c.scales[0].max(), c.scales[1].max(), c.scale)
+                elif kind == "fp8":
+                    slack = logit_slack(q, k, c.scale) + float((q @ k.T).abs().max()) * c.scale * 4 * FP32_HALF
+                    tol = tol + 4 * slack * v.abs().max()
+                got = out[s, h * Hq // Hkv:(h + 1) * Hq // Hkv].double()
+                assert torch.all((got - ref).abs() <= tol), (window, s, h)
+
+
+@pytest.mark.parametrize("spread", [1e2, 1e5])
+def test_int8_value_factors_far_apart(cuda_device, spread):
+    """Neighbouring blocks whose V factors differ by 1 to `spread`, in either order, zero
+    ones among them. Weights times a block's factor over the largest are rounded to
+    f16: by half a subnormal step, 2^-25 of the largest factor's values, at least."""
+    lens = [1, 16, 17, 32, 33, 100, 500, 900]
+    c = Case(lens, 4, 2, 64, 300, 20, 72, "int8")
+    g = torch.Generator().manual_seed(73)
+    c.scales[1] = torch.exp(torch.rand(c.b.num_blocks, 2, generator=g) * torch.log(torch.tensor(spread)))
+    c.scales[1][torch.rand(c.b.num_blocks, 2, generator=g) < 0.1] = 0.0
+    c.kv = [[c.tokens(s, h) for h in range(2)] for s in range(len(lens))]
+    out, err = c.call(cuda_device)
+    assert err.item() == 0
+    out = out.cpu()
+    for s, n in enumerate(lens):
+        t = sight(n, 300, 20)
+        for h in range(2):
+            k, v = (x[t] for x in c.kv[s][h])
+            q = c.q[s, 2 * h:2 * h + 2].double()
+            ref, tol = attention_ref(q, k, v, c.scale)
+            top = c.scales[1].max()
+            tol = tol + int8_slack(q, v, c.scales[0].max(), top, c.scale) + len(t) * 2.0 ** -25 * float(top)
+            assert torch.all((out[s, 2 * h:2 * h + 2].double() - ref).abs() <= tol), (s, h)

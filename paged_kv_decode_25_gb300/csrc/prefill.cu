@@ -1827,10 +1827,10 @@ __global__ void __launch_bounds__(kT2Threads, 1)
 //   * rows are stored 16 bytes a lane (as pairs of values the stores took 2.7 us).
 //
 // Bound by the pipeline of tensor cores and exponentials within the stages (1.64 us for 256
-// rows and 128 keys, 82 % of the tensor peak) and by what two masked stages (2 us each) and
-// the stores (1.5 to 2 us) add to an item. Measured: 16 chunks of 512 tokens behind windows
-// of 1,024 (32/8 heads of 128) 161 us, 0.83 PFLOP/s of visible pairs; two prompts of 12,000
-// to 16,000 behind 4,096 (28/4) 1,135 us, 1.22 PFLOP/s; a prompt of 700 behind 256 17 us. A
+// rows and 128 keys, 82 % of the tensor peak) and by what two masked stages and the stores
+// add to an item (5 us). Measured: 16 chunks of 512 tokens behind windows
+// of 1,024 (32/8 heads of 128) 153 us, 0.87 PFLOP/s of visible pairs; two prompts of 12,000
+// to 16,000 behind 4,096 (28/4) 1,126 us, 1.23 PFLOP/s; a prompt of 700 behind 256 16 us. A
 // block per item: 207, 1,272, 19.5.
 
 // Warps 0 .. 15 softmax, 16 MMA, 17 producer, and two that only fill up their warpgroup:

@@ -281,3 +281,36 @@ def test_graph_and_streams(cuda_device):
             with torch.cuda.stream(st):
                 call(x)
         same()
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_e4m3_quotients_bit_for_bit(cuda_device, seed):
+    """Every bf16 value over scales of all sizes (ones with all bits set, powers of two,
+    denormal and near the largest): the code of the IEEE single precision quotient."""
+    mi, dev = _mi(), cuda_device
+    g = torch.Generator().manual_seed(seed)
+    Hkv, d, T, NB = 32, 128, 512, 32
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    # a head has 512 x 128 values: each of them once
+    v = torch.stack([bits[torch.randperm(65536, generator=g)].view(T, d) for _ in range(Hkv)], 1).contiguous()
+    mant = 1 + torch.rand(Hkv, generator=g)
+    scale = torch.ldexp(mant, torch.randint(-12, 4, (Hkv,), generator=g))
+    scale[:12] = torch.ldexp(mant[:12], torch.randint(-126, 127, (12,), generator=g))
+    scale[12:24] = torch.tensor([2 - 2.0 ** -23, 1.0, 2.0 ** -60, 2.0 ** -60 * (1 - 2.0 ** -24), 2.0 ** 60,
+                                 2.0 ** 60 * (1 + 2.0 ** -23), 1 + 2.0 ** -23, 3.0, 1 / 3, 448.0, 1e-40, 3e38])
+    q = torch.zeros(T, Hkv, d, dtype=torch.bfloat16, device=dev)
+    w = torch.ones(d, dtype=torch.bfloat16, device=dev)
+    rope = torch.zeros(1, d // 2, 2, device=dev)
+    kc, vc = (torch.zeros(NB, Hkv, 16, d, dtype=torch.uint8, device=dev) for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    mi.check(mi.mi_paged_kv_append_norm_fp8(
+        mi.dims(T, Hkv, Hkv, d, NB, 1), q, torch.zeros_like(q), v.to(dev), w, w, 1e-6,
+        torch.zeros(T, dtype=torch.int32, device=dev), torch.arange(T, dtype=torch.int32, device=dev), rope, 1,
+        torch.empty_like(q), kc, vc, torch.ones(Hkv, device=dev), scale.to(dev), dev_err=err))
+    assert err.item() == 0
+    got = vc.cpu().view(NB, Hkv, 16, d).transpose(1, 2).reshape(T, Hkv, d)
+    want = (v.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    nan = torch.isnan(v.float())
+    assert torch.all((got[nan] & 0x7F) == 0x7F)
+    bad = (got != want) & ~nan
+    assert not bad.any(), (int(bad.sum()), v[bad][:4].tolist(), got[bad][:4].tolist(), want[bad][:4].tolist())

@@ -1830,7 +1830,7 @@ __global__ void __launch_bounds__(kT2Threads, 1)
 // rows and 128 keys, 82 % of the tensor peak) and by what two masked stages and the stores
 // add to an item (5 us). Measured: 16 chunks of 512 tokens behind windows
 // of 1,024 (32/8 heads of 128) 153 us, 0.87 PFLOP/s of visible pairs; two prompts of 12,000
-// to 16,000 behind 4,096 (28/4) 1,126 us, 1.23 PFLOP/s; a prompt of 700 behind 256 16 us. A
+// to 16,000 behind 4,096 (28/4) 1,121 us, 1.24 PFLOP/s; a prompt of 700 behind 256 16 us. A
 // block per item: 207, 1,272, 19.5.
 
 // Warps 0 .. 15 softmax, 16 MMA, 17 producer, and two that only fill up their warpgroup:

@@ -285,7 +285,8 @@ __device__ __forceinline__ uint32_t i8x2_to_f16x2(uint32_t u, uint32_t sel) {
 
 // The same pair without the subtraction: f16 values 1152 + code, exact. A
 // caller that multiplies them on tensor cores takes 1152 times the other
-// operand's sum back off the result.
+// operand's sum back off the result (a few products long: tensor cores cut sums
+// towards zero, which adds up in an accumulator that the bias fills).
 __device__ __forceinline__ uint32_t i8x2_to_f16x2_biased(uint32_t u, uint32_t sel) {
     return __byte_perm(u, 0x64646464u, sel);
 }

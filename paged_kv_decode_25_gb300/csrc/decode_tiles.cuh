@@ -494,12 +494,14 @@ struct Fp8State {
 };
 
 // Tensor-core tile over INT8 K/V tiles quantised in 64-token groups: the e4m3
-// tile's data movement and fragment orders. Each code enters the MMAs as the
-// f16 value 1152 + code (a byte permute, exact), and the bias is taken back
-// off the results: from the scores, 1152 times the sum of the head's q (a
-// constant per head, folded into the scaling FMA); from O, 1152 times the
-// sum of the f16 probabilities that went into the PV products (summed per
-// lane like the running sum and subtracted once, at the store). A block's
+// tile's data movement and fragment orders. K's codes enter the MMAs as the f16
+// values 1152 + code (a byte permute, exact); the bias comes back off the scores,
+// 1152 times the sum of the head's q (a constant per head, folded into the scaling
+// FMA). V's codes enter as themselves, one subtraction a pair: O adds up over
+// hundreds of blocks, and the tensor cores cut each sum towards zero, so that with
+// the bias in it O lost a part of 1152 times the probabilities in every block (a
+// hundredth of the outputs behind a window of 8,192; 66 thousandths where the
+// weights are equal). A block's
 // codes stand for code * a / 127, a the maximum of its group (one per block
 // and head, staged with the tile): K's factor multiplies the block's scores;
 // V's factor is taken relative to a reference factor of the warp (the first
@@ -517,7 +519,6 @@ struct Int8State {
     float o[kK][4];
     float m[2], l[2];
     float koff[2];  // kBias * sum of q over the dims, for this lane's two heads
-    float sp[2];    // this lane's sum of the f16 probabilities fed to the PV products
     float sl2, vref, rvref;
 
     template <class Params>
@@ -526,7 +527,6 @@ struct Int8State {
         for (int mt = 0; mt < kK; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
         m[0] = m[1] = kNegInf;
         l[0] = l[1] = 0.f;
-        sp[0] = sp[1] = 0.f;
         sl2 = p.sl2 * (1.f / 127.f);
         vref = 0.f;
         rvref = 0.f;
@@ -621,8 +621,6 @@ struct Int8State {
         const float rel = fv * rvref;
         const uint32_t x0 = pack_f16x2(p0 * rel, p1 * rel);
         const uint32_t x1 = pack_f16x2(p2 * rel, p3 * rel);
-        sp[0] = sp[0] * ov0 + (f16_lo(x0) + f16_lo(x1));
-        sp[1] = sp[1] * ov1 + (f16_hi(x0) + f16_hi(x1));
         if (__any_sync(0xffffffffu, ov0 != 1.f || ov1 != 1.f)) {
 #pragma unroll
             for (int mt = 0; mt < kK; ++mt) {
@@ -645,10 +643,10 @@ struct Int8State {
                 const uint32_t w3 = lds32(vt + swz8<HD>(2 * cc + 9, chunk) + inb);
                 const uint32_t lo01 = __byte_perm(w0, w1, 0x5140) ^ kFlip, hi01 = __byte_perm(w0, w1, 0x7362) ^ kFlip;
                 const uint32_t lo89 = __byte_perm(w2, w3, 0x5140) ^ kFlip, hi89 = __byte_perm(w2, w3, 0x7362) ^ kFlip;
-                mma_f16_16816(o[2 * t], i8x2_to_f16x2_biased(lo01, kLo), i8x2_to_f16x2_biased(lo01, kHi),
-                              i8x2_to_f16x2_biased(lo89, kLo), i8x2_to_f16x2_biased(lo89, kHi), b0, b1);
-                mma_f16_16816(o[2 * t + 1], i8x2_to_f16x2_biased(hi01, kLo), i8x2_to_f16x2_biased(hi01, kHi),
-                              i8x2_to_f16x2_biased(hi89, kLo), i8x2_to_f16x2_biased(hi89, kHi), b0, b1);
+                mma_f16_16816(o[2 * t], i8x2_to_f16x2(lo01, kLo), i8x2_to_f16x2(lo01, kHi),
+                              i8x2_to_f16x2(lo89, kLo), i8x2_to_f16x2(lo89, kHi), b0, b1);
+                mma_f16_16816(o[2 * t + 1], i8x2_to_f16x2(hi01, kLo), i8x2_to_f16x2(hi01, kHi),
+                              i8x2_to_f16x2(hi89, kLo), i8x2_to_f16x2(hi89, kHi), b0, b1);
             }
         }
     }
@@ -713,7 +711,7 @@ struct Int8State {
             rvref = 1.f / fv;
         }
         uint32_t b[2][2];
-        float l0 = 0.f, l1 = 0.f, sp0 = 0.f, sp1 = 0.f;
+        float l0 = 0.f, l1 = 0.f;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const float p0 = ex2(s[x][0] - r0), p1 = ex2(s[x][1] - r1), p2 = ex2(s[x][2] - r0), p3 = ex2(s[x][3] - r1);
@@ -721,15 +719,11 @@ struct Int8State {
             l1 += p1 + p3;
             const float rel = (x ? av1 : av0) * (1.f / 127.f) * rvref;
             const uint32_t x0 = pack_f16x2(p0 * rel, p1 * rel), x1 = pack_f16x2(p2 * rel, p3 * rel);
-            sp0 += f16_lo(x0) + f16_lo(x1);
-            sp1 += f16_hi(x0) + f16_hi(x1);
             b[x][0] = movmatrix_trans(x0);
             b[x][1] = movmatrix_trans(x1);
         }
         l[0] = l[0] * al0 + l0;
         l[1] = l[1] * al1 + l1;
-        sp[0] = sp[0] * ov0 + sp0;
-        sp[1] = sp[1] * ov1 + sp1;
         if (__any_sync(0xffffffffu, ov0 != 1.f || ov1 != 1.f)) {
 #pragma unroll
             for (int mt = 0; mt < kK; ++mt) {
@@ -752,10 +746,10 @@ struct Int8State {
                 const uint32_t w3 = lds32(v + swz8<HD>(2 * cc + 9, chunk) + inb);
                 const uint32_t lo01 = __byte_perm(w0, w1, 0x5140) ^ kFlip, hi01 = __byte_perm(w0, w1, 0x7362) ^ kFlip;
                 const uint32_t lo89 = __byte_perm(w2, w3, 0x5140) ^ kFlip, hi89 = __byte_perm(w2, w3, 0x7362) ^ kFlip;
-                mma_f16_16816(o[2 * t], i8x2_to_f16x2_biased(lo01, kLo), i8x2_to_f16x2_biased(lo01, kHi),
-                              i8x2_to_f16x2_biased(lo89, kLo), i8x2_to_f16x2_biased(lo89, kHi), b[x][0], b[x][1]);
-                mma_f16_16816(o[2 * t + 1], i8x2_to_f16x2_biased(hi01, kLo), i8x2_to_f16x2_biased(hi01, kHi),
-                              i8x2_to_f16x2_biased(hi89, kLo), i8x2_to_f16x2_biased(hi89, kHi), b[x][0], b[x][1]);
+                mma_f16_16816(o[2 * t], i8x2_to_f16x2(lo01, kLo), i8x2_to_f16x2(lo01, kHi),
+                              i8x2_to_f16x2(lo89, kLo), i8x2_to_f16x2(lo89, kHi), b[x][0], b[x][1]);
+                mma_f16_16816(o[2 * t + 1], i8x2_to_f16x2(hi01, kLo), i8x2_to_f16x2(hi01, kHi),
+                              i8x2_to_f16x2(hi89, kLo), i8x2_to_f16x2(hi89, kHi), b[x][0], b[x][1]);
             }
         }
     }
@@ -769,8 +763,6 @@ struct Int8State {
         for (int sh = 4; sh < 32; sh <<= 1) {
             l[0] += __shfl_xor_sync(0xffffffffu, l[0], sh);
             l[1] += __shfl_xor_sync(0xffffffffu, l[1], sh);
-            sp[0] += __shfl_xor_sync(0xffffffffu, sp[0], sh);
-            sp[1] += __shfl_xor_sync(0xffffffffu, sp[1], sh);
         }
     }
     template <class F>
@@ -780,13 +772,12 @@ struct Int8State {
         for (int t = 0; t < kK / 2; ++t)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const float v[4] = {(o[2 * t][w] - kBias * sp[w]) * vref, (o[2 * t][2 + w] - kBias * sp[w]) * vref, (o[2 * t + 1][w] - kBias * sp[w]) * vref, (o[2 * t + 1][2 + w] - kBias * sp[w]) * vref};
+                const float v[4] = {o[2 * t][w] * vref, o[2 * t][2 + w] * vref, o[2 * t + 1][w] * vref, o[2 * t + 1][2 + w] * vref};
                 f(w, 4 * (8 * t + r), v);
             }
     }
 
-    // Reduce the per-thread sums and write (m, l, (O - bias * probability
-    // sum) * reference) of this warp to smem.
+    // Reduce the per-thread sums and write (m, l, O * reference) of this warp to smem.
     __device__ __forceinline__ void store(float* mbuf, float* lbuf, float* obuf, int G, int lane) {
         sums();
         const int h0 = (lane & 3) * 2, h1 = h0 + 1;
@@ -794,22 +785,21 @@ struct Int8State {
             if (h0 < G) { mbuf[h0] = m[0]; lbuf[h0] = l[0]; }
             if (h1 < G) { mbuf[h1] = m[1]; lbuf[h1] = l[1]; }
         }
-        const float b0 = kBias * sp[0], b1 = kBias * sp[1];
         const int r = lane >> 2;
 #pragma unroll
         for (int t = 0; t < kK / 2; ++t) {
             const int d0 = 4 * (8 * t + r);
             if (h0 < G) {
-                obuf[h0 * HD + d0] = (o[2 * t][0] - b0) * vref;
-                obuf[h0 * HD + d0 + 1] = (o[2 * t][2] - b0) * vref;
-                obuf[h0 * HD + d0 + 2] = (o[2 * t + 1][0] - b0) * vref;
-                obuf[h0 * HD + d0 + 3] = (o[2 * t + 1][2] - b0) * vref;
+                obuf[h0 * HD + d0] = o[2 * t][0] * vref;
+                obuf[h0 * HD + d0 + 1] = o[2 * t][2] * vref;
+                obuf[h0 * HD + d0 + 2] = o[2 * t + 1][0] * vref;
+                obuf[h0 * HD + d0 + 3] = o[2 * t + 1][2] * vref;
             }
             if (h1 < G) {
-                obuf[h1 * HD + d0] = (o[2 * t][1] - b1) * vref;
-                obuf[h1 * HD + d0 + 1] = (o[2 * t][3] - b1) * vref;
-                obuf[h1 * HD + d0 + 2] = (o[2 * t + 1][1] - b1) * vref;
-                obuf[h1 * HD + d0 + 3] = (o[2 * t + 1][3] - b1) * vref;
+                obuf[h1 * HD + d0] = o[2 * t][1] * vref;
+                obuf[h1 * HD + d0 + 1] = o[2 * t][3] * vref;
+                obuf[h1 * HD + d0 + 2] = o[2 * t + 1][1] * vref;
+                obuf[h1 * HD + d0 + 3] = o[2 * t + 1][3] * vref;
             }
         }
     }

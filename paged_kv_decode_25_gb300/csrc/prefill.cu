@@ -39,6 +39,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "prefill_items.cuh"
 #include "prefix.cuh"
 #include "sliding.cuh"
 #include "tc.cuh"
@@ -55,14 +56,12 @@ constexpr int kPStages = 3;
 constexpr int kMaxGroup = 8;
 constexpr int kTileGroup = 8;                   // row tiles of one (request, head) launched together
 
-struct PrefillParams {
+struct PrefillParams : PrefillBatch {
     const uint16_t* q;             // [T][Hq][HD], RoPE applied
     const int32_t* block_tables;   // [R][mbps]
-    const int32_t* context_lens;   // [R], counting the new tokens
-    const int32_t* query_start;    // [R + 1]
     uint16_t* out;                 // [T][Hq][HD]
     int32_t* dev_err;
-    int R, Hq, Hkv, G, num_blocks, mbps, T, max_q;
+    int R, Hq, Hkv, num_blocks;
     float sl2;                     // scale * log2(e)
     long long wait_ns;             // bound on every mbarrier wait of the launch
     int withhold;                  // failure-detection test: each producer withholds its first K copy
@@ -77,40 +76,21 @@ struct SlidingParams : PrefillParams {
 // (request r, KV head h), with `tile_rows` (token, head) rows per tile.
 // Returns false when the CTA has nothing to do (past the request's last row,
 // or a bad request, which is reported once).
-struct Item {
-    int r, h, q0, m, n, first, nrows, rho0, rows_here, p_hi, nblk;
-};
-
 __device__ __forceinline__ bool work_item(const PrefillParams& p, int tile_rows, Item& it) {
     const int kw = blockIdx.x % kTileGroup;
     const int rest0 = blockIdx.x / kTileGroup;
     it.h = rest0 % p.Hkv;
-    const int rest = rest0 / p.Hkv;
-    it.r = rest % p.R;
+    const int rest = rest0 / p.Hkv, r = rest % p.R;
     const int k = (rest / p.R) * kTileGroup + kw;
     const bool reporter = k == 0 && it.h == 0 && threadIdx.x == 0;  // one error report per request
-    it.q0 = __ldg(p.query_start + it.r);
-    const int q1 = __ldg(p.query_start + it.r + 1);
-    it.m = q1 - it.q0;
-    if (it.q0 < 0 || q1 > p.T || it.m < 0 || it.m > p.max_q) {
-        if (reporter) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
+    if (!tile_item(p, tile_rows, r, k, it)) {
+        if (reporter && it.m < 0) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
         return false;
     }
-    it.nrows = it.m * p.G;
-    const int tiles = (it.nrows + tile_rows - 1) / tile_rows;
-    if (k >= tiles) return false;
-    int n = __ldg(p.context_lens + it.r);
-    if (n > p.mbps * kBlock) {
-        if (reporter) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
-        n = p.mbps * kBlock;
+    if (reporter) {
+        if (__ldg(p.context_lens + r) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
+        if (it.m > it.n) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
     }
-    if (it.m > n && reporter) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
-    it.n = n;
-    it.first = n - it.m;  // position of new token 0 (negative only when m > n)
-    it.rho0 = (tiles - 1 - k) * tile_rows;
-    it.rows_here = min(tile_rows, it.nrows - it.rho0);
-    it.p_hi = it.first + (it.rho0 + it.rows_here - 1) / p.G;  // position of the CTA's last row
-    it.nblk = it.p_hi >= 0 ? it.p_hi / kBlock + 1 : 0;        // blocks any row of the CTA reads
     return true;
 }
 
@@ -1853,45 +1833,12 @@ struct SlideSmem : Tc2Smem<HD> {
     static constexpr int kTotal = kBarX + (1 + kItems) * 8 + 1024;
 };
 
-// 256 rows of a request and KV head; r < 0: no more.
-struct SlideItem {
-    int r, h, q0, first, n, p_hi;  // as Item
-    int tok0, m;                   // the item's first of the request's m new tokens
-    int head, gap, nblk;  // the blocks 0 .. head - 1 and from head + gap on, nblk in all
-    int lo, sinks;        // tokens that some row of the request sees: below sinks, and from lo on
-};
-
-// A request's tiles of `rows` rows; 0 where it is refused.
-__device__ __forceinline__ int slide_tiles(const PrefillParams& p, int r, int rows) {
-    const int q0 = __ldg(p.query_start + r), q1 = __ldg(p.query_start + r + 1), m = q1 - q0;
-    if (q0 < 0 || q1 > p.T || m < 0 || m > p.max_q) return 0;
-    return (m * p.G + rows - 1) / rows;
-}
-
 __device__ SlideItem slide_item(const SlidingParams& p, const long long* sums, int rows, long long x) {
-    SlideItem it;
     auto tiles_of = [&](int r) { return (long long)p.Hkv * slide_tiles(p, r, rows); };
     long long before;
-    it.r = flat_find(p.R, tiles_of, sums, x, before);
-    const int tiles = slide_tiles(p, it.r, rows), o = (int)(x - before);
-    it.h = o / tiles;
-    const int k = o - it.h * tiles;
-    it.q0 = __ldg(p.query_start + it.r);
-    const int m = __ldg(p.query_start + it.r + 1) - it.q0;
-    it.n = min(__ldg(p.context_lens + it.r), p.mbps * kBlock);
-    it.m = m;
-    it.first = it.n - m;
-    it.tok0 = (tiles - 1 - k) * (rows / p.G);
-    it.p_hi = it.first + min(it.tok0 + rows / p.G, m) - 1;
-    auto window_of = [&](int pos) { return pos >= p.window ? pos - p.window + 1 : 0; };
-    const int from = window_of(max(0, it.first + it.tok0));  // the first row's window
-    it.head = (min(p.sinks, from) + kBlock - 1) / kBlock;
-    const int all = it.p_hi >= 0 ? it.p_hi / kBlock + 1 : 0;
-    it.gap = max(0, min(from / kBlock, all) - it.head);
-    it.nblk = all - it.gap;
-    it.lo = window_of(max(0, it.first));
-    it.sinks = min(p.sinks, it.lo);
-    return it;
+    const int r = flat_find(p.R, tiles_of, sums, x, before);
+    const int tiles = slide_tiles(p, r, rows), o = (int)(x - before), h = o / tiles;
+    return slide_tile_item(p, p.window, p.sinks, rows, r, h, tiles, o - h * tiles);
 }
 
 // The keys of a stage that count for a row, as bits: local keys below `sink` and
@@ -2047,14 +1994,9 @@ __global__ void __launch_bounds__(kSlideThreads, 1)
     pdl_trigger();
     // each request once
     for (int r = blockIdx.x + gridDim.x * threadIdx.x; r < p.R; r += gridDim.x * kSlideThreads) {
-        const int q0 = __ldg(p.query_start + r), q1 = __ldg(p.query_start + r + 1), m = q1 - q0;
-        const int n = __ldg(p.context_lens + r);
-        if (q0 < 0 || q1 > p.T || m < 0 || m > p.max_q) {
-            raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
-        } else if (m > 0) {
-            if (n > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
-            if (m > min(n, p.mbps * kBlock)) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
-        }
+        const int m = new_tokens(p, r).m;
+        if (m < 0 || m > held_tokens(p, r)) raise_err(p.dev_err, MI_DEVERR_BAD_QUERY);
+        if (m > 0 && __ldg(p.context_lens + r) > p.mbps * kBlock) raise_err(p.dev_err, MI_DEVERR_BAD_CONTEXT);
     }
     const long long items =
         flat_scan(p.R, [&](int r) { return (long long)p.Hkv * slide_tiles(p, r, rows); }, sums);  // (ends with a barrier)

@@ -61,7 +61,8 @@ typedef enum mi_status {
 #define MI_DEVERR_BAD_CONTEXT  0x8 /* context length above max_blocks_per_seq * block_size */
 #define MI_DEVERR_TIMEOUT      0x10 /* a staged copy did not land within the wait limit */
 #define MI_DEVERR_BAD_SCALE    0x40 /* FP8 append: a KV head's scale is not a positive finite number */
-#define MI_DEVERR_INTERNAL     0x80 /* a kernel could not lay out its shared memory (the call did nothing) */
+#define MI_DEVERR_INTERNAL     0x80 /* a kernel could not lay out its shared memory, or its partial results in
+                                       the workspace (the call did nothing) */
 #define MI_DEVERR_BAD_QUERY    0x20 /* prefill: query_start not within [0, total_q] and ascending,
                                        a request longer than max_query_len, or more
                                        new tokens than context; shared prefixes:

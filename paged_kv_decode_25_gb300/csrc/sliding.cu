@@ -30,16 +30,11 @@
 #include "common.cuh"
 #include "decode_tiles.cuh"
 #include "sliding.cuh"
+#include "sliding_plan.cuh"
 #include "tma.cuh"
 
 namespace mi {
 namespace {
-
-constexpr int kSlideWarps = 4;
-
-// Blocks per SM. (Four for one-byte caches, at 128 registers a thread: 116 us instead
-// of 92 for 128 windows of 4,096 tokens, 4 KV heads, e4m3.)
-constexpr int kSlideBlocks = 3;
 
 template <int HD, int VAR>
 struct SlideShape {
@@ -51,16 +46,6 @@ struct SlideShape {
     static constexpr int kStages = 16384 / kStage < 4 ? 16384 / kStage : 4;
     static constexpr int kSmem = kSlideWarps * kStages * kStage + 1024;  // slack to align the tiles
 };
-
-// Pieces that have partial results, at most, per warp of the grid.
-constexpr int kSplitPerWarp = 8;
-// In a warp's block times: a piece's own cost (its queries, its output), that of a
-// split unit's end, and of adding up 512 outputs of a piece there. Fitted, with
-// SlideParams::alone, to 15 shapes (1 to 256 requests, windows of 128 to 4,096, the three
-// types) cut into 1 to 24 pieces: the plan's choice is within 0.9 % of the best one on
-// average. (More rounds of shorter pieces lose to one round: each costs its results and
-// counts, and the additions fall to the blocks that end last.)
-constexpr float kPieceCost = 16.f, kSplitCost = 1.f, kMergeCost = 0.1f;
 
 // Piece i of the np of (request b, head h): blocks in sight j .. j1 - 1; `slot`: the
 // unit's first partial result. b < 0: no more pieces.
@@ -88,8 +73,7 @@ struct SlideParams {
     int32_t* dev_err;
     int B, Hq, Hkv, G, num_blocks, mbps, window, sinks, most, slot_floats;
     float sl2;                     // scale * log2(e)
-    float flow;                    // a block's time at full memory rate over its time in a warp, times all warps
-    float alone;                   // a warp's share of that time which others on its SM do not lengthen
+    float flow, alone;             // slide_flow, slide_alone
     long long wait_ns;
     int withhold;                  // failure-detection test: each warp withholds its first copy
 };
@@ -99,56 +83,25 @@ __device__ __forceinline__ Sight sight_of(const SlideParams& p, int b) {
     return Sight(n < 0 ? 0 : (n > cap ? cap : n), p.window, p.sinks);
 }
 
-// The blocks of a piece, for requests before b0 and for those from it on.
-struct Cut {
-    int step, tail_step, b0;
-};
-
-// Chosen by every block of the launch alike: a lane tries 1 to 16 pieces for the
-// largest unit, or 16 to 448 in steps of a quarter. Warps take whole pieces in turn;
-// what the last round leaves over is cut so that every warp has some of it. The time
-// is that of the rounds, or of all bytes at the memory's rate, and the end of the
-// unit with the most pieces.
+// The best of 32 cuts, chosen by every block of the launch alike.
 __device__ Cut cut_units(const SlideParams& p, float warps, float blocks, float units, int largest, int hd, int lane) {
-    const float all = blocks * p.flow;  // time of all blocks at the memory's rate, in a warp's block times
-    const float np = lane < 16 ? (float)(lane + 1) : (float)((16 + 4 * (lane & 3)) << ((lane - 16) >> 2));
-    const float big = (float)largest;
-    const float least = fmaxf(1.f, ceilf(__fdividef(2.f * blocks, (float)kSplitPerWarp * warps)));
-    const float step = fmaxf(least, ceilf(__fdividef(big, np)));
-    const float most = ceilf(__fdividef(big, step)), outs = (float)((p.G * hd + 511) / 512);
-    auto end_cost = [&](float pieces) { return pieces > 1.f ? kSplitCost + kMergeCost * pieces * outs : 0.f; };
-    // the largest units have `most` pieces, the others half a piece more than their share
-    const float fill = __fdividef(blocks, units * big);
-    const float rounds = __fdividef(fmaxf(units * (most * fill + 0.5f * (1.f - fill)), units), warps);
-    const float whole = floorf(rounds), over = rounds - whole;
-    float tail_step = step, part = 1.f;  // part: of the requests, before b0
-    const float last = over > 0.f ? p.alone + (1.f - p.alone) * over : 0.f;
-    float cost = fmaxf(all, (whole + last) * (step + kPieceCost)) + end_cost(most);
-    if (whole > 0.f && over > 0.01f) {
-        const float tail_np = fminf(16.f, __fdividef(most * fill, over));  // so that they fill a round
-        const float s = fminf(step, fmaxf(least, ceilf(__fdividef(big, fmaxf(1.f, tail_np)))));
-        const float c = fmaxf(all, whole * (step + kPieceCost) + s + kPieceCost) +
-                        end_cost(fmaxf(most, ceilf(__fdividef(big, s))));
-        if (c < cost) {
-            cost = c;
-            tail_step = s;
-            part = __fdividef(whole, rounds);
-        }
-    }
-    cost += 0.01f * most;
+    const CutSizes sizes = {warps, blocks, units, largest, p.G * hd, p.flow, p.alone};
+    CutTry c = try_cut(sizes, lane, [](float a, float b) { return __fdividef(a, b); });
+    float cost = c.cost;
     int who = lane;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+        const float x = __shfl_xor_sync(0xffffffffu, cost, o);
         const int w = __shfl_xor_sync(0xffffffffu, who, o);
-        if (c < cost || (c == cost && w < who)) {
-            cost = c;
+        if (x < cost || (x == cost && w < who)) {
+            cost = x;
             who = w;
         }
     }
-    const float b0 = part < 1.f ? part * (float)p.B : (float)p.B;
-    return {max(1, (int)__shfl_sync(0xffffffffu, step, who)), max(1, (int)__shfl_sync(0xffffffffu, tail_step, who)),
-            min(p.B, (int)__shfl_sync(0xffffffffu, b0, who))};
+    c.step = __shfl_sync(0xffffffffu, c.step, who);
+    c.tail_step = __shfl_sync(0xffffffffu, c.tail_step, who);
+    c.part = __shfl_sync(0xffffffffu, c.part, who);
+    return Cut(c, p.B, largest);
 }
 
 // A split unit counts its finished pieces in a word: the call's tag in the high 48
@@ -257,7 +210,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     // usual batches: blocks in sight, pieces before, those of split units; larger ones: chunks' sums
     __shared__ union {
         struct {
-            int held[kFlatOneWarp], first[kFlatOneWarp + 1], first_split[kFlatOneWarp];
+            int held[kFlatOneWarp], first[kFlatOneWarp + 1], first_split[kFlatOneWarp], split;
         };
         struct {
             long long sums[flat_words(kThreads)], split_sums[flat_words(kThreads)];
@@ -318,23 +271,18 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     if (largest == 0) return;
     const int warps = gridDim.x * kSlideWarps;
     const Cut cut = cut_units(p, (float)warps, (float)blocks, (float)units, largest, HD, lane);
-    auto pieces_of = [&](int b, int nb) {
-        const int step = b < cut.b0 ? cut.step : cut.tail_step;
-        return (nb + step - 1) / step;
-    };
+    auto pieces_of = [&](int b, int nb) { return cut.pieces(b, nb); };
     auto pieces = [&](int b) { return (long long)p.Hkv * pieces_of(b, sight_of(p, b).blocks); };
     auto splits = [&](int b) {
         const int np = pieces_of(b, sight_of(p, b).blocks);
         return np > 1 ? (long long)p.Hkv * np : 0LL;
     };
-    // As a rule every context is longer than the window, and every request before b0
-    // has as many pieces as any other, and so from it on: then places are divisions.
-    const int even0 = pieces_of(0, largest), even1 = pieces_of(p.B, largest);  // (b0 0: the first is not used)
-    const bool even = pieces_of(0, smallest) == even0 && pieces_of(p.B, smallest) == even1 && smallest > 0;
-    const int per0 = p.Hkv * even0, per1 = p.Hkv * even1, head_pieces = cut.b0 * per0;
+    const EvenCut even(cut, p.B, p.Hkv, smallest, largest);
     int total;
-    if (even) {
-        total = head_pieces + (p.B - cut.b0) * per1;
+    bool fits = true;  // the split pieces have places (as they must, see try_cut)
+    if (even.even) {
+        total = even.total(p.B);
+        fits = even.split(p.B) <= p.most;
     } else if (small) {
         if (warp == 0) {
             const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
@@ -353,7 +301,10 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
                     y += t;
                 }
             }
-            if (lane == 31) plan.first[p.B] = x;
+            if (lane == 31) {
+                plan.first[p.B] = x;
+                plan.split = y;
+            }
             x -= v;
             y -= w;
             for (int b = b0; b < b1; ++b) {
@@ -366,9 +317,14 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
         }
         __syncthreads();
         total = plan.first[p.B];
+        fits = plan.split <= p.most;
     } else {
         total = (int)flat_scan(p.B, pieces, plan.sums);
-        (void)flat_scan(p.B, splits, plan.split_sums);
+        fits = flat_scan(p.B, splits, plan.split_sums) <= p.most;
+    }
+    if (!fits) {
+        if (tid == 0) raise_err(p.dev_err, MI_DEVERR_INTERNAL);
+        return;
     }
     // ---------------------------------------------------------- the pieces --
     // The issuing side runs up to S blocks ahead, across pieces, and looks one piece
@@ -391,13 +347,9 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
         c.np = c.j = c.j1 = 0;
         if (x < total) {
             int o, nb;
-            if (even) {
-                const bool tail = x >= head_pieces;
-                const int y = tail ? x - head_pieces : x, per = tail ? per1 : per0, r = y / per;
-                c.b = tail ? cut.b0 + r : r;
-                o = y - r * per;
+            if (even.even) {
+                even.find(x, c.b, o, c.slot);
                 nb = small ? plan.held[c.b] : sight_of(p, c.b).blocks;
-                c.slot = x - o - (tail && even0 == 1 ? head_pieces : 0);  // (unused without a split)
             } else if (small) {
                 int lo = 0, hi = p.B;  // first[lo] <= x < first[hi]
                 while (hi - lo > 1) {
@@ -605,7 +557,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
     if (dead && lane == 0)  // the copies in flight land first
         for (int i = 0; i < S; ++i)
             if ((copied >> (kBlocks * i)) & ((1u << kBlocks) - 1u)) (void)mbar_wait_bounded(full + 8 * i, (phase >> i) & 1u, drain_limit(p.wait_ns));
-    if (even0 == 1 && even1 == 1) return;  // no unit is split
+    if (even.n0 == 1 && even.n1 == 1) return;  // no unit is split
     // All of the block's warps add up what they owe. (One warp a unit took 12 us for two
     // units of 7 pieces and 7 heads. Counting all pieces only here left most units to
     // the blocks that end last: 185 us instead of 98 with 21 pieces a unit.)
@@ -665,7 +617,6 @@ mi_status check_sliding(const mi_dims* dims, int32_t window, int32_t sinks) {
     return MI_OK;
 }
 
-int slide_slots(int sms) { return kSplitPerWarp * kSlideWarps * kSlideBlocks * sms + 64; }
 size_t slot_floats(const mi_dims& D) { return (size_t)(D.Hq / D.Hkv) * D.head_dim + 8; }
 
 // Workspace: [words | partial results].
@@ -727,12 +678,8 @@ mi_status attention_sliding(const mi_dims* dims, const void* q, const void* k_ca
     p.sinks = sinks;
     p.slot_floats = (int)slot_floats(D);
     p.sl2 = scale * 1.4426950408889634f;
-    // 6.8 TB/s; a warp's block takes about 0.75 us (bf16: its ring's latency, whoever else
-    // is there) or 1 (one-byte codes, of which an SM's warps share the time: 128 windows of
-    // 4,096 in e4m3 take 0.65 us a block with 3.4 warps an SM, 0.88 with 6.7, 1.05 with 10.1,
-    // 1.3 with 12)
-    p.flow = (float)(2 * kBlock * HD * elem_bytes(var)) / 6.8e12f / (var == kVarMma ? 0.75e-6f : 1e-6f);
-    p.alone = var == kVarMma ? 1.f : 0.6f;
+    p.flow = slide_flow(HD, elem_bytes(var));
+    p.alone = slide_alone(elem_bytes(var));
     p.wait_ns = test_wait_limit_ns();
     p.withhold = test_withhold_copy() ? 1 : 0;
     const cudaStream_t st = (cudaStream_t)stream;

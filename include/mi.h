@@ -154,6 +154,11 @@ mi_status mi_kv_pool_shrink(mi_kv_pool* pool, int32_t seq_id, int32_t num_tokens
  * i < *n_copies (mi_kv_copy_planes), before either sequence's next append (and
  * before the copies of a fork of the fork, which read them); with INT8 caches the
  * open-group rows of its slot too. Both sequences are used now.
+ * Columns of src_seq that mi_kv_pool_slide gave back are -1 in dst_seq's table, too.
+ * A fork of k tokens fewer than src_seq held when it was slid looks k tokens further
+ * back than src_seq did, so such sources are slid with window + k; where they were
+ * not, the fork is made, and attention over its window meets the missing blocks
+ * (MI_DEVERR_BAD_BLOCK, their tokens left out).
  * MI_ERR_UNKNOWN_SEQ if src_seq is not resident. MI_ERR_INVALID_ARG: dst_seq out
  * of range, resident or swapped out, more tokens than src_seq holds, group_tokens
  * not a positive multiple of 16, fewer than *n_copies places in the arrays
@@ -168,8 +173,9 @@ mi_status mi_kv_pool_fork(mi_kv_pool* pool, int32_t src_seq, int32_t dst_seq, in
  * tokens - window, but none of the open group. They leave the table in order
  * (columns of -1). Call it once the attention of the sequence's newest tokens has
  * been queued: a chunk's earlier tokens look further back than its last. A
- * sequence that may shrink by k tokens later (drafts taken back) is slid with window
- * + k: blocks given back do not return.
+ * sequence that may shrink by k tokens later (drafts taken back), or be forked k
+ * tokens back, is slid with window + k: blocks given back do not return. (The pool does
+ * not know the attention's window, so it cannot refuse what comes too late.)
  * *n_released (or NULL) gets their number. The use clock does not move.
  * MI_ERR_UNKNOWN_SEQ if seq_id is not resident; MI_ERR_INVALID_ARG for window < 1,
  * sinks < 0 or a group_tokens that is not a positive multiple of 16. */

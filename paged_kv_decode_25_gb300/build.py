@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -50,6 +51,25 @@ def _stale() -> bool:
     return any(os.path.getmtime(f) > t for f in srcs + hdrs + [os.path.abspath(__file__)])
 
 
+def launch_registers(text: str, kernel: str):
+    """Registers of each instantiation of `kernel` in what `ptxas -v` printed."""
+    found = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", text, re.S)
+    return [int(n) for name, n in found if kernel in name]
+
+
+def check_registers(text: str) -> None:
+    """The sliding prefill's warps pass registers among themselves (setmaxnreg), out of
+    those the kernel is launched with: with fewer than its shares add up to they would
+    wait without end, so a compiler that takes another number is refused here. (The call
+    asks again before its first launch.)"""
+    with open(os.path.join(CSRC, "prefill.cu")) as f:
+        want = int(re.search(r"kSlideRegs = (\d+);", f.read()).group(1))
+    have = launch_registers(text, "slide_tc2_kernel")
+    if any(n != want for n in have):
+        raise RuntimeError("slide_tc2_kernel is laid out for launches of %d registers a thread, and this nvcc gives it %s: "
+                           "kSlideRegs, kSlideFewRegs and kSlideManyRegs in prefill.cu have to follow" % (want, have))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
@@ -59,7 +79,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     objs = []
     for f in CU_SOURCES:
         o = os.path.join(OUT_DIR, f + ".o")
-        jobs.append([nvcc] + NVCC_FLAGS + ["-c", os.path.join(CSRC, f), "-o", o])
+        report = ["-Xptxas", "-v"] if f == "prefill.cu" else []
+        jobs.append([nvcc] + NVCC_FLAGS + report + ["-c", os.path.join(CSRC, f), "-o", o])
         objs.append(o)
     for f in CPP_SOURCES:
         o = os.path.join(OUT_DIR, f + ".o")
@@ -72,6 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError("build failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, file=sys.stderr)
+        if "-v" in cmd:
+            check_registers(r.stdout + r.stderr)
 
     with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
         list(ex.map(run, jobs))

@@ -33,6 +33,7 @@
 //     the tiles with the most keys first, as a longest-first schedule wants,
 //     while the 8 tiles of a group read the same K/V through L2 at about the
 //     same time. Tiles past a request's last row exit at once.
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -2409,14 +2410,18 @@ template <int HD>
 bool prepare_slide() {
     static std::mutex mu;
     static CUcontext done[256] = {};
-    // registers that the launch does not have would be waited for without end
-    static const bool enough = [] {
+    // Registers that the launch does not have would be waited for without end: the build
+    // refuses such a kernel, and so does this. (A query that failed says nothing about
+    // the kernel: it is made again.)
+    static std::atomic<bool> enough{false};
+    if (!enough) {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(slide_tc2_kernel<HD>)) == cudaSuccess &&
-               a.numRegs == kSlideRegs;
-    }();
-    return enough &&
-           raise_smem_once(reinterpret_cast<const void*>(slide_tc2_kernel<HD>), SlideSmem<HD>::kTotal, done, mu);
+        if (cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(slide_tc2_kernel<HD>)) != cudaSuccess ||
+            a.numRegs != kSlideRegs)
+            return false;
+        enough = true;
+    }
+    return raise_smem_once(reinterpret_cast<const void*>(slide_tc2_kernel<HD>), SlideSmem<HD>::kTotal, done, mu);
 }
 
 template <int HD>

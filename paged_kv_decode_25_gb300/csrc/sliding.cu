@@ -163,9 +163,13 @@ __device__ void merge_outputs(const SlideParams& p, int b, int h, int slot, int 
             v[i] = __ldcg(reinterpret_cast<const float4*>(at + x));
         }
         float t = top;
+        bool any = top != kNegInf;  // (a NaN, which fmaxf passes over, counts)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t = fmaxf(t, lse[i]);
-        if (t == kNegInf) continue;  // nothing in sight so far
+        for (int i = 0; i < 8; ++i) {
+            t = fmaxf(t, lse[i]);
+            any |= lse[i] != kNegInf;
+        }
+        if (!any) continue;  // nothing in sight so far
         const float f = ex2(top - t);
         top = t;
         den *= f;
@@ -539,7 +543,7 @@ __global__ void __launch_bounds__(kSlideWarps * 32, kSlideBlocks)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 const int g = 2 * (lane & 3) + w;
-                if (lane < 4 && g < p.G) part[p.G * HD + g] = st.l[w] > 0.f ? st.m[w] + log2f(st.l[w]) : kNegInf;
+                if (lane < 4 && g < p.G) part[p.G * HD + g] = st.l[w] == 0.f ? kNegInf : st.m[w] + log2f(st.l[w]);
             }
             __syncwarp();
             if (counted == done && owes < kOwed) {

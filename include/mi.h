@@ -583,7 +583,8 @@ mi_status mi_paged_decode_attention_int8(const mi_dims* dims, const void* q, con
  * the softmax where it was trained to be): with p its position, tokens t <= p with
  * t > p - window or t < sinks. window >= 1 (it counts the token itself), sinks >= 0;
  * a window no smaller than the context sees all of it. Keys keep the rotation of
- * the position they were appended at. */
+ * the position they were appended at. A query that is not finite gives a NaN row (a
+ * row whose scores are all -inf counts as one that sees no key, and is zero). */
 
 /* mi_paged_decode_attention within the window: with n = context_lens[b],
  *   out[b][j] = sum_t softmax_t(scale * <q[b][j], K_t>) V_t,

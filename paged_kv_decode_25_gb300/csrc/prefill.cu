@@ -2344,9 +2344,10 @@ __global__ void __launch_bounds__(kSlideThreads, 1)
             r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 1);
             r.la += __shfl_xor_sync(0xffffffffu, r.la, 2);
             r.lb += __shfl_xor_sync(0xffffffffu, r.lb, 2);
-            // rows before position 0 are +0, and so is a row without a key
-            const float inva = position(toka) >= 0 && r.la > 0.f ? 1.f / r.la : 0.f;
-            const float invb = position(tokb) >= 0 && r.lb > 0.f ? 1.f / r.lb : 0.f;
+            // rows before position 0 are +0, and so is a row without a key (one whose sum is
+            // NaN is not)
+            const float inva = position(toka) >= 0 && r.la != 0.f ? 1.f / r.la : 0.f;
+            const float invb = position(tokb) >= 0 && r.lb != 0.f ? 1.f / r.lb : 0.f;
             uint16_t* out = p.out + ((long long)(it(offsetof(SlideItem, q0)) + it(offsetof(SlideItem, tok0))) * p.Hq +
                                      (long long)it(offsetof(SlideItem, h)) * p.G) * HD + 8 * c4;
             uint16_t* outa = out + ((long long)toka * p.Hq + (t * tr + rla) % p.G) * HD;

@@ -85,7 +85,8 @@ const char* mi_status_string(mi_status s);
  *    by popping the missing ones in order and appending them. All or nothing.
  *  - mi_kv_pool_free(seq) pushes seq's blocks in table order (so the next pop
  *    returns its last block) and forgets seq.
- * The pool is host memory only and never touches the GPU.
+ * The pool is host memory only and never touches the GPU. A call that finds no
+ * memory for a table is MI_ERR_INVALID_ARG and changes nothing.
  * ------------------------------------------------------------------------ */
 typedef struct mi_kv_pool mi_kv_pool; /* opaque; owned by the library */
 

@@ -6,6 +6,7 @@
 // demand like the allocate sketch of the nxmr.cn article (§2.1
 // "KV缓存的内存革命"), but fixed in size: an allocation that does not fit fails
 // and leaves the pool as it was.
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -39,6 +40,18 @@ struct mi_kv_pool {
     // one table fewer holds block b (b < 0: a column given back already)
     void give(int32_t b) {
         if (b >= 0 && --refs[(size_t)b] == 0) free_stack.push_back(b);
+    }
+    // Room for n blocks in a table, so that adding them throws nothing (grown by half at
+    // least: a sequence grows block by block); false: no memory.
+    static bool make_room(std::vector<int32_t>& t, int64_t n) {
+        const int64_t have = (int64_t)t.capacity();
+        if (have >= n) return true;
+        try {
+            t.reserve((size_t)std::max(n, have + have / 2));
+        } catch (...) {
+            return false;
+        }
+        return true;
     }
     bool resident(int32_t seq) const { return seq >= 0 && (size_t)seq < tables.size() && live[(size_t)seq]; }
     // whether the block of token n - 1 of a table was given back
@@ -114,6 +127,7 @@ extern "C" mi_status mi_kv_pool_alloc(mi_kv_pool* p, int32_t seq, int32_t num_to
     if (need > p->max_blocks_per_seq) return MI_ERR_INVALID_ARG;
     const int64_t extra = need - (int64_t)t.size();
     if (extra > (int64_t)p->free_stack.size()) return MI_ERR_OUT_OF_BLOCKS;
+    if (!p->make_room(t, need)) return MI_ERR_INVALID_ARG;
     for (int64_t i = 0; i < extra; ++i) t.push_back(p->take());
     p->tokens[(size_t)seq] = num_tokens;
     p->live[(size_t)seq] = 1;
@@ -127,7 +141,13 @@ extern "C" mi_status mi_kv_pool_alloc_batch(mi_kv_pool* p, const int32_t* seq_id
     if (!p || count < 0 || (count > 0 && (!seq_ids || !num_tokens))) return MI_ERR_INVALID_ARG;
     // check the whole batch first, earlier entries applied on a copy of the
     // state they touch, so that either every entry is made or none
-    std::vector<int64_t> size(p->tables.size(), -1), toks(p->tables.size(), -1);
+    std::vector<int64_t> size, toks;
+    try {
+        size.assign(p->tables.size(), -1);
+        toks.assign(p->tables.size(), -1);
+    } catch (...) {
+        return MI_ERR_INVALID_ARG;
+    }
     int64_t extra_total = 0;
     for (int32_t i = 0; i < count; ++i) {
         const int32_t seq = seq_ids[i], n = num_tokens[i];
@@ -144,6 +164,8 @@ extern "C" mi_status mi_kv_pool_alloc_batch(mi_kv_pool* p, const int32_t* seq_id
         toks[(size_t)seq] = n;
     }
     if (extra_total > (int64_t)p->free_stack.size()) return MI_ERR_OUT_OF_BLOCKS;
+    for (int32_t i = 0; i < count; ++i)
+        if (!p->make_room(p->tables[(size_t)seq_ids[i]], size[(size_t)seq_ids[i]])) return MI_ERR_INVALID_ARG;
     for (int32_t i = 0; i < count; ++i) {
         const mi_status st = mi_kv_pool_alloc(p, seq_ids[i], num_tokens[i]);
         if (st != MI_OK) return st;  // not reached: the batch was checked above
@@ -332,7 +354,7 @@ extern "C" mi_status mi_kv_pool_swap_in(mi_kv_pool* p, int32_t seq, int32_t* blo
     if (need > max_out || (need > 0 && !blocks_out)) return MI_ERR_INVALID_ARG;
     if (need > (int64_t)p->free_stack.size()) return MI_ERR_OUT_OF_BLOCKS;
     std::vector<int32_t>& t = p->tables[(size_t)seq];
-    int32_t at = 0;
+    int32_t at = 0;  // (the table has kept its room)
     for (int64_t i = 0, g = 0; i < cols; ++i) {
         if (g < (int64_t)gone.size() && gone[(size_t)g] == i) {
             t.push_back(-1);

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kPageThreads) copy_planes_kernel(const __grid_
     const Plane& pl = p.plane[lo];
     const int x = item - pl.first;
     const int per = rows_per_item(pl.row_bytes), pieces = (int)pieces_per_row(pl.row_bytes);
-    const int i0 = x / pieces * per, i1 = min(p.n, i0 + per);
+    const int i0 = x / pieces * per, i1 = i0 + min(per, p.n - i0);  // (n may be near 2^31)
     const long long from = (long long)(x % pieces) * kItemBytes;
     const int len = (int)min((long long)kItemBytes, pl.row_bytes - from);
     if (((reinterpret_cast<uintptr_t>(pl.base) | (uintptr_t)pl.row_bytes) & 15u) == 0)

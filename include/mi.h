@@ -154,7 +154,9 @@ mi_status mi_kv_pool_shrink(mi_kv_pool* pool, int32_t seq_id, int32_t num_tokens
  * order: their contents are the caller's to copy, copy_src[i] to copy_dst[i] for
  * i < *n_copies (mi_kv_copy_planes), before either sequence's next append (and
  * before the copies of a fork of the fork, which read them); with INT8 caches the
- * open-group rows of its slot too. Both sequences are used now.
+ * open-group rows of its slot too: those are of src_seq's own open group, so INT8
+ * sequences are forked within that or at a multiple of 64 tokens. Both sequences are
+ * used now.
  * Columns of src_seq that mi_kv_pool_slide gave back are -1 in dst_seq's table, too.
  * A fork of k tokens fewer than src_seq held when it was slid looks k tokens further
  * back than src_seq did, so such sources are slid with window + k; where they were
@@ -611,7 +613,10 @@ mi_status mi_paged_decode_attention_sliding_fp8(const mi_dims* dims, const void*
                                                 void* workspace, size_t workspace_bytes, int32_t* dev_err,
                                                 mi_stream_t stream);
 
-/* The same over INT8 caches (mi_paged_decode_attention_int8). */
+/* The same over INT8 caches (mi_paged_decode_attention_int8). Blocks are taken two at a
+ * time, so a block's f16 probabilities are relative to the largest V factor up to its
+ * pair's end: of a block beside one with a far larger factor (at a group's edge), values
+ * lose at most 2^-25 of the larger factor's. */
 mi_status mi_paged_decode_attention_sliding_int8(const mi_dims* dims, const void* q, const void* k_cache,
                                                  const void* v_cache, const float* k_amax, const float* v_amax,
                                                  const int32_t* block_tables, const int32_t* context_lens,

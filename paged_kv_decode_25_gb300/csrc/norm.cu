@@ -14,8 +14,9 @@
 // (its cosines, sines and weights are then read once) where there are many rows.
 //
 // Measured: 12,821 tokens (32/8 heads of 128, bf16, one projection's rows) 52 us, 6.2 TB/s,
-// 91 % of a copy's rate; 5,000 tokens into e4m3 (28/4) 20 us, 4.5 TB/s, bound by its
-// quotients and conversions, and 1.6 waves of blocks; a step of 64 tokens 2.1 us on the
+// 91 % of a copy's rate; 5,000 tokens into e4m3 (28/4) 20.2 us, 4.4 TB/s: 1.6 waves of
+// blocks, fp32 arithmetic value by value, 12 bytes of spill (16.6 where inputs are in
+// L2; 18.3 with a product for a quotient); a step of 64 tokens 2.3 us on the
 // device. Five blocks an SM (96 registers), four groups' loads in flight: 55 us with four
 // blocks, 58 with two groups. A row in one warp from 16 warps an SM on: parts of rows
 // read cosines and weights again (5,000 tokens: 22.5 us in bf16, 23.7 from 40 on).

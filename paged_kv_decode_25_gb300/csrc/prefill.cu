@@ -1794,7 +1794,8 @@ __global__ void __launch_bounds__(kT2Threads, 1)
 //
 // mi_paged_prefill_attention_sliding on the pipeline of prefill_tc2_kernel. A row at
 // position p sees keys t <= p with t > p - window or t < sinks, so an item (256 rows
-// of a request and KV head) has window / 128 + 2 stages whatever the context: what a
+// of a request and KV head) has the stages of window + 64 (G = 4) keys, 9 for a window of
+// 1,024, whatever the context: what a
 // block does around its stages (setting up, the first copies, two masked stages, the
 // stores) took 13 of 30 us for windows of 1,024 with a block per item. So
 //   * one block per SM takes items in turn and its barriers run on from item to item:
@@ -1808,16 +1809,19 @@ __global__ void __launch_bounds__(kT2Threads, 1)
 //   * rows are stored 16 bytes a lane (as pairs of values the stores took 2.7 us).
 //
 // Bound by the pipeline of tensor cores and exponentials within the stages (1.64 us for 256
-// rows and 128 keys, 82 % of the tensor peak) and by what two masked stages and the stores
-// add to an item (5 us). Measured: 16 chunks of 512 tokens behind windows
-// of 1,024 (32/8 heads of 128) 153 us, 0.87 PFLOP/s of visible pairs; two prompts of 12,000
-// to 16,000 behind 4,096 (28/4) 1,121 us, 1.24 PFLOP/s; a prompt of 700 behind 256 16 us. A
-// block per item: 207, 1,272, 19.5.
+// rows and 128 keys, 82 % of the tensor peak), by what two masked stages and the stores
+// add to an item (5 us), and by items taken in a fixed turn (63 stages on the busiest SM,
+// 58.5 on average, for the chunks). Measured, calls in a row: 16 chunks of 512 tokens behind
+// windows of 1,024 (32/8 heads of 128) 152 us, 0.87 PFLOP/s of visible pairs; two prompts of
+// 12,000 to 16,000 behind 4,096 (28/4) 1,115 us, 1.25 PFLOP/s; a prompt of 700 behind 256 16
+// us. On the device 151, 1,086, 16 (207, 1,272, 19.5 with a block per item). Weights enter
+// the second product as bf16 (half a step 2^-8 of each), their sum in fp32 before that.
 
 // Warps 0 .. 15 softmax, 16 MMA, 17 producer, and two that only fill up their warpgroup:
 // the four give registers to the sixteen, whose 64 scores leave 96 too few. (With 18
-// warps of 96 and the masked stage a function of its own 159 us for the chunks below,
-// now 151; with shares of 32 and 112 the small roles spill: 167.)
+// warps of 96 and the masked stage a function of its own 159 us on the device for the
+// chunks above, now 151; with shares of 32 and 112 the small roles spill: 167. As it is,
+// 8 to 20 bytes a thread spill.)
 constexpr int kSlideThreads = (kT2MmaWarp + 4) * 32, kSlideRegs = 96;  // at launch
 constexpr int kSlideFewRegs = 64, kSlideManyRegs = 104;
 static_assert(128 * kSlideFewRegs + 32 * kT2MmaWarp * kSlideManyRegs <= kSlideThreads * kSlideRegs,

@@ -14,13 +14,15 @@
 // others the warp that counts the last piece adds all of them up by their
 // log-sum-exps. (A second launch for that cost 5 us a call more.)
 //
-// Measured, bytes in sight over the whole call: 64 requests behind windows of 1,024
-// (32/8 heads of 128, bf16) 48 us, 5.1 TB/s, of which the stream itself runs at 7 between
-// 6 us of plan and first copies and 4 to 5 of last pieces; 128 behind 4,096 (28/4, e4m3)
-// 93 us, 5.6 TB/s, and 256 behind 128 (16/8, INT8) 24 us, 2.5 TB/s: there no pipe is busy
-// above 40 % (issue 37, integer 36, tensor 13), the warps wait for their own results. So
-// one-byte blocks go two to a stage: 97 us with one. A single request takes 12 us, latency
-// from end to end.
+// Measured, calls in a row over inputs that L2 does not hold, bytes in sight over the
+// call's time: 64 requests behind windows of 1,024 (32/8 heads of 128, bf16) 48.7 us, 5.1
+// TB/s, of which the stream itself runs at 7 between 6 us of plan and first copies and 4 to 5
+// of last pieces; 128 behind 4,096 (28/4, e4m3) 94 us, 5.5 TB/s: no pipe is busy above 41 %
+// (integer; issue 35, tensor 15), the warps wait for their own results, so one-byte blocks
+// go two to a stage (on the device 92 us, 97 with one); 256 behind 128 (16/8, INT8) 27 us,
+// 2.3 TB/s (24.6 on the device): 1.1 rounds of pieces of 2 to 5 double blocks, each behind
+// a load of its queries (integer pipe 26 %, issue 23). A single request takes 11 us,
+// latency from end to end.
 #include <atomic>
 #include <chrono>
 #include <cmath>

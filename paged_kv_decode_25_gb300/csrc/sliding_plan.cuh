@@ -8,8 +8,8 @@
 namespace mi {
 
 constexpr int kSlideWarps = 4;
-// Blocks per SM. (Four for one-byte caches, at 128 registers a thread: 116 us instead
-// of 92 for 128 windows of 4,096 tokens, 4 KV heads, e4m3.)
+// Blocks per SM. (Four for one-byte caches, at 128 registers a thread: 116 us on the
+// device instead of 92 for 128 windows of 4,096 tokens, 4 KV heads, e4m3.)
 constexpr int kSlideBlocks = 3;
 // Pieces that have partial results, at most, per warp of the grid.
 constexpr int kSplitPerWarp = 8;
